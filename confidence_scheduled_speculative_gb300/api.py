@@ -49,6 +49,8 @@ COST_ADDITIVE = 1
 COST_ADDITIVE_INTERP = 2
 DTYPE_BF16 = 0
 DTYPE_F32 = 1
+DTYPE_E4M3 = 2
+MAX_WINDOW = 32
 MAX_TIERS = 64
 
 
@@ -83,6 +85,22 @@ class dspark_plan_options(ctypes.Structure):
     _fields_ = [("conf_generation", ctypes.c_void_p), ("req_generation", ctypes.c_void_p),
                 ("lagged_conf_logits", ctypes.c_void_p), ("align_to_tiers", ctypes.c_int32),
                 ("host_tiers", ctypes.POINTER(ctypes.c_int32)), ("n_tiers", ctypes.c_int32)]
+
+
+class dspark_kv_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("n_requests", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
+
+
+class dspark_norm_rope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("cos_sin", ctypes.c_void_p), ("n_pos", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -145,6 +163,19 @@ _SIGS = {
     "dspark_sts_fit_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
     "dspark_sts_fit": (ctypes.c_int, [_VP, _VP, _VP, _I64, _I32, ctypes.POINTER(ctypes.c_float),
                                       _I32, _I32, _VP, _VP, _VP, _VP, _VP, _SZ, _VP, _VP]),
+    "dspark_qk_norm_rope": (ctypes.c_int, [_VP, _I64, _VP, _I64, _I32, _I32, _I32, _I32,
+                                           ctypes.POINTER(dspark_norm_rope), _VP, _VP, _I32, _VP,
+                                           _I64, _VP, _I64, _VP, _VP]),
+    "dspark_kv_append": (ctypes.c_int, [_VP, _I64, _VP, _I64, _VP, _I64, _I32, _I32,
+                                        ctypes.POINTER(dspark_kv_cache),
+                                        ctypes.POINTER(dspark_norm_rope), _VP, _VP, _VP, _VP,
+                                        _I32, _VP, _I64, _VP, _VP]),
+    "dspark_kv_read": (ctypes.c_int, [ctypes.POINTER(dspark_kv_cache), _VP, _VP, _I32, _I32, _I32,
+                                      _VP, _VP, _I64, _VP, _VP]),
+    "dspark_tree_attention_workspace_bytes": (_SZ, [_I32, _I32]),
+    "dspark_tree_attention": (ctypes.c_int, [_VP, _I64, _I32, _I32, _I32, _VP, _VP, _I32, _VP,
+                                             ctypes.c_float, ctypes.POINTER(dspark_kv_cache),
+                                             _VP, _I64, _VP, _VP, _SZ, _VP, _VP]),
 }
 
 
@@ -559,3 +590,185 @@ def dspark_sts_fit(rec_logits, *, rec_correct, rec_tested, N, gamma, temp_grid, 
         _p(workspace), workspace.numel() * workspace.element_size(),
         _p(status, torch.int32, "status"), _stream(stream))
     _check("dspark_sts_fit", rc)
+
+
+# --------------------------------------------- verify window over a cache
+
+class KVCache:
+    """One layer's paged cache over tensors the caller owns (the C ABI's
+    dspark_kv_cache, filled once).
+
+    ``k``, ``v``: [n_pages, page_size, n_kv_heads, head_dim], bfloat16, float32
+    or float8_e4m3fn, of the same strides with a unit inner one; tokens and
+    heads may lie in either order (pass a transposed view).  ``block_table``:
+    int32 [n_requests, table_width].  ``k_scale``, ``v_scale``: fp32 [n_pages,
+    n_kv_heads, page_size], for float8 only.  The tensors are kept referenced."""
+
+    def __init__(self, k, v, block_table, k_scale=None, v_scale=None):
+        kinds = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32,
+                 torch.float8_e4m3fn: DTYPE_E4M3}
+        for name, t in (("k", k), ("v", v)):
+            if not t.is_cuda or t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError(f"{name}: expected a 4-D CUDA tensor with unit inner stride")
+        if k.dtype not in kinds or v.dtype != k.dtype:
+            raise ValueError("k and v: expected one of bfloat16, float32 and float8_e4m3fn")
+        if v.shape != k.shape or v.stride() != k.stride():
+            raise ValueError("v: expected the shape and strides of k")
+        if block_table.dim() != 2:
+            raise ValueError("block_table: expected a 2-D tensor")
+        n_pages, page, heads, dim = k.shape
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (t is not None) != (k.dtype == torch.float8_e4m3fn):
+                raise ValueError(f"{name}: expected with float8_e4m3fn entries, and only with them")
+            if t is not None and tuple(t.shape) != (n_pages, heads, page):
+                raise ValueError(f"{name}: expected shape {(n_pages, heads, page)}")
+        self.k, self.v, self.block_table = k, v, block_table
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.n_kv_heads, self.head_dim = heads, dim
+        self.desc = dspark_kv_cache(
+            kinds[k.dtype], n_pages, page, heads, dim, block_table.size(0), block_table.size(1),
+            k.stride(0), k.stride(1), k.stride(2), k.data_ptr(), v.data_ptr(),
+            _p(k_scale, torch.float32, "k_scale"), _p(v_scale, torch.float32, "v_scale"),
+            _p(block_table, torch.int32, "block_table"))
+        self.ref = ctypes.byref(self.desc)
+
+
+def _rows(t: torch.Tensor, name: str, dtype, heads=None, dim=None, rows=None) -> tuple[int, int]:
+    """Pointer and row stride of [rows, heads, head_dim] rows: heads packed,
+    any row stride."""
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name}: expected a 3-D CUDA tensor [rows, heads, head_dim]")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    n, h, d = t.shape
+    ld, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise ValueError(f"{name}: expected packed heads with unit inner stride")
+    if (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise ValueError(f"{name}: expected {heads} heads of {dim} elements, got {h} of {d}")
+    if rows is not None and n < rows:
+        raise ValueError(f"{name}: expected at least {rows} rows, got {n}")
+    return t.data_ptr(), ld if n > 1 else max(ld, h * d)
+
+
+def _index(t, n, name):
+    if t is not None and t.numel() < n:
+        raise ValueError(f"{name}: expected at least {n} elements, got {t.numel()}")
+    return _p(t, torch.int32, name)
+
+
+def _norm_rope(dtype, dim, q_weight, k_weight, eps, cos_sin, interleaved):
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and w.numel() != dim:
+            raise ValueError(f"{name}: expected {dim} elements")
+    n_pos, rope_dim = (0, 0) if cos_sin is None else cos_sin.shape
+    return dspark_norm_rope(_p(q_weight, dtype, "q_weight"), _p(k_weight, dtype, "k_weight"), eps,
+                            _p(cos_sin, torch.float32, "cos_sin"), n_pos, rope_dim,
+                            1 if interleaved else 0)
+
+
+def dspark_qk_norm_rope(q, k, *, status, pos=None, totals=None, q_weight=None, k_weight=None,
+                        eps=1e-6, cos_sin=None, interleaved=False, q_out=None, k_out=None,
+                        max_rows=None, stream=None) -> None:
+    """RMS norm of each head's queries and keys (where a weight is given) and
+    rotation of their first cos_sin.size(1) elements (where ``cos_sin`` is:
+    fp32 [n_pos, rope_dim], cosines then sines), in one pass.  ``q``, ``k``:
+    [rows, heads, head_dim] bfloat16 or float32 with packed heads, either may
+    be None; the outputs default to the inputs themselves (in place)."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q and k: expected at least one of them")
+    dtype, dim = first.dtype, first.size(2)
+    code = _dtype_code(first)
+    max_rows = first.size(0) if max_rows is None else max_rows
+    args = []
+    for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+        if t is None:
+            args.append((None, 0, None, 0, 0))
+            continue
+        heads = t.size(1)
+        args.append(_rows(t, name, dtype, heads, dim, max_rows)
+                    + _rows(t if o is None else o, name + "_out", dtype, heads, dim, max_rows)
+                    + (heads,))
+    (qp, lq, qo, lqo, hq), (kp, lk, ko, lko, hk) = args
+    nr = _norm_rope(dtype, dim, q_weight, k_weight, eps, cos_sin, interleaved)
+    rc = load().dspark_qk_norm_rope(
+        qp, lq, kp, lk, code, hq, hk, dim, ctypes.byref(nr), _index(pos, max_rows, "pos"),
+        _index(totals, 1, "totals"), max_rows, qo, lqo, ko, lko,
+        _p(status, torch.int32, "status"), _stream(stream))
+    _check("dspark_qk_norm_rope", rc)
+
+
+def dspark_kv_append(k, v, cache: KVCache, *, req, status, pos=None, cache_pos=None, q=None,
+                     q_out=None, totals=None, q_weight=None, k_weight=None, eps=1e-6,
+                     cos_sin=None, interleaved=False, max_rows=None, stream=None) -> None:
+    """dspark_qk_norm_rope with the keys, and the values as they are, going
+    into ``cache`` at the rows' positions (``cache_pos``, else ``pos``);
+    quantised there if it holds float8.  ``q`` (with ``q_out``, in place by
+    default) rides along in the same pass."""
+    dtype, dim, hkv = k.dtype, cache.head_dim, cache.n_kv_heads
+    code = _dtype_code(k)
+    max_rows = k.size(0) if max_rows is None else max_rows
+    qp = lq = qo = lqo = None
+    hq = 0
+    if q is not None:
+        hq = q.size(1)
+        qp, lq = _rows(q, "q", dtype, hq, dim, max_rows)
+        qo, lqo = _rows(q if q_out is None else q_out, "q_out", dtype, hq, dim, max_rows)
+    kp, lk = _rows(k, "k", dtype, hkv, dim, max_rows)
+    vp, lv = _rows(v, "v", dtype, hkv, dim, max_rows)
+    nr = None
+    if q_weight is not None or k_weight is not None or cos_sin is not None:
+        nr = _norm_rope(dtype, dim, q_weight, k_weight, eps, cos_sin, interleaved)
+    rc = load().dspark_kv_append(
+        qp, lq or 0, kp, lk, vp, lv, code, hq, cache.ref, None if nr is None else ctypes.byref(nr),
+        _index(req, max_rows, "req"), _index(pos, max_rows, "pos"),
+        _index(cache_pos, max_rows, "cache_pos"), _index(totals, 1, "totals"), max_rows, qo,
+        lqo or 0, _p(status, torch.int32, "status"), _stream(stream))
+    _check("dspark_kv_append", rc)
+
+
+def dspark_kv_read(cache: KVCache, *, start, cu_rows, k_out, v_out, status, max_rows=None,
+                   stream=None) -> None:
+    """Positions start[r], start[r]+1, ... of each request back as rows
+    cu_rows[r]..cu_rows[r+1]-1 of ``k_out`` and ``v_out`` ([rows, n_kv_heads,
+    head_dim], bfloat16 or float32)."""
+    B = start.numel()
+    max_rows = k_out.size(0) if max_rows is None else max_rows
+    kp, ld = _rows(k_out, "k_out", k_out.dtype, cache.n_kv_heads, cache.head_dim, max_rows)
+    vp, ldv = _rows(v_out, "v_out", k_out.dtype, cache.n_kv_heads, cache.head_dim, max_rows)
+    if ldv != ld:
+        raise ValueError("v_out: expected the row stride of k_out")
+    rc = load().dspark_kv_read(
+        cache.ref, _p(start, torch.int32, "start"), _index(cu_rows, B + 1, "cu_rows"), B,
+        max_rows, _dtype_code(k_out), kp, vp, ld, _p(status, torch.int32, "status"),
+        _stream(stream))
+    _check("dspark_kv_read", rc)
+
+
+def dspark_tree_attention_workspace_bytes(n_q_heads: int, head_dim: int) -> int:
+    return int(load().dspark_tree_attention_workspace_bytes(n_q_heads, head_dim))
+
+
+def dspark_tree_attention(q, cache: KVCache, *, cu_seqlens, prefix_lens, scale, out, workspace,
+                          status, ancestors=None, lse=None, max_rows=None, stream=None) -> None:
+    """Attention of the packed window's rows ``q`` [rows, n_q_heads, head_dim]
+    over ``cache``: every position before the request's prefix length and the
+    window's tokens whose bit is set in the row's ``ancestors`` word (int32
+    bits [rows]; None: a chain).  ``out`` like ``q``; ``lse`` fp32 [rows,
+    n_q_heads], optional."""
+    hq, dim = q.size(1), cache.head_dim
+    code = _dtype_code(q)
+    max_rows = q.size(0) if max_rows is None else max_rows
+    B = prefix_lens.numel()
+    qp, lq = _rows(q, "q", q.dtype, hq, dim, max_rows)
+    op, lo = _rows(out, "out", q.dtype, hq, dim, max_rows)
+    if lse is not None and lse.numel() < max_rows * hq:
+        raise ValueError(f"lse: expected at least {max_rows * hq} elements")
+    rc = load().dspark_tree_attention(
+        qp, lq, code, hq, max_rows, _index(cu_seqlens, B + 1, "cu_seqlens"),
+        _p(prefix_lens, torch.int32, "prefix_lens"), B, _index(ancestors, max_rows, "ancestors"),
+        scale, cache.ref, op, lo, _p(lse, torch.float32, "lse"), _p(workspace),
+        workspace.numel() * workspace.element_size(), _p(status, torch.int32, "status"),
+        _stream(stream))
+    _check("dspark_tree_attention", rc)

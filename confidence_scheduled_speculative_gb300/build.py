@@ -26,7 +26,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libdspark.so")
 CHECKED_LIB_PATH = os.path.join(OUT_DIR, "libdspark_checked.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["api.cu", "plan.cu", "pack.cu", "accept.cu", "scatter.cu", "sample.cu", "calib.cu"]
+SOURCES = ["api.cu", "plan.cu", "pack.cu", "accept.cu", "scatter.cu", "sample.cu", "calib.cu",
+           "cache.cu", "attend.cu"]
 
 
 def nvcc() -> str:

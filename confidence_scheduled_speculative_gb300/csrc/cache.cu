@@ -1,0 +1,624 @@
+// cache.cu -- norms and rotation of queries and keys, the write of keys and
+// values into a paged cache (quantised to E4M3 on the way, if it is one), and
+// the reading of cache entries back into rows.
+//
+// The mathematics, for one row and head x in R^D, all in 32 bits:
+//   y = x / sqrt(mean(x^2) + eps) * w          (queries and keys, if a weight is given)
+//   (a, b) -> (a c - b s, b c + a s)           (the pairs of the first rope_dim elements)
+//   E4M3: scale = max(max|y| / 448, 2^-100), code = e4m3(y / scale)
+// Each element is read once and written once and costs some ten operations,
+// so the bound is HBM bandwidth; for a window of a few rows it is the launch.
+//
+// append_kernel   eight elements a lane (16 bytes of bf16), 8, 16 or 32 lanes a
+//   head, so that a head's sums, its maximum and the partner of a rotated
+//   element are warp shuffles away and nothing is read twice.  A warp takes
+//   kHeadsPerLane heads a lane group of one row: the row's cosines and sines
+//   stay in registers over them, and their loads are all in flight together.
+// append_any_kernel   any alignment, stride and even head size: one warp a
+//   (row, head), one element a lane and step.
+// read_kernel     a CTA takes 32 output rows: their slots are looked up by one
+//   warp (binary search in cu_rows, then the block table), then all threads
+//   stream the rows' elements.
+
+#include "kvcache.cuh"
+
+#include <type_traits>
+
+namespace dspark {
+
+constexpr int kAppendThreads = 256;
+constexpr int kHeadsPerLane = 4;
+constexpr int kReadThreads = 256;
+constexpr int kReadRows = 32;
+
+struct NoCache {};
+
+struct AppendArgs {
+    const void *in[3];  // q, k, v
+    long long ld_in[3];
+    int heads[3];
+    void *out[2];  // q_out, k_out (no cache)
+    long long ld_out[2];
+    const void *weight[2];
+    float eps;
+    const float *cos_sin;  // null: no rotation
+    int n_pos, rope_dim, interleaved;
+    const int32_t *req, *pos, *cache_pos, *totals;
+    int max_rows, head_dim;
+    KvView cache;
+    int32_t *status;
+};
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void load8(const float *p, float *x) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const e4m3 *p, float *x) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned w = i < 2 ? v.x : v.y;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * (i & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float *x) {
+    uint4 v;
+    unsigned *w = reinterpret_cast<unsigned *>(&v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const unsigned *>(&b);
+    }
+    *reinterpret_cast<uint4 *>(p) = v;
+}
+__device__ __forceinline__ void store8(float *p, const float *x) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+__device__ __forceinline__ int rows_of(const AppendArgs &a) {
+    if (!a.totals) return a.max_rows;
+    return max(0, min(__ldg(a.totals), a.max_rows));
+}
+
+// The slot of a row's key and value: false for a pad row or a bad one (flagged).
+__device__ __forceinline__ bool row_slot(const AppendArgs &a, int row, int *page, int *token) {
+    const int r = __ldg(a.req + row);
+    if (r < 0) return false;
+    *page = kv_page(a.cache, r, __ldg((a.cache_pos ? a.cache_pos : a.pos) + row), token);
+    if (*page < 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+    return *page >= 0;
+}
+
+// The row's position in the rotation's table: false when it is outside (flagged).
+__device__ __forceinline__ bool row_angle(const AppendArgs &a, int row, int *p) {
+    *p = 0;
+    if (!a.cos_sin) return true;
+    if (a.req && __ldg(a.req + row) < 0) return false;
+    *p = __ldg(a.pos + row);
+    const bool ok = *p >= 0 && *p < a.n_pos;
+    if (!ok) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+    return ok;
+}
+
+template <typename T, typename C>
+__global__ void __launch_bounds__(kAppendThreads)
+append_kernel(AppendArgs a, int lanes_per_head) {
+    constexpr bool kCache = !std::is_same<C, NoCache>::value;
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int D = a.head_dim, groups = 32 / lanes_per_head;
+    const int group = lane / lanes_per_head, chunk = lane % lanes_per_head;
+    const int H = a.heads[0] + a.heads[1] + a.heads[2];
+    const int per_warp = groups * kHeadsPerLane;
+    const int blocks = (H + per_warp - 1) / per_warp;
+    const long long unit = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const long long row64 = div_nonneg(unit, blocks);
+    if (row64 >= rows_of(a)) return;
+    const int row = (int)row64;
+    const int h0 = (int)(unit - row64 * blocks) * per_warp + group;
+    const bool has = chunk * 8 < D;  // a lane past a head that is not a power of two
+
+    // every load of the warp's heads in flight before the first is used
+    float x[kHeadsPerLane][8];
+    int kind[kHeadsPerLane], head[kHeadsPerLane];
+#pragma unroll
+    for (int i = 0; i < kHeadsPerLane; ++i) {
+        int h = h0 + i * groups;
+        kind[i] = h >= H ? 3 : (h < a.heads[0] ? 0 : (h < a.heads[0] + a.heads[1] ? 1 : 2));
+        head[i] = h - (kind[i] > 0 ? a.heads[0] : 0) - (kind[i] > 1 ? a.heads[1] : 0);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
+        if (kind[i] < 3 && has)
+            load8(static_cast<const T *>(a.in[kind[i]]) + row * a.ld_in[kind[i]] +
+                      (long long)head[i] * D + chunk * 8,
+                  x[i]);
+    }
+    const bool pad = a.req && __ldg(a.req + row) < 0;
+    int p, page = -1, token = 0;
+    const bool angle = !pad && row_angle(a, row, &p);
+    bool slot = false;
+    if (kCache && !pad && h0 - group + per_warp > a.heads[0]) slot = row_slot(a, row, &page, &token);
+
+    // this lane's cosines and sines, and how it is rotated: with the lane that
+    // holds the other half (sign +-1), within itself, or not at all (0)
+    float c[8], s[8];
+    int partner = lane;
+    float sign = 0.0f;
+    if (a.cos_sin && angle && chunk * 8 < a.rope_dim) {
+        const float *cs = a.cos_sin + (long long)p * a.rope_dim, *sn = cs + a.rope_dim / 2;
+        if (a.interleaved) {
+            const float4 cc = __ldg(reinterpret_cast<const float4 *>(cs + chunk * 4));
+            const float4 ss = __ldg(reinterpret_cast<const float4 *>(sn + chunk * 4));
+            c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
+            s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
+            sign = 1.0f;
+        } else {
+            const int half = a.rope_dim / 16, first = chunk < half ? chunk : chunk - half;
+            load8(cs + first * 8, c);
+            load8(sn + first * 8, s);
+            partner = lane + (chunk < half ? half : -half);
+            sign = chunk < half ? -1.0f : 1.0f;
+        }
+    }
+
+#pragma unroll
+    for (int i = 0; i < kHeadsPerLane; ++i) {
+        // the shuffles below are the whole warp's: every lane goes through
+        // them, whatever its head is
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[i][e];
+        const T *w = kind[i] < 2 ? static_cast<const T *>(a.weight[kind[i]]) : nullptr;
+        if (a.weight[0] || a.weight[1]) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+            for (int o = lanes_per_head >> 1; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+            if (w && has) {
+                const float inv = 1.0f / sqrtf(ss / (float)D + a.eps);
+                float g[8];
+                load8(w + chunk * 8, g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * g[e];
+            }
+        }
+        if (a.cos_sin) {
+            if (a.interleaved) {
+                if (kind[i] < 2 && sign != 0.0f) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float u = y[2 * e], v = y[2 * e + 1];
+                        y[2 * e] = u * c[e] - v * s[e];
+                        y[2 * e + 1] = v * c[e] + u * s[e];
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float o = __shfl_sync(kFullMask, y[e], partner);
+                    if (kind[i] < 2 && sign != 0.0f) y[e] = y[e] * c[e] + sign * o * s[e];
+                }
+            }
+        }
+        if (!kCache || kind[i] == 0) {
+            if (kind[i] < 2 && has && angle)
+                store8(static_cast<T *>(a.out[kind[i]]) + row * a.ld_out[kind[i]] +
+                           (long long)head[i] * D + chunk * 8,
+                       y);
+            if (!kCache) continue;
+        }
+        if constexpr (kCache) {
+            const bool write = has && slot && (kind[i] == 2 || (kind[i] == 1 && angle));
+            unsigned char *base = kind[i] == 1 ? a.cache.k : a.cache.v;
+            const long long at = kv_offset(a.cache, page, token, head[i]) + chunk * 8;
+            if constexpr (std::is_same<C, e4m3>::value) {
+                unsigned m = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+                for (int o = lanes_per_head >> 1; o; o >>= 1)
+                    m = max(m, __shfl_xor_sync(kFullMask, m, o));
+                if (write) {
+                    const float scale = e4m3_scale(m);
+                    uint2 codes = make_uint2(0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const unsigned two = e4m3_pair(__fdiv_rn(y[2 * e], scale),
+                                                       __fdiv_rn(y[2 * e + 1], scale));
+                        (e < 2 ? codes.x : codes.y) |= two << (16 * (e & 1));
+                    }
+                    *reinterpret_cast<uint2 *>(base + at) = codes;
+                    if (chunk == 0) {
+                        (kind[i] == 1 ? a.cache.k_scale
+                                      : a.cache.v_scale)[kv_scale_offset(a.cache, page, token, head[i])] = scale;
+                        if (m >= 0x7F800000u) flag(a.status, DSPARK_STATUS_BAD_INPUT);
+                    }
+                }
+            } else {
+                if (write) store8(reinterpret_cast<C *>(base) + at, y);
+            }
+        }
+    }
+}
+
+// Any layout: one warp a (row, head).  Every element and its rotation partner
+// are read before the first is written, so the call may run in place.
+template <typename T, typename C>
+__global__ void __launch_bounds__(kAppendThreads) append_any_kernel(AppendArgs a) {
+    constexpr bool kCache = !std::is_same<C, NoCache>::value;
+    constexpr int kSteps = DSPARK_MAX_HEAD_DIM / 32;
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, D = a.head_dim;
+    const int H = a.heads[0] + a.heads[1] + a.heads[2];
+    const long long unit = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const long long row64 = div_nonneg(unit, H);
+    if (row64 >= rows_of(a)) return;
+    const int row = (int)row64;
+    int head = (int)(unit - row64 * H), kind = 0;
+    while (head >= a.heads[kind]) head -= a.heads[kind++];
+    if (a.req && __ldg(a.req + row) < 0) return;
+    int p;
+    if (kind < 2 && !row_angle(a, row, &p)) return;
+    int page = -1, token = 0;
+    if (kCache && kind > 0 && !row_slot(a, row, &page, &token)) return;
+
+    const T *src = static_cast<const T *>(a.in[kind]) + row * a.ld_in[kind] + (long long)head * D;
+    const T *w = kind < 2 ? static_cast<const T *>(a.weight[kind]) : nullptr;
+    const int R = kind < 2 && a.cos_sin ? a.rope_dim : 0;
+    float y[kSteps], other[kSteps], ss = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kSteps; ++t) {
+        const int d = lane + 32 * t;
+        y[t] = d < D ? elem_value(src[d]) : 0.0f;
+        ss = fmaf(y[t], y[t], ss);
+        const int o = a.interleaved ? d ^ 1 : (d < R / 2 ? d + R / 2 : d - R / 2);
+        other[t] = d < R ? elem_value(src[o]) * (w ? elem_value(w[o]) : 1.0f) : 0.0f;
+        if (d < D && w) y[t] *= elem_value(w[d]);
+    }
+    float inv = 1.0f;
+    if (w) {
+        for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+        inv = 1.0f / sqrtf(ss / (float)D + a.eps);
+    }
+    unsigned m = 0;
+#pragma unroll
+    for (int t = 0; t < kSteps; ++t) {
+        const int d = lane + 32 * t;
+        y[t] *= inv;
+        if (d < R) {
+            const int i = a.interleaved ? d >> 1 : (d < R / 2 ? d : d - R / 2);
+            const bool first = a.interleaved ? !(d & 1) : d < R / 2;
+            const float *cs = a.cos_sin + (long long)p * R;
+            const float c = __ldg(cs + i), s = __ldg(cs + R / 2 + i);
+            y[t] = y[t] * c + (first ? -1.0f : 1.0f) * (other[t] * inv) * s;
+        }
+        m = max(m, __float_as_uint(y[t]) & 0x7FFFFFFFu);
+    }
+    __syncwarp();
+    if (!kCache || kind == 0) {
+        T *dst = static_cast<T *>(a.out[kind]) + row * a.ld_out[kind] + (long long)head * D;
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t)
+            if (lane + 32 * t < D) elem_store(dst + lane + 32 * t, y[t]);
+        return;
+    }
+    if constexpr (kCache) {
+        unsigned char *base = kind == 1 ? a.cache.k : a.cache.v;
+        const long long at = kv_offset(a.cache, page, token, head);
+        float scale = 1.0f;
+        if constexpr (std::is_same<C, e4m3>::value) {
+            for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(kFullMask, m, o));
+            scale = e4m3_scale(m);
+            if (lane == 0) {
+                (kind == 1 ? a.cache.k_scale
+                           : a.cache.v_scale)[kv_scale_offset(a.cache, page, token, head)] = scale;
+                if (m >= 0x7F800000u) flag(a.status, DSPARK_STATUS_BAD_INPUT);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < kSteps; ++t) {
+            const int d = lane + 32 * t;
+            if (d >= D) continue;
+            if constexpr (std::is_same<C, e4m3>::value)
+                base[at + d] = (unsigned char)(e4m3_pair(__fdiv_rn(y[t], scale), 0.0f) & 0xFF);
+            else
+                elem_store(reinterpret_cast<C *>(base) + at + d, y[t]);
+        }
+    }
+}
+
+struct ReadArgs {
+    KvView cache;
+    const int32_t *start, *cu;
+    int B, max_rows;
+    void *out[2];
+    long long ld_out;
+    int32_t *status;
+};
+
+// kVec elements a thread and step: 8 where rows, slots and head size allow
+// 16-byte loads (8-byte ones of E4M3 codes), else 1.
+template <typename C, typename T, int kVec>
+__global__ void __launch_bounds__(kReadThreads) read_kernel(ReadArgs a) {
+    __shared__ int pages[kReadRows], tokens[kReadRows];
+    pdl_trigger();
+    pdl_wait();
+    const int row0 = blockIdx.x * kReadRows;
+    const int total = __ldg(a.cu + a.B);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && total > a.max_rows)
+        flag(a.status, DSPARK_STATUS_CAPACITY);
+    const int rows = min(total, a.max_rows);
+    if (row0 >= rows) return;
+    if (threadIdx.x < kReadRows) {
+        const int row = row0 + threadIdx.x;
+        int page = -1, token = 0;
+        if (row < rows) {
+            // the last request that starts at or before the row
+            int lo = 0, hi = a.B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (__ldg(a.cu + mid) <= row) lo = mid;
+                else hi = mid - 1;
+            }
+            page = kv_page(a.cache, lo, (long long)__ldg(a.start + lo) + (row - __ldg(a.cu + lo)), &token);
+            if (page < 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+        }
+        pages[threadIdx.x] = page;
+        tokens[threadIdx.x] = token;
+    }
+    __syncthreads();
+    const int D = a.cache.head_dim, per_head = D / kVec, per_row = a.cache.n_kv_heads * per_head;
+    const int n = min(kReadRows, rows - row0) * per_row;
+    const C *src[2] = {reinterpret_cast<const C *>(a.cache.k), reinterpret_cast<const C *>(a.cache.v)};
+    const float *scales[2] = {a.cache.k_scale, a.cache.v_scale};
+#pragma unroll 2
+    for (int i = threadIdx.x; i < n; i += kReadThreads) {
+        const int j = i / per_row, at = i - j * per_row, head = at / per_head;
+        const int page = pages[j];
+        if (page < 0) continue;
+        const int d = (at - head * per_head) * kVec;
+        const long long from = kv_offset(a.cache, page, tokens[j], head) + d;
+        const long long to = (row0 + j) * a.ld_out + (long long)head * D + d;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float scale = 1.0f;
+            if constexpr (std::is_same<C, e4m3>::value)
+                scale = __ldg(scales[which] + kv_scale_offset(a.cache, page, tokens[j], head));
+            T *dst = static_cast<T *>(a.out[which]) + to;
+            if constexpr (kVec == 8) {
+                float x[8];
+                load8(src[which] + from, x);
+                if constexpr (std::is_same<C, e4m3>::value) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= scale;
+                }
+                store8(dst, x);
+            } else {
+                float x = elem_value(src[which][from]);
+                if constexpr (std::is_same<C, e4m3>::value) x *= scale;
+                elem_store(dst, x);
+            }
+        }
+    }
+}
+
+template <typename T, typename C>
+cudaError_t launch_append(const AppendArgs &a, bool vec, cudaStream_t stream) {
+    const int H = a.heads[0] + a.heads[1] + a.heads[2];
+    constexpr int kWarps = kAppendThreads / 32;
+    if (vec) {
+        const int lanes = a.head_dim <= 64 ? 8 : (a.head_dim <= 128 ? 16 : 32);
+        const int per_warp = 32 / lanes * kHeadsPerLane;
+        const long long units = (long long)a.max_rows * ((H + per_warp - 1) / per_warp);
+        const long long grid = (units + kWarps - 1) / kWarps;
+        if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+        return launch_pdl(append_kernel<T, C>, dim3((unsigned)grid), dim3(kAppendThreads), 0,
+                          stream, a, lanes);
+    }
+    const long long grid = ((long long)a.max_rows * H + kWarps - 1) / kWarps;
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    return launch_pdl(append_any_kernel<T, C>, dim3((unsigned)grid), dim3(kAppendThreads), 0,
+                      stream, a);
+}
+
+template <typename T>
+cudaError_t launch_append_cache(const AppendArgs &a, int cache_dtype, bool vec, cudaStream_t st) {
+    if (cache_dtype < 0) return launch_append<T, NoCache>(a, vec, st);
+    if (cache_dtype == DSPARK_DTYPE_BF16) return launch_append<T, __nv_bfloat16>(a, vec, st);
+    if (cache_dtype == DSPARK_DTYPE_F32) return launch_append<T, float>(a, vec, st);
+    return launch_append<T, e4m3>(a, vec, st);
+}
+
+template <typename C, typename T>
+cudaError_t launch_read(const ReadArgs &a, bool vec, cudaStream_t stream) {
+    const dim3 grid((a.max_rows + kReadRows - 1) / kReadRows), block(kReadThreads);
+    if (vec) return launch_pdl(read_kernel<C, T, 8>, grid, block, 0, stream, a);
+    return launch_pdl(read_kernel<C, T, 1>, grid, block, 0, stream, a);
+}
+
+template <typename C>
+cudaError_t launch_read_out(const ReadArgs &a, int out_dtype, bool vec, cudaStream_t stream) {
+    if (out_dtype == DSPARK_DTYPE_BF16) return launch_read<C, __nv_bfloat16>(a, vec, stream);
+    return launch_read<C, float>(a, vec, stream);
+}
+
+namespace {
+
+// Whether p and a stride of ld elements keep 16-byte (E4M3: 8-byte) accesses of
+// eight elements aligned.
+bool eights(const void *p, long long ld, int elem_bytes) {
+    return aligned(p, elem_bytes == 1 ? 8 : 16) && ld % (elem_bytes == 4 ? 4 : 8) == 0;
+}
+
+bool cache_eights(const dspark_kv_cache &c) {
+    const int e = kv_elem_bytes(c.dtype);
+    return c.head_dim % 8 == 0 && eights(c.k, c.page_stride, e) && eights(c.v, c.token_stride, e) &&
+           eights(c.k, c.head_stride, e);
+}
+
+// The checks that the two writing calls share; fills the arguments they share.
+int fill_append(AppendArgs &a, const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                int32_t dtype, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                const dspark_norm_rope *nr, const int32_t *pos, const int32_t *totals,
+                int32_t max_rows, void *q_out, int64_t ld_q_out, int32_t *status) {
+    if (!status || max_rows < 0 || n_q_heads < 0 || n_kv_heads < 0) return DSPARK_ERR_INVALID_ARG;
+    if (dtype != DSPARK_DTYPE_BF16 && dtype != DSPARK_DTYPE_F32) return DSPARK_ERR_INVALID_ARG;
+    if (head_dim < 2 || head_dim > DSPARK_MAX_HEAD_DIM || head_dim % 2)
+        return DSPARK_ERR_UNSUPPORTED;
+    if ((n_q_heads > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr))
+        return DSPARK_ERR_INVALID_ARG;
+    if ((n_kv_heads > 0) != (k != nullptr)) return DSPARK_ERR_INVALID_ARG;
+    if (q && (ld_q < (int64_t)n_q_heads * head_dim || ld_q_out < (int64_t)n_q_heads * head_dim))
+        return DSPARK_ERR_INVALID_ARG;
+    if (k && ld_k < (int64_t)n_kv_heads * head_dim) return DSPARK_ERR_INVALID_ARG;
+    a = AppendArgs{};
+    if (nr) {
+        if (!(nr->eps >= 0.0f)) return DSPARK_ERR_INVALID_ARG;
+        if (nr->cos_sin) {
+            if (!pos || nr->n_pos < 0 || nr->rope_dim < 2 || nr->rope_dim > head_dim ||
+                nr->rope_dim % 2)
+                return DSPARK_ERR_INVALID_ARG;
+            a.cos_sin = nr->cos_sin;
+            a.n_pos = nr->n_pos;
+            a.rope_dim = nr->rope_dim;
+            a.interleaved = nr->interleaved != 0;
+        }
+        a.weight[0] = nr->q_weight;
+        a.weight[1] = nr->k_weight;
+        a.eps = nr->eps;
+    }
+    a.in[0] = q;
+    a.in[1] = k;
+    a.ld_in[0] = ld_q;
+    a.ld_in[1] = ld_k;
+    a.heads[0] = n_q_heads;
+    a.heads[1] = n_kv_heads;
+    a.out[0] = q_out;
+    a.ld_out[0] = ld_q_out;
+    a.pos = pos;
+    a.totals = totals;
+    a.max_rows = max_rows;
+    a.head_dim = head_dim;
+    a.status = status;
+    return DSPARK_OK;
+}
+
+// Whether the shared operands allow append_kernel: eight elements a lane.
+bool append_eights(const AppendArgs &a, int dtype) {
+    const int e = kv_elem_bytes(dtype);
+    bool ok = a.head_dim % 8 == 0;
+    for (int i = 0; i < 3; ++i) ok = ok && eights(a.in[i], a.ld_in[i], e);
+    for (int i = 0; i < 2; ++i) ok = ok && eights(a.out[i], a.ld_out[i], e) && aligned(a.weight[i], 16);
+    if (a.cos_sin)  // half pairs: both halves whole lanes; neighbours: whole lanes
+        ok = ok && aligned(a.cos_sin, 16) && a.rope_dim % (a.interleaved ? 8 : 16) == 0;
+    return ok;
+}
+
+}  // namespace
+
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" int dspark_qk_norm_rope(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                   int32_t dtype, int32_t n_q_heads, int32_t n_kv_heads,
+                                   int32_t head_dim, const dspark_norm_rope *nr,
+                                   const int32_t *pos, const int32_t *totals, int32_t max_rows,
+                                   void *q_out, int64_t ld_q_out, void *k_out, int64_t ld_k_out,
+                                   int32_t *status, void *stream) {
+    AppendArgs a;
+    if (!nr || (!q && !k) || (k != nullptr) != (k_out != nullptr)) return DSPARK_ERR_INVALID_ARG;
+    const int rc = fill_append(a, q, ld_q, k, ld_k, dtype, n_q_heads, n_kv_heads, head_dim, nr, pos,
+                               totals, max_rows, q_out, ld_q_out, status);
+    if (rc != DSPARK_OK) return rc;
+    if (k && ld_k_out < (int64_t)n_kv_heads * head_dim) return DSPARK_ERR_INVALID_ARG;
+    a.out[1] = k_out;
+    a.ld_out[1] = ld_k_out;
+    if (max_rows == 0) return DSPARK_OK;
+    const bool vec = append_eights(a, dtype);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == DSPARK_DTYPE_BF16
+                              ? launch_append_cache<__nv_bfloat16>(a, -1, vec, st)
+                              : launch_append_cache<float>(a, -1, vec, st);
+    return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+extern "C" int dspark_kv_append(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                const void *v, int64_t ld_v, int32_t dtype, int32_t n_q_heads,
+                                const dspark_kv_cache *cache, const dspark_norm_rope *nr,
+                                const int32_t *req, const int32_t *pos, const int32_t *cache_pos,
+                                const int32_t *totals, int32_t max_rows, void *q_out,
+                                int64_t ld_q_out, int32_t *status, void *stream) {
+    int rc = kv_check(cache);
+    if (rc != DSPARK_OK) return rc;
+    if (!k || !v || !req || (!pos && !cache_pos)) return DSPARK_ERR_INVALID_ARG;
+    AppendArgs a;
+    rc = fill_append(a, q, ld_q, k, ld_k, dtype, n_q_heads, cache->n_kv_heads, cache->head_dim, nr,
+                     pos, totals, max_rows, q_out, ld_q_out, status);
+    if (rc != DSPARK_OK) return rc;
+    if (ld_v < (int64_t)cache->n_kv_heads * cache->head_dim) return DSPARK_ERR_INVALID_ARG;
+    a.in[2] = v;
+    a.ld_in[2] = ld_v;
+    a.heads[2] = cache->n_kv_heads;
+    a.req = req;
+    a.cache_pos = cache_pos;
+    a.cache = kv_view(*cache);
+    if (max_rows == 0) return DSPARK_OK;
+    const bool vec = append_eights(a, dtype) && cache_eights(*cache);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == DSPARK_DTYPE_BF16
+                              ? launch_append_cache<__nv_bfloat16>(a, cache->dtype, vec, st)
+                              : launch_append_cache<float>(a, cache->dtype, vec, st);
+    return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+extern "C" int dspark_kv_read(const dspark_kv_cache *cache, const int32_t *start,
+                              const int32_t *cu_rows, int32_t B, int32_t max_rows,
+                              int32_t out_dtype, void *k_out, void *v_out, int64_t ld_out,
+                              int32_t *status, void *stream) {
+    const int rc = kv_check(cache);
+    if (rc != DSPARK_OK) return rc;
+    if (!start || !cu_rows || !k_out || !v_out || !status || max_rows < 0 || B < 1 ||
+        B > cache->n_requests || ld_out < (int64_t)cache->n_kv_heads * cache->head_dim)
+        return DSPARK_ERR_INVALID_ARG;
+    if (out_dtype != DSPARK_DTYPE_BF16 && out_dtype != DSPARK_DTYPE_F32)
+        return DSPARK_ERR_INVALID_ARG;
+    if ((long long)cache->n_kv_heads * cache->head_dim * kReadRows > 0x7FFFFFFF)
+        return DSPARK_ERR_UNSUPPORTED;
+    ReadArgs a;
+    a.cache = kv_view(*cache);
+    a.start = start;
+    a.cu = cu_rows;
+    a.B = B;
+    a.max_rows = max_rows;
+    a.out[0] = k_out;
+    a.out[1] = v_out;
+    a.ld_out = ld_out;
+    a.status = status;
+    const int e = kv_elem_bytes(out_dtype);
+    const bool vec = cache_eights(*cache) && eights(k_out, ld_out, e) && eights(v_out, ld_out, e);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (max_rows == 0) return DSPARK_OK;
+    cudaError_t err;
+    if (cache->dtype == DSPARK_DTYPE_BF16)
+        err = launch_read_out<__nv_bfloat16>(a, out_dtype, vec, st);
+    else if (cache->dtype == DSPARK_DTYPE_F32)
+        err = launch_read_out<float>(a, out_dtype, vec, st);
+    else
+        err = launch_read_out<e4m3>(a, out_dtype, vec, st);
+    return err == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}

@@ -612,6 +612,161 @@ DSPARK_API int dspark_sts_fit(const float *rec_logits, const int32_t *rec_correc
                               int64_t *n_obs, void *workspace, size_t workspace_bytes,
                               int32_t *status, void *stream);
 
+/* --------------------------------------------- verify window over a cache
+ *
+ * What a target layer does with the packed window between the pack and the
+ * accept ([ROUND] §三, §四: the target forward over the compact verify rows
+ * at their own positions): norms and rotation of queries and keys, the write
+ * of the drafted tokens' keys and values into a paged cache, and attention
+ * of the drafted tokens over that cache.  The pages describe no kernel for
+ * these; the formulas are below.  Every index (requests, positions, window
+ * lengths) is read on the device, from the pack's outputs. */
+
+#define DSPARK_DTYPE_E4M3 2 /* 8-bit cache entries: 4 exponent, 3 mantissa bits, +-448, no infinity */
+#define DSPARK_MAX_HEAD_DIM 256
+#define DSPARK_MAX_WINDOW 32 /* drafted tokens of one request in dspark_tree_attention */
+
+/* One layer's paged cache (host struct pointing at DEVICE memory).  Position
+ * p of request r lies in page g = block_table[r * table_width + p / page_size]
+ * at token p % page_size; element d of head h is at
+ *   g * page_stride + (p % page_size) * token_stride + h * head_stride + d
+ * elements from k (and from v: both have the same layout), so either order of
+ * tokens and heads inside a page is a choice of strides.  An E4M3 entry has
+ * one fp32 scale for each token and head, at
+ *   (g * n_kv_heads + h) * page_size + p % page_size
+ * of k_scale / v_scale, and stands for code * scale. */
+typedef struct {
+    int32_t dtype;       /* DSPARK_DTYPE_BF16, _F32 or _E4M3 */
+    int32_t n_pages;     /* pages in the pool, >= 1 */
+    int32_t page_size;   /* tokens a page, >= 1 */
+    int32_t n_kv_heads;  /* >= 1 */
+    int32_t head_dim;    /* 2..DSPARK_MAX_HEAD_DIM, even */
+    int32_t n_requests;  /* rows of block_table, >= 1 */
+    int32_t table_width; /* pages a row of block_table lists, >= 1 */
+    int64_t page_stride, token_stride, head_stride; /* elements, >= 0 */
+    void *k, *v;
+    float *k_scale, *v_scale;   /* E4M3 only, else NULL */
+    const int32_t *block_table; /* [n_requests, table_width] */
+} dspark_kv_cache;
+
+/* Norm and rotation of one call (host struct).  In 32 bits, rounded once at
+ * the end, for each row and head:
+ *   y_d = x_d / sqrt(mean(x^2) + eps) * weight_d    (weight given, else y = x)
+ *   the first rope_dim elements in pairs (a, b), pair i with the cosine
+ *   c = cos_sin[pos * rope_dim + i] and the sine s = cos_sin[pos * rope_dim +
+ *   rope_dim / 2 + i]:  (a, b) -> (a c - b s, b c + a s). */
+typedef struct {
+    const void *q_weight, *k_weight; /* [head_dim], type of the rows; NULL = no norm */
+    float eps;                       /* >= 0 */
+    const float *cos_sin;            /* device [n_pos, rope_dim]; NULL = no rotation */
+    int32_t n_pos;
+    int32_t rope_dim;                /* even, 2..head_dim (ignored without cos_sin) */
+    int32_t interleaved;             /* pair i: 0 = elements (i, i + rope_dim/2), 1 = (2i, 2i+1) */
+} dspark_norm_rope;
+
+/* Norms and rotation of queries and keys, in one pass.
+ *   q, k         [max_rows, heads * head_dim] rows of `dtype` (BF16 or F32), ld_*
+ *                elements apart (slices of one projection's rows will do).
+ *                Either may be NULL with its output (and 0 heads)
+ *   q_out, k_out outputs of the same type; may be q and k themselves (in
+ *                place) and must not overlap them in any other way
+ *   pos          device [max_rows] int32: the rows' positions (the pack's
+ *                packed_pos); may be NULL without cos_sin
+ *   totals       device int32 (nullable): rows from totals[0] on are pads and
+ *                left alone; NULL = all max_rows rows
+ * A row whose position is outside [0, n_pos) is not written and flags
+ * DSPARK_STATUS_BAD_INDEX.
+ * Errors: INVALID_ARG (null pointer, dtype, a stride below a row's elements,
+ * negative counts, rope_dim odd or outside 2..head_dim, eps negative or NaN);
+ * UNSUPPORTED (head_dim odd or outside 2..DSPARK_MAX_HEAD_DIM); CUDA. */
+DSPARK_API int dspark_qk_norm_rope(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                   int32_t dtype, int32_t n_q_heads, int32_t n_kv_heads,
+                                   int32_t head_dim, const dspark_norm_rope *nr /* host */,
+                                   const int32_t *pos, const int32_t *totals, int32_t max_rows,
+                                   void *q_out, int64_t ld_q_out, void *k_out, int64_t ld_k_out,
+                                   int32_t *status, void *stream);
+
+/* The same pass with the keys, and the values as they are, going into the
+ * cache.
+ *   k, v         [max_rows, n_kv_heads * head_dim] rows of `dtype`
+ *   q, q_out     as above; NULL with n_q_heads = 0 when only the cache is written
+ *   nr           host, nullable: keys (and queries) are written unchanged
+ *   req          device [max_rows]: a row's request (the pack's packed_req); a
+ *                negative one marks a pad row, which is left alone
+ *   pos          device [max_rows]: positions for the rotation
+ *   cache_pos    device [max_rows] (nullable: pos): positions in the cache.  A
+ *                tree's nodes rotate by depth and are stored in window order
+ * An E4M3 entry: scale = max(max_d |x_d| / 448, 2^-100), codes x / scale
+ * rounded to nearest even, all from the 32-bit values.  A head with a NaN or
+ * an infinity reads back as NaN and flags DSPARK_STATUS_BAD_INPUT.
+ * A request >= n_requests, a cache position outside the block table or a page
+ * outside the pool flags DSPARK_STATUS_BAD_INDEX, and that row's keys and
+ * values are not written.  Two rows of a call must not share a slot.
+ * Errors as above, and for the cache: INVALID_ARG (null pointers, dtype,
+ * counts < 1, negative strides, E4M3 without scales). */
+DSPARK_API int dspark_kv_append(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                const void *v, int64_t ld_v, int32_t dtype, int32_t n_q_heads,
+                                const dspark_kv_cache *cache /* host */,
+                                const dspark_norm_rope *nr /* host */, const int32_t *req,
+                                const int32_t *pos, const int32_t *cache_pos,
+                                const int32_t *totals, int32_t max_rows, void *q_out,
+                                int64_t ld_q_out, int32_t *status, void *stream);
+
+/* Cache entries back as rows: positions start[r], start[r]+1, ... of request
+ * r < B go to rows cu_rows[r]..cu_rows[r+1]-1.
+ *   start        device [B]; cu_rows device [B+1], ascending from 0
+ *   k_out, v_out [max_rows, n_kv_heads * head_dim] rows of out_dtype (BF16 or
+ *                F32), ld_out elements apart: code * scale in 32 bits,
+ *                rounded once
+ * Rows from min(cu_rows[B], max_rows) on are left alone (CAPACITY if cu_rows[B]
+ * is larger); a position outside the block table or a page outside the pool
+ * flags BAD_INDEX and its row is not written.
+ * Errors: INVALID_ARG (null pointer, B outside 1..n_requests, out_dtype,
+ * ld_out below a row, max_rows < 0, the cache's); UNSUPPORTED (head_dim); CUDA. */
+DSPARK_API int dspark_kv_read(const dspark_kv_cache *cache /* host */, const int32_t *start,
+                              const int32_t *cu_rows, int32_t B, int32_t max_rows,
+                              int32_t out_dtype, void *k_out, void *v_out, int64_t ld_out,
+                              int32_t *status, void *stream);
+
+/* Workspace of dspark_tree_attention, for any number of requests, rows and
+ * positions; need not be cleared. */
+DSPARK_API size_t dspark_tree_attention_workspace_bytes(int32_t n_q_heads, int32_t head_dim);
+
+/* Attention of the drafted tokens over the cache that holds their requests'
+ * prefixes and the tokens themselves (dspark_kv_append first).  Packed row
+ * cu_seqlens[r] + i is token i of request r's window of L <= 32 tokens, at
+ * cache position prefix_lens[r] + i.  It sees every position below
+ * prefix_lens[r], and token j of the window iff bit j of its ancestors word is
+ * set (j < L); ancestors NULL = a chain, bits 0..i.  For query head h, with
+ * kv head h / (n_q_heads / n_kv_heads), over the visible positions p:
+ *   s_p = scale * q . k_p    m = max s_p    l = sum exp(s_p - m)
+ *   out = sum exp(s_p - m) v_p / l          lse = m + ln l
+ * A row that sees nothing gets out = 0 and lse = -inf.  What a row does not
+ * see has no effect on it, NaN and infinities included.
+ *   q, out       [max_rows, n_q_heads * head_dim] rows of `dtype` (BF16 or
+ *                F32), ld_* elements apart
+ *   lse          [max_rows, n_q_heads] fp32, nullable
+ *   prefix_lens  device [B], >= 0; cu_seqlens device [B+1]; window length 0 is
+ *                a request without rows
+ * Sums and softmax statistics are held in 32 bits.  BF16 rows over a BF16 or
+ * E4M3 cache with head_dim 64 or 128, page_size a multiple of 16 and 16-byte
+ * aligned layouts run on the tensor cores, the weights exp(s - m) rounded to
+ * the 16-bit type of the products; anything else in 32 bits throughout.
+ * A window of more than 32 tokens or outside max_rows (BAD_LEN), and positions
+ * past the block table or a page outside the pool (BAD_INDEX): that request's
+ * rows are unspecified, the others not affected.  Rows of no request are left
+ * alone.
+ * Errors: INVALID_ARG (null pointer, B outside 1..n_requests, n_q_heads not a
+ * positive multiple of n_kv_heads, dtype, a stride below a row, max_rows < 0,
+ * scale not finite, the cache's); UNSUPPORTED (head_dim); WORKSPACE; CUDA. */
+DSPARK_API int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype, int32_t n_q_heads,
+                                     int32_t max_rows, const int32_t *cu_seqlens,
+                                     const int32_t *prefix_lens, int32_t B,
+                                     const uint32_t *ancestors, float scale,
+                                     const dspark_kv_cache *cache /* host */, void *out,
+                                     int64_t ld_out, float *lse, void *workspace,
+                                     size_t workspace_bytes, int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
