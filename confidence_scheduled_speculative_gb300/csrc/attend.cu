@@ -12,6 +12,9 @@
 //   position, each with a running maximum and sum, joined at the end.
 
 #include "kvcache.cuh"
+#include "tensor.cuh"
+
+#include <atomic>
 
 namespace dspark {
 
@@ -156,13 +159,695 @@ cudaError_t launch_any(const AttendArgs &a, int cache_dtype, cudaStream_t stream
     return launch_pdl(attend_any_kernel<T, e4m3>, grid, block, 0, stream, a);
 }
 
+// ------------------------------------------------- tensor-core kernel
+
+constexpr int kTile = 64;           // positions a step
+constexpr int kRowsPerTile = 128;   // (token, query head) rows of one kv head
+constexpr int kMaxCtas = 320;       // two for each of up to 160 SMs
+constexpr int kTensorThreads = 192; // softmax warps 0-3, copy warp 4, matrix warp 5
+constexpr int kTmemCols = 256;      // two score tiles of 64, the output's up to 128
+constexpr float kLazy = 8.0f;       // log2 of how far weights may grow past 1
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kDescInts = 8;
+constexpr int kSmemSlot64 = 20, kSmemSlot128 = 21;
+
+struct TensorArgs {
+    AttendArgs a;
+    int group, box;
+    float *part_o;   // [2 kMaxCtas][D / 4][128] float4
+    float *part_ml;  // [2 kMaxCtas][2][128]
+    int *desc;       // [kMaxCtas][kDescInts]: the split job that begins in a CTA
+};
+
+template <int D>
+struct TensorSmem {
+    static constexpr int kQBytes = kRowsPerTile * D * 2;
+    static constexpr int kBufBytes = kTile * D * 2;
+    static constexpr int kBufs = D == 128 ? 5 : 9;
+    static constexpr int kControl = kQBytes + kBufs * kBufBytes;
+    static constexpr int kTotal = kControl + 1024;
+};
+
+// The barriers and words behind the buffers.  A wait tells a phase from the next
+// one only; the barriers that come in twos serve every other tile, so that a
+// role one tile behind another still waits for the phase it means.
+struct Control {
+    unsigned long long full[9], empty[9], s_full[2], p_ready[2], o_done[2], q_full, drain;
+    unsigned tmem, nonfinite;
+    int abort;
+    int start_r;
+    long long start_off, total;
+    long long scan[40];
+};
+
+// A request's jobs: every (kv head, 128 rows) pair reads all its tiles.
+struct Request {
+    int row0, len, P, tiles, row_tiles;
+};
+
+__device__ __forceinline__ bool load_request(const TensorArgs &t, int r, Request *q, bool report) {
+    if (!window_of(t.a, r, &q->row0, &q->len, &q->P, report)) return false;
+    q->tiles = (q->P + q->len + kTile - 1) / kTile;
+    q->row_tiles = (q->len * t.group + kRowsPerTile - 1) / kRowsPerTile;
+    return true;
+}
+
+// The first tile of CTA c when T tiles are dealt to n CTAs, and the CTA of a tile.
+__device__ __forceinline__ long long first_tile(long long c, long long T, int n) { return c * T / n; }
+__device__ __forceinline__ int cta_of(long long tile, long long T, int n) {
+    return (int)(((tile + 1) * n - 1) / T);
+}
+
+// Consecutive tiles of one job that a CTA works through.
+struct Segment {
+    Request q;
+    int r, head, row_tile, first, count;
+};
+
+// Walks a CTA's tiles job by job: requests in order, in each the kv heads, in
+// each the row tiles (which read the same keys and values, so the later ones
+// find them in L2).  Every warp role walks on its own and sees the same.
+struct Walk {
+    long long left;
+    Request q;
+    int r, head, row_tile, tile;
+
+    __device__ __forceinline__ void begin(const TensorArgs &t, int r0, long long off, long long n) {
+        left = n;
+        r = r0;
+        if (n <= 0) return;
+        load_request(t, r, &q, false);
+        const long long job = off / q.tiles;
+        tile = (int)(off - job * q.tiles);
+        head = (int)(job / q.row_tiles);
+        row_tile = (int)(job - (long long)head * q.row_tiles);
+    }
+    __device__ __forceinline__ bool next(const TensorArgs &t, Segment *s) {
+        if (left <= 0) return false;
+        s->q = q;
+        s->r = r;
+        s->head = head;
+        s->row_tile = row_tile;
+        s->first = tile;
+        s->count = (int)min((long long)(q.tiles - tile), left);
+        left -= s->count;
+        tile = 0;
+        if (++row_tile == q.row_tiles) {
+            row_tile = 0;
+            if (++head == t.a.cache.n_kv_heads) {
+                head = 0;
+                if (left > 0)
+                    while (!load_request(t, ++r, &q, false)) {
+                    }
+            }
+        }
+        return true;
+    }
+};
+
+// Ring position of a segment's loads, in the order they are used:
+// K0, K1, V0, K2, V1, ..., V(n-1).
+__device__ __forceinline__ int ring_v(int tile, int n) { return tile < n - 1 ? 2 * tile + 2 : 2 * n - 1; }
+
+template <int D>
+__global__ void __launch_bounds__(kTensorThreads, 2)
+attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const TensorArgs t) {
+    using S = TensorSmem<D>;
+    constexpr int kHalves = D / 64;       // 128-byte columns blocks of a row
+    constexpr int kChunks = D / 8;        // 16-byte chunks of a row
+    constexpr int kHalfBytes = kTile * 128;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Control &ctl = *reinterpret_cast<Control *>(smem + S::kControl);
+    const AttendArgs &a = t.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_addr(smem);
+    const uint32_t ring = base + S::kQBytes;
+
+    pdl_wait();
+    pdl_trigger();
+
+    // this CTA's share of all tiles: each thread sums a run of requests, a scan
+    // over the threads finds the request that holds the first of its tiles
+    const int per = (a.B + kTensorThreads - 1) / kTensorThreads;
+    long long mine = 0;
+    for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r) {
+        Request q;
+        if (load_request(t, r, &q, blockIdx.x == 0))
+            mine += (long long)q.tiles * q.row_tiles * a.cache.n_kv_heads;
+    }
+    long long T;
+    const long long before = block_exclusive_scan<long long>(mine, ctl.scan, &T);
+    const int n_ctas = (int)min((long long)gridDim.x, T);
+    const int cta = blockIdx.x;
+    if (tid == 0) t.desc[cta * kDescInts] = 0;
+    if (cta >= n_ctas) return;
+    const long long lo = first_tile(cta, T, n_ctas), hi = first_tile(cta + 1, T, n_ctas);
+    if (lo >= before && lo < before + mine) {
+        long long at = before;
+        for (int r = tid * per;; ++r) {
+            Request q;
+            if (!load_request(t, r, &q, false)) continue;
+            const long long n = (long long)q.tiles * q.row_tiles * a.cache.n_kv_heads;
+            if (lo < at + n) {
+                ctl.start_r = r;
+                ctl.start_off = lo - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    if (tid == 0) {
+        for (int i = 0; i < S::kBufs; ++i) {
+            mbar_init(smem_addr(&ctl.full[i]), 1);
+            mbar_init(smem_addr(&ctl.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&ctl.s_full[i]), 1);
+            mbar_init(smem_addr(&ctl.p_ready[i]), 4);
+            mbar_init(smem_addr(&ctl.o_done[i]), 1);
+        }
+        mbar_init(smem_addr(&ctl.q_full), 128);
+        mbar_init(smem_addr(&ctl.drain), 1);
+        ctl.abort = 0;
+        ctl.nonfinite = 0;
+        fence_mbar_init();
+    }
+    if (warp == 5) tmem_alloc(smem_addr(&ctl.tmem), kTmemCols);
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = ctl.tmem, tmem_o = tmem + 2 * kTile;
+    volatile int *abort = &ctl.abort;
+    Walk walk;
+    walk.begin(t, ctl.start_r, ctl.start_off, hi - lo);
+    Segment s;
+    unsigned loads = 0;  // ring position of the segment's first load
+
+    if (warp == 4) {
+        // ------------------------------------------------ copy warp
+        const int boxes = kTile / t.box, box = lane / kHalves, half = lane % kHalves;
+        const bool issues = box < boxes;
+        bool ok = true;
+        // where this lane's box of tile j lies: a page outside the pool (past
+        // the request's end too) arrives as zeros
+        auto find = [&](const Segment &s, int j, int *page, int *token) {
+            const int pos = j * kTile + box * t.box;
+            *page = a.cache.n_pages;
+            *token = 0;
+            if (issues && pos < s.q.P + s.q.len) {
+                const int g = kv_page(a.cache, s.r, pos, token);
+                if (g >= 0) *page = g;
+                else flag(a.status, DSPARK_STATUS_BAD_INDEX);
+            }
+        };
+        auto load = [&](const CUtensorMap *map, int head, int page, int token) {
+            const unsigned slot = loads % S::kBufs, phase = loads / S::kBufs & 1;
+            ok = ok && role_wait(smem_addr(&ctl.empty[slot]), phase ^ 1, abort, a.status);
+            ok = __all_sync(kFullMask, ok);
+            if (!ok) return;
+            const uint32_t bar = smem_addr(&ctl.full[slot]);
+            if (lane == 0) mbar_expect(bar, S::kBufBytes);
+            __syncwarp();
+            if (issues)
+                tma_load_4d(ring + slot * S::kBufBytes + half * kHalfBytes + box * t.box * 128, map,
+                            half * 64, token, head, page, bar);
+            ++loads;
+        };
+        while (ok && walk.next(t, &s)) {
+            int page, token, page1 = 0, token1 = 0;
+            find(s, s.first, &page, &token);
+            load(&map_k, s.head, page, token);
+            for (int i = 0; i < s.count && ok; ++i) {
+                if (i + 1 < s.count) {
+                    find(s, s.first + i + 1, &page1, &token1);
+                    load(&map_k, s.head, page1, token1);
+                    if (!ok) break;
+                }
+                load(&map_v, s.head, page, token);
+                page = page1;
+                token = token1;
+            }
+        }
+    } else if (warp == 5) {
+        // ---------------------------------------------- matrix warp
+        if (lane == 0) {
+            constexpr uint32_t word_qk = mma_word(true, kTile, false);
+            constexpr uint32_t word_pv = mma_word(true, D, true);
+            unsigned done = 0, seg = 0;  // tiles and segments so far
+            bool ok = true;
+            auto wait = [&](unsigned long long *bar, unsigned parity) {
+                ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
+                return ok;
+            };
+            auto qk = [&](unsigned tile, unsigned load) {
+                const unsigned slot = load % S::kBufs;
+                if (!wait(&ctl.full[slot], load / S::kBufs)) return;
+                tmem_fence_after();
+                const uint32_t buf = ring + slot * S::kBufBytes;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ss(tmem + (tile & 1) * kTile,
+                           smem_operand(base + (k / 4) * kRowsPerTile * 128 + (k % 4) * 32, 16),
+                           smem_operand(buf + (k / 4) * kHalfBytes + (k % 4) * 32, 16), word_qk, k > 0);
+                mma_commit(smem_addr(&ctl.empty[slot]));
+                mma_commit(smem_addr(&ctl.s_full[tile & 1]));
+            };
+            while (ok && walk.next(t, &s)) {
+                if (!wait(&ctl.q_full, seg)) break;
+                qk(done, loads);
+                for (int i = 0; i < s.count && ok; ++i) {
+                    const unsigned tile = done + i;
+                    if (i + 1 < s.count) {
+                        // its scores take the place of the weights before last
+                        if (i > 0 && !wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) break;
+                        qk(tile + 1, loads + 2 * i + 1);
+                    }
+                    const unsigned load = loads + ring_v(i, s.count), slot = load % S::kBufs;
+                    if (!wait(&ctl.full[slot], load / S::kBufs)) break;
+                    if (!wait(&ctl.p_ready[tile & 1], tile >> 1)) break;
+                    tmem_fence_after();
+                    const uint32_t buf = ring + slot * S::kBufBytes;
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_ts(tmem_o, tmem + (tile & 1) * kTile + k * 8,
+                               smem_operand(buf + k * 16 * 128, kHalfBytes), word_pv,
+                               i > 0 || k > 0);
+                    mma_commit(smem_addr(&ctl.empty[slot]));
+                    mma_commit(smem_addr(&ctl.o_done[tile & 1]));
+                }
+                done += s.count;
+                loads += 2 * s.count;
+                ++seg;
+            }
+            // after a timeout: products still under way write tensor memory and
+            // barriers of this block
+            if (!ok) {
+                mma_commit(smem_addr(&ctl.drain));
+                mbar_wait(smem_addr(&ctl.drain), 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------- softmax warps
+        const int m = tid;  // row of the tile, lane of tensor memory
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
+        const unsigned sign = a.scale < 0.0f ? 0x80008000u : 0u;
+        unsigned done = 0, seg = 0;
+        bool ok = true;
+        auto wait = [&](unsigned long long *bar, unsigned parity) {
+            ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
+            return ok;
+        };
+        while (ok && walk.next(t, &s)) {
+            const int n = s.q.P + s.q.len, rows = s.q.len * t.group;
+            const int row_base = s.row_tile * kRowsPerTile, row = row_base + m;
+            const bool valid = row < rows, active = row_base + warp * 32 < rows;
+            const int token = min(row, rows - 1) / t.group;
+            const int head = s.head * t.group + min(row, rows - 1) - token * t.group;
+            const int packed = s.q.row0 + token;
+            const unsigned bits = ancestors_of(a, packed, token, s.q.len);
+
+            // the tile's queries, swizzled; rows past the last are left as they
+            // are: a row of the product depends on its own query alone
+            named_sync(1, 128);
+            if (tid == 0) ctl.nonfinite = 0;
+            const int q_rows = min(kRowsPerTile, (rows - row_base + 31) & ~31);
+            for (int i = tid; i < q_rows * kChunks; i += 128) {
+                const int qr = i / kChunks, ch = i % kChunks;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row_base + qr < rows) {
+                    const int tok = (row_base + qr) / t.group;
+                    const int hq = s.head * t.group + (row_base + qr) - tok * t.group;
+                    v = __ldg(reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(a.q) + (s.q.row0 + tok) * a.ld_q +
+                        (long long)hq * D + ch * 8));
+                    v.x ^= sign, v.y ^= sign, v.z ^= sign, v.w ^= sign;
+                }
+                *reinterpret_cast<uint4 *>(smem + (ch / 8) * kRowsPerTile * 128 + qr * 128 +
+                                           ((ch % 8 ^ (qr & 7)) << 4)) = v;
+            }
+            fence_async_proxy();
+            mbar_arrive(smem_addr(&ctl.q_full));
+
+            float mx = -INFINITY, l = 0.0f;  // running maximum (times c) and sum
+            for (int i = 0; i < s.count; ++i) {
+                const unsigned tile = done + i, b = tile & 1;
+                const int p0 = (s.first + i) * kTile;
+                if (!wait(&ctl.s_full[b], tile >> 1)) break;
+                if (active) {
+                    tmem_fence_after();
+                    uint32_t x[kTile];
+                    tmem_load32(lanes + b * kTile, x);
+                    tmem_load32(lanes + b * kTile + 32, x + 32);
+                    tmem_wait_load(x);
+                    tmem_wait_load(x + 32);
+                    if (p0 + kTile > s.q.P) {
+                        // the tile reaches the window: prefix positions, then
+                        // this row's ancestors
+                        const int pre = max(s.q.P - p0, 0), skip = max(p0 - s.q.P, 0);
+                        const unsigned long long w = skip < 32 ? (unsigned long long)(bits >> skip) : 0;
+                        const unsigned long long sees = w << pre | ((1ull << pre) - 1);
+#pragma unroll
+                        for (int j = 0; j < kTile; ++j)
+                            if (!(sees >> j & 1)) x[j] = 0xFF800000u;
+                    }
+                    float top = __uint_as_float(x[0]);
+#pragma unroll
+                    for (int j = 1; j < kTile; ++j) top = fmaxf(top, __uint_as_float(x[j]));
+                    top *= c;
+                    // The maximum moves only when it grows by 2^kLazy: until then
+                    // the weights may pass 1, and the output stays as it is.
+                    const bool grow = top > mx + kLazy || (mx == -INFINITY && top > mx);
+                    if (__any_sync(kFullMask, grow)) {
+                        const float f = grow ? exp2_approx(mx - top) : 1.0f;
+                        if (grow) mx = top;
+                        l *= f;
+                        if (i > 0) {
+                            if (!wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) break;
+                            tmem_fence_after();
+#pragma unroll
+                            for (int h = 0; h < D / 32; ++h) {
+                                uint32_t o[32];
+                                tmem_load32(lanes + 2 * kTile + h * 32, o);
+                                tmem_wait_load(o);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_store32(lanes + 2 * kTile + h * 32, o);
+                            }
+                        }
+                    }
+                    const float shift = mx == -INFINITY ? 0.0f : mx;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    uint32_t w[kTile / 2];
+#pragma unroll
+                    for (int j = 0; j < kTile; j += 2) {
+                        const float u = exp2_approx(fmaf(__uint_as_float(x[j]), c, -shift));
+                        const float v = exp2_approx(fmaf(__uint_as_float(x[j + 1]), c, -shift));
+                        sum[j / 2 % 2 * 2] += u;
+                        sum[j / 2 % 2 * 2 + 1] += v;
+                        const __nv_bfloat162 two = __floats2bfloat162_rn(u, v);
+                        w[j / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_store32(lanes + b * kTile, w);
+                    tmem_wait_store();
+                }
+                if (p0 + kTile > s.q.P) {
+                    // Values past the request's end become zeros, and so do NaN
+                    // and infinities of the window (0 x NaN would reach rows that
+                    // do not see them); the rows that do get them at the end.
+                    const unsigned load = loads + ring_v(i, s.count), slot = load % S::kBufs;
+                    if (!wait(&ctl.full[slot], load / S::kBufs)) break;
+                    unsigned char *buf = smem + S::kQBytes + slot * S::kBufBytes;
+                    for (int j = tid; j < kTile * kChunks; j += 128) {
+                        const int tok = j / kChunks, ch = j % kChunks, pos = p0 + tok;
+                        if (pos < s.q.P) continue;
+                        uint4 *at = reinterpret_cast<uint4 *>(buf + (ch / 8) * kHalfBytes + tok * 128 +
+                                                              ((ch % 8 ^ (tok & 7)) << 4));
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (pos < n) {
+                            v = *at;
+                            unsigned *e = reinterpret_cast<unsigned *>(&v);
+                            bool bad = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const bool lo16 = (e[k] & 0x7F80u) == 0x7F80u;
+                                const bool hi16 = (e[k] & 0x7F800000u) == 0x7F800000u;
+                                bad = bad || lo16 || hi16;
+                                if (lo16) e[k] &= 0xFFFF0000u;
+                                if (hi16) e[k] &= 0x0000FFFFu;
+                            }
+                            if (!bad) continue;
+                            atomicOr(&ctl.nonfinite, 1u << (pos - s.q.P));
+                        }
+                        *at = v;
+                    }
+                    fence_async_proxy();
+                }
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[b]));
+            }
+            const unsigned last = done + s.count - 1;
+            if (!wait(&ctl.o_done[last & 1], last >> 1)) break;
+            done += s.count;
+            loads += 2 * s.count;
+            tmem_fence_after();
+
+            const bool whole = s.count == s.q.tiles;
+            const float shift = mx == -INFINITY ? 0.0f : mx;
+            const unsigned extra = *(volatile unsigned *)&ctl.nonfinite & bits;
+            const int slot = 2 * cta + (seg > 0);
+            if (active) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + packed * a.ld_out +
+                                     (long long)head * D;
+#pragma unroll 1
+                for (int h = 0; h < D / 32; ++h) {
+                    uint32_t o[32];
+                    tmem_load32(lanes + 2 * kTile + h * 32, o);
+                    tmem_wait_load(o);
+                    for (unsigned e = extra; e; e &= e - 1) {
+                        int tok;
+                        const int page = kv_page(a.cache, s.r, (long long)s.q.P + __ffs(e) - 1, &tok);
+                        if (page < 0) continue;
+                        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(a.cache.v) +
+                                                 kv_offset(a.cache, page, tok, s.head) + h * 32;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float y = elem_value(v[j]);
+                            if (!(y - y == 0.0f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + y);
+                        }
+                    }
+                    if (!whole) {
+                        float4 *part = reinterpret_cast<float4 *>(t.part_o) +
+                                       ((long long)slot * (D / 4) + h * 8) * kRowsPerTile + m;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            part[j * kRowsPerTile] =
+                                make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                            __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                    } else if (valid) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float u = __uint_as_float(o[2 * j]) * inv, v = __uint_as_float(o[2 * j + 1]) * inv;
+                            if (l == 0.0f) u = v = 0.0f;
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(u, v);
+                            w[j] = *reinterpret_cast<const uint32_t *>(&two);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            reinterpret_cast<uint4 *>(out + h * 32)[j] =
+                                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                    }
+                }
+                if (!whole) {
+                    t.part_ml[(long long)slot * 2 * kRowsPerTile + m] = mx;
+                    t.part_ml[((long long)slot * 2 + 1) * kRowsPerTile + m] = l;
+                } else if (valid && a.lse) {
+                    a.lse[(long long)packed * a.n_q_heads + head] =
+                        l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
+                }
+            }
+            tmem_fence_before();
+            ++seg;
+            // the job that begins here and ends in a later CTA, for the join
+            if (tid == 0 && walk.left <= 0) {
+                int *d = t.desc + cta * kDescInts;
+                if (s.first == 0 && !whole) {
+                    // its first tile's number is the CTA's last tile's, less the ones before it
+                    const long long g0 = hi - s.count;
+                    d[1] = cta_of(g0 + s.q.tiles - 1, T, n_ctas);
+                    d[2] = slot;
+                    d[3] = s.q.row0;
+                    d[4] = s.head;
+                    d[5] = row_base;
+                    d[6] = rows;
+                    d[0] = 1;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (ctl.abort && warp == 4 && lane == 0) {
+        // copies still under way write this block's buffers
+        const unsigned n = min(loads, (unsigned)S::kBufs);
+        for (unsigned i = loads - n; i < loads; ++i)
+            mbar_wait(smem_addr(&ctl.full[i % S::kBufs]), i / S::kBufs & 1);
+    }
+    if (warp == 5) tmem_free(tmem, kTmemCols);
+}
+
+// Joins the parts of the jobs that several CTAs share, in the CTAs' order: a
+// block a job (the CTA it begins in) and 32 columns, a lane a row, the warps
+// every eighth part.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const TensorArgs t) {
+    __shared__ float4 part[kJoinWarps][8][32];
+    __shared__ float part_l[kJoinWarps][32];
+    pdl_wait();
+    pdl_trigger();
+    const int *d = t.desc + blockIdx.x * kDescInts;
+    if (__ldcg(d) == 0) return;
+    const int c0 = blockIdx.x, c1 = __ldcg(d + 1), slot0 = __ldcg(d + 2), row0 = __ldcg(d + 3);
+    const int kv_head = __ldcg(d + 4), row_base = __ldcg(d + 5), rows = __ldcg(d + 6);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int in_tile = min(kRowsPerTile, rows - row_base);
+    for (int base = 0; base < in_tile; base += 32) {
+        const int m = base + lane;
+        auto ml = [&](int c, int which) {
+            const long long slot = c == c0 ? slot0 : 2 * c;
+            return __ldcg(t.part_ml + (slot * 2 + which) * kRowsPerTile + m);
+        };
+        float top = -INFINITY;
+        for (int c = c0; c <= c1; ++c) top = fmaxf(top, ml(c, 0));
+        const float shift = top == -INFINITY ? 0.0f : top;
+        float l = 0.0f;
+        float4 o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
+            const float f = exp2_approx(ml(c, 0) - shift);
+            l += f * ml(c, 1);
+            const long long slot = c == c0 ? slot0 : 2 * c;
+            const float4 *p = reinterpret_cast<const float4 *>(t.part_o) +
+                              (slot * (D / 4) + blockIdx.y * 8) * kRowsPerTile + m;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 x = __ldcg(p + j * kRowsPerTile);
+                o[j].x += f * x.x, o[j].y += f * x.y, o[j].z += f * x.z, o[j].w += f * x.w;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) part[warp][j][lane] = o[j];
+        part_l[warp][lane] = l;
+        __syncthreads();
+        // warp j joins columns 4j..4j+3
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float4 y = part[w][warp][lane];
+            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            l += part_l[w][lane];
+        }
+        __syncthreads();
+        if (m >= in_tile) continue;
+        const int row = row_base + m, token = row / t.group;
+        const int head = kv_head * t.group + row - token * t.group;
+        const long long packed = row0 + token;
+        const float inv = 1.0f / l;
+        if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+        const __nv_bfloat162 u = __floats2bfloat162_rn(x.x, x.y), v = __floats2bfloat162_rn(x.z, x.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
+                                   (long long)head * D + blockIdx.y * 32 + warp * 4) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
+        if (t.a.lse && blockIdx.y == 0 && warp == 0)
+            t.a.lse[packed * t.a.n_q_heads + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
+    }
+}
+
+namespace {
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once.
+EncodeFn encoder() {
+    static std::atomic<EncodeFn> kept{nullptr};
+    EncodeFn f = kept.load(std::memory_order_acquire);
+    if (f) return f;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+        return nullptr;
+    f = reinterpret_cast<EncodeFn>(p);
+    kept.store(f, std::memory_order_release);
+    return f;
+}
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
+// The cache as [page][head][token][element] with boxes of `box` tokens and 64
+// elements, rows of a box swizzled.
+bool encode(CUtensorMap *map, const dspark_kv_cache &c, void *p, int box) {
+    const EncodeFn f = encoder();
+    if (!f) return false;
+    const int e = kv_elem_bytes(c.dtype);
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
+                                (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * e, (cuuint64_t)c.head_stride * e,
+                                   (cuuint64_t)c.page_stride * e};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, boxes, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t part_o_bytes(int D) { return (size_t)2 * kMaxCtas * kRowsPerTile * D * 4; }
+size_t part_ml_bytes() { return (size_t)2 * kMaxCtas * kRowsPerTile * 2 * 4; }
+size_t desc_bytes() { return (size_t)kMaxCtas * kDescInts * 4; }
+
+// Whether a call runs on the tensor cores: 16-bit rows, head sizes whose
+// output and two score tiles fit half of tensor memory, boxes of whole 8-row
+// swizzle groups inside a page, and the strides and bases that TMA and the
+// 16-byte accesses take.
+bool tensor_fits(const AttendArgs &a, int dtype, const dspark_kv_cache &c) {
+    if (dtype != DSPARK_DTYPE_BF16 || c.dtype != DSPARK_DTYPE_BF16) return false;
+    if ((c.head_dim != 64 && c.head_dim != 128) || c.page_size % 16) return false;
+    const int e = kv_elem_bytes(c.dtype);
+    const int64_t strides[3] = {c.token_stride, c.head_stride, c.page_stride};
+    for (int64_t s : strides)
+        if (s * e % 16 || s < 1 || s * e >= (1ll << 40)) return false;
+    return aligned(c.k, 16) && aligned(c.v, 16) && aligned(a.q, 16) && aligned(a.out, 16) &&
+           a.ld_q % 8 == 0 && a.ld_out % 8 == 0;
+}
+
+template <int D>
+cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *workspace,
+                          int smem_slot, cudaStream_t stream) {
+    TensorArgs t;
+    t.a = a;
+    t.group = a.n_q_heads / c.n_kv_heads;
+    t.box = gcd(c.page_size, kTile);
+    unsigned char *w = static_cast<unsigned char *>(workspace);
+    t.part_o = reinterpret_cast<float *>(w);
+    t.part_ml = reinterpret_cast<float *>(w + part_o_bytes(D));
+    t.desc = reinterpret_cast<int *>(w + part_o_bytes(D) + part_ml_bytes());
+    CUtensorMap map_k, map_v;
+    if (!encode(&map_k, c, c.k, t.box) || !encode(&map_v, c, c.v, t.box)) return cudaErrorUnknown;
+    constexpr int kSmem = TensorSmem<D>::kTotal;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_tensor_kernel<D>), kSmem, smem_slot);
+    if (e != cudaSuccess) return e;
+    const int grid = min(2 * sm_count(), kMaxCtas);
+    e = launch_pdl(attend_tensor_kernel<D>, dim3(grid), dim3(kTensorThreads), kSmem, stream, map_k,
+                   map_v, t);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32), dim3(kJoinWarps * 32), 0, stream, t);
+}
+
+}  // namespace
+
 }  // namespace dspark
 
 using namespace dspark;
 
 extern "C" size_t dspark_tree_attention_workspace_bytes(int32_t n_q_heads, int32_t head_dim) {
     if (n_q_heads < 1 || head_dim < 2 || head_dim > DSPARK_MAX_HEAD_DIM) return 0;
-    return 256;
+    return round256(part_o_bytes(head_dim) + part_ml_bytes() + desc_bytes());
 }
 
 extern "C" int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype, int32_t n_q_heads,
@@ -202,8 +887,12 @@ extern "C" int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype,
     a.cache = kv_view(*cache);
     a.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == DSPARK_DTYPE_BF16
-                              ? launch_any<__nv_bfloat16>(a, cache->dtype, st)
-                              : launch_any<float>(a, cache->dtype, st);
+    cudaError_t e;
+    if (tensor_fits(a, dtype, *cache))
+        e = cache->head_dim == 64 ? launch_tensor<64>(a, *cache, workspace, kSmemSlot64, st)
+                                  : launch_tensor<128>(a, *cache, workspace, kSmemSlot128, st);
+    else
+        e = dtype == DSPARK_DTYPE_BF16 ? launch_any<__nv_bfloat16>(a, cache->dtype, st)
+                                       : launch_any<float>(a, cache->dtype, st);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
