@@ -15,6 +15,7 @@
 #include "tensor.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace dspark {
 
@@ -164,13 +165,11 @@ cudaError_t launch_any(const AttendArgs &a, int cache_dtype, cudaStream_t stream
 constexpr int kTile = 64;           // positions a step
 constexpr int kRowsPerTile = 128;   // (token, query head) rows of one kv head
 constexpr int kMaxCtas = 320;       // two for each of up to 160 SMs
-constexpr int kTensorThreads = 192; // softmax warps 0-3, copy warp 4, matrix warp 5
 constexpr int kTmemCols = 256;      // two score tiles of 64, the output's up to 128
 constexpr float kLazy = 8.0f;       // log2 of how far weights may grow past 1
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kDescInts = 8;
-constexpr int kSmemSlot64 = 20, kSmemSlot128 = 21;
 
 struct TensorArgs {
     AttendArgs a;
@@ -180,26 +179,46 @@ struct TensorArgs {
     int *desc;       // [kMaxCtas][kDescInts]: the split job that begins in a CTA
 };
 
-template <int D>
-struct TensorSmem {
+// Shared memory and warps of a CTA.  Over a 16-bit cache the copies land in the
+// operand ring; E4M3 codes land in a staging ring, from which four warps convert
+// them into the operand ring.
+template <int D, bool kQuant>
+struct TensorShape {
     static constexpr int kQBytes = kRowsPerTile * D * 2;
     static constexpr int kBufBytes = kTile * D * 2;
-    static constexpr int kBufs = D == 128 ? 5 : 9;
-    static constexpr int kControl = kQBytes + kBufs * kBufBytes;
-    static constexpr int kTotal = kControl + 1024;
+    static constexpr int kBufs = kQuant ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 9);
+    static constexpr int kStageBytes = kTile * D;
+    static constexpr int kStages = kQuant ? (D == 128 ? 3 : 8) : 0;
+    static constexpr int kStageAt = kQBytes + kBufs * kBufBytes;
+    static constexpr int kControl = kStageAt + kStages * kStageBytes;
+    static constexpr int kTotal = kControl + (kQuant ? 4096 : 1024);
+    static constexpr int kCopyWarp = kQuant ? 8 : 4, kMatrixWarp = kCopyWarp + 1;
+    static constexpr int kThreads = kQuant ? 384 : 192;
 };
 
 // The barriers and words behind the buffers.  A wait tells a phase from the next
 // one only; the barriers that come in twos serve every other tile, so that a
 // role one tile behind another still waits for the phase it means.
-struct Control {
-    unsigned long long full[9], empty[9], s_full[2], p_ready[2], o_done[2], q_full, drain;
-    unsigned tmem, nonfinite;
+struct alignas(16) Control {
+    unsigned long long full[9], empty[9], stage_full[8], stage_empty[8];
+    unsigned long long s_full[2], p_ready[2], o_done[2], scales[2], q_full, drain;
+    unsigned tmem;
+    unsigned nonfinite[4];  // window tokens whose values were zeroed, by segment
     int abort;
     int start_r;
-    long long start_off, total;
+    long long start_off;
     long long scan[40];
 };
+// What the scales of a tile's tokens become (E4M3), for every other tile.
+struct TileScales {
+    float k[2][kTile];        // k_scale times the scores' factor, to base 2
+    float v_log2[2][kTile];   // log2 v_scale: part of a weight's exponent
+    float v_inv[2][kTile];    // 1 / v_scale: takes it out of the sum of weights
+    float raw[2][2][kTile];   // the scales as they are: k, v
+    float q[kRowsPerTile];    // powers of two taken out of the queries
+};
+static_assert(sizeof(Control) <= 1024 && sizeof(Control) % 16 == 0 &&
+              sizeof(Control) + sizeof(TileScales) <= 4096, "control area");
 
 // A request's jobs: every (kv head, 128 rows) pair reads all its tiles.
 struct Request {
@@ -270,16 +289,41 @@ struct Walk {
 // K0, K1, V0, K2, V1, ..., V(n-1).
 __device__ __forceinline__ int ring_v(int tile, int n) { return tile < n - 1 ? 2 * tile + 2 : 2 * n - 1; }
 
-template <int D>
-__global__ void __launch_bounds__(kTensorThreads, 2)
+// Eight bfloat16 of a query row, spread over `lanes` lanes, become halves: exact
+// (a half has more digits), with a power of two taken out of a row whose largest
+// element is far from 1.  Returns that power.
+__device__ __forceinline__ float to_halves(uint4 *v, int lanes) {
+    unsigned *w = reinterpret_cast<unsigned *>(v);
+    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
+    for (int o = lanes >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
+    const int e = (int)(top >> 7);  // biased exponent; 255: NaN or infinity
+    const bool far = top != 0 && e != 255 && (e < 125 || e > 141);
+    const int by = far ? max(e, 1) - 127 : 0;
+    const float f = __int_as_float((127 - by) << 23);  // by >= -126: normal up to 2^126; by = 127: 0
+    const float g = by == 127 ? 0x1p-127f : f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 two = __floats2half2_rn(__uint_as_float(w[i] << 16) * g,
+                                              __uint_as_float(w[i] & 0xFFFF0000u) * g);
+        w[i] = *reinterpret_cast<const unsigned *>(&two);
+    }
+    return __int_as_float((by + 127) << 23);
+}
+
+template <int D, bool kQuant>
+__global__ void __launch_bounds__(TensorShape<D, kQuant>::kThreads, 2)
 attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const TensorArgs t) {
-    using S = TensorSmem<D>;
-    constexpr int kHalves = D / 64;       // 128-byte columns blocks of a row
+    using S = TensorShape<D, kQuant>;
+    constexpr int kThreads = S::kThreads;
+    constexpr int kHalves = D / 64;       // 128-byte column blocks of a row
     constexpr int kChunks = D / 8;        // 16-byte chunks of a row
     constexpr int kHalfBytes = kTile * 128;
     extern __shared__ __align__(1024) unsigned char smem[];
     Control &ctl = *reinterpret_cast<Control *>(smem + S::kControl);
+    TileScales &sc = *reinterpret_cast<TileScales *>(smem + S::kControl + sizeof(Control));
     const AttendArgs &a = t.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = smem_addr(smem);
@@ -290,7 +334,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
 
     // this CTA's share of all tiles: each thread sums a run of requests, a scan
     // over the threads finds the request that holds the first of its tiles
-    const int per = (a.B + kTensorThreads - 1) / kTensorThreads;
+    const int per = (a.B + kThreads - 1) / kThreads;
     long long mine = 0;
     for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r) {
         Request q;
@@ -320,21 +364,26 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     }
     if (tid == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
-            mbar_init(smem_addr(&ctl.full[i]), 1);
+            mbar_init(smem_addr(&ctl.full[i]), kQuant ? 4 : 1);
             mbar_init(smem_addr(&ctl.empty[i]), 1);
+        }
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(smem_addr(&ctl.stage_full[i]), 1);
+            mbar_init(smem_addr(&ctl.stage_empty[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
             mbar_init(smem_addr(&ctl.p_ready[i]), 4);
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
+            mbar_init(smem_addr(&ctl.scales[i]), 4);
         }
         mbar_init(smem_addr(&ctl.q_full), 128);
         mbar_init(smem_addr(&ctl.drain), 1);
         ctl.abort = 0;
-        ctl.nonfinite = 0;
+        for (int i = 0; i < 4; ++i) ctl.nonfinite[i] = 0;
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc(smem_addr(&ctl.tmem), kTmemCols);
+    if (warp == S::kMatrixWarp) tmem_alloc(smem_addr(&ctl.tmem), kTmemCols);
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = ctl.tmem, tmem_o = tmem + 2 * kTile;
@@ -344,9 +393,18 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     Segment s;
     unsigned loads = 0;  // ring position of the segment's first load
 
-    if (warp == 4) {
+    // Over E4M3 the softmax warps take registers from the others: of the 3 x 80 a
+    // thread that the three warpgroups were launched with, 136 + 56 + 48.
+    if (warp >= S::kCopyWarp) {
+        if constexpr (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == S::kCopyWarp) {
         // ------------------------------------------------ copy warp
-        const int boxes = kTile / t.box, box = lane / kHalves, half = lane % kHalves;
+        constexpr int kParts = kQuant ? 1 : kHalves;  // boxes side by side
+        constexpr int kSlots = kQuant ? S::kStages : S::kBufs;
+        constexpr int kBytes = kQuant ? S::kStageBytes : S::kBufBytes;
+        unsigned long long *filled = kQuant ? ctl.stage_full : ctl.full;
+        unsigned long long *freed = kQuant ? ctl.stage_empty : ctl.empty;
+        const int boxes = kTile / t.box, box = lane / kParts, half = lane % kParts;
         const bool issues = box < boxes;
         bool ok = true;
         // where this lane's box of tile j lies: a page outside the pool (past
@@ -362,16 +420,18 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             }
         };
         auto load = [&](const CUtensorMap *map, int head, int page, int token) {
-            const unsigned slot = loads % S::kBufs, phase = loads / S::kBufs & 1;
-            ok = ok && role_wait(smem_addr(&ctl.empty[slot]), phase ^ 1, abort, a.status);
+            const unsigned slot = loads % kSlots, phase = loads / kSlots & 1;
+            ok = ok && role_wait(smem_addr(&freed[slot]), phase ^ 1, abort, a.status);
             ok = __all_sync(kFullMask, ok);
             if (!ok) return;
-            const uint32_t bar = smem_addr(&ctl.full[slot]);
-            if (lane == 0) mbar_expect(bar, S::kBufBytes);
+            const uint32_t bar = smem_addr(&filled[slot]);
+            if (lane == 0) mbar_expect(bar, kBytes);
             __syncwarp();
-            if (issues)
-                tma_load_4d(ring + slot * S::kBufBytes + half * kHalfBytes + box * t.box * 128, map,
-                            half * 64, token, head, page, bar);
+            if (issues) {
+                const uint32_t dst = kQuant ? base + S::kStageAt + slot * kBytes + box * t.box * D
+                                            : ring + slot * kBytes + half * kHalfBytes + box * t.box * 128;
+                tma_load_4d(dst, map, half * 64, token, head, page, bar);
+            }
             ++loads;
         };
         while (ok && walk.next(t, &s)) {
@@ -389,11 +449,11 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 token = token1;
             }
         }
-    } else if (warp == 5) {
+        } else if (warp == S::kMatrixWarp) {
         // ---------------------------------------------- matrix warp
         if (lane == 0) {
-            constexpr uint32_t word_qk = mma_word(true, kTile, false);
-            constexpr uint32_t word_pv = mma_word(true, D, true);
+            constexpr uint32_t word_qk = mma_word(!kQuant, kTile, false);
+            constexpr uint32_t word_pv = mma_word(!kQuant, D, true);
             unsigned done = 0, seg = 0;  // tiles and segments so far
             bool ok = true;
             auto wait = [&](unsigned long long *bar, unsigned parity) {
@@ -448,8 +508,129 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             }
         }
         __syncwarp();
+        }
+    } else if (kQuant && warp >= 4) {
+        // --------------------------------------------- converting warps
+        if constexpr (kQuant) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+            constexpr int kUnits = D / 16;  // 16 codes a thread and step
+            const int ct = tid - 128, token = ct & (kTile - 1), which = ct / kTile;
+            unsigned done = 0, seg = 0;
+            bool ok = true;
+            auto wait = [&](unsigned long long *bar, unsigned parity) {
+                ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
+                return ok;
+            };
+            const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);
+            // this thread's scale (of token `token`; k or v) of tile j
+            auto fetch = [&](const Segment &s, int j) {
+                const int pos = j * kTile + token;
+                int tok;
+                const int page = pos < s.q.P + s.q.len ? kv_page(a.cache, s.r, pos, &tok) : -1;
+                return page < 0 ? 1.0f
+                                : __ldg((which ? a.cache.v_scale : a.cache.k_scale) +
+                                        kv_scale_offset(a.cache, page, tok, s.head));
+            };
+            // The next staged tile becomes halves.  Codes convert exactly; the
+            // scales go into the scores and weights, save one that is NaN or
+            // infinite, whose products with the codes are written instead.
+            auto convert = [&](const Segment &s, int j, const float *scale, bool values) {
+                const unsigned stage = loads % S::kStages, slot = loads % S::kBufs;
+                if (!wait(&ctl.stage_full[stage], loads / S::kStages)) return;
+                if (!wait(&ctl.empty[slot], loads / S::kBufs + 1)) return;
+                const unsigned char *src = smem + S::kStageAt + stage * S::kStageBytes;
+                unsigned char *dst = smem + S::kQBytes + slot * S::kBufBytes;
+                const int p0 = j * kTile, n = s.q.P + s.q.len;
+#pragma unroll
+                for (int i = 0; i < kTile * kUnits / 128; ++i) {
+                    const int unit = i * 128 + ct, tok = unit / kUnits, part = unit % kUnits;
+                    uint4 v = *reinterpret_cast<const uint4 *>(src + unit * 16);
+                    const unsigned *code = reinterpret_cast<const unsigned *>(&v);
+                    uint32_t h[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const __half2_raw two = __nv_cvt_fp8x2_to_halfraw2(
+                            (__nv_fp8x2_storage_t)(code[e / 2] >> (e & 1) * 16), __NV_E4M3);
+                        h[e] = (uint32_t)two.x | (uint32_t)two.y << 16;
+                    }
+                    const float f = scale[tok];
+                    const bool odd = !(f - f == 0.0f) || (values && f < 0.0f);
+                    const int pos = p0 + tok;
+                    if (odd || (values && pos >= s.q.P)) {
+                        bool bad = false;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float2 x = __half22float2(*reinterpret_cast<__half2 *>(&h[e]));
+                            if (odd) {
+                                const float g = f < 0.0f && f - f == 0.0f ? -1.0f : f;
+                                x.x *= g, x.y *= g;
+                            }
+                            // as in the 16-bit case: NaN and infinities of the
+                            // window's values are added at the end
+                            if (values && pos >= s.q.P) {
+                                if (pos >= n) x.x = x.y = 0.0f;
+                                if (!(x.x - x.x == 0.0f)) x.x = 0.0f, bad = true;
+                                if (!(x.y - x.y == 0.0f)) x.y = 0.0f, bad = true;
+                            }
+                            const __half2 two = __floats2half2_rn(x.x, x.y);
+                            h[e] = *reinterpret_cast<const uint32_t *>(&two);
+                        }
+                        if (bad) atomicOr(&ctl.nonfinite[seg & 3], 1u << (pos - s.q.P));
+                    }
+                    // chunks 2 part and 2 part + 1 of the token's row; lanes of
+                    // one half start with the one, of the other with the other,
+                    // so that eight lanes cover the eight chunk columns
+                    unsigned char *row = dst + part / 4 * kHalfBytes + tok * 128;
+                    const int flip = part / 4 & 1, ch = part % 4 * 2;
+                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                    *reinterpret_cast<uint4 *>(row + ((ch + flip ^ (tok & 7)) << 4)) = flip ? hi : lo;
+                    *reinterpret_cast<uint4 *>(row + ((ch + 1 - flip ^ (tok & 7)) << 4)) = flip ? lo : hi;
+                }
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&ctl.full[slot]));
+                    mbar_arrive(smem_addr(&ctl.stage_empty[stage]));
+                }
+                ++loads;
+            };
+            while (walk.next(t, &s)) {
+                float mine = fetch(s, s.first);
+                // A warp that gave up still comes to every barrier of the four.
+                auto keys = [&](int i) {
+                    const unsigned tile = done + i, b = tile & 1;
+                    ok = named_all(2, 128, ok);  // the values of tile - 2 are converted
+                    if (ok && tile >= 2) wait(&ctl.p_ready[b], (tile >> 1) + 1);
+                    if (ok) {
+                        sc.raw[b][which][token] = mine;
+                        const bool fine = mine - mine == 0.0f;
+                        if (which) {
+                            const float f = fine ? fmaxf(fabsf(mine), 0x1p-100f) : 1.0f;
+                            sc.v_log2[b][token] = log2f(f);
+                            sc.v_inv[b][token] = 1.0f / f;
+                        } else {
+                            sc.k[b][token] = (fine ? mine : 1.0f) * c;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&ctl.scales[b]));
+                    }
+                    ok = named_all(2, 128, ok);
+                    if (!ok) return;
+                    if (i + 1 < s.count) mine = fetch(s, s.first + i + 1);
+                    convert(s, s.first + i, sc.raw[b][0], false);
+                };
+                keys(0);
+                for (int i = 0; i < s.count; ++i) {
+                    if (i + 1 < s.count) keys(i + 1);
+                    if (ok) convert(s, s.first + i, sc.raw[(done + i) & 1][1], true);
+                }
+                done += s.count;
+                ++seg;
+            }
+        }
     } else {
         // --------------------------------------------- softmax warps
+        if constexpr (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         const int m = tid;  // row of the tile, lane of tensor memory
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
@@ -460,7 +641,10 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
             return ok;
         };
-        while (ok && walk.next(t, &s)) {
+        for (;;) {
+            // a warp that gave up still comes to the four warps' barriers
+            ok = named_all(1, 128, ok);
+            if (!ok || !walk.next(t, &s)) break;
             const int n = s.q.P + s.q.len, rows = s.q.len * t.group;
             const int row_base = s.row_tile * kRowsPerTile, row = row_base + m;
             const bool valid = row < rows, active = row_base + warp * 32 < rows;
@@ -471,8 +655,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
 
             // the tile's queries, swizzled; rows past the last are left as they
             // are: a row of the product depends on its own query alone
-            named_sync(1, 128);
-            if (tid == 0) ctl.nonfinite = 0;
+            if (tid == 0) ctl.nonfinite[(seg + 3) & 3] = 0;  // the segment's before
             const int q_rows = min(kRowsPerTile, (rows - row_base + 31) & ~31);
             for (int i = tid; i < q_rows * kChunks; i += 128) {
                 const int qr = i / kChunks, ch = i % kChunks;
@@ -485,11 +668,20 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         (long long)hq * D + ch * 8));
                     v.x ^= sign, v.y ^= sign, v.z ^= sign, v.w ^= sign;
                 }
+                if constexpr (kQuant) {
+                    const float f = to_halves(&v, kChunks);
+                    if (ch == 0) sc.q[qr] = f;
+                }
                 *reinterpret_cast<uint4 *>(smem + (ch / 8) * kRowsPerTile * 128 + qr * 128 +
                                            ((ch % 8 ^ (qr & 7)) << 4)) = v;
             }
             fence_async_proxy();
             mbar_arrive(smem_addr(&ctl.q_full));
+            float factor = 1.0f;
+            if constexpr (kQuant) {
+                named_sync(1, 128);
+                if (active) factor = sc.q[m];
+            }
 
             float mx = -INFINITY, l = 0.0f;  // running maximum (times c) and sum
             for (int i = 0; i < s.count; ++i) {
@@ -503,6 +695,24 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     tmem_load32(lanes + b * kTile + 32, x + 32);
                     tmem_wait_load(x);
                     tmem_wait_load(x + 32);
+                    if constexpr (kQuant) {
+                        // scores to base 2, plus log2 of the value's scale
+                        if (!wait(&ctl.scales[b], tile >> 1)) break;
+                        if (__any_sync(kFullMask, factor != 1.0f)) {
+#pragma unroll
+                            for (int j = 0; j < kTile; ++j)
+                                x[j] = __float_as_uint(__uint_as_float(x[j]) * factor);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kTile; j += 4) {
+                            const float4 ks = *reinterpret_cast<const float4 *>(&sc.k[b][j]);
+                            const float4 vs = *reinterpret_cast<const float4 *>(&sc.v_log2[b][j]);
+                            x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), ks.x, vs.x));
+                            x[j + 1] = __float_as_uint(fmaf(__uint_as_float(x[j + 1]), ks.y, vs.y));
+                            x[j + 2] = __float_as_uint(fmaf(__uint_as_float(x[j + 2]), ks.z, vs.z));
+                            x[j + 3] = __float_as_uint(fmaf(__uint_as_float(x[j + 3]), ks.w, vs.w));
+                        }
+                    }
                     if (p0 + kTile > s.q.P) {
                         // the tile reaches the window: prefix positions, then
                         // this row's ancestors
@@ -516,7 +726,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     float top = __uint_as_float(x[0]);
 #pragma unroll
                     for (int j = 1; j < kTile; ++j) top = fmaxf(top, __uint_as_float(x[j]));
-                    top *= c;
+                    if constexpr (!kQuant) top *= c;
                     // The maximum moves only when it grows by 2^kLazy: until then
                     // the weights may pass 1, and the output stays as it is.
                     const bool grow = top > mx + kLazy || (mx == -INFINITY && top > mx);
@@ -544,18 +754,29 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     uint32_t w[kTile / 2];
 #pragma unroll
                     for (int j = 0; j < kTile; j += 2) {
-                        const float u = exp2_approx(fmaf(__uint_as_float(x[j]), c, -shift));
-                        const float v = exp2_approx(fmaf(__uint_as_float(x[j + 1]), c, -shift));
-                        sum[j / 2 % 2 * 2] += u;
-                        sum[j / 2 % 2 * 2 + 1] += v;
-                        const __nv_bfloat162 two = __floats2bfloat162_rn(u, v);
-                        w[j / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                        float &s0 = sum[j / 2 % 2 * 2], &s1 = sum[j / 2 % 2 * 2 + 1];
+                        if constexpr (kQuant) {
+                            const float u = exp2_approx(__uint_as_float(x[j]) - shift);
+                            const float v = exp2_approx(__uint_as_float(x[j + 1]) - shift);
+                            const float2 inv = *reinterpret_cast<const float2 *>(&sc.v_inv[b][j]);
+                            s0 = fmaf(u, inv.x, s0);
+                            s1 = fmaf(v, inv.y, s1);
+                            const __half2 two = __floats2half2_rn(u, v);
+                            w[j / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                        } else {
+                            const float u = exp2_approx(fmaf(__uint_as_float(x[j]), c, -shift));
+                            const float v = exp2_approx(fmaf(__uint_as_float(x[j + 1]), c, -shift));
+                            s0 += u;
+                            s1 += v;
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(u, v);
+                            w[j / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                        }
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tmem_store32(lanes + b * kTile, w);
                     tmem_wait_store();
                 }
-                if (p0 + kTile > s.q.P) {
+                if (!kQuant && p0 + kTile > s.q.P) {
                     // Values past the request's end become zeros, and so do NaN
                     // and infinities of the window (0 x NaN would reach rows that
                     // do not see them); the rows that do get them at the end.
@@ -581,7 +802,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                                 if (hi16) e[k] &= 0x0000FFFFu;
                             }
                             if (!bad) continue;
-                            atomicOr(&ctl.nonfinite, 1u << (pos - s.q.P));
+                            atomicOr(&ctl.nonfinite[seg & 3], 1u << (pos - s.q.P));
                         }
                         *at = v;
                     }
@@ -592,14 +813,14 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[b]));
             }
             const unsigned last = done + s.count - 1;
-            if (!wait(&ctl.o_done[last & 1], last >> 1)) break;
+            if (!wait(&ctl.o_done[last & 1], last >> 1)) continue;
             done += s.count;
             loads += 2 * s.count;
             tmem_fence_after();
 
             const bool whole = s.count == s.q.tiles;
             const float shift = mx == -INFINITY ? 0.0f : mx;
-            const unsigned extra = *(volatile unsigned *)&ctl.nonfinite & bits;
+            const unsigned extra = *(volatile unsigned *)&ctl.nonfinite[seg & 3] & bits;
             const int slot = 2 * cta + (seg > 0);
             if (active) {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -614,11 +835,15 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         int tok;
                         const int page = kv_page(a.cache, s.r, (long long)s.q.P + __ffs(e) - 1, &tok);
                         if (page < 0) continue;
-                        const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(a.cache.v) +
-                                                 kv_offset(a.cache, page, tok, s.head) + h * 32;
+                        using E = typename std::conditional<kQuant, e4m3, __nv_bfloat16>::type;
+                        const E *v = reinterpret_cast<const E *>(a.cache.v) +
+                                     kv_offset(a.cache, page, tok, s.head) + h * 32;
+                        float f = 1.0f;
+                        if constexpr (kQuant)
+                            f = __ldg(a.cache.v_scale + kv_scale_offset(a.cache, page, tok, s.head));
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            const float y = elem_value(v[j]);
+                            const float y = elem_value(v[j]) * f;
                             if (!(y - y == 0.0f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + y);
                         }
                     }
@@ -673,13 +898,14 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         }
     }
     __syncthreads();
-    if (ctl.abort && warp == 4 && lane == 0) {
+    if (ctl.abort && warp == S::kCopyWarp && lane == 0) {
         // copies still under way write this block's buffers
-        const unsigned n = min(loads, (unsigned)S::kBufs);
-        for (unsigned i = loads - n; i < loads; ++i)
-            mbar_wait(smem_addr(&ctl.full[i % S::kBufs]), i / S::kBufs & 1);
+        constexpr unsigned kSlots = kQuant ? S::kStages : S::kBufs;
+        unsigned long long *filled = kQuant ? ctl.stage_full : ctl.full;
+        for (unsigned i = loads - min(loads, kSlots); i < loads; ++i)
+            mbar_wait(smem_addr(&filled[i % kSlots]), i / kSlots & 1);
     }
-    if (warp == 5) tmem_free(tmem, kTmemCols);
+    if (warp == S::kMatrixWarp) tmem_free(tmem, kTmemCols);
 }
 
 // Joins the parts of the jobs that several CTAs share, in the CTAs' order: a
@@ -779,8 +1005,8 @@ EncodeFn encoder() {
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-// The cache as [page][head][token][element] with boxes of `box` tokens and 64
-// elements, rows of a box swizzled.
+// The cache as [page][head][token][element]; boxes of `box` tokens by 64 elements
+// under the 128-byte swizzle, or by a whole row of E4M3 codes as they are.
 bool encode(CUtensorMap *map, const dspark_kv_cache &c, void *p, int box) {
     const EncodeFn f = encoder();
     if (!f) return false;
@@ -789,9 +1015,12 @@ bool encode(CUtensorMap *map, const dspark_kv_cache &c, void *p, int box) {
                                 (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * e, (cuuint64_t)c.head_stride * e,
                                    (cuuint64_t)c.page_stride * e};
-    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
-    return f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims, strides, boxes, ones,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const bool quant = c.dtype == DSPARK_DTYPE_E4M3;
+    const cuuint32_t boxes[4] = {quant ? (cuuint32_t)c.head_dim : 64u, (cuuint32_t)box, 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return f(map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims,
+             strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             quant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -806,7 +1035,7 @@ size_t desc_bytes() { return (size_t)kMaxCtas * kDescInts * 4; }
 // swizzle groups inside a page, and the strides and bases that TMA and the
 // 16-byte accesses take.
 bool tensor_fits(const AttendArgs &a, int dtype, const dspark_kv_cache &c) {
-    if (dtype != DSPARK_DTYPE_BF16 || c.dtype != DSPARK_DTYPE_BF16) return false;
+    if (dtype != DSPARK_DTYPE_BF16 || c.dtype == DSPARK_DTYPE_F32) return false;
     if ((c.head_dim != 64 && c.head_dim != 128) || c.page_size % 16) return false;
     const int e = kv_elem_bytes(c.dtype);
     const int64_t strides[3] = {c.token_stride, c.head_stride, c.page_stride};
@@ -816,9 +1045,11 @@ bool tensor_fits(const AttendArgs &a, int dtype, const dspark_kv_cache &c) {
            a.ld_q % 8 == 0 && a.ld_out % 8 == 0;
 }
 
-template <int D>
+template <int D, bool kQuant>
 cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *workspace,
-                          int smem_slot, cudaStream_t stream) {
+                          cudaStream_t stream) {
+    using S = TensorShape<D, kQuant>;
+    constexpr int kSmemSlot = 20 + (D == 128) + 2 * kQuant;  // of ensure_smem
     TensorArgs t;
     t.a = a;
     t.group = a.n_q_heads / c.n_kv_heads;
@@ -829,12 +1060,12 @@ cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *w
     t.desc = reinterpret_cast<int *>(w + part_o_bytes(D) + part_ml_bytes());
     CUtensorMap map_k, map_v;
     if (!encode(&map_k, c, c.k, t.box) || !encode(&map_v, c, c.v, t.box)) return cudaErrorUnknown;
-    constexpr int kSmem = TensorSmem<D>::kTotal;
-    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_tensor_kernel<D>), kSmem, smem_slot);
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_tensor_kernel<D, kQuant>),
+                                S::kTotal, kSmemSlot);
     if (e != cudaSuccess) return e;
     const int grid = min(2 * sm_count(), kMaxCtas);
-    e = launch_pdl(attend_tensor_kernel<D>, dim3(grid), dim3(kTensorThreads), kSmem, stream, map_k,
-                   map_v, t);
+    e = launch_pdl(attend_tensor_kernel<D, kQuant>, dim3(grid), dim3(S::kThreads), S::kTotal, stream,
+                   map_k, map_v, t);
     if (e != cudaSuccess) return e;
     return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32), dim3(kJoinWarps * 32), 0, stream, t);
 }
@@ -888,9 +1119,12 @@ extern "C" int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype,
     a.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
+    const bool quant = cache->dtype == DSPARK_DTYPE_E4M3, small = cache->head_dim == 64;
     if (tensor_fits(a, dtype, *cache))
-        e = cache->head_dim == 64 ? launch_tensor<64>(a, *cache, workspace, kSmemSlot64, st)
-                                  : launch_tensor<128>(a, *cache, workspace, kSmemSlot128, st);
+        e = quant ? small ? launch_tensor<64, true>(a, *cache, workspace, st)
+                          : launch_tensor<128, true>(a, *cache, workspace, st)
+            : small ? launch_tensor<64, false>(a, *cache, workspace, st)
+                    : launch_tensor<128, false>(a, *cache, workspace, st);
     else
         e = dtype == DSPARK_DTYPE_BF16 ? launch_any<__nv_bfloat16>(a, cache->dtype, st)
                                        : launch_any<float>(a, cache->dtype, st);

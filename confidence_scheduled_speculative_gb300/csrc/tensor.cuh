@@ -60,6 +60,18 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// The same, and whether `ok` holds for all of the threads.
+__device__ __forceinline__ bool named_all(int id, int threads, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+        " barrier.cta.red.and.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(all)
+        : "r"((uint32_t)ok), "r"(id), "r"(threads)
+        : "memory");
+    return all != 0;
+}
+
 // One box of a 4-D tensor map into shared memory, completing on `bar`.  The
 // innermost coordinate is always a multiple of 16 bytes; a box outside the
 // tensor arrives as zeros.
