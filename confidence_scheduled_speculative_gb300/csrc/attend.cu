@@ -173,7 +173,9 @@ constexpr int kDescInts = 8;
 
 struct TensorArgs {
     AttendArgs a;
-    int group, box;
+    int group;   // query heads a kv head
+    int tokens;  // window tokens a row tile: all their heads in 128 rows
+    int box;     // cache tokens a TMA box
     float *part_o;   // [2 kMaxCtas][D / 4][128] float4
     float *part_ml;  // [2 kMaxCtas][2][128]
     int *desc;       // [kMaxCtas][kDescInts]: the split job that begins in a CTA
@@ -201,7 +203,8 @@ struct TensorShape {
 // role one tile behind another still waits for the phase it means.
 struct alignas(16) Control {
     unsigned long long full[9], empty[9], stage_full[8], stage_empty[8];
-    unsigned long long s_full[2], p_ready[2], o_done[2], scales[2], q_full, drain;
+    unsigned long long s_full[2], p_ready[2], o_done[2], scales[2];
+    unsigned long long q_raw, q_full, q_empty, drain;
     unsigned tmem;
     unsigned nonfinite[4];  // window tokens whose values were zeroed, by segment
     int abort;
@@ -215,7 +218,6 @@ struct TileScales {
     float v_log2[2][kTile];   // log2 v_scale: part of a weight's exponent
     float v_inv[2][kTile];    // 1 / v_scale: takes it out of the sum of weights
     float raw[2][2][kTile];   // the scales as they are: k, v
-    float q[kRowsPerTile];    // powers of two taken out of the queries
 };
 static_assert(sizeof(Control) <= 1024 && sizeof(Control) % 16 == 0 &&
               sizeof(Control) + sizeof(TileScales) <= 4096, "control area");
@@ -228,7 +230,7 @@ struct Request {
 __device__ __forceinline__ bool load_request(const TensorArgs &t, int r, Request *q, bool report) {
     if (!window_of(t.a, r, &q->row0, &q->len, &q->P, report)) return false;
     q->tiles = (q->P + q->len + kTile - 1) / kTile;
-    q->row_tiles = (q->len * t.group + kRowsPerTile - 1) / kRowsPerTile;
+    q->row_tiles = (q->len + t.tokens - 1) / t.tokens;
     return true;
 }
 
@@ -289,25 +291,60 @@ struct Walk {
 // K0, K1, V0, K2, V1, ..., V(n-1).
 __device__ __forceinline__ int ring_v(int tile, int n) { return tile < n - 1 ? 2 * tile + 2 : 2 * n - 1; }
 
-// Eight bfloat16 of a query row, spread over `lanes` lanes, become halves: exact
-// (a half has more digits), with a power of two taken out of a row whose largest
-// element is far from 1.  Returns that power.
-__device__ __forceinline__ float to_halves(uint4 *v, int lanes) {
-    unsigned *w = reinterpret_cast<unsigned *>(v);
+// Where a position lies, for a lane that steps through the tiles of a segment:
+// the table's entry is loaded ahead of its use.
+struct Place {
+    int col, token;
+    __device__ __forceinline__ void begin(const KvView &c, int pos) {
+        col = (unsigned)pos / (unsigned)c.page_size;
+        token = pos - col * c.page_size;
+    }
+    __device__ __forceinline__ void step(const KvView &c) {
+        token += kTile;
+        while (token >= c.page_size) {
+            token -= c.page_size;
+            ++col;
+        }
+    }
+    // the entry; the pool's size, a page it does not have, past the end
+    __device__ __forceinline__ int entry(const KvView &c, int r, bool in) const {
+        return in ? __ldg(c.table + (long long)r * c.table_width + col) : c.n_pages;
+    }
+};
+
+// A query row of bfloat16 in swizzled shared memory becomes halves in place:
+// exactly (a half has more digits), with a power of two taken out of a row whose
+// largest element is far from 1.  Returns that power.
+template <int D>
+__device__ __forceinline__ float row_to_halves(unsigned char *q, int row) {
+    auto chunk = [&](int i) {
+        return reinterpret_cast<uint4 *>(q + i / 8 * kRowsPerTile * 128 + row * 128 +
+                                         ((i % 8 ^ (row & 7)) << 4));
+    };
     unsigned top = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
-    for (int o = lanes >> 1; o; o >>= 1) top = max(top, __shfl_xor_sync(kFullMask, top, o));
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 v = *chunk(i);
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, w[k] >> 16 & 0x7FFFu));
+    }
     const int e = (int)(top >> 7);  // biased exponent; 255: NaN or infinity
     const bool far = top != 0 && e != 255 && (e < 125 || e > 141);
     const int by = far ? max(e, 1) - 127 : 0;
-    const float f = __int_as_float((127 - by) << 23);  // by >= -126: normal up to 2^126; by = 127: 0
-    const float g = by == 127 ? 0x1p-127f : f;
+    const float f = by == 127 ? 0x1p-127f : __int_as_float((127 - by) << 23);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 two = __floats2half2_rn(__uint_as_float(w[i] << 16) * g,
-                                              __uint_as_float(w[i] & 0xFFFF0000u) * g);
-        w[i] = *reinterpret_cast<const unsigned *>(&two);
+    for (int i = 0; i < D / 8; ++i) {
+        uint4 *at = chunk(i);
+        uint4 v = *at;
+        unsigned *w = reinterpret_cast<unsigned *>(&v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __half2 two = __floats2half2_rn(__uint_as_float(w[k] << 16) * f,
+                                                  __uint_as_float(w[k] & 0xFFFF0000u) * f);
+            w[k] = *reinterpret_cast<const unsigned *>(&two);
+        }
+        *at = v;
     }
     return __int_as_float((by + 127) << 23);
 }
@@ -315,7 +352,8 @@ __device__ __forceinline__ float to_halves(uint4 *v, int lanes) {
 template <int D, bool kQuant>
 __global__ void __launch_bounds__(TensorShape<D, kQuant>::kThreads, 2)
 attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
-                     const __grid_constant__ CUtensorMap map_v, const TensorArgs t) {
+                     const __grid_constant__ CUtensorMap map_v,
+                     const __grid_constant__ CUtensorMap map_q, const TensorArgs t) {
     using S = TensorShape<D, kQuant>;
     constexpr int kThreads = S::kThreads;
     constexpr int kHalves = D / 64;       // 128-byte column blocks of a row
@@ -377,7 +415,9 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
             mbar_init(smem_addr(&ctl.scales[i]), 4);
         }
-        mbar_init(smem_addr(&ctl.q_full), 128);
+        mbar_init(smem_addr(&ctl.q_raw), 1);
+        mbar_init(smem_addr(&ctl.q_full), 4);
+        mbar_init(smem_addr(&ctl.q_empty), 1);
         mbar_init(smem_addr(&ctl.drain), 1);
         ctl.abort = 0;
         for (int i = 0; i < 4; ++i) ctl.nonfinite[i] = 0;
@@ -390,7 +430,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     volatile int *abort = &ctl.abort;
     Walk walk;
     walk.begin(t, ctl.start_r, ctl.start_off, hi - lo);
-    Segment s;
+    Segment s = {};
     unsigned loads = 0;  // ring position of the segment's first load
 
     // Over E4M3 the softmax warps take registers from the others: of the 3 x 80 a
@@ -398,116 +438,141 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     if (warp >= S::kCopyWarp) {
         if constexpr (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == S::kCopyWarp) {
-        // ------------------------------------------------ copy warp
-        constexpr int kParts = kQuant ? 1 : kHalves;  // boxes side by side
-        constexpr int kSlots = kQuant ? S::kStages : S::kBufs;
-        constexpr int kBytes = kQuant ? S::kStageBytes : S::kBufBytes;
-        unsigned long long *filled = kQuant ? ctl.stage_full : ctl.full;
-        unsigned long long *freed = kQuant ? ctl.stage_empty : ctl.empty;
-        const int boxes = kTile / t.box, box = lane / kParts, half = lane % kParts;
-        const bool issues = box < boxes;
-        bool ok = true;
-        // where this lane's box of tile j lies: a page outside the pool (past
-        // the request's end too) arrives as zeros
-        auto find = [&](const Segment &s, int j, int *page, int *token) {
-            const int pos = j * kTile + box * t.box;
-            *page = a.cache.n_pages;
-            *token = 0;
-            if (issues && pos < s.q.P + s.q.len) {
-                const int g = kv_page(a.cache, s.r, pos, token);
-                if (g >= 0) *page = g;
-                else flag(a.status, DSPARK_STATUS_BAD_INDEX);
-            }
-        };
-        auto load = [&](const CUtensorMap *map, int head, int page, int token) {
-            const unsigned slot = loads % kSlots, phase = loads / kSlots & 1;
-            ok = ok && role_wait(smem_addr(&freed[slot]), phase ^ 1, abort, a.status);
-            ok = __all_sync(kFullMask, ok);
-            if (!ok) return;
-            const uint32_t bar = smem_addr(&filled[slot]);
-            if (lane == 0) mbar_expect(bar, kBytes);
-            __syncwarp();
-            if (issues) {
-                const uint32_t dst = kQuant ? base + S::kStageAt + slot * kBytes + box * t.box * D
-                                            : ring + slot * kBytes + half * kHalfBytes + box * t.box * 128;
-                tma_load_4d(dst, map, half * 64, token, head, page, bar);
-            }
-            ++loads;
-        };
-        while (ok && walk.next(t, &s)) {
-            int page, token, page1 = 0, token1 = 0;
-            find(s, s.first, &page, &token);
-            load(&map_k, s.head, page, token);
-            for (int i = 0; i < s.count && ok; ++i) {
-                if (i + 1 < s.count) {
-                    find(s, s.first + i + 1, &page1, &token1);
-                    load(&map_k, s.head, page1, token1);
-                    if (!ok) break;
-                }
-                load(&map_v, s.head, page, token);
-                page = page1;
-                token = token1;
-            }
-        }
-        } else if (warp == S::kMatrixWarp) {
-        // ---------------------------------------------- matrix warp
-        if (lane == 0) {
-            constexpr uint32_t word_qk = mma_word(!kQuant, kTile, false);
-            constexpr uint32_t word_pv = mma_word(!kQuant, D, true);
-            unsigned done = 0, seg = 0;  // tiles and segments so far
+            // -------------------------------------------- copy warp
+            constexpr int kParts = kQuant ? 1 : kHalves;  // boxes side by side
+            constexpr int kSlots = kQuant ? S::kStages : S::kBufs;
+            constexpr int kBytes = kQuant ? S::kStageBytes : S::kBufBytes;
+            unsigned long long *filled = kQuant ? ctl.stage_full : ctl.full;
+            unsigned long long *freed = kQuant ? ctl.stage_empty : ctl.empty;
+            const int boxes = kTile / t.box, box = lane / kParts, half = lane % kParts;
+            const bool issues = box < boxes;
+            const uint32_t dst = kQuant ? base + S::kStageAt + box * t.box * D
+                                        : ring + half * kHalfBytes + box * t.box * 128;
+            unsigned seg = 0;
             bool ok = true;
             auto wait = [&](unsigned long long *bar, unsigned parity) {
                 ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
-                return ok;
+                return ok = __all_sync(kFullMask, ok);
             };
-            auto qk = [&](unsigned tile, unsigned load) {
-                const unsigned slot = load % S::kBufs;
-                if (!wait(&ctl.full[slot], load / S::kBufs)) return;
-                tmem_fence_after();
-                const uint32_t buf = ring + slot * S::kBufBytes;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_ss(tmem + (tile & 1) * kTile,
-                           smem_operand(base + (k / 4) * kRowsPerTile * 128 + (k % 4) * 32, 16),
-                           smem_operand(buf + (k / 4) * kHalfBytes + (k % 4) * 32, 16), word_qk, k > 0);
-                mma_commit(smem_addr(&ctl.empty[slot]));
-                mma_commit(smem_addr(&ctl.s_full[tile & 1]));
+            auto load = [&](const CUtensorMap *map, int page, int token) {
+                const unsigned slot = loads % kSlots;
+                if (!wait(&freed[slot], loads / kSlots + 1)) return;
+                const uint32_t bar = smem_addr(&filled[slot]);
+                if (lane == 0) mbar_expect(bar, kBytes);
+                __syncwarp();
+                if (issues) tma_load_4d(dst + slot * kBytes, map, half * 64, token, s.head, page, bar);
+                ++loads;
             };
             while (ok && walk.next(t, &s)) {
-                if (!wait(&ctl.q_full, seg)) break;
-                qk(done, loads);
-                for (int i = 0; i < s.count && ok; ++i) {
-                    const unsigned tile = done + i;
-                    if (i + 1 < s.count) {
-                        // its scores take the place of the weights before last
-                        if (i > 0 && !wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) break;
-                        qk(tile + 1, loads + 2 * i + 1);
-                    }
-                    const unsigned load = loads + ring_v(i, s.count), slot = load % S::kBufs;
-                    if (!wait(&ctl.full[slot], load / S::kBufs)) break;
-                    if (!wait(&ctl.p_ready[tile & 1], tile >> 1)) break;
-                    tmem_fence_after();
-                    const uint32_t buf = ring + slot * S::kBufBytes;
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ts(tmem_o, tmem + (tile & 1) * kTile + k * 8,
-                               smem_operand(buf + k * 16 * 128, kHalfBytes), word_pv,
-                               i > 0 || k > 0);
-                    mma_commit(smem_addr(&ctl.empty[slot]));
-                    mma_commit(smem_addr(&ctl.o_done[tile & 1]));
-                }
-                done += s.count;
-                loads += 2 * s.count;
+                // this lane's box of each tile; a page outside the pool, as past
+                // the request's end, arrives as zeros
+                const int n = s.q.P + s.q.len;
+                int pos = s.first * kTile + box * t.box;
+                Place at;
+                at.begin(a.cache, issues ? pos : 0);
+                auto entry = [&]() { return at.entry(a.cache, s.r, issues && pos < n); };
+                auto checked = [&](int page, int where) {
+                    if ((unsigned)page < (unsigned)a.cache.n_pages) return page;
+                    if (issues && where < n) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+                    return a.cache.n_pages;
+                };
+                int page = entry(), token = at.token;
+                pos += kTile;
+                at.step(a.cache);
+                int page1 = s.count > 1 ? entry() : 0;
+                page = checked(page, pos - kTile);
+                load(&map_k, page, token);
+                // the queries, once the products with the last ones are done
+                if (seg > 0 && !wait(&ctl.q_empty, seg - 1)) break;
+                if (lane == 0) mbar_expect(smem_addr(&ctl.q_raw), t.group * t.tokens * D * 2);
+                __syncwarp();
+                if (lane < kHalves)
+                    tma_load_4d(base + lane * kRowsPerTile * 128, &map_q, lane * 64, 0, s.head,
+                                s.q.row0 + s.row_tile * t.tokens, smem_addr(&ctl.q_raw));
                 ++seg;
+                for (int i = 0; i < s.count && ok; ++i) {
+                    const int token1 = at.token;
+                    if (i + 1 < s.count) {
+                        const int now = checked(page1, pos);
+                        pos += kTile;
+                        at.step(a.cache);
+                        if (i + 2 < s.count) page1 = entry();
+                        load(&map_k, now, token1);
+                        if (ok) load(&map_v, page, token);
+                        page = now;
+                        token = token1;
+                    } else {
+                        load(&map_v, page, token);
+                    }
+                }
             }
-            // after a timeout: products still under way write tensor memory and
-            // barriers of this block
-            if (!ok) {
-                mma_commit(smem_addr(&ctl.drain));
-                mbar_wait(smem_addr(&ctl.drain), 0);
+            if (!ok && lane == 0) {
+                // copies still under way write this block's buffers
+                for (unsigned i = loads - min(loads, (unsigned)kSlots); i < loads; ++i)
+                    mbar_wait(smem_addr(&filled[i % kSlots]), i / kSlots & 1);
+                if (seg > 0) mbar_wait(smem_addr(&ctl.q_raw), (seg - 1) & 1);
             }
-        }
-        __syncwarp();
+        } else if (warp == S::kMatrixWarp) {
+            // ------------------------------------------ matrix warp
+            if (lane == 0) {
+                constexpr uint32_t word_qk = mma_word(!kQuant, kTile, false);
+                constexpr uint32_t word_pv = mma_word(!kQuant, D, true);
+                const uint64_t desc_q = smem_operand(base, 16), desc_ring = smem_operand(ring, kHalfBytes);
+                unsigned long long *queries = kQuant ? &ctl.q_full : &ctl.q_raw;
+                unsigned done = 0, seg = 0;  // tiles and segments so far
+                bool ok = true;
+                auto wait = [&](unsigned long long *bar, unsigned parity) {
+                    ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
+                    return ok;
+                };
+                auto qk = [&](unsigned tile, unsigned load, bool last) {
+                    const unsigned slot = load % S::kBufs;
+                    if (!wait(&ctl.full[slot], load / S::kBufs)) return;
+                    tmem_fence_after();
+                    const uint64_t buf = desc_ring + slot * (S::kBufBytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ss(tmem + (tile & 1) * kTile,
+                               desc_q + ((k / 4 * kRowsPerTile * 128 + k % 4 * 32) >> 4),
+                               buf + ((k / 4 * kHalfBytes + k % 4 * 32) >> 4), word_qk, k > 0);
+                    mma_commit(smem_addr(&ctl.s_full[tile & 1]));
+                    mma_commit(smem_addr(&ctl.empty[slot]));
+                    if (last) mma_commit(smem_addr(&ctl.q_empty));
+                };
+                while (ok && walk.next(t, &s)) {
+                    if (!wait(queries, seg)) break;
+                    qk(done, loads, s.count == 1);
+                    for (int i = 0; i < s.count && ok; ++i) {
+                        const unsigned tile = done + i;
+                        if (i + 1 < s.count) {
+                            // its scores take the place of the weights before last
+                            if (i > 0 && !wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) break;
+                            qk(tile + 1, loads + 2 * i + 1, i + 2 == s.count);
+                        }
+                        const unsigned load = loads + ring_v(i, s.count), slot = load % S::kBufs;
+                        if (!wait(&ctl.full[slot], load / S::kBufs)) break;
+                        if (!wait(&ctl.p_ready[tile & 1], tile >> 1)) break;
+                        tmem_fence_after();
+                        const uint64_t buf = desc_ring + slot * (S::kBufBytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ts(tmem_o, tmem + (tile & 1) * kTile + k * 8,
+                                   buf + (k * 16 * 128 >> 4), word_pv, i > 0 || k > 0);
+                        mma_commit(smem_addr(&ctl.o_done[tile & 1]));
+                        mma_commit(smem_addr(&ctl.empty[slot]));
+                    }
+                    done += s.count;
+                    loads += 2 * s.count;
+                    ++seg;
+                }
+                // after a timeout: products still under way write tensor memory
+                // and barriers of this block
+                if (!ok) {
+                    mma_commit(smem_addr(&ctl.drain));
+                    mbar_wait(smem_addr(&ctl.drain), 0);
+                }
+            }
+            __syncwarp();
         }
     } else if (kQuant && warp >= 4) {
         // --------------------------------------------- converting warps
@@ -521,51 +586,63 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
                 return ok;
             };
-            const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);
-            // this thread's scale (of token `token`; k or v) of tile j
-            auto fetch = [&](const Segment &s, int j) {
-                const int pos = j * kTile + token;
-                int tok;
-                const int page = pos < s.q.P + s.q.len ? kv_page(a.cache, s.r, pos, &tok) : -1;
-                return page < 0 ? 1.0f
-                                : __ldg((which ? a.cache.v_scale : a.cache.k_scale) +
-                                        kv_scale_offset(a.cache, page, tok, s.head));
+            const float c = copysignf(fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f), a.scale);
+            // 16 staged codes at `unit`, as halves: exact
+            auto halves = [&](const uint4 &v, uint32_t *h) {
+                const unsigned code[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const __half2_raw two = __nv_cvt_fp8x2_to_halfraw2(
+                        (__nv_fp8x2_storage_t)(code[e / 2] >> (e & 1) * 16), __NV_E4M3);
+                    h[e] = (uint32_t)two.x | (uint32_t)two.y << 16;
+                }
             };
-            // The next staged tile becomes halves.  Codes convert exactly; the
-            // scales go into the scores and weights, save one that is NaN or
-            // infinite, whose products with the codes are written instead.
-            auto convert = [&](const Segment &s, int j, const float *scale, bool values) {
+            // Their place is chunks 2 part and 2 part + 1 of the token's row.  Lanes
+            // of one half start with the one, of the other with the other, so that
+            // eight lanes cover the eight chunk columns of shared memory.
+            auto put = [&](unsigned char *dst, int tok, int part, const uint32_t *h) {
+                unsigned char *row = dst + part / 4 * kHalfBytes + tok * 128;
+                const int flip = part / 4 & 1, ch = part % 4 * 2;
+                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                *reinterpret_cast<uint4 *>(row + ((ch + flip ^ (tok & 7)) << 4)) = flip ? hi : lo;
+                *reinterpret_cast<uint4 *>(row + ((ch + 1 - flip ^ (tok & 7)) << 4)) = flip ? lo : hi;
+            };
+            // The next staged tile becomes halves.  The scales go into the scores
+            // and weights, save those that are not plain numbers (`regular` says
+            // that all are): their products with the codes are written instead.
+            auto convert = [&](int j, const float *scale, bool values, bool regular) {
                 const unsigned stage = loads % S::kStages, slot = loads % S::kBufs;
                 if (!wait(&ctl.stage_full[stage], loads / S::kStages)) return;
                 if (!wait(&ctl.empty[slot], loads / S::kBufs + 1)) return;
                 const unsigned char *src = smem + S::kStageAt + stage * S::kStageBytes;
                 unsigned char *dst = smem + S::kQBytes + slot * S::kBufBytes;
                 const int p0 = j * kTile, n = s.q.P + s.q.len;
+                if (regular && !(values && p0 + kTile > s.q.P)) {
+                    constexpr int kSteps = kTile * kUnits / 128;
+                    uint4 v[kSteps];
 #pragma unroll
-                for (int i = 0; i < kTile * kUnits / 128; ++i) {
-                    const int unit = i * 128 + ct, tok = unit / kUnits, part = unit % kUnits;
-                    uint4 v = *reinterpret_cast<const uint4 *>(src + unit * 16);
-                    const unsigned *code = reinterpret_cast<const unsigned *>(&v);
-                    uint32_t h[8];
+                    for (int i = 0; i < kSteps; ++i)
+                        v[i] = *reinterpret_cast<const uint4 *>(src + (i * 128 + ct) * 16);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const __half2_raw two = __nv_cvt_fp8x2_to_halfraw2(
-                            (__nv_fp8x2_storage_t)(code[e / 2] >> (e & 1) * 16), __NV_E4M3);
-                        h[e] = (uint32_t)two.x | (uint32_t)two.y << 16;
+                    for (int i = 0; i < kSteps; ++i) {
+                        uint32_t h[8];
+                        halves(v[i], h);
+                        put(dst, (i * 128 + ct) / kUnits, ct % kUnits, h);
                     }
-                    const float f = scale[tok];
-                    const bool odd = !(f - f == 0.0f) || (values && f < 0.0f);
-                    const int pos = p0 + tok;
-                    if (odd || (values && pos >= s.q.P)) {
+                } else {
+#pragma unroll 1
+                    for (int i = ct; i < kTile * kUnits; i += 128) {
+                        const int tok = i / kUnits, pos = p0 + tok;
+                        uint32_t h[8];
+                        halves(*reinterpret_cast<const uint4 *>(src + i * 16), h);
+                        const float f = scale[tok];
+                        const float g = f - f == 0.0f ? values && f < 0.0f ? -1.0f : 1.0f : f;
                         bool bad = false;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             float2 x = __half22float2(*reinterpret_cast<__half2 *>(&h[e]));
-                            if (odd) {
-                                const float g = f < 0.0f && f - f == 0.0f ? -1.0f : f;
-                                x.x *= g, x.y *= g;
-                            }
-                            // as in the 16-bit case: NaN and infinities of the
+                            x.x *= g, x.y *= g;
+                            // as over a 16-bit cache: NaN and infinities of the
                             // window's values are added at the end
                             if (values && pos >= s.q.P) {
                                 if (pos >= n) x.x = x.y = 0.0f;
@@ -576,15 +653,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             h[e] = *reinterpret_cast<const uint32_t *>(&two);
                         }
                         if (bad) atomicOr(&ctl.nonfinite[seg & 3], 1u << (pos - s.q.P));
+                        put(dst, tok, i % kUnits, h);
                     }
-                    // chunks 2 part and 2 part + 1 of the token's row; lanes of
-                    // one half start with the one, of the other with the other,
-                    // so that eight lanes cover the eight chunk columns
-                    unsigned char *row = dst + part / 4 * kHalfBytes + tok * 128;
-                    const int flip = part / 4 & 1, ch = part % 4 * 2;
-                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                    *reinterpret_cast<uint4 *>(row + ((ch + flip ^ (tok & 7)) << 4)) = flip ? hi : lo;
-                    *reinterpret_cast<uint4 *>(row + ((ch + 1 - flip ^ (tok & 7)) << 4)) = flip ? lo : hi;
                 }
                 fence_async_proxy();
                 __syncwarp();
@@ -594,35 +664,57 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 }
                 ++loads;
             };
+            const float *scales = which ? a.cache.v_scale : a.cache.k_scale;
             while (walk.next(t, &s)) {
-                float mine = fetch(s, s.first);
+                // this thread's scale of each tile (of token `token`, k or v): the
+                // table's entry two tiles ahead, the scale one
+                const int n = s.q.P + s.q.len;
+                int pos = s.first * kTile + token;
+                Place at;
+                at.begin(a.cache, pos);
+                auto scale_at = [&](int page) {
+                    return (unsigned)page < (unsigned)a.cache.n_pages
+                               ? __ldg(scales + kv_scale_offset(a.cache, page, at.token, s.head))
+                               : 1.0f;
+                };
+                float mine = scale_at(at.entry(a.cache, s.r, pos < n));
+                pos += kTile;
+                at.step(a.cache);
+                int page1 = at.entry(a.cache, s.r, s.count > 1 && pos < n);
                 // A warp that gave up still comes to every barrier of the four.
                 auto keys = [&](int i) {
                     const unsigned tile = done + i, b = tile & 1;
                     ok = named_all(2, 128, ok);  // the values of tile - 2 are converted
                     if (ok && tile >= 2) wait(&ctl.p_ready[b], (tile >> 1) + 1);
+                    const bool fine = mine - mine == 0.0f;
                     if (ok) {
                         sc.raw[b][which][token] = mine;
-                        const bool fine = mine - mine == 0.0f;
                         if (which) {
                             const float f = fine ? fmaxf(fabsf(mine), 0x1p-100f) : 1.0f;
                             sc.v_log2[b][token] = log2f(f);
-                            sc.v_inv[b][token] = 1.0f / f;
+                            sc.v_inv[b][token] = __frcp_rn(f);
                         } else {
                             sc.k[b][token] = (fine ? mine : 1.0f) * c;
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_addr(&ctl.scales[b]));
                     }
-                    ok = named_all(2, 128, ok);
-                    if (!ok) return;
-                    if (i + 1 < s.count) mine = fetch(s, s.first + i + 1);
-                    convert(s, s.first + i, sc.raw[b][0], false);
+                    const bool regular = named_all(2, 128, ok && fine && !(which && mine < 0.0f));
+                    if (i + 1 < s.count) {
+                        mine = scale_at(page1);
+                        pos += kTile;
+                        at.step(a.cache);
+                        page1 = at.entry(a.cache, s.r, i + 2 < s.count && pos < n);
+                    }
+                    if (ok) convert(s.first + i, sc.raw[b][0], false, regular);
+                    return regular;
                 };
-                keys(0);
+                bool regular = keys(0);
                 for (int i = 0; i < s.count; ++i) {
-                    if (i + 1 < s.count) keys(i + 1);
-                    if (ok) convert(s, s.first + i, sc.raw[(done + i) & 1][1], true);
+                    bool next = true;
+                    if (i + 1 < s.count) next = keys(i + 1);
+                    if (ok) convert(s.first + i, sc.raw[(done + i) & 1][1], true, regular);
+                    regular = next;
                 }
                 done += s.count;
                 ++seg;
@@ -634,7 +726,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         const int m = tid;  // row of the tile, lane of tensor memory
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
-        const unsigned sign = a.scale < 0.0f ? 0x80008000u : 0u;
+        const bool negative = a.scale < 0.0f;
         unsigned done = 0, seg = 0;
         bool ok = true;
         auto wait = [&](unsigned long long *bar, unsigned parity) {
@@ -645,42 +737,21 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             // a warp that gave up still comes to the four warps' barriers
             ok = named_all(1, 128, ok);
             if (!ok || !walk.next(t, &s)) break;
-            const int n = s.q.P + s.q.len, rows = s.q.len * t.group;
-            const int row_base = s.row_tile * kRowsPerTile, row = row_base + m;
-            const bool valid = row < rows, active = row_base + warp * 32 < rows;
-            const int token = min(row, rows - 1) / t.group;
-            const int head = s.head * t.group + min(row, rows - 1) - token * t.group;
-            const int packed = s.q.row0 + token;
+            // row m: head m % group of the tile's token m / group
+            const int n = s.q.P + s.q.len, token0 = s.row_tile * t.tokens;
+            const int rows = min(t.tokens, s.q.len - token0) * t.group;
+            const bool valid = m < rows, active = warp * 32 < rows;
+            const int mm = min(m, rows - 1), token = token0 + mm / t.group;
+            const int head = s.head * t.group + mm % t.group, packed = s.q.row0 + token;
             const unsigned bits = ancestors_of(a, packed, token, s.q.len);
-
-            // the tile's queries, swizzled; rows past the last are left as they
-            // are: a row of the product depends on its own query alone
             if (tid == 0) ctl.nonfinite[(seg + 3) & 3] = 0;  // the segment's before
-            const int q_rows = min(kRowsPerTile, (rows - row_base + 31) & ~31);
-            for (int i = tid; i < q_rows * kChunks; i += 128) {
-                const int qr = i / kChunks, ch = i % kChunks;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row_base + qr < rows) {
-                    const int tok = (row_base + qr) / t.group;
-                    const int hq = s.head * t.group + (row_base + qr) - tok * t.group;
-                    v = __ldg(reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(a.q) + (s.q.row0 + tok) * a.ld_q +
-                        (long long)hq * D + ch * 8));
-                    v.x ^= sign, v.y ^= sign, v.z ^= sign, v.w ^= sign;
-                }
-                if constexpr (kQuant) {
-                    const float f = to_halves(&v, kChunks);
-                    if (ch == 0) sc.q[qr] = f;
-                }
-                *reinterpret_cast<uint4 *>(smem + (ch / 8) * kRowsPerTile * 128 + qr * 128 +
-                                           ((ch % 8 ^ (qr & 7)) << 4)) = v;
-            }
-            fence_async_proxy();
-            mbar_arrive(smem_addr(&ctl.q_full));
             float factor = 1.0f;
             if constexpr (kQuant) {
-                named_sync(1, 128);
-                if (active) factor = sc.q[m];
+                if (!wait(&ctl.q_raw, seg)) continue;
+                if (active) factor = row_to_halves<D>(smem, m);
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
             }
 
             float mx = -INFINITY, l = 0.0f;  // running maximum (times c) and sum
@@ -707,11 +778,17 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         for (int j = 0; j < kTile; j += 4) {
                             const float4 ks = *reinterpret_cast<const float4 *>(&sc.k[b][j]);
                             const float4 vs = *reinterpret_cast<const float4 *>(&sc.v_log2[b][j]);
-                            x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), ks.x, vs.x));
-                            x[j + 1] = __float_as_uint(fmaf(__uint_as_float(x[j + 1]), ks.y, vs.y));
-                            x[j + 2] = __float_as_uint(fmaf(__uint_as_float(x[j + 2]), ks.z, vs.z));
-                            x[j + 3] = __float_as_uint(fmaf(__uint_as_float(x[j + 3]), ks.w, vs.w));
+                            const float2 lo = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                                                   make_float2(ks.x, ks.y), make_float2(vs.x, vs.y));
+                            const float2 hi = fma2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])),
+                                                   make_float2(ks.z, ks.w), make_float2(vs.z, vs.w));
+                            x[j] = __float_as_uint(lo.x), x[j + 1] = __float_as_uint(lo.y);
+                            x[j + 2] = __float_as_uint(hi.x), x[j + 3] = __float_as_uint(hi.y);
                         }
+                    }
+                    if (!kQuant && negative) {
+#pragma unroll
+                        for (int j = 0; j < kTile; ++j) x[j] ^= 0x80000000u;
                     }
                     if (p0 + kTile > s.q.P) {
                         // the tile reaches the window: prefix positions, then
@@ -723,9 +800,13 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         for (int j = 0; j < kTile; ++j)
                             if (!(sees >> j & 1)) x[j] = 0xFF800000u;
                     }
-                    float top = __uint_as_float(x[0]);
+                    float tops[4];
 #pragma unroll
-                    for (int j = 1; j < kTile; ++j) top = fmaxf(top, __uint_as_float(x[j]));
+                    for (int j = 0; j < 4; ++j) tops[j] = __uint_as_float(x[j]);
+#pragma unroll
+                    for (int j = 4; j < kTile; ++j)
+                        tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     if constexpr (!kQuant) top *= c;
                     // The maximum moves only when it grows by 2^kLazy: until then
                     // the weights may pass 1, and the output stays as it is.
@@ -750,29 +831,27 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         }
                     }
                     const float shift = mx == -INFINITY ? 0.0f : mx;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                    const float2 cc = make_float2(kQuant ? 1.0f : c, kQuant ? 1.0f : c);
+                    const float2 minus = make_float2(-shift, -shift);
                     uint32_t w[kTile / 2];
 #pragma unroll
                     for (int j = 0; j < kTile; j += 2) {
-                        float &s0 = sum[j / 2 % 2 * 2], &s1 = sum[j / 2 % 2 * 2 + 1];
+                        const float2 y = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                                              cc, minus);
+                        const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                        float2 &to = sum[j / 2 & 1];
                         if constexpr (kQuant) {
-                            const float u = exp2_approx(__uint_as_float(x[j]) - shift);
-                            const float v = exp2_approx(__uint_as_float(x[j + 1]) - shift);
-                            const float2 inv = *reinterpret_cast<const float2 *>(&sc.v_inv[b][j]);
-                            s0 = fmaf(u, inv.x, s0);
-                            s1 = fmaf(v, inv.y, s1);
-                            const __half2 two = __floats2half2_rn(u, v);
+                            to = fma2(u, *reinterpret_cast<const float2 *>(&sc.v_inv[b][j]), to);
+                            const __half2 two = __floats2half2_rn(u.x, u.y);
                             w[j / 2] = *reinterpret_cast<const uint32_t *>(&two);
                         } else {
-                            const float u = exp2_approx(fmaf(__uint_as_float(x[j]), c, -shift));
-                            const float v = exp2_approx(fmaf(__uint_as_float(x[j + 1]), c, -shift));
-                            s0 += u;
-                            s1 += v;
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(u, v);
+                            to = add2(u, to);
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(u.x, u.y);
                             w[j / 2] = *reinterpret_cast<const uint32_t *>(&two);
                         }
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tmem_store32(lanes + b * kTile, w);
                     tmem_wait_store();
                 }
@@ -890,7 +969,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     d[2] = slot;
                     d[3] = s.q.row0;
                     d[4] = s.head;
-                    d[5] = row_base;
+                    d[5] = token0;
                     d[6] = rows;
                     d[0] = 1;
                 }
@@ -898,13 +977,6 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         }
     }
     __syncthreads();
-    if (ctl.abort && warp == S::kCopyWarp && lane == 0) {
-        // copies still under way write this block's buffers
-        constexpr unsigned kSlots = kQuant ? S::kStages : S::kBufs;
-        unsigned long long *filled = kQuant ? ctl.stage_full : ctl.full;
-        for (unsigned i = loads - min(loads, kSlots); i < loads; ++i)
-            mbar_wait(smem_addr(&filled[i % kSlots]), i / kSlots & 1);
-    }
     if (warp == S::kMatrixWarp) tmem_free(tmem, kTmemCols);
 }
 
@@ -922,10 +994,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Tens
     const int *d = t.desc + blockIdx.x * kDescInts;
     if (__ldcg(d) == 0) return;
     const int c0 = blockIdx.x, c1 = __ldcg(d + 1), slot0 = __ldcg(d + 2), row0 = __ldcg(d + 3);
-    const int kv_head = __ldcg(d + 4), row_base = __ldcg(d + 5), rows = __ldcg(d + 6);
+    const int kv_head = __ldcg(d + 4), token0 = __ldcg(d + 5), rows = __ldcg(d + 6);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int in_tile = min(kRowsPerTile, rows - row_base);
-    for (int base = 0; base < in_tile; base += 32) {
+    for (int base = 0; base < rows; base += 32) {
         const int m = base + lane;
         auto ml = [&](int c, int which) {
             const long long slot = c == c0 ? slot0 : 2 * c;
@@ -964,10 +1035,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Tens
             l += part_l[w][lane];
         }
         __syncthreads();
-        if (m >= in_tile) continue;
-        const int row = row_base + m, token = row / t.group;
-        const int head = kv_head * t.group + row - token * t.group;
-        const long long packed = row0 + token;
+        if (m >= rows) continue;
+        const int head = kv_head * t.group + m % t.group;
+        const long long packed = row0 + token0 + m / t.group;
         const float inv = 1.0f / l;
         if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
@@ -1005,22 +1075,21 @@ EncodeFn encoder() {
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-// The cache as [page][head][token][element]; boxes of `box` tokens by 64 elements
-// under the 128-byte swizzle, or by a whole row of E4M3 codes as they are.
-bool encode(CUtensorMap *map, const dspark_kv_cache &c, void *p, int box) {
+// A 4-D tensor map of 16-bit elements (boxes of 64 elements a row, under the
+// 128-byte swizzle) or of bytes (boxes of `width` a row, as they are).
+bool encode(CUtensorMap *map, const void *p, int elem_bytes, int width, const int64_t (&dims)[4],
+            const int64_t (&strides)[3], int box1, int box3) {
     const EncodeFn f = encoder();
     if (!f) return false;
-    const int e = kv_elem_bytes(c.dtype);
-    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
-                                (cuuint64_t)c.n_kv_heads, (cuuint64_t)c.n_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride * e, (cuuint64_t)c.head_stride * e,
-                                   (cuuint64_t)c.page_stride * e};
-    const bool quant = c.dtype == DSPARK_DTYPE_E4M3;
-    const cuuint32_t boxes[4] = {quant ? (cuuint32_t)c.head_dim : 64u, (cuuint32_t)box, 1, 1};
+    cuuint64_t d[4], s[3];
+    for (int i = 0; i < 4; ++i) d[i] = (cuuint64_t)dims[i];
+    for (int i = 0; i < 3; ++i) s[i] = (cuuint64_t)(strides[i] * elem_bytes);
+    const cuuint32_t box[4] = {(cuuint32_t)width, (cuuint32_t)box1, 1, (cuuint32_t)box3};
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    return f(map, quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p, dims,
-             strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             quant ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+    const bool codes = elem_bytes == 1;
+    return f(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void *>(p), d, s, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1037,12 +1106,13 @@ size_t desc_bytes() { return (size_t)kMaxCtas * kDescInts * 4; }
 bool tensor_fits(const AttendArgs &a, int dtype, const dspark_kv_cache &c) {
     if (dtype != DSPARK_DTYPE_BF16 || c.dtype == DSPARK_DTYPE_F32) return false;
     if ((c.head_dim != 64 && c.head_dim != 128) || c.page_size % 16) return false;
+    if (a.n_q_heads / c.n_kv_heads > kRowsPerTile) return false;
     const int e = kv_elem_bytes(c.dtype);
     const int64_t strides[3] = {c.token_stride, c.head_stride, c.page_stride};
     for (int64_t s : strides)
         if (s * e % 16 || s < 1 || s * e >= (1ll << 40)) return false;
     return aligned(c.k, 16) && aligned(c.v, 16) && aligned(a.q, 16) && aligned(a.out, 16) &&
-           a.ld_q % 8 == 0 && a.ld_out % 8 == 0;
+           a.ld_q % 8 == 0 && a.ld_out % 8 == 0 && a.ld_q < (1ll << 39);
 }
 
 template <int D, bool kQuant>
@@ -1053,19 +1123,30 @@ cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *w
     TensorArgs t;
     t.a = a;
     t.group = a.n_q_heads / c.n_kv_heads;
+    t.tokens = min(kRowsPerTile / t.group, DSPARK_MAX_WINDOW);
     t.box = gcd(c.page_size, kTile);
     unsigned char *w = static_cast<unsigned char *>(workspace);
     t.part_o = reinterpret_cast<float *>(w);
     t.part_ml = reinterpret_cast<float *>(w + part_o_bytes(D));
     t.desc = reinterpret_cast<int *>(w + part_o_bytes(D) + part_ml_bytes());
-    CUtensorMap map_k, map_v;
-    if (!encode(&map_k, c, c.k, t.box) || !encode(&map_v, c, c.v, t.box)) return cudaErrorUnknown;
+    // the cache as [page][head][token][element], the queries as [row][kv head]
+    // [head of it][element]
+    const int64_t dims[4] = {D, c.page_size, c.n_kv_heads, c.n_pages};
+    const int64_t strides[3] = {c.token_stride, c.head_stride, c.page_stride};
+    const int64_t q_dims[4] = {D, t.group, c.n_kv_heads, a.max_rows};
+    const int64_t q_strides[3] = {D, (int64_t)t.group * D, a.ld_q};
+    const int e_bytes = kv_elem_bytes(c.dtype), width = kQuant ? D : 64;
+    CUtensorMap map_k, map_v, map_q;
+    if (!encode(&map_k, c.k, e_bytes, width, dims, strides, t.box, 1) ||
+        !encode(&map_v, c.v, e_bytes, width, dims, strides, t.box, 1) ||
+        !encode(&map_q, a.q, 2, 64, q_dims, q_strides, t.group, t.tokens))
+        return cudaErrorUnknown;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_tensor_kernel<D, kQuant>),
                                 S::kTotal, kSmemSlot);
     if (e != cudaSuccess) return e;
     const int grid = min(2 * sm_count(), kMaxCtas);
     e = launch_pdl(attend_tensor_kernel<D, kQuant>, dim3(grid), dim3(S::kThreads), S::kTotal, stream,
-                   map_k, map_v, t);
+                   map_k, map_v, map_q, t);
     if (e != cudaSuccess) return e;
     return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32), dim3(kJoinWarps * 32), 0, stream, t);
 }
