@@ -181,46 +181,51 @@ struct TensorArgs {
     int *desc;       // [kMaxCtas][kDescInts]: the split job that begins in a CTA
 };
 
-// Shared memory and warps of a CTA.  Over a 16-bit cache the copies land in the
-// operand ring; E4M3 codes land in a staging ring, from which four warps convert
-// them into the operand ring.
+// Shared memory and warps of a CTA.
+//   16-bit cache: one ring of buffers, into which keys and values are copied and
+//     from which they are multiplied.
+//   E4M3 cache: the keys' codes are operands as they are (their ring: kBufs), the
+//     values' codes are staged (kStages) and converted by four warps into two
+//     buffers of halves.
 template <int D, bool kQuant>
 struct TensorShape {
     static constexpr int kQBytes = kRowsPerTile * D * 2;
-    static constexpr int kBufBytes = kTile * D * 2;
-    static constexpr int kBufs = kQuant ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 9);
-    static constexpr int kStageBytes = kTile * D;
-    static constexpr int kStages = kQuant ? (D == 128 ? 3 : 8) : 0;
+    static constexpr int kBufBytes = kTile * D * (kQuant ? 1 : 2);
+    static constexpr int kBufs = kQuant ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 9);
+    static constexpr int kStages = kQuant ? (D == 128 ? 2 : 6) : 0;
     static constexpr int kStageAt = kQBytes + kBufs * kBufBytes;
-    static constexpr int kControl = kStageAt + kStages * kStageBytes;
-    static constexpr int kTotal = kControl + (kQuant ? 4096 : 1024);
-    static constexpr int kCopyWarp = kQuant ? 8 : 4, kMatrixWarp = kCopyWarp + 1;
+    static constexpr int kOpBytes = kTile * D * 2;
+    static constexpr int kOpAt = kStageAt + kStages * kBufBytes;
+    static constexpr int kControl = kOpAt + (kQuant ? 2 * kOpBytes : 0);
+    static constexpr int kTotal = kControl + (kQuant ? 3072 : 1024);
+    static constexpr int kCopyWarp = kQuant ? 8 : 4, kMatrixWarp = kCopyWarp + 1, kScaleWarp = 10;
     static constexpr int kThreads = kQuant ? 384 : 192;
+    static_assert(kTotal <= 113 * 1024, "two CTAs an SM");
 };
 
 // The barriers and words behind the buffers.  A wait tells a phase from the next
 // one only; the barriers that come in twos serve every other tile, so that a
 // role one tile behind another still waits for the phase it means.
 struct alignas(16) Control {
-    unsigned long long full[9], empty[9], stage_full[8], stage_empty[8];
+    unsigned long long full[9], empty[9], stage_full[6], stage_empty[6], op_full[2], op_empty[2];
     unsigned long long s_full[2], p_ready[2], o_done[2], scales[2];
     unsigned long long q_raw, q_full, q_empty, drain;
     unsigned tmem;
     unsigned nonfinite[4];  // window tokens whose values were zeroed, by segment
     int abort;
-    int start_r;
-    long long start_off;
+    int start_r, start_head, start_row_tile, start_tile;  // this CTA's first tile
     long long scan[40];
 };
 // What the scales of a tile's tokens become (E4M3), for every other tile.
 struct TileScales {
-    float k[2][kTile];        // k_scale times the scores' factor, to base 2
-    float v_log2[2][kTile];   // log2 v_scale: part of a weight's exponent
-    float v_inv[2][kTile];    // 1 / v_scale: takes it out of the sum of weights
-    float raw[2][2][kTile];   // the scales as they are: k, v
+    float k[2][kTile];       // k_scale times the scores' factor, to base 2
+    float v_log2[2][kTile];  // log2 v_scale: part of a weight's exponent
+    float v_inv[2][kTile];   // 1 / v_scale: takes it out of the sum of weights
+    float v[2][kTile];       // v_scale itself
+    int odd[2];              // whether a v_scale is negative, NaN or infinite
+    int pad[2];
 };
-static_assert(sizeof(Control) <= 1024 && sizeof(Control) % 16 == 0 &&
-              sizeof(Control) + sizeof(TileScales) <= 4096, "control area");
+static_assert(sizeof(Control) <= 1024 && sizeof(Control) + sizeof(TileScales) <= 3072, "control area");
 
 // A request's jobs: every (kv head, 128 rows) pair reads all its tiles.
 struct Request {
@@ -234,11 +239,23 @@ __device__ __forceinline__ bool load_request(const TensorArgs &t, int r, Request
     return true;
 }
 
-// The first tile of CTA c when T tiles are dealt to n CTAs, and the CTA of a tile.
-__device__ __forceinline__ long long first_tile(long long c, long long T, int n) { return c * T / n; }
-__device__ __forceinline__ int cta_of(long long tile, long long T, int n) {
-    return (int)(((tile + 1) * n - 1) / T);
-}
+// T tiles dealt to n CTAs in order: each gets each = T / n and the first of every
+// n / (T % n) one more.
+struct Deal {
+    int n, rest;
+    long long each;
+    __device__ __forceinline__ long long first(int c) const { return c * each + c * rest / n; }
+    // the CTA, c or later, that a tile falls to
+    __device__ __forceinline__ int cta_of(long long tile, int c) const {
+        int hi = n - 1;
+        while (c < hi) {
+            const int mid = (c + hi + 1) >> 1;
+            if (first(mid) <= tile) c = mid;
+            else hi = mid - 1;
+        }
+        return c;
+    }
+};
 
 // Consecutive tiles of one job that a CTA works through.
 struct Segment {
@@ -250,46 +267,51 @@ struct Segment {
 // each the row tiles (which read the same keys and values, so the later ones
 // find them in L2).  Every warp role walks on its own and sees the same.
 struct Walk {
-    long long left;
+    int left, r, head, row_tile, tile;
     Request q;
-    int r, head, row_tile, tile;
 
-    __device__ __forceinline__ void begin(const TensorArgs &t, int r0, long long off, long long n) {
+    __device__ __forceinline__ void begin(const TensorArgs &t, const Control &ctl, int n) {
         left = n;
-        r = r0;
-        if (n <= 0) return;
-        load_request(t, r, &q, false);
-        const long long job = off / q.tiles;
-        tile = (int)(off - job * q.tiles);
-        head = (int)(job / q.row_tiles);
-        row_tile = (int)(job - (long long)head * q.row_tiles);
+        r = ctl.start_r;
+        head = ctl.start_head;
+        row_tile = ctl.start_row_tile;
+        tile = ctl.start_tile;
+        q.row_tiles = 0;  // not loaded yet
     }
     __device__ __forceinline__ bool next(const TensorArgs &t, Segment *s) {
         if (left <= 0) return false;
+        if (q.row_tiles == 0)
+            while (!load_request(t, r, &q, false)) ++r;
         s->q = q;
         s->r = r;
         s->head = head;
         s->row_tile = row_tile;
         s->first = tile;
-        s->count = (int)min((long long)(q.tiles - tile), left);
+        s->count = min(q.tiles - tile, left);
         left -= s->count;
         tile = 0;
         if (++row_tile == q.row_tiles) {
             row_tile = 0;
             if (++head == t.a.cache.n_kv_heads) {
                 head = 0;
-                if (left > 0)
-                    while (!load_request(t, ++r, &q, false)) {
-                    }
+                ++r;
+                q.row_tiles = 0;
             }
         }
         return true;
     }
 };
 
-// Ring position of a segment's loads, in the order they are used:
-// K0, K1, V0, K2, V1, ..., V(n-1).
-__device__ __forceinline__ int ring_v(int tile, int n) { return tile < n - 1 ? 2 * tile + 2 : 2 * n - 1; }
+// A place in a ring of `slots` barriers and buffers, and the parity of its phase.
+struct Ring {
+    unsigned slot, parity;
+    __device__ __forceinline__ void step(unsigned slots) {
+        if (++slot == slots) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
 
 // Where a position lies, for a lane that steps through the tiles of a segment:
 // the table's entry is loaded ahead of its use.
@@ -312,41 +334,20 @@ struct Place {
     }
 };
 
-// A query row of bfloat16 in swizzled shared memory becomes halves in place:
-// exactly (a half has more digits), with a power of two taken out of a row whose
-// largest element is far from 1.  Returns that power.
-template <int D>
-__device__ __forceinline__ float row_to_halves(unsigned char *q, int row) {
-    auto chunk = [&](int i) {
-        return reinterpret_cast<uint4 *>(q + i / 8 * kRowsPerTile * 128 + row * 128 +
-                                         ((i % 8 ^ (row & 7)) << 4));
-    };
-    unsigned top = 0;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-        const uint4 v = *chunk(i);
-        const unsigned w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, w[k] >> 16 & 0x7FFFu));
-    }
-    const int e = (int)(top >> 7);  // biased exponent; 255: NaN or infinity
-    const bool far = top != 0 && e != 255 && (e < 125 || e > 141);
-    const int by = far ? max(e, 1) - 127 : 0;
-    const float f = by == 127 ? 0x1p-127f : __int_as_float((127 - by) << 23);
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-        uint4 *at = chunk(i);
-        uint4 v = *at;
-        unsigned *w = reinterpret_cast<unsigned *>(&v);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __half2 two = __floats2half2_rn(__uint_as_float(w[k] << 16) * f,
-                                                  __uint_as_float(w[k] & 0xFFFF0000u) * f);
-            w[k] = *reinterpret_cast<const unsigned *>(&two);
-        }
-        *at = v;
-    }
-    return __int_as_float((by + 127) << 23);
+// Two E4M3 values' worth of a query: x = hi + lo.  A bfloat16 has 8 significant
+// digits; hi takes the upper four, and what remains of x has at most four more, so
+// that hi + lo = x exactly while lo's last digit is at least E4M3's smallest step.
+__device__ __forceinline__ void split_pair(float x0, float x1, unsigned *hi, unsigned *lo) {
+    *hi = e4m3_pair(x0, x1);
+    const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)*hi, __NV_E4M3)));
+    *lo = e4m3_pair(x0 - h.x, x1 - h.y);
+}
+
+// Where 16-byte chunk c of row r lies in rows of `row_bytes` (64 or 128) under the
+// swizzle of that width.
+template <int kRowBytes>
+__device__ __forceinline__ int swizzled(int r, int c) {
+    return kRowBytes == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ (r >> 1 & 3)) << 4);
 }
 
 template <int D, bool kQuant>
@@ -385,7 +386,11 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     const int cta = blockIdx.x;
     if (tid == 0) t.desc[cta * kDescInts] = 0;
     if (cta >= n_ctas) return;
-    const long long lo = first_tile(cta, T, n_ctas), hi = first_tile(cta + 1, T, n_ctas);
+    Deal deal;
+    deal.n = n_ctas;
+    deal.each = T / n_ctas;
+    deal.rest = (int)(T - deal.each * n_ctas);
+    const long long lo = deal.first(cta), hi = deal.first(cta + 1);
     if (lo >= before && lo < before + mine) {
         long long at = before;
         for (int r = tid * per;; ++r) {
@@ -393,8 +398,11 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             if (!load_request(t, r, &q, false)) continue;
             const long long n = (long long)q.tiles * q.row_tiles * a.cache.n_kv_heads;
             if (lo < at + n) {
+                const long long job = (lo - at) / q.tiles;
                 ctl.start_r = r;
-                ctl.start_off = lo - at;
+                ctl.start_tile = (int)(lo - at - job * q.tiles);
+                ctl.start_head = (int)job / q.row_tiles;
+                ctl.start_row_tile = (int)job % q.row_tiles;
                 break;
             }
             at += n;
@@ -402,7 +410,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     }
     if (tid == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
-            mbar_init(smem_addr(&ctl.full[i]), kQuant ? 4 : 1);
+            mbar_init(smem_addr(&ctl.full[i]), 1);
             mbar_init(smem_addr(&ctl.empty[i]), 1);
         }
         for (int i = 0; i < S::kStages; ++i) {
@@ -413,7 +421,9 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
             mbar_init(smem_addr(&ctl.p_ready[i]), 4);
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
-            mbar_init(smem_addr(&ctl.scales[i]), 4);
+            mbar_init(smem_addr(&ctl.scales[i]), 1);
+            mbar_init(smem_addr(&ctl.op_full[i]), 4);
+            mbar_init(smem_addr(&ctl.op_empty[i]), 1);
         }
         mbar_init(smem_addr(&ctl.q_raw), 1);
         mbar_init(smem_addr(&ctl.q_full), 4);
@@ -429,9 +439,9 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     const uint32_t tmem = ctl.tmem, tmem_o = tmem + 2 * kTile;
     volatile int *abort = &ctl.abort;
     Walk walk;
-    walk.begin(t, ctl.start_r, ctl.start_off, hi - lo);
+    walk.begin(t, ctl, (int)(hi - lo));
     Segment s = {};
-    unsigned loads = 0;  // ring position of the segment's first load
+    Ring ring_at = {0, 0};
 
     // Over E4M3 the softmax warps take registers from the others: of the 3 x 80 a
     // thread that the three warpgroups were launched with, 136 + 56 + 48.
@@ -440,28 +450,15 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         if (warp == S::kCopyWarp) {
             // -------------------------------------------- copy warp
             constexpr int kParts = kQuant ? 1 : kHalves;  // boxes side by side
-            constexpr int kSlots = kQuant ? S::kStages : S::kBufs;
-            constexpr int kBytes = kQuant ? S::kStageBytes : S::kBufBytes;
-            unsigned long long *filled = kQuant ? ctl.stage_full : ctl.full;
-            unsigned long long *freed = kQuant ? ctl.stage_empty : ctl.empty;
             const int boxes = kTile / t.box, box = lane / kParts, half = lane % kParts;
             const bool issues = box < boxes;
-            const uint32_t dst = kQuant ? base + S::kStageAt + box * t.box * D
-                                        : ring + half * kHalfBytes + box * t.box * 128;
+            const uint32_t dst = ring + half * kHalfBytes + box * t.box * (kQuant ? D : 128);
+            Ring stage_at = {0, 0};  // the values' ring, over E4M3
             unsigned seg = 0;
             bool ok = true;
             auto wait = [&](unsigned long long *bar, unsigned parity) {
                 ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
                 return ok = __all_sync(kFullMask, ok);
-            };
-            auto load = [&](const CUtensorMap *map, int page, int token) {
-                const unsigned slot = loads % kSlots;
-                if (!wait(&freed[slot], loads / kSlots + 1)) return;
-                const uint32_t bar = smem_addr(&filled[slot]);
-                if (lane == 0) mbar_expect(bar, kBytes);
-                __syncwarp();
-                if (issues) tma_load_4d(dst + slot * kBytes, map, half * 64, token, s.head, page, bar);
-                ++loads;
             };
             while (ok && walk.next(t, &s)) {
                 // this lane's box of each tile; a page outside the pool, as past
@@ -470,54 +467,72 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 int pos = s.first * kTile + box * t.box;
                 Place at;
                 at.begin(a.cache, issues ? pos : 0);
-                auto entry = [&]() { return at.entry(a.cache, s.r, issues && pos < n); };
-                auto checked = [&](int page, int where) {
-                    if ((unsigned)page < (unsigned)a.cache.n_pages) return page;
-                    if (issues && where < n) flag(a.status, DSPARK_STATUS_BAD_INDEX);
-                    return a.cache.n_pages;
-                };
-                int page = entry(), token = at.token;
-                pos += kTile;
-                at.step(a.cache);
-                int page1 = s.count > 1 ? entry() : 0;
-                page = checked(page, pos - kTile);
-                load(&map_k, page, token);
-                // the queries, once the products with the last ones are done
-                if (seg > 0 && !wait(&ctl.q_empty, seg - 1)) break;
-                if (lane == 0) mbar_expect(smem_addr(&ctl.q_raw), t.group * t.tokens * D * 2);
-                __syncwarp();
-                if (lane < kHalves)
-                    tma_load_4d(base + lane * kRowsPerTile * 128, &map_q, lane * 64, 0, s.head,
-                                s.q.row0 + s.row_tile * t.tokens, smem_addr(&ctl.q_raw));
-                ++seg;
-                for (int i = 0; i < s.count && ok; ++i) {
-                    const int token1 = at.token;
-                    if (i + 1 < s.count) {
-                        const int now = checked(page1, pos);
-                        pos += kTile;
-                        at.step(a.cache);
-                        if (i + 2 < s.count) page1 = entry();
-                        load(&map_k, now, token1);
-                        if (ok) load(&map_v, page, token);
-                        page = now;
-                        token = token1;
-                    } else {
-                        load(&map_v, page, token);
+                auto entry = [&](bool in) { return at.entry(a.cache, s.r, issues && in && pos < n); };
+                int page = 0, token = 0, page1 = entry(true), token1;  // of the values and the keys
+                // In the order of use: K0, K1, V0, K2, V1, ..., V(n-1)
+                for (int i = 0; i <= s.count; ++i) {
+                    token1 = at.token;
+                    if (i < s.count) {
+                        if (issues && pos < n && (unsigned)page1 >= (unsigned)a.cache.n_pages) {
+                            flag(a.status, DSPARK_STATUS_BAD_INDEX);
+                            page1 = a.cache.n_pages;
+                        }
                     }
+                    pos += kTile;
+                    at.step(a.cache);
+                    const int page2 = entry(i + 1 < s.count);
+#pragma unroll 1
+                    for (int which = 0; which < 2; ++which) {  // keys of tile i, values of tile i - 1
+                        if (which == 0 ? i == s.count : i == 0) continue;
+                        const bool staged = kQuant && which == 1;
+                        Ring &r = staged ? stage_at : ring_at;
+                        if (!wait((staged ? ctl.stage_empty : ctl.empty) + r.slot, r.parity ^ 1)) break;
+                        const uint32_t bar = smem_addr((staged ? ctl.stage_full : ctl.full) + r.slot);
+                        if (lane == 0) mbar_expect(bar, S::kBufBytes);
+                        __syncwarp();
+                        if (issues)
+                            tma_load_4d(dst + (staged ? S::kStageAt - S::kQBytes : 0) + r.slot * S::kBufBytes,
+                                        which == 0 ? &map_k : &map_v, half * 64, which == 0 ? token1 : token,
+                                        s.head, which == 0 ? page1 : page, bar);
+                        if (staged) stage_at.step(S::kStages > 0 ? S::kStages : 1);
+                        else ring_at.step(S::kBufs);
+                    }
+                    if (!ok) break;
+                    if (i == 0) {
+                        // the queries, once the products with the last ones are done
+                        if (seg > 0 && !wait(&ctl.q_empty, seg - 1)) break;
+                        if (lane == 0) mbar_expect(smem_addr(&ctl.q_raw), t.group * t.tokens * D * 2);
+                        __syncwarp();
+                        if (lane < kHalves)
+                            tma_load_4d(base + lane * kRowsPerTile * 128, &map_q, lane * 64, 0, s.head,
+                                        s.q.row0 + s.row_tile * t.tokens, smem_addr(&ctl.q_raw));
+                        ++seg;
+                    }
+                    page = page1;
+                    token = token1;
+                    page1 = page2;
                 }
             }
             if (!ok && lane == 0) {
-                // copies still under way write this block's buffers
-                for (unsigned i = loads - min(loads, (unsigned)kSlots); i < loads; ++i)
-                    mbar_wait(smem_addr(&filled[i % kSlots]), i / kSlots & 1);
+                // copies still under way write this block's buffers: the last load
+                // of each slot, complete or never begun
+                for (int i = 0; i < S::kBufs; ++i)
+                    mbar_wait(smem_addr(&ctl.full[i]), i < (int)ring_at.slot ? ring_at.parity : ring_at.parity ^ 1);
+                for (int i = 0; i < S::kStages; ++i)
+                    mbar_wait(smem_addr(&ctl.stage_full[i]),
+                              i < (int)stage_at.slot ? stage_at.parity : stage_at.parity ^ 1);
                 if (seg > 0) mbar_wait(smem_addr(&ctl.q_raw), (seg - 1) & 1);
             }
         } else if (warp == S::kMatrixWarp) {
             // ------------------------------------------ matrix warp
             if (lane == 0) {
-                constexpr uint32_t word_qk = mma_word(!kQuant, kTile, false);
+                // over E4M3: codes times the queries' two parts, then halves
+                constexpr uint32_t word_qk = kQuant ? mma_word_e4m3(kTile) : mma_word(true, kTile, false);
                 constexpr uint32_t word_pv = mma_word(!kQuant, D, true);
-                const uint64_t desc_q = smem_operand(base, 16), desc_ring = smem_operand(ring, kHalfBytes);
+                constexpr int kKeyRow = kQuant ? D : 128;  // bytes of a row of the first product
+                const uint64_t desc_q = smem_operand(base, 16, kKeyRow);
+                const uint64_t desc_k = smem_operand(ring, 16, kKeyRow);
+                const uint64_t desc_v = smem_operand(kQuant ? base + S::kOpAt : ring, kHalfBytes, 128);
                 unsigned long long *queries = kQuant ? &ctl.q_full : &ctl.q_raw;
                 unsigned done = 0, seg = 0;  // tiles and segments so far
                 bool ok = true;
@@ -525,44 +540,52 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
                     return ok;
                 };
-                auto qk = [&](unsigned tile, unsigned load, bool last) {
-                    const unsigned slot = load % S::kBufs;
-                    if (!wait(&ctl.full[slot], load / S::kBufs)) return;
-                    tmem_fence_after();
-                    const uint64_t buf = desc_ring + slot * (S::kBufBytes >> 4);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_ss(tmem + (tile & 1) * kTile,
-                               desc_q + ((k / 4 * kRowsPerTile * 128 + k % 4 * 32) >> 4),
-                               buf + ((k / 4 * kHalfBytes + k % 4 * 32) >> 4), word_qk, k > 0);
-                    mma_commit(smem_addr(&ctl.s_full[tile & 1]));
-                    mma_commit(smem_addr(&ctl.empty[slot]));
-                    if (last) mma_commit(smem_addr(&ctl.q_empty));
-                };
                 while (ok && walk.next(t, &s)) {
                     if (!wait(queries, seg)) break;
-                    qk(done, loads, s.count == 1);
-                    for (int i = 0; i < s.count && ok; ++i) {
-                        const unsigned tile = done + i;
-                        if (i + 1 < s.count) {
-                            // its scores take the place of the weights before last
-                            if (i > 0 && !wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) break;
-                            qk(tile + 1, loads + 2 * i + 1, i + 2 == s.count);
-                        }
-                        const unsigned load = loads + ring_v(i, s.count), slot = load % S::kBufs;
-                        if (!wait(&ctl.full[slot], load / S::kBufs)) break;
-                        if (!wait(&ctl.p_ready[tile & 1], tile >> 1)) break;
-                        tmem_fence_after();
-                        const uint64_t buf = desc_ring + slot * (S::kBufBytes >> 4);
+                    for (int i = 0; i <= s.count && ok; ++i) {
+                        if (i < s.count) {
+                            // scores of tile i, in the place of the weights of tile i - 2
+                            const unsigned tile = done + i;
+                            if (i > 1 && !wait(&ctl.o_done[tile & 1], (tile - 2) >> 1)) break;
+                            if (!wait(&ctl.full[ring_at.slot], ring_at.parity)) break;
+                            tmem_fence_after();
+                            const uint64_t buf = desc_k + ring_at.slot * (S::kBufBytes >> 4);
+                            const uint32_t d = tmem + (tile & 1) * kTile;
+                            if constexpr (kQuant) {
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem_o, tmem + (tile & 1) * kTile + k * 8,
-                                   buf + (k * 16 * 128 >> 4), word_pv, i > 0 || k > 0);
-                        mma_commit(smem_addr(&ctl.o_done[tile & 1]));
-                        mma_commit(smem_addr(&ctl.empty[slot]));
+                                for (int k = 0; k < D / 16; ++k)  // 32 codes a step, for either part
+                                    mma_ss_e4m3(d, desc_q + (k % 2 * (S::kQBytes / 2) + k / 2 * 32 >> 4),
+                                                buf + (k / 2 * 32 >> 4), word_qk, k > 0);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k)
+                                    mma_ss(d, desc_q + ((k / 4 * kRowsPerTile * 128 + k % 4 * 32) >> 4),
+                                           buf + ((k / 4 * kHalfBytes + k % 4 * 32) >> 4), word_qk, k > 0);
+                            }
+                            mma_commit(smem_addr(&ctl.s_full[tile & 1]));
+                            mma_commit(smem_addr(&ctl.empty[ring_at.slot]));
+                            if (i + 1 == s.count) mma_commit(smem_addr(&ctl.q_empty));
+                            ring_at.step(S::kBufs);
+                        }
+                        if (i > 0) {
+                            const unsigned tile = done + i - 1;
+                            const unsigned slot = kQuant ? tile & 1 : ring_at.slot;
+                            if (!wait(kQuant ? &ctl.op_full[slot] : &ctl.full[slot],
+                                      kQuant ? tile >> 1 : ring_at.parity))
+                                break;
+                            if (!wait(&ctl.p_ready[tile & 1], tile >> 1)) break;
+                            tmem_fence_after();
+                            const uint64_t buf = desc_v + slot * (S::kOpBytes >> 4);
+#pragma unroll
+                            for (int k = 0; k < kTile / 16; ++k)
+                                mma_ts(tmem_o, tmem + (tile & 1) * kTile + k * 8,
+                                       buf + (k * 16 * 128 >> 4), word_pv, i > 1 || k > 0);
+                            mma_commit(smem_addr(&ctl.o_done[tile & 1]));
+                            mma_commit(smem_addr(kQuant ? &ctl.op_empty[slot] : &ctl.empty[slot]));
+                            if (!kQuant) ring_at.step(S::kBufs);
+                        }
                     }
                     done += s.count;
-                    loads += 2 * s.count;
                     ++seg;
                 }
                 // after a timeout: products still under way write tensor memory
@@ -573,29 +596,100 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 }
             }
             __syncwarp();
+        } else if (kQuant && warp == S::kScaleWarp) {
+            // ------------------------------------------- scale warp
+            if constexpr (kQuant) {
+                const float c = copysignf(fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f), a.scale);
+                unsigned done = 0;
+                bool ok = true;
+                while (ok && walk.next(t, &s)) {
+                    // a lane's two tokens, 32 apart: the table's entries two tiles
+                    // ahead, the scales one
+                    const int n = s.q.P + s.q.len;
+                    int pos = s.first * kTile + lane;
+                    Place at[2];
+                    at[0].begin(a.cache, pos);
+                    at[1].begin(a.cache, pos + 32);
+                    float ks[2], vs[2];
+                    int page[2];
+                    auto entries = [&](bool in) {
+                        page[0] = at[0].entry(a.cache, s.r, in && pos < n);
+                        page[1] = at[1].entry(a.cache, s.r, in && pos + 32 < n);
+                    };
+                    auto fetch = [&]() {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const bool in = (unsigned)page[i] < (unsigned)a.cache.n_pages;
+                            const long long from =
+                                in ? kv_scale_offset(a.cache, page[i], at[i].token, s.head) : 0;
+                            ks[i] = in ? __ldg(a.cache.k_scale + from) : 1.0f;
+                            vs[i] = in ? __ldg(a.cache.v_scale + from) : 1.0f;
+                        }
+                        pos += kTile;
+                        at[0].step(a.cache);
+                        at[1].step(a.cache);
+                    };
+                    entries(true);
+                    fetch();
+                    entries(s.count > 1);
+                    for (int i = 0; i < s.count; ++i) {
+                        const unsigned tile = done + i, b = tile & 1;
+                        float k[2], log2v[2], inv[2], raw[2];
+                        bool odd = false;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const bool fine = vs[j] - vs[j] == 0.0f;
+                            // a NaN or infinite k_scale makes the score NaN
+                            k[j] = ks[j] - ks[j] == 0.0f ? ks[j] * c : __int_as_float(0x7FC00000);
+                            const float f = fine ? fmaxf(fabsf(vs[j]), 0x1p-100f) : 1.0f;
+                            log2v[j] = log2f(f);
+                            inv[j] = 1.0f / f;
+                            raw[j] = vs[j];
+                            odd = odd || !fine || vs[j] < 0.0f;
+                        }
+                        odd = __any_sync(kFullMask, odd);
+                        if (i + 1 < s.count) {
+                            fetch();
+                            entries(i + 2 < s.count);
+                        }
+                        // the tile before last is through with its scales
+                        if (tile >= 2)
+                            ok = ok && role_wait(smem_addr(&ctl.o_done[b]), (tile >> 1) + 1 & 1, abort,
+                                                 a.status);
+                        if (!(ok = __all_sync(kFullMask, ok))) break;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            sc.k[b][lane + 32 * j] = k[j];
+                            sc.v_log2[b][lane + 32 * j] = log2v[j];
+                            sc.v_inv[b][lane + 32 * j] = inv[j];
+                            sc.v[b][lane + 32 * j] = raw[j];
+                        }
+                        if (lane == 0) sc.odd[b] = odd;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&ctl.scales[b]));
+                    }
+                    done += s.count;
+                }
+            }
         }
     } else if (kQuant && warp >= 4) {
         // --------------------------------------------- converting warps
         if constexpr (kQuant) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+            // A value's code becomes a half of 2^-8 times its size by moving its bits:
+            // both formats have the same digits of exponent below the sign up to the
+            // bias (7 and 15), subnormals included.  Of a word's four codes the first
+            // and third end up side by side, then the second and fourth: columns
+            // 4i + 1 and 4i + 2 of the output change places, and change back at the
+            // end, with the 2^8.
             constexpr int kUnits = D / 16;  // 16 codes a thread and step
-            const int ct = tid - 128, token = ct & (kTile - 1), which = ct / kTile;
+            constexpr int kSteps = kTile * kUnits / 128;
+            const int ct = tid - 128;
             unsigned done = 0, seg = 0;
             bool ok = true;
             auto wait = [&](unsigned long long *bar, unsigned parity) {
                 ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
                 return ok;
-            };
-            const float c = copysignf(fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f), a.scale);
-            // 16 staged codes at `unit`, as halves: exact
-            auto halves = [&](const uint4 &v, uint32_t *h) {
-                const unsigned code[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const __half2_raw two = __nv_cvt_fp8x2_to_halfraw2(
-                        (__nv_fp8x2_storage_t)(code[e / 2] >> (e & 1) * 16), __NV_E4M3);
-                    h[e] = (uint32_t)two.x | (uint32_t)two.y << 16;
-                }
             };
             // Their place is chunks 2 part and 2 part + 1 of the token's row.  Lanes
             // of one half start with the one, of the other with the other, so that
@@ -607,114 +701,81 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 *reinterpret_cast<uint4 *>(row + ((ch + flip ^ (tok & 7)) << 4)) = flip ? hi : lo;
                 *reinterpret_cast<uint4 *>(row + ((ch + 1 - flip ^ (tok & 7)) << 4)) = flip ? lo : hi;
             };
-            // The next staged tile becomes halves.  The scales go into the scores
-            // and weights, save those that are not plain numbers (`regular` says
-            // that all are): their products with the codes are written instead.
-            auto convert = [&](int j, const float *scale, bool values, bool regular) {
-                const unsigned stage = loads % S::kStages, slot = loads % S::kBufs;
-                if (!wait(&ctl.stage_full[stage], loads / S::kStages)) return;
-                if (!wait(&ctl.empty[slot], loads / S::kBufs + 1)) return;
-                const unsigned char *src = smem + S::kStageAt + stage * S::kStageBytes;
-                unsigned char *dst = smem + S::kQBytes + slot * S::kBufBytes;
-                const int p0 = j * kTile, n = s.q.P + s.q.len;
-                if (regular && !(values && p0 + kTile > s.q.P)) {
-                    constexpr int kSteps = kTile * kUnits / 128;
-                    uint4 v[kSteps];
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i)
-                        v[i] = *reinterpret_cast<const uint4 *>(src + (i * 128 + ct) * 16);
-#pragma unroll
-                    for (int i = 0; i < kSteps; ++i) {
-                        uint32_t h[8];
-                        halves(v[i], h);
-                        put(dst, (i * 128 + ct) / kUnits, ct % kUnits, h);
-                    }
-                } else {
-#pragma unroll 1
-                    for (int i = ct; i < kTile * kUnits; i += 128) {
-                        const int tok = i / kUnits, pos = p0 + tok;
-                        uint32_t h[8];
-                        halves(*reinterpret_cast<const uint4 *>(src + i * 16), h);
-                        const float f = scale[tok];
-                        const float g = f - f == 0.0f ? values && f < 0.0f ? -1.0f : 1.0f : f;
-                        bool bad = false;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float2 x = __half22float2(*reinterpret_cast<__half2 *>(&h[e]));
-                            x.x *= g, x.y *= g;
-                            // as over a 16-bit cache: NaN and infinities of the
-                            // window's values are added at the end
-                            if (values && pos >= s.q.P) {
-                                if (pos >= n) x.x = x.y = 0.0f;
-                                if (!(x.x - x.x == 0.0f)) x.x = 0.0f, bad = true;
-                                if (!(x.y - x.y == 0.0f)) x.y = 0.0f, bad = true;
-                            }
-                            const __half2 two = __floats2half2_rn(x.x, x.y);
-                            h[e] = *reinterpret_cast<const uint32_t *>(&two);
-                        }
-                        if (bad) atomicOr(&ctl.nonfinite[seg & 3], 1u << (pos - s.q.P));
-                        put(dst, tok, i % kUnits, h);
-                    }
-                }
-                fence_async_proxy();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_addr(&ctl.full[slot]));
-                    mbar_arrive(smem_addr(&ctl.stage_empty[stage]));
-                }
-                ++loads;
-            };
-            const float *scales = which ? a.cache.v_scale : a.cache.k_scale;
-            while (walk.next(t, &s)) {
-                // this thread's scale of each tile (of token `token`, k or v): the
-                // table's entry two tiles ahead, the scale one
+            while (ok && walk.next(t, &s)) {
                 const int n = s.q.P + s.q.len;
-                int pos = s.first * kTile + token;
-                Place at;
-                at.begin(a.cache, pos);
-                auto scale_at = [&](int page) {
-                    return (unsigned)page < (unsigned)a.cache.n_pages
-                               ? __ldg(scales + kv_scale_offset(a.cache, page, at.token, s.head))
-                               : 1.0f;
-                };
-                float mine = scale_at(at.entry(a.cache, s.r, pos < n));
-                pos += kTile;
-                at.step(a.cache);
-                int page1 = at.entry(a.cache, s.r, s.count > 1 && pos < n);
-                // A warp that gave up still comes to every barrier of the four.
-                auto keys = [&](int i) {
-                    const unsigned tile = done + i, b = tile & 1;
-                    ok = named_all(2, 128, ok);  // the values of tile - 2 are converted
-                    if (ok && tile >= 2) wait(&ctl.p_ready[b], (tile >> 1) + 1);
-                    const bool fine = mine - mine == 0.0f;
-                    if (ok) {
-                        sc.raw[b][which][token] = mine;
-                        if (which) {
-                            const float f = fine ? fmaxf(fabsf(mine), 0x1p-100f) : 1.0f;
-                            sc.v_log2[b][token] = log2f(f);
-                            sc.v_inv[b][token] = __frcp_rn(f);
-                        } else {
-                            sc.k[b][token] = (fine ? mine : 1.0f) * c;
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_addr(&ctl.scales[b]));
-                    }
-                    const bool regular = named_all(2, 128, ok && fine && !(which && mine < 0.0f));
-                    if (i + 1 < s.count) {
-                        mine = scale_at(page1);
-                        pos += kTile;
-                        at.step(a.cache);
-                        page1 = at.entry(a.cache, s.r, i + 2 < s.count && pos < n);
-                    }
-                    if (ok) convert(s.first + i, sc.raw[b][0], false, regular);
-                    return regular;
-                };
-                bool regular = keys(0);
                 for (int i = 0; i < s.count; ++i) {
-                    bool next = true;
-                    if (i + 1 < s.count) next = keys(i + 1);
-                    if (ok) convert(s.first + i, sc.raw[(done + i) & 1][1], true, regular);
-                    regular = next;
+                    const unsigned tile = done + i, b = tile & 1, stage = ring_at.slot;
+                    if (!wait(&ctl.scales[b], tile >> 1)) break;
+                    if (!wait(&ctl.stage_full[stage], ring_at.parity)) break;
+                    if (!wait(&ctl.op_empty[b], (tile >> 1) + 1)) break;
+                    const unsigned char *src = smem + S::kStageAt + stage * S::kBufBytes;
+                    unsigned char *dst = smem + S::kOpAt + b * S::kOpBytes;
+                    const int p0 = (s.first + i) * kTile;
+                    bool plain = p0 + kTile <= s.q.P && !*(volatile int *)&sc.odd[b];
+                    uint4 v[kSteps];
+                    if (plain) {
+                        unsigned nan = 0;
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            v[k] = *reinterpret_cast<const uint4 *>(src + (k * 128 + ct) * 16);
+                            const unsigned w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)  // a code of all ones carries into the sign
+                                nan |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                        }
+                        plain = __all_sync(kFullMask, nan == 0);
+                    }
+                    if (plain) {
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            const unsigned w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                            uint32_t h[8];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                h[2 * e] = (w[e] << 7 & 0x3F803F80u) | (w[e] << 8 & 0x80008000u);
+                                h[2 * e + 1] = (w[e] >> 1 & 0x3F803F80u) | (w[e] & 0x80008000u);
+                            }
+                            put(dst, (k * 128 + ct) / kUnits, ct % kUnits, h);
+                        }
+                    } else {
+                        // Scales that are not plain numbers (or negative) go into the
+                        // values; values past the request's end become zeros, and so
+                        // do NaN and infinities of the window, which the rows that see
+                        // them get at the end.
+#pragma unroll 1
+                        for (int k = ct; k < kTile * kUnits; k += 128) {
+                            const int tok = k / kUnits, pos = p0 + tok;
+                            const float f = sc.v[b][tok];
+                            const float g = f - f == 0.0f ? copysignf(0x1p-8f, f) : f;
+                            bool bad = false;
+#pragma unroll 1
+                            for (int e = 0; e < 4; ++e) {
+                                const unsigned w = reinterpret_cast<const unsigned *>(src + k * 16)[e];
+                                float x[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    x[y] = e4m3_value(w >> 8 * y & 0xFF) * g;
+                                    if (pos >= n) x[y] = 0.0f;
+                                    if (pos >= s.q.P && !(x[y] - x[y] == 0.0f)) x[y] = 0.0f, bad = true;
+                                }
+                                const __half2 even = __floats2half2_rn(x[0], x[2]);
+                                const __half2 odd = __floats2half2_rn(x[1], x[3]);
+                                unsigned char *row = dst + k % kUnits / 4 * kHalfBytes + tok * 128;
+                                const int ch = k % kUnits % 4 * 2 + e / 2;
+                                *reinterpret_cast<uint2 *>(row + ((ch ^ (tok & 7)) << 4) + (e & 1) * 8) =
+                                    make_uint2(*reinterpret_cast<const uint32_t *>(&even),
+                                               *reinterpret_cast<const uint32_t *>(&odd));
+                            }
+                            if (bad) atomicOr(&ctl.nonfinite[seg & 3], 1u << (pos - s.q.P));
+                        }
+                    }
+                    fence_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&ctl.op_full[b]));
+                        mbar_arrive(smem_addr(&ctl.stage_empty[stage]));
+                    }
+                    ring_at.step(S::kStages);
                 }
                 done += s.count;
                 ++seg;
@@ -727,6 +788,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
         const bool negative = a.scale < 0.0f;
+        unsigned loads = 0;  // of the segments before
         unsigned done = 0, seg = 0;
         bool ok = true;
         auto wait = [&](unsigned long long *bar, unsigned parity) {
@@ -747,8 +809,49 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             if (tid == 0) ctl.nonfinite[(seg + 3) & 3] = 0;  // the segment's before
             float factor = 1.0f;
             if constexpr (kQuant) {
-                if (!wait(&ctl.q_raw, seg)) continue;
-                if (active) factor = row_to_halves<D>(smem, m);
+                // The tile's queries as two E4M3 values an element (split_pair), each
+                // part a row-major operand of its own, in the place of the bfloat16
+                // rows.  A power of two brings a row's largest element to 128..256; a
+                // row with a NaN or an infinity has NaN for all its scores.
+                wait(&ctl.q_raw, seg);
+                uint32_t w[D / 2];
+                unsigned most = 0;
+                if (active) {
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            smem + j / 8 * kRowsPerTile * 128 + swizzled<128>(m, j % 8));
+                        w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+                    }
+#pragma unroll
+                    for (int j = 0; j < D / 2; ++j) most = max(most, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
+                }
+                if (!(ok = named_all(1, 128, ok))) continue;
+                const int e = min(max((int)(most >> 7), 8), 254) - 134;
+                factor = most >= 0x7F80u ? __int_as_float(0x7FC00000) : __int_as_float((e + 127) << 23);
+                if (active) {
+                    const float inv = __int_as_float((127 - e) << 23);
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            unsigned h[2], r[2];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const unsigned two = w[8 * j + 2 * k + y];
+                                split_pair(__uint_as_float(two << 16) * inv,
+                                           __uint_as_float(two & 0xFFFF0000u) * inv, &h[y], &r[y]);
+                            }
+                            hi[k] = h[0] | h[1] << 16;
+                            lo[k] = r[0] | r[1] << 16;
+                        }
+                        *reinterpret_cast<uint4 *>(smem + swizzled<D>(m, j)) =
+                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(smem + S::kQBytes / 2 + swizzled<D>(m, j)) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                }
                 fence_async_proxy();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
@@ -769,18 +872,15 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     if constexpr (kQuant) {
                         // scores to base 2, plus log2 of the value's scale
                         if (!wait(&ctl.scales[b], tile >> 1)) break;
-                        if (__any_sync(kFullMask, factor != 1.0f)) {
-#pragma unroll
-                            for (int j = 0; j < kTile; ++j)
-                                x[j] = __float_as_uint(__uint_as_float(x[j]) * factor);
-                        }
 #pragma unroll
                         for (int j = 0; j < kTile; j += 4) {
                             const float4 ks = *reinterpret_cast<const float4 *>(&sc.k[b][j]);
                             const float4 vs = *reinterpret_cast<const float4 *>(&sc.v_log2[b][j]);
-                            const float2 lo = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                            const float2 lo = fma2(mul2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                                                        make_float2(factor, factor)),
                                                    make_float2(ks.x, ks.y), make_float2(vs.x, vs.y));
-                            const float2 hi = fma2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])),
+                            const float2 hi = fma2(mul2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])),
+                                                        make_float2(factor, factor)),
                                                    make_float2(ks.z, ks.w), make_float2(vs.z, vs.w));
                             x[j] = __float_as_uint(lo.x), x[j + 1] = __float_as_uint(lo.y);
                             x[j + 2] = __float_as_uint(hi.x), x[j + 3] = __float_as_uint(hi.y);
@@ -818,7 +918,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         if (i > 0) {
                             if (!wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) break;
                             tmem_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < D / 32; ++h) {
                                 uint32_t o[32];
                                 tmem_load32(lanes + 2 * kTile + h * 32, o);
@@ -859,7 +959,9 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     // Values past the request's end become zeros, and so do NaN
                     // and infinities of the window (0 x NaN would reach rows that
                     // do not see them); the rows that do get them at the end.
-                    const unsigned load = loads + ring_v(i, s.count), slot = load % S::kBufs;
+                    // (loads come K0, K1, V0, K2, V1, ..., V(n-1))
+                    const unsigned load = loads + (i + 1 < s.count ? 2 * i + 2 : 2 * i + 1);
+                    const unsigned slot = load % S::kBufs;
                     if (!wait(&ctl.full[slot], load / S::kBufs)) break;
                     unsigned char *buf = smem + S::kQBytes + slot * S::kBufBytes;
                     for (int j = tid; j < kTile * kChunks; j += 128) {
@@ -910,6 +1012,16 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     uint32_t o[32];
                     tmem_load32(lanes + 2 * kTile + h * 32, o);
                     tmem_wait_load(o);
+                    if constexpr (kQuant) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const uint32_t second = o[j + 1];
+                            o[j + 1] = o[j + 2];
+                            o[j + 2] = second;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * 256.0f);
+                    }
                     for (unsigned e = extra; e; e &= e - 1) {
                         int tok;
                         const int page = kv_page(a.cache, s.r, (long long)s.q.P + __ffs(e) - 1, &tok);
@@ -965,7 +1077,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 if (s.first == 0 && !whole) {
                     // its first tile's number is the CTA's last tile's, less the ones before it
                     const long long g0 = hi - s.count;
-                    d[1] = cta_of(g0 + s.q.tiles - 1, T, n_ctas);
+                    d[1] = deal.cta_of(g0 + s.q.tiles - 1, cta);
                     d[2] = slot;
                     d[3] = s.q.row0;
                     d[4] = s.head;
@@ -1075,9 +1187,9 @@ EncodeFn encoder() {
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-// A 4-D tensor map of 16-bit elements (boxes of 64 elements a row, under the
-// 128-byte swizzle) or of bytes (boxes of `width` a row, as they are).
-bool encode(CUtensorMap *map, const void *p, int elem_bytes, int width, const int64_t (&dims)[4],
+// A 4-D tensor map of bfloat16 or bytes; boxes of `width` elements a row, with the
+// swizzle of that many bytes or none.
+bool encode(CUtensorMap *map, const void *p, int elem_bytes, int width, bool swizzle, const int64_t (&dims)[4],
             const int64_t (&strides)[3], int box1, int box3) {
     const EncodeFn f = encoder();
     if (!f) return false;
@@ -1089,7 +1201,8 @@ bool encode(CUtensorMap *map, const void *p, int elem_bytes, int width, const in
     const bool codes = elem_bytes == 1;
     return f(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
              const_cast<void *>(p), d, s, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+             : width * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1137,9 +1250,9 @@ cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *w
     const int64_t q_strides[3] = {D, (int64_t)t.group * D, a.ld_q};
     const int e_bytes = kv_elem_bytes(c.dtype), width = kQuant ? D : 64;
     CUtensorMap map_k, map_v, map_q;
-    if (!encode(&map_k, c.k, e_bytes, width, dims, strides, t.box, 1) ||
-        !encode(&map_v, c.v, e_bytes, width, dims, strides, t.box, 1) ||
-        !encode(&map_q, a.q, 2, 64, q_dims, q_strides, t.group, t.tokens))
+    if (!encode(&map_k, c.k, e_bytes, width, true, dims, strides, t.box, 1) ||
+        !encode(&map_v, c.v, e_bytes, width, !kQuant, dims, strides, t.box, 1) ||
+        !encode(&map_q, a.q, 2, 64, true, q_dims, q_strides, t.group, t.tokens))
         return cudaErrorUnknown;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_tensor_kernel<D, kQuant>),
                                 S::kTotal, kSmemSlot);

@@ -12,15 +12,15 @@ namespace dspark {
 
 // ------------------------------------------------------------- mbarriers
 
-constexpr unsigned long long kRoleWaitNs = 2000000000ull;  // 2 s: far beyond any pass
+constexpr int kRoleWaitLooks = 1 << 24;  // a second or more: far beyond any pass
 
 // Wait for a phase of an mbarrier, for warps that wait on one another inside a
-// block.  Gives up (false) after kRoleWaitNs, or as soon as another warp of
-// the block has (*abort); whoever gives up first reports the timeout.
+// block.  Gives up (false) after kRoleWaitLooks looks, or soon after another warp
+// of the block has (*abort); whoever gives up first reports the timeout.  Kept to
+// a few instructions: it stands in the kernel some thirty times.
 __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, volatile int *abort,
                                           int32_t *status) {
-    unsigned long long start = 0;
-    for (int i = 0;; ++i) {
+    for (int i = 1;; ++i) {
         uint32_t done;
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
@@ -29,14 +29,12 @@ __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, volatil
             : "r"(bar), "r"(parity)
             : "memory");
         if (done) return true;
-        if ((i & 63) != 63) continue;
-        if (*abort) return false;
-        const unsigned long long now = global_ns();
-        if (!start) start = now;
-        if (now - start >= kRoleWaitNs) {
-            *abort = 1;
-            flag(status, DSPARK_STATUS_TIMEOUT);
-            return false;
+        if (!(i & 1023)) {
+            if (i == kRoleWaitLooks && !*abort) {
+                *abort = 1;
+                flag(status, DSPARK_STATUS_TIMEOUT);
+            }
+            if (*abort) return false;
         }
     }
 }
@@ -150,14 +148,15 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t *r) {
 
 // --------------------------------------------------------- tcgen05.mma
 
-// Shared-memory operand of 16-bit elements under the 128-byte swizzle: rows of
-// 128 bytes, the 16-byte chunk c of row r at chunk c ^ (r & 7), groups of eight
-// rows 1024 bytes apart.  Rows are the M or N index with 64 consecutive k a row
-// (K-major; lead unused), or the k index with 64 consecutive n a row (N-major;
-// the next 64 n lie `lead` bytes on).
-__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead) {
+// Shared-memory operand in rows of 128 or 64 bytes under the swizzle of that width:
+// the 16-byte chunk c of row r at chunk c ^ (r & 7), or c ^ (r / 2 & 3), groups of
+// eight rows one after another.  Rows are the M or N index with consecutive k a row
+// (K-major; `lead` unused), or the k index with consecutive n a row (N-major; the
+// next row's worth of n lies `lead` bytes on).
+__device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead, int row_bytes) {
     return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)((lead >> 4) & 0x3FFF) << 16 |
-           (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+           (uint64_t)(8 * row_bytes >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)(row_bytes == 128 ? 2 : 4) << 61;
 }
 
 // Instruction word of a 16-bit product with 32-bit accumulators, M = 128:
@@ -165,6 +164,11 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr, uint32_t lead) {
 constexpr uint32_t mma_word(bool bf16, int n, bool b_n_major) {
     return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_n_major ? 1u << 16 : 0u) |
            (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+
+// The same for E4M3 operands, both K-major.
+constexpr uint32_t mma_word_e4m3(int n) {
+    return 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
 // D += A B (D = A B when !accumulate), one K step of 16, A in shared memory.
@@ -176,7 +180,16 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
         : "memory");
 }
-// The same with A in tensor memory (two 16-bit k a column).
+// The same for E4M3 operands, one K step of 32.
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t word,
+                                            bool accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// The 16-bit product with A in tensor memory (two 16-bit k a column).
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t word,
                                        bool accumulate) {
     asm volatile(
@@ -212,6 +225,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         " mov.b64 z, {%6, %7};\n fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " mul.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
