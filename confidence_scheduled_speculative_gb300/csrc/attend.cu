@@ -197,7 +197,7 @@ struct TensorShape {
     static constexpr int kOpBytes = kTile * D * 2;
     static constexpr int kOpAt = kStageAt + kStages * kBufBytes;
     static constexpr int kControl = kOpAt + (kQuant ? 2 * kOpBytes : 0);
-    static constexpr int kTotal = kControl + (kQuant ? 3072 : 1024);
+    static constexpr int kTotal = kControl + (kQuant ? 4096 : 1024);
     static constexpr int kCopyWarp = kQuant ? 8 : 4, kMatrixWarp = kCopyWarp + 1, kScaleWarp = 10;
     static constexpr int kThreads = kQuant ? 384 : 192;
     static_assert(kTotal <= 113 * 1024, "two CTAs an SM");
@@ -224,8 +224,9 @@ struct TileScales {
     float v[2][kTile];       // v_scale itself
     int odd[2];              // whether a v_scale is negative, NaN or infinite
     int pad[2];
+    float q[2][kRowsPerTile];  // what the queries were divided by, for every other segment
 };
-static_assert(sizeof(Control) <= 1024 && sizeof(Control) + sizeof(TileScales) <= 3072, "control area");
+static_assert(sizeof(Control) <= 1024 && sizeof(Control) + sizeof(TileScales) <= 4096, "control area");
 
 // A request's jobs: every (kv head, 128 rows) pair reads all its tiles.
 struct Request {
@@ -443,10 +444,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     Segment s = {};
     Ring ring_at = {0, 0};
 
-    // Over E4M3 the softmax warps take registers from the others: of the 3 x 80 a
-    // thread that the three warpgroups were launched with, 136 + 56 + 48.
     if (warp >= S::kCopyWarp) {
-        if constexpr (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == S::kCopyWarp) {
             // -------------------------------------------- copy warp
             constexpr int kParts = kQuant ? 1 : kHalves;  // boxes side by side
@@ -675,7 +673,6 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     } else if (kQuant && warp >= 4) {
         // --------------------------------------------- converting warps
         if constexpr (kQuant) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
             // A value's code becomes a half of 2^-8 times its size by moving its bits:
             // both formats have the same digits of exponent below the sign up to the
             // bias (7 and 15), subnormals included.  Of a word's four codes the first
@@ -701,8 +698,75 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 *reinterpret_cast<uint4 *>(row + ((ch + flip ^ (tok & 7)) << 4)) = flip ? hi : lo;
                 *reinterpret_cast<uint4 *>(row + ((ch + 1 - flip ^ (tok & 7)) << 4)) = flip ? lo : hi;
             };
-            while (ok && walk.next(t, &s)) {
+            for (;;) {
+                // a warp that gave up still comes to the four warps' barriers
+                ok = named_all(2, 128, ok);
+                if (!ok || !walk.next(t, &s)) break;
                 const int n = s.q.P + s.q.len;
+                // The tile's queries, a row a thread, as two E4M3 values an element
+                // (split_pair): each part a K-major operand of its own, in the place
+                // of the bfloat16 rows.  A power of two brings a row's largest element
+                // to 128..256; a row with a NaN or an infinity gets NaN scores.
+                wait(&ctl.q_raw, seg);
+                unsigned most = 0;
+                if (ok) {
+#pragma unroll 4
+                    for (int j = 0; j < D / 8; ++j) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            smem + j / 8 * kRowsPerTile * 128 + swizzled<128>(ct, j % 8));
+                        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) most = max(most, max(w[k] & 0x7FFFu, w[k] >> 16 & 0x7FFFu));
+                    }
+                }
+                const int exponent = min(max((int)(most >> 7), 8), 254) - 134;
+                const float by = __int_as_float((127 - exponent) << 23);
+                sc.q[seg & 1][ct] =
+                    most >= 0x7F80u ? __int_as_float(0x7FC00000) : __int_as_float((exponent + 127) << 23);
+                uint4 kept[4];  // the low parts of the first 64 elements: their place is not free yet
+#pragma unroll 1
+                for (int h = 0; h < kHalves; ++h) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = *reinterpret_cast<const uint4 *>(smem + h * kRowsPerTile * 128 +
+                                                                swizzled<128>(ct, j));
+                    if (D == 64) named_sync(2, 128);  // shorter rows: in the place of other threads' ones
+                    uint4 low[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const unsigned w[8] = {v[2 * j].x,     v[2 * j].y,     v[2 * j].z,     v[2 * j].w,
+                                               v[2 * j + 1].x, v[2 * j + 1].y, v[2 * j + 1].z, v[2 * j + 1].w};
+                        unsigned hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            unsigned h0, h1, l0, l1;
+                            split_pair(__uint_as_float(w[2 * k] << 16) * by,
+                                       __uint_as_float(w[2 * k] & 0xFFFF0000u) * by, &h0, &l0);
+                            split_pair(__uint_as_float(w[2 * k + 1] << 16) * by,
+                                       __uint_as_float(w[2 * k + 1] & 0xFFFF0000u) * by, &h1, &l1);
+                            hi[k] = h0 | h1 << 16;
+                            lo[k] = l0 | l1 << 16;
+                        }
+                        *reinterpret_cast<uint4 *>(smem + swizzled<D>(ct, 4 * h + j)) =
+                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        low[j] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    if (h + 1 < kHalves) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) kept[j] = low[j];
+                        continue;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        unsigned char *part = smem + S::kQBytes / 2;
+                        if (kHalves == 2) *reinterpret_cast<uint4 *>(part + swizzled<D>(ct, j)) = kept[j];
+                        *reinterpret_cast<uint4 *>(part + swizzled<D>(ct, 4 * h + j)) = low[j];
+                    }
+                }
+                fence_async_proxy();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
                 for (int i = 0; i < s.count; ++i) {
                     const unsigned tile = done + i, b = tile & 1, stage = ring_at.slot;
                     if (!wait(&ctl.scales[b], tile >> 1)) break;
@@ -712,32 +776,25 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     unsigned char *dst = smem + S::kOpAt + b * S::kOpBytes;
                     const int p0 = (s.first + i) * kTile;
                     bool plain = p0 + kTile <= s.q.P && !*(volatile int *)&sc.odd[b];
-                    uint4 v[kSteps];
                     if (plain) {
                         unsigned nan = 0;
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < kSteps; ++k) {
-                            v[k] = *reinterpret_cast<const uint4 *>(src + (k * 128 + ct) * 16);
-                            const unsigned w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)  // a code of all ones carries into the sign
-                                nan |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                        }
-                        plain = __all_sync(kFullMask, nan == 0);
-                    }
-                    if (plain) {
-#pragma unroll
-                        for (int k = 0; k < kSteps; ++k) {
-                            const unsigned w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                            const uint4 v = *reinterpret_cast<const uint4 *>(src + (k * 128 + ct) * 16);
+                            const unsigned w[4] = {v.x, v.y, v.z, v.w};
                             uint32_t h[8];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
+                                // a code of all ones, a NaN, carries into the sign
+                                nan |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                                 h[2 * e] = (w[e] << 7 & 0x3F803F80u) | (w[e] << 8 & 0x80008000u);
                                 h[2 * e + 1] = (w[e] >> 1 & 0x3F803F80u) | (w[e] & 0x80008000u);
                             }
                             put(dst, (k * 128 + ct) / kUnits, ct % kUnits, h);
                         }
-                    } else {
+                        plain = __all_sync(kFullMask, nan == 0);
+                    }
+                    if (!plain) {
                         // Scales that are not plain numbers (or negative) go into the
                         // values; values past the request's end become zeros, and so
                         // do NaN and infinities of the window, which the rows that see
@@ -783,7 +840,6 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         }
     } else {
         // --------------------------------------------- softmax warps
-        if constexpr (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         const int m = tid;  // row of the tile, lane of tensor memory
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
@@ -808,106 +864,89 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             const unsigned bits = ancestors_of(a, packed, token, s.q.len);
             if (tid == 0) ctl.nonfinite[(seg + 3) & 3] = 0;  // the segment's before
             float factor = 1.0f;
-            if constexpr (kQuant) {
-                // The tile's queries as two E4M3 values an element (split_pair), each
-                // part a row-major operand of its own, in the place of the bfloat16
-                // rows.  A power of two brings a row's largest element to 128..256; a
-                // row with a NaN or an infinity has NaN for all its scores.
-                wait(&ctl.q_raw, seg);
-                uint32_t w[D / 2];
-                unsigned most = 0;
-                if (active) {
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            smem + j / 8 * kRowsPerTile * 128 + swizzled<128>(m, j % 8));
-                        w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-                    }
-#pragma unroll
-                    for (int j = 0; j < D / 2; ++j) most = max(most, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
-                }
-                if (!(ok = named_all(1, 128, ok))) continue;
-                const int e = min(max((int)(most >> 7), 8), 254) - 134;
-                factor = most >= 0x7F80u ? __int_as_float(0x7FC00000) : __int_as_float((e + 127) << 23);
-                if (active) {
-                    const float inv = __int_as_float((127 - e) << 23);
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            unsigned h[2], r[2];
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const unsigned two = w[8 * j + 2 * k + y];
-                                split_pair(__uint_as_float(two << 16) * inv,
-                                           __uint_as_float(two & 0xFFFF0000u) * inv, &h[y], &r[y]);
-                            }
-                            hi[k] = h[0] | h[1] << 16;
-                            lo[k] = r[0] | r[1] << 16;
-                        }
-                        *reinterpret_cast<uint4 *>(smem + swizzled<D>(m, j)) =
-                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(smem + S::kQBytes / 2 + swizzled<D>(m, j)) =
-                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
-                }
-                fence_async_proxy();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
-            }
-
             float mx = -INFINITY, l = 0.0f;  // running maximum (times c) and sum
             for (int i = 0; i < s.count; ++i) {
                 const unsigned tile = done + i, b = tile & 1;
                 const int p0 = (s.first + i) * kTile;
                 if (!wait(&ctl.s_full[b], tile >> 1)) break;
                 if (active) {
+                    if (kQuant && !wait(&ctl.scales[b], tile >> 1)) break;
                     tmem_fence_after();
-                    uint32_t x[kTile];
-                    tmem_load32(lanes + b * kTile, x);
-                    tmem_load32(lanes + b * kTile + 32, x + 32);
-                    tmem_wait_load(x);
-                    tmem_wait_load(x + 32);
-                    if constexpr (kQuant) {
-                        // scores to base 2, plus log2 of the value's scale
-                        if (!wait(&ctl.scales[b], tile >> 1)) break;
-#pragma unroll
-                        for (int j = 0; j < kTile; j += 4) {
-                            const float4 ks = *reinterpret_cast<const float4 *>(&sc.k[b][j]);
-                            const float4 vs = *reinterpret_cast<const float4 *>(&sc.v_log2[b][j]);
-                            const float2 lo = fma2(mul2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
-                                                        make_float2(factor, factor)),
-                                                   make_float2(ks.x, ks.y), make_float2(vs.x, vs.y));
-                            const float2 hi = fma2(mul2(make_float2(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])),
-                                                        make_float2(factor, factor)),
-                                                   make_float2(ks.z, ks.w), make_float2(vs.z, vs.w));
-                            x[j] = __float_as_uint(lo.x), x[j + 1] = __float_as_uint(lo.y);
-                            x[j + 2] = __float_as_uint(hi.x), x[j + 3] = __float_as_uint(hi.y);
-                        }
-                    }
-                    if (!kQuant && negative) {
-#pragma unroll
-                        for (int j = 0; j < kTile; ++j) x[j] ^= 0x80000000u;
-                    }
+                    const uint32_t at = lanes + b * kTile;
+                    // what this row sees of the tile: prefix positions, then its
+                    // ancestors in the window
+                    unsigned long long sees = ~0ull;
                     if (p0 + kTile > s.q.P) {
-                        // the tile reaches the window: prefix positions, then
-                        // this row's ancestors
                         const int pre = max(s.q.P - p0, 0), skip = max(p0 - s.q.P, 0);
                         const unsigned long long w = skip < 32 ? (unsigned long long)(bits >> skip) : 0;
-                        const unsigned long long sees = w << pre | ((1ull << pre) - 1);
-#pragma unroll
-                        for (int j = 0; j < kTile; ++j)
-                            if (!(sees >> j & 1)) x[j] = 0xFF800000u;
+                        sees = w << pre | ((1ull << pre) - 1);
                     }
-                    float tops[4];
+                    const bool all = __all_sync(kFullMask, sees == ~0ull);
+                    float top;
+                    uint32_t x[kQuant ? 16 : kTile];
+                    if constexpr (kQuant) {
+                        if (i == 0) factor = sc.q[seg & 1][m];
+                        top = -INFINITY;
+                        // Scores to base 2, plus log2 of the value's scale, in the
+                        // scores' place.  Sixteen columns a step of a loop, here and
+                        // below: the warps of a scheduler run four kinds of code in
+                        // turn, which unrolled is more than its instruction cache.
+#pragma unroll 1
+                        for (int j = 0; j < kTile; j += 16) {
+                            float4 ks[4], vs[4];
+                            tmem_load16(at + j, x);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) tops[j] = __uint_as_float(x[j]);
+                            for (int k = 0; k < 4; ++k) {
+                                ks[k] = load_shared4(smem_addr(&sc.k[b][j + 4 * k]));
+                                vs[k] = load_shared4(smem_addr(&sc.v_log2[b][j + 4 * k]));
+                            }
+                            tmem_wait_load16(x);
+                            const float2 ff = make_float2(factor, factor);
+                            const unsigned sixteen = (unsigned)(sees >> j);
 #pragma unroll
-                    for (int j = 4; j < kTile; ++j)
-                        tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
-                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    if constexpr (!kQuant) top *= c;
+                            for (int k = 0; k < 16; k += 2) {
+                                const float4 kk = ks[k / 4], vv = vs[k / 4];
+                                const float2 y = fma2(mul2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ff),
+                                                      k & 2 ? make_float2(kk.z, kk.w) : make_float2(kk.x, kk.y),
+                                                      k & 2 ? make_float2(vv.z, vv.w) : make_float2(vv.x, vv.y));
+                                x[k] = __float_as_uint(y.x);
+                                x[k + 1] = __float_as_uint(y.y);
+                            }
+                            if (!all) {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    if (!(sixteen >> k & 1)) x[k] = 0xFF800000u;
+                            }
+                            float tops[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+#pragma unroll
+                            for (int k = 2; k < 16; ++k)
+                                tops[k & 1] = fmaxf(tops[k & 1], __uint_as_float(x[k]));
+                            top = fmaxf(top, fmaxf(tops[0], tops[1]));
+                            tmem_store16(at + j, x);
+                        }
+                        tmem_wait_store();
+                    } else {
+                        tmem_load32(at, x);
+                        tmem_load32(at + 32, x + 32);
+                        tmem_wait_load(x);
+                        tmem_wait_load(x + 32);
+                        if (negative) {
+#pragma unroll
+                            for (int j = 0; j < kTile; ++j) x[j] ^= 0x80000000u;
+                        }
+                        if (!all) {
+#pragma unroll
+                            for (int j = 0; j < kTile; ++j)
+                                if (!(sees >> j & 1)) x[j] = 0xFF800000u;
+                        }
+                        float tops[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) tops[j] = __uint_as_float(x[j]);
+#pragma unroll
+                        for (int j = 4; j < kTile; ++j)
+                            tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
+                        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * c;
+                    }
                     // The maximum moves only when it grows by 2^kLazy: until then
                     // the weights may pass 1, and the output stays as it is.
                     const bool grow = top > mx + kLazy || (mx == -INFINITY && top > mx);
@@ -919,40 +958,58 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             if (!wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) break;
                             tmem_fence_after();
 #pragma unroll 1
-                            for (int h = 0; h < D / 32; ++h) {
-                                uint32_t o[32];
-                                tmem_load32(lanes + 2 * kTile + h * 32, o);
-                                tmem_wait_load(o);
+                            for (int h = 0; h < D / 16; ++h) {
+                                uint32_t o[16];
+                                tmem_load16(lanes + 2 * kTile + h * 16, o);
+                                tmem_wait_load16(o);
 #pragma unroll
-                                for (int j = 0; j < 32; ++j)
+                                for (int j = 0; j < 16; ++j)
                                     o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_store32(lanes + 2 * kTile + h * 32, o);
+                                tmem_store16(lanes + 2 * kTile + h * 16, o);
                             }
                         }
                     }
                     const float shift = mx == -INFINITY ? 0.0f : mx;
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    const float2 cc = make_float2(kQuant ? 1.0f : c, kQuant ? 1.0f : c);
                     const float2 minus = make_float2(-shift, -shift);
-                    uint32_t w[kTile / 2];
+                    if constexpr (kQuant) {
+#pragma unroll 1
+                        for (int j = 0; j < kTile; j += 16) {
+                            float4 inv[4];
+                            uint32_t w[8];
+                            tmem_load16(at + j, x);
 #pragma unroll
-                    for (int j = 0; j < kTile; j += 2) {
-                        const float2 y = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
-                                              cc, minus);
-                        const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                        float2 &to = sum[j / 2 & 1];
-                        if constexpr (kQuant) {
-                            to = fma2(u, *reinterpret_cast<const float2 *>(&sc.v_inv[b][j]), to);
-                            const __half2 two = __floats2half2_rn(u.x, u.y);
-                            w[j / 2] = *reinterpret_cast<const uint32_t *>(&two);
-                        } else {
-                            to = add2(u, to);
+                            for (int k = 0; k < 4; ++k) inv[k] = load_shared4(smem_addr(&sc.v_inv[b][j + 4 * k]));
+                            tmem_wait_load16(x);
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) {
+                                const float2 y =
+                                    add2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), minus);
+                                const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                                const float4 f = inv[k / 4];
+                                sum[k / 2 & 1] = fma2(u, k & 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y),
+                                                      sum[k / 2 & 1]);
+                                const __half2 two = __floats2half2_rn(u.x, u.y);
+                                w[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                            }
+                            // over scores that have been read (columns j / 2 <= j)
+                            tmem_store8(at + j / 2, w);
+                        }
+                    } else {
+                        const float2 cc = make_float2(c, c);
+                        uint32_t w[kTile / 2];
+#pragma unroll
+                        for (int j = 0; j < kTile; j += 2) {
+                            const float2 y = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                                                  cc, minus);
+                            const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                            sum[j / 2 & 1] = add2(u, sum[j / 2 & 1]);
                             const __nv_bfloat162 two = __floats2bfloat162_rn(u.x, u.y);
                             w[j / 2] = *reinterpret_cast<const uint32_t *>(&two);
                         }
+                        tmem_store32(at, w);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    tmem_store32(lanes + b * kTile, w);
                     tmem_wait_store();
                 }
                 if (!kQuant && p0 + kTile > s.q.P) {
