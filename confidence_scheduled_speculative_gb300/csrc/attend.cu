@@ -437,7 +437,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     if (warp == S::kMatrixWarp) tmem_alloc(smem_addr(&ctl.tmem), kTmemCols);
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = ctl.tmem, tmem_o = tmem + 2 * kTile;
+    const uint32_t tmem = ctl.tmem;
     volatile int *abort = &ctl.abort;
     Walk walk;
     walk.begin(t, ctl, (int)(hi - lo));
@@ -523,32 +523,38 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             }
         } else if (warp == S::kMatrixWarp) {
             // ------------------------------------------ matrix warp
-            if (lane == 0) {
-                // over E4M3: codes times the queries' two parts, then halves
-                constexpr uint32_t word_qk = kQuant ? mma_word_e4m3(kTile) : mma_word(true, kTile, false);
-                constexpr uint32_t word_pv = mma_word(!kQuant, D, true);
-                constexpr int kKeyRow = kQuant ? D : 128;  // bytes of a row of the first product
-                const uint64_t desc_q = smem_operand(base, 16, kKeyRow);
-                const uint64_t desc_k = smem_operand(ring, 16, kKeyRow);
-                const uint64_t desc_v = smem_operand(kQuant ? base + S::kOpAt : ring, kHalfBytes, 128);
-                unsigned long long *queries = kQuant ? &ctl.q_full : &ctl.q_raw;
-                unsigned done = 0, seg = 0;  // tiles and segments so far
-                bool ok = true;
-                auto wait = [&](unsigned long long *bar, unsigned parity) {
-                    ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
-                    return ok;
-                };
-                while (ok && walk.next(t, &s)) {
-                    if (!wait(queries, seg)) break;
-                    for (int i = 0; i <= s.count && ok; ++i) {
-                        if (i < s.count) {
-                            // scores of tile i, in the place of the weights of tile i - 2
-                            const unsigned tile = done + i;
-                            if (i > 1 && !wait(&ctl.o_done[tile & 1], (tile - 2) >> 1)) break;
-                            if (!wait(&ctl.full[ring_at.slot], ring_at.parity)) break;
-                            tmem_fence_after();
-                            const uint64_t buf = desc_k + ring_at.slot * (S::kBufBytes >> 4);
-                            const uint32_t d = tmem + (tile & 1) * kTile;
+            // The whole warp keeps step, so that addresses stay in uniform
+            // registers; one lane issues.
+            // over E4M3: codes times the queries' two parts, then halves
+            constexpr uint32_t word_qk = kQuant ? mma_word_e4m3(kTile) : mma_word(true, kTile, false);
+            constexpr uint32_t word_pv = mma_word(!kQuant, D, true);
+            constexpr int kKeyRow = kQuant ? D : 128;  // bytes of a row of the first product
+            const uint32_t ubase = __shfl_sync(kFullMask, base, 0);
+            const uint32_t utmem = __shfl_sync(kFullMask, tmem, 0);
+            const uint64_t desc_q = smem_operand(ubase, 16, kKeyRow);
+            const uint64_t desc_k = smem_operand(ubase + S::kQBytes, 16, kKeyRow);
+            const uint64_t desc_v = smem_operand(ubase + (kQuant ? S::kOpAt : S::kQBytes), kHalfBytes, 128);
+            unsigned long long *queries = kQuant ? &ctl.q_full : &ctl.q_raw;
+            const bool leader = elect_one();
+            unsigned done = 0, seg = 0;  // tiles and segments so far
+            bool ok = true;
+            auto wait = [&](unsigned long long *bar, unsigned parity) {
+                ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
+                return ok = __all_sync(kFullMask, ok);
+            };
+            while (ok && walk.next(t, &s)) {
+                if (!wait(queries, seg)) break;
+                const int count = __shfl_sync(kFullMask, s.count, 0);
+                for (int i = 0; i <= count && ok; ++i) {
+                    if (i < count) {
+                        // scores of tile i, in the place of the weights of tile i - 2
+                        const unsigned tile = done + i;
+                        if (i > 1 && !wait(&ctl.o_done[tile & 1], (tile - 2) >> 1)) break;
+                        if (!wait(&ctl.full[ring_at.slot], ring_at.parity)) break;
+                        tmem_fence_after();
+                        const uint64_t buf = desc_k + ring_at.slot * (S::kBufBytes >> 4);
+                        const uint32_t d = utmem + (tile & 1) * kTile;
+                        if (leader) {
                             if constexpr (kQuant) {
 #pragma unroll
                                 for (int k = 0; k < D / 16; ++k)  // 32 codes a step, for either part
@@ -562,36 +568,41 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             }
                             mma_commit(smem_addr(&ctl.s_full[tile & 1]));
                             mma_commit(smem_addr(&ctl.empty[ring_at.slot]));
-                            if (i + 1 == s.count) mma_commit(smem_addr(&ctl.q_empty));
-                            ring_at.step(S::kBufs);
+                            if (i + 1 == count) mma_commit(smem_addr(&ctl.q_empty));
                         }
-                        if (i > 0) {
-                            const unsigned tile = done + i - 1;
-                            const unsigned slot = kQuant ? tile & 1 : ring_at.slot;
-                            if (!wait(kQuant ? &ctl.op_full[slot] : &ctl.full[slot],
-                                      kQuant ? tile >> 1 : ring_at.parity))
-                                break;
-                            if (!wait(&ctl.p_ready[tile & 1], tile >> 1)) break;
-                            tmem_fence_after();
-                            const uint64_t buf = desc_v + slot * (S::kOpBytes >> 4);
+                        __syncwarp();
+                        ring_at.step(S::kBufs);
+                    }
+                    if (i > 0) {
+                        const unsigned tile = done + i - 1;
+                        const unsigned slot = kQuant ? tile & 1 : ring_at.slot;
+                        if (!wait(kQuant ? &ctl.op_full[slot] : &ctl.full[slot],
+                                  kQuant ? tile >> 1 : ring_at.parity))
+                            break;
+                        if (!wait(&ctl.p_ready[tile & 1], tile >> 1)) break;
+                        tmem_fence_after();
+                        const uint64_t buf = desc_v + slot * (S::kOpBytes >> 4);
+                        const uint32_t w = utmem + (tile & 1) * kTile;
+                        if (leader) {
 #pragma unroll
                             for (int k = 0; k < kTile / 16; ++k)
-                                mma_ts(tmem_o, tmem + (tile & 1) * kTile + k * 8,
-                                       buf + (k * 16 * 128 >> 4), word_pv, i > 1 || k > 0);
+                                mma_ts(utmem + 2 * kTile, w + k * 8, buf + (k * 16 * 128 >> 4), word_pv,
+                                       i > 1 || k > 0);
                             mma_commit(smem_addr(&ctl.o_done[tile & 1]));
                             mma_commit(smem_addr(kQuant ? &ctl.op_empty[slot] : &ctl.empty[slot]));
-                            if (!kQuant) ring_at.step(S::kBufs);
                         }
+                        __syncwarp();
+                        if (!kQuant) ring_at.step(S::kBufs);
                     }
-                    done += s.count;
-                    ++seg;
                 }
-                // after a timeout: products still under way write tensor memory
-                // and barriers of this block
-                if (!ok) {
-                    mma_commit(smem_addr(&ctl.drain));
-                    mbar_wait(smem_addr(&ctl.drain), 0);
-                }
+                done += count;
+                ++seg;
+            }
+            // after a timeout: products still under way write tensor memory and
+            // barriers of this block
+            if (!ok && leader) {
+                mma_commit(smem_addr(&ctl.drain));
+                mbar_wait(smem_addr(&ctl.drain), 0);
             }
             __syncwarp();
         } else if (kQuant && warp == S::kScaleWarp) {
