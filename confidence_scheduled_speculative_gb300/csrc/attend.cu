@@ -36,19 +36,23 @@ struct AttendArgs {
     int32_t *status;
 };
 
-// Request r's window: rows [*row0, *row0 + *len) and prefix *P.  False when it
-// has none or one that cannot be used (flagged by the caller that asks for it).
-__device__ __forceinline__ bool window_of(const AttendArgs &a, int r, int *row0, int *len, int *P,
-                                          bool report) {
-    const int lo = __ldg(a.cu + r), hi = __ldg(a.cu + r + 1);
-    *row0 = lo;
-    *len = hi - lo;
-    *P = __ldg(a.prefix + r);
-    if (hi == lo) return false;
+// A request's entries as they are: rows [lo, hi) and the prefix length.
+struct Window {
+    int lo, hi, P;
+};
+
+__device__ __forceinline__ Window load_window(const AttendArgs &a, int r) {
+    return {__ldg(a.cu + r), __ldg(a.cu + r + 1), __ldg(a.prefix + r)};
+}
+
+// Whether a window has rows and can be used; with `report`, flags why not.
+__device__ __forceinline__ bool usable(const AttendArgs &a, const Window &w, bool report) {
+    if (w.hi == w.lo) return false;
     int bad = 0;
-    if (lo < 0 || hi < lo || hi - lo > DSPARK_MAX_WINDOW || hi > a.max_rows)
+    if (w.lo < 0 || w.hi < w.lo || w.hi - w.lo > DSPARK_MAX_WINDOW || w.hi > a.max_rows)
         bad = DSPARK_STATUS_BAD_LEN;
-    else if (*P < 0 || (long long)*P + *len > (long long)a.cache.table_width * a.cache.page_size)
+    else if (w.P < 0 ||
+             (long long)w.P + (w.hi - w.lo) > (long long)a.cache.table_width * a.cache.page_size)
         bad = DSPARK_STATUS_BAD_INDEX;
     if (bad && report) flag(a.status, bad);
     return !bad;
@@ -76,8 +80,9 @@ __global__ void __launch_bounds__(kAnyWarps * 32) attend_any_kernel(AttendArgs a
         else hi = mid - 1;
     }
     const int r = lo;
-    int row0, len, P;
-    if (!window_of(a, r, &row0, &len, &P, threadIdx.x == 0) || row < row0) return;
+    const Window win = load_window(a, r);
+    if (!usable(a, win, threadIdx.x == 0) || row < win.lo) return;
+    const int row0 = win.lo, len = win.hi - win.lo, P = win.P;
     const unsigned bits = ancestors_of(a, row, row - row0, len);
     const int kh = h / (a.n_q_heads / a.cache.n_kv_heads);
 
@@ -175,6 +180,7 @@ struct TensorArgs {
     AttendArgs a;
     int group;   // query heads a kv head
     int tokens;  // window tokens a row tile: all their heads in 128 rows
+    int few;     // window tokens whose heads fit in 64 rows
     int box;     // cache tokens a TMA box
     float *part_o;   // [2 kMaxCtas][D / 4][128] float4
     float *part_ml;  // [2 kMaxCtas][2][128]
@@ -197,9 +203,10 @@ struct TensorShape {
     static constexpr int kOpBytes = kTile * D * 2;
     static constexpr int kOpAt = kStageAt + kStages * kBufBytes;
     static constexpr int kControl = kOpAt + (kQuant ? 2 * kOpBytes : 0);
-    static constexpr int kTotal = kControl + (kQuant ? 4096 : 1024);
+    static constexpr int kTotal = kControl + (kQuant ? 5120 : 1024);
     static constexpr int kCopyWarp = kQuant ? 8 : 4, kMatrixWarp = kCopyWarp + 1, kScaleWarp = 10;
     static constexpr int kThreads = kQuant ? 384 : 192;
+    static constexpr int kJobCost = 2;  // of a job's begin and end, in tiles
     static_assert(kTotal <= 113 * 1024, "two CTAs an SM");
 };
 
@@ -209,11 +216,12 @@ struct TensorShape {
 struct alignas(16) Control {
     unsigned long long full[9], empty[9], stage_full[6], stage_empty[6], op_full[2], op_empty[2];
     unsigned long long s_full[2], p_ready[2], o_done[2], scales[2];
-    unsigned long long q_raw, q_full, q_empty, drain;
+    unsigned long long q_raw[2], q_full[2], q_empty[2], drain;
     unsigned tmem;
     unsigned nonfinite[4];  // window tokens whose values were zeroed, by segment
     int abort;
-    int start_r, start_head, start_row_tile, start_tile;  // this CTA's first tile
+    int start_r, start_head, start_row_tile, start_unit;  // where this CTA begins
+    int start_row0, start_len, start_P, start_tiles, start_row_tiles;
     long long scan[40];
 };
 // What the scales of a tile's tokens become (E4M3), for every other tile.
@@ -224,34 +232,38 @@ struct TileScales {
     float v[2][kTile];       // v_scale itself
     int odd[2];              // whether a v_scale is negative, NaN or infinite
     int pad[2];
-    float q[2][kRowsPerTile];  // what the queries were divided by, for every other segment
+    float q[4][kRowsPerTile];  // what the queries were divided by, by segment
 };
-static_assert(sizeof(Control) <= 1024 && sizeof(Control) + sizeof(TileScales) <= 4096, "control area");
+static_assert(sizeof(Control) <= 1024 && sizeof(Control) + sizeof(TileScales) <= 5120, "control area");
 
 // A request's jobs: every (kv head, 128 rows) pair reads all its tiles.
 struct Request {
     int row0, len, P, tiles, row_tiles;
 };
 
-__device__ __forceinline__ bool load_request(const TensorArgs &t, int r, Request *q, bool report) {
-    if (!window_of(t.a, r, &q->row0, &q->len, &q->P, report)) return false;
+__device__ __forceinline__ bool to_request(const TensorArgs &t, const Window &w, Request *q, bool report) {
+    if (!usable(t.a, w, report)) return false;
+    q->row0 = w.lo;
+    q->len = w.hi - w.lo;
+    q->P = w.P;
     q->tiles = (q->P + q->len + kTile - 1) / kTile;
     q->row_tiles = (q->len + t.tokens - 1) / t.tokens;
     return true;
 }
 
-// T tiles dealt to n CTAs in order: each gets each = T / n and the first of every
-// n / (T % n) one more.
+// T units dealt to n CTAs in order, each T / n of them or one more.  A job counts
+// its tiles and, before them, some units for its beginning and end, so that CTAs
+// with many short jobs get fewer tiles.
 struct Deal {
     int n, rest;
     long long each;
     __device__ __forceinline__ long long first(int c) const { return c * each + c * rest / n; }
-    // the CTA, c or later, that a tile falls to
-    __device__ __forceinline__ int cta_of(long long tile, int c) const {
+    // the CTA, c or later, that a unit falls to
+    __device__ __forceinline__ int cta_of(long long unit, int c) const {
         int hi = n - 1;
         while (c < hi) {
             const int mid = (c + hi + 1) >> 1;
-            if (first(mid) <= tile) c = mid;
+            if (first(mid) <= unit) c = mid;
             else hi = mid - 1;
         }
         return c;
@@ -260,46 +272,55 @@ struct Deal {
 
 // Consecutive tiles of one job that a CTA works through.
 struct Segment {
-    Request q;
+    Request q = {};
     int r, head, row_tile, first, count;
 };
 
-// Walks a CTA's tiles job by job: requests in order, in each the kv heads, in
+// Walks a CTA's units job by job: requests in order, in each the kv heads, in
 // each the row tiles (which read the same keys and values, so the later ones
-// find them in L2).  Every warp role walks on its own and sees the same.
+// find them in L2).  Every warp role walks on its own and sees the same; the
+// next request is loaded while the present one is worked on.
+template <int kJobCost>
 struct Walk {
-    int left, r, head, row_tile, tile;
-    Request q;
+    int left, r, head, row_tile, unit;
+    Request q = {};
+    Window ahead;
 
     __device__ __forceinline__ void begin(const TensorArgs &t, const Control &ctl, int n) {
         left = n;
         r = ctl.start_r;
         head = ctl.start_head;
         row_tile = ctl.start_row_tile;
-        tile = ctl.start_tile;
-        q.row_tiles = 0;  // not loaded yet
+        unit = ctl.start_unit;
+        q = {ctl.start_row0, ctl.start_len, ctl.start_P, ctl.start_tiles, ctl.start_row_tiles};
+        ahead = load_window(t.a, min(r + 1, t.a.B - 1));
     }
     __device__ __forceinline__ bool next(const TensorArgs &t, Segment *s) {
-        if (left <= 0) return false;
-        if (q.row_tiles == 0)
-            while (!load_request(t, r, &q, false)) ++r;
-        s->q = q;
-        s->r = r;
-        s->head = head;
-        s->row_tile = row_tile;
-        s->first = tile;
-        s->count = min(q.tiles - tile, left);
-        left -= s->count;
-        tile = 0;
-        if (++row_tile == q.row_tiles) {
-            row_tile = 0;
-            if (++head == t.a.cache.n_kv_heads) {
-                head = 0;
-                ++r;
-                q.row_tiles = 0;
+        while (left > 0) {
+            const int take = min(q.tiles + kJobCost - unit, left);
+            s->q = q;
+            s->r = r;
+            s->head = head;
+            s->row_tile = row_tile;
+            s->first = max(unit - kJobCost, 0);
+            s->count = max(unit + take - kJobCost, 0) - s->first;
+            left -= take;
+            unit = 0;
+            if (++row_tile == q.row_tiles) {
+                row_tile = 0;
+                if (++head == t.a.cache.n_kv_heads) {
+                    head = 0;
+                    while (left > 0) {
+                        const bool has = to_request(t, ahead, &q, false);
+                        ++r;
+                        ahead = load_window(t.a, min(r + 1, t.a.B - 1));
+                        if (has) break;
+                    }
+                }
             }
+            if (s->count > 0) return true;
         }
-        return true;
+        return false;
     }
 };
 
@@ -355,7 +376,8 @@ template <int D, bool kQuant>
 __global__ void __launch_bounds__(TensorShape<D, kQuant>::kThreads, 2)
 attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v,
-                     const __grid_constant__ CUtensorMap map_q, const TensorArgs t) {
+                     const __grid_constant__ CUtensorMap map_q,
+                     const __grid_constant__ CUtensorMap map_few, const TensorArgs t) {
     using S = TensorShape<D, kQuant>;
     constexpr int kThreads = S::kThreads;
     constexpr int kHalves = D / 64;       // 128-byte column blocks of a row
@@ -369,46 +391,6 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     const uint32_t base = smem_addr(smem);
     const uint32_t ring = base + S::kQBytes;
 
-    pdl_wait();
-    pdl_trigger();
-
-    // this CTA's share of all tiles: each thread sums a run of requests, a scan
-    // over the threads finds the request that holds the first of its tiles
-    const int per = (a.B + kThreads - 1) / kThreads;
-    long long mine = 0;
-    for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r) {
-        Request q;
-        if (load_request(t, r, &q, blockIdx.x == 0))
-            mine += (long long)q.tiles * q.row_tiles * a.cache.n_kv_heads;
-    }
-    long long T;
-    const long long before = block_exclusive_scan<long long>(mine, ctl.scan, &T);
-    const int n_ctas = (int)min((long long)gridDim.x, T);
-    const int cta = blockIdx.x;
-    if (tid == 0) t.desc[cta * kDescInts] = 0;
-    if (cta >= n_ctas) return;
-    Deal deal;
-    deal.n = n_ctas;
-    deal.each = T / n_ctas;
-    deal.rest = (int)(T - deal.each * n_ctas);
-    const long long lo = deal.first(cta), hi = deal.first(cta + 1);
-    if (lo >= before && lo < before + mine) {
-        long long at = before;
-        for (int r = tid * per;; ++r) {
-            Request q;
-            if (!load_request(t, r, &q, false)) continue;
-            const long long n = (long long)q.tiles * q.row_tiles * a.cache.n_kv_heads;
-            if (lo < at + n) {
-                const long long job = (lo - at) / q.tiles;
-                ctl.start_r = r;
-                ctl.start_tile = (int)(lo - at - job * q.tiles);
-                ctl.start_head = (int)job / q.row_tiles;
-                ctl.start_row_tile = (int)job % q.row_tiles;
-                break;
-            }
-            at += n;
-        }
-    }
     if (tid == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(smem_addr(&ctl.full[i]), 1);
@@ -425,26 +407,87 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             mbar_init(smem_addr(&ctl.scales[i]), 1);
             mbar_init(smem_addr(&ctl.op_full[i]), 4);
             mbar_init(smem_addr(&ctl.op_empty[i]), 1);
+            mbar_init(smem_addr(&ctl.q_raw[i]), 1);
+            mbar_init(smem_addr(&ctl.q_full[i]), 4);
+            mbar_init(smem_addr(&ctl.q_empty[i]), 1);
         }
-        mbar_init(smem_addr(&ctl.q_raw), 1);
-        mbar_init(smem_addr(&ctl.q_full), 4);
-        mbar_init(smem_addr(&ctl.q_empty), 1);
         mbar_init(smem_addr(&ctl.drain), 1);
         ctl.abort = 0;
         for (int i = 0; i < 4; ++i) ctl.nonfinite[i] = 0;
         fence_mbar_init();
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+        prefetch_map(&map_q);
+        prefetch_map(&map_few);
     }
     if (warp == S::kMatrixWarp) tmem_alloc(smem_addr(&ctl.tmem), kTmemCols);
+    pdl_wait();
+    pdl_trigger();
+
+    // this CTA's share of all units: each thread sums a run of requests, a scan
+    // over the threads finds the request that holds the first of its units
+    const int per = (a.B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    Request q = {};
+    auto units = [&]() { return (long long)(q.tiles + S::kJobCost) * q.row_tiles * a.cache.n_kv_heads; };
+    for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
+        if (to_request(t, load_window(a, r), &q, blockIdx.x == 0)) mine += units();
+    long long T;
+    const long long before = block_exclusive_scan<long long>(mine, ctl.scan, &T);
+    const int n_ctas = (int)min((long long)gridDim.x, (T + S::kJobCost + 1) / (S::kJobCost + 2));
+    const int cta = blockIdx.x;
+    if (tid == 0) t.desc[cta * kDescInts] = 0;
+    if (cta >= n_ctas) {
+        if (warp == S::kMatrixWarp) {
+            __syncwarp();
+            tmem_free(*(volatile unsigned *)&ctl.tmem, kTmemCols);
+        }
+        return;
+    }
+    Deal deal;
+    deal.n = n_ctas;
+    deal.each = T / n_ctas;
+    deal.rest = (int)(T - deal.each * n_ctas);
+    const long long lo = deal.first(cta), hi = deal.first(cta + 1);
+    if (lo >= before && lo < before + mine) {
+        long long at = before;
+        for (int r = tid * per;; ++r) {
+            // (with one request a thread it is the one just loaded)
+            if (per > 1 && !to_request(t, load_window(a, r), &q, false)) continue;
+            if (lo >= at + units()) {
+                at += units();
+                continue;
+            }
+            const int job = (int)((lo - at) / (q.tiles + S::kJobCost));
+            ctl.start_r = r;
+            ctl.start_unit = (int)(lo - at - (long long)job * (q.tiles + S::kJobCost));
+            ctl.start_head = job / q.row_tiles;
+            ctl.start_row_tile = job % q.row_tiles;
+            ctl.start_row0 = q.row0;
+            ctl.start_len = q.len;
+            ctl.start_P = q.P;
+            ctl.start_tiles = q.tiles;
+            ctl.start_row_tiles = q.row_tiles;
+            break;
+        }
+    }
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = ctl.tmem;
     volatile int *abort = &ctl.abort;
-    Walk walk;
+    Walk<S::kJobCost> walk;
     walk.begin(t, ctl, (int)(hi - lo));
     Segment s = {};
     Ring ring_at = {0, 0};
+    // The queries of a segment whose rows fit in 64 take one half of their buffer
+    // and the next such segment's the other, so that they are there in time.
+    auto few_rows = [&](const Segment &s) { return s.q.len - s.row_tile * t.tokens <= t.few; };
+    auto q_offset = [&](const Segment &s, unsigned seg) { return few_rows(s) ? (seg & 1) * 8192u : 0u; };
 
+    // Over E4M3 the softmax warps take registers from the copying and multiplying
+    // ones: of 80 a thread at launch in each of three warpgroups, 104, 80 and 56.
     if (warp >= S::kCopyWarp) {
+        if constexpr (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == S::kCopyWarp) {
             // -------------------------------------------- copy warp
             constexpr int kParts = kQuant ? 1 : kHalves;  // boxes side by side
@@ -453,7 +496,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             const uint32_t dst = ring + half * kHalfBytes + box * t.box * (kQuant ? D : 128);
             Ring stage_at = {0, 0};  // the values' ring, over E4M3
             unsigned seg = 0;
-            bool ok = true;
+            bool ok = true, few_before = false;
             auto wait = [&](unsigned long long *bar, unsigned parity) {
                 ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
                 return ok = __all_sync(kFullMask, ok);
@@ -497,13 +540,19 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     }
                     if (!ok) break;
                     if (i == 0) {
-                        // the queries, once the products with the last ones are done
-                        if (seg > 0 && !wait(&ctl.q_empty, seg - 1)) break;
-                        if (lane == 0) mbar_expect(smem_addr(&ctl.q_raw), t.group * t.tokens * D * 2);
+                        // the queries, once the products with the ones there before
+                        // are done: the last segment's, or the ones before those
+                        const bool few = few_rows(s);
+                        if (seg > 1 && !wait(&ctl.q_empty[seg & 1], (seg - 2) >> 1)) break;
+                        if (seg > 0 && !(few && few_before) && !wait(&ctl.q_empty[(seg - 1) & 1], (seg - 1) >> 1))
+                            break;
+                        const uint32_t bar = smem_addr(&ctl.q_raw[seg & 1]);
+                        if (lane == 0) mbar_expect(bar, t.group * (few ? t.few : t.tokens) * D * 2);
                         __syncwarp();
                         if (lane < kHalves)
-                            tma_load_4d(base + lane * kRowsPerTile * 128, &map_q, lane * 64, 0, s.head,
-                                        s.q.row0 + s.row_tile * t.tokens, smem_addr(&ctl.q_raw));
+                            tma_load_4d(base + lane * kRowsPerTile * 128 + q_offset(s, seg), few ? &map_few : &map_q,
+                                        lane * 64, 0, s.head, s.q.row0 + s.row_tile * t.tokens, bar);
+                        few_before = few;
                         ++seg;
                     }
                     page = page1;
@@ -519,7 +568,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 for (int i = 0; i < S::kStages; ++i)
                     mbar_wait(smem_addr(&ctl.stage_full[i]),
                               i < (int)stage_at.slot ? stage_at.parity : stage_at.parity ^ 1);
-                if (seg > 0) mbar_wait(smem_addr(&ctl.q_raw), (seg - 1) & 1);
+                for (unsigned i = seg > 2 ? seg - 2 : 0; i < seg; ++i)
+                    mbar_wait(smem_addr(&ctl.q_raw[i & 1]), i >> 1 & 1);
             }
         } else if (warp == S::kMatrixWarp) {
             // ------------------------------------------ matrix warp
@@ -534,7 +584,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             const uint64_t desc_q = smem_operand(ubase, 16, kKeyRow);
             const uint64_t desc_k = smem_operand(ubase + S::kQBytes, 16, kKeyRow);
             const uint64_t desc_v = smem_operand(ubase + (kQuant ? S::kOpAt : S::kQBytes), kHalfBytes, 128);
-            unsigned long long *queries = kQuant ? &ctl.q_full : &ctl.q_raw;
+            unsigned long long *queries = kQuant ? ctl.q_full : ctl.q_raw;
             const bool leader = elect_one();
             unsigned done = 0, seg = 0;  // tiles and segments so far
             bool ok = true;
@@ -543,13 +593,17 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 return ok = __all_sync(kFullMask, ok);
             };
             while (ok && walk.next(t, &s)) {
-                if (!wait(queries, seg)) break;
+                if (!wait(queries + (seg & 1), seg >> 1)) break;
+                const bool few = few_rows(s);
+                const uint64_t queries_at = desc_q + (q_offset(s, seg) >> 4);
+                // their second parts, over E4M3
+                const unsigned part = (D == 64 && few ? 4096 : S::kQBytes / 2) >> 4;
                 const int count = __shfl_sync(kFullMask, s.count, 0);
                 for (int i = 0; i <= count && ok; ++i) {
                     if (i < count) {
                         // scores of tile i, in the place of the weights of tile i - 2
                         const unsigned tile = done + i;
-                        if (i > 1 && !wait(&ctl.o_done[tile & 1], (tile - 2) >> 1)) break;
+                        if (tile > 1 && !wait(&ctl.o_done[tile & 1], (tile - 2) >> 1)) break;
                         if (!wait(&ctl.full[ring_at.slot], ring_at.parity)) break;
                         tmem_fence_after();
                         const uint64_t buf = desc_k + ring_at.slot * (S::kBufBytes >> 4);
@@ -558,17 +612,17 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             if constexpr (kQuant) {
 #pragma unroll
                                 for (int k = 0; k < D / 16; ++k)  // 32 codes a step, for either part
-                                    mma_ss_e4m3(d, desc_q + (k % 2 * (S::kQBytes / 2) + k / 2 * 32 >> 4),
+                                    mma_ss_e4m3(d, queries_at + k % 2 * part + (k / 2 * 32 >> 4),
                                                 buf + (k / 2 * 32 >> 4), word_qk, k > 0);
                             } else {
 #pragma unroll
                                 for (int k = 0; k < D / 16; ++k)
-                                    mma_ss(d, desc_q + ((k / 4 * kRowsPerTile * 128 + k % 4 * 32) >> 4),
+                                    mma_ss(d, queries_at + ((k / 4 * kRowsPerTile * 128 + k % 4 * 32) >> 4),
                                            buf + ((k / 4 * kHalfBytes + k % 4 * 32) >> 4), word_qk, k > 0);
                             }
                             mma_commit(smem_addr(&ctl.s_full[tile & 1]));
                             mma_commit(smem_addr(&ctl.empty[ring_at.slot]));
-                            if (i + 1 == count) mma_commit(smem_addr(&ctl.q_empty));
+                            if (i + 1 == count) mma_commit(smem_addr(&ctl.q_empty[seg & 1]));
                         }
                         __syncwarp();
                         ring_at.step(S::kBufs);
@@ -718,13 +772,16 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 // (split_pair): each part a K-major operand of its own, in the place
                 // of the bfloat16 rows.  A power of two brings a row's largest element
                 // to 128..256; a row with a NaN or an infinity gets NaN scores.
-                wait(&ctl.q_raw, seg);
+                wait(&ctl.q_raw[seg & 1], seg >> 1);
+                const bool few = few_rows(s), mine = ct < (few ? 64 : 128);
+                unsigned char *rows = smem + q_offset(s, seg);
+                unsigned char *second = rows + (D == 64 && few ? 4096 : S::kQBytes / 2);
                 unsigned most = 0;
-                if (ok) {
+                if (mine) {
 #pragma unroll 4
                     for (int j = 0; j < D / 8; ++j) {
                         const uint4 v = *reinterpret_cast<const uint4 *>(
-                            smem + j / 8 * kRowsPerTile * 128 + swizzled<128>(ct, j % 8));
+                            rows + j / 8 * kRowsPerTile * 128 + swizzled<128>(ct, j % 8));
                         const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) most = max(most, max(w[k] & 0x7FFFu, w[k] >> 16 & 0x7FFFu));
@@ -732,17 +789,20 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 }
                 const int exponent = min(max((int)(most >> 7), 8), 254) - 134;
                 const float by = __int_as_float((127 - exponent) << 23);
-                sc.q[seg & 1][ct] =
+                sc.q[seg & 3][ct] =
                     most >= 0x7F80u ? __int_as_float(0x7FC00000) : __int_as_float((exponent + 127) << 23);
                 uint4 kept[4];  // the low parts of the first 64 elements: their place is not free yet
 #pragma unroll 1
                 for (int h = 0; h < kHalves; ++h) {
                     uint4 v[8];
+                    if (mine) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] = *reinterpret_cast<const uint4 *>(smem + h * kRowsPerTile * 128 +
-                                                                swizzled<128>(ct, j));
+                        for (int j = 0; j < 8; ++j)
+                            v[j] = *reinterpret_cast<const uint4 *>(rows + h * kRowsPerTile * 128 +
+                                                                    swizzled<128>(ct, j));
+                    }
                     if (D == 64) named_sync(2, 128);  // shorter rows: in the place of other threads' ones
+                    if (!mine) continue;
                     uint4 low[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -759,7 +819,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             hi[k] = h0 | h1 << 16;
                             lo[k] = l0 | l1 << 16;
                         }
-                        *reinterpret_cast<uint4 *>(smem + swizzled<D>(ct, 4 * h + j)) =
+                        *reinterpret_cast<uint4 *>(rows + swizzled<D>(ct, 4 * h + j)) =
                             make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         low[j] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
@@ -770,14 +830,13 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        unsigned char *part = smem + S::kQBytes / 2;
-                        if (kHalves == 2) *reinterpret_cast<uint4 *>(part + swizzled<D>(ct, j)) = kept[j];
-                        *reinterpret_cast<uint4 *>(part + swizzled<D>(ct, 4 * h + j)) = low[j];
+                        if (kHalves == 2) *reinterpret_cast<uint4 *>(second + swizzled<D>(ct, j)) = kept[j];
+                        *reinterpret_cast<uint4 *>(second + swizzled<D>(ct, 4 * h + j)) = low[j];
                     }
                 }
                 fence_async_proxy();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
+                if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full[seg & 1]));
                 for (int i = 0; i < s.count; ++i) {
                     const unsigned tile = done + i, b = tile & 1, stage = ring_at.slot;
                     if (!wait(&ctl.scales[b], tile >> 1)) break;
@@ -851,6 +910,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         }
     } else {
         // --------------------------------------------- softmax warps
+        if constexpr (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int m = tid;  // row of the tile, lane of tensor memory
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
@@ -893,37 +953,63 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         sees = w << pre | ((1ull << pre) - 1);
                     }
                     const bool all = __all_sync(kFullMask, sees == ~0ull);
-                    float top;
-                    uint32_t x[kQuant ? 16 : kTile];
+                    // The maximum moves only when it grows by 2^kLazy: until then the
+                    // weights may pass 1, and sum and output stay as they are.
+                    auto raise = [&](float top, bool grow) {
+                        const float f = grow ? exp2_approx(mx - top) : 1.0f;
+                        if (grow) mx = top;
+                        l *= f;
+                        if (i > 0) {
+                            if (!wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) return f;
+                            tmem_fence_after();
+#pragma unroll 1
+                            for (int h = 0; h < D / 16; ++h) {
+                                uint32_t o[16];
+                                tmem_load16(lanes + 2 * kTile + h * 16, o);
+                                tmem_wait_load16(o);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_store16(lanes + 2 * kTile + h * 16, o);
+                            }
+                        }
+                        return f;
+                    };
+                    auto grows = [&](float top) {
+                        return top > mx + kLazy || (mx == -INFINITY && top > mx);
+                    };
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     if constexpr (kQuant) {
-                        if (i == 0) factor = sc.q[seg & 1][m];
-                        top = -INFINITY;
-                        // Scores to base 2, plus log2 of the value's scale, in the
-                        // scores' place.  Sixteen columns a step of a loop, here and
-                        // below: the warps of a scheduler run four kinds of code in
-                        // turn, which unrolled is more than its instruction cache.
+                        // Sixteen columns a step of a loop that is not unrolled: the
+                        // warps of a scheduler run four kinds of code in turn, which
+                        // unrolled is more than its instruction cache.
+                        if (i == 0) factor = sc.q[seg & 3][m];
+                        const float2 ff = make_float2(factor, factor);
 #pragma unroll 1
                         for (int j = 0; j < kTile; j += 16) {
-                            float4 ks[4], vs[4];
+                            uint32_t x[16];
+                            float4 f1[4], f2[4];
                             tmem_load16(at + j, x);
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                ks[k] = load_shared4(smem_addr(&sc.k[b][j + 4 * k]));
-                                vs[k] = load_shared4(smem_addr(&sc.v_log2[b][j + 4 * k]));
+                                f1[k] = load_shared4(smem_addr(&sc.k[b][j + 4 * k]));
+                                f2[k] = load_shared4(smem_addr(&sc.v_log2[b][j + 4 * k]));
                             }
                             tmem_wait_load16(x);
-                            const float2 ff = make_float2(factor, factor);
-                            const unsigned sixteen = (unsigned)(sees >> j);
+                            // scores to base 2, plus log2 of the value's scale
 #pragma unroll
                             for (int k = 0; k < 16; k += 2) {
-                                const float4 kk = ks[k / 4], vv = vs[k / 4];
+                                const float4 kk = f1[k / 4], vv = f2[k / 4];
                                 const float2 y = fma2(mul2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ff),
                                                       k & 2 ? make_float2(kk.z, kk.w) : make_float2(kk.x, kk.y),
                                                       k & 2 ? make_float2(vv.z, vv.w) : make_float2(vv.x, vv.y));
                                 x[k] = __float_as_uint(y.x);
                                 x[k + 1] = __float_as_uint(y.y);
                             }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) f1[k] = load_shared4(smem_addr(&sc.v_inv[b][j + 4 * k]));
                             if (!all) {
+                                const unsigned sixteen = (unsigned)(sees >> j);
 #pragma unroll
                                 for (int k = 0; k < 16; ++k)
                                     if (!(sixteen >> k & 1)) x[k] = 0xFF800000u;
@@ -932,11 +1018,49 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
                             for (int k = 2; k < 16; ++k)
                                 tops[k & 1] = fmaxf(tops[k & 1], __uint_as_float(x[k]));
-                            top = fmaxf(top, fmaxf(tops[0], tops[1]));
-                            tmem_store16(at + j, x);
+                            const float top = fmaxf(tops[0], tops[1]);
+                            const bool grow = grows(top);
+                            if (__any_sync(kFullMask, grow)) {
+                                const float f = raise(top, grow);
+                                sum[0] = mul2(sum[0], make_float2(f, f));
+                                sum[1] = mul2(sum[1], make_float2(f, f));
+                                if (j > 0) {  // this tile's weights so far
+                                    tmem_wait_store();
+#pragma unroll 1
+                                    for (int h = 0; h < j / 2; h += 8) {
+                                        uint32_t o[8];
+                                        tmem_load8(at + h, o);
+                                        tmem_wait_load8(o);
+#pragma unroll
+                                        for (int k = 0; k < 8; ++k) {
+                                            const float2 u = __half22float2(*reinterpret_cast<__half2 *>(&o[k]));
+                                            const __half2 two = __floats2half2_rn(u.x * f, u.y * f);
+                                            o[k] = *reinterpret_cast<const uint32_t *>(&two);
+                                        }
+                                        tmem_store8(at + h, o);
+                                    }
+                                }
+                            }
+                            const float shift = mx == -INFINITY ? 0.0f : mx;
+                            const float2 minus = make_float2(-shift, -shift);
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) {
+                                const float2 y =
+                                    add2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), minus);
+                                const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                                const float4 inv = f1[k / 4];
+                                sum[k / 2 & 1] = fma2(u, k & 2 ? make_float2(inv.z, inv.w) : make_float2(inv.x, inv.y),
+                                                      sum[k / 2 & 1]);
+                                const __half2 two = __floats2half2_rn(u.x, u.y);
+                                w[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                            }
+                            // over scores that have been read (columns up to j)
+                            tmem_store8(at + j / 2, w);
                         }
-                        tmem_wait_store();
+                        if (!ok) break;
                     } else {
+                        uint32_t x[kTile], w[kTile / 2];
                         tmem_load32(at, x);
                         tmem_load32(at + 32, x + 32);
                         tmem_wait_load(x);
@@ -956,59 +1080,14 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
                         for (int j = 4; j < kTile; ++j)
                             tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
-                        top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * c;
-                    }
-                    // The maximum moves only when it grows by 2^kLazy: until then
-                    // the weights may pass 1, and the output stays as it is.
-                    const bool grow = top > mx + kLazy || (mx == -INFINITY && top > mx);
-                    if (__any_sync(kFullMask, grow)) {
-                        const float f = grow ? exp2_approx(mx - top) : 1.0f;
-                        if (grow) mx = top;
-                        l *= f;
-                        if (i > 0) {
-                            if (!wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) break;
-                            tmem_fence_after();
-#pragma unroll 1
-                            for (int h = 0; h < D / 16; ++h) {
-                                uint32_t o[16];
-                                tmem_load16(lanes + 2 * kTile + h * 16, o);
-                                tmem_wait_load16(o);
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_store16(lanes + 2 * kTile + h * 16, o);
-                            }
+                        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * c;
+                        const bool grow = grows(top);
+                        if (__any_sync(kFullMask, grow)) {
+                            raise(top, grow);
+                            if (!ok) break;
                         }
-                    }
-                    const float shift = mx == -INFINITY ? 0.0f : mx;
-                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    const float2 minus = make_float2(-shift, -shift);
-                    if constexpr (kQuant) {
-#pragma unroll 1
-                        for (int j = 0; j < kTile; j += 16) {
-                            float4 inv[4];
-                            uint32_t w[8];
-                            tmem_load16(at + j, x);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) inv[k] = load_shared4(smem_addr(&sc.v_inv[b][j + 4 * k]));
-                            tmem_wait_load16(x);
-#pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                const float2 y =
-                                    add2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), minus);
-                                const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                                const float4 f = inv[k / 4];
-                                sum[k / 2 & 1] = fma2(u, k & 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y),
-                                                      sum[k / 2 & 1]);
-                                const __half2 two = __floats2half2_rn(u.x, u.y);
-                                w[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
-                            }
-                            // over scores that have been read (columns j / 2 <= j)
-                            tmem_store8(at + j / 2, w);
-                        }
-                    } else {
-                        const float2 cc = make_float2(c, c);
-                        uint32_t w[kTile / 2];
+                        const float shift = mx == -INFINITY ? 0.0f : mx;
+                        const float2 cc = make_float2(c, c), minus = make_float2(-shift, -shift);
 #pragma unroll
                         for (int j = 0; j < kTile; j += 2) {
                             const float2 y = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
@@ -1143,9 +1222,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             if (tid == 0 && walk.left <= 0) {
                 int *d = t.desc + cta * kDescInts;
                 if (s.first == 0 && !whole) {
-                    // its first tile's number is the CTA's last tile's, less the ones before it
-                    const long long g0 = hi - s.count;
-                    d[1] = deal.cta_of(g0 + s.q.tiles - 1, cta);
+                    // (its last tile comes q.tiles - count units after the CTA's last)
+                    d[1] = deal.cta_of(hi - 1 + s.q.tiles - s.count, cta);
                     d[2] = slot;
                     d[3] = s.q.row0;
                     d[4] = s.head;
@@ -1160,10 +1238,11 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     if (warp == S::kMatrixWarp) tmem_free(tmem, kTmemCols);
 }
 
-// Joins the parts of the jobs that several CTAs share, in the CTAs' order: a
-// block a job (the CTA it begins in) and 32 columns, a lane a row, the warps
-// every eighth part.
-constexpr int kJoinWarps = 8;
+// Joins the parts of the jobs that several CTAs share, in the CTAs' order: a block
+// a job (the CTA it begins in), 32 rows (a lane each) and 32 columns (four a warp).
+// Up to kFewParts a warp adds the parts of its columns one after the other, all
+// their loads in flight; more of them are dealt to the warps, each all columns.
+constexpr int kJoinWarps = 8, kFewParts = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const TensorArgs t) {
@@ -1171,42 +1250,63 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Tens
     __shared__ float part_l[kJoinWarps][32];
     pdl_wait();
     pdl_trigger();
-    const int *d = t.desc + blockIdx.x * kDescInts;
-    if (__ldcg(d) == 0) return;
-    const int c0 = blockIdx.x, c1 = __ldcg(d + 1), slot0 = __ldcg(d + 2), row0 = __ldcg(d + 3);
-    const int kv_head = __ldcg(d + 4), token0 = __ldcg(d + 5), rows = __ldcg(d + 6);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int base = 0; base < rows; base += 32) {
-        const int m = base + lane;
-        auto ml = [&](int c, int which) {
-            const long long slot = c == c0 ? slot0 : 2 * c;
-            return __ldcg(t.part_ml + (slot * 2 + which) * kRowsPerTile + m);
-        };
-        float top = -INFINITY;
+    const int4 d0 = __ldcg(reinterpret_cast<const int4 *>(t.desc) + blockIdx.x * 2);
+    const int4 d1 = __ldcg(reinterpret_cast<const int4 *>(t.desc) + blockIdx.x * 2 + 1);
+    const int base = (blockIdx.y & 3) * 32, columns = blockIdx.y / 4 * 32;
+    const int c0 = blockIdx.x, c1 = d0.y, kv_head = d1.x, token0 = d1.y, rows = d1.z;
+    if (!d0.x || base >= rows) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, m = base + lane;
+    auto slot = [&](int c) { return (long long)(c == c0 ? d0.z : 2 * c); };
+    auto ml = [&](int c, int which) {
+        return __ldcg(t.part_ml + (slot(c) * 2 + which) * kRowsPerTile + m);
+    };
+    auto from = [&](int c) {
+        return reinterpret_cast<const float4 *>(t.part_o) + (slot(c) * (D / 4) + columns / 4) * kRowsPerTile + m;
+    };
+    float top = -INFINITY, l = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c1 - c0 < kFewParts) {
+        float pm[kFewParts], pl[kFewParts];
+        float4 po[kFewParts];
+#pragma unroll
+        for (int i = 0; i < kFewParts; ++i) {
+            const bool in = c0 + i <= c1;
+            pm[i] = in ? ml(c0 + i, 0) : -INFINITY;
+            pl[i] = in ? ml(c0 + i, 1) : 0.0f;
+            po[i] = in ? __ldcg(from(c0 + i) + warp * kRowsPerTile) : x;
+        }
+#pragma unroll
+        for (int i = 0; i < kFewParts; ++i) top = fmaxf(top, pm[i]);
+        const float shift = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int i = 0; i < kFewParts; ++i) {
+            if (c0 + i > c1) continue;
+            const float f = exp2_approx(pm[i] - shift);
+            l += f * pl[i];
+            x.x += f * po[i].x, x.y += f * po[i].y, x.z += f * po[i].z, x.w += f * po[i].w;
+        }
+    } else {
+#pragma unroll 8
         for (int c = c0; c <= c1; ++c) top = fmaxf(top, ml(c, 0));
         const float shift = top == -INFINITY ? 0.0f : top;
-        float l = 0.0f;
         float4 o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int j = 0; j < 8; ++j) o[j] = x;
+#pragma unroll 2
         for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
             const float f = exp2_approx(ml(c, 0) - shift);
             l += f * ml(c, 1);
-            const long long slot = c == c0 ? slot0 : 2 * c;
-            const float4 *p = reinterpret_cast<const float4 *>(t.part_o) +
-                              (slot * (D / 4) + blockIdx.y * 8) * kRowsPerTile + m;
+            const float4 *p = from(c);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float4 x = __ldcg(p + j * kRowsPerTile);
-                o[j].x += f * x.x, o[j].y += f * x.y, o[j].z += f * x.z, o[j].w += f * x.w;
+                const float4 y = __ldcg(p + j * kRowsPerTile);
+                o[j].x += f * y.x, o[j].y += f * y.y, o[j].z += f * y.z, o[j].w += f * y.w;
             }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) part[warp][j][lane] = o[j];
         part_l[warp][lane] = l;
         __syncthreads();
-        // warp j joins columns 4j..4j+3
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         l = 0.0f;
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) {
@@ -1214,20 +1314,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Tens
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
             l += part_l[w][lane];
         }
-        __syncthreads();
-        if (m >= rows) continue;
-        const int head = kv_head * t.group + m % t.group;
-        const long long packed = row0 + token0 + m / t.group;
-        const float inv = 1.0f / l;
-        if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-        const __nv_bfloat162 u = __floats2bfloat162_rn(x.x, x.y), v = __floats2bfloat162_rn(x.z, x.w);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
-                                   (long long)head * D + blockIdx.y * 32 + warp * 4) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
-        if (t.a.lse && blockIdx.y == 0 && warp == 0)
-            t.a.lse[packed * t.a.n_q_heads + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
     }
+    if (m >= rows) return;
+    const int head = kv_head * t.group + m % t.group;
+    const long long packed = d0.w + token0 + m / t.group;
+    const float inv = 1.0f / l, shift = top == -INFINITY ? 0.0f : top;
+    if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+    const __nv_bfloat162 u = __floats2bfloat162_rn(x.x, x.y), v = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
+                               (long long)head * D + columns + warp * 4) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
+    if (t.a.lse && columns == 0 && warp == 0)
+        t.a.lse[packed * t.a.n_q_heads + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
 }
 
 namespace {
@@ -1305,6 +1404,7 @@ cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *w
     t.a = a;
     t.group = a.n_q_heads / c.n_kv_heads;
     t.tokens = min(kRowsPerTile / t.group, DSPARK_MAX_WINDOW);
+    t.few = min(kRowsPerTile / 2 / t.group, DSPARK_MAX_WINDOW);
     t.box = gcd(c.page_size, kTile);
     unsigned char *w = static_cast<unsigned char *>(workspace);
     t.part_o = reinterpret_cast<float *>(w);
@@ -1317,19 +1417,20 @@ cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *w
     const int64_t q_dims[4] = {D, t.group, c.n_kv_heads, a.max_rows};
     const int64_t q_strides[3] = {D, (int64_t)t.group * D, a.ld_q};
     const int e_bytes = kv_elem_bytes(c.dtype), width = kQuant ? D : 64;
-    CUtensorMap map_k, map_v, map_q;
+    CUtensorMap map_k, map_v, map_q, map_few;
     if (!encode(&map_k, c.k, e_bytes, width, true, dims, strides, t.box, 1) ||
         !encode(&map_v, c.v, e_bytes, width, !kQuant, dims, strides, t.box, 1) ||
-        !encode(&map_q, a.q, 2, 64, true, q_dims, q_strides, t.group, t.tokens))
+        !encode(&map_q, a.q, 2, 64, true, q_dims, q_strides, t.group, t.tokens) ||
+        !encode(&map_few, a.q, 2, 64, true, q_dims, q_strides, t.group, max(t.few, 1)))
         return cudaErrorUnknown;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_tensor_kernel<D, kQuant>),
                                 S::kTotal, kSmemSlot);
     if (e != cudaSuccess) return e;
     const int grid = min(2 * sm_count(), kMaxCtas);
     e = launch_pdl(attend_tensor_kernel<D, kQuant>, dim3(grid), dim3(S::kThreads), S::kTotal, stream,
-                   map_k, map_v, map_q, t);
+                   map_k, map_v, map_q, map_few, t);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32), dim3(kJoinWarps * 32), 0, stream, t);
+    return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32 * 4), dim3(kJoinWarps * 32), 0, stream, t);
 }
 
 }  // namespace
