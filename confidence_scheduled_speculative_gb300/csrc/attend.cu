@@ -980,45 +980,55 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     };
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                     if constexpr (kQuant) {
-                        // Sixteen columns a step of a loop that is not unrolled: the
+                        // Half of the columns a step of a loop that is not unrolled: the
                         // warps of a scheduler run four kinds of code in turn, which
-                        // unrolled is more than its instruction cache.
+                        // unrolled is more than its instruction cache; fewer columns a
+                        // step leave the latencies of its loads one after the other.
+                        constexpr int kStep = 32;
                         if (i == 0) factor = sc.q[seg & 3][m];
                         const float2 ff = make_float2(factor, factor);
 #pragma unroll 1
-                        for (int j = 0; j < kTile; j += 16) {
-                            uint32_t x[16];
+                        for (int j = 0; j < kTile; j += kStep) {
+                            uint32_t x[kStep];
+                            tmem_load32(at + j, x);
                             float4 f1[4], f2[4];
-                            tmem_load16(at + j, x);
+                            auto scales = [&](int h) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                f1[k] = load_shared4(smem_addr(&sc.k[b][j + 4 * k]));
-                                f2[k] = load_shared4(smem_addr(&sc.v_log2[b][j + 4 * k]));
-                            }
-                            tmem_wait_load16(x);
+                                for (int k = 0; k < 4; ++k) {
+                                    f1[k] = load_shared4(smem_addr(&sc.k[b][j + h + 4 * k]));
+                                    f2[k] = load_shared4(smem_addr(&sc.v_log2[b][j + h + 4 * k]));
+                                }
+                            };
+                            scales(0);
+                            tmem_wait_load(x);
                             // scores to base 2, plus log2 of the value's scale
 #pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                const float4 kk = f1[k / 4], vv = f2[k / 4];
-                                const float2 y = fma2(mul2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), ff),
-                                                      k & 2 ? make_float2(kk.z, kk.w) : make_float2(kk.x, kk.y),
-                                                      k & 2 ? make_float2(vv.z, vv.w) : make_float2(vv.x, vv.y));
-                                x[k] = __float_as_uint(y.x);
-                                x[k + 1] = __float_as_uint(y.y);
-                            }
+                            for (int h = 0; h < kStep; h += 16) {
+                                if (h > 0) scales(h);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) f1[k] = load_shared4(smem_addr(&sc.v_inv[b][j + 4 * k]));
+                                for (int k = 0; k < 16; k += 2) {
+                                    uint32_t *y = x + h + k;
+                                    const float4 kk = f1[k / 4], vv = f2[k / 4];
+                                    const float2 z = fma2(mul2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), ff),
+                                                          k & 2 ? make_float2(kk.z, kk.w) : make_float2(kk.x, kk.y),
+                                                          k & 2 ? make_float2(vv.z, vv.w) : make_float2(vv.x, vv.y));
+                                    y[0] = __float_as_uint(z.x);
+                                    y[1] = __float_as_uint(z.y);
+                                }
+                            }
                             if (!all) {
-                                const unsigned sixteen = (unsigned)(sees >> j);
+                                const unsigned some = (unsigned)(sees >> j);
 #pragma unroll
-                                for (int k = 0; k < 16; ++k)
-                                    if (!(sixteen >> k & 1)) x[k] = 0xFF800000u;
+                                for (int k = 0; k < kStep; ++k)
+                                    if (!(some >> k & 1)) x[k] = 0xFF800000u;
                             }
-                            float tops[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+                            float tops[4];
 #pragma unroll
-                            for (int k = 2; k < 16; ++k)
-                                tops[k & 1] = fmaxf(tops[k & 1], __uint_as_float(x[k]));
-                            const float top = fmaxf(tops[0], tops[1]);
+                            for (int k = 0; k < 4; ++k) tops[k] = __uint_as_float(x[k]);
+#pragma unroll
+                            for (int k = 4; k < kStep; ++k)
+                                tops[k & 3] = fmaxf(tops[k & 3], __uint_as_float(x[k]));
+                            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                             const bool grow = grows(top);
                             if (__any_sync(kFullMask, grow)) {
                                 const float f = raise(top, grow);
@@ -1043,20 +1053,26 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             }
                             const float shift = mx == -INFINITY ? 0.0f : mx;
                             const float2 minus = make_float2(-shift, -shift);
-                            uint32_t w[8];
 #pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                const float2 y =
-                                    add2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), minus);
-                                const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                                const float4 inv = f1[k / 4];
-                                sum[k / 2 & 1] = fma2(u, k & 2 ? make_float2(inv.z, inv.w) : make_float2(inv.x, inv.y),
-                                                      sum[k / 2 & 1]);
-                                const __half2 two = __floats2half2_rn(u.x, u.y);
-                                w[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                            for (int h = 0; h < kStep; h += 16) {
+                                uint32_t w[8];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    f1[k] = load_shared4(smem_addr(&sc.v_inv[b][j + h + 4 * k]));
+#pragma unroll
+                                for (int k = 0; k < 16; k += 2) {
+                                    const uint32_t *z = x + h + k;
+                                    const float2 y = add2(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])), minus);
+                                    const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                                    const float4 inv = f1[k / 4];
+                                    sum[k / 2 & 1] = fma2(u, k & 2 ? make_float2(inv.z, inv.w) : make_float2(inv.x, inv.y),
+                                                          sum[k / 2 & 1]);
+                                    const __half2 two = __floats2half2_rn(u.x, u.y);
+                                    w[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                                }
+                                // over scores that have been read (columns up to j + h)
+                                tmem_store8(at + (j + h) / 2, w);
                             }
-                            // over scores that have been read (columns up to j)
-                            tmem_store8(at + j / 2, w);
                         }
                         if (!ok) break;
                     } else {
