@@ -484,8 +484,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     auto few_rows = [&](const Segment &s) { return s.q.len - s.row_tile * t.tokens <= t.few; };
     auto q_offset = [&](const Segment &s, unsigned seg) { return few_rows(s) ? (seg & 1) * 8192u : 0u; };
 
-    // Over E4M3 the softmax warps take registers from the copying and multiplying
-    // ones: of 80 a thread at launch in each of three warpgroups, 104, 80 and 56.
+    // Over E4M3 the softmax warps take registers from the others: of 80 a thread at
+    // launch in each of three warpgroups, 112, 72 and 56.
     if (warp >= S::kCopyWarp) {
         if constexpr (kQuant) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == S::kCopyWarp) {
@@ -738,6 +738,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     } else if (kQuant && warp >= 4) {
         // --------------------------------------------- converting warps
         if constexpr (kQuant) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
             // A value's code becomes a half of 2^-8 times its size by moving its bits:
             // both formats have the same digits of exponent below the sign up to the
             // bias (7 and 15), subnormals included.  Of a word's four codes the first
@@ -910,7 +911,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         }
     } else {
         // --------------------------------------------- softmax warps
-        if constexpr (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        if constexpr (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
         const int m = tid;  // row of the tile, lane of tensor memory
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
@@ -934,8 +935,23 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             const int head = s.head * t.group + mm % t.group, packed = s.q.row0 + token;
             const unsigned bits = ancestors_of(a, packed, token, s.q.len);
             if (tid == 0) ctl.nonfinite[(seg + 3) & 3] = 0;  // the segment's before
-            float factor = 1.0f;
-            float mx = -INFINITY, l = 0.0f;  // running maximum (times c) and sum
+
+            // The scores are taken as fragments: of the warp's rows a thread has
+            // four, 16 h + 8 k + lane / 4, and of each sixteen columns.  16 rows or
+            // fewer are one half's work, and few scales serve a thread.
+            float mx[2][2], l[2][2], factor[2][2];  // running maximum (to base 2), sum
+            unsigned seen[2][2];                    // ancestor bits
+            const int halves = rows - warp * 32 > 16 ? 2 : 1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int token_k = token0 + min(warp * 32 + 16 * h + 8 * k + lane / 4, rows - 1) / t.group;
+                    mx[h][k] = -INFINITY;
+                    l[h][k] = 0.0f;
+                    factor[h][k] = 1.0f;
+                    seen[h][k] = active ? ancestors_of(a, s.q.row0 + token_k, token_k, s.q.len) : 0;
+                }
             for (int i = 0; i < s.count; ++i) {
                 const unsigned tile = done + i, b = tile & 1;
                 const int p0 = (s.first + i) * kTile;
@@ -943,179 +959,125 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 if (active) {
                     if (kQuant && !wait(&ctl.scales[b], tile >> 1)) break;
                     tmem_fence_after();
-                    const uint32_t at = lanes + b * kTile;
-                    // what this row sees of the tile: prefix positions, then its
-                    // ancestors in the window
-                    unsigned long long sees = ~0ull;
-                    if (p0 + kTile > s.q.P) {
-                        const int pre = max(s.q.P - p0, 0), skip = max(p0 - s.q.P, 0);
-                        const unsigned long long w = skip < 32 ? (unsigned long long)(bits >> skip) : 0;
-                        sees = w << pre | ((1ull << pre) - 1);
-                    }
-                    const bool all = __all_sync(kFullMask, sees == ~0ull);
-                    // The maximum moves only when it grows by 2^kLazy: until then the
-                    // weights may pass 1, and sum and output stay as they are.
-                    auto raise = [&](float top, bool grow) {
-                        const float f = grow ? exp2_approx(mx - top) : 1.0f;
-                        if (grow) mx = top;
-                        l *= f;
-                        if (i > 0) {
-                            if (!wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) return f;
-                            tmem_fence_after();
-#pragma unroll 1
-                            for (int h = 0; h < D / 16; ++h) {
-                                uint32_t o[16];
-                                tmem_load16(lanes + 2 * kTile + h * 16, o);
-                                tmem_wait_load16(o);
+                    const bool prefix_only = p0 + kTile <= s.q.P;
+                    auto half = [&](const int h) {
+                        float(&mh)[2] = mx[h];
+                        const uint32_t at = lanes + ((uint32_t)(16 * h) << 16);
+                        const int column = 2 * (lane & 3);
+                        uint32_t x[32];
+                        tmem_load_rows16(at + b * kTile, x);
+                        if constexpr (kQuant) {
+                            if (i == 0)
 #pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_store16(lanes + 2 * kTile + h * 16, o);
-                            }
+                                for (int k = 0; k < 2; ++k)
+                                    factor[h][k] = sc.q[seg & 3][warp * 32 + 16 * h + 8 * k + lane / 4];
                         }
-                        return f;
-                    };
-                    auto grows = [&](float top) {
-                        return top > mx + kLazy || (mx == -INFINITY && top > mx);
-                    };
-                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    if constexpr (kQuant) {
-                        // Half of the columns a step of a loop that is not unrolled: the
-                        // warps of a scheduler run four kinds of code in turn, which
-                        // unrolled is more than its instruction cache; fewer columns a
-                        // step leave the latencies of its loads one after the other.
-                        constexpr int kStep = 32;
-                        if (i == 0) factor = sc.q[seg & 3][m];
-                        const float2 ff = make_float2(factor, factor);
-#pragma unroll 1
-                        for (int j = 0; j < kTile; j += kStep) {
-                            uint32_t x[kStep];
-                            tmem_load32(at + j, x);
-                            float4 f1[4], f2[4];
-                            auto scales = [&](int h) {
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    f1[k] = load_shared4(smem_addr(&sc.k[b][j + h + 4 * k]));
-                                    f2[k] = load_shared4(smem_addr(&sc.v_log2[b][j + h + 4 * k]));
-                                }
-                            };
-                            scales(0);
-                            tmem_wait_load(x);
+                        tmem_wait_load(x);
+                        auto pair = [&](int e) {  // elements 2e and 2e + 1, of row e % 2
+                            return make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+                        };
+                        if constexpr (kQuant) {
                             // scores to base 2, plus log2 of the value's scale
 #pragma unroll
-                            for (int h = 0; h < kStep; h += 16) {
-                                if (h > 0) scales(h);
+                            for (int j = 0; j < 8; ++j) {
+                                const float2 ks = *reinterpret_cast<const float2 *>(&sc.k[b][8 * j + column]);
+                                const float2 vs = *reinterpret_cast<const float2 *>(&sc.v_log2[b][8 * j + column]);
 #pragma unroll
-                                for (int k = 0; k < 16; k += 2) {
-                                    uint32_t *y = x + h + k;
-                                    const float4 kk = f1[k / 4], vv = f2[k / 4];
-                                    const float2 z = fma2(mul2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), ff),
-                                                          k & 2 ? make_float2(kk.z, kk.w) : make_float2(kk.x, kk.y),
-                                                          k & 2 ? make_float2(vv.z, vv.w) : make_float2(vv.x, vv.y));
-                                    y[0] = __float_as_uint(z.x);
-                                    y[1] = __float_as_uint(z.y);
+                                for (int k = 0; k < 2; ++k) {
+                                    const float f = factor[h][k];
+                                    const float2 y = fma2(mul2(pair(2 * j + k), make_float2(f, f)), ks, vs);
+                                    x[4 * j + 2 * k] = __float_as_uint(y.x);
+                                    x[4 * j + 2 * k + 1] = __float_as_uint(y.y);
                                 }
                             }
-                            if (!all) {
-                                const unsigned some = (unsigned)(sees >> j);
+                        } else if (negative) {
 #pragma unroll
-                                for (int k = 0; k < kStep; ++k)
-                                    if (!(some >> k & 1)) x[k] = 0xFF800000u;
+                            for (int j = 0; j < 32; ++j) x[j] ^= 0x80000000u;
+                        }
+                        if (!prefix_only) {
+                            // prefix positions, then the row's ancestors in the window
+                            const int pre = max(s.q.P - p0, 0), skip = max(p0 - s.q.P, 0);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const unsigned long long w = skip < 32 ? (unsigned long long)(seen[h][k] >> skip) : 0;
+                                const unsigned long long sees = (w << pre | ((1ull << pre) - 1)) >> column;
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (!(sees >> (8 * j + e) & 1)) x[4 * j + 2 * k + e] = 0xFF800000u;
                             }
-                            float tops[4];
+                        }
+                        // The maximum moves only when it grows by 2^kLazy: until then the
+                        // weights may pass 1, and sum and output stay as they are.
+                        float top[2];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) tops[k] = __uint_as_float(x[k]);
+                        for (int k = 0; k < 2; ++k) {
+                            top[k] = fmaxf(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
 #pragma unroll
-                            for (int k = 4; k < kStep; ++k)
-                                tops[k & 3] = fmaxf(tops[k & 3], __uint_as_float(x[k]));
-                            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                            const bool grow = grows(top);
-                            if (__any_sync(kFullMask, grow)) {
-                                const float f = raise(top, grow);
-                                sum[0] = mul2(sum[0], make_float2(f, f));
-                                sum[1] = mul2(sum[1], make_float2(f, f));
-                                if (j > 0) {  // this tile's weights so far
-                                    tmem_wait_store();
+                            for (int j = 1; j < 8; ++j)
+                                top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[4 * j + 2 * k]),
+                                                             __uint_as_float(x[4 * j + 2 * k + 1])));
+                            if (!kQuant) top[k] *= c;
+                        }
+                        auto grows = [&](int k) {
+                            return top[k] > mh[k] + kLazy || (mh[k] == -INFINITY && top[k] > mh[k]);
+                        };
+                        if (__any_sync(kFullMask, grows(0) || grows(1))) {
+                            float f[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                top[k] = fmaxf(top[k], __shfl_xor_sync(kFullMask, top[k], 1));
+                                top[k] = fmaxf(top[k], __shfl_xor_sync(kFullMask, top[k], 2));
+                                const bool grow = grows(k);
+                                f[k] = grow ? exp2_approx(mh[k] - top[k]) : 1.0f;
+                                if (grow) mh[k] = top[k];
+                                l[h][k] *= f[k];
+                            }
+                            if (i > 0) {
+                                if (!wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) return;
+                                tmem_fence_after();
 #pragma unroll 1
-                                    for (int h = 0; h < j / 2; h += 8) {
-                                        uint32_t o[8];
-                                        tmem_load8(at + h, o);
-                                        tmem_wait_load8(o);
+                                for (int d = 0; d < D; d += 64) {
+                                    uint32_t o[32];
+                                    tmem_load_rows16(at + 2 * kTile + d, o);
+                                    tmem_wait_load(o);
 #pragma unroll
-                                        for (int k = 0; k < 8; ++k) {
-                                            const float2 u = __half22float2(*reinterpret_cast<__half2 *>(&o[k]));
-                                            const __half2 two = __floats2half2_rn(u.x * f, u.y * f);
-                                            o[k] = *reinterpret_cast<const uint32_t *>(&two);
-                                        }
-                                        tmem_store8(at + h, o);
-                                    }
+                                    for (int j = 0; j < 32; ++j)
+                                        o[j] = __float_as_uint(__uint_as_float(o[j]) * f[j >> 1 & 1]);
+                                    tmem_store_rows16(at + 2 * kTile + d, o);
                                 }
                             }
-                            const float shift = mx == -INFINITY ? 0.0f : mx;
-                            const float2 minus = make_float2(-shift, -shift);
+                        }
+                        uint32_t w[16];
 #pragma unroll
-                            for (int h = 0; h < kStep; h += 16) {
-                                uint32_t w[8];
+                        for (int k = 0; k < 2; ++k) {
+                            const float shift = mh[k] == -INFINITY ? 0.0f : mh[k];
+                            float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    f1[k] = load_shared4(smem_addr(&sc.v_inv[b][j + h + 4 * k]));
-#pragma unroll
-                                for (int k = 0; k < 16; k += 2) {
-                                    const uint32_t *z = x + h + k;
-                                    const float2 y = add2(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])), minus);
+                            for (int j = 0; j < 8; ++j) {
+                                if constexpr (kQuant) {
+                                    const float2 y = add2(pair(2 * j + k), make_float2(-shift, -shift));
                                     const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                                    const float4 inv = f1[k / 4];
-                                    sum[k / 2 & 1] = fma2(u, k & 2 ? make_float2(inv.z, inv.w) : make_float2(inv.x, inv.y),
-                                                          sum[k / 2 & 1]);
+                                    sum = fma2(u, *reinterpret_cast<const float2 *>(&sc.v_inv[b][8 * j + column]), sum);
                                     const __half2 two = __floats2half2_rn(u.x, u.y);
-                                    w[k / 2] = *reinterpret_cast<const uint32_t *>(&two);
+                                    w[2 * j + k] = *reinterpret_cast<const uint32_t *>(&two);
+                                } else {
+                                    const float2 y = fma2(pair(2 * j + k), make_float2(c, c), make_float2(-shift, -shift));
+                                    const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                                    sum = add2(u, sum);
+                                    const __nv_bfloat162 two = __floats2bfloat162_rn(u.x, u.y);
+                                    w[2 * j + k] = *reinterpret_cast<const uint32_t *>(&two);
                                 }
-                                // over scores that have been read (columns up to j + h)
-                                tmem_store8(at + (j + h) / 2, w);
                             }
+                            l[h][k] += sum.x + sum.y;
                         }
-                        if (!ok) break;
-                    } else {
-                        uint32_t x[kTile], w[kTile / 2];
-                        tmem_load32(at, x);
-                        tmem_load32(at + 32, x + 32);
-                        tmem_wait_load(x);
-                        tmem_wait_load(x + 32);
-                        if (negative) {
-#pragma unroll
-                            for (int j = 0; j < kTile; ++j) x[j] ^= 0x80000000u;
-                        }
-                        if (!all) {
-#pragma unroll
-                            for (int j = 0; j < kTile; ++j)
-                                if (!(sees >> j & 1)) x[j] = 0xFF800000u;
-                        }
-                        float tops[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) tops[j] = __uint_as_float(x[j]);
-#pragma unroll
-                        for (int j = 4; j < kTile; ++j)
-                            tops[j & 3] = fmaxf(tops[j & 3], __uint_as_float(x[j]));
-                        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * c;
-                        const bool grow = grows(top);
-                        if (__any_sync(kFullMask, grow)) {
-                            raise(top, grow);
-                            if (!ok) break;
-                        }
-                        const float shift = mx == -INFINITY ? 0.0f : mx;
-                        const float2 cc = make_float2(c, c), minus = make_float2(-shift, -shift);
-#pragma unroll
-                        for (int j = 0; j < kTile; j += 2) {
-                            const float2 y = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
-                                                  cc, minus);
-                            const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                            sum[j / 2 & 1] = add2(u, sum[j / 2 & 1]);
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(u.x, u.y);
-                            w[j / 2] = *reinterpret_cast<const uint32_t *>(&two);
-                        }
-                        tmem_store32(at, w);
-                    }
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                        // the weights over the scores, which have been read
+                        tmem_store_pairs16(at + b * kTile, w);
+                    };
+                    half(0);
+                    if (halves == 2) half(1);
+                    if (!ok) break;
                     tmem_wait_store();
                 }
                 if (!kQuant && p0 + kTile > s.q.P) {
@@ -1163,11 +1125,24 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             tmem_fence_after();
 
             const bool whole = s.count == s.q.tiles;
-            const float shift = mx == -INFINITY ? 0.0f : mx;
+            // from here on a lane is a row
+            float row_mx = 0.0f, row_l = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float sum = l[h][k];
+                    sum += __shfl_xor_sync(kFullMask, sum, 1);
+                    sum += __shfl_xor_sync(kFullMask, sum, 2);
+                    const float u = __shfl_sync(kFullMask, mx[h][k], lane % 8 * 4);
+                    const float v = __shfl_sync(kFullMask, sum, lane % 8 * 4);
+                    if (lane / 8 == 2 * h + k) row_mx = u, row_l = v;
+                }
+            const float shift = row_mx == -INFINITY ? 0.0f : row_mx;
             const unsigned extra = *(volatile unsigned *)&ctl.nonfinite[seg & 3] & bits;
             const int slot = 2 * cta + (seg > 0);
             if (active) {
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const float inv = row_l == 0.0f ? 0.0f : 1.0f / row_l;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + packed * a.ld_out +
                                      (long long)head * D;
 #pragma unroll 1
@@ -1214,7 +1189,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             float u = __uint_as_float(o[2 * j]) * inv, v = __uint_as_float(o[2 * j + 1]) * inv;
-                            if (l == 0.0f) u = v = 0.0f;
+                            if (row_l == 0.0f) u = v = 0.0f;
                             const __nv_bfloat162 two = __floats2bfloat162_rn(u, v);
                             w[j] = *reinterpret_cast<const uint32_t *>(&two);
                         }
@@ -1225,11 +1200,11 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     }
                 }
                 if (!whole) {
-                    t.part_ml[(long long)slot * 2 * kRowsPerTile + m] = mx;
-                    t.part_ml[((long long)slot * 2 + 1) * kRowsPerTile + m] = l;
+                    t.part_ml[(long long)slot * 2 * kRowsPerTile + m] = row_mx;
+                    t.part_ml[((long long)slot * 2 + 1) * kRowsPerTile + m] = row_l;
                 } else if (valid && a.lse) {
                     a.lse[(long long)packed * a.n_q_heads + head] =
-                        l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
+                        row_l == 0.0f ? -INFINITY : shift * kLn2 + logf(row_l);
                 }
             }
             tmem_fence_before();
