@@ -705,8 +705,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             // a NaN or infinite k_scale makes the score NaN
                             k[j] = ks[j] - ks[j] == 0.0f ? ks[j] * c : __int_as_float(0x7FC00000);
                             const float f = fine ? fmaxf(fabsf(vs[j]), 0x1p-100f) : 1.0f;
-                            log2v[j] = log2f(f);
-                            inv[j] = 1.0f / f;
+                            log2v[j] = __log2f(f);
+                            inv[j] = __frcp_rn(f);
                             raw[j] = vs[j];
                             odd = odd || !fine || vs[j] < 0.0f;
                         }
@@ -754,16 +754,15 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
                 return ok;
             };
-            // Their place is chunks 2 part and 2 part + 1 of the token's row.  Lanes
-            // of one half start with the one, of the other with the other, so that
-            // eight lanes cover the eight chunk columns of shared memory.
-            auto put = [&](unsigned char *dst, int tok, int part, const uint32_t *h) {
-                unsigned char *row = dst + part / 4 * kHalfBytes + tok * 128;
-                const int flip = part / 4 & 1, ch = part % 4 * 2;
-                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                *reinterpret_cast<uint4 *>(row + ((ch + flip ^ (tok & 7)) << 4)) = flip ? hi : lo;
-                *reinterpret_cast<uint4 *>(row + ((ch + 1 - flip ^ (tok & 7)) << 4)) = flip ? lo : hi;
-            };
+            // Their place is chunks 2 part and 2 part + 1 of the token's row.  Lanes of one
+            // half start with the one, of the other with the other, so that eight lanes
+            // cover the eight chunk columns of shared memory.  A thread's tokens are
+            // 128 / kUnits apart, a multiple of eight: its places differ by whole rows.
+            const int part = ct % kUnits, own = ct / kUnits;
+            const unsigned flip = part / 4 & 1;
+            const unsigned place = S::kOpAt + part / 4 * kHalfBytes + own * 128;
+            const unsigned first = place + (((part % 4 * 2 + flip) ^ (own & 7)) << 4);
+            const unsigned last = place + (((part % 4 * 2 + 1 - flip) ^ (own & 7)) << 4);
             for (;;) {
                 // a warp that gave up still comes to the four warps' barriers
                 ok = named_all(2, 128, ok);
@@ -848,22 +847,30 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     const int p0 = (s.first + i) * kTile;
                     bool plain = p0 + kTile <= s.q.P && !*(volatile int *)&sc.odd[b];
                     if (plain) {
-                        unsigned nan = 0;
+                        __half2 most_h = __float2half2_rn(0.0f);
+                        const unsigned char *from = src + ct * 16;
+                        unsigned char *to = smem + b * S::kOpBytes;
 #pragma unroll 1
                         for (int k = 0; k < kSteps; ++k) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(src + (k * 128 + ct) * 16);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(from);
                             const unsigned w[4] = {v.x, v.y, v.z, v.w};
-                            uint32_t h[8];
+                            uint32_t g[8];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                // a code of all ones, a NaN, carries into the sign
-                                nan |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                                h[2 * e] = (w[e] << 7 & 0x3F803F80u) | (w[e] << 8 & 0x80008000u);
-                                h[2 * e + 1] = (w[e] >> 1 & 0x3F803F80u) | (w[e] & 0x80008000u);
+                                g[2 * e] = (w[e] << 7 & 0x3F803F80u) | (w[e] << 8 & 0x80008000u);
+                                g[2 * e + 1] = (w[e] >> 1 & 0x3F803F80u) | (w[e] & 0x80008000u);
                             }
-                            put(dst, (k * 128 + ct) / kUnits, ct % kUnits, h);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                most_h = __hmax2(most_h, __habs2(*reinterpret_cast<__half2 *>(&g[e])));
+                            const uint4 lo = make_uint4(g[0], g[1], g[2], g[3]), hi = make_uint4(g[4], g[5], g[6], g[7]);
+                            *reinterpret_cast<uint4 *>(to + first) = flip ? hi : lo;
+                            *reinterpret_cast<uint4 *>(to + last) = flip ? lo : hi;
+                            from += 2048;
+                            to += 128 / kUnits * 128;
                         }
-                        plain = __all_sync(kFullMask, nan == 0);
+                        // a code of all ones, which is NaN, has become 1.875: the largest
+                        plain = __all_sync(kFullMask, __low2float(most_h) < 1.875f && __high2float(most_h) < 1.875f);
                     }
                     if (!plain) {
                         // Scales that are not plain numbers (or negative) go into the
@@ -939,19 +946,21 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             // The scores are taken as fragments: of the warp's rows a thread has
             // four, 16 h + 8 k + lane / 4, and of each sixteen columns.  16 rows or
             // fewer are one half's work, and few scales serve a thread.
-            float mx[2][2], l[2][2], factor[2][2];  // running maximum (to base 2), sum
-            unsigned seen[2][2];                    // ancestor bits
             const int halves = rows - warp * 32 > 16 ? 2 : 1;
+            struct Row {
+                float mx, l, factor;  // running maximum (to base 2), sum; query's power of two
+                unsigned seen;        // ancestor bits
+            } now[2], other[2];       // of the half at hand, and of the other
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < 2; ++k) {
+                auto row_of = [&](int h) -> Row {
                     const int token_k = token0 + min(warp * 32 + 16 * h + 8 * k + lane / 4, rows - 1) / t.group;
-                    mx[h][k] = -INFINITY;
-                    l[h][k] = 0.0f;
-                    factor[h][k] = 1.0f;
-                    seen[h][k] = active ? ancestors_of(a, s.q.row0 + token_k, token_k, s.q.len) : 0;
-                }
+                    return {-INFINITY, 0.0f, 1.0f,
+                            active ? ancestors_of(a, s.q.row0 + token_k, token_k, s.q.len) : 0u};
+                };
+                now[k] = row_of(0);
+                other[k] = row_of(1);
+            }
             for (int i = 0; i < s.count; ++i) {
                 const unsigned tile = done + i, b = tile & 1;
                 const int p0 = (s.first + i) * kTile;
@@ -960,8 +969,10 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     if (kQuant && !wait(&ctl.scales[b], tile >> 1)) break;
                     tmem_fence_after();
                     const bool prefix_only = p0 + kTile <= s.q.P;
-                    auto half = [&](const int h) {
-                        float(&mh)[2] = mx[h];
+                    // (a loop, not two copies: the warps of a scheduler run several kinds
+                    // of code in turn, and all of it is to stay in the instruction cache)
+#pragma unroll 1
+                    for (int h = 0; h < halves; ++h) {
                         const uint32_t at = lanes + ((uint32_t)(16 * h) << 16);
                         const int column = 2 * (lane & 3);
                         uint32_t x[32];
@@ -970,7 +981,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             if (i == 0)
 #pragma unroll
                                 for (int k = 0; k < 2; ++k)
-                                    factor[h][k] = sc.q[seg & 3][warp * 32 + 16 * h + 8 * k + lane / 4];
+                                    now[k].factor = sc.q[seg & 3][warp * 32 + 16 * h + 8 * k + lane / 4];
                         }
                         tmem_wait_load(x);
                         auto pair = [&](int e) {  // elements 2e and 2e + 1, of row e % 2
@@ -984,7 +995,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                                 const float2 vs = *reinterpret_cast<const float2 *>(&sc.v_log2[b][8 * j + column]);
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
-                                    const float f = factor[h][k];
+                                    const float f = now[k].factor;
                                     const float2 y = fma2(mul2(pair(2 * j + k), make_float2(f, f)), ks, vs);
                                     x[4 * j + 2 * k] = __float_as_uint(y.x);
                                     x[4 * j + 2 * k + 1] = __float_as_uint(y.y);
@@ -999,7 +1010,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             const int pre = max(s.q.P - p0, 0), skip = max(p0 - s.q.P, 0);
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const unsigned long long w = skip < 32 ? (unsigned long long)(seen[h][k] >> skip) : 0;
+                                const unsigned long long w = skip < 32 ? (unsigned long long)(now[k].seen >> skip) : 0;
                                 const unsigned long long sees = (w << pre | ((1ull << pre) - 1)) >> column;
 #pragma unroll
                                 for (int j = 0; j < 8; ++j)
@@ -1021,7 +1032,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             if (!kQuant) top[k] *= c;
                         }
                         auto grows = [&](int k) {
-                            return top[k] > mh[k] + kLazy || (mh[k] == -INFINITY && top[k] > mh[k]);
+                            return top[k] > now[k].mx + kLazy || (now[k].mx == -INFINITY && top[k] > now[k].mx);
                         };
                         if (__any_sync(kFullMask, grows(0) || grows(1))) {
                             float f[2];
@@ -1030,12 +1041,12 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                                 top[k] = fmaxf(top[k], __shfl_xor_sync(kFullMask, top[k], 1));
                                 top[k] = fmaxf(top[k], __shfl_xor_sync(kFullMask, top[k], 2));
                                 const bool grow = grows(k);
-                                f[k] = grow ? exp2_approx(mh[k] - top[k]) : 1.0f;
-                                if (grow) mh[k] = top[k];
-                                l[h][k] *= f[k];
+                                f[k] = grow ? exp2_approx(now[k].mx - top[k]) : 1.0f;
+                                if (grow) now[k].mx = top[k];
+                                now[k].l *= f[k];
                             }
                             if (i > 0) {
-                                if (!wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) return;
+                                if (!wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) break;
                                 tmem_fence_after();
 #pragma unroll 1
                                 for (int d = 0; d < D; d += 64) {
@@ -1052,7 +1063,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         uint32_t w[16];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const float shift = mh[k] == -INFINITY ? 0.0f : mh[k];
+                            const float shift = now[k].mx == -INFINITY ? 0.0f : now[k].mx;
                             float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
@@ -1070,13 +1081,18 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                                     w[2 * j + k] = *reinterpret_cast<const uint32_t *>(&two);
                                 }
                             }
-                            l[h][k] += sum.x + sum.y;
+                            now[k].l += sum.x + sum.y;
                         }
                         // the weights over the scores, which have been read
                         tmem_store_pairs16(at + b * kTile, w);
-                    };
-                    half(0);
-                    if (halves == 2) half(1);
+                        if (halves == 2)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const Row r = now[k];
+                                now[k] = other[k];
+                                other[k] = r;
+                            }
+                    }
                     if (!ok) break;
                     tmem_wait_store();
                 }
@@ -1131,10 +1147,10 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    float sum = l[h][k];
+                    float sum = h ? other[k].l : now[k].l;
                     sum += __shfl_xor_sync(kFullMask, sum, 1);
                     sum += __shfl_xor_sync(kFullMask, sum, 2);
-                    const float u = __shfl_sync(kFullMask, mx[h][k], lane % 8 * 4);
+                    const float u = __shfl_sync(kFullMask, h ? other[k].mx : now[k].mx, lane % 8 * 4);
                     const float v = __shfl_sync(kFullMask, sum, lane % 8 * 4);
                     if (lane / 8 == 2 * h + k) row_mx = u, row_l = v;
                 }
