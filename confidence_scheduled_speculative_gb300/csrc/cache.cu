@@ -9,11 +9,12 @@
 // Each element is read once and written once and costs some ten operations,
 // so the bound is HBM bandwidth; for a window of a few rows it is the launch.
 //
-// append_kernel   eight elements a lane (16 bytes of bf16), 8, 16 or 32 lanes a
-//   head, so that a head's sums, its maximum and the partner of a rotated
-//   element are warp shuffles away and nothing is read twice.  A warp takes
-//   kHeadsPerLane heads a lane group of one row: the row's cosines and sines
-//   stay in registers over them, and their loads are all in flight together.
+// append_kernel   a warp takes one row, or a part of its heads where rows are few, and
+//   steps through them a few heads a lane group at a time, the next ones'
+//   loads in flight.  The row's position, slot, cosines and sines are fetched once.
+//   A head is D / 8 lanes of eight elements: four and the four that they rotate with,
+//   so that the rotation stays in a lane and a head's sum and maximum are a few
+//   shuffles; nothing is read twice.
 // append_any_kernel   any alignment, stride and even head size: one warp a
 //   (row, head), one element a lane and step.
 // read_kernel     a CTA takes 32 output rows: their slots are looked up by one
@@ -27,7 +28,10 @@
 namespace dspark {
 
 constexpr int kAppendThreads = 256;
-constexpr int kHeadsPerLane = 4;
+// heads a lane group has in flight: 64 bytes a lane
+template <typename T>
+constexpr int kHeadsPerLane = 16 / sizeof(T) / 2;
+constexpr int kWarpsWanted = 24;  // an SM, before a warp takes all heads of a row
 constexpr int kReadThreads = 256;
 constexpr int kReadRows = 32;
 
@@ -49,22 +53,42 @@ struct AppendArgs {
     int32_t *status;
 };
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
-    const unsigned w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// Four elements as they lie in memory, as numbers, and back.
+template <typename T>
+struct Four;
+template <>
+struct Four<__nv_bfloat16> {
+    using Raw = uint2;
+    __device__ static void unpack(const Raw &v, float *x) {
+        x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
     }
+    __device__ static Raw pack(const float *x) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+        return make_uint2(*reinterpret_cast<const unsigned *>(&a), *reinterpret_cast<const unsigned *>(&b));
+    }
+};
+template <>
+struct Four<float> {
+    using Raw = float4;
+    __device__ static void unpack(const Raw &v, float *x) {
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    }
+    __device__ static Raw pack(const float *x) { return make_float4(x[0], x[1], x[2], x[3]); }
+};
+
+// Eight elements as numbers, and back.
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+    Four<__nv_bfloat16>::unpack(make_uint2(v.x, v.y), x);
+    Four<__nv_bfloat16>::unpack(make_uint2(v.z, v.w), x + 4);
 }
 __device__ __forceinline__ void load8(const float *p, float *x) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    Four<float>::unpack(__ldg(reinterpret_cast<const float4 *>(p)), x);
+    Four<float>::unpack(__ldg(reinterpret_cast<const float4 *>(p) + 1), x + 4);
 }
 __device__ __forceinline__ void load8(const e4m3 *p, float *x) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const unsigned w = i < 2 ? v.x : v.y;
@@ -74,18 +98,12 @@ __device__ __forceinline__ void load8(const e4m3 *p, float *x) {
     }
 }
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float *x) {
-    uint4 v;
-    unsigned *w = reinterpret_cast<unsigned *>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const unsigned *>(&b);
-    }
-    *reinterpret_cast<uint4 *>(p) = v;
+    const uint2 a = Four<__nv_bfloat16>::pack(x), b = Four<__nv_bfloat16>::pack(x + 4);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(a.x, a.y, b.x, b.y);
 }
 __device__ __forceinline__ void store8(float *p, const float *x) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    reinterpret_cast<float4 *>(p)[0] = Four<float>::pack(x);
+    reinterpret_cast<float4 *>(p)[1] = Four<float>::pack(x + 4);
 }
 
 __device__ __forceinline__ int rows_of(const AppendArgs &a) {
@@ -114,141 +132,167 @@ __device__ __forceinline__ bool row_angle(const AppendArgs &a, int row, int *p) 
 }
 
 template <typename T, typename C>
-__global__ void __launch_bounds__(kAppendThreads)
-append_kernel(AppendArgs a, int lanes_per_head) {
+__global__ void __launch_bounds__(kAppendThreads, 3)
+append_kernel(AppendArgs a, int lanes_per_head, int parts) {
     constexpr bool kCache = !std::is_same<C, NoCache>::value;
+    constexpr int kHeads = kHeadsPerLane<T>;
+    using Raw = typename Four<T>::Raw;
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int D = a.head_dim, groups = 32 / lanes_per_head;
-    const int group = lane / lanes_per_head, chunk = lane % lanes_per_head;
-    const int H = a.heads[0] + a.heads[1] + a.heads[2];
-    const int per_warp = groups * kHeadsPerLane;
-    const int blocks = (H + per_warp - 1) / per_warp;
-    const long long unit = (long long)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
-    const long long row64 = div_nonneg(unit, blocks);
-    if (row64 >= rows_of(a)) return;
-    const int row = (int)row64;
-    const int h0 = (int)(unit - row64 * blocks) * per_warp + group;
+    const int lane = threadIdx.x & 31, D = a.head_dim;
+    const unsigned unit = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const int row = unit / (unsigned)parts, part = unit - row * parts;
+    if (row >= a.max_rows) return;
+    const int groups = 32 / lanes_per_head, group = lane / lanes_per_head;
+    const int chunk = lane % lanes_per_head;
+    const int H = a.heads[0] + a.heads[1] + a.heads[2], step = groups * kHeads;
+    const int per = ((H + step - 1) / step + parts - 1) / parts * step;  // heads of a part
+    const int begin = part * per, end = min(begin + per, H);
     const bool has = chunk * 8 < D;  // a lane past a head that is not a power of two
 
-    // every load of the warp's heads in flight before the first is used
-    float x[kHeadsPerLane][8];
-    int kind[kHeadsPerLane], head[kHeadsPerLane];
-#pragma unroll
-    for (int i = 0; i < kHeadsPerLane; ++i) {
-        int h = h0 + i * groups;
-        kind[i] = h >= H ? 3 : (h < a.heads[0] ? 0 : (h < a.heads[0] + a.heads[1] ? 1 : 2));
-        head[i] = h - (kind[i] > 0 ? a.heads[0] : 0) - (kind[i] > 1 ? a.heads[1] : 0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = 0.0f;
-        if (kind[i] < 3 && has)
-            load8(static_cast<const T *>(a.in[kind[i]]) + row * a.ld_in[kind[i]] +
-                      (long long)head[i] * D + chunk * 8,
-                  x[i]);
-    }
-    const bool pad = a.req && __ldg(a.req + row) < 0;
-    int p, page = -1, token = 0;
-    const bool angle = !pad && row_angle(a, row, &p);
-    bool slot = false;
-    if (kCache && !pad && h0 - group + per_warp > a.heads[0]) slot = row_slot(a, row, &page, &token);
-
-    // this lane's cosines and sines, and how it is rotated: with the lane that
-    // holds the other half (sign +-1), within itself, or not at all (0)
-    float c[8], s[8];
-    int partner = lane;
-    float sign = 0.0f;
-    if (a.cos_sin && angle && chunk * 8 < a.rope_dim) {
-        const float *cs = a.cos_sin + (long long)p * a.rope_dim, *sn = cs + a.rope_dim / 2;
-        if (a.interleaved) {
-            const float4 cc = __ldg(reinterpret_cast<const float4 *>(cs + chunk * 4));
-            const float4 ss = __ldg(reinterpret_cast<const float4 *>(sn + chunk * 4));
-            c[0] = cc.x, c[1] = cc.y, c[2] = cc.z, c[3] = cc.w;
-            s[0] = ss.x, s[1] = ss.y, s[2] = ss.z, s[3] = ss.w;
-            sign = 1.0f;
-        } else {
-            const int half = a.rope_dim / 16, first = chunk < half ? chunk : chunk - half;
-            load8(cs + first * 8, c);
-            load8(sn + first * 8, s);
-            partner = lane + (chunk < half ? half : -half);
-            sign = chunk < half ? -1.0f : 1.0f;
-        }
+    // where this lane's two fours of a head lie: an element and its partner, which
+    // is R / 2 on in the first R, or the next one in neighbouring pairs; the rest
+    // lie anywhere
+    const int R = a.cos_sin ? a.rope_dim : 0;
+    int at0 = chunk * 8, at1 = at0 + 4;
+    bool turned = at0 < R;
+    if (!a.interleaved && R) {
+        turned = chunk * 4 < R / 2;
+        const int rest = chunk * 4 - R / 2;
+        at0 = turned ? chunk * 4 : R + rest;
+        at1 = turned ? at0 + R / 2 : R + (D - R) / 2 + rest;
     }
 
+    // the heads of one step, as they lie in memory
+    Raw raw[kHeads][2];
+    auto kind_of = [&](int h) { return h < a.heads[0] ? 0 : (h < a.heads[0] + a.heads[1] ? 1 : 2); };
+    auto head_of = [&](int h, int kind) {
+        return h - (kind > 0 ? a.heads[0] : 0) - (kind > 1 ? a.heads[1] : 0);
+    };
+    auto fetch = [&](int h0) {
 #pragma unroll
-    for (int i = 0; i < kHeadsPerLane; ++i) {
-        // the shuffles below are the whole warp's: every lane goes through
-        // them, whatever its head is
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = x[i][e];
-        const T *w = kind[i] < 2 ? static_cast<const T *>(a.weight[kind[i]]) : nullptr;
-        if (a.weight[0] || a.weight[1]) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-            for (int o = lanes_per_head >> 1; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
-            if (w && has) {
-                const float inv = 1.0f / sqrtf(ss / (float)D + a.eps);
-                float g[8];
-                load8(w + chunk * 8, g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * g[e];
+        for (int i = 0; i < kHeads; ++i) {
+            const int h = h0 + i * groups + group;
+            if (h < end && has) {
+                const int kind = kind_of(h);
+                const T *p = static_cast<const T *>(a.in[kind]) + row * a.ld_in[kind] +
+                             head_of(h, kind) * D;
+                raw[i][0] = *reinterpret_cast<const Raw *>(p + at0);
+                raw[i][1] = *reinterpret_cast<const Raw *>(p + at1);
+            } else {
+                raw[i][0] = raw[i][1] = Raw{};
             }
         }
-        if (a.cos_sin) {
-            if (a.interleaved) {
-                if (kind[i] < 2 && sign != 0.0f) {
+    };
+    if (begin >= end) return;
+    fetch(begin);
+    const int total = a.totals ? __ldg(a.totals) : a.max_rows;
+    const int r = a.req ? __ldg(a.req + row) : 0;
+    const int position = a.pos ? __ldg(a.pos + row) : 0;
+    const int place = a.cache_pos ? __ldg(a.cache_pos + row) : position;
+    if (row >= total || r < 0) return;
+    const bool angle = !R || (position >= 0 && position < a.n_pos);
+    if (!angle) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+    int page = -1, token = 0;
+    if (kCache && end > a.heads[0]) {
+        page = kv_page(a.cache, r, place, &token);
+        if (page < 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+    }
+    float c[4], s[4];
+    if (turned && angle) {
+        const float *cs = a.cos_sin + (long long)position * R + chunk * 4;
+        Four<float>::unpack(__ldg(reinterpret_cast<const float4 *>(cs)), c);
+        Four<float>::unpack(__ldg(reinterpret_cast<const float4 *>(cs + R / 2)), s);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[e] = 1.0f, s[e] = 0.0f;
+    }
+
+    for (int h0 = begin; h0 < end; h0 += step) {
+        Raw now[kHeads][2];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) now[i][0] = raw[i][0], now[i][1] = raw[i][1];
+        if (h0 + step < end) fetch(h0 + step);
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            // the shuffles are the whole warp's: every lane goes through them
+            const int h = h0 + i * groups + group;
+            const bool in = h < end && has;
+            const int kind = kind_of(h), head = head_of(h, kind);
+            float y[8];
+            Four<T>::unpack(now[i][0], y);
+            Four<T>::unpack(now[i][1], y + 4);
+            if (a.weight[0] || a.weight[1]) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+                for (int o = lanes_per_head >> 1; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+                const T *w = kind < 2 ? static_cast<const T *>(a.weight[kind]) : nullptr;
+                if (w && in) {
+                    const float inv = rsqrtf(ss / (float)D + a.eps);
+                    float g[8];
+                    Four<T>::unpack(__ldg(reinterpret_cast<const Raw *>(w + at0)), g);
+                    Four<T>::unpack(__ldg(reinterpret_cast<const Raw *>(w + at1)), g + 4);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * g[e];
+                }
+            }
+            if (turned && kind < 2) {
+                if (a.interleaved) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float u = y[2 * e], v = y[2 * e + 1];
                         y[2 * e] = u * c[e] - v * s[e];
                         y[2 * e + 1] = v * c[e] + u * s[e];
                     }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float o = __shfl_sync(kFullMask, y[e], partner);
-                    if (kind[i] < 2 && sign != 0.0f) y[e] = y[e] * c[e] + sign * o * s[e];
-                }
-            }
-        }
-        if (!kCache || kind[i] == 0) {
-            if (kind[i] < 2 && has && angle)
-                store8(static_cast<T *>(a.out[kind[i]]) + row * a.ld_out[kind[i]] +
-                           (long long)head[i] * D + chunk * 8,
-                       y);
-            if (!kCache) continue;
-        }
-        if constexpr (kCache) {
-            const bool write = has && slot && (kind[i] == 2 || (kind[i] == 1 && angle));
-            unsigned char *base = kind[i] == 1 ? a.cache.k : a.cache.v;
-            const long long at = kv_offset(a.cache, page, token, head[i]) + chunk * 8;
-            if constexpr (std::is_same<C, e4m3>::value) {
-                unsigned m = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(y[e]) & 0x7FFFFFFFu);
-                for (int o = lanes_per_head >> 1; o; o >>= 1)
-                    m = max(m, __shfl_xor_sync(kFullMask, m, o));
-                if (write) {
-                    const float scale = e4m3_scale(m);
-                    uint2 codes = make_uint2(0, 0);
+                } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const unsigned two = e4m3_pair(__fdiv_rn(y[2 * e], scale),
-                                                       __fdiv_rn(y[2 * e + 1], scale));
-                        (e < 2 ? codes.x : codes.y) |= two << (16 * (e & 1));
-                    }
-                    *reinterpret_cast<uint2 *>(base + at) = codes;
-                    if (chunk == 0) {
-                        (kind[i] == 1 ? a.cache.k_scale
-                                      : a.cache.v_scale)[kv_scale_offset(a.cache, page, token, head[i])] = scale;
-                        if (m >= 0x7F800000u) flag(a.status, DSPARK_STATUS_BAD_INPUT);
+                        const float u = y[e], v = y[e + 4];
+                        y[e] = u * c[e] - v * s[e];
+                        y[e + 4] = v * c[e] + u * s[e];
                     }
                 }
-            } else {
-                if (write) store8(reinterpret_cast<C *>(base) + at, y);
+            }
+            if (!kCache || kind == 0) {
+                if (in && angle) {
+                    T *p = static_cast<T *>(a.out[kind]) + row * a.ld_out[kind] + head * D;
+                    *reinterpret_cast<Raw *>(p + at0) = Four<T>::pack(y);
+                    *reinterpret_cast<Raw *>(p + at1) = Four<T>::pack(y + 4);
+                }
+                if (!kCache) continue;
+            }
+            if constexpr (kCache) {
+                const bool write = in && page >= 0 && (kind == 2 || (kind == 1 && angle));
+                unsigned char *base = kind == 1 ? a.cache.k : a.cache.v;
+                const long long to = kv_offset(a.cache, page, token, head);
+                if constexpr (std::is_same<C, e4m3>::value) {
+                    if (!__any_sync(kFullMask, kind > 0 && h < end)) continue;
+                    unsigned m = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+                    for (int o = lanes_per_head >> 1; o; o >>= 1)
+                        m = max(m, __shfl_xor_sync(kFullMask, m, o));
+                    if (write) {
+                        const float scale = e4m3_scale(m);
+                        unsigned codes[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            codes[e] = e4m3_pair(__fdiv_rn(y[2 * e], scale), __fdiv_rn(y[2 * e + 1], scale));
+                        *reinterpret_cast<unsigned *>(base + to + at0) = codes[0] | codes[1] << 16;
+                        *reinterpret_cast<unsigned *>(base + to + at1) = codes[2] | codes[3] << 16;
+                        if (chunk == 0) {
+                            (kind == 1 ? a.cache.k_scale
+                                       : a.cache.v_scale)[kv_scale_offset(a.cache, page, token, head)] = scale;
+                            if (m >= 0x7F800000u) flag(a.status, DSPARK_STATUS_BAD_INPUT);
+                        }
+                    }
+                } else if (write && kind > 0) {
+                    using Stored = typename Four<C>::Raw;
+                    C *p = reinterpret_cast<C *>(base) + to;
+                    *reinterpret_cast<Stored *>(p + at0) = Four<C>::pack(y);
+                    *reinterpret_cast<Stored *>(p + at1) = Four<C>::pack(y + 4);
+                }
             }
         }
     }
@@ -421,13 +465,16 @@ cudaError_t launch_append(const AppendArgs &a, bool vec, cudaStream_t stream) {
     const int H = a.heads[0] + a.heads[1] + a.heads[2];
     constexpr int kWarps = kAppendThreads / 32;
     if (vec) {
+        // a warp a row streams best; few rows are split over their heads until every
+        // SM has kWarpsWanted warps
         const int lanes = a.head_dim <= 64 ? 8 : (a.head_dim <= 128 ? 16 : 32);
-        const int per_warp = 32 / lanes * kHeadsPerLane;
-        const long long units = (long long)a.max_rows * ((H + per_warp - 1) / per_warp);
-        const long long grid = (units + kWarps - 1) / kWarps;
-        if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+        const int step = 32 / lanes * kHeadsPerLane<T>, steps = (H + step - 1) / step;
+        const long long want = (long long)kWarpsWanted * sm_count();
+        const int parts = (int)max(1ll, min((long long)steps, want / a.max_rows));
+        const long long grid = ((long long)a.max_rows * parts + kWarps - 1) / kWarps;
+        if (grid > 0x7FFFFFFF / kWarps) return cudaErrorInvalidConfiguration;
         return launch_pdl(append_kernel<T, C>, dim3((unsigned)grid), dim3(kAppendThreads), 0,
-                          stream, a, lanes);
+                          stream, a, lanes, parts);
     }
     const long long grid = ((long long)a.max_rows * H + kWarps - 1) / kWarps;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
@@ -458,16 +505,17 @@ cudaError_t launch_read_out(const ReadArgs &a, int out_dtype, bool vec, cudaStre
 
 namespace {
 
-// Whether p and a stride of ld elements keep 16-byte (E4M3: 8-byte) accesses of
-// eight elements aligned.
-bool eights(const void *p, long long ld, int elem_bytes) {
-    return aligned(p, elem_bytes == 1 ? 8 : 16) && ld % (elem_bytes == 4 ? 4 : 8) == 0;
+// Whether p and a stride of ld elements keep accesses of n elements (16 bytes at
+// most) aligned.
+bool aligned_to(const void *p, long long ld, int n, int elem_bytes) {
+    const int bytes = n * elem_bytes < 16 ? n * elem_bytes : 16;
+    return aligned(p, bytes) && ld * elem_bytes % bytes == 0;
 }
 
-bool cache_eights(const dspark_kv_cache &c) {
+bool cache_aligned(const dspark_kv_cache &c, int n) {
     const int e = kv_elem_bytes(c.dtype);
-    return c.head_dim % 8 == 0 && eights(c.k, c.page_stride, e) && eights(c.v, c.token_stride, e) &&
-           eights(c.k, c.head_stride, e);
+    return c.head_dim % n == 0 && aligned_to(c.k, c.page_stride, n, e) &&
+           aligned_to(c.v, c.token_stride, n, e) && aligned_to(c.k, c.head_stride, n, e);
 }
 
 // The checks that the two writing calls share; fills the arguments they share.
@@ -517,14 +565,14 @@ int fill_append(AppendArgs &a, const void *q, int64_t ld_q, const void *k, int64
     return DSPARK_OK;
 }
 
-// Whether the shared operands allow append_kernel: eight elements a lane.
-bool append_eights(const AppendArgs &a, int dtype) {
+// Whether the shared operands allow append_kernel: lanes of two fours.
+bool append_fours(const AppendArgs &a, int dtype) {
     const int e = kv_elem_bytes(dtype);
     bool ok = a.head_dim % 8 == 0;
-    for (int i = 0; i < 3; ++i) ok = ok && eights(a.in[i], a.ld_in[i], e);
-    for (int i = 0; i < 2; ++i) ok = ok && eights(a.out[i], a.ld_out[i], e) && aligned(a.weight[i], 16);
-    if (a.cos_sin)  // half pairs: both halves whole lanes; neighbours: whole lanes
-        ok = ok && aligned(a.cos_sin, 16) && a.rope_dim % (a.interleaved ? 8 : 16) == 0;
+    for (int i = 0; i < 3; ++i) ok = ok && aligned_to(a.in[i], a.ld_in[i], 4, e);
+    for (int i = 0; i < 2; ++i)
+        ok = ok && aligned_to(a.out[i], a.ld_out[i], 4, e) && aligned(a.weight[i], 4 * e);
+    if (a.cos_sin) ok = ok && aligned(a.cos_sin, 16) && a.rope_dim % 8 == 0;
     return ok;
 }
 
@@ -549,7 +597,7 @@ extern "C" int dspark_qk_norm_rope(const void *q, int64_t ld_q, const void *k, i
     a.out[1] = k_out;
     a.ld_out[1] = ld_k_out;
     if (max_rows == 0) return DSPARK_OK;
-    const bool vec = append_eights(a, dtype);
+    const bool vec = append_fours(a, dtype);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == DSPARK_DTYPE_BF16
                               ? launch_append_cache<__nv_bfloat16>(a, -1, vec, st)
@@ -578,7 +626,7 @@ extern "C" int dspark_kv_append(const void *q, int64_t ld_q, const void *k, int6
     a.cache_pos = cache_pos;
     a.cache = kv_view(*cache);
     if (max_rows == 0) return DSPARK_OK;
-    const bool vec = append_eights(a, dtype) && cache_eights(*cache);
+    const bool vec = append_fours(a, dtype) && cache_aligned(*cache, 4);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == DSPARK_DTYPE_BF16
                               ? launch_append_cache<__nv_bfloat16>(a, cache->dtype, vec, st)
@@ -610,7 +658,7 @@ extern "C" int dspark_kv_read(const dspark_kv_cache *cache, const int32_t *start
     a.ld_out = ld_out;
     a.status = status;
     const int e = kv_elem_bytes(out_dtype);
-    const bool vec = cache_eights(*cache) && eights(k_out, ld_out, e) && eights(v_out, ld_out, e);
+    const bool vec = cache_aligned(*cache, 8) && aligned_to(k_out, ld_out, 8, e) && aligned_to(v_out, ld_out, 8, e);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (max_rows == 0) return DSPARK_OK;
     cudaError_t err;
