@@ -22,6 +22,7 @@
 //   stream the rows' elements.
 
 #include "kvcache.cuh"
+#include "pairs.cuh"
 
 #include <type_traits>
 
@@ -31,7 +32,7 @@ constexpr int kAppendThreads = 256;
 // heads a lane group has in flight: 64 bytes a lane
 template <typename T>
 constexpr int kHeadsPerLane = 16 / sizeof(T) / 2;
-constexpr int kWarpsWanted = 24;  // an SM, before a warp takes all heads of a row
+constexpr int kWarpsWanted = 48;  // an SM, before a warp takes all heads of a row
 constexpr int kReadThreads = 256;
 constexpr int kReadRows = 32;
 
@@ -146,7 +147,7 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
     const int groups = 32 / lanes_per_head, group = lane / lanes_per_head;
     const int chunk = lane % lanes_per_head;
     const int H = a.heads[0] + a.heads[1] + a.heads[2], step = groups * kHeads;
-    const int per = ((H + step - 1) / step + parts - 1) / parts * step;  // heads of a part
+    const int per = ((H + step - 1) / step + parts - 1) / parts * step;  // heads a part
     const int begin = part * per, end = min(begin + per, H);
     const bool has = chunk * 8 < D;  // a lane past a head that is not a power of two
 
@@ -163,29 +164,33 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
         at1 = turned ? at0 + R / 2 : R + (D - R) / 2 + rest;
     }
 
-    // the heads of one step, as they lie in memory
+    // the heads of one step of a kind, as they lie in memory
     Raw raw[kHeads][2];
-    auto kind_of = [&](int h) { return h < a.heads[0] ? 0 : (h < a.heads[0] + a.heads[1] ? 1 : 2); };
-    auto head_of = [&](int h, int kind) {
-        return h - (kind > 0 ? a.heads[0] : 0) - (kind > 1 ? a.heads[1] : 0);
-    };
-    auto fetch = [&](int h0) {
+    auto fetch = [&](const T *p, int h, int last) {
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            const int h = h0 + i * groups + group;
-            if (h < end && has) {
-                const int kind = kind_of(h);
-                const T *p = static_cast<const T *>(a.in[kind]) + row * a.ld_in[kind] +
-                             head_of(h, kind) * D;
+        for (int i = 0; i < kHeads; ++i, p += groups * D, h += groups) {
+            raw[i][0] = raw[i][1] = Raw{};
+            if (h < last && has) {
                 raw[i][0] = *reinterpret_cast<const Raw *>(p + at0);
                 raw[i][1] = *reinterpret_cast<const Raw *>(p + at1);
-            } else {
-                raw[i][0] = raw[i][1] = Raw{};
             }
         }
     };
+    // the part's heads of a kind: [from, to), and where the group's first lies
+    auto from = [&](int kind) {
+        const int before = kind == 0 ? 0 : (kind == 1 ? a.heads[0] : a.heads[0] + a.heads[1]);
+        return max(begin - before, 0);
+    };
+    auto to = [&](int kind) {
+        const int before = kind == 0 ? 0 : (kind == 1 ? a.heads[0] : a.heads[0] + a.heads[1]);
+        return min(end - before, a.heads[kind]);
+    };
+    auto source = [&](int kind) {
+        return static_cast<const T *>(a.in[kind]) + row * a.ld_in[kind] + (from(kind) + group) * D;
+    };
     if (begin >= end) return;
-    fetch(begin);
+    const int kind0 = begin < a.heads[0] ? 0 : (begin < a.heads[0] + a.heads[1] ? 1 : 2);
+    fetch(source(kind0), from(kind0) + group, to(kind0));
     const int total = a.totals ? __ldg(a.totals) : a.max_rows;
     const int r = a.req ? __ldg(a.req + row) : 0;
     const int position = a.pos ? __ldg(a.pos + row) : 0;
@@ -198,104 +203,125 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
         page = kv_page(a.cache, r, place, &token);
         if (page < 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
     }
-    float c[4], s[4];
-    if (turned && angle) {
+    // (a, b) -> (a c - b s, b c + a s), two elements an instruction: of the lane's four
+    // pairs of elements the cosines, and the sines that the partners come with
+    float2 cos2[4], sin2[4];
+    turned = turned && angle;
+    if (turned) {
         const float *cs = a.cos_sin + (long long)position * R + chunk * 4;
-        Four<float>::unpack(__ldg(reinterpret_cast<const float4 *>(cs)), c);
-        Four<float>::unpack(__ldg(reinterpret_cast<const float4 *>(cs + R / 2)), s);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] = 1.0f, s[e] = 0.0f;
-    }
-
-    for (int h0 = begin; h0 < end; h0 += step) {
-        Raw now[kHeads][2];
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) now[i][0] = raw[i][0], now[i][1] = raw[i][1];
-        if (h0 + step < end) fetch(h0 + step);
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            // the shuffles are the whole warp's: every lane goes through them
-            const int h = h0 + i * groups + group;
-            const bool in = h < end && has;
-            const int kind = kind_of(h), head = head_of(h, kind);
-            float y[8];
-            Four<T>::unpack(now[i][0], y);
-            Four<T>::unpack(now[i][1], y + 4);
-            if (a.weight[0] || a.weight[1]) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-                for (int o = lanes_per_head >> 1; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
-                const T *w = kind < 2 ? static_cast<const T *>(a.weight[kind]) : nullptr;
-                if (w && in) {
-                    const float inv = rsqrtf(ss / (float)D + a.eps);
-                    float g[8];
-                    Four<T>::unpack(__ldg(reinterpret_cast<const Raw *>(w + at0)), g);
-                    Four<T>::unpack(__ldg(reinterpret_cast<const Raw *>(w + at1)), g + 4);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = y[e] * inv * g[e];
-                }
-            }
-            if (turned && kind < 2) {
-                if (a.interleaved) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float u = y[2 * e], v = y[2 * e + 1];
-                        y[2 * e] = u * c[e] - v * s[e];
-                        y[2 * e + 1] = v * c[e] + u * s[e];
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float u = y[e], v = y[e + 4];
-                        y[e] = u * c[e] - v * s[e];
-                        y[e + 4] = v * c[e] + u * s[e];
-                    }
-                }
-            }
-            if (!kCache || kind == 0) {
-                if (in && angle) {
-                    T *p = static_cast<T *>(a.out[kind]) + row * a.ld_out[kind] + head * D;
-                    *reinterpret_cast<Raw *>(p + at0) = Four<T>::pack(y);
-                    *reinterpret_cast<Raw *>(p + at1) = Four<T>::pack(y + 4);
-                }
-                if (!kCache) continue;
-            }
-            if constexpr (kCache) {
-                const bool write = in && page >= 0 && (kind == 2 || (kind == 1 && angle));
-                unsigned char *base = kind == 1 ? a.cache.k : a.cache.v;
-                const long long to = kv_offset(a.cache, page, token, head);
-                if constexpr (std::is_same<C, e4m3>::value) {
-                    if (!__any_sync(kFullMask, kind > 0 && h < end)) continue;
-                    unsigned m = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(y[e]) & 0x7FFFFFFFu);
-                    for (int o = lanes_per_head >> 1; o; o >>= 1)
-                        m = max(m, __shfl_xor_sync(kFullMask, m, o));
-                    if (write) {
-                        const float scale = e4m3_scale(m);
-                        unsigned codes[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            codes[e] = e4m3_pair(__fdiv_rn(y[2 * e], scale), __fdiv_rn(y[2 * e + 1], scale));
-                        *reinterpret_cast<unsigned *>(base + to + at0) = codes[0] | codes[1] << 16;
-                        *reinterpret_cast<unsigned *>(base + to + at1) = codes[2] | codes[3] << 16;
-                        if (chunk == 0) {
-                            (kind == 1 ? a.cache.k_scale
-                                       : a.cache.v_scale)[kv_scale_offset(a.cache, page, token, head)] = scale;
-                            if (m >= 0x7F800000u) flag(a.status, DSPARK_STATUS_BAD_INPUT);
-                        }
-                    }
-                } else if (write && kind > 0) {
-                    using Stored = typename Four<C>::Raw;
-                    C *p = reinterpret_cast<C *>(base) + to;
-                    *reinterpret_cast<Stored *>(p + at0) = Four<C>::pack(y);
-                    *reinterpret_cast<Stored *>(p + at1) = Four<C>::pack(y + 4);
-                }
-            }
+        const float4 c = __ldg(reinterpret_cast<const float4 *>(cs));
+        const float4 s = __ldg(reinterpret_cast<const float4 *>(cs + R / 2));
+        if (a.interleaved) {
+            cos2[0] = make_float2(c.x, c.x), cos2[1] = make_float2(c.y, c.y);
+            cos2[2] = make_float2(c.z, c.z), cos2[3] = make_float2(c.w, c.w);
+            sin2[0] = make_float2(-s.x, s.x), sin2[1] = make_float2(-s.y, s.y);
+            sin2[2] = make_float2(-s.z, s.z), sin2[3] = make_float2(-s.w, s.w);
+        } else {
+            cos2[0] = cos2[2] = make_float2(c.x, c.y), cos2[1] = cos2[3] = make_float2(c.z, c.w);
+            sin2[0] = make_float2(-s.x, -s.y), sin2[1] = make_float2(-s.z, -s.w);
+            sin2[2] = make_float2(s.x, s.y), sin2[3] = make_float2(s.z, s.w);
         }
     }
+
+    // queries, keys and values one kind after the other, each its own code
+    auto run = [&](auto kind_c) {
+        constexpr int kKind = decltype(kind_c)::value;
+        const int first = from(kKind), last = to(kKind);
+        if (first >= last) return;
+        const T *in = source(kKind);
+        if (kKind != kind0) fetch(in, first + group, last);
+        T *out = nullptr;
+        if (kKind < 2 && (!kCache || kKind == 0))
+            out = static_cast<T *>(a.out[kKind < 2 ? kKind : 0]) + row * a.ld_out[kKind < 2 ? kKind : 0] +
+                  (first + group) * D;
+        const T *weight = kKind < 2 ? static_cast<const T *>(a.weight[kKind < 2 ? kKind : 0]) : nullptr;
+        float2 w[4];
+        if (weight && has) {
+            Four<T>::unpack(__ldg(reinterpret_cast<const Raw *>(weight + at0)), reinterpret_cast<float *>(w));
+            Four<T>::unpack(__ldg(reinterpret_cast<const Raw *>(weight + at1)), reinterpret_cast<float *>(w + 2));
+        }
+        [[maybe_unused]] unsigned char *stored = kKind == 1 ? a.cache.k : a.cache.v;
+        [[maybe_unused]] float *scales = kKind == 1 ? a.cache.k_scale : a.cache.v_scale;
+        long long slot = kv_offset(a.cache, page, token, first + group);
+        long long scale_slot = kv_scale_offset(a.cache, page, token, first + group);
+        for (int h0 = first + group; h0 - group < last; h0 += step) {
+            Raw now[kHeads][2];
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) now[i][0] = raw[i][0], now[i][1] = raw[i][1];
+            in += step * D;
+            if (h0 - group + step < last) fetch(in, h0 + step, last);
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                // the shuffles are the whole warp's: every lane goes through them
+                const bool mine = h0 + i * groups < last && has;
+                float2 y[4];
+                Four<T>::unpack(now[i][0], reinterpret_cast<float *>(y));
+                Four<T>::unpack(now[i][1], reinterpret_cast<float *>(y + 2));
+                if (kKind < 2 && weight) {
+                    float2 sum = mul2(y[0], y[0]);
+#pragma unroll
+                    for (int e = 1; e < 4; ++e) sum = fma2(y[e], y[e], sum);
+                    float ss = sum.x + sum.y;
+                    for (int o = lanes_per_head >> 1; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+                    const float inv = rsqrtf(ss / (float)D + a.eps);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], make_float2(inv, inv)), w[e]);
+                }
+                if (kKind < 2 && turned) {
+                    float2 z[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 other = a.interleaved ? make_float2(y[e].y, y[e].x) : y[e ^ 2];
+                        z[e] = fma2(y[e], cos2[e], mul2(other, sin2[e]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = z[e];
+                }
+                const float *x = reinterpret_cast<const float *>(y);
+                if (kKind < 2 && (!kCache || kKind == 0)) {
+                    if (mine && angle) {
+                        T *p = out + i * groups * D;
+                        *reinterpret_cast<Raw *>(p + at0) = Four<T>::pack(x);
+                        *reinterpret_cast<Raw *>(p + at1) = Four<T>::pack(x + 4);
+                    }
+                } else if constexpr (kCache) {
+                    const bool write = mine && page >= 0 && (kKind == 2 || angle);
+                    const long long at = slot + (long long)i * groups * a.cache.head_stride;
+                    if constexpr (std::is_same<C, e4m3>::value) {
+                        unsigned m = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+                        for (int o = lanes_per_head >> 1; o; o >>= 1)
+                            m = max(m, __shfl_xor_sync(kFullMask, m, o));
+                        if (write) {
+                            const float scale = e4m3_scale(m);
+                            unsigned codes[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                codes[e] = e4m3_pair(__fdiv_rn(y[e].x, scale), __fdiv_rn(y[e].y, scale));
+                            *reinterpret_cast<unsigned *>(stored + at + at0) = codes[0] | codes[1] << 16;
+                            *reinterpret_cast<unsigned *>(stored + at + at1) = codes[2] | codes[3] << 16;
+                            if (chunk == 0) {
+                                scales[scale_slot + (long long)i * groups * a.cache.page_size] = scale;
+                                if (m >= 0x7F800000u) flag(a.status, DSPARK_STATUS_BAD_INPUT);
+                            }
+                        }
+                    } else if (write) {
+                        using Stored = typename Four<C>::Raw;
+                        C *p = reinterpret_cast<C *>(stored) + at;
+                        *reinterpret_cast<Stored *>(p + at0) = Four<C>::pack(x);
+                        *reinterpret_cast<Stored *>(p + at1) = Four<C>::pack(x + 4);
+                    }
+                }
+            }
+            if (out) out += step * D;
+            slot += (long long)step * a.cache.head_stride;
+            scale_slot += (long long)step * a.cache.page_size;
+        }
+    };
+    run(std::integral_constant<int, 0>{});
+    run(std::integral_constant<int, 1>{});
+    if constexpr (kCache) run(std::integral_constant<int, 2>{});
 }
 
 // Any layout: one warp a (row, head).  Every element and its rotation partner
