@@ -28,7 +28,7 @@
 
 namespace dspark {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 // heads a lane group has in flight: 64 bytes a lane
 template <typename T>
 constexpr int kHeadsPerLane = 16 / sizeof(T) / 2;
@@ -132,9 +132,8 @@ __device__ __forceinline__ bool row_angle(const AppendArgs &a, int row, int *p) 
     return ok;
 }
 
-template <typename T, typename C>
-__global__ void __launch_bounds__(kAppendThreads, 3)
-append_kernel(AppendArgs a, int lanes_per_head, int parts) {
+template <typename T, typename C, int kLanes>
+__global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(AppendArgs a, int parts) {
     constexpr bool kCache = !std::is_same<C, NoCache>::value;
     constexpr int kHeads = kHeadsPerLane<T>;
     using Raw = typename Four<T>::Raw;
@@ -144,9 +143,9 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
     const unsigned unit = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const int row = unit / (unsigned)parts, part = unit - row * parts;
     if (row >= a.max_rows) return;
-    const int groups = 32 / lanes_per_head, group = lane / lanes_per_head;
-    const int chunk = lane % lanes_per_head;
-    const int H = a.heads[0] + a.heads[1] + a.heads[2], step = groups * kHeads;
+    constexpr int groups = 32 / kLanes, step = groups * kHeads;  // kLanes lanes a head
+    const int group = lane / kLanes, chunk = lane % kLanes;
+    const int H = a.heads[0] + a.heads[1] + a.heads[2];
     const int per = ((H + step - 1) / step + parts - 1) / parts * step;  // heads a part
     const int begin = part * per, end = min(begin + per, H);
     const bool has = chunk * 8 < D;  // a lane past a head that is not a power of two
@@ -168,11 +167,11 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
     Raw raw[kHeads][2];
     auto fetch = [&](const T *p, int h, int last) {
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i, p += groups * D, h += groups) {
+        for (int i = 0; i < kHeads; ++i) {
             raw[i][0] = raw[i][1] = Raw{};
-            if (h < last && has) {
-                raw[i][0] = *reinterpret_cast<const Raw *>(p + at0);
-                raw[i][1] = *reinterpret_cast<const Raw *>(p + at1);
+            if (h + i * groups < last && has) {
+                raw[i][0] = *reinterpret_cast<const Raw *>(p + i * groups * D);
+                raw[i][1] = *reinterpret_cast<const Raw *>(p + i * groups * D + (at1 - at0));
             }
         }
     };
@@ -186,7 +185,7 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
         return min(end - before, a.heads[kind]);
     };
     auto source = [&](int kind) {
-        return static_cast<const T *>(a.in[kind]) + row * a.ld_in[kind] + (from(kind) + group) * D;
+        return static_cast<const T *>(a.in[kind]) + row * a.ld_in[kind] + (from(kind) + group) * D + at0;
     };
     if (begin >= end) return;
     const int kind0 = begin < a.heads[0] ? 0 : (begin < a.heads[0] + a.heads[1] ? 1 : 2);
@@ -224,6 +223,7 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
     }
 
     // queries, keys and values one kind after the other, each its own code
+    const float share = 1.0f / (float)D;
     auto run = [&](auto kind_c) {
         constexpr int kKind = decltype(kind_c)::value;
         const int first = from(kKind), last = to(kKind);
@@ -233,7 +233,7 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
         T *out = nullptr;
         if (kKind < 2 && (!kCache || kKind == 0))
             out = static_cast<T *>(a.out[kKind < 2 ? kKind : 0]) + row * a.ld_out[kKind < 2 ? kKind : 0] +
-                  (first + group) * D;
+                  (first + group) * D + at0;
         const T *weight = kKind < 2 ? static_cast<const T *>(a.weight[kKind < 2 ? kKind : 0]) : nullptr;
         float2 w[4];
         if (weight && has) {
@@ -262,8 +262,9 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
 #pragma unroll
                     for (int e = 1; e < 4; ++e) sum = fma2(y[e], y[e], sum);
                     float ss = sum.x + sum.y;
-                    for (int o = lanes_per_head >> 1; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
-                    const float inv = rsqrtf(ss / (float)D + a.eps);
+#pragma unroll
+                    for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+                    const float inv = rsqrtf(fmaf(ss, share, a.eps));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) y[e] = mul2(mul2(y[e], make_float2(inv, inv)), w[e]);
                 }
@@ -281,8 +282,8 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
                 if (kKind < 2 && (!kCache || kKind == 0)) {
                     if (mine && angle) {
                         T *p = out + i * groups * D;
-                        *reinterpret_cast<Raw *>(p + at0) = Four<T>::pack(x);
-                        *reinterpret_cast<Raw *>(p + at1) = Four<T>::pack(x + 4);
+                        *reinterpret_cast<Raw *>(p) = Four<T>::pack(x);
+                        *reinterpret_cast<Raw *>(p + (at1 - at0)) = Four<T>::pack(x + 4);
                     }
                 } else if constexpr (kCache) {
                     const bool write = mine && page >= 0 && (kKind == 2 || angle);
@@ -291,7 +292,8 @@ append_kernel(AppendArgs a, int lanes_per_head, int parts) {
                         unsigned m = 0;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-                        for (int o = lanes_per_head >> 1; o; o >>= 1)
+#pragma unroll
+                        for (int o = kLanes / 2; o; o >>= 1)
                             m = max(m, __shfl_xor_sync(kFullMask, m, o));
                         if (write) {
                             const float scale = e4m3_scale(m);
@@ -499,8 +501,10 @@ cudaError_t launch_append(const AppendArgs &a, bool vec, cudaStream_t stream) {
         const int parts = (int)max(1ll, min((long long)steps, want / a.max_rows));
         const long long grid = ((long long)a.max_rows * parts + kWarps - 1) / kWarps;
         if (grid > 0x7FFFFFFF / kWarps) return cudaErrorInvalidConfiguration;
-        return launch_pdl(append_kernel<T, C>, dim3((unsigned)grid), dim3(kAppendThreads), 0,
-                          stream, a, lanes, parts);
+        return launch_pdl(lanes == 8    ? append_kernel<T, C, 8>
+                          : lanes == 16 ? append_kernel<T, C, 16>
+                                        : append_kernel<T, C, 32>,
+                          dim3((unsigned)grid), dim3(kAppendThreads), 0, stream, a, parts);
     }
     const long long grid = ((long long)a.max_rows * H + kWarps - 1) / kWarps;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
