@@ -365,6 +365,12 @@ __device__ __forceinline__ void split_pair(float x0, float x1, unsigned *hi, uns
     *lo = e4m3_pair(x0 - h.x, x1 - h.y);
 }
 
+// Two E4M3 codes, in the low half of a word, as halves: exact.
+__device__ __forceinline__ uint32_t two_halves(unsigned codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+    return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+
 // Where 16-byte chunk c of row r lies in rows of `row_bytes` (64 or 128) under the
 // swizzle of that width.
 template <int kRowBytes>
@@ -739,12 +745,6 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         // --------------------------------------------- converting warps
         if constexpr (kQuant) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-            // A value's code becomes a half of 2^-8 times its size by moving its bits:
-            // both formats have the same digits of exponent below the sign up to the
-            // bias (7 and 15), subnormals included.  Of a word's four codes the first
-            // and third end up side by side, then the second and fourth: columns
-            // 4i + 1 and 4i + 2 of the output change places, and change back at the
-            // end, with the 2^8.
             constexpr int kUnits = D / 16;  // 16 codes a thread and step
             constexpr int kSteps = kTile * kUnits / 128;
             const int ct = tid - 128;
@@ -845,34 +845,21 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     const unsigned char *src = smem + S::kStageAt + stage * S::kBufBytes;
                     unsigned char *dst = smem + S::kOpAt + b * S::kOpBytes;
                     const int p0 = (s.first + i) * kTile;
-                    bool plain = p0 + kTile <= s.q.P && !*(volatile int *)&sc.odd[b];
-                    if (plain) {
-                        __half2 most_h = __float2half2_rn(0.0f);
+                    if (p0 + kTile <= s.q.P && !*(volatile int *)&sc.odd[b]) {
                         const unsigned char *from = src + ct * 16;
                         unsigned char *to = smem + b * S::kOpBytes;
 #pragma unroll 1
                         for (int k = 0; k < kSteps; ++k) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(from);
-                            const unsigned w[4] = {v.x, v.y, v.z, v.w};
-                            uint32_t g[8];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                g[2 * e] = (w[e] << 7 & 0x3F803F80u) | (w[e] << 8 & 0x80008000u);
-                                g[2 * e + 1] = (w[e] >> 1 & 0x3F803F80u) | (w[e] & 0x80008000u);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                most_h = __hmax2(most_h, __habs2(*reinterpret_cast<__half2 *>(&g[e])));
-                            const uint4 lo = make_uint4(g[0], g[1], g[2], g[3]), hi = make_uint4(g[4], g[5], g[6], g[7]);
-                            *reinterpret_cast<uint4 *>(to + first) = flip ? hi : lo;
-                            *reinterpret_cast<uint4 *>(to + last) = flip ? lo : hi;
+                            const uint2 v0 = *reinterpret_cast<const uint2 *>(from + flip * 8);
+                            const uint2 v1 = *reinterpret_cast<const uint2 *>(from + 8 - flip * 8);
+                            *reinterpret_cast<uint4 *>(to + first) =
+                                make_uint4(two_halves(v0.x), two_halves(v0.x >> 16), two_halves(v0.y), two_halves(v0.y >> 16));
+                            *reinterpret_cast<uint4 *>(to + last) =
+                                make_uint4(two_halves(v1.x), two_halves(v1.x >> 16), two_halves(v1.y), two_halves(v1.y >> 16));
                             from += 2048;
                             to += 128 / kUnits * 128;
                         }
-                        // a code of all ones, which is NaN, has become 1.875: the largest
-                        plain = __all_sync(kFullMask, __low2float(most_h) < 1.875f && __high2float(most_h) < 1.875f);
-                    }
-                    if (!plain) {
+                    } else {
                         // Scales that are not plain numbers (or negative) go into the
                         // values; values past the request's end become zeros, and so
                         // do NaN and infinities of the window, which the rows that see
@@ -881,25 +868,21 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         for (int k = ct; k < kTile * kUnits; k += 128) {
                             const int tok = k / kUnits, pos = p0 + tok;
                             const float f = sc.v[b][tok];
-                            const float g = f - f == 0.0f ? copysignf(0x1p-8f, f) : f;
+                            const float g = f - f == 0.0f ? copysignf(1.0f, f) : f;
                             bool bad = false;
 #pragma unroll 1
-                            for (int e = 0; e < 4; ++e) {
-                                const unsigned w = reinterpret_cast<const unsigned *>(src + k * 16)[e];
-                                float x[4];
+                            for (int e = 0; e < 8; ++e) {
+                                const unsigned w = reinterpret_cast<const unsigned short *>(src + k * 16)[e];
+                                float x[2] = {e4m3_value(w & 0xFF) * g, e4m3_value(w >> 8) * g};
 #pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    x[y] = e4m3_value(w >> 8 * y & 0xFF) * g;
+                                for (int y = 0; y < 2; ++y) {
                                     if (pos >= n) x[y] = 0.0f;
                                     if (pos >= s.q.P && !(x[y] - x[y] == 0.0f)) x[y] = 0.0f, bad = true;
                                 }
-                                const __half2 even = __floats2half2_rn(x[0], x[2]);
-                                const __half2 odd = __floats2half2_rn(x[1], x[3]);
+                                const __half2 two = __floats2half2_rn(x[0], x[1]);
                                 unsigned char *row = dst + k % kUnits / 4 * kHalfBytes + tok * 128;
-                                const int ch = k % kUnits % 4 * 2 + e / 2;
-                                *reinterpret_cast<uint2 *>(row + ((ch ^ (tok & 7)) << 4) + (e & 1) * 8) =
-                                    make_uint2(*reinterpret_cast<const uint32_t *>(&even),
-                                               *reinterpret_cast<const uint32_t *>(&odd));
+                                const int ch = k % kUnits % 4 * 2 + e / 4;
+                                *reinterpret_cast<__half2 *>(row + ((ch ^ (tok & 7)) << 4) + e % 4 * 4) = two;
                             }
                             if (bad) atomicOr(&ctl.nonfinite[seg & 3], 1u << (pos - s.q.P));
                         }
@@ -1166,16 +1149,6 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     uint32_t o[32];
                     tmem_load32(lanes + 2 * kTile + h * 32, o);
                     tmem_wait_load(o);
-                    if constexpr (kQuant) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const uint32_t second = o[j + 1];
-                            o[j + 1] = o[j + 2];
-                            o[j + 2] = second;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * 256.0f);
-                    }
                     for (unsigned e = extra; e; e &= e - 1) {
                         int tok;
                         const int page = kv_page(a.cache, s.r, (long long)s.q.P + __ffs(e) - 1, &tok);
