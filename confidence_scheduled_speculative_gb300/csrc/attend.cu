@@ -204,8 +204,9 @@ struct TensorShape {
     static constexpr int kOpAt = kStageAt + kStages * kBufBytes;
     static constexpr int kControl = kOpAt + (kQuant ? 2 * kOpBytes : 0);
     static constexpr int kTotal = kControl + (kQuant ? 5120 : 1024);
-    static constexpr int kCopyWarp = kQuant ? 8 : 4, kMatrixWarp = kCopyWarp + 1, kScaleWarp = 10;
-    static constexpr int kThreads = kQuant ? 384 : 192;
+    static constexpr int kCopyWarp = kQuant ? 8 : 4;
+    static constexpr int kScoreWarp = kCopyWarp + 1, kValueWarp = kCopyWarp + 2, kScaleWarp = 11;
+    static constexpr int kThreads = kQuant ? 384 : 224;
     static constexpr int kJobCost = 2;  // of a job's begin and end, in tiles
     static_assert(kTotal <= 113 * 1024, "two CTAs an SM");
 };
@@ -216,7 +217,7 @@ struct TensorShape {
 struct alignas(16) Control {
     unsigned long long full[9], empty[9], stage_full[6], stage_empty[6], op_full[2], op_empty[2];
     unsigned long long s_full[2], p_ready[2], o_done[2], scales[2];
-    unsigned long long q_raw[2], q_full[2], q_empty[2], drain;
+    unsigned long long q_raw[2], q_full[2], q_empty[2], drain[2];
     unsigned tmem;
     unsigned nonfinite[4];  // window tokens whose values were zeroed, by segment
     int abort;
@@ -407,7 +408,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             mbar_init(smem_addr(&ctl.stage_empty[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&ctl.s_full[i]), 1);
+            mbar_init(smem_addr(&ctl.s_full[i]), kQuant ? 2 : 1);  // the product; the scales
             mbar_init(smem_addr(&ctl.p_ready[i]), 4);
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
             mbar_init(smem_addr(&ctl.scales[i]), 1);
@@ -416,8 +417,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             mbar_init(smem_addr(&ctl.q_raw[i]), 1);
             mbar_init(smem_addr(&ctl.q_full[i]), 4);
             mbar_init(smem_addr(&ctl.q_empty[i]), 1);
+            mbar_init(smem_addr(&ctl.drain[i]), 1);
         }
-        mbar_init(smem_addr(&ctl.drain), 1);
         ctl.abort = 0;
         for (int i = 0; i < 4; ++i) ctl.nonfinite[i] = 0;
         fence_mbar_init();
@@ -426,7 +427,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         prefetch_map(&map_q);
         prefetch_map(&map_few);
     }
-    if (warp == S::kMatrixWarp) tmem_alloc(smem_addr(&ctl.tmem), kTmemCols);
+    if (warp == S::kScoreWarp) tmem_alloc(smem_addr(&ctl.tmem), kTmemCols);
     pdl_wait();
     pdl_trigger();
 
@@ -444,7 +445,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     const int cta = blockIdx.x;
     if (tid == 0) t.desc[cta * kDescInts] = 0;
     if (cta >= n_ctas) {
-        if (warp == S::kMatrixWarp) {
+        if (warp == S::kScoreWarp) {
             __syncwarp();
             tmem_free(*(volatile unsigned *)&ctl.tmem, kTmemCols);
         }
@@ -577,20 +578,16 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 for (unsigned i = seg > 2 ? seg - 2 : 0; i < seg; ++i)
                     mbar_wait(smem_addr(&ctl.q_raw[i & 1]), i >> 1 & 1);
             }
-        } else if (warp == S::kMatrixWarp) {
-            // ------------------------------------------ matrix warp
-            // The whole warp keeps step, so that addresses stay in uniform
-            // registers; one lane issues.
-            // over E4M3: codes times the queries' two parts, then halves
-            constexpr uint32_t word_qk = kQuant ? mma_word_e4m3(kTile) : mma_word(true, kTile, false);
-            constexpr uint32_t word_pv = mma_word(!kQuant, D, true);
-            constexpr int kKeyRow = kQuant ? D : 128;  // bytes of a row of the first product
+        } else if (warp == S::kScoreWarp || warp == S::kValueWarp) {
+            // ---------------------------------------- matrix warps
+            // One issues the products of queries and keys, the other those of weights
+            // and values: issuing a tile's products, with the waits before and the
+            // commits behind them, takes one warp longer than the products take.  Each
+            // warp keeps step as a whole, so that addresses stay in uniform registers;
+            // one lane issues.
+            const bool scores = warp == S::kScoreWarp;
             const uint32_t ubase = __shfl_sync(kFullMask, base, 0);
             const uint32_t utmem = __shfl_sync(kFullMask, tmem, 0);
-            const uint64_t desc_q = smem_operand(ubase, 16, kKeyRow);
-            const uint64_t desc_k = smem_operand(ubase + S::kQBytes, 16, kKeyRow);
-            const uint64_t desc_v = smem_operand(ubase + (kQuant ? S::kOpAt : S::kQBytes), kHalfBytes, 128);
-            unsigned long long *queries = kQuant ? ctl.q_full : ctl.q_raw;
             const bool leader = elect_one();
             unsigned done = 0, seg = 0;  // tiles and segments so far
             bool ok = true;
@@ -598,16 +595,27 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
                 return ok = __all_sync(kFullMask, ok);
             };
-            while (ok && walk.next(t, &s)) {
-                if (!wait(queries + (seg & 1), seg >> 1)) break;
-                const bool few = few_rows(s);
-                const uint64_t queries_at = desc_q + (q_offset(s, seg) >> 4);
-                // their second parts, over E4M3
-                const unsigned part = (D == 64 && few ? 4096 : S::kQBytes / 2) >> 4;
-                const int count = __shfl_sync(kFullMask, s.count, 0);
-                for (int i = 0; i <= count && ok; ++i) {
-                    if (i < count) {
-                        // scores of tile i, in the place of the weights of tile i - 2
+            // over E4M3 keys have a ring of their own; else the loads lie in one, K0, K1,
+            // V0, K2, V1, ..., V(n-1)
+            auto skip = [&](int n) {
+                for (; n > 0; --n) ring_at.step(S::kBufs);
+            };
+            if (scores) {
+                // over E4M3: codes times the queries' two parts
+                constexpr uint32_t word = kQuant ? mma_word_e4m3(kTile) : mma_word(true, kTile, false);
+                constexpr int kKeyRow = kQuant ? D : 128;  // bytes of a row
+                const uint64_t desc_q = smem_operand(ubase, 16, kKeyRow);
+                const uint64_t desc_k = smem_operand(ubase + S::kQBytes, 16, kKeyRow);
+                unsigned long long *queries = kQuant ? ctl.q_full : ctl.q_raw;
+                while (ok && walk.next(t, &s)) {
+                    if (!wait(queries + (seg & 1), seg >> 1)) break;
+                    const bool few = few_rows(s);
+                    const uint64_t queries_at = desc_q + (q_offset(s, seg) >> 4);
+                    // their second parts, over E4M3
+                    const unsigned part = (D == 64 && few ? 4096 : S::kQBytes / 2) >> 4;
+                    const int count = __shfl_sync(kFullMask, s.count, 0);
+                    for (int i = 0; i < count; ++i) {
+                        // in the place of the weights of tile - 2
                         const unsigned tile = done + i;
                         if (tile > 1 && !wait(&ctl.o_done[tile & 1], (tile - 2) >> 1)) break;
                         if (!wait(&ctl.full[ring_at.slot], ring_at.parity)) break;
@@ -619,22 +627,31 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
                                 for (int k = 0; k < D / 16; ++k)  // 32 codes a step, for either part
                                     mma_ss_e4m3(d, queries_at + k % 2 * part + (k / 2 * 32 >> 4),
-                                                buf + (k / 2 * 32 >> 4), word_qk, k > 0);
+                                                buf + (k / 2 * 32 >> 4), word, k > 0);
                             } else {
 #pragma unroll
                                 for (int k = 0; k < D / 16; ++k)
                                     mma_ss(d, queries_at + ((k / 4 * kRowsPerTile * 128 + k % 4 * 32) >> 4),
-                                           buf + ((k / 4 * kHalfBytes + k % 4 * 32) >> 4), word_qk, k > 0);
+                                           buf + ((k / 4 * kHalfBytes + k % 4 * 32) >> 4), word, k > 0);
                             }
                             mma_commit(smem_addr(&ctl.s_full[tile & 1]));
                             mma_commit(smem_addr(&ctl.empty[ring_at.slot]));
                             if (i + 1 == count) mma_commit(smem_addr(&ctl.q_empty[seg & 1]));
                         }
                         __syncwarp();
-                        ring_at.step(S::kBufs);
+                        skip(kQuant ? 1 : (i == 0 ? 1 : 2) + (i + 1 == count));
                     }
-                    if (i > 0) {
-                        const unsigned tile = done + i - 1;
+                    done += count;
+                    ++seg;
+                }
+            } else {
+                constexpr uint32_t word = mma_word(!kQuant, D, true);
+                const uint64_t desc_v = smem_operand(ubase + (kQuant ? S::kOpAt : S::kQBytes), kHalfBytes, 128);
+                while (ok && walk.next(t, &s)) {
+                    const int count = __shfl_sync(kFullMask, s.count, 0);
+                    if (!kQuant) skip(count > 1 ? 2 : 1);
+                    for (int i = 0; i < count; ++i) {
+                        const unsigned tile = done + i;
                         const unsigned slot = kQuant ? tile & 1 : ring_at.slot;
                         if (!wait(kQuant ? &ctl.op_full[slot] : &ctl.full[slot],
                                   kQuant ? tile >> 1 : ring_at.parity))
@@ -646,23 +663,22 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         if (leader) {
 #pragma unroll
                             for (int k = 0; k < kTile / 16; ++k)
-                                mma_ts(utmem + 2 * kTile, w + k * 8, buf + (k * 16 * 128 >> 4), word_pv,
-                                       i > 1 || k > 0);
+                                mma_ts(utmem + 2 * kTile, w + k * 8, buf + (k * 16 * 128 >> 4), word,
+                                       i > 0 || k > 0);
                             mma_commit(smem_addr(&ctl.o_done[tile & 1]));
                             mma_commit(smem_addr(kQuant ? &ctl.op_empty[slot] : &ctl.empty[slot]));
                         }
                         __syncwarp();
-                        if (!kQuant) ring_at.step(S::kBufs);
+                        if (!kQuant) skip(i + 2 < count ? 2 : 1);
                     }
+                    done += count;
                 }
-                done += count;
-                ++seg;
             }
             // after a timeout: products still under way write tensor memory and
             // barriers of this block
             if (!ok && leader) {
-                mma_commit(smem_addr(&ctl.drain));
-                mbar_wait(smem_addr(&ctl.drain), 0);
+                mma_commit(smem_addr(&ctl.drain[scores]));
+                mbar_wait(smem_addr(&ctl.drain[scores]), 0);
             }
             __syncwarp();
         } else if (kQuant && warp == S::kScaleWarp) {
@@ -735,7 +751,10 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         }
                         if (lane == 0) sc.odd[b] = odd;
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_addr(&ctl.scales[b]));
+                        if (lane == 0) {
+                            mbar_arrive(smem_addr(&ctl.s_full[b]));
+                            mbar_arrive(smem_addr(&ctl.scales[b]));
+                        }
                     }
                     done += s.count;
                 }
@@ -949,7 +968,6 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 const int p0 = (s.first + i) * kTile;
                 if (!wait(&ctl.s_full[b], tile >> 1)) break;
                 if (active) {
-                    if (kQuant && !wait(&ctl.scales[b], tile >> 1)) break;
                     tmem_fence_after();
                     const bool prefix_only = p0 + kTile <= s.q.P;
                     // (a loop, not two copies: the warps of a scheduler run several kinds
@@ -960,7 +978,15 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         const int column = 2 * (lane & 3);
                         uint32_t x[32];
                         tmem_load_rows16(at + b * kTile, x);
+                        // (all of the scales' loads before the first use: one after the
+                        // other their latencies are most of a tile's time)
+                        [[maybe_unused]] float2 f1[8], f2[8];
                         if constexpr (kQuant) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                f1[j] = *reinterpret_cast<const float2 *>(&sc.k[b][8 * j + column]);
+                                f2[j] = *reinterpret_cast<const float2 *>(&sc.v_log2[b][8 * j + column]);
+                            }
                             if (i == 0)
 #pragma unroll
                                 for (int k = 0; k < 2; ++k)
@@ -974,12 +1000,10 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             // scores to base 2, plus log2 of the value's scale
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                const float2 ks = *reinterpret_cast<const float2 *>(&sc.k[b][8 * j + column]);
-                                const float2 vs = *reinterpret_cast<const float2 *>(&sc.v_log2[b][8 * j + column]);
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     const float f = now[k].factor;
-                                    const float2 y = fma2(mul2(pair(2 * j + k), make_float2(f, f)), ks, vs);
+                                    const float2 y = fma2(mul2(pair(2 * j + k), make_float2(f, f)), f1[j], f2[j]);
                                     x[4 * j + 2 * k] = __float_as_uint(y.x);
                                     x[4 * j + 2 * k + 1] = __float_as_uint(y.y);
                                 }
@@ -1044,6 +1068,11 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             }
                         }
                         uint32_t w[16];
+                        if constexpr (kQuant) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                f1[j] = *reinterpret_cast<const float2 *>(&sc.v_inv[b][8 * j + column]);
+                        }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const float shift = now[k].mx == -INFINITY ? 0.0f : now[k].mx;
@@ -1053,7 +1082,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                                 if constexpr (kQuant) {
                                     const float2 y = add2(pair(2 * j + k), make_float2(-shift, -shift));
                                     const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                                    sum = fma2(u, *reinterpret_cast<const float2 *>(&sc.v_inv[b][8 * j + column]), sum);
+                                    sum = fma2(u, f1[j], sum);
                                     const __half2 two = __floats2half2_rn(u.x, u.y);
                                     w[2 * j + k] = *reinterpret_cast<const uint32_t *>(&two);
                                 } else {
@@ -1215,7 +1244,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         }
     }
     __syncthreads();
-    if (warp == S::kMatrixWarp) tmem_free(tmem, kTmemCols);
+    if (warp == S::kScoreWarp) tmem_free(tmem, kTmemCols);
 }
 
 // Joins the parts of the jobs that several CTAs share, in the CTAs' order: a block

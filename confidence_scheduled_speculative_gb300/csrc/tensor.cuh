@@ -13,24 +13,24 @@ namespace dspark {
 
 // ------------------------------------------------------------- mbarriers
 
-constexpr int kLooks = 1 << 14, kLookNs = 100000;  // 1.6 s: far beyond any pass
+constexpr int kLooks = 1 << 18;  // a second: far beyond any pass
 
 // Wait for a phase of an mbarrier, for warps that wait on one another inside a
-// block: each look suspends the thread until the phase is over, or for kLookNs.
-// Gives up (false) after kLooks looks, or once another warp of the block has
-// (*abort); whoever gives up first reports the timeout.  Kept to a few instructions:
-// the wait stands in the kernel some thirty times, and all that its warps run in turn
-// has to fit in the instruction cache.
+// block: a look suspends the thread until the phase is over, or for some
+// microseconds.  Gives up (false) after kLooks looks, or once another warp of the
+// block has (*abort); whoever gives up first reports the timeout.  Kept to a few
+// instructions: the wait stands in the kernel some thirty times, and all that its
+// warps run in turn has to fit in the instruction cache.
 __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, volatile int *abort,
                                           int32_t *status) {
 #pragma unroll 1
     for (int left = kLooks;;) {
         uint32_t done;
         asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
             " selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(kLookNs)
+            : "r"(bar), "r"(parity)
             : "memory");
         if (done) return true;
         if (*abort) return false;
