@@ -189,6 +189,8 @@ def library_path() -> str:
 def load() -> ctypes.CDLL:
     """Load libdspark.so; raise if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -218,8 +220,8 @@ def _p(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = "")
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without the object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -633,28 +635,33 @@ class KVCache:
         self.ref = ctypes.byref(self.desc)
 
 
-def _rows(t: torch.Tensor, name: str, dtype, heads=None, dim=None, rows=None) -> tuple[int, int]:
+def _rows(t: torch.Tensor, name: str, dtype, heads: int, dim: int, rows: int) -> tuple[int, int]:
     """Pointer and row stride of [rows, heads, head_dim] rows: heads packed,
     any row stride."""
-    if not t.is_cuda or t.dim() != 3:
+    if t.dim() != 3 or not t.is_cuda:
         raise ValueError(f"{name}: expected a 3-D CUDA tensor [rows, heads, head_dim]")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     n, h, d = t.shape
     ld, sh, sd = t.stride()
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: expected packed heads with unit inner stride")
-    if (heads is not None and h != heads) or (dim is not None and d != dim):
+    if h != heads or d != dim:
         raise ValueError(f"{name}: expected {heads} heads of {dim} elements, got {h} of {d}")
-    if rows is not None and n < rows:
+    if n < rows:
         raise ValueError(f"{name}: expected at least {rows} rows, got {n}")
     return t.data_ptr(), ld if n > 1 else max(ld, h * d)
 
 
 def _index(t, n, name):
-    if t is not None and t.numel() < n:
+    """Pointer of at least n contiguous int32 elements, or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+        return _p(t, torch.int32, name)  # says what is wrong
+    if t.numel() < n:
         raise ValueError(f"{name}: expected at least {n} elements, got {t.numel()}")
-    return _p(t, torch.int32, name)
+    return t.data_ptr()
 
 
 def _norm_rope(dtype, dim, q_weight, k_weight, eps, cos_sin, interleaved):

@@ -175,6 +175,7 @@ constexpr float kLazy = 8.0f;       // log2 of how far weights may grow past 1
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kDescInts = 8;
+constexpr int kWholeTiles = 8;
 
 struct TensorArgs {
     AttendArgs a;
@@ -182,6 +183,7 @@ struct TensorArgs {
     int tokens;  // window tokens a row tile: all their heads in 128 rows
     int few;     // window tokens whose heads fit in 64 rows
     int box;     // cache tokens a TMA box
+    int whole;   // no job is split
     float *part_o;   // [2 kMaxCtas][D / 4][128] float4
     float *part_ml;  // [2 kMaxCtas][2][128]
     int *desc;       // [kMaxCtas][kDescInts]: the split job that begins in a CTA
@@ -254,9 +256,9 @@ __device__ __forceinline__ bool to_request(const TensorArgs &t, const Window &w,
 
 // T units dealt to n CTAs in order, each T / n of them or one more.  A job counts
 // its tiles and, before them, some units for its beginning and end, so that CTAs
-// with many short jobs get fewer tiles.
+// with many short jobs get fewer tiles; where no job is split it is one unit.
 struct Deal {
-    int n, rest;
+    int n, rest;  // below 1024
     long long each;
     __device__ __forceinline__ long long first(int c) const { return c * each + c * rest / n; }
     // the CTA, c or later, that a unit falls to
@@ -298,13 +300,13 @@ struct Walk {
     }
     __device__ __forceinline__ bool next(const TensorArgs &t, Segment *s) {
         while (left > 0) {
-            const int take = min(q.tiles + kJobCost - unit, left);
+            const int take = t.whole ? 1 : min(q.tiles + kJobCost - unit, left);
             s->q = q;
             s->r = r;
             s->head = head;
             s->row_tile = row_tile;
             s->first = max(unit - kJobCost, 0);
-            s->count = max(unit + take - kJobCost, 0) - s->first;
+            s->count = t.whole ? q.tiles : max(unit + take - kJobCost, 0) - s->first;
             left -= take;
             unit = 0;
             if (++row_tile == q.row_tiles) {
@@ -436,14 +438,17 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     const int per = (a.B + kThreads - 1) / kThreads;
     long long mine = 0;
     Request q = {};
-    auto units = [&]() { return (long long)(q.tiles + S::kJobCost) * q.row_tiles * a.cache.n_kv_heads; };
+    auto job_units = [&]() { return t.whole ? 1 : q.tiles + S::kJobCost; };
+    auto units = [&]() { return (long long)job_units() * (q.row_tiles * a.cache.n_kv_heads); };
     for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
         if (to_request(t, load_window(a, r), &q, blockIdx.x == 0)) mine += units();
     long long T;
     const long long before = block_exclusive_scan<long long>(mine, ctl.scan, &T);
-    const int n_ctas = (int)min((long long)gridDim.x, (T + S::kJobCost + 1) / (S::kJobCost + 2));
+    // (a CTA with less than two tiles to do would cost more than it brings)
+    const int n_ctas =
+        (int)min((long long)gridDim.x, t.whole ? T : (T + S::kJobCost + 1) / (S::kJobCost + 2));
     const int cta = blockIdx.x;
-    if (tid == 0) t.desc[cta * kDescInts] = 0;
+    if (tid == 0 && !t.whole) t.desc[cta * kDescInts] = 0;
     if (cta >= n_ctas) {
         if (warp == S::kScoreWarp) {
             __syncwarp();
@@ -453,7 +458,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     }
     Deal deal;
     deal.n = n_ctas;
-    deal.each = T / n_ctas;
+    deal.each = div_nonneg(T, n_ctas);
     deal.rest = (int)(T - deal.each * n_ctas);
     const long long lo = deal.first(cta), hi = deal.first(cta + 1);
     if (lo >= before && lo < before + mine) {
@@ -465,9 +470,9 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 at += units();
                 continue;
             }
-            const int job = (int)((lo - at) / (q.tiles + S::kJobCost));
+            const int job = (int)div_nonneg(lo - at, job_units());
             ctl.start_r = r;
-            ctl.start_unit = (int)(lo - at - (long long)job * (q.tiles + S::kJobCost));
+            ctl.start_unit = (int)(lo - at - (long long)job * job_units());
             ctl.start_head = job / q.row_tiles;
             ctl.start_row_tile = job % q.row_tiles;
             ctl.start_row0 = q.row0;
@@ -1435,10 +1440,13 @@ cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *w
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_tensor_kernel<D, kQuant>),
                                 S::kTotal, kSmemSlot);
     if (e != cudaSuccess) return e;
+    // A split job's parts are joined by a second launch.  Where no request can have more
+    // than kWholeTiles tiles, a job stays whole and that launch is not made.
+    t.whole = (long long)c.table_width * c.page_size <= kWholeTiles * kTile;
     const int grid = min(2 * sm_count(), kMaxCtas);
     e = launch_pdl(attend_tensor_kernel<D, kQuant>, dim3(grid), dim3(S::kThreads), S::kTotal, stream,
                    map_k, map_v, map_q, map_few, t);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || t.whole) return e;
     return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32 * 4), dim3(kJoinWarps * 32), 0, stream, t);
 }
 
