@@ -8,4 +8,4 @@ binding (argument marshalling only); ``workloads`` draws seeded synthetic
 inputs.
 """
 
-__all__ = ["api", "workloads"]
+__all__ = ["api", "decode", "engine", "workloads"]
