@@ -11,7 +11,9 @@
 //   throughout: a CTA a (row, query head), its four warps take every fourth
 //   position, each with a running maximum and sum, joined at the end.
 
+#include "fewrows.cuh"
 #include "kvcache.cuh"
+#include "schedule.cuh"
 #include "tensor.cuh"
 
 #include <atomic>
@@ -21,48 +23,6 @@ namespace dspark {
 
 constexpr int kAnyWarps = 4;
 constexpr int kAnySteps = DSPARK_MAX_HEAD_DIM / 32;
-
-struct AttendArgs {
-    const void *q;
-    long long ld_q;
-    void *out;
-    long long ld_out;
-    float *lse;
-    const int32_t *cu, *prefix;
-    const uint32_t *ancestors;
-    int B, n_q_heads, max_rows;
-    float scale;
-    KvView cache;
-    int32_t *status;
-};
-
-// A request's entries as they are: rows [lo, hi) and the prefix length.
-struct Window {
-    int lo, hi, P;
-};
-
-__device__ __forceinline__ Window load_window(const AttendArgs &a, int r) {
-    return {__ldg(a.cu + r), __ldg(a.cu + r + 1), __ldg(a.prefix + r)};
-}
-
-// Whether a window has rows and can be used; with `report`, flags why not.
-__device__ __forceinline__ bool usable(const AttendArgs &a, const Window &w, bool report) {
-    if (w.hi == w.lo) return false;
-    int bad = 0;
-    if (w.lo < 0 || w.hi < w.lo || w.hi - w.lo > DSPARK_MAX_WINDOW || w.hi > a.max_rows)
-        bad = DSPARK_STATUS_BAD_LEN;
-    else if (w.P < 0 ||
-             (long long)w.P + (w.hi - w.lo) > (long long)a.cache.table_width * a.cache.page_size)
-        bad = DSPARK_STATUS_BAD_INDEX;
-    if (bad && report) flag(a.status, bad);
-    return !bad;
-}
-
-// The window tokens that token i of a window sees, as bits.
-__device__ __forceinline__ unsigned ancestors_of(const AttendArgs &a, int row, int i, int len) {
-    const unsigned all = 0xFFFFFFFFu >> (32 - len);
-    return (a.ancestors ? __ldg(a.ancestors + row) : 0xFFFFFFFFu >> (31 - i)) & all;
-}
 
 template <typename T, typename C>
 __global__ void __launch_bounds__(kAnyWarps * 32) attend_any_kernel(AttendArgs a) {
@@ -167,28 +127,6 @@ cudaError_t launch_any(const AttendArgs &a, int cache_dtype, cudaStream_t stream
 
 // ------------------------------------------------- tensor-core kernel
 
-constexpr int kTile = 64;           // positions a step
-constexpr int kRowsPerTile = 128;   // (token, query head) rows of one kv head
-constexpr int kMaxCtas = 320;       // two for each of up to 160 SMs
-constexpr int kTmemCols = 256;      // two score tiles of 64, the output's up to 128
-constexpr float kLazy = 8.0f;       // log2 of how far weights may grow past 1
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kDescInts = 8;
-constexpr int kWholeTiles = 8;
-
-struct TensorArgs {
-    AttendArgs a;
-    int group;   // query heads a kv head
-    int tokens;  // window tokens a row tile: all their heads in 128 rows
-    int few;     // window tokens whose heads fit in 64 rows
-    int box;     // cache tokens a TMA box
-    int whole;   // no job is split
-    float *part_o;   // [2 kMaxCtas][D / 4][128] float4
-    float *part_ml;  // [2 kMaxCtas][2][128]
-    int *desc;       // [kMaxCtas][kDescInts]: the split job that begins in a CTA
-};
-
 // Shared memory and warps of a CTA.
 //   16-bit cache: one ring of buffers, into which keys and values are copied and
 //     from which they are multiplied.
@@ -223,8 +161,7 @@ struct alignas(16) Control {
     unsigned tmem;
     unsigned nonfinite[4];  // window tokens whose values were zeroed, by segment
     int abort;
-    int start_r, start_head, start_row_tile, start_unit;  // where this CTA begins
-    int start_row0, start_len, start_P, start_tiles, start_row_tiles;
+    Begin begin;
     long long scan[40];
 };
 // What the scales of a tile's tokens become (E4M3), for every other tile.
@@ -238,94 +175,6 @@ struct TileScales {
     float q[4][kRowsPerTile];  // what the queries were divided by, by segment
 };
 static_assert(sizeof(Control) <= 1024 && sizeof(Control) + sizeof(TileScales) <= 5120, "control area");
-
-// A request's jobs: every (kv head, 128 rows) pair reads all its tiles.
-struct Request {
-    int row0, len, P, tiles, row_tiles;
-};
-
-__device__ __forceinline__ bool to_request(const TensorArgs &t, const Window &w, Request *q, bool report) {
-    if (!usable(t.a, w, report)) return false;
-    q->row0 = w.lo;
-    q->len = w.hi - w.lo;
-    q->P = w.P;
-    q->tiles = (q->P + q->len + kTile - 1) / kTile;
-    q->row_tiles = (q->len + t.tokens - 1) / t.tokens;
-    return true;
-}
-
-// T units dealt to n CTAs in order, each T / n of them or one more.  A job counts
-// its tiles and, before them, some units for its beginning and end, so that CTAs
-// with many short jobs get fewer tiles; where no job is split it is one unit.
-struct Deal {
-    int n, rest;  // below 1024
-    long long each;
-    __device__ __forceinline__ long long first(int c) const { return c * each + c * rest / n; }
-    // the CTA, c or later, that a unit falls to
-    __device__ __forceinline__ int cta_of(long long unit, int c) const {
-        int hi = n - 1;
-        while (c < hi) {
-            const int mid = (c + hi + 1) >> 1;
-            if (first(mid) <= unit) c = mid;
-            else hi = mid - 1;
-        }
-        return c;
-    }
-};
-
-// Consecutive tiles of one job that a CTA works through.
-struct Segment {
-    Request q = {};
-    int r, head, row_tile, first, count;
-};
-
-// Walks a CTA's units job by job: requests in order, in each the kv heads, in
-// each the row tiles (which read the same keys and values, so the later ones
-// find them in L2).  Every warp role walks on its own and sees the same; the
-// next request is loaded while the present one is worked on.
-template <int kJobCost>
-struct Walk {
-    int left, r, head, row_tile, unit;
-    Request q = {};
-    Window ahead;
-
-    __device__ __forceinline__ void begin(const TensorArgs &t, const Control &ctl, int n) {
-        left = n;
-        r = ctl.start_r;
-        head = ctl.start_head;
-        row_tile = ctl.start_row_tile;
-        unit = ctl.start_unit;
-        q = {ctl.start_row0, ctl.start_len, ctl.start_P, ctl.start_tiles, ctl.start_row_tiles};
-        ahead = load_window(t.a, min(r + 1, t.a.B - 1));
-    }
-    __device__ __forceinline__ bool next(const TensorArgs &t, Segment *s) {
-        while (left > 0) {
-            const int take = t.whole ? 1 : min(q.tiles + kJobCost - unit, left);
-            s->q = q;
-            s->r = r;
-            s->head = head;
-            s->row_tile = row_tile;
-            s->first = max(unit - kJobCost, 0);
-            s->count = t.whole ? q.tiles : max(unit + take - kJobCost, 0) - s->first;
-            left -= take;
-            unit = 0;
-            if (++row_tile == q.row_tiles) {
-                row_tile = 0;
-                if (++head == t.a.cache.n_kv_heads) {
-                    head = 0;
-                    while (left > 0) {
-                        const bool has = to_request(t, ahead, &q, false);
-                        ++r;
-                        ahead = load_window(t.a, min(r + 1, t.a.B - 1));
-                        if (has) break;
-                    }
-                }
-            }
-            if (s->count > 0) return true;
-        }
-        return false;
-    }
-};
 
 // A place in a ring of `slots` barriers and buffers, and the parity of its phase.
 struct Ring {
@@ -366,12 +215,6 @@ __device__ __forceinline__ void split_pair(float x0, float x1, unsigned *hi, uns
     *hi = e4m3_pair(x0, x1);
     const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)*hi, __NV_E4M3)));
     *lo = e4m3_pair(x0 - h.x, x1 - h.y);
-}
-
-// Two E4M3 codes, in the low half of a word, as halves: exact.
-__device__ __forceinline__ uint32_t two_halves(unsigned codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
 }
 
 // Where 16-byte chunk c of row r lies in rows of `row_bytes` (64 or 128) under the
@@ -433,62 +276,22 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     pdl_wait();
     pdl_trigger();
 
-    // this CTA's share of all units: each thread sums a run of requests, a scan
-    // over the threads finds the request that holds the first of its units
-    const int per = (a.B + kThreads - 1) / kThreads;
-    long long mine = 0;
-    Request q = {};
-    auto job_units = [&]() { return t.whole ? 1 : q.tiles + S::kJobCost; };
-    auto units = [&]() { return (long long)job_units() * (q.row_tiles * a.cache.n_kv_heads); };
-    for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
-        if (to_request(t, load_window(a, r), &q, blockIdx.x == 0)) mine += units();
-    long long T;
-    const long long before = block_exclusive_scan<long long>(mine, ctl.scan, &T);
-    // (a CTA with less than two tiles to do would cost more than it brings)
-    const int n_ctas =
-        (int)min((long long)gridDim.x, t.whole ? T : (T + S::kJobCost + 1) / (S::kJobCost + 2));
+    Deal deal;
+    long long lo, hi;
     const int cta = blockIdx.x;
-    if (tid == 0 && !t.whole) t.desc[cta * kDescInts] = 0;
-    if (cta >= n_ctas) {
+    if (!share_of<kThreads, S::kJobCost>(t, &ctl.begin, ctl.scan, &deal, &lo, &hi)) {
         if (warp == S::kScoreWarp) {
             __syncwarp();
             tmem_free(*(volatile unsigned *)&ctl.tmem, kTmemCols);
         }
         return;
     }
-    Deal deal;
-    deal.n = n_ctas;
-    deal.each = div_nonneg(T, n_ctas);
-    deal.rest = (int)(T - deal.each * n_ctas);
-    const long long lo = deal.first(cta), hi = deal.first(cta + 1);
-    if (lo >= before && lo < before + mine) {
-        long long at = before;
-        for (int r = tid * per;; ++r) {
-            // (with one request a thread it is the one just loaded)
-            if (per > 1 && !to_request(t, load_window(a, r), &q, false)) continue;
-            if (lo >= at + units()) {
-                at += units();
-                continue;
-            }
-            const int job = (int)div_nonneg(lo - at, job_units());
-            ctl.start_r = r;
-            ctl.start_unit = (int)(lo - at - (long long)job * job_units());
-            ctl.start_head = job / q.row_tiles;
-            ctl.start_row_tile = job % q.row_tiles;
-            ctl.start_row0 = q.row0;
-            ctl.start_len = q.len;
-            ctl.start_P = q.P;
-            ctl.start_tiles = q.tiles;
-            ctl.start_row_tiles = q.row_tiles;
-            break;
-        }
-    }
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = ctl.tmem;
     volatile int *abort = &ctl.abort;
     Walk<S::kJobCost> walk;
-    walk.begin(t, ctl, (int)(hi - lo));
+    walk.begin(t, ctl.begin, (int)(hi - lo));
     Segment s = {};
     Ring ring_at = {0, 0};
     // The queries of a segment whose rows fit in 64 take one half of their buffer
@@ -1041,7 +844,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             for (int j = 1; j < 8; ++j)
                                 top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[4 * j + 2 * k]),
                                                              __uint_as_float(x[4 * j + 2 * k + 1])));
-                            if (!kQuant) top[k] *= c;
+                            if (kQuant) top[k] -= kHalfRoom;
+                            else top[k] *= c;
                         }
                         auto grows = [&](int k) {
                             return top[k] > now[k].mx + kLazy || (now[k].mx == -INFINITY && top[k] > now[k].mx);
@@ -1409,21 +1213,55 @@ bool tensor_fits(const AttendArgs &a, int dtype, const dspark_kv_cache &c) {
            a.ld_q % 8 == 0 && a.ld_out % 8 == 0 && a.ld_q < (1ll << 39);
 }
 
+// Whether few rows over E4M3 are the rows of one tile of fewrows.cuh, on average: what
+// the device finds (`rows` of the window), and what the call's sizes say of it.
+bool few_fits(const AttendArgs &a, const dspark_kv_cache &c) {
+    return c.dtype == DSPARK_DTYPE_E4M3 && a.n_q_heads / c.n_kv_heads <= kFewRows &&
+           aligned(c.k_scale, 16) && aligned(c.v_scale, 16);
+}
+
+TensorArgs tensor_args(const AttendArgs &a, const dspark_kv_cache &c, void *workspace, int rows) {
+    TensorArgs t;
+    t.a = a;
+    t.group = a.n_q_heads / c.n_kv_heads;
+    t.tokens = min(rows / t.group, DSPARK_MAX_WINDOW);
+    t.few = min(rows / 2 / t.group, DSPARK_MAX_WINDOW);
+    t.box = gcd(c.page_size, kTile);
+    unsigned char *w = static_cast<unsigned char *>(workspace);
+    const size_t o = part_o_bytes(c.head_dim);
+    t.part_o = reinterpret_cast<float *>(w);
+    t.part_ml = reinterpret_cast<float *>(w + o);
+    t.desc = reinterpret_cast<int *>(w + o + part_ml_bytes());
+    // A split job's parts are joined by a second launch.  Where no request can have more
+    // than kWholeTiles tiles, a job stays whole and that launch is not made.
+    t.whole = (long long)c.table_width * c.page_size <= kWholeTiles * kTile;
+    return t;
+}
+
+template <int D>
+cudaError_t launch_join(const TensorArgs &t, int grid, cudaStream_t stream) {
+    if (t.whole) return cudaSuccess;
+    return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32 * 4), dim3(kJoinWarps * 32), 0, stream, t);
+}
+
+template <int D>
+cudaError_t launch_few(const AttendArgs &a, const dspark_kv_cache &c, void *workspace,
+                       cudaStream_t stream) {
+    constexpr int kSmem = FewShape<D>::kRing + (int)sizeof(FewControl);
+    const TensorArgs t = tensor_args(a, c, workspace, kFewRows);
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_few_kernel<D>), kSmem, 24 + (D == 128));
+    if (e != cudaSuccess) return e;
+    const int grid = min(2 * sm_count(), kMaxCtas);
+    e = launch_pdl(attend_few_kernel<D>, dim3(grid), dim3(kFewWarps * 32), kSmem, stream, t);
+    return e != cudaSuccess ? e : launch_join<D>(t, grid, stream);
+}
+
 template <int D, bool kQuant>
 cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *workspace,
                           cudaStream_t stream) {
     using S = TensorShape<D, kQuant>;
     constexpr int kSmemSlot = 20 + (D == 128) + 2 * kQuant;  // of ensure_smem
-    TensorArgs t;
-    t.a = a;
-    t.group = a.n_q_heads / c.n_kv_heads;
-    t.tokens = min(kRowsPerTile / t.group, DSPARK_MAX_WINDOW);
-    t.few = min(kRowsPerTile / 2 / t.group, DSPARK_MAX_WINDOW);
-    t.box = gcd(c.page_size, kTile);
-    unsigned char *w = static_cast<unsigned char *>(workspace);
-    t.part_o = reinterpret_cast<float *>(w);
-    t.part_ml = reinterpret_cast<float *>(w + part_o_bytes(D));
-    t.desc = reinterpret_cast<int *>(w + part_o_bytes(D) + part_ml_bytes());
+    const TensorArgs t = tensor_args(a, c, workspace, kRowsPerTile);
     // the cache as [page][head][token][element], the queries as [row][kv head]
     // [head of it][element]
     const int64_t dims[4] = {D, c.page_size, c.n_kv_heads, c.n_pages};
@@ -1440,14 +1278,10 @@ cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *w
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_tensor_kernel<D, kQuant>),
                                 S::kTotal, kSmemSlot);
     if (e != cudaSuccess) return e;
-    // A split job's parts are joined by a second launch.  Where no request can have more
-    // than kWholeTiles tiles, a job stays whole and that launch is not made.
-    t.whole = (long long)c.table_width * c.page_size <= kWholeTiles * kTile;
     const int grid = min(2 * sm_count(), kMaxCtas);
     e = launch_pdl(attend_tensor_kernel<D, kQuant>, dim3(grid), dim3(S::kThreads), S::kTotal, stream,
                    map_k, map_v, map_q, map_few, t);
-    if (e != cudaSuccess || t.whole) return e;
-    return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32 * 4), dim3(kJoinWarps * 32), 0, stream, t);
+    return e != cudaSuccess ? e : launch_join<D>(t, grid, stream);
 }
 
 }  // namespace
@@ -1500,7 +1334,9 @@ extern "C" int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype,
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     const bool quant = cache->dtype == DSPARK_DTYPE_E4M3, small = cache->head_dim == 64;
-    if (tensor_fits(a, dtype, *cache))
+    if (tensor_fits(a, dtype, *cache) && few_fits(a, *cache) && few_on_average(a, a.max_rows))
+        e = small ? launch_few<64>(a, *cache, workspace, st) : launch_few<128>(a, *cache, workspace, st);
+    else if (tensor_fits(a, dtype, *cache))
         e = quant ? small ? launch_tensor<64, true>(a, *cache, workspace, st)
                           : launch_tensor<128, true>(a, *cache, workspace, st)
             : small ? launch_tensor<64, false>(a, *cache, workspace, st)

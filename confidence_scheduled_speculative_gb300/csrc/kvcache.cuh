@@ -69,6 +69,12 @@ __device__ __forceinline__ unsigned e4m3_pair(float x0, float x1) {
     return __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
 }
 
+// Two E4M3 codes, in the low half of a word, as halves: exact.
+__device__ __forceinline__ uint32_t two_halves(unsigned codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+    return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+
 }  // namespace dspark
 
 // ---------------------------------------------------------------- host side

@@ -1,0 +1,225 @@
+// schedule.cuh -- how attend.cu and fewrows.cuh share a call's work: the window as
+// the device finds it, and its jobs dealt to the CTAs in tiles of positions.
+#pragma once
+
+#include "kvcache.cuh"
+
+namespace dspark {
+
+struct AttendArgs {
+    const void *q;
+    long long ld_q;
+    void *out;
+    long long ld_out;
+    float *lse;
+    const int32_t *cu, *prefix;
+    const uint32_t *ancestors;
+    int B, n_q_heads, max_rows;
+    float scale;
+    KvView cache;
+    int32_t *status;
+};
+
+// A request's entries as they are: rows [lo, hi) and the prefix length.
+struct Window {
+    int lo, hi, P;
+};
+
+__device__ __forceinline__ Window load_window(const AttendArgs &a, int r) {
+    return {__ldg(a.cu + r), __ldg(a.cu + r + 1), __ldg(a.prefix + r)};
+}
+
+// Whether a window has rows and can be used; with `report`, flags why not.
+__device__ __forceinline__ bool usable(const AttendArgs &a, const Window &w, bool report) {
+    if (w.hi == w.lo) return false;
+    int bad = 0;
+    if (w.lo < 0 || w.hi < w.lo || w.hi - w.lo > DSPARK_MAX_WINDOW || w.hi > a.max_rows)
+        bad = DSPARK_STATUS_BAD_LEN;
+    else if (w.P < 0 ||
+             (long long)w.P + (w.hi - w.lo) > (long long)a.cache.table_width * a.cache.page_size)
+        bad = DSPARK_STATUS_BAD_INDEX;
+    if (bad && report) flag(a.status, bad);
+    return !bad;
+}
+
+constexpr int kFewRows = 8;  // query rows of a kv head that fewrows.cuh multiplies at once
+
+// Whether that many rows are, on average, one such tile a request and kv head.
+__host__ __device__ inline bool few_on_average(const AttendArgs &a, int rows) {
+    return (long long)rows * (a.n_q_heads / a.cache.n_kv_heads) <= (long long)kFewRows * a.B;
+}
+
+// The window tokens that token i of a window sees, as bits.
+__device__ __forceinline__ unsigned ancestors_of(const AttendArgs &a, int row, int i, int len) {
+    const unsigned all = 0xFFFFFFFFu >> (32 - len);
+    return (a.ancestors ? __ldg(a.ancestors + row) : 0xFFFFFFFFu >> (31 - i)) & all;
+}
+
+constexpr int kTile = 64;           // positions a step
+constexpr int kRowsPerTile = 128;   // (token, query head) rows of one kv head
+constexpr int kMaxCtas = 320;       // two for each of up to 160 SMs
+constexpr int kTmemCols = 256;      // two score tiles of 64, the output's up to 128
+constexpr float kLazy = 8.0f;       // log2 of how far weights may grow past 1
+// Weights as halves (over E4M3) are taken 2^kHalfRoom times larger, so that those far
+// below the largest keep their digits: with 2^kLazy in front a half still holds them.
+constexpr float kHalfRoom = 6.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kDescInts = 8;
+constexpr int kWholeTiles = 8;
+
+struct TensorArgs {
+    AttendArgs a;
+    int group;   // query heads a kv head
+    int tokens;  // window tokens a row tile: all their heads in 128 rows
+    int few;     // window tokens whose heads fit in 64 rows
+    int box;     // cache tokens a TMA box
+    int whole;   // no job is split
+    float *part_o;   // [2 kMaxCtas][D / 4][128] float4
+    float *part_ml;  // [2 kMaxCtas][2][128]
+    int *desc;       // [kMaxCtas][kDescInts]: the split job that begins in a CTA
+};
+
+// A request's jobs: every (kv head, 128 rows) pair reads all its tiles.
+struct Request {
+    int row0, len, P, tiles, row_tiles;
+};
+
+__device__ __forceinline__ bool to_request(const TensorArgs &t, const Window &w, Request *q, bool report) {
+    if (!usable(t.a, w, report)) return false;
+    q->row0 = w.lo;
+    q->len = w.hi - w.lo;
+    q->P = w.P;
+    q->tiles = (q->P + q->len + kTile - 1) / kTile;
+    q->row_tiles = (q->len + t.tokens - 1) / t.tokens;
+    return true;
+}
+
+// Where a CTA's share begins.
+struct Begin {
+    int r, head, row_tile, unit;
+    Request q;
+};
+
+// T units dealt to n CTAs in order, each T / n of them or one more.  A job counts
+// its tiles and, before them, some units for its beginning and end, so that CTAs
+// with many short jobs get fewer tiles; where no job is split it is one unit.
+struct Deal {
+    int n, rest;  // below 1024
+    long long each;
+    __device__ __forceinline__ long long first(int c) const { return c * each + c * rest / n; }
+    // the CTA, c or later, that a unit falls to
+    __device__ __forceinline__ int cta_of(long long unit, int c) const {
+        int hi = n - 1;
+        while (c < hi) {
+            const int mid = (c + hi + 1) >> 1;
+            if (first(mid) <= unit) c = mid;
+            else hi = mid - 1;
+        }
+        return c;
+    }
+};
+
+// Consecutive tiles of one job that a CTA works through.
+struct Segment {
+    Request q = {};
+    int r, head, row_tile, first, count;
+};
+
+// Walks a CTA's units job by job: requests in order, in each the kv heads, in
+// each the row tiles (which read the same keys and values, so the later ones
+// find them in L2).  Every warp role walks on its own and sees the same; the
+// next request is loaded while the present one is worked on.
+template <int kJobCost>
+struct Walk {
+    int left, r, head, row_tile, unit;
+    Request q = {};
+    Window ahead;
+
+    __device__ __forceinline__ void begin(const TensorArgs &t, const Begin &b, int n) {
+        left = n;
+        r = b.r;
+        head = b.head;
+        row_tile = b.row_tile;
+        unit = b.unit;
+        q = b.q;
+        ahead = load_window(t.a, min(r + 1, t.a.B - 1));
+    }
+    __device__ __forceinline__ bool next(const TensorArgs &t, Segment *s) {
+        while (left > 0) {
+            const int take = t.whole ? 1 : min(q.tiles + kJobCost - unit, left);
+            s->q = q;
+            s->r = r;
+            s->head = head;
+            s->row_tile = row_tile;
+            s->first = max(unit - kJobCost, 0);
+            s->count = t.whole ? q.tiles : max(unit + take - kJobCost, 0) - s->first;
+            left -= take;
+            unit = 0;
+            if (++row_tile == q.row_tiles) {
+                row_tile = 0;
+                if (++head == t.a.cache.n_kv_heads) {
+                    head = 0;
+                    while (left > 0) {
+                        const bool has = to_request(t, ahead, &q, false);
+                        ++r;
+                        ahead = load_window(t.a, min(r + 1, t.a.B - 1));
+                        if (has) break;
+                    }
+                }
+            }
+            if (s->count > 0) return true;
+        }
+        return false;
+    }
+};
+
+// This CTA's units [lo, hi) of all of them, and where they begin (for all after the
+// next barrier); false where none are left for it.  Each thread sums a run of
+// requests, and a scan over the threads finds the request that holds the first.
+template <int kThreads, int kJobCost>
+__device__ __forceinline__ bool share_of(const TensorArgs &t, Begin *begin, long long *scan, Deal *deal,
+                                         long long *lo, long long *hi) {
+    const AttendArgs &a = t.a;
+    const int tid = threadIdx.x, cta = blockIdx.x;
+    const int per = (a.B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    Request q = {};
+    auto job_units = [&]() { return t.whole ? 1 : q.tiles + kJobCost; };
+    auto units = [&]() { return (long long)job_units() * (q.row_tiles * a.cache.n_kv_heads); };
+    for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
+        if (to_request(t, load_window(a, r), &q, cta == 0)) mine += units();
+    long long T;
+    const long long before = block_exclusive_scan<long long>(mine, scan, &T);
+    // (a CTA with less than two tiles to do would cost more than it brings)
+    const int n_ctas =
+        (int)min((long long)gridDim.x, t.whole ? T : (T + kJobCost + 1) / (kJobCost + 2));
+    if (tid == 0 && !t.whole) t.desc[cta * kDescInts] = 0;
+    if (cta >= n_ctas) return false;
+    deal->n = n_ctas;
+    deal->each = div_nonneg(T, n_ctas);
+    deal->rest = (int)(T - deal->each * n_ctas);
+    *lo = deal->first(cta);
+    *hi = deal->first(cta + 1);
+    if (*lo >= before && *lo < before + mine) {
+        long long at = before;
+        for (int r = tid * per;; ++r) {
+            // (with one request a thread it is the one just loaded)
+            if (per > 1 && !to_request(t, load_window(a, r), &q, false)) continue;
+            if (*lo >= at + units()) {
+                at += units();
+                continue;
+            }
+            const int job = (int)div_nonneg(*lo - at, job_units());
+            begin->r = r;
+            begin->unit = (int)(*lo - at - (long long)job * job_units());
+            begin->head = job / q.row_tiles;
+            begin->row_tile = job % q.row_tiles;
+            begin->q = q;
+            break;
+        }
+    }
+    return true;
+}
+
+}  // namespace dspark

@@ -66,7 +66,16 @@ class Problem:
             return 0.0
         return wo.BF16 if self.cache.kind == "bf16" else wo.F16
 
-    def check(self, skip=()):
+    def smallest_weight(self, r, n):
+        """What weights lose as halves where they are far below the largest (of weight
+        times scale): half of the smallest step 2^-24, taken 2^6 finer, of codes up
+        to 448, for each of n positions."""
+        if self.dtype != torch.bfloat16 or self.cache.kind != "e4m3":
+            return 0.0
+        page, tok = self.cache.slots(r, 0, n)
+        return n * 2.0 ** -31 * 448 * float(self.cache.v_scale[page, :, tok].abs().max())
+
+    def check(self, skip=(), far_below=False):
         lo = 0
         for r, (P, L) in enumerate(zip(self.prefix, self.win)):
             if L and r not in skip:
@@ -78,6 +87,8 @@ class Problem:
                 fine = torch.isfinite(o)
                 u = self.unit()
                 bound = (tol + u * o_abs) * (1 + wo.BF16) + wo.out_unit(self.dtype) * o.abs() + 1e-38
+                if far_below:
+                    bound = bound + self.smallest_weight(r, P + L)
                 off = ((got - o).abs() - bound)[fine]
                 assert not off.numel() or float(off.max()) <= 0, (r, float(off.max()))
                 assert torch.equal(got_lse == -math.inf, lse == -math.inf), r
@@ -276,3 +287,96 @@ def test_argument_errors(api, dev):
     with pytest.raises(ValueError):
         api.dspark_tree_attention(p.q, p.cache.kv(), lse=p.lse[:1], **ok)
     assert int(p.status) == 0 and bool((p.out == 7).all())
+
+
+# Decoding over the 8-bit cache, no more rows than requests (pad=0, or empty windows
+# beside the longer ones), which takes a kernel of its own up to 8 heads a key head.
+SINGLES = [
+    dict(prefix=[0], win=[1], hq=1, hkv=1, D=64, page=16),
+    dict(prefix=[1], win=[1], hq=8, hkv=1, D=128, page=64),
+    dict(prefix=[0, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129], win=[1] * 11, hq=8, hkv=2, D=128, page=16),
+    dict(prefix=[0, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129], win=[1] * 11, hq=5, hkv=1, D=64, page=48),
+    # past the lengths at which every job stays whole
+    dict(prefix=[700, 3, 512, 0, 1], win=[1] * 5, hq=16, hkv=2, D=128, page=256),
+    dict(prefix=[30001], win=[1], hq=16, hkv=2, D=128, page=16),
+    dict(prefix=[20000, 5, 9000], win=[1, 1, 1], hq=12, hkv=4, D=64, page=80),
+    # longer windows beside empty ones; row tiles of one, two, four and eight tokens
+    dict(prefix=[300, 7, 0, 1000, 9, 50], win=[4, 0, 1, 0, 0, 0], hq=8, hkv=1, D=128, page=32),
+    dict(prefix=[640] + [33] * 40, win=[32] + [0] * 33 + [1] * 7, hq=8, hkv=2, D=128, page=64),
+    dict(prefix=[63] + [33] * 40, win=[31] + [0] * 40, hq=6, hkv=3, D=64, page=64),
+    dict(prefix=[14, 333, 1200], win=[3, 0, 0], hq=2, hkv=2, D=128, page=64),
+    # more requests than a CTA has threads
+    dict(prefix=[(37 * i) % 300 for i in range(700)], win=[i % 3 > 0 for i in range(700)], hq=4, hkv=2,
+         D=64, page=64),
+    dict(prefix=[(91 * i) % 900 for i in range(300)], win=[1] * 300, hq=8, hkv=1, D=128, page=16),
+    # nine heads a key head: not this kernel
+    dict(prefix=[700, 3], win=[1, 1], hq=9, hkv=1, D=128, page=64),
+]
+
+
+@pytest.mark.parametrize("i", range(len(SINGLES)))
+@pytest.mark.parametrize("tree", [None, "orphans"])
+def test_single_tokens_over_8_bits(api, dev, i, tree):
+    shape = {**SINGLES[i], "win": [int(w) for w in SINGLES[i]["win"]]}
+    p = Problem(300 + i, tree=tree, kind="e4m3", pad=0, **shape).run(api)
+    p.check()
+    assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_more_requests_than_threads(api, dev, kind):
+    p = Problem(320, [(37 * i) % 200 for i in range(900)], [(i * 7) % 4 for i in range(900)], 4, 2, 64, 64,
+                kind, tree="tree").run(api)
+    p.check()
+    assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("pad", [0, 9])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_odd_scales_and_unseen_values(api, dev, pad, bad):
+    """Negative scales; scales and values that are not finite in places that a row
+    does not see, in ones that it does, and past the requests' ends (pad=0: single
+    tokens and empty windows)."""
+    win = [3, 1, 1, 0, 0, 1] if pad == 0 else [3, 1, 1, 0, 2, 1]
+    p = Problem(330, [37, 64, 5, 90, 20, 600], win, 8, 2, 128, 16, "e4m3", tree="orphans", pad=pad)
+    c = p.cache
+    used = torch.zeros((c.n_pages, 16), dtype=torch.bool, device="cuda")
+    for r, (P, L) in enumerate(zip(p.prefix, p.win)):
+        g, t = c.slots(r, 0, P + L)
+        used[g, t] = True
+    for t in (c.k, c.v):
+        t.view(torch.uint8)[~used] = 0x7F
+    for s in (c.k_scale, c.v_scale):
+        s *= torch.where(torch.rand(s.shape, device="cuda") < 0.3, -1.0, 1.0)
+        s.masked_fill_(~used[:, None, :], bad)
+    c.put("v", 0, 37 + 1, bad)  # a token of the window that the rows after it do not see
+    c.put("k", 0, 37 + 1, bad)
+    c.put("v", 5, 17, math.nan)  # in a prefix
+    p.run(api).check()
+    assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_queries_of_wide_range(api, dev, kind, pad):
+    """Queries whose elements differ by orders of magnitude, and rows of them that are
+    tiny, huge, zero, infinite or NaN."""
+    p = Problem(340, [130, 40, 77, 9, 21, 64], [1] * 6, 4, 2, 128, 64, kind, pad=pad)
+    p.q[:6] *= 2.0 ** torch.randint(-9, 1, p.q[:6].shape, device="cuda")
+    p.q[1] *= 2.0 ** -100
+    p.q[2] *= 2.0 ** 7
+    p.q[3] = 0
+    p.q[4, 1, 7] = math.nan
+    p.run(api).check(far_below=True)  # one-hot weights: dimensions where the one value is zero
+    assert int(p.status) == 0
+
+
+def test_bad_pages_of_single_tokens(api, dev):
+    p = Problem(350, [40, 100, 33, 64], [1] * 4, 4, 2, 64, 16, "e4m3", pad=0)
+    p.cache.table[1, 2] = p.cache.n_pages + 5
+    p.run(api).check(skip=(1,))
+    assert int(p.status) == api.STATUS_BAD_INDEX
+    p = Problem(351, [40, 100, 33, 64], [1] * 4, 4, 2, 64, 16, "e4m3", pad=0)
+    p.prefix_lens[2] = 10 ** 6
+    p.run(api).check(skip=(2,))
+    assert int(p.status) == api.STATUS_BAD_INDEX
