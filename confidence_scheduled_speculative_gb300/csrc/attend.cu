@@ -279,7 +279,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     Deal deal;
     long long lo, hi;
     const int cta = blockIdx.x;
-    if (!share_of<kThreads, S::kJobCost>(t, &ctl.begin, ctl.scan, &deal, &lo, &hi)) {
+    if ((kQuant && t.choose && few_on_average(a, __ldg(a.cu + a.B))) ||
+        !share_of<kThreads, S::kJobCost>(t, &ctl.begin, ctl.scan, &deal, &lo, &hi)) {
         if (warp == S::kScoreWarp) {
             __syncwarp();
             tmem_free(*(volatile unsigned *)&ctl.tmem, kTmemCols);
@@ -680,9 +681,9 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             const uint2 v0 = *reinterpret_cast<const uint2 *>(from + flip * 8);
                             const uint2 v1 = *reinterpret_cast<const uint2 *>(from + 8 - flip * 8);
                             *reinterpret_cast<uint4 *>(to + first) =
-                                make_uint4(two_halves(v0.x), two_halves(v0.x >> 16), two_halves(v0.y), two_halves(v0.y >> 16));
+                                eight_halves(v0);
                             *reinterpret_cast<uint4 *>(to + last) =
-                                make_uint4(two_halves(v1.x), two_halves(v1.x >> 16), two_halves(v1.y), two_halves(v1.y >> 16));
+                                eight_halves(v1);
                             from += 2048;
                             to += 128 / kUnits * 128;
                         }
@@ -1070,7 +1071,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Tens
     pdl_trigger();
     const int4 d0 = __ldcg(reinterpret_cast<const int4 *>(t.desc) + blockIdx.x * 2);
     const int4 d1 = __ldcg(reinterpret_cast<const int4 *>(t.desc) + blockIdx.x * 2 + 1);
-    const int base = (blockIdx.y & 3) * 32, columns = blockIdx.y / 4 * 32;
+    const int base = blockIdx.y / (D / 32) * 32, columns = blockIdx.y % (D / 32) * 32;
     const int c0 = blockIdx.x, c1 = d0.y, kv_head = d1.x, token0 = d1.y, rows = d1.z;
     if (!d0.x || base >= rows) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, m = base + lane;
@@ -1235,33 +1236,36 @@ TensorArgs tensor_args(const AttendArgs &a, const dspark_kv_cache &c, void *work
     // A split job's parts are joined by a second launch.  Where no request can have more
     // than kWholeTiles tiles, a job stays whole and that launch is not made.
     t.whole = (long long)c.table_width * c.page_size <= kWholeTiles * kTile;
+    t.choose = 0;
     return t;
 }
 
 template <int D>
-cudaError_t launch_join(const TensorArgs &t, int grid, cudaStream_t stream) {
+cudaError_t launch_join(const TensorArgs &t, int grid, int rows, cudaStream_t stream) {
     if (t.whole) return cudaSuccess;
-    return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32 * 4), dim3(kJoinWarps * 32), 0, stream, t);
+    return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32 * ((rows + 31) / 32)), dim3(kJoinWarps * 32), 0, stream, t);
 }
 
 template <int D>
-cudaError_t launch_few(const AttendArgs &a, const dspark_kv_cache &c, void *workspace,
+cudaError_t launch_few(const AttendArgs &a, const dspark_kv_cache &c, void *workspace, bool choose,
                        cudaStream_t stream) {
     constexpr int kSmem = FewShape<D>::kRing + (int)sizeof(FewControl);
-    const TensorArgs t = tensor_args(a, c, workspace, kFewRows);
+    TensorArgs t = tensor_args(a, c, workspace, kFewRows);
+    t.choose = choose;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(attend_few_kernel<D>), kSmem, 24 + (D == 128));
     if (e != cudaSuccess) return e;
     const int grid = min(2 * sm_count(), kMaxCtas);
     e = launch_pdl(attend_few_kernel<D>, dim3(grid), dim3(kFewWarps * 32), kSmem, stream, t);
-    return e != cudaSuccess ? e : launch_join<D>(t, grid, stream);
+    return e != cudaSuccess || choose ? e : launch_join<D>(t, grid, kFewRows, stream);
 }
 
 template <int D, bool kQuant>
-cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *workspace,
+cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *workspace, bool choose,
                           cudaStream_t stream) {
     using S = TensorShape<D, kQuant>;
     constexpr int kSmemSlot = 20 + (D == 128) + 2 * kQuant;  // of ensure_smem
-    const TensorArgs t = tensor_args(a, c, workspace, kRowsPerTile);
+    TensorArgs t = tensor_args(a, c, workspace, kRowsPerTile);
+    t.choose = choose;
     // the cache as [page][head][token][element], the queries as [row][kv head]
     // [head of it][element]
     const int64_t dims[4] = {D, c.page_size, c.n_kv_heads, c.n_pages};
@@ -1281,7 +1285,7 @@ cudaError_t launch_tensor(const AttendArgs &a, const dspark_kv_cache &c, void *w
     const int grid = min(2 * sm_count(), kMaxCtas);
     e = launch_pdl(attend_tensor_kernel<D, kQuant>, dim3(grid), dim3(S::kThreads), S::kTotal, stream,
                    map_k, map_v, map_q, map_few, t);
-    return e != cudaSuccess ? e : launch_join<D>(t, grid, stream);
+    return e != cudaSuccess ? e : launch_join<D>(t, grid, min(t.tokens, a.max_rows) * t.group, stream);
 }
 
 }  // namespace
@@ -1334,15 +1338,22 @@ extern "C" int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype,
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     const bool quant = cache->dtype == DSPARK_DTYPE_E4M3, small = cache->head_dim == 64;
-    if (tensor_fits(a, dtype, *cache) && few_fits(a, *cache) && few_on_average(a, a.max_rows))
-        e = small ? launch_few<64>(a, *cache, workspace, st) : launch_few<128>(a, *cache, workspace, st);
-    else if (tensor_fits(a, dtype, *cache))
-        e = quant ? small ? launch_tensor<64, true>(a, *cache, workspace, st)
-                          : launch_tensor<128, true>(a, *cache, workspace, st)
-            : small ? launch_tensor<64, false>(a, *cache, workspace, st)
-                    : launch_tensor<128, false>(a, *cache, workspace, st);
-    else
+    if (tensor_fits(a, dtype, *cache)) {
+        // Few rows over E4M3: where the rows that the window has room for leave it open
+        // (a window padded to a tier), both kernels are launched, and the rows that it
+        // holds tell which of them works and which returns at once (2 us).
+        const bool few = quant && few_fits(a, *cache), always = few && few_on_average(a, a.max_rows);
+        e = cudaSuccess;
+        if (few) e = small ? launch_few<64>(a, *cache, workspace, !always, st)
+                           : launch_few<128>(a, *cache, workspace, !always, st);
+        if (e == cudaSuccess && !always)
+            e = quant ? small ? launch_tensor<64, true>(a, *cache, workspace, few, st)
+                              : launch_tensor<128, true>(a, *cache, workspace, few, st)
+                : small ? launch_tensor<64, false>(a, *cache, workspace, false, st)
+                        : launch_tensor<128, false>(a, *cache, workspace, false, st);
+    } else {
         e = dtype == DSPARK_DTYPE_BF16 ? launch_any<__nv_bfloat16>(a, cache->dtype, st)
                                        : launch_any<float>(a, cache->dtype, st);
+    }
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }

@@ -19,7 +19,9 @@ namespace dspark {
 constexpr int kFewWarps = 8;
 constexpr int kFewChunk = 16;   // positions a step of a warp
 constexpr int kFewStages = 3;   // steps in flight a warp
-constexpr int kFewJobCost = 2;  // of a job's begin and end, in tiles
+// What a job's begin and end cost, in tiles of its products: 32 requests of up to 8192
+// tokens take 89, 82, 77, 75.5, 75.9 and 78 us at 1, 2, 4, 6, 8 and 12.
+constexpr int kFewJobCost = 6;
 
 template <int D>
 struct FewShape {
@@ -30,6 +32,7 @@ struct FewShape {
 };
 struct FewControl {
     Begin begin;
+    Walk<kFewJobCost> walk;
     Segment seg[4];  // the present one, the next, and the one after
     unsigned nonfinite[2];  // window tokens whose values were zeroed, by segment
     int stage[kFewWarps];   // where the warps left their outputs
@@ -58,6 +61,17 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+// One and two units in the last place, for normal numbers.
+__device__ __forceinline__ float reciprocal_approx(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t pack_halves(float x, float y) {
     const __half2 two = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&two);
@@ -77,17 +91,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
     Deal deal;
     long long lo, hi;
     const int cta = blockIdx.x;
+    if (t.choose && !few_on_average(a, __ldg(a.cu + a.B))) return;
     if (!share_of<kFewWarps * 32, kFewJobCost>(t, &ctl.begin, ctl.scan, &deal, &lo, &hi)) return;
     __syncthreads();
     // one thread walks; the others read the segments it leaves
-    Walk<kFewJobCost> walk;
     auto leave = [&](unsigned k) {
-        Segment s = {};
-        if (!walk.next(t, &s)) s.count = 0;
-        ctl.seg[k & 3] = s;
+        if (!ctl.walk.next(t, &ctl.seg[k & 3])) ctl.seg[k & 3].count = 0;
     };
     if (tid == 0) {
-        walk.begin(t, ctl.begin, (int)(hi - lo));
+        ctl.walk.begin(t, ctl.begin, (int)(hi - lo));
         leave(0);
         leave(1);
         ctl.nonfinite[0] = ctl.nonfinite[1] = 0;
@@ -101,6 +113,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
     // The copies run ahead of the products by up to kFewStages steps, into the next
     // segment too.  A warp takes every kFewWarps-th step of a segment.
     unsigned fetched = 0, used = 0, fk = 0;
+    uint32_t f_stage = 0, stage = 0;  // of the next step to copy, to multiply: bytes
     int fi = 0, fn = 0, f_left = 0, f_page = -1, f_token = 0;
     long long f_head = 0, f_scale = 0;
     auto steps_of = [&](const Segment &s) {
@@ -118,6 +131,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
         f_scale = (long long)s.head * a.cache.page_size;
     };
     enter(0);
+    // this lane's part of a step: of K two tokens' bytes, of V four tokens', and of
+    // the scales (eight lanes) four
+    const long long k_lane = g * a.cache.token_stride + c * 16;
+    const long long v_lane = 2 * c * a.cache.token_stride + g * (D / 8);
+    const float *s_lane = (lane < 4 ? a.cache.k_scale : a.cache.v_scale) + 4 * c;
+    auto copy_v = [](uint32_t dst, const void *src, bool in) {
+        if (D == 128) copy16(dst, src, in);
+        else copy8(dst, src, in);
+    };
     auto fetch = [&](unsigned k) {  // one more step, of segment k or the next
         if (fi == fn && fk == k) enter(k + 1);
         if (fi == fn) return false;
@@ -141,30 +163,38 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
         // a page outside the pool, as past the request's end, arrives as zeros
         const bool in = page >= 0;
         const long long from = in ? page * a.cache.page_stride + token * a.cache.token_stride + f_head : 0;
-        const uint32_t to = ring_at + fetched % kFewStages * S::kStage;
+        const unsigned char *k_from = a.cache.k + from + k_lane, *v_from = a.cache.v + from + v_lane;
+        const long long s_from =
+            in ? (long long)page * a.cache.n_kv_heads * a.cache.page_size + f_scale + token : 0;
+        const uint32_t to = ring_at + f_stage + lane * 16;
+        const uint32_t v_to = ring_at + f_stage + S::kCodes + lane * (D / 8);
+        const long long stride = a.cache.token_stride;
+        if (in && f_left >= kFewChunk) {
 #pragma unroll
-        for (int j = 0; j < 2 * kWords; ++j) {
-            const int tok = g + 8 * (j / kWords);
-            copy16(to + j * 512 + lane * 16,
-                   a.cache.k + (in ? from + tok * a.cache.token_stride : 0) + j % kWords * 64 + c * 16,
-                   in && tok < f_left);
-        }
+            for (int j = 0; j < 2 * kWords; ++j)
+                copy16(to + j * 512, k_from + j / kWords * 8 * stride + j % kWords * 64, true);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int tok = 2 * c + (j & 1) + 8 * (j >> 1);
-            const unsigned char *src =
-                a.cache.v + (in ? from + tok * a.cache.token_stride : 0) + g * (D / 8);
-            if (D == 128) copy16(to + S::kCodes + j * 512 + lane * 16, src, in && tok < f_left);
-            else copy8(to + S::kCodes + j * 256 + lane * 8, src, in && tok < f_left);
+            for (int j = 0; j < 4; ++j) copy_v(v_to + j * 4 * D, v_from + ((j & 1) + 8 * (j >> 1)) * stride, true);
+        } else {
+            // tokens past the end as zeros: none of them is read
+            const int left = in ? f_left : 0;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                const bool some = g + 8 * h < left;
+#pragma unroll
+                for (int j = 0; j < kWords; ++j)
+                    copy16(to + (h * kWords + j) * 512, k_from + (some ? h * 8 * stride : -k_lane) + j * 64, some);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const bool has = 2 * c + j + 8 * h < left;
+                    copy_v(v_to + (2 * h + j) * 4 * D, v_from + (has ? (j + 8 * h) * stride : -v_lane), has);
+                }
+            }
         }
-        if (lane < 8) {
-            const float *src = lane < 4 ? a.cache.k_scale : a.cache.v_scale;
-            const long long at =
-                in ? (long long)page * a.cache.n_kv_heads * a.cache.page_size + f_scale + token : 0;
-            copy16(to + 2 * S::kCodes + lane * 16, src + at + 4 * (lane & 3), in);
-        }
+        if (lane < 8) copy16(to + 2 * S::kCodes, s_lane + s_from, in);
         asm volatile("cp.async.commit_group;" ::: "memory");
         ++fetched;
+        f_stage = f_stage == (kFewStages - 1) * S::kStage ? 0 : f_stage + S::kStage;
         ++fi;
         f_left -= kFewWarps * kFewChunk;
         return true;
@@ -231,12 +261,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
             else if (fetched - used > 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
             else asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncwarp();  // the scales are other lanes' copies
-            const unsigned char *at = ring + used % kFewStages * S::kStage;
+            const unsigned char *at = ring + stage;
+            stage = stage == (kFewStages - 1) * S::kStage ? 0 : stage + S::kStage;
             const float *ks = reinterpret_cast<const float *>(at + 2 * S::kCodes), *vs = ks + kFewChunk;
             const bool window = pos + kFewChunk > P;
 
             // scores of tokens g and g + 8 by rows 2c and 2c + 1
-            float z[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float z[4] = {0.0f, 0.0f, 0.0f, 0.0f}, z2[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             {
                 uint4 w[2][kWords];
 #pragma unroll
@@ -246,10 +277,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
                 for (int j = 0; j < kSteps; ++j) {
                     const unsigned x = reinterpret_cast<const unsigned *>(w[0])[j];
                     const unsigned y = reinterpret_cast<const unsigned *>(w[1])[j];
-                    const uint32_t halves[4] = {two_halves(x), two_halves(y), two_halves(x >> 16),
-                                                two_halves(y >> 16)};
-                    mma_16x8(z, halves, q[j][0], q[j][1]);
+                    uint32_t halves[4];
+                    four_halves(x, &halves[0], &halves[2]);
+                    four_halves(y, &halves[1], &halves[3]);
+                    mma_16x8(j & 1 ? z2 : z, halves, q[j][0], q[j][1]);
                 }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) z[x] += z2[x];
             }
             // Scores to base 2, plus log2 of the value's scale: the weights then are
             // those of the values' codes, and the sum divides it out again.
@@ -257,20 +291,23 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
             bool odd = false;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int token = g + 8 * h, p = pos + token;
-                float kf = ks[token], vf = vs[token];
-                if (p >= n) kf = vf = 1.0f;
+                float kf = ks[g + 8 * h], vf = vs[g + 8 * h];
+                if (window && pos + g + 8 * h >= n) kf = vf = 1.0f;
                 const bool fine = vf - vf == 0.0f;
                 odd = odd || !fine || vf < 0.0f;
                 // a NaN or infinite k_scale makes the score NaN
                 kf = kf - kf == 0.0f ? kf * scale : __int_as_float(0x7FC00000);
                 vf = fine ? fmaxf(fabsf(vf), 0x1p-100f) : 1.0f;
-                const float log2v = __log2f(vf);
-                inv[h] = __frcp_rn(vf);
+                const float log2v = log2_approx(vf);
+                inv[h] = reciprocal_approx(vf);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    z[2 * h + e] = fmaf(z[2 * h + e] * by_row[e], kf, log2v);
-                    if (window && p >= P && (p >= n || !(sees[e] >> (p - P) & 1))) z[2 * h + e] = -INFINITY;
+                for (int e = 0; e < 2; ++e) z[2 * h + e] = fmaf(z[2 * h + e] * by_row[e], kf, log2v);
+            }
+            if (window) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int p = pos + g + 8 * (x >> 1);
+                    if (p >= P && (p >= n || !(sees[x & 1] >> (p - P) & 1))) z[x] = -INFINITY;
                 }
             }
             // The maximum moves only when it grows by 2^kLazy: until then the
@@ -343,9 +380,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
                 for (int h = 0; h < 2; ++h) {
                     const unsigned x = reinterpret_cast<const unsigned *>(&v[2 * h])[j / 2];
                     const unsigned y = reinterpret_cast<const unsigned *>(&v[2 * h + 1])[j / 2];
-                    const unsigned both = __byte_perm(x, y, j & 1 ? 0x7362 : 0x5140);
-                    halves[2 * h] = two_halves(both);
-                    halves[2 * h + 1] = two_halves(both >> 16);
+                    four_halves(__byte_perm(x, y, j & 1 ? 0x7362 : 0x5140), &halves[2 * h], &halves[2 * h + 1]);
                 }
                 if (special) {
 #pragma unroll
@@ -365,6 +400,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
             __syncwarp();
         }
 
+        const uint32_t last = stage ? stage - S::kStage : (kFewStages - 1) * S::kStage;
         // The warps' parts meet in shared memory, in the stage that is free; then a
         // warp joins a row.
 #pragma unroll
@@ -375,14 +411,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
                 ctl.mx[warp][2 * c + e] = mx[e];
                 ctl.l[warp][2 * c + e] = l[e];
             }
-            float *to = reinterpret_cast<float *>(ring + (used + 2) % kFewStages * S::kStage) +
+            float *to = reinterpret_cast<float *>(ring + last) +
                         (2 * c + e) * D + g * (D / 8);
 #pragma unroll
             for (int j = 0; j < kSteps; j += 2)
                 *reinterpret_cast<float4 *>(to + 2 * j) =
                     make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
         }
-        if (lane == 0) ctl.stage[warp] = (used + 2) % kFewStages;
+        if (lane == 0) ctl.stage[warp] = warp * kFewStages * S::kStage + last;
         __syncthreads();
         const int slot = 2 * cta + (k > 0), m = warp;
         if (m < rows) {
@@ -398,7 +434,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
                 sum = fmaf(f, ctl.l[i][m], sum);
                 if (!mine) continue;
                 const float4 y = *reinterpret_cast<const float4 *>(
-                    smem + (i * kFewStages + ctl.stage[i]) * S::kStage + (m * D + lane * 4) * 4);
+                    smem + ctl.stage[i] + (m * D + lane * 4) * 4);
                 x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y);
                 x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
             }

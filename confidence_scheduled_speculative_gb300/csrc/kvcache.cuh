@@ -69,10 +69,19 @@ __device__ __forceinline__ unsigned e4m3_pair(float x0, float x1) {
     return __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
 }
 
-// Two E4M3 codes, in the low half of a word, as halves: exact.
-__device__ __forceinline__ uint32_t two_halves(unsigned codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+// The four E4M3 codes of a word as halves, the lower two and the upper: exact.
+__device__ __forceinline__ void four_halves(unsigned codes, uint32_t *lower, uint32_t *upper) {
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+        " cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+        : "=r"(*lower), "=r"(*upper)
+        : "r"(codes));
+}
+
+__device__ __forceinline__ uint4 eight_halves(uint2 codes) {
+    uint4 x;
+    four_halves(codes.x, &x.x, &x.y);
+    four_halves(codes.y, &x.z, &x.w);
+    return x;
 }
 
 }  // namespace dspark

@@ -75,6 +75,7 @@ struct TensorArgs {
     int few;     // window tokens whose heads fit in 64 rows
     int box;     // cache tokens a TMA box
     int whole;   // no job is split
+    int choose;  // both kernels are launched: the rows of the window tell which one works
     float *part_o;   // [2 kMaxCtas][D / 4][128] float4
     float *part_ml;  // [2 kMaxCtas][2][128]
     int *desc;       // [kMaxCtas][kDescInts]: the split job that begins in a CTA
