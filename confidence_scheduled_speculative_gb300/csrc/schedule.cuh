@@ -44,9 +44,13 @@ __device__ __forceinline__ bool usable(const AttendArgs &a, const Window &w, boo
 
 constexpr int kFewRows = 8;  // query rows of a kv head that fewrows.cuh multiplies at once
 
-// Whether that many rows are, on average, one such tile a request and kv head.
+// Whether that many rows of a window are few enough, over E4M3, for fewrows.cuh to read
+// the keys and values once for every eight of them: up to twice a request and kv head,
+// on average.  32 requests of up to 8192 tokens and 8 heads of 128, there and in the
+// kernel of 128 rows a tile: 4 rows 72 and 122 us, 10 rows 96 and 125, 14 rows 125 and
+// 139, 16 rows 134 and 139, 18 rows 144 and 139, 20 and more rows slower.
 __host__ __device__ inline bool few_on_average(const AttendArgs &a, int rows) {
-    return (long long)rows * (a.n_q_heads / a.cache.n_kv_heads) <= (long long)kFewRows * a.B;
+    return (long long)rows * (a.n_q_heads / a.cache.n_kv_heads) <= 2ll * kFewRows * a.B;
 }
 
 // The window tokens that token i of a window sees, as bits.
@@ -65,7 +69,10 @@ constexpr float kLazy = 8.0f;       // log2 of how far weights may grow past 1
 constexpr float kHalfRoom = 6.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kDescInts = 8;
+constexpr int kDescInts = 8;  // of a split job, for the join
+// The most tiles of a request for which jobs stay whole and the joining launch is not
+// made.  Whole and split: 8 requests of up to 300 tokens 13 and 21 us, of 440 15 and 21,
+// of 900 21 and 23, of 1900 32 and 25; 200 requests of 300 52 and 49, of 900 92 and 74.
 constexpr int kWholeTiles = 8;
 
 struct TensorArgs {

@@ -26,7 +26,8 @@
  *   - `status` (device int32[1], zeroed by the caller) collects
  *     DSPARK_STATUS_* bits that the kernels OR in for conditions only the
  *     device can see.  Kernels never trap or assert; their only waits on
- *     memory (the scatter's copy barriers) give up after 200 ms and set
+ *     memory (the scatter's copy barriers, and those between the warps of
+ *     the attention) give up, after 200 ms and about a second, and set
  *     DSPARK_STATUS_TIMEOUT.
  *   - Calls are stateless and thread-safe; concurrent calls must not share
  *     workspaces.
@@ -749,9 +750,14 @@ DSPARK_API size_t dspark_tree_attention_workspace_bytes(int32_t n_q_heads, int32
  *   prefix_lens  device [B], >= 0; cu_seqlens device [B+1]; window length 0 is
  *                a request without rows
  * Sums and softmax statistics are held in 32 bits.  BF16 rows over a BF16 or
- * E4M3 cache with head_dim 64 or 128, page_size a multiple of 16 and 16-byte
- * aligned layouts run on the tensor cores, the weights exp(s - m) rounded to
- * the 16-bit type of the products; anything else in 32 bits throughout.
+ * E4M3 cache with head_dim 64 or 128, at most 128 query heads a kv head,
+ * page_size a multiple of 16 and 16-byte aligned bases and strides run on the
+ * tensor cores, the weights exp(s - m) rounded to the 16-bit type of the
+ * products (BF16; over E4M3 a half, whose smallest step is 2^-30 of the
+ * largest weight times scale); anything else in 32 bits throughout.  Over
+ * E4M3 a query's elements below 2^-10 of its largest are taken to 2^-18 of it.
+ * The order of all sums is fixed by the lengths: a call repeated gives the
+ * same bits.
  * A window of more than 32 tokens or outside max_rows (BAD_LEN), and positions
  * past the block table or a page outside the pool (BAD_INDEX): that request's
  * rows are unspecified, the others not affected.  Rows of no request are left
