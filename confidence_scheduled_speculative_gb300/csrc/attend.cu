@@ -436,7 +436,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             };
             if (scores) {
                 // over E4M3: codes times the queries' two parts
-                constexpr uint32_t word = kQuant ? mma_word_e4m3(kTile) : mma_word(true, kTile, false);
+                constexpr uint32_t all_rows = kQuant ? mma_word_e4m3(kTile) : mma_word(true, kTile, false);
                 constexpr int kKeyRow = kQuant ? D : 128;  // bytes of a row
                 const uint64_t desc_q = smem_operand(ubase, 16, kKeyRow);
                 const uint64_t desc_k = smem_operand(ubase + S::kQBytes, 16, kKeyRow);
@@ -444,6 +444,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                 while (ok && walk.next(t, &s)) {
                     if (!wait(queries + (seg & 1), seg >> 1)) break;
                     const bool few = few_rows(s);
+                    const uint32_t word = all_rows - (few ? kHalfRows : 0);
                     const uint64_t queries_at = desc_q + (q_offset(s, seg) >> 4);
                     // their second parts, over E4M3
                     const unsigned part = (D == 64 && few ? 4096 : S::kQBytes / 2) >> 4;
@@ -479,9 +480,10 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                     ++seg;
                 }
             } else {
-                constexpr uint32_t word = mma_word(!kQuant, D, true);
+                constexpr uint32_t all_rows = mma_word(!kQuant, D, true);
                 const uint64_t desc_v = smem_operand(ubase + (kQuant ? S::kOpAt : S::kQBytes), kHalfBytes, 128);
                 while (ok && walk.next(t, &s)) {
+                    const uint32_t word = all_rows - (few_rows(s) ? kHalfRows : 0);
                     const int count = __shfl_sync(kFullMask, s.count, 0);
                     if (!kQuant) skip(count > 1 ? 2 : 1);
                     for (int i = 0; i < count; ++i) {
@@ -755,7 +757,6 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     } else {
         // --------------------------------------------- softmax warps
         if constexpr (kQuant) asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
-        const int m = tid;  // row of the tile, lane of tensor memory
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
         const bool negative = a.scale < 0.0f;
@@ -770,10 +771,14 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             // a warp that gave up still comes to the four warps' barriers
             ok = named_all(1, 128, ok);
             if (!ok || !walk.next(t, &s)) break;
+            // 64 rows or fewer are 16 a warp, so that each has half the work (18 rows a kv
+            // head over E4M3, 32 requests: 139 -> 123 us)
+            const bool few = few_rows(s), own = !few || lane < 16;
+            const int first_row = warp * (few ? 16 : 32), m = first_row + lane;
             // row m: head m % group of the tile's token m / group
             const int n = s.q.P + s.q.len, token0 = s.row_tile * t.tokens;
             const int rows = min(t.tokens, s.q.len - token0) * t.group;
-            const bool valid = m < rows, active = warp * 32 < rows;
+            const bool valid = own && m < rows, active = first_row < rows;
             const int mm = min(m, rows - 1), token = token0 + mm / t.group;
             const int head = s.head * t.group + mm % t.group, packed = s.q.row0 + token;
             const unsigned bits = ancestors_of(a, packed, token, s.q.len);
@@ -782,7 +787,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             // The scores are taken as fragments: of the warp's rows a thread has
             // four, 16 h + 8 k + lane / 4, and of each sixteen columns.  16 rows or
             // fewer are one half's work, and few scales serve a thread.
-            const int halves = rows - warp * 32 > 16 ? 2 : 1;
+            const int halves = !few && rows - first_row > 16 ? 2 : 1;
             struct Row {
                 float mx, l, factor;  // running maximum (to base 2), sum; query's power of two
                 unsigned seen;        // ancestor bits
@@ -790,7 +795,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 auto row_of = [&](int h) -> Row {
-                    const int token_k = token0 + min(warp * 32 + 16 * h + 8 * k + lane / 4, rows - 1) / t.group;
+                    const int token_k = token0 + min(first_row + 16 * h + 8 * k + lane / 4, rows - 1) / t.group;
                     return {-INFINITY, 0.0f, 1.0f,
                             active ? ancestors_of(a, s.q.row0 + token_k, token_k, s.q.len) : 0u};
                 };
@@ -824,7 +829,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                             if (i == 0)
 #pragma unroll
                                 for (int k = 0; k < 2; ++k)
-                                    now[k].factor = sc.q[seg & 3][warp * 32 + 16 * h + 8 * k + lane / 4];
+                                    now[k].factor = sc.q[seg & 3][first_row + 16 * h + 8 * k + lane / 4];
                         }
                         tmem_wait_load(x);
                         auto pair = [&](int e) {  // elements 2e and 2e + 1, of row e % 2
@@ -1034,7 +1039,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                                        ((long long)slot * (D / 4) + h * 8) * kRowsPerTile + m;
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            part[j * kRowsPerTile] =
+                            if (own) part[j * kRowsPerTile] =
                                 make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
                                             __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
                     } else if (valid) {
@@ -1052,10 +1057,10 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                                 make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                     }
                 }
-                if (!whole) {
+                if (!whole && own) {
                     t.part_ml[(long long)slot * 2 * kRowsPerTile + m] = row_mx;
                     t.part_ml[((long long)slot * 2 + 1) * kRowsPerTile + m] = row_l;
-                } else if (valid && a.lse) {
+                } else if (whole && valid && a.lse) {
                     a.lse[(long long)packed * a.n_q_heads + head] =
                         row_l == 0.0f ? -INFINITY : shift * kLn2 + logf(row_l);
                 }

@@ -47,8 +47,9 @@ constexpr int kFewRows = 8;  // query rows of a kv head that fewrows.cuh multipl
 // Whether that many rows of a window are few enough, over E4M3, for fewrows.cuh to read
 // the keys and values once for every eight of them: up to twice a request and kv head,
 // on average.  32 requests of up to 8192 tokens and 8 heads of 128, there and in the
-// kernel of 128 rows a tile: 4 rows 72 and 122 us, 10 rows 96 and 125, 14 rows 125 and
-// 139, 16 rows 134 and 139, 18 rows 144 and 139, 20 and more rows slower.
+// kernel of 128 rows a tile: 4 rows 74 and 120 us, 10 rows 96 and 120, 12 rows 113 and
+// 120, 14 rows 125 and 121, 18 rows 144 and 122; of up to 800 tokens: 4 rows 24 and 43,
+// 14 rows 34 and 43.
 __host__ __device__ inline bool few_on_average(const AttendArgs &a, int rows) {
     return (long long)rows * (a.n_q_heads / a.cache.n_kv_heads) <= 2ll * kFewRows * a.B;
 }

@@ -202,6 +202,10 @@ constexpr uint32_t mma_word(bool bf16, int n, bool b_n_major) {
            (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
+// What to take off an instruction word for M = 64: rows 16 w .. 16 w + 15 then lie in
+// lanes 32 w .. 32 w + 15 of tensor memory, of the product and of a left operand there.
+constexpr uint32_t kHalfRows = (uint32_t)(64 >> 4) << 24;
+
 // The same for E4M3 operands, both K-major.
 constexpr uint32_t mma_word_e4m3(int n) {
     return 1u << 4 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
