@@ -1087,21 +1087,24 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     if (warp == S::kScoreWarp) tmem_free(tmem, kTmemCols);
 }
 
-// Joins the parts of the jobs that several CTAs share, in the CTAs' order: a block
-// a job (the CTA it begins in), 32 rows (a lane each) and 32 columns (four a warp).
-// Up to kFewParts a warp adds the parts of its columns one after the other, all
-// their loads in flight; more of them are dealt to the warps, each all columns.
-constexpr int kJoinWarps = 8, kFewParts = 8;
+// Joins the parts of the jobs that several CTAs share, in the CTAs' order: a block a job
+// (the CTA it begins in; most begin none and leave at once) and 32 rows, a lane each.  A
+// warp adds its eighth of the columns over the parts, kBatch of them in flight; where they
+// are more than kFewParts, each warp takes every eighth part and 16 columns at a time, and
+// the warps' sums are added.  Two documents of 131040 tokens, 32 jobs of ten or eleven
+// parts of 128 rows: 19 us with a block for every 32 columns, 7 us as it is.
+constexpr int kJoinWarps = 8, kFewParts = 32, kBatch = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const TensorArgs t) {
-    __shared__ float4 part[kJoinWarps][8][32];
+    constexpr int kOwn = D / 4 / kJoinWarps;  // a warp's columns, in fours
+    __shared__ float4 part[kJoinWarps][4][32];
     __shared__ float part_l[kJoinWarps][32];
     pdl_wait();
     pdl_trigger();
     const int4 d0 = __ldcg(reinterpret_cast<const int4 *>(t.desc) + blockIdx.x * 2);
     const int4 d1 = __ldcg(reinterpret_cast<const int4 *>(t.desc) + blockIdx.x * 2 + 1);
-    const int base = blockIdx.y / (D / 32) * 32, columns = blockIdx.y % (D / 32) * 32;
+    const int base = blockIdx.y * 32;
     const int c0 = blockIdx.x, c1 = d0.y, kv_head = d1.x, token0 = d1.y, rows = d1.z;
     if (!d0.x || base >= rows) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, m = base + lane;
@@ -1109,73 +1112,93 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Tens
     auto ml = [&](int c, int which) {
         return __ldcg(t.part_ml + (slot(c) * 2 + which) * kRowsPerTile + m);
     };
-    auto from = [&](int c) {
-        return reinterpret_cast<const float4 *>(t.part_o) + (slot(c) * (D / 4) + columns / 4) * kRowsPerTile + m;
+    auto from = [&](int c, int four) {
+        return reinterpret_cast<const float4 *>(t.part_o) + (slot(c) * (D / 4) + four) * kRowsPerTile + m;
+    };
+    const int head = kv_head * t.group + m % t.group;
+    const long long packed = d0.w + token0 + m / t.group;
+    auto put = [&](int four, float4 x, float l) {
+        if (m >= rows) return;
+        const float inv = 1.0f / l;
+        if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+        const __nv_bfloat162 u = __floats2bfloat162_rn(x.x, x.y), v = __floats2bfloat162_rn(x.z, x.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
+                                   (long long)head * D + four * 4) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
+    };
+    auto put_lse = [&](float shift, float l) {
+        if (m < rows && t.a.lse)
+            t.a.lse[packed * t.a.n_q_heads + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
     };
     float top = -INFINITY, l = 0.0f;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c = c0; c <= c1; c += 8) {
+        float pm[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pm[i] = c + i <= c1 ? ml(c + i, 0) : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, pm[i]);
+    }
+    const float shift = top == -INFINITY ? 0.0f : top;
+    float4 x[4] = {};
+    auto add = [&](float4 *x, float f, float4 y) {
+        x->x = fmaf(f, y.x, x->x), x->y = fmaf(f, y.y, x->y), x->z = fmaf(f, y.z, x->z), x->w = fmaf(f, y.w, x->w);
+    };
     if (c1 - c0 < kFewParts) {
-        float pm[kFewParts], pl[kFewParts];
-        float4 po[kFewParts];
+#pragma unroll 1
+        for (int c = c0; c <= c1; c += kBatch) {
+            float pm[kBatch], pl[kBatch];
+            float4 po[kBatch][kOwn];
 #pragma unroll
-        for (int i = 0; i < kFewParts; ++i) {
-            const bool in = c0 + i <= c1;
-            pm[i] = in ? ml(c0 + i, 0) : -INFINITY;
-            pl[i] = in ? ml(c0 + i, 1) : 0.0f;
-            po[i] = in ? __ldcg(from(c0 + i) + warp * kRowsPerTile) : x;
-        }
+            for (int i = 0; i < kBatch; ++i) {
+                if (c + i > c1) continue;
+                pm[i] = ml(c + i, 0);
+                pl[i] = ml(c + i, 1);
 #pragma unroll
-        for (int i = 0; i < kFewParts; ++i) top = fmaxf(top, pm[i]);
-        const float shift = top == -INFINITY ? 0.0f : top;
+                for (int j = 0; j < kOwn; ++j) po[i][j] = __ldcg(from(c + i, warp * kOwn + j));
+            }
 #pragma unroll
-        for (int i = 0; i < kFewParts; ++i) {
-            if (c0 + i > c1) continue;
-            const float f = exp2_approx(pm[i] - shift);
-            l += f * pl[i];
-            x.x += f * po[i].x, x.y += f * po[i].y, x.z += f * po[i].z, x.w += f * po[i].w;
-        }
-    } else {
-#pragma unroll 8
-        for (int c = c0; c <= c1; ++c) top = fmaxf(top, ml(c, 0));
-        const float shift = top == -INFINITY ? 0.0f : top;
-        float4 o[8];
+            for (int i = 0; i < kBatch; ++i) {
+                if (c + i > c1) continue;
+                const float f = exp2_approx(pm[i] - shift);
+                l = fmaf(f, pl[i], l);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = x;
-#pragma unroll 2
-        for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
-            const float f = exp2_approx(ml(c, 0) - shift);
-            l += f * ml(c, 1);
-            const float4 *p = from(c);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float4 y = __ldcg(p + j * kRowsPerTile);
-                o[j].x += f * y.x, o[j].y += f * y.y, o[j].z += f * y.z, o[j].w += f * y.w;
+                for (int j = 0; j < kOwn; ++j) add(&x[j], f, po[i][j]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) part[warp][j][lane] = o[j];
+        for (int j = 0; j < kOwn; ++j) put(warp * kOwn + j, x[j], l);
+        if (warp == 0) put_lse(shift, l);
+        return;
+    }
+#pragma unroll 1
+    for (int four = 0; four < D / 4; four += 4) {
+        float4 o[4] = {};
+        l = 0.0f;
+#pragma unroll 4
+        for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
+            const float f = exp2_approx(ml(c, 0) - shift);
+            l = fmaf(f, ml(c, 1), l);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) add(&o[j], f, __ldcg(from(c, four + j)));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[warp][j][lane] = o[j];
         part_l[warp][lane] = l;
         __syncthreads();
-        l = 0.0f;
+        if (warp < 4) {
+            l = 0.0f;
+            float4 y = {};
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-            const float4 y = part[w][warp][lane];
-            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-            l += part_l[w][lane];
+            for (int w = 0; w < kJoinWarps; ++w) {
+                add(&y, 1.0f, part[w][warp][lane]);
+                l += part_l[w][lane];
+            }
+            put(four + warp, y, l);
+            if (four == 0 && warp == 0) put_lse(shift, l);
         }
+        __syncthreads();
     }
-    if (m >= rows) return;
-    const int head = kv_head * t.group + m % t.group;
-    const long long packed = d0.w + token0 + m / t.group;
-    const float inv = 1.0f / l, shift = top == -INFINITY ? 0.0f : top;
-    if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-    const __nv_bfloat162 u = __floats2bfloat162_rn(x.x, x.y), v = __floats2bfloat162_rn(x.z, x.w);
-    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
-                               (long long)head * D + columns + warp * 4) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
-    if (t.a.lse && columns == 0 && warp == 0)
-        t.a.lse[packed * t.a.n_q_heads + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
 }
 
 namespace {
@@ -1272,7 +1295,7 @@ TensorArgs tensor_args(const AttendArgs &a, const dspark_kv_cache &c, void *work
 template <int D>
 cudaError_t launch_join(const TensorArgs &t, int grid, int rows, cudaStream_t stream) {
     if (t.whole) return cudaSuccess;
-    return launch_pdl(attend_join_kernel<D>, dim3(grid, D / 32 * ((rows + 31) / 32)), dim3(kJoinWarps * 32), 0, stream, t);
+    return launch_pdl(attend_join_kernel<D>, dim3(grid, (rows + 31) / 32), dim3(kJoinWarps * 32), 0, stream, t);
 }
 
 template <int D>
