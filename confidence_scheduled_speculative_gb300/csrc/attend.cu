@@ -1067,57 +1067,54 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             }
             tmem_fence_before();
             ++seg;
-            // the job that begins here and ends in a later CTA, for the join
-            if (tid == 0 && walk.left <= 0) {
-                int *d = t.desc + cta * kDescInts;
-                if (s.first == 0 && !whole) {
-                    // (its last tile comes q.tiles - count units after the CTA's last)
-                    d[1] = deal.cta_of(hi - 1 + s.q.tiles - s.count, cta);
-                    d[2] = slot;
-                    d[3] = s.q.row0;
-                    d[4] = s.head;
-                    d[5] = token0;
-                    d[6] = rows;
-                    d[0] = 1;
-                }
-            }
+            if (tid == 0 && walk.left <= 0 && !whole) note_split(t, s, deal, lo, hi, seg - 1, token0, rows);
         }
     }
     __syncthreads();
     if (warp == S::kScoreWarp) tmem_free(tmem, kTmemCols);
 }
 
-// Joins the parts of the jobs that several CTAs share, in the CTAs' order: a block a job
-// (the CTA it begins in; most begin none and leave at once) and 32 rows, a lane each.  A
-// warp adds its eighth of the columns over the parts, kBatch of them in flight; where they
-// are more than kFewParts, each warp takes every eighth part and 16 columns at a time, and
-// the warps' sums are added.  Two documents of 131040 tokens, 32 jobs of ten or eleven
-// parts of 128 rows: 19 us with a block for every 32 columns, 7 us as it is.
-constexpr int kJoinWarps = 8, kFewParts = 32, kBatch = 4;
+// Joins the parts of the jobs that several CTAs share, in the CTAs' order: a block for
+// each of these CTAs but the last takes its share of the columns, four of them a warp, and
+// 32 rows, a lane each; warps to spare deal the parts among them.  Each block does little,
+// and most do nothing (a CTA whose jobs are whole), so that the launch is what it costs;
+// with one block a job instead, a call of a single token over 131040 takes 94 us, not 76.
+constexpr int kJoinWarps = 16;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const TensorArgs t) {
-    constexpr int kOwn = D / 4 / kJoinWarps;  // a warp's columns, in fours
-    __shared__ float4 part[kJoinWarps][4][32];
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) attend_join_kernel(const TensorArgs t) {
+    constexpr int kFours = D / 4;
+    __shared__ float4 part[kJoinWarps][32];
     __shared__ float part_l[kJoinWarps][32];
     pdl_wait();
     pdl_trigger();
-    const int4 d0 = __ldcg(reinterpret_cast<const int4 *>(t.desc) + blockIdx.x * 2);
-    const int4 d1 = __ldcg(reinterpret_cast<const int4 *>(t.desc) + blockIdx.x * 2 + 1);
+    int c0 = blockIdx.x;
+    auto job = [&](int i) { return __ldcg(reinterpret_cast<const int4 *>(t.desc) + c0 * 2 + i); };
+    int4 d0 = job(0), d1 = job(1);
+    if (!d0.x) {
+        if (d1.w < 0) return;
+        c0 = d1.w;
+        d0 = job(0);
+        d1 = job(1);
+    }
     const int base = blockIdx.y * 32;
-    const int c0 = blockIdx.x, c1 = d0.y, kv_head = d1.x, token0 = d1.y, rows = d1.z;
-    if (!d0.x || base >= rows) return;
+    const int c1 = d0.y, kv_head = d1.x, token0 = d1.y, rows = d1.z;
+    const int share = blockIdx.x - c0, shares = min(max(c1 - c0, 1), kFours);
+    if (base >= rows || share >= shares) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, m = base + lane;
     auto slot = [&](int c) { return (long long)(c == c0 ? d0.z : 2 * c); };
     auto ml = [&](int c, int which) {
         return __ldcg(t.part_ml + (slot(c) * 2 + which) * kRowsPerTile + m);
     };
-    auto from = [&](int c, int four) {
-        return reinterpret_cast<const float4 *>(t.part_o) + (slot(c) * (D / 4) + four) * kRowsPerTile + m;
-    };
     const int head = kv_head * t.group + m % t.group;
     const long long packed = d0.w + token0 + m / t.group;
-    auto put = [&](int four, float4 x, float l) {
+    auto from = [&](int c, int four) {
+        return __ldcg(reinterpret_cast<const float4 *>(t.part_o) + (slot(c) * kFours + four) * kRowsPerTile + m);
+    };
+    auto add = [](float4 &x, float f, float4 y) {
+        x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
+    };
+    auto put = [&](int four, float4 x, float shift, float l) {
         if (m >= rows) return;
         const float inv = 1.0f / l;
         if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1126,79 +1123,72 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Tens
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
                                    (long long)head * D + four * 4) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
-    };
-    auto put_lse = [&](float shift, float l) {
-        if (m < rows && t.a.lse)
+        if (t.a.lse && four == 0)
             t.a.lse[packed * t.a.n_q_heads + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
     };
-    float top = -INFINITY, l = 0.0f;
-    for (int c = c0; c <= c1; c += 8) {
-        float pm[8];
+    const int begin = share * kFours / shares, end = (share + 1) * kFours / shares;
+    float top = -INFINITY;
+    if (end - begin > kJoinWarps) {
+        // then there are two parts: all loads before the first use
+        constexpr int kOwn = kFours / kJoinWarps, kParts = 2;
+        float pm[kParts], pl[kParts], l = 0.0f;
+        float4 po[kParts][kOwn], x[kOwn] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) pm[i] = c + i <= c1 ? ml(c + i, 0) : -INFINITY;
+        for (int i = 0; i < kParts; ++i) {
+            pm[i] = c0 + i <= c1 ? ml(c0 + i, 0) : -INFINITY;
+            pl[i] = c0 + i <= c1 ? ml(c0 + i, 1) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, pm[i]);
-    }
-    const float shift = top == -INFINITY ? 0.0f : top;
-    float4 x[4] = {};
-    auto add = [&](float4 *x, float f, float4 y) {
-        x->x = fmaf(f, y.x, x->x), x->y = fmaf(f, y.y, x->y), x->z = fmaf(f, y.z, x->z), x->w = fmaf(f, y.w, x->w);
-    };
-    if (c1 - c0 < kFewParts) {
-#pragma unroll 1
-        for (int c = c0; c <= c1; c += kBatch) {
-            float pm[kBatch], pl[kBatch];
-            float4 po[kBatch][kOwn];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (c + i > c1) continue;
-                pm[i] = ml(c + i, 0);
-                pl[i] = ml(c + i, 1);
-#pragma unroll
-                for (int j = 0; j < kOwn; ++j) po[i][j] = __ldcg(from(c + i, warp * kOwn + j));
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (c + i > c1) continue;
-                const float f = exp2_approx(pm[i] - shift);
-                l = fmaf(f, pl[i], l);
-#pragma unroll
-                for (int j = 0; j < kOwn; ++j) add(&x[j], f, po[i][j]);
+            for (int j = 0; j < kOwn; ++j) {
+                const int four = begin + warp + j * kJoinWarps;
+                if (c0 + i <= c1 && four < end) po[i][j] = from(c0 + i, four);
             }
         }
 #pragma unroll
-        for (int j = 0; j < kOwn; ++j) put(warp * kOwn + j, x[j], l);
-        if (warp == 0) put_lse(shift, l);
+        for (int i = 0; i < kParts; ++i) top = fmaxf(top, pm[i]);
+        const float shift = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            if (c0 + i > c1) continue;
+            const float f = exp2_approx(pm[i] - shift);
+            l = fmaf(f, pl[i], l);
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j)
+                if (begin + warp + j * kJoinWarps < end) add(x[j], f, po[i][j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+            if (begin + warp + j * kJoinWarps < end) put(begin + warp + j * kJoinWarps, x[j], shift, l);
         return;
     }
-#pragma unroll 1
-    for (int four = 0; four < D / 4; four += 4) {
-        float4 o[4] = {};
-        l = 0.0f;
+    // a four of columns a warp; warps to spare deal the parts among them
+    const int n = end - begin, deals = kJoinWarps / n, deal = warp / n, four = begin + warp % n;
 #pragma unroll 4
-        for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
+    for (int c = c0 + warp; c <= c1; c += kJoinWarps) top = fmaxf(top, ml(c, 0));
+    part_l[warp][lane] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, part_l[w][lane]);
+    const float shift = top == -INFINITY ? 0.0f : top;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+    if (deal < deals) {
+#pragma unroll 4
+        for (int c = c0 + deal; c <= c1; c += deals) {
             const float f = exp2_approx(ml(c, 0) - shift);
             l = fmaf(f, ml(c, 1), l);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) add(&o[j], f, __ldcg(from(c, four + j)));
+            add(x, f, from(c, four));
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[warp][j][lane] = o[j];
-        part_l[warp][lane] = l;
-        __syncthreads();
-        if (warp < 4) {
-            l = 0.0f;
-            float4 y = {};
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) {
-                add(&y, 1.0f, part[w][warp][lane]);
-                l += part_l[w][lane];
-            }
-            put(four + warp, y, l);
-            if (four == 0 && warp == 0) put_lse(shift, l);
-        }
-        __syncthreads();
     }
+    __syncthreads();
+    part[warp][lane] = x;
+    part_l[warp][lane] = l;
+    __syncthreads();
+    if (deal > 0) return;
+    for (int w = warp + n; w < n * deals; w += n) {
+        add(x, 1.0f, part[w][lane]);
+        l += part_l[w][lane];
+    }
+    put(four, x, shift, l);
 }
 
 namespace {

@@ -486,18 +486,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
             }
         }
         if (tid == 0) {
-            // the job that begins here and ends in a later CTA, for the join
-            if (ctl.seg[k + 1 & 3].count == 0 && s.first == 0 && !whole) {
-                int *d = t.desc + cta * kDescInts;
-                // (its last tile comes q.tiles - count units after the CTA's last)
-                d[1] = deal.cta_of(hi - 1 + s.q.tiles - s.count, cta);
-                d[2] = slot;
-                d[3] = s.q.row0;
-                d[4] = s.head;
-                d[5] = token0;
-                d[6] = rows;
-                d[0] = 1;
-            }
+            if (ctl.seg[k + 1 & 3].count == 0 && !whole) note_split(t, s, deal, lo, hi, k, token0, rows);
             leave(k + 2);
             ctl.nonfinite[k + 1 & 1] = 0;
         }

@@ -203,7 +203,10 @@ __device__ __forceinline__ bool share_of(const TensorArgs &t, Begin *begin, long
     // (a CTA with less than two tiles to do would cost more than it brings)
     const int n_ctas =
         (int)min((long long)gridDim.x, t.whole ? T : (T + kJobCost + 1) / (kJobCost + 2));
-    if (tid == 0 && !t.whole) t.desc[cta * kDescInts] = 0;
+    if (tid == 0 && !t.whole) {
+        t.desc[cta * kDescInts] = 0;
+        t.desc[cta * kDescInts + 7] = -1;
+    }
     if (cta >= n_ctas) return false;
     deal->n = n_ctas;
     deal->each = div_nonneg(T, n_ctas);
@@ -229,6 +232,27 @@ __device__ __forceinline__ bool share_of(const TensorArgs &t, Begin *begin, long
         }
     }
     return true;
+}
+
+// Tells the join, after a CTA's last segment s (its k-th) that is not a whole job, of
+// the job that begins here and ends in a later CTA, or of the one that the whole of
+// this CTA lies in.
+__device__ __forceinline__ void note_split(const TensorArgs &t, const Segment &s, const Deal &deal,
+                                           long long lo, long long hi, unsigned k, int token0, int rows) {
+    const int cta = blockIdx.x;
+    int *d = t.desc + cta * kDescInts;
+    if (s.first == 0) {
+        // (its last tile comes q.tiles - count units after the CTA's last)
+        d[1] = deal.cta_of(hi - 1 + s.q.tiles - s.count, cta);
+        d[2] = 2 * cta + (k > 0);
+        d[3] = s.q.row0;
+        d[4] = s.head;
+        d[5] = token0;
+        d[6] = rows;
+        d[0] = 1;
+    } else if (k == 0 && s.first + s.count < s.q.tiles) {
+        d[7] = deal.cta_of(lo - s.first, 0);  // where its first tile is
+    }
 }
 
 }  // namespace dspark
