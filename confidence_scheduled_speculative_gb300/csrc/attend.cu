@@ -27,11 +27,12 @@
 //   that one's softmax runs beside the other's products; the tiles of all jobs are dealt
 //   evenly to them (schedule.cuh), so jobs are split along the positions where there are
 //   few, and attend_join_kernel adds the parts in a fixed order.
-//   Over bfloat16 the bound is HBM: 16 requests with windows, 8 query heads a kv head,
-//   557 MB in 103 us (5.4 TB/s, 0.79 of a copy); 4.4 GB in 760 us (5.8 TB/s, 0.85).
-//   Over E4M3 half the bytes take the same steps and the bound is a step's chain of
-//   waits, scores, exponentials and conversions (2300 cycles of a warp): two requests of
-//   up to 131072 tokens with 160 rows a kv head, read twice, 522 MB in 297 us (1.8 TB/s).
+//   Over bfloat16 the bound is HBM: 32 requests of up to 8192 tokens with windows of up
+//   to nine and 32 query heads, 557 MB, in 98 to 102 us by box (5.5 TB/s, 0.81 of a copy);
+//   256 requests with up to 17 and 64 heads, 4.4 GB, in 757 to 777 us (5.7 TB/s, 0.84).
+//   Over E4M3 half the bytes take the same steps, and the bound is a step's softmax and
+//   conversions with the waits between them: two requests of up to 131040 tokens with 160
+//   rows a kv head, read twice, 522 MB in 298 us (1.75 TB/s, 0.26; issue slots half used).
 //   There few rows go to attend_few_kernel (fewrows.cuh).
 
 #include "fewrows.cuh"
