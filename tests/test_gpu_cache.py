@@ -354,3 +354,31 @@ def test_argument_errors(api, dev):
     with pytest.raises(ValueError):
         api.dspark_qk_norm_rope(None, None, status=st)
     assert int(st) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_codes_are_the_rounded_quotients(api, dev, D):
+    """Every code is the 32-bit quotient x / scale rounded to nearest even, bit for
+    bit, for heads of all magnitudes with large and small elements."""
+    rows, heads, page = 4096, 8, 64
+    g = torch.Generator("cuda").manual_seed(60)
+    x = torch.randn((rows, heads, D), generator=g, device="cuda")
+    x *= torch.exp2(torch.randint(-90, 90, (rows, heads, 1), generator=g, device="cuda").float())
+    x *= torch.exp2(torch.randint(-12, 1, x.shape, generator=g, device="cuda").float())
+    i32 = dict(dtype=torch.int32, device="cuda")
+    k, v = (torch.zeros((rows // page, page, heads, D), device="cuda", dtype=torch.uint8)
+            .view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.zeros((rows // page, heads, page), device="cuda") for _ in range(2))
+    kv = api.KVCache(k, v, torch.arange(rows // page, **i32).view(1, -1), ks, vs)
+    status = torch.zeros(1, **i32)
+    api.dspark_kv_append(x, -x, kv, req=torch.zeros(rows, **i32), pos=torch.arange(rows, **i32),
+                         status=status)
+    torch.cuda.synchronize()
+    # (by 64 bits: a quotient of 24-bit numbers rounded twice this way is the quotient
+    # rounded once, while torch may divide by a number as it multiplies by its inverse)
+    scale = (x.abs().amax(-1).double() / 448).float().clamp_min(2.0 ** -100)
+    want = (x.double() / scale[..., None].double()).float().to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(ks.transpose(1, 2).reshape(rows, heads), scale)
+    assert torch.equal(k.view(torch.uint8).view(rows, heads, D), want)
+    assert torch.equal(v.view(torch.uint8).view(rows, heads, D), want ^ 0x80)
+    assert int(status) == 0
