@@ -36,8 +36,8 @@ constexpr int kAppendThreads = 128;
 // heads a lane group has in flight: 64 bytes a lane
 template <typename T>
 constexpr int kHeadsPerLane = 16 / sizeof(T) / 2;
-// Warps an SM before a warp takes all heads of a row: 256 requests of up to 17 tokens take 23 us
-// at 48, 28 at 24 and below, 31 at 96.
+// Warps an SM before a warp takes all heads of a row: a window of 256 requests of up to
+// 17 tokens takes 20 us at 48, 26 at 24 and below, 26 at 96.
 constexpr int kWarpsWanted = 48;
 constexpr int kReadThreads = 256;
 constexpr int kReadRows = 16;  // long prefixes 132 us; of 32 rows 137, of 64 139
