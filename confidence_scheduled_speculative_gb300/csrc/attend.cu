@@ -340,8 +340,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             unsigned seg = 0;
             bool ok = true, few_before = false;
             auto wait = [&](unsigned long long *bar, unsigned parity) {
-                ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
-                return ok = __all_sync(kFullMask, ok);
+                return ok = warp_wait(ok, smem_addr(bar), parity, abort, a.status);
             };
             while (ok && walk.next(t, &s)) {
                 // this lane's box of each tile; a page outside the pool, as past
@@ -427,8 +426,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             unsigned done = 0, seg = 0;  // tiles and segments so far
             bool ok = true;
             auto wait = [&](unsigned long long *bar, unsigned parity) {
-                ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
-                return ok = __all_sync(kFullMask, ok);
+                return ok = warp_wait(ok, smem_addr(bar), parity, abort, a.status);
             };
             // over E4M3 keys have a ring of their own; else the loads lie in one, K0, K1,
             // V0, K2, V1, ..., V(n-1)
@@ -576,9 +574,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                         }
                         // the tile before last is through with its scales
                         if (tile >= 2)
-                            ok = ok && role_wait(smem_addr(&ctl.o_done[b]), (tile >> 1) + 1 & 1, abort,
-                                                 a.status);
-                        if (!(ok = __all_sync(kFullMask, ok))) break;
+                            ok = warp_wait(ok, smem_addr(&ctl.o_done[b]), (tile >> 1) + 1, abort, a.status);
+                        if (!ok) break;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             sc.k[b][lane + 32 * j] = k[j];
@@ -607,8 +604,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
             unsigned done = 0, seg = 0;
             bool ok = true;
             auto wait = [&](unsigned long long *bar, unsigned parity) {
-                ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
-                return ok;
+                return ok = warp_wait(ok, smem_addr(bar), parity, abort, a.status);
             };
             // Their place is chunks 2 part and 2 part + 1 of the token's row.  Lanes of one
             // half start with the one, of the other with the other, so that eight lanes
@@ -765,8 +761,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
         unsigned done = 0, seg = 0;
         bool ok = true;
         auto wait = [&](unsigned long long *bar, unsigned parity) {
-            ok = ok && role_wait(smem_addr(bar), parity & 1, abort, a.status);
-            return ok;
+            return ok = warp_wait(ok, smem_addr(bar), parity, abort, a.status);
         };
         for (;;) {
             // a warp that gave up still comes to the four warps' barriers
@@ -946,8 +941,8 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
                                 other[k] = r;
                             }
                     }
+                    tmem_wait_store();  // before giving up too: the columns are about to be freed
                     if (!ok) break;
-                    tmem_wait_store();
                 }
                 if (!kQuant && p0 + kTile > s.q.P) {
                     // Values past the request's end become zeros, and so do NaN

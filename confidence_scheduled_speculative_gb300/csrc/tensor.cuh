@@ -41,6 +41,15 @@ __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// The same for a whole warp that has come this far (`ok`), with one answer for all its
+// lanes: what follows a wait are instructions that the warp executes as a whole
+// (tensor memory, shuffles, barriers), so no lane may go on where another gives up.
+// Every role of attend.cu waits through this.
+__device__ __forceinline__ bool warp_wait(bool ok, uint32_t bar, uint32_t parity, volatile int *abort,
+                                          int32_t *status) {
+    return __all_sync(0xFFFFFFFFu, ok && role_wait(bar, parity & 1, abort, status));
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
