@@ -29,14 +29,18 @@ __device__ __forceinline__ Window load_window(const AttendArgs &a, int r) {
     return {__ldg(a.cu + r), __ldg(a.cu + r + 1), __ldg(a.prefix + r)};
 }
 
+// A request's last position is below this: the kernels count positions in 32 bits and
+// step past the end, by at most 32 steps of 128 (the few-row kernel's look ahead).
+constexpr long long kMaxPositions = (1ll << 31) - 8192;
+
 // Whether a window has rows and can be used; with `report`, flags why not.
 __device__ __forceinline__ bool usable(const AttendArgs &a, const Window &w, bool report) {
     if (w.hi == w.lo) return false;
     int bad = 0;
     if (w.lo < 0 || w.hi < w.lo || w.hi - w.lo > DSPARK_MAX_WINDOW || w.hi > a.max_rows)
         bad = DSPARK_STATUS_BAD_LEN;
-    else if (w.P < 0 ||
-             (long long)w.P + (w.hi - w.lo) > (long long)a.cache.table_width * a.cache.page_size)
+    else if (w.P < 0 || (long long)w.P + (w.hi - w.lo) >
+                            min((long long)a.cache.table_width * a.cache.page_size, kMaxPositions))
         bad = DSPARK_STATUS_BAD_INDEX;
     if (bad && report) flag(a.status, bad);
     return !bad;

@@ -759,9 +759,9 @@ DSPARK_API size_t dspark_tree_attention_workspace_bytes(int32_t n_q_heads, int32
  * The order of all sums is fixed by the lengths: a call repeated gives the
  * same bits.
  * A window of more than 32 tokens or outside max_rows (BAD_LEN), and positions
- * past the block table or a page outside the pool (BAD_INDEX): that request's
- * rows are unspecified, the others not affected.  Rows of no request are left
- * alone.
+ * past the block table, positions from 2^31 - 8192 on or a page outside the pool
+ * (BAD_INDEX): that request's rows are unspecified, the others not affected.
+ * Rows of no request are left alone.
  * Errors: INVALID_ARG (null pointer, B outside 1..n_requests, n_q_heads not a
  * positive multiple of n_kv_heads, dtype, a stride below a row, max_rows < 0,
  * scale not finite, the cache's); UNSUPPORTED (head_dim); WORKSPACE; CUDA. */

@@ -1,0 +1,40 @@
+"""Calls of the attention side of a window that have to be refused or flagged, each
+beside what has to go on working."""
+
+import math
+
+import pytest
+import torch
+
+import window_oracle as wo
+from gpu_helpers import require_gpu
+from test_gpu_attention import Problem
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api():
+    require_gpu()
+    from confidence_scheduled_speculative_gb300 import api
+    return api
+
+
+# A bfloat16 cache and an E4M3 one on the tensor cores (the latter with eight query rows
+# a step and, nine heads a key head, with 64), and 32 bits.
+KINDS = [("bf16", "bf16", 2, 64), ("e4m3", "bf16", 4, 64), ("e4m3", "bf16", 9, 128), ("f32", "f32", 2, 64)]
+
+
+@pytest.mark.parametrize("kind,dtype,group,D", KINDS)
+@pytest.mark.parametrize("first", [2 ** 31 - 5, 2 ** 31 - 8195])
+def test_positions_that_32_bits_cannot_count(api, kind, dtype, group, D, first):
+    """A table that lists 2^31 positions: the last of them are more than the kernels'
+    counters hold.  The request is flagged, the others come out right."""
+    page = 1 << 16
+    p = Problem(500, [40, 100, 700], [4, 4, 3], group, 1, D, page, kind, dtype=dtype)
+    table = torch.zeros((3, (1 << 31) // page), dtype=torch.int32, device="cuda")
+    table[:, :p.cache.table.size(1)] = p.cache.table
+    p.cache.table = table
+    p.prefix_lens[1] = first
+    p.run(api).check(skip=(1,))
+    assert int(p.status) == api.STATUS_BAD_INDEX
