@@ -762,8 +762,9 @@ def dspark_tree_attention(q, cache: KVCache, *, cu_seqlens, prefix_lens, scale, 
     """Attention of the packed window's rows ``q`` [rows, n_q_heads, head_dim]
     over ``cache``: every position before the request's prefix length and the
     window's tokens whose bit is set in the row's ``ancestors`` word (int32
-    bits [rows]; None: a chain).  ``out`` like ``q``; ``lse`` fp32 [rows,
-    n_q_heads], optional."""
+    bits [rows]; None: a chain).  ``out`` like ``q`` and beside it, not over it
+    (slices of one buffer's rows will do); ``lse`` fp32 [rows, n_q_heads],
+    optional."""
     hq, dim = q.size(1), cache.head_dim
     code = _dtype_code(q)
     max_rows = q.size(0) if max_rows is None else max_rows

@@ -1231,6 +1231,26 @@ bool encode(CUtensorMap *map, const void *p, int elem_bytes, int width, bool swi
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether any of `rows` rows of `bytes` at a, ld_a bytes apart, shares a byte with one
+// of those at b (no stride is below `bytes`).  Slices of one buffer, side by side or
+// one after the other, do not.
+bool rows_overlap(const void *a, int64_t ld_a, const void *b, int64_t ld_b, int64_t rows, int64_t bytes) {
+    const int64_t x = (int64_t)reinterpret_cast<uintptr_t>(a), y = (int64_t)reinterpret_cast<uintptr_t>(b);
+    if (y >= x + (rows - 1) * ld_a + bytes || x >= y + (rows - 1) * ld_b + bytes) return false;
+    // the rows of b that begin last before, and first after, the begin of a row of a
+    // (with equal strides one row of a stands for all)
+    for (int64_t i = 0; i < (ld_a == ld_b ? 1 : rows); ++i) {
+        const int64_t from = x + i * ld_a - y;
+        const int64_t first = from / ld_b - (from % ld_b < 0);
+        for (int64_t j = first; j <= first + 1; ++j) {
+            const bool there = ld_a == ld_b ? j > -rows && j < rows : j >= 0 && j < rows;
+            const int64_t off = j * ld_b - from;
+            if (there && off < bytes && off > -bytes) return true;
+        }
+    }
+    return false;
+}
+
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t part_o_bytes(int D) { return (size_t)2 * kMaxCtas * kRowsPerTile * D * 4; }
@@ -1358,6 +1378,10 @@ extern "C" int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype,
         workspace_bytes < dspark_tree_attention_workspace_bytes(n_q_heads, cache->head_dim))
         return DSPARK_ERR_WORKSPACE;
     if (max_rows == 0) return DSPARK_OK;
+    // (a split job reads its queries again after another CTA has written its outputs)
+    const int64_t e_bytes = kv_elem_bytes(dtype);
+    if (rows_overlap(q, ld_q * e_bytes, out, ld_out * e_bytes, max_rows, width * e_bytes))
+        return DSPARK_ERR_INVALID_ARG;
     AttendArgs a;
     a.q = q;
     a.ld_q = ld_q;

@@ -745,7 +745,8 @@ DSPARK_API size_t dspark_tree_attention_workspace_bytes(int32_t n_q_heads, int32
  * A row that sees nothing gets out = 0 and lse = -inf.  What a row does not
  * see has no effect on it, NaN and infinities included.
  *   q, out       [max_rows, n_q_heads * head_dim] rows of `dtype` (BF16 or
- *                F32), ld_* elements apart
+ *                F32), ld_* elements apart; out must not share an element with
+ *                q (slices of one buffer's rows will do)
  *   lse          [max_rows, n_q_heads] fp32, nullable
  *   prefix_lens  device [B], >= 0; cu_seqlens device [B+1]; window length 0 is
  *                a request without rows
@@ -764,7 +765,8 @@ DSPARK_API size_t dspark_tree_attention_workspace_bytes(int32_t n_q_heads, int32
  * Rows of no request are left alone.
  * Errors: INVALID_ARG (null pointer, B outside 1..n_requests, n_q_heads not a
  * positive multiple of n_kv_heads, dtype, a stride below a row, max_rows < 0,
- * scale not finite, the cache's); UNSUPPORTED (head_dim); WORKSPACE; CUDA. */
+ * scale not finite, out over q, the cache's); UNSUPPORTED (head_dim, more than
+ * 65535 query heads); WORKSPACE; CUDA. */
 DSPARK_API int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype, int32_t n_q_heads,
                                      int32_t max_rows, const int32_t *cu_seqlens,
                                      const int32_t *prefix_lens, int32_t B,

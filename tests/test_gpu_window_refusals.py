@@ -38,3 +38,26 @@ def test_positions_that_32_bits_cannot_count(api, kind, dtype, group, D, first):
     p.prefix_lens[1] = first
     p.run(api).check(skip=(1,))
     assert int(p.status) == api.STATUS_BAD_INDEX
+
+
+def test_output_beside_the_queries(api):
+    """Queries and outputs as slices of one buffer: side by side, after one another, and
+    in rows of different strides.  Over one another they are refused, and nothing is
+    written."""
+    for kind, dtype, group, D in KINDS:
+        p = Problem(510, [600, 30], [9, 5], group, 1, D, 64, kind, dtype=dtype, pad=0)
+        n = p.rows
+        both = torch.zeros((2 * n, 2 * group, D), device="cuda", dtype=p.dtype)
+        for q, out in ((both[:n, :group], both[:n, group:]), (both[n:, group:], both[:n, group:]),
+                       (both[:n, group:], both.view(4 * n, group, D)[2 * n:3 * n])):
+            q.copy_(p.q)
+            p.q, p.out = q, out
+            p.run(api).check()
+            assert int(p.status) == 0
+        before = both.clone()
+        for q, out in ((both[:n, :group], both[:n, :group]), (both[:n, :group], both[1:n + 1, :group]),
+                       (both[:n, :group], both.view(4 * n, group, D)[:n])):
+            p.q, p.out = q, out
+            with pytest.raises(api.DsparkError):
+                p.run(api)
+        assert torch.equal(before, both)
