@@ -56,6 +56,9 @@ __global__ void __launch_bounds__(kAnyWarps * 32) attend_any_kernel(AttendArgs a
     pdl_wait();
     const int row = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int D = a.cache.head_dim;
+    // (the requests' windows are looked at by one CTA: a window outside the rows has none)
+    if (row == 0 && h == 0)
+        for (int r = threadIdx.x; r < a.B; r += kAnyWarps * 32) usable(a, load_window(a, r), true);
     if (row >= __ldg(a.cu + a.B)) return;
     int lo = 0, hi = a.B - 1;  // the last request that starts at or before the row
     while (lo < hi) {
@@ -65,7 +68,7 @@ __global__ void __launch_bounds__(kAnyWarps * 32) attend_any_kernel(AttendArgs a
     }
     const int r = lo;
     const Window win = load_window(a, r);
-    if (!usable(a, win, threadIdx.x == 0) || row < win.lo) return;
+    if (!usable(a, win, false) || row < win.lo) return;
     const int row0 = win.lo, len = win.hi - win.lo, P = win.P;
     const unsigned bits = ancestors_of(a, row, row - row0, len);
     const int kh = h / (a.n_q_heads / a.cache.n_kv_heads);

@@ -61,3 +61,25 @@ def test_output_beside_the_queries(api):
             with pytest.raises(api.DsparkError):
                 p.run(api)
         assert torch.equal(before, both)
+
+
+@pytest.mark.parametrize("kind,dtype,group,D", KINDS)
+def test_windows_outside_the_rows(api, kind, dtype, group, D):
+    """A window that begins behind the last row, or ends before it begins, is flagged in
+    every kernel, not left out without a word."""
+    def call(p, rows):
+        ws = api.workspace(api.dspark_tree_attention_workspace_bytes(p.hq, p.D))
+        api.dspark_tree_attention(p.q, p.cache.kv(), cu_seqlens=p.cu, prefix_lens=p.prefix_lens,
+                                  scale=p.scale, out=p.out, lse=p.lse, workspace=ws, status=p.status,
+                                  max_rows=rows)
+        torch.cuda.synchronize()
+
+    p = Problem(520, [40, 20, 33], [4, 3, 2], group, 1, D, 64, kind, dtype=dtype)
+    call(p, 7)  # the third request's rows are 7 and 8
+    p.rows = 7
+    p.check(skip=(2,))
+    assert int(p.status) == api.STATUS_BAD_LEN
+    p = Problem(521, [40, 20, 33], [4, 3, 0], group, 1, D, 64, kind, dtype=dtype)
+    p.cu[3] = 5  # the third request: rows 7 to 5
+    call(p, 7)
+    assert int(p.status) == api.STATUS_BAD_LEN
