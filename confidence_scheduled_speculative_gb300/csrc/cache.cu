@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(AppendArgs a,
                         *reinterpret_cast<Raw *>(p + (at1 - at0)) = Four<T>::pack(x + 4);
                     }
                 } else if constexpr (kCache) {
-                    const bool write = mine && page >= 0 && (kKind == 2 || angle);
+                    const bool write = mine && page >= 0 && angle;
                     const long long at = slot + (long long)i * groups * a.cache.head_stride;
                     if constexpr (std::is_same<C, e4m3>::value) {
                         unsigned m = 0;
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_any_kernel(AppendArgs a
     while (head >= a.heads[kind]) head -= a.heads[kind++];
     if (a.req && __ldg(a.req + row) < 0) return;
     int p;
-    if (kind < 2 && !row_angle(a, row, &p)) return;
+    if (!row_angle(a, row, &p)) return;
     int page = -1, token = 0;
     if (kCache && kind > 0 && !row_slot(a, row, &page, &token)) return;
 

@@ -702,7 +702,8 @@ DSPARK_API int dspark_qk_norm_rope(const void *q, int64_t ld_q, const void *k, i
  * an infinity reads back as NaN and flags DSPARK_STATUS_BAD_INPUT.
  * A request >= n_requests, a cache position outside the block table or a page
  * outside the pool flags DSPARK_STATUS_BAD_INDEX, and that row's keys and
- * values are not written.  Two rows of a call must not share a slot.
+ * values are not written; with cos_sin, a position outside [0, n_pos) flags the
+ * same, and nothing of that row is written.  Two rows of a call must not share a slot.
  * Errors as above, and for the cache: INVALID_ARG (null pointers, dtype,
  * counts < 1, negative strides, E4M3 without scales). */
 DSPARK_API int dspark_kv_append(const void *q, int64_t ld_q, const void *k, int64_t ld_k,

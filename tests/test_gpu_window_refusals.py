@@ -83,3 +83,24 @@ def test_windows_outside_the_rows(api, kind, dtype, group, D):
     p.cu[3] = 5  # the third request: rows 7 to 5
     call(p, 7)
     assert int(p.status) == api.STATUS_BAD_LEN
+
+
+@pytest.mark.parametrize("kind,dtype,D", [("bf16", "bf16", 64), ("e4m3", "bf16", 128), ("f32", "f32", 34)])
+def test_a_row_that_cannot_be_rotated_is_not_stored(api, kind, dtype, D):
+    """A position outside the rotation's table: neither the row's key nor its value (nor
+    its query) is written, so that the slot keeps what it held as a whole."""
+    gen = torch.Generator().manual_seed(530)
+    c = wo.Cache(gen, kind, [40], 2, D, 16)
+    x = torch.randn((4, 6, D), device="cuda").to(wo.DTYPES[dtype])
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cos_sin = torch.zeros((10, 2), device="cuda")
+    before = {n: c.values(n, 0, 0, 40) for n in "kv"}
+    q_out, status = torch.full((4, 2, D), 7.0, device="cuda", dtype=x.dtype), torch.zeros(1, **i32)
+    api.dspark_kv_append(x[:, 2:4], x[:, 4:], c.kv(), q=x[:, :2], q_out=q_out, req=torch.zeros(4, **i32),
+                         pos=torch.tensor([9, 10, -1, 0], **i32), cache_pos=torch.tensor([5, 6, 7, 39], **i32),
+                         cos_sin=cos_sin, status=status)
+    assert int(status) == api.STATUS_BAD_INDEX
+    assert bool((q_out[1:3] == 7).all()) and bool((q_out[[0, 3]] != 7).all())
+    for n, t in before.items():
+        same = (c.values(n, 0, 0, 40) == t).flatten(1).all(1)
+        assert same.nonzero()[:, 0].tolist() == [p for p in range(40) if p not in (5, 39)], n
