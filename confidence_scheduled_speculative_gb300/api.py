@@ -635,6 +635,9 @@ class KVCache:
         self.ref = ctypes.byref(self.desc)
 
 
+_NO_ROWS = 256  # a tensor without elements has no address; one that is never read stands for it
+
+
 def _rows(t: torch.Tensor, name: str, dtype, heads: int, dim: int, rows: int) -> tuple[int, int]:
     """Pointer and row stride of [rows, heads, head_dim] rows: heads packed,
     any row stride."""
@@ -650,7 +653,7 @@ def _rows(t: torch.Tensor, name: str, dtype, heads: int, dim: int, rows: int) ->
         raise ValueError(f"{name}: expected {heads} heads of {dim} elements, got {h} of {d}")
     if n < rows:
         raise ValueError(f"{name}: expected at least {rows} rows, got {n}")
-    return t.data_ptr(), ld if n > 1 else max(ld, h * d)
+    return t.data_ptr() if n else _NO_ROWS, ld if n > 1 else max(ld, h * d)
 
 
 def _index(t, n, name):
@@ -661,7 +664,7 @@ def _index(t, n, name):
         return _p(t, torch.int32, name)  # says what is wrong
     if t.numel() < n:
         raise ValueError(f"{name}: expected at least {n} elements, got {t.numel()}")
-    return t.data_ptr()
+    return t.data_ptr() if t.numel() else _NO_ROWS
 
 
 def _norm_rope(dtype, dim, q_weight, k_weight, eps, cos_sin, interleaved):

@@ -104,3 +104,25 @@ def test_a_row_that_cannot_be_rotated_is_not_stored(api, kind, dtype, D):
     for n, t in before.items():
         same = (c.values(n, 0, 0, 40) == t).flatten(1).all(1)
         assert same.nonzero()[:, 0].tolist() == [p for p in range(40) if p not in (5, 39)], n
+
+
+def test_windows_without_rows(api):
+    """A step in which no row is left: every call takes tensors of no rows and does
+    nothing."""
+    c = wo.Cache(torch.Generator().manual_seed(540), "bf16", [40, 3], 2, 64, 16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.zeros((0, 8, 64), device="cuda", dtype=torch.bfloat16)
+    none, status = torch.zeros(0, **i32), torch.zeros(1, **i32)
+    before = [t.clone() for t in (c.k, c.v)]
+    api.dspark_qk_norm_rope(x[:, :4], x[:, 4:6], pos=none, cos_sin=torch.ones((9, 64), device="cuda"),
+                            status=status)
+    api.dspark_kv_append(x[:, 4:6], x[:, 6:], c.kv(), q=x[:, :4], req=none, pos=none, status=status)
+    zeros = torch.zeros(3, **i32)
+    api.dspark_kv_read(c.kv(), start=zeros[:2], cu_rows=zeros, k_out=x[:, :2], v_out=x[:, 2:4],
+                       status=status)
+    ws = api.workspace(api.dspark_tree_attention_workspace_bytes(4, 64))
+    api.dspark_tree_attention(x[:, :4], c.kv(), cu_seqlens=zeros, prefix_lens=zeros[:2], scale=0.125,
+                              out=x[:, 4:], ancestors=none, lse=torch.zeros((0, 4), device="cuda"),
+                              workspace=ws, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and all(torch.equal(a, b) for a, b in zip(before, (c.k, c.v)))
