@@ -694,6 +694,8 @@ def dspark_qk_norm_rope(q, k, *, status, pos=None, totals=None, q_weight=None, k
     args = []
     for name, t, o in (("q", q, q_out), ("k", k, k_out)):
         if t is None:
+            if o is not None:
+                raise ValueError(f"{name}_out: expected with {name} only")
             args.append((None, 0, None, 0, 0))
             continue
         heads = t.size(1)
@@ -721,6 +723,8 @@ def dspark_kv_append(k, v, cache: KVCache, *, req, status, pos=None, cache_pos=N
     max_rows = k.size(0) if max_rows is None else max_rows
     qp = lq = qo = lqo = None
     hq = 0
+    if q is None and q_out is not None:
+        raise ValueError("q_out: expected with q only")
     if q is not None:
         hq = q.size(1)
         qp, lq = _rows(q, "q", dtype, hq, dim, max_rows)

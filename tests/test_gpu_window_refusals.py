@@ -1,8 +1,6 @@
 """Calls of the attention side of a window that have to be refused or flagged, each
 beside what has to go on working."""
 
-import math
-
 import pytest
 import torch
 
@@ -126,3 +124,16 @@ def test_windows_without_rows(api):
                               workspace=ws, status=status)
     torch.cuda.synchronize()
     assert int(status) == 0 and all(torch.equal(a, b) for a, b in zip(before, (c.k, c.v)))
+
+
+def test_outputs_without_their_inputs(api):
+    """An output whose input is not given would stay unwritten: refused."""
+    c = wo.Cache(torch.Generator().manual_seed(550), "bf16", [40], 2, 64, 16)
+    x = torch.zeros((3, 8, 64), device="cuda", dtype=torch.bfloat16)
+    i, status = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="q_out"):
+        api.dspark_kv_append(x[:, :2], x[:, 2:4], c.kv(), req=i, pos=i, q_out=x[:, 4:], status=status)
+    with pytest.raises(ValueError, match="k_out"):
+        api.dspark_qk_norm_rope(x[:, :2], None, k_out=x[:, 4:], status=status)
+    with pytest.raises(ValueError, match="q_out"):
+        api.dspark_qk_norm_rope(None, x[:, :2], q_out=x[:, 4:], status=status)
