@@ -48,15 +48,17 @@ class PagedCache:
         self.workspace = api.workspace(
             api.dspark_tree_attention_workspace_bytes(n_q_heads, head_dim), device)
 
-    def append(self, q, k, v, *, req, pos, status, totals=None, q_out=None, norm=None, cos_sin=None,
-               stream=None) -> None:
+    def append(self, q, k, v, *, req, pos, status, cache_pos=None, totals=None, q_out=None, norm=None,
+               cos_sin=None, stream=None) -> None:
         """The window's keys and values into their pages, its queries
         normalised and rotated in the same pass (in place, or to ``q_out``).
-        ``norm``: the query's and the key's norm weights."""
+        ``norm``: the query's and the key's norm weights.  ``cache_pos``: where
+        the rows are stored, if that is not where they are rotated to (a
+        tree's tokens rotate by their depth and lie in window order)."""
         q_weight, k_weight = norm or (None, None)
-        api.dspark_kv_append(k, v, self.cache, req=req, pos=pos, q=q, q_out=q_out, totals=totals,
-                             q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin, status=status,
-                             stream=stream)
+        api.dspark_kv_append(k, v, self.cache, req=req, pos=pos, cache_pos=cache_pos, q=q, q_out=q_out,
+                             totals=totals, q_weight=q_weight, k_weight=k_weight, cos_sin=cos_sin,
+                             status=status, stream=stream)
 
     def attend(self, q, out, *, cu_seqlens, prefix_lens, scale, status, ancestors=None,
                stream=None) -> None:
