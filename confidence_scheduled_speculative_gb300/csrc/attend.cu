@@ -272,6 +272,20 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     const uint32_t base = smem_addr(smem);
     const uint32_t ring = base + S::kQBytes;
 
+    // Behind fewrows.cuh's kernel, which may do the call.  That one lets this one start
+    // only after its own wait, so the lengths are there to read; and if it does the call,
+    // one CTA waits for it, as the join waits for these only, and the others make room.
+    if (kQuant && t.choose) {
+        pdl_trigger();
+        Request q;
+        long long dearer = 0;
+        for (int r = tid; r < a.B; r += kThreads)
+            if (to_request(t, load_window(a, r), &q, false)) dearer += few_dearer(t, q);
+        if (block_sum<long long>(dearer, ctl.scan) <= 0) {
+            if (blockIdx.x == 0) pdl_wait();
+            return;
+        }
+    }
     if (tid == 0) {
         for (int i = 0; i < S::kBufs; ++i) {
             mbar_init(smem_addr(&ctl.full[i]), 1);
@@ -308,8 +322,7 @@ attend_tensor_kernel(const __grid_constant__ CUtensorMap map_k,
     Deal deal;
     long long lo, hi;
     const int cta = blockIdx.x;
-    if ((kQuant && t.choose && few_on_average(a, __ldg(a.cu + a.B))) ||
-        !share_of<kThreads, S::kJobCost>(t, &ctl.begin, ctl.scan, &deal, &lo, &hi)) {
+    if (!share_of<kThreads, S::kJobCost, false>(t, &ctl.begin, ctl.scan, &deal, &lo, &hi)) {
         if (warp == S::kScoreWarp) {
             __syncwarp();
             tmem_free(*(volatile unsigned *)&ctl.tmem, kTmemCols);
@@ -1404,10 +1417,11 @@ extern "C" int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype,
     cudaError_t e;
     const bool quant = cache->dtype == DSPARK_DTYPE_E4M3, small = cache->head_dim == 64;
     if (tensor_fits(a, dtype, *cache)) {
-        // Few rows over E4M3: where the rows that the window has room for leave it open
-        // (a window padded to a tier), both kernels are launched, and the rows that it
-        // holds tell which of them works and which returns at once (2 us).
-        const bool few = quant && few_fits(a, *cache), always = few && few_on_average(a, a.max_rows);
+        // Few rows over E4M3: where the rows that the call has room for are not few in any
+        // one request, both kernels are launched, and the requests' lengths tell which of
+        // them works and which returns at once (2 us).
+        const bool few = quant && few_fits(a, *cache);
+        const bool always = few && a.max_rows * (a.n_q_heads / cache->n_kv_heads) <= kFewRows;
         e = cudaSuccess;
         if (few) e = small ? launch_few<64>(a, *cache, workspace, !always, st)
                            : launch_few<128>(a, *cache, workspace, !always, st);

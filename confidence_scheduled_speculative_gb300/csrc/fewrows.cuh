@@ -102,8 +102,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
     Deal deal;
     long long lo, hi;
     const int cta = blockIdx.x;
-    if (t.choose && !few_on_average(a, __ldg(a.cu + a.B))) return;
-    if (!share_of<kFewWarps * 32, kFewJobCost>(t, &ctl.begin, ctl.scan, &deal, &lo, &hi)) return;
+    if (!share_of<kFewWarps * 32, kFewJobCost, true>(t, &ctl.begin, ctl.scan, &deal, &lo, &hi)) return;
     __syncthreads();
     // one thread walks; the others read the segments it leaves
     auto leave = [&](unsigned k) {

@@ -48,16 +48,6 @@ __device__ __forceinline__ bool usable(const AttendArgs &a, const Window &w, boo
 
 constexpr int kFewRows = 8;  // query rows of a kv head that fewrows.cuh multiplies at once
 
-// Whether that many rows of a window are few enough, over E4M3, for fewrows.cuh to read
-// the keys and values once for every eight of them: up to twice a request and kv head,
-// on average.  32 requests of up to 8192 tokens and 8 heads of 128, there and in the
-// kernel of 128 rows a tile: 4 rows 74 and 120 us, 10 rows 96 and 120, 12 rows 113 and
-// 120, 14 rows 125 and 121, 18 rows 144 and 122; of up to 800 tokens: 4 rows 24 and 43,
-// 14 rows 34 and 43.
-__host__ __device__ inline bool few_on_average(const AttendArgs &a, int rows) {
-    return (long long)rows * (a.n_q_heads / a.cache.n_kv_heads) <= 2ll * kFewRows * a.B;
-}
-
 // The window tokens that token i of a window sees, as bits.
 __device__ __forceinline__ unsigned ancestors_of(const AttendArgs &a, int row, int i, int len) {
     const unsigned all = 0xFFFFFFFFu >> (32 - len);
@@ -87,7 +77,7 @@ struct TensorArgs {
     int few;     // window tokens whose heads fit in 64 rows
     int box;     // cache tokens a TMA box
     int whole;   // no job is split
-    int choose;  // both kernels are launched: the rows of the window tell which one works
+    int choose;  // both kernels are launched: either finds out which of them works (few_dearer)
     float *part_o;   // [2 kMaxCtas][D / 4][128] float4
     float *part_ml;  // [2 kMaxCtas][2][128]
     int *desc;       // [kMaxCtas][kDescInts]: the split job that begins in a CTA
@@ -106,6 +96,27 @@ __device__ __forceinline__ bool to_request(const TensorArgs &t, const Window &w,
     q->tiles = (q->P + q->len + kTile - 1) / kTile;
     q->row_tiles = (q->len + t.tokens - 1) / t.tokens;
     return true;
+}
+
+// How much dearer, over E4M3, a request is to fewrows.cuh's kernel than to the one of 128
+// rows; the kernel for which the requests' sum is less does the call.  It goes by each
+// request's own length and rows, so that neither empty windows nor short requests beside
+// a long one count for more than they take.  A pass of eight rows takes 4/7 of one of 128,
+// and a job's begin and end cost the latter some tiles more.  There and in the kernel of
+// 128 rows a tile, each launched alone, us (4 heads a kv head, 8 kv heads of 128):
+//   32 requests of up to 8192 tokens, 1 to 2 tokens each 74 and 113, 3 or 4 (two passes)
+//   119 and 113, 5 172 and 116, 1 to 5 108 and 113, 1 to 6 117 and 114;  of 800, 3 or 4
+//   tokens 41 and 45, 6 55 and 46;  of 300, 4 tokens 21 and 18;  2 of 8192, 4 tokens 29
+//   and 27, 6 35 and 27;  256 of 1000, 2 tokens 137 and 240, 4 255 and 242, 6 374 and 249
+//   one token over 131040 72 and 79;  8 of 32 with 8 tokens, the others without, 116 and
+//   56;  8 heads a kv head: 2 of 64 with 32 tokens, the others without, 206 and 52; one of
+//   32 tokens over 100000 beside 63 single tokens 1129 and 199
+//   2 kv heads, 32 requests, 1 token 31 and 43, 4 44 and 43;  heads of 64, 1 token 48 and
+//   81, 4 82 and 81, 6 117 and 86
+// Finding out costs the one that does the call 1 to 4 us.
+__device__ __forceinline__ long long few_dearer(const TensorArgs &t, const Request &q) {
+    const int few = kFewRows / t.group, all = kRowsPerTile / t.group;  // window tokens a pass
+    return 4ll * q.tiles * ((q.len + few - 1) / few) - (7ll * q.tiles + 24) * ((q.len + all - 1) / all);
 }
 
 // Where a CTA's share begins.
@@ -190,18 +201,23 @@ struct Walk {
 // This CTA's units [lo, hi) of all of them, and where they begin (for all after the
 // next barrier); false where none are left for it.  Each thread sums a run of
 // requests, and a scan over the threads finds the request that holds the first.
-template <int kThreads, int kJobCost>
+// kFew: of fewrows.cuh, which has none if the other kernel does the call.
+template <int kThreads, int kJobCost, bool kFew>
 __device__ __forceinline__ bool share_of(const TensorArgs &t, Begin *begin, long long *scan, Deal *deal,
                                          long long *lo, long long *hi) {
     const AttendArgs &a = t.a;
     const int tid = threadIdx.x, cta = blockIdx.x;
     const int per = (a.B + kThreads - 1) / kThreads;
-    long long mine = 0;
+    long long mine = 0, dearer = 0;
     Request q = {};
     auto job_units = [&]() { return t.whole ? 1 : q.tiles + kJobCost; };
     auto units = [&]() { return (long long)job_units() * (q.row_tiles * a.cache.n_kv_heads); };
     for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
-        if (to_request(t, load_window(a, r), &q, cta == 0)) mine += units();
+        if (to_request(t, load_window(a, r), &q, cta == 0)) {
+            mine += units();
+            if (kFew) dearer += few_dearer(t, q);
+        }
+    if (kFew && t.choose && block_sum<long long>(dearer, scan) > 0) return false;
     long long T;
     const long long before = block_exclusive_scan<long long>(mine, scan, &T);
     // (a CTA with less than two tiles to do would cost more than it brings)
