@@ -70,3 +70,130 @@ G4, G8 = dict(hq=8, hkv=2, D=128, page=64), dict(hq=16, hkv=2, D=128, page=64)
 def test_the_work_decides(api, wide, shape):
     """Passes over the long prefixes decide, not rows over requests."""
     assert _wide_did(api, shape) == wide
+
+
+# ------------------------------------------------- the one of 128 rows
+
+SHAPES = [
+    dict(prefix=[0], win=[1], hq=1, hkv=1, D=64, page=16),
+    dict(prefix=[0, 5, 0, 16], win=[1, 1, 3, 1], hq=8, hkv=2, D=128, page=16),
+    # lengths around tile and page ends, windows of zero
+    dict(prefix=[63, 64, 65, 127, 128, 1, 0], win=[1, 1, 1, 1, 17, 0, 0], hq=8, hkv=1, D=128, page=64),
+    dict(prefix=[15, 16, 17, 31, 48, 200], win=[1, 2, 1, 9, 32, 5], hq=12, hkv=4, D=64, page=48),
+    # 64 rows and fewer, then more, of one request after another; one row past 64 and 128
+    dict(prefix=[700, 90, 1300], win=[32, 16, 17], hq=8, hkv=2, D=64, page=64),
+    dict(prefix=[129, 4000], win=[13, 26], hq=5, hkv=1, D=128, page=32),
+    dict(prefix=[511], win=[32], hq=32, hkv=2, D=64, page=48),
+    dict(prefix=[300, 9], win=[3, 32], hq=86, hkv=2, D=128, page=16),  # 43 heads a kv head
+    # many requests, more than a CTA has threads; jobs split over many CTAs
+    dict(prefix=[(37 * i) % 500 for i in range(70)], win=[i % 6 for i in range(70)], hq=4, hkv=2, D=128, page=64),
+    dict(prefix=[(37 * i) % 200 for i in range(900)], win=[(i * 7) % 4 for i in range(900)], hq=4, hkv=2,
+         D=64, page=64),
+    dict(prefix=[30001], win=[1], hq=16, hkv=2, D=128, page=16),
+    dict(prefix=[20000, 3], win=[17, 32], hq=8, hkv=1, D=64, page=128),
+]
+
+
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+@pytest.mark.parametrize("tree", [None, "orphans"])
+def test_wide(api, i, tree):
+    p = Wide(620 + i, tree=tree, kind="e4m3", **SHAPES[i]).run(api)
+    p.check()
+    assert int(p.status) == 0
+    out, lse = p.out.clone(), p.lse.clone()
+    p.run(api)
+    assert torch.equal(out, p.out) and torch.equal(lse, p.lse)  # a call repeated
+
+
+KERNELS = [pytest.param(Problem, [1, 1, 1, 0, 1, 1], id="few"), pytest.param(Wide, [3, 1, 32, 0, 2, 1], id="wide")]
+
+
+@pytest.mark.parametrize("kernel,win", KERNELS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf, None])
+def test_odd_scales(api, kernel, win, D, bad):
+    """Negative scales of keys and values (bad=None: nothing else, in prefixes as in
+    windows); scales and codes that are not finite past the ends, in pages of no
+    request, in tokens that a row does not see, and in a prefix."""
+    p = kernel(640, [137, 264, 5, 90, 20, 600], win, 8, 2, D, 16, "e4m3", tree="orphans", pad=0)
+    c = p.cache
+    for s in (c.k_scale, c.v_scale):
+        s *= torch.where(torch.rand(s.shape, device="cuda") < 0.3, -1.0, 1.0)
+    if bad is not None:
+        used = torch.zeros((c.n_pages, 16), dtype=torch.bool, device="cuda")
+        for r, (P, L) in enumerate(zip(p.prefix, p.win)):
+            g, t = c.slots(r, 0, P + L)
+            used[g, t] = True
+        for t in (c.k, c.v):
+            t.view(torch.uint8)[~used] = 0x7F
+        for s in (c.k_scale, c.v_scale):
+            s.masked_fill_(~used[:, None, :], bad)
+        for which in "kv":
+            if win[0] > 1:
+                c.put(which, 0, 137 + 1, bad)  # which the rows after it do not see
+            if win[2] > 1:
+                c.put(which, 2, 5 + 7, bad)
+        c.put("v", 5, 17, math.nan)
+    p.run(api).check()
+    assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("kernel,win", [pytest.param(Problem, [1, 1], id="few"), pytest.param(Wide, [3, 20], id="wide")])
+@pytest.mark.parametrize("slope", [1, -1])
+def test_a_maximum_that_moves(api, kernel, win, slope):
+    """Scores of thousands that rise, or fall, along the prefix."""
+    p = kernel(650, [700, 3], win, 4, 1, 128, 64, "e4m3", q_scale=0.0)
+    ramp = torch.arange(p.cache.table.size(1) * 64, device="cuda").float() / 64
+    for r in range(2):
+        n = p.prefix[r] + p.win[r]
+        g, t = p.cache.slots(r, 0, n)
+        p.cache.k.view(torch.uint8)[g, t, :, 5] = 0x38
+        p.cache.k_scale[g, :, t] = (ramp[:n] * slope + (12 if slope < 0 else 0))[:, None]
+    p.q[:, :, 5] = 1000.0
+    p.run(api).check()
+
+
+@pytest.mark.parametrize("kernel,win", [pytest.param(Problem, [1, 1], id="few"), pytest.param(Wide, [4, 32], id="wide")])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0 ** -20])
+def test_scales_of_the_scores(api, kernel, win, scale):
+    p = kernel(660, [200, 70], win, 4, 2, 64, 32, "e4m3")
+    p.scale = scale
+    p.run(api).check()
+
+
+@pytest.mark.parametrize("kernel,win", [pytest.param(Problem, [1] * 4, id="few"), pytest.param(Wide, [4, 32, 3, 2], id="wide")])
+def test_bad_requests_leave_the_others(api, kernel, win):
+    def problem(seed):
+        return kernel(seed, [40, 100, 33, 64], win, 4, 2, 64, 16, "e4m3")
+    p = problem(670)
+    p.cache.table[1, 2] = p.cache.n_pages + 5
+    p.run(api).check(skip=(1,))
+    assert int(p.status) == api.STATUS_BAD_INDEX
+    p = problem(671)
+    p.cache.table[2, 0] = -1
+    p.prefix_lens[3] = -7
+    p.run(api).check(skip=(2, 3))
+    assert int(p.status) == api.STATUS_BAD_INDEX
+    p = problem(672)
+    p.prefix_lens[2] = 10 ** 6
+    p.run(api).check(skip=(2,))
+    assert int(p.status) == api.STATUS_BAD_INDEX
+    if win[1] == 32:
+        p = problem(673)
+        p.cu[2] += 1  # 33 rows, and the next request two
+        p.run(api).check(skip=(1, 2))
+        assert int(p.status) == api.STATUS_BAD_LEN
+
+
+def test_wide_pool_past_32_bits(api):
+    """Pages past 2^32 elements of the pool."""
+    page, heads, D = 1024, 8, 128
+    n = (1 << 32) // (page * heads * D) + 2
+    p = Wide(680, [1500], [17], 16, heads, D, page, "e4m3", filled=False, pool=n)
+    g = torch.Generator("cuda").manual_seed(1)
+    p.cache.table[:] = torch.tensor([[n - 1, n - 2]], dtype=torch.int32)
+    for t in (p.cache.k, p.cache.v):
+        t.view(torch.uint8)[n - 2:] = torch.randint(0, 127, (2, page, heads, D), generator=g,
+                                                    device="cuda", dtype=torch.uint8)
+    p.run(api).check()
+    assert int(p.status) == 0
