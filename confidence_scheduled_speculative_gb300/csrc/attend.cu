@@ -239,7 +239,9 @@ struct Place {
 
 // Two E4M3 values' worth of a query: x = hi + lo.  A bfloat16 has 8 significant
 // digits; hi takes the upper four, and what remains of x has at most four more, so
-// that hi + lo = x exactly while lo's last digit is at least E4M3's smallest step.
+// that hi + lo = x exactly while lo's last digit is at least E4M3's smallest step, 2^-9:
+// from 2^-2 on.  Below it half a step is lost, 2^-10, which is at most 2^-17 of a row's
+// largest element (brought to 128..256).
 __device__ __forceinline__ void split_pair(float x0, float x1, unsigned *hi, unsigned *lo) {
     *hi = e4m3_pair(x0, x1);
     const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)*hi, __NV_E4M3)));

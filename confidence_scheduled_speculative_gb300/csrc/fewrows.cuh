@@ -72,12 +72,13 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// One and two units in the last place, for normal numbers.
+// Off by at most one unit in the last place, for normal numbers.
 __device__ __forceinline__ float reciprocal_approx(float x) {
     float y;
     asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Off by at most 2^-22, for x in (1/2, 2), and by 2^-22 of itself elsewhere.
 __device__ __forceinline__ float log2_approx(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 2) attend_few_kernel(const Ten
         if (fk < k) enter(k);
 
         // Query row g as the right operand, scaled by a power of two to halves: the
-        // row's largest element to below 2^15, so that any element down to 2^-29 of
+        // row's largest element to 2^14..2^15, so that any element down to 2^-31 of
         // it keeps its eight digits.
         uint32_t q[kSteps][2];
         float by_row[2];       // what rows 2c and 2c + 1 were divided by

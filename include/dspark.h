@@ -749,15 +749,17 @@ DSPARK_API size_t dspark_tree_attention_workspace_bytes(int32_t n_q_heads, int32
  *                F32), ld_* elements apart; out must not share an element with
  *                q (slices of one buffer's rows will do)
  *   lse          [max_rows, n_q_heads] fp32, nullable
- *   prefix_lens  device [B], >= 0; cu_seqlens device [B+1]; window length 0 is
- *                a request without rows
+ *   prefix_lens  device [B], >= 0; cu_seqlens device [B+1], ascending; window
+ *                length 0 is a request without rows
  * Sums and softmax statistics are held in 32 bits.  BF16 rows over a BF16 or
  * E4M3 cache with head_dim 64 or 128, at most 128 query heads a kv head,
  * page_size a multiple of 16 and 16-byte aligned bases and strides run on the
  * tensor cores, the weights exp(s - m) rounded to the 16-bit type of the
  * products (BF16; over E4M3 a half, whose smallest step is 2^-30 of the
  * largest weight times scale); anything else in 32 bits throughout.  Over
- * E4M3 a query's elements below 2^-10 of its largest are taken to 2^-18 of it.
+ * E4M3 a query's elements below 2^-9 of its largest are taken to 2^-17 of it
+ * (where few rows a kv head leave the products to a second kernel, with at most
+ * 8 query heads a kv head and 16-byte aligned scales: below 2^-31, to 2^-39).
  * The order of all sums is fixed by the lengths: a call repeated gives the
  * same bits.
  * A window of more than 32 tokens or outside max_rows (BAD_LEN), and positions

@@ -197,3 +197,66 @@ def test_wide_pool_past_32_bits(api):
                                                     device="cuda", dtype=torch.uint8)
     p.run(api).check()
     assert int(p.status) == 0
+
+
+# Over E4M3 the kernel of 128 rows takes a query as two E4M3 numbers, hi + lo, after a
+# power of two has brought the row's largest element to 128..256.  E4M3 has four digits
+# and a smallest step of 2^-9: a bfloat16 of eight digits is hi + lo exactly while its
+# last digit is 2^-9 or more, which holds from 2^-2 on, 2^-9 of a largest element of
+# 128.  Below, half a step is lost: 2^-10, at most 2^-17 of the largest.
+
+def test_query_split_by_its_formats():
+    """That bound, over every bfloat16 from 256 down, against the largest element of the
+    range, by rounding to E4M3 as torch does."""
+    bits = torch.arange(0, 0x4380, dtype=torch.int32)  # 0 .. 256
+    x = (bits << 16).view(torch.float32)
+    hi = x.to(torch.float8_e4m3fn).float()
+    lo = (x - hi).to(torch.float8_e4m3fn).float()
+    off = (x.double() - hi.double() - lo.double()).abs()
+    assert not bool(off[x >= 128 * 2.0 ** -9].any())
+    assert 2.0 ** -18 < float(off.max()) / 128 <= 2.0 ** -17
+
+
+class Split(Wide):
+    """With what the queries' parts lose."""
+
+    def check(self):
+        lo = 0
+        for r, (P, L) in enumerate(zip(self.prefix, self.win)):
+            if not L:
+                continue
+            q = self.q[lo:lo + L]
+            o, lse, tol, lse_tol, o_abs = wo.attention(q, self.cache, r, P, L, self.bits[r], self.scale)
+            # each small element's loss times the largest key element it may meet
+            size = torch.nan_to_num(q.double().abs())
+            most = size.amax(-1, keepdim=True)
+            lost = torch.where(size < most * 2.0 ** -9, most * 2.0 ** -17, 0.0)
+            k = self.cache.values("k", r, 0, P + L).abs().permute(1, 2, 0)  # [kv heads, D, n]
+            k = k.repeat_interleave(self.hq // k.size(0), 0)
+            e = torch.einsum("lhd,hdn->lhn", lost, k).amax(-1) * abs(self.scale)
+            got, got_lse = self.out[lo:lo + L].double(), self.lse[lo:lo + L].double()
+            assert torch.equal(torch.isnan(got), torch.isnan(o)), r
+            # (weights off by exp(+-e), their sum likewise; weights as halves, far below
+            # the largest of all; a position's weight is one step off at the least)
+            bound = (tol + (self.unit() + torch.expm1(2 * e)[..., None]) * o_abs) * (1 + wo.BF16) \
+                + wo.BF16 * o.abs() + 1e-38 + self.smallest_weight(r, P + L)
+            off = ((got - o).abs() - bound)[torch.isfinite(o)]
+            assert float(off.max()) <= 0, (r, float(off.max()))
+            off = ((got_lse - lse).abs() - lse_tol - e)[torch.isfinite(lse)]
+            assert float(off.max()) <= 0, (r, float(off.max()))
+            lo += L
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_wide_queries_of_wide_range(api, D):
+    """Queries whose elements differ by up to 2^16, and rows that are tiny, huge, zero or
+    hold a NaN."""
+    win = [1, 5, 17, 2, 3, 32]
+    p = Split(690, [130, 40, 77, 9, 21, 64], win, 4, 2, D, 64, "e4m3")
+    p.q *= 2.0 ** torch.randint(-16, 1, p.q.shape, device="cuda")
+    p.q[1] *= 2.0 ** -100
+    p.q[7] *= 2.0 ** 5
+    p.q[9] = 0
+    p.q[24, 1, 7] = math.nan
+    p.run(api).check()
+    assert int(p.status) == 0
