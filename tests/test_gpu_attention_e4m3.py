@@ -260,3 +260,30 @@ def test_wide_queries_of_wide_range(api, D):
     p.q[24, 1, 7] = math.nan
     p.run(api).check()
     assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("kernel", [Problem, Wide])
+def test_one_captured_call_serves_both_kernels(api, kernel):
+    """A graph holds both kernels; the lengths at each replay choose anew."""
+    p = kernel(700, [900] * 12, [3] * 12, 8, 1, 128, 64, "e4m3")
+    if kernel is Wide:
+        p.run(api)  # moves the scales
+    ws = api.workspace(api.dspark_tree_attention_workspace_bytes(p.hq, p.D))
+    kv, graph = p.cache.kv(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.dspark_tree_attention(p.q, kv, cu_seqlens=p.cu, prefix_lens=p.prefix_lens, scale=p.scale,
+                                  out=p.out, lse=p.lse, workspace=ws, status=p.status)
+    for win, prefix in (([1] * 12, [870 + i for i in range(12)]), ([32] + [0] * 10 + [4], [870] * 12),
+                        ([3] * 12, [5] * 12), ([0] * 11 + [1], [900] * 12), ([0] * 12, [0] * 12),
+                        ([32, 2, 2], [0, 850, 850])):
+        win, prefix = win + [0] * (12 - len(win)), prefix + [0] * (12 - len(prefix))
+        p.win, p.prefix, p.rows = win, prefix, sum(win)
+        p.bits = [wo.chain_bits(w) for w in win]
+        p.cu.copy_(torch.tensor([0] + win).cumsum(0))
+        p.prefix_lens.copy_(torch.tensor(prefix))
+        p.out.fill_(7.0)
+        p.lse.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        p.check()
+    assert int(p.status) == 0
