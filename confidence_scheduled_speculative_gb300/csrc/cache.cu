@@ -17,7 +17,8 @@
 //   shuffles; nothing is read twice.  Eight prompts of 4096 tokens, 32 and 8 heads of
 //   128: 455 MB in 77 us (5.9 TB/s, 0.86 of a copy); the rotation alone of four with 64
 //   heads 62 us (6.1 TB/s, 0.89); 256 windows of up to 17 tokens into E4M3 20 us (4.6
-//   TB/s: a row's chain of dependent loads and the arithmetic, in one wave of CTAs).
+//   TB/s: a row's chain of dependent loads and the arithmetic, in two waves of CTAs, 1776
+//   where 912 fit; 84 to 96 bytes of spills in the kernels from bfloat16 into E4M3).
 // append_any_kernel   any alignment, stride and even head size: one warp a
 //   (row, head), one element a lane and step.
 // read_kernel     a CTA takes 16 output rows: their slots are looked up by one

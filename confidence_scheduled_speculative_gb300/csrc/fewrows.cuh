@@ -16,8 +16,8 @@
 // A CTA's eight warps take the steps of a job in turn, each with a running maximum, sum
 // and output of its own and its own copies in flight, so that nothing is waited for until
 // the job's end.  A stage in shared memory is written and read by the same lanes, but for
-// the scales.  32 requests of up to 8192 tokens, 4 heads a kv head, 286 MB: 72 us (4.0
-// TB/s, 0.58 of a copy; 120 us in the kernel of 128 rows a tile).  What bounds it is the
+// the scales.  32 requests of up to 8192 tokens, 4 heads a kv head, 286 MB: 75 us (3.8
+// TB/s, 0.56 of a copy; 113 us in the kernel of 128 rows a tile).  What bounds it is the
 // chain inside a warp: 445 instructions a step, issued in 44% of the cycles by the four
 // warps a scheduler has room for.
 #pragma once
