@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kAppendThreads, 6) append_kernel(AppendArgs a,
             out = static_cast<T *>(a.out[kKind < 2 ? kKind : 0]) + row * a.ld_out[kKind < 2 ? kKind : 0] +
                   (first + group) * D + at0;
         const T *weight = kKind < 2 ? static_cast<const T *>(a.weight[kKind < 2 ? kKind : 0]) : nullptr;
-        float2 w[4];
+        // (zero where a lane has no elements, whose products count for the largest one)
+        float2 w[4] = {};
         if (weight && has) {
             Four<T>::unpack(__ldg(reinterpret_cast<const Raw *>(weight + at0)), reinterpret_cast<float *>(w));
             Four<T>::unpack(__ldg(reinterpret_cast<const Raw *>(weight + at1)), reinterpret_cast<float *>(w + 2));
