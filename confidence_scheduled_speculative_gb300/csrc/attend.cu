@@ -29,7 +29,7 @@
 //   few, and attend_join_kernel adds the parts in a fixed order.
 //   Over bfloat16 the bound is HBM: 32 requests of up to 8192 tokens with windows of up
 //   to nine and 32 query heads, 557 MB, in 98 to 102 us by box (5.5 TB/s, 0.81 of a copy);
-//   256 requests with up to 17 and 64 heads, 4.4 GB, in 757 to 777 us (5.7 TB/s, 0.84).
+//   256 requests with up to 17 and 64 heads, 4.4 GB, in 763 to 787 us (5.6 to 5.8 TB/s, 0.83).
 //   Over E4M3 half the bytes take the same steps, and the bound is a step's softmax and
 //   conversions with the waits between them: two requests of up to 131040 tokens, 80 and
 //   160 rows a kv head, the latter in two passes, 522 MB in 289 us (1.81 TB/s, 0.27; issue
