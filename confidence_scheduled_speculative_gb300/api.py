@@ -97,6 +97,15 @@ class dspark_kv_cache(ctypes.Structure):
                 ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
 
 
+class dspark_latent_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("n_requests", ctypes.c_int32),
+                ("table_width", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("data", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p)]
+
+
 class dspark_norm_rope(ctypes.Structure):
     _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
                 ("eps", ctypes.c_float), ("cos_sin", ctypes.c_void_p), ("n_pos", ctypes.c_int32),
@@ -176,6 +185,25 @@ _SIGS = {
     "dspark_tree_attention": (ctypes.c_int, [_VP, _I64, _I32, _I32, _I32, _VP, _VP, _I32, _VP,
                                              ctypes.c_float, ctypes.POINTER(dspark_kv_cache),
                                              _VP, _I64, _VP, _VP, _SZ, _VP, _VP]),
+    "dspark_latent_append": (ctypes.c_int, [_VP, _I64, _VP, _I64, _I64, _I32, _I32,
+                                            ctypes.POINTER(dspark_latent_cache),
+                                            ctypes.POINTER(dspark_norm_rope), _VP, _VP, _VP, _VP,
+                                            _I32, _VP, _I64, _I64, _VP, _VP]),
+    "dspark_latent_attention_workspace_bytes": (_SZ, [_I32, _I32]),
+    "dspark_latent_attention": (ctypes.c_int, [_VP, _I64, _I32, _I32, _I32, _VP, _VP, _I32, _VP,
+                                               ctypes.c_float, ctypes.POINTER(dspark_latent_cache),
+                                               _VP, _I64, _VP, _VP, _SZ, _VP, _VP]),
+    "dspark_prompt_attention": (ctypes.c_int, [_VP, _I64, _VP, _I64, _I64, _VP, _I64, _VP, _I64,
+                                               _I64, _I32, _I32, _I32, _I32, _I32, _I32, _I32,
+                                               _I32, _VP, _VP, _I32, ctypes.c_float, _VP, _I64,
+                                               _VP, _VP, _VP]),
+    "dspark_attention_weights": (ctypes.c_int, [_VP, _I64, _I32, _I32, _I32, _VP, _VP, _I32, _VP,
+                                                ctypes.c_float, ctypes.POINTER(dspark_kv_cache),
+                                                _VP, _VP, ctypes.c_float, _VP, _VP, _I32, _VP,
+                                                _VP, _VP, _VP]),
+    "dspark_kv_evict_workspace_bytes": (_SZ, [_I32, _I32, _I32]),
+    "dspark_kv_evict": (ctypes.c_int, [ctypes.POINTER(dspark_kv_cache), _VP, _VP, _I32, _I32,
+                                       _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _SZ, _VP, _VP]),
 }
 
 
@@ -787,3 +815,217 @@ def dspark_tree_attention(q, cache: KVCache, *, cu_seqlens, prefix_lens, scale, 
         workspace.numel() * workspace.element_size(), _p(status, torch.int32, "status"),
         _stream(stream))
     _check("dspark_tree_attention", rc)
+
+
+# ---------------------------------------------- attention, latent cache
+
+class LatentCache:
+    """One layer's paged latent cache over tensors the caller owns (the C ABI's
+    dspark_latent_cache, filled once).
+
+    ``pages``: [n_pages, page_size, latent_dim + rope_dim], bfloat16 or float32, any
+    strides with a unit inner one; a token's latent vector, then its rotated key part.
+    ``block_table``: int32 [n_requests, table_width].  The tensors are kept referenced."""
+
+    def __init__(self, pages, block_table, latent_dim):
+        kinds = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+        if not pages.is_cuda or pages.dim() != 3 or pages.stride(2) != 1:
+            raise ValueError("pages: expected a 3-D CUDA tensor with unit inner stride")
+        if pages.dtype not in kinds:
+            raise ValueError("pages: expected bfloat16 or float32")
+        if block_table.dim() != 2:
+            raise ValueError("block_table: expected a 2-D tensor")
+        n_pages, page, dim = pages.shape
+        if not 0 < latent_dim < dim:
+            raise ValueError(f"latent_dim: expected 1..{dim - 1}, a part of the entries")
+        self.pages, self.block_table = pages, block_table
+        self.latent_dim, self.rope_dim = latent_dim, dim - latent_dim
+        self.desc = dspark_latent_cache(
+            kinds[pages.dtype], n_pages, page, latent_dim, dim - latent_dim, block_table.size(0),
+            block_table.size(1), pages.stride(0), pages.stride(1), pages.data_ptr(),
+            _p(block_table, torch.int32, "block_table"))
+        self.ref = ctypes.byref(self.desc)
+
+
+def _heads(t: torch.Tensor, name: str, dtype, heads: int, dim: int, rows: int) -> tuple[int, int, int]:
+    """Pointer, row stride and head stride of [rows, heads, dim], any strides but the inner."""
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a 3-D CUDA tensor [rows, heads, elements]")
+    n, h, d = t.shape
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.stride(2) != 1 and d > 1:
+        raise ValueError(f"{name}: expected unit inner stride")
+    if h != heads or d != dim:
+        raise ValueError(f"{name}: expected {heads} heads of {dim} elements, got {h} of {d}")
+    if n < rows:
+        raise ValueError(f"{name}: expected at least {rows} rows, got {n}")
+    hs = t.stride(1) if h > 1 else max(t.stride(1), d)
+    ld = t.stride(0) if n > 1 else max(t.stride(0), (h - 1) * hs + d)
+    return t.data_ptr() if n else _NO_ROWS, ld, hs
+
+
+def dspark_latent_append(x, cache: LatentCache, *, req, pos, cos_sin, status, cache_pos=None,
+                         q_rope=None, q_rope_out=None, totals=None, weight=None, eps=1e-6,
+                         interleaved=False, max_rows=None, stream=None) -> None:
+    """Rows ``x`` [rows, latent_dim + rope_dim] into ``cache`` at the rows' positions
+    (``cache_pos``, else ``pos``): the latent part RMS normalised (where ``weight``
+    [latent_dim] is given), the key part rotated by ``cos_sin`` (fp32 [n_pos, rope_dim],
+    cosines then sines).  ``q_rope`` [rows, heads, rope_dim], in any strides (the queries'
+    trailing elements), is rotated along, to ``q_rope_out`` or in place."""
+    dtype = x.dtype
+    code = _dtype_code(x)
+    dim = cache.latent_dim + cache.rope_dim
+    max_rows = x.size(0) if max_rows is None else max_rows
+    if x.dim() != 2:
+        raise ValueError("x: expected a 2-D tensor [rows, latent_dim + rope_dim]")
+    xp, ld_x, _ = _heads(x[:, None, :], "x", dtype, 1, dim, max_rows)
+    if weight is not None and weight.numel() != cache.latent_dim:
+        raise ValueError(f"weight: expected {cache.latent_dim} elements")
+    if cos_sin.dim() != 2 or cos_sin.size(1) != cache.rope_dim:
+        raise ValueError(f"cos_sin: expected shape [n_pos, {cache.rope_dim}]")
+    qp = qo = None
+    lq = hs = lqo = hso = heads = 0
+    if q_rope is None and q_rope_out is not None:
+        raise ValueError("q_rope_out: expected with q_rope only")
+    if q_rope is not None:
+        heads = q_rope.size(1)
+        out = q_rope if q_rope_out is None else q_rope_out
+        qp, lq, hs = _heads(q_rope, "q_rope", dtype, heads, cache.rope_dim, max_rows)
+        qo, lqo, hso = _heads(out, "q_rope_out", dtype, heads, cache.rope_dim, max_rows)
+    nr = dspark_norm_rope(None, _p(weight, dtype, "weight"), eps, _p(cos_sin, torch.float32, "cos_sin"),
+                          cos_sin.size(0), cache.rope_dim, 1 if interleaved else 0)
+    rc = load().dspark_latent_append(
+        xp, ld_x, qp, lq, hs, code, heads, cache.ref, ctypes.byref(nr), _index(req, max_rows, "req"),
+        _index(pos, max_rows, "pos"), _index(cache_pos, max_rows, "cache_pos"),
+        _index(totals, 1, "totals"), max_rows, qo, lqo, hso, _p(status, torch.int32, "status"),
+        _stream(stream))
+    _check("dspark_latent_append", rc)
+
+
+def dspark_latent_attention_workspace_bytes(n_q_heads: int, latent_dim: int) -> int:
+    return int(load().dspark_latent_attention_workspace_bytes(n_q_heads, latent_dim))
+
+
+def dspark_latent_attention(q, cache: LatentCache, *, cu_seqlens, prefix_lens, scale, out,
+                            workspace, status, ancestors=None, lse=None, max_rows=None,
+                            stream=None) -> None:
+    """dspark_tree_attention over a latent cache, absorbed: ``q`` [rows, n_q_heads,
+    latent_dim + rope_dim] holds each head's query times its key projection, then the
+    rotated part; ``out`` [rows, n_q_heads, latent_dim] is to be multiplied by the
+    heads' value projections.  ``out`` beside ``q``, not over it."""
+    hq, dim = q.size(1), cache.latent_dim + cache.rope_dim
+    code = _dtype_code(q)
+    max_rows = q.size(0) if max_rows is None else max_rows
+    B = prefix_lens.numel()
+    qp, lq = _rows(q, "q", q.dtype, hq, dim, max_rows)
+    op, lo = _rows(out, "out", q.dtype, hq, cache.latent_dim, max_rows)
+    if lse is not None and lse.numel() < max_rows * hq:
+        raise ValueError(f"lse: expected at least {max_rows * hq} elements")
+    rc = load().dspark_latent_attention(
+        qp, lq, code, hq, max_rows, _index(cu_seqlens, B + 1, "cu_seqlens"),
+        _p(prefix_lens, torch.int32, "prefix_lens"), B, _index(ancestors, max_rows, "ancestors"),
+        scale, cache.ref, op, lo, _p(lse, torch.float32, "lse"), _p(workspace),
+        workspace.numel() * workspace.element_size(), _p(status, torch.int32, "status"),
+        _stream(stream))
+    _check("dspark_latent_attention", rc)
+
+
+def dspark_prompt_attention(q, k, v, *, cu_seqlens, cu_keys, scale, out, status, k_shared=None,
+                            lse=None, max_rows=None, max_keys=None, stream=None) -> None:
+    """Causal attention of ragged prompts: request r's queries are rows cu_seqlens[r] to
+    cu_seqlens[r+1]-1 of ``q`` [rows, n_q_heads, key_dim + shared_dim], its keys and values rows
+    cu_keys[r] to cu_keys[r+1]-1 of ``k`` [keys, n_kv_heads, key_dim], ``v`` [keys, n_kv_heads,
+    value_dim] (any strides but the inner) and ``k_shared`` [keys, shared_dim], the key part
+    that all heads share (None: there is none).  The last query stands at the last key.
+    ``out`` [rows, n_q_heads, value_dim], beside ``q``; ``lse`` fp32 [rows, n_q_heads]."""
+    hq, hkv, K, V = q.size(1), k.size(1), k.size(2), v.size(2)
+    code = _dtype_code(q)
+    max_rows = q.size(0) if max_rows is None else max_rows
+    max_keys = k.size(0) if max_keys is None else max_keys
+    B = cu_seqlens.numel() - 1
+    S, sp, ls = 0, None, 0
+    if k_shared is not None:
+        if k_shared.dim() != 2:
+            raise ValueError("k_shared: expected a 2-D tensor [keys, shared_dim]")
+        S = k_shared.size(1)
+        sp, ls, _ = _heads(k_shared[:, None, :], "k_shared", q.dtype, 1, S, max_keys)
+    qp, lq = _rows(q, "q", q.dtype, hq, K + S, max_rows)
+    kp, lk, hk = _heads(k, "k", q.dtype, hkv, K, max_keys)
+    vp, lv, hv = _heads(v, "v", q.dtype, hkv, V, max_keys)
+    op, lo = _rows(out, "out", q.dtype, hq, V, max_rows)
+    if lse is not None and lse.numel() < max_rows * hq:
+        raise ValueError(f"lse: expected at least {max_rows * hq} elements")
+    rc = load().dspark_prompt_attention(
+        qp, lq, kp, lk, hk, sp, ls, vp, lv, hv, code, hq, hkv, K, S, V, max_rows, max_keys,
+        _p(cu_seqlens, torch.int32, "cu_seqlens"), _index(cu_keys, B + 1, "cu_keys"), B, scale, op,
+        lo, _p(lse, torch.float32, "lse"), _p(status, torch.int32, "status"), _stream(stream))
+    _check("dspark_prompt_attention", rc)
+
+
+# -------------------------------------------- a cache that is kept short
+
+def _ledger(t, dtype, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _p(t, dtype, name)
+
+
+def dspark_attention_weights(q, cache: KVCache, *, lse, cu_seqlens, prefix_lens, scale, weights,
+                             status, weights_out=None, counts=None, decay=1.0, ancestors=None,
+                             pos=None, positions=None, max_rows=None, stream=None) -> None:
+    """Adds the attention of a window's rows (``q``, ``lse`` and the rest as
+    dspark_tree_attention had and left them) to what each position of the cache has
+    gathered, ``weights`` fp32 [B, n_kv_heads, length] (in place by default), after its
+    decay; ``counts`` [B]: how many rows of each window count (the accepted ones).  With
+    ``positions`` (int32 like ``weights``) the new entries' ``pos`` are noted there."""
+    hq, hkv, B = q.size(1), cache.n_kv_heads, prefix_lens.numel()
+    code = _dtype_code(q)
+    max_rows = q.size(0) if max_rows is None else max_rows
+    if weights.dim() != 3:
+        raise ValueError("weights: expected a 3-D tensor [B, n_kv_heads, length]")
+    length = weights.size(2)
+    shape = (B, hkv, length)
+    qp, lq = _rows(q, "q", q.dtype, hq, cache.head_dim, max_rows)
+    if lse.numel() < max_rows * hq:
+        raise ValueError(f"lse: expected at least {max_rows * hq} elements")
+    rc = load().dspark_attention_weights(
+        qp, lq, code, hq, max_rows, _index(cu_seqlens, B + 1, "cu_seqlens"),
+        _p(prefix_lens, torch.int32, "prefix_lens"), B, _index(ancestors, max_rows, "ancestors"),
+        scale, cache.ref, _p(lse, torch.float32, "lse") or _NO_ROWS, _index(counts, B, "counts"), decay,
+        _ledger(weights, torch.float32, shape, "weights"),
+        _ledger(weights if weights_out is None else weights_out, torch.float32, shape, "weights_out"),
+        length, _index(pos, max_rows, "pos"),
+        None if positions is None else _ledger(positions, torch.int32, shape, "positions"),
+        _p(status, torch.int32, "status"), _stream(stream))
+    _check("dspark_attention_weights", rc)
+
+
+def dspark_kv_evict_workspace_bytes(B: int, n_kv_heads: int, length: int) -> int:
+    return int(load().dspark_kv_evict_workspace_bytes(B, n_kv_heads, length))
+
+
+def dspark_kv_evict(cache: KVCache, *, lens, now, keep, recent, weights, positions, workspace,
+                    status, weights_out=None, positions_out=None, new_lens=None,
+                    stream=None) -> None:
+    """Cuts each request's cache from ``lens`` [B] down to at most ``keep`` entries a kv head:
+    those whose position is among the ``recent`` last of ``now`` [B] tokens, then those of
+    the largest ``weights``.  Entries that stay from behind the new end move into the
+    places left before it.  ``weights``, ``positions`` ([B, n_kv_heads, length], fp32 and
+    int32) and ``lens`` are updated, in place by default."""
+    B = lens.numel()
+    if weights.dim() != 3:
+        raise ValueError("weights: expected a 3-D tensor [B, n_kv_heads, length]")
+    length = weights.size(2)
+    shape = (B, cache.n_kv_heads, length)
+    rc = load().dspark_kv_evict(
+        cache.ref, _p(lens, torch.int32, "lens"), _index(now, B, "now"), B, keep, recent,
+        _ledger(weights, torch.float32, shape, "weights"),
+        _ledger(weights if weights_out is None else weights_out, torch.float32, shape, "weights_out"),
+        _ledger(positions, torch.int32, shape, "positions"),
+        _ledger(positions if positions_out is None else positions_out, torch.int32, shape,
+                "positions_out"),
+        length, _index(lens if new_lens is None else new_lens, B, "new_lens"), _p(workspace),
+        workspace.numel() * workspace.element_size(), _p(status, torch.int32, "status"),
+        _stream(stream))
+    _check("dspark_kv_evict", rc)

@@ -27,7 +27,7 @@ LIB_PATH = os.path.join(OUT_DIR, "libdspark.so")
 CHECKED_LIB_PATH = os.path.join(OUT_DIR, "libdspark_checked.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "plan.cu", "pack.cu", "accept.cu", "scatter.cu", "sample.cu", "calib.cu",
-           "cache.cu", "attend.cu"]
+           "cache.cu", "attend.cu", "latent.cu", "latent_attend.cu", "prompt.cu", "evict.cu"]
 
 
 def nvcc() -> str:

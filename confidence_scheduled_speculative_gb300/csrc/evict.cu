@@ -1,0 +1,447 @@
+// evict.cu -- a cache that is kept short: the attention weights that its positions gather
+// step by step, and the eviction of the entries that gathered least.
+//
+// Gathering, for request r, kv head h and position p, over the window's rows that count
+// and the head's query heads that see p:
+//   weights_out_p = decay weights_p + sum exp(scale q . k_p - lse)
+// with lse the rows' log sums that the attention left, so the terms are its softmax.
+//
+// weights_any_kernel   any types, strides, head and page sizes, in 32 bits throughout: a
+//   warp a position, its key held in registers, one row and query head after another.
+//
+// Eviction, for each (request, kv head): of n entries those `keep` stay that rank first by
+// (fresh, weight, lower place).  An entry's rank is a 32-bit key (rank_key); the keep-th
+// largest is found by its digits, and as many entries equal to it stay, in order, as are
+// needed.  The entries that stay from place `keep` on then fill the places left below
+// it, the i-th the i-th: so all reads lie at or behind place `keep` and all writes before
+// it, entries move in any order and in parallel, and no more than have to.
+//
+// evict_select_kernel  a CTA a (request, kv head): three passes for the digits (a histogram
+//   of each in shared memory, integer counts), then three in which each warp walks a
+//   run of places of its own: entries equal to the border, entries moved, and the list
+//   of moves, with the ledger.
+// evict_move_kernel    a CTA 64 moves of a (request, kv head): both slots looked up by a
+//   thread, then the entries' pieces streamed by all.
+
+#include "kvcache.cuh"
+#include "schedule.cuh"
+
+namespace dspark {
+
+// ------------------------------------------------------------- gathering
+
+struct WeightsArgs {
+    AttendArgs a;
+    const float *lse;
+    const int32_t *counts;
+    float decay;
+    const float *weights;
+    float *weights_out;
+    int length;
+    const int32_t *pos;
+    int32_t *positions;
+};
+
+// How many rows of a window count, -1 if the request is left alone; with `report`,
+// flags why.
+__device__ __forceinline__ int counted(const WeightsArgs &t, const Window &w, int r, bool report) {
+    if (w.hi != w.lo && !usable(t.a, w, report)) return -1;
+    // (a request without rows still has a prefix that decays)
+    const int n = t.counts ? __ldg(t.counts + r) : w.hi - w.lo;
+    int bad = 0;
+    if (n < 0 || n > w.hi - w.lo || w.P < 0) bad = DSPARK_STATUS_BAD_LEN;
+    else if ((long long)w.P + n > t.length) bad = DSPARK_STATUS_CAPACITY;
+    if (bad && report) flag(t.a.status, bad);
+    return bad ? -1 : n;
+}
+
+constexpr int kWeightsWarps = 8;
+constexpr int kWeightsPositions = 64;  // a CTA
+constexpr int kWeightsSteps = DSPARK_MAX_HEAD_DIM / 32;
+
+template <typename T, typename C>
+__global__ void __launch_bounds__(kWeightsWarps * 32) weights_any_kernel(WeightsArgs t) {
+    pdl_trigger();
+    pdl_wait();
+    const AttendArgs &a = t.a;
+    const int r = blockIdx.z, kh = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Window w = load_window(a, r);
+    const int n = counted(t, w, r, blockIdx.x == 0 && kh == 0 && threadIdx.x == 0);
+    if (n < 0) return;
+    const int D = a.cache.head_dim, G = a.n_q_heads / a.cache.n_kv_heads;
+    const long long line = ((long long)r * a.cache.n_kv_heads + kh) * t.length;
+    for (int i = warp; i < kWeightsPositions; i += kWeightsWarps) {
+        const long long p = (long long)blockIdx.x * kWeightsPositions + i;
+        if (p >= t.length) return;
+        float sum = 0.0f;
+        if (n > 0 && p < w.P + n) {
+            int token;
+            const int page = kv_page(a.cache, r, p, &token);
+            if (page < 0 && lane == 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+            if (page >= 0) {
+                const C *k = reinterpret_cast<const C *>(a.cache.k) + kv_offset(a.cache, page, token, kh);
+                const float f =
+                    sizeof(C) == 1 ? __ldg(a.cache.k_scale + kv_scale_offset(a.cache, page, token, kh)) : 1.0f;
+                float kv[kWeightsSteps];
+#pragma unroll
+                for (int s = 0; s < kWeightsSteps; ++s) kv[s] = lane + 32 * s < D ? elem_value(k[lane + 32 * s]) * f : 0.0f;
+                for (int j = 0; j < n; ++j) {
+                    const int row = w.lo + j;
+                    if (p >= w.P && !(ancestors_of(a, row, j, w.hi - w.lo) >> (p - w.P) & 1)) continue;
+                    for (int g = 0; g < G; ++g) {
+                        const int h = kh * G + g;
+                        const T *q = static_cast<const T *>(a.q) + row * a.ld_q + (long long)h * D;
+                        float s = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < kWeightsSteps; ++e)
+                            if (lane + 32 * e < D) s = fmaf(elem_value(q[lane + 32 * e]), kv[e], s);
+                        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(kFullMask, s, x);
+                        sum += expf(fmaf(s, a.scale, -t.lse[(long long)row * a.n_q_heads + h]));
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            t.weights_out[line + p] = p < w.P ? fmaf(t.decay, t.weights[line + p], sum) : sum;
+            if (t.positions && p >= w.P && p < w.P + n) t.positions[line + p] = __ldg(t.pos + w.lo + (p - w.P));
+        }
+    }
+}
+
+// -------------------------------------------------------------- eviction
+
+struct EvictArgs {
+    KvView cache;
+    const int32_t *lens, *now;
+    int B, keep, recent, length;
+    const float *weights;
+    float *weights_out;
+    const int32_t *positions;
+    int32_t *positions_out;
+    int32_t *new_lens;
+    int most;          // moves of a (request, kv head), at most
+    int32_t *n_moves;  // [B][n_kv_heads]
+    int32_t *cut;      // [B]: the new lengths, until every head has read the old
+    int32_t *moves;    // [B][n_kv_heads][2][most]: places left, places they are filled from
+    int32_t *status;
+};
+
+// Larger for what is to stay: the fresh first, then by weight, NaN last.
+__device__ __forceinline__ unsigned rank_key(float w, int position, long long fresh_from) {
+    if (position >= fresh_from) return 0xFFFFFFFFu;
+    if (w != w) return 0;
+    const unsigned b = __float_as_uint(w + 0.0f);  // (-0 is 0)
+    return b >> 31 ? ~b : b | 0x80000000u;
+}
+
+constexpr int kSelectThreads = 1024, kSelectWarps = kSelectThreads / 32;
+constexpr int kDigits = 2048;
+
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(EvictArgs a) {
+    __shared__ int hist[kDigits];
+    __shared__ int scan[40], of_warp[2][kSelectWarps], found[2];
+    pdl_trigger();
+    pdl_wait();
+    const int h = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int line = r * a.cache.n_kv_heads + h;
+    const int n = __ldg(a.lens + r);
+    const bool bad = n < 0 || n > a.length || n > (long long)a.cache.table_width * a.cache.page_size;
+    const int end = bad ? n : min(n, a.keep);
+    if (tid == 0) {
+        a.n_moves[line] = 0;
+        if (h == 0) a.cut[r] = end;
+        if (bad && h == 0) flag(a.status, DSPARK_STATUS_BAD_LEN);
+    }
+    if (bad) return;
+    const float *w_in = a.weights + (long long)line * a.length;
+    const int32_t *p_in = a.positions + (long long)line * a.length;
+    float *w_out = a.weights_out + (long long)line * a.length;
+    int32_t *p_out = a.positions_out + (long long)line * a.length;
+    const bool apart = a.weights_out != a.weights, apart_p = a.positions_out != a.positions;
+    if (n > a.keep) {
+        const long long fresh_from = (long long)__ldg(a.now + r) - a.recent;
+        auto key = [&](int p) { return rank_key(w_in[p], p_in[p], fresh_from); };
+        // the keep-th largest key, eleven, eleven and ten bits at a time
+        unsigned border = 0;
+        int need = a.keep;  // of the entries that agree with the border's digits so far
+        bool nan = false;
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+            for (int i = tid; i < kDigits; i += kSelectThreads) hist[i] = 0;
+            __syncthreads();
+#pragma unroll 4
+            for (int p = tid; p < n; p += kSelectThreads) {
+                const unsigned k = key(p);
+                if (pass == 0) nan = nan || k == 0;
+                else if (k >> (shift + bits) != border) continue;
+                atomicAdd(&hist[k >> shift & ((1 << bits) - 1)], 1);
+            }
+            __syncthreads();
+            // thread t holds the digits 2 t and 2 t + 1 from above
+            const int digits = 1 << bits, top = digits - 1 - 2 * tid;
+            const int c0 = top >= 0 ? hist[top] : 0, c1 = top >= 1 ? hist[top - 1] : 0;
+            int total;
+            const int above = block_exclusive_scan<int>(c0 + c1, scan, &total);
+            if (above < need && above + c0 + c1 >= need) {
+                const bool second = above + c0 < need;
+                found[0] = second ? top - 1 : top;
+                found[1] = need - above - (second ? c0 : 0);
+            }
+            __syncthreads();
+            border = border << bits | (unsigned)found[0];
+            need = found[1];
+        }
+        if (nan) flag(a.status, DSPARK_STATUS_BAD_INPUT);
+        // each warp's run of places: how many keys equal the border before it
+        const int run = (n + kSelectThreads - 1) / kSelectThreads * 32;
+        const int from = min(warp * run, n), to = min(from + run, n);
+        int mine = 0;
+        for (int p = from + lane; p < to; p += 32) mine += key(p) == border;
+        mine = __reduce_add_sync(kFullMask, mine);
+        if (lane == 0) of_warp[0][warp] = mine;
+        __syncthreads();
+        int equal0 = 0;
+        for (int i = 0; i < warp; ++i) equal0 += of_warp[0][i];
+        __syncthreads();
+        // whether the place of this lane's turn stays, in order along the run
+        const unsigned before = lanemask_lt();
+        auto stays = [&](int p, int *equal) {
+            const unsigned k = p < to ? key(p) : 0;
+            const bool eq = p < to && k == border;
+            const unsigned eqs = __ballot_sync(kFullMask, eq);
+            const bool yes = p < to && (k > border || (eq && *equal + __popc(eqs & before) < need));
+            *equal += __popc(eqs);
+            return yes;
+        };
+        int left = 0, moved = 0, equal = equal0;
+        for (int p0 = from; p0 < to; p0 += 32) {
+            const int p = p0 + lane;
+            const bool yes = stays(p, &equal);
+            left += __popc(__ballot_sync(kFullMask, p < min(to, a.keep) && !yes));
+            moved += __popc(__ballot_sync(kFullMask, p >= a.keep && yes));
+        }
+        if (lane == 0) {
+            of_warp[0][warp] = left;
+            of_warp[1][warp] = moved;
+        }
+        __syncthreads();
+        left = moved = 0;
+        int total = 0;
+        for (int i = 0; i < kSelectWarps; ++i) {
+            if (i < warp) left += of_warp[0][i], moved += of_warp[1][i];
+            total += of_warp[1][i];
+        }
+        int32_t *to_list = a.moves + (long long)line * 2 * a.most, *from_list = to_list + a.most;
+        equal = equal0;
+        for (int p0 = from; p0 < to; p0 += 32) {
+            const int p = p0 + lane;
+            const bool yes = stays(p, &equal);
+            const bool is_left = p < min(to, a.keep) && !yes, is_moved = p >= a.keep && yes;
+            const unsigned lefts = __ballot_sync(kFullMask, is_left), moves = __ballot_sync(kFullMask, is_moved);
+            const int i = left + __popc(lefts & before), j = moved + __popc(moves & before);
+            if (is_left && in_bounds(i, a.most, a.status)) to_list[i] = p;
+            if (is_moved && in_bounds(j, a.most, a.status)) from_list[j] = p;
+            left += __popc(lefts);
+            moved += __popc(moves);
+        }
+        if (tid == 0) a.n_moves[line] = total;
+        __syncthreads();
+        // the ledger: entries that stay where they are, then those moved, then none
+        if (apart || apart_p)
+            for (int p = tid; p < end; p += kSelectThreads) {
+                if (apart) w_out[p] = w_in[p];
+                if (apart_p) p_out[p] = p_in[p];
+            }
+        __syncthreads();
+        for (int i = tid; i < total; i += kSelectThreads) {
+            const int p = to_list[i], of = from_list[i];
+            w_out[p] = w_in[of];
+            p_out[p] = p_in[of];
+        }
+        __syncthreads();
+    } else if (apart || apart_p) {
+        for (int p = tid; p < end; p += kSelectThreads) {
+            if (apart) w_out[p] = w_in[p];
+            if (apart_p) p_out[p] = p_in[p];
+        }
+    }
+    for (int p = end + tid; p < a.length; p += kSelectThreads) {
+        w_out[p] = 0.0f;
+        p_out[p] = 0;
+    }
+}
+
+constexpr int kMoveThreads = 256, kMoves = 64;
+
+// One entry's elements, kPiece bytes at a time.
+template <typename Piece>
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, int elem_bytes) {
+    __shared__ long long at[2][kMoves];
+    pdl_trigger();
+    pdl_wait();
+    const int h = blockIdx.y, r = blockIdx.z, tid = threadIdx.x, line = r * a.cache.n_kv_heads + h;
+    if (blockIdx.x == 0 && h == 0 && tid == 0) a.new_lens[r] = a.cut[r];
+    const int n = min(a.n_moves[line] - (int)blockIdx.x * kMoves, kMoves);
+    if (n <= 0) return;
+    const KvView &c = a.cache;
+    const int32_t *lists = a.moves + (long long)line * 2 * a.most + (long long)blockIdx.x * kMoves;
+    if (tid < n) {
+        int token[2], page[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            page[i] = kv_page(c, r, lists[(long long)i * a.most + tid], &token[i]);
+            at[i][tid] = page[i] < 0 ? -1 : kv_offset(c, page[i], token[i], h) * elem_bytes;
+        }
+        if (page[0] < 0 || page[1] < 0) {
+            flag(a.status, DSPARK_STATUS_BAD_INDEX);
+            at[0][tid] = -1;
+        } else if (c.k_scale) {
+            const long long to = kv_scale_offset(c, page[0], token[0], h), of = kv_scale_offset(c, page[1], token[1], h);
+            c.k_scale[to] = c.k_scale[of];
+            c.v_scale[to] = c.v_scale[of];
+        }
+    }
+    __syncthreads();
+    const int pieces = c.head_dim * elem_bytes / (int)sizeof(Piece);
+#pragma unroll 4
+    for (int i = tid; i < n * 2 * pieces; i += kMoveThreads) {
+        const int entry = i / (2 * pieces), rest = i - entry * 2 * pieces, v = rest >= pieces;
+        const int piece = rest - v * pieces;
+        if (at[0][entry] < 0) continue;
+        unsigned char *base = v ? c.v : c.k;
+        reinterpret_cast<Piece *>(base + at[0][entry])[piece] =
+            reinterpret_cast<const Piece *>(base + at[1][entry])[piece];
+    }
+}
+
+namespace {
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Entries that can move: as many as are kept, or as lie behind them.
+int most_moves(int keep, int length) { return length > keep ? min(keep, length - keep) : 0; }
+
+template <typename T>
+cudaError_t launch_weights(const WeightsArgs &t, int cache_dtype, cudaStream_t stream) {
+    const dim3 grid((t.length + kWeightsPositions - 1) / kWeightsPositions, t.a.cache.n_kv_heads, t.a.B);
+    const dim3 block(kWeightsWarps * 32);
+    if (cache_dtype == DSPARK_DTYPE_BF16)
+        return launch_pdl(weights_any_kernel<T, __nv_bfloat16>, grid, block, 0, stream, t);
+    if (cache_dtype == DSPARK_DTYPE_F32) return launch_pdl(weights_any_kernel<T, float>, grid, block, 0, stream, t);
+    return launch_pdl(weights_any_kernel<T, e4m3>, grid, block, 0, stream, t);
+}
+
+template <typename Piece>
+cudaError_t launch_moves(const EvictArgs &a, int elem_bytes, cudaStream_t stream) {
+    const dim3 grid(max((a.most + kMoves - 1) / kMoves, 1), a.cache.n_kv_heads, a.B);
+    return launch_pdl(evict_move_kernel<Piece>, grid, dim3(kMoveThreads), 0, stream, a, elem_bytes);
+}
+
+}  // namespace
+
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" int dspark_attention_weights(const void *q, int64_t ld_q, int32_t dtype, int32_t n_q_heads,
+                                        int32_t max_rows, const int32_t *cu_seqlens, const int32_t *prefix_lens,
+                                        int32_t B, const uint32_t *ancestors, float scale,
+                                        const dspark_kv_cache *cache, const float *lse, const int32_t *counts,
+                                        float decay, const float *weights, float *weights_out, int32_t length,
+                                        const int32_t *pos, int32_t *positions, int32_t *status, void *stream) {
+    const int rc = kv_check(cache);
+    if (rc != DSPARK_OK) return rc;
+    if (!q || !lse || !weights || !weights_out || !cu_seqlens || !prefix_lens || !status || max_rows < 0 ||
+        B < 1 || B > cache->n_requests || n_q_heads < 1 || n_q_heads % cache->n_kv_heads || length < 1)
+        return DSPARK_ERR_INVALID_ARG;
+    if (dtype != DSPARK_DTYPE_BF16 && dtype != DSPARK_DTYPE_F32) return DSPARK_ERR_INVALID_ARG;
+    if (ld_q < (int64_t)n_q_heads * cache->head_dim || (pos != nullptr) != (positions != nullptr))
+        return DSPARK_ERR_INVALID_ARG;
+    if (!(scale - scale == 0.0f) || !(decay - decay == 0.0f)) return DSPARK_ERR_INVALID_ARG;
+    if (n_q_heads > 65535 || B > 65535) return DSPARK_ERR_UNSUPPORTED;
+    WeightsArgs t;
+    AttendArgs &a = t.a;
+    a.q = q;
+    a.ld_q = ld_q;
+    a.out = nullptr;
+    a.ld_out = 0;
+    a.lse = nullptr;
+    a.cu = cu_seqlens;
+    a.prefix = prefix_lens;
+    a.ancestors = ancestors;
+    a.B = B;
+    a.n_q_heads = n_q_heads;
+    a.max_rows = max_rows;
+    a.scale = scale;
+    a.cache = kv_view(*cache);
+    a.status = status;
+    t.lse = lse;
+    t.counts = counts;
+    t.decay = decay;
+    t.weights = weights;
+    t.weights_out = weights_out;
+    t.length = length;
+    t.pos = pos;
+    t.positions = positions;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == DSPARK_DTYPE_BF16 ? launch_weights<__nv_bfloat16>(t, cache->dtype, st)
+                                                     : launch_weights<float>(t, cache->dtype, st);
+    return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+extern "C" size_t dspark_kv_evict_workspace_bytes(int32_t B, int32_t n_kv_heads, int32_t length) {
+    if (B < 1 || n_kv_heads < 1 || length < 1) return 0;
+    const size_t lines = (size_t)B * n_kv_heads;
+    return round256(B * 4) + round256(lines * 4) + round256(lines * 2 * (length / 2) * 4);
+}
+
+extern "C" int dspark_kv_evict(const dspark_kv_cache *cache, const int32_t *lens, const int32_t *now, int32_t B,
+                               int32_t keep, int32_t recent, const float *weights, float *weights_out,
+                               const int32_t *positions, int32_t *positions_out, int32_t length,
+                               int32_t *new_lens, void *workspace, size_t workspace_bytes, int32_t *status,
+                               void *stream) {
+    const int rc = kv_check(cache);
+    if (rc != DSPARK_OK) return rc;
+    if (!lens || !now || !weights || !weights_out || !positions || !positions_out || !new_lens || !status ||
+        B < 1 || B > cache->n_requests || length < 1 || keep < 1 || recent < 0 || recent > keep)
+        return DSPARK_ERR_INVALID_ARG;
+    if (cache->n_kv_heads > 65535 || B > 65535) return DSPARK_ERR_UNSUPPORTED;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < dspark_kv_evict_workspace_bytes(B, cache->n_kv_heads, length))
+        return DSPARK_ERR_WORKSPACE;
+    EvictArgs a;
+    a.cache = kv_view(*cache);
+    if (cache->dtype != DSPARK_DTYPE_E4M3) a.cache.k_scale = a.cache.v_scale = nullptr;
+    a.lens = lens;
+    a.now = now;
+    a.B = B;
+    a.keep = keep;
+    a.recent = recent;
+    a.length = length;
+    a.weights = weights;
+    a.weights_out = weights_out;
+    a.positions = positions;
+    a.positions_out = positions_out;
+    a.new_lens = new_lens;
+    a.most = most_moves(keep, length);
+    const size_t lines = (size_t)B * cache->n_kv_heads;
+    unsigned char *w = static_cast<unsigned char *>(workspace);
+    a.cut = reinterpret_cast<int32_t *>(w);
+    a.n_moves = reinterpret_cast<int32_t *>(w + round256(B * 4));
+    a.moves = reinterpret_cast<int32_t *>(w + round256(B * 4) + round256(lines * 4));
+    a.status = status;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e =
+        launch_pdl(evict_select_kernel, dim3(cache->n_kv_heads, B), dim3(kSelectThreads), 0, st, a);
+    if (e == cudaSuccess) {
+        const int elem = kv_elem_bytes(cache->dtype);
+        const bool wide = cache->head_dim * elem % 16 == 0 && aligned(cache->k, 16) && aligned(cache->v, 16) &&
+                          cache->page_stride * elem % 16 == 0 && cache->token_stride * elem % 16 == 0 &&
+                          cache->head_stride * elem % 16 == 0;
+        e = wide        ? launch_moves<uint4>(a, elem, st)
+            : elem == 4 ? launch_moves<uint32_t>(a, elem, st)
+            : elem == 2 ? launch_moves<uint16_t>(a, elem, st)
+                        : launch_moves<uint8_t>(a, elem, st);
+    }
+    return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}

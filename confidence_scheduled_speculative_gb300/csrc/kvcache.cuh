@@ -128,4 +128,25 @@ inline KvView kv_view(const dspark_kv_cache &c) {
     return w;
 }
 
+// Whether any of `rows` rows of `bytes_a` at a, ld_a bytes apart, shares a byte with one
+// of `bytes_b` at b, ld_b apart (no stride is below its rows' bytes).  Slices of one
+// buffer, side by side or one after the other, do not.
+inline bool rows_overlap(const void *a, int64_t ld_a, int64_t bytes_a, const void *b, int64_t ld_b,
+                         int64_t bytes_b, int64_t rows) {
+    const int64_t x = (int64_t)reinterpret_cast<uintptr_t>(a), y = (int64_t)reinterpret_cast<uintptr_t>(b);
+    if (y >= x + (rows - 1) * ld_a + bytes_a || x >= y + (rows - 1) * ld_b + bytes_b) return false;
+    // the rows of b that begin last before, and first after, the begin of a row of a
+    // (with equal strides one row of a stands for all)
+    for (int64_t i = 0; i < (ld_a == ld_b ? 1 : rows); ++i) {
+        const int64_t from = x + i * ld_a - y;
+        const int64_t first = from / ld_b - (from % ld_b < 0);
+        for (int64_t j = first; j <= first + 1; ++j) {
+            const bool there = ld_a == ld_b ? j > -rows && j < rows : j >= 0 && j < rows;
+            const int64_t off = j * ld_b - from;  // from the begin of a's row to that of b's
+            if (there && off < bytes_a && off > -bytes_b) return true;
+        }
+    }
+    return false;
+}
+
 }  // namespace dspark

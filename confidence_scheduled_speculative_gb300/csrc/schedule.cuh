@@ -46,6 +46,17 @@ __device__ __forceinline__ bool usable(const AttendArgs &a, const Window &w, boo
     return !bad;
 }
 
+// The last request that starts at or before a row.
+__device__ __forceinline__ int request_of(const AttendArgs &a, int row) {
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(a.cu + mid) <= row) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
 constexpr int kFewRows = 8;  // query rows of a kv head that fewrows.cuh multiplies at once
 
 // The window tokens that token i of a window sees, as bits.

@@ -778,6 +778,200 @@ DSPARK_API int dspark_tree_attention(const void *q, int64_t ld_q, int32_t dtype,
                                      int64_t ld_out, float *lse, void *workspace,
                                      size_t workspace_bytes, int32_t *status, void *stream);
 
+/* ------------------------------------------------ attention, latent cache
+ *
+ * Models whose keys and values are projections of one latent vector a token,
+ * shared by all heads, keep only that vector c (latent_dim elements) and a key
+ * part r (rope_dim elements) that is rotated and shared too.  A window of
+ * drafted tokens attends in the absorbed form: the key projection is taken into
+ * the queries and the value projection is applied to the outputs, both by the
+ * caller's own products.  A prompt attends in the expanded form, over keys and
+ * values of every head.  The formulas are below. */
+
+#define DSPARK_MAX_LATENT_DIM 512
+#define DSPARK_MAX_LATENT_ROPE 128
+
+/* One layer's paged latent cache (host struct pointing at DEVICE memory).
+ * Position p of request r lies in page g = block_table[r * table_width + p /
+ * page_size]: its latent vector, and its rotated key part directly behind it, from
+ * element g * page_stride + (p % page_size) * token_stride of data. */
+typedef struct {
+    int32_t dtype;       /* DSPARK_DTYPE_BF16 or _F32 */
+    int32_t n_pages;     /* pages in the pool, >= 1 */
+    int32_t page_size;   /* tokens a page, >= 1 */
+    int32_t latent_dim;  /* 2..DSPARK_MAX_LATENT_DIM, even */
+    int32_t rope_dim;    /* 2..DSPARK_MAX_LATENT_ROPE, even */
+    int32_t n_requests;  /* rows of block_table, >= 1 */
+    int32_t table_width; /* pages a row of block_table lists, >= 1 */
+    int64_t page_stride, token_stride; /* elements, >= 0 */
+    void *data;
+    const int32_t *block_table; /* [n_requests, table_width] */
+} dspark_latent_cache;
+
+/* Rows [latent | key part] into the cache, and the queries' rotated parts, in one
+ * pass.  In 32 bits, rounded once at the end:
+ *   c_d = x_d / sqrt(mean(x^2) + eps) * weight_d over the latent part (k_weight
+ *   given, else c = x); the key part, and each head's query part, rotated.
+ *   x            [max_rows, latent_dim + rope_dim] rows of `dtype` (BF16 or F32),
+ *                ld_x elements apart
+ *   q, q_out     the rope_dim elements of n_q_heads heads a row, rows ld_* and
+ *                heads hs_* elements apart, so that q may be a slice of the
+ *                queries' projection and q_out of the absorbed queries.  They may
+ *                be the same (in place) and must not overlap in any other way.
+ *                Both NULL with n_q_heads = 0 when only the cache is written
+ *   nr           host: k_weight is [latent_dim] or NULL, q_weight NULL; cos_sin and
+ *                its rope_dim, which is the cache's, are required
+ *   req, pos, cache_pos, totals   as in dspark_kv_append
+ * A request >= n_requests, a cache position outside the block table or a page
+ * outside the pool flags DSPARK_STATUS_BAD_INDEX, and that row is not stored (its
+ * query part is written); a position outside [0, n_pos) flags the same, and
+ * nothing of that row is written.  Two rows of a call must not share a slot.
+ * Errors: INVALID_ARG (null pointer, dtype, a stride below what it spans, negative
+ * counts, rope_dim not the cache's, eps negative or NaN, a query weight, and for
+ * the cache null pointers, dtype, counts < 1, negative strides); UNSUPPORTED
+ * (latent_dim, rope_dim); CUDA. */
+DSPARK_API int dspark_latent_append(const void *x, int64_t ld_x, const void *q, int64_t ld_q,
+                                    int64_t hs_q, int32_t dtype, int32_t n_q_heads,
+                                    const dspark_latent_cache *cache /* host */,
+                                    const dspark_norm_rope *nr /* host */, const int32_t *req,
+                                    const int32_t *pos, const int32_t *cache_pos,
+                                    const int32_t *totals, int32_t max_rows, void *q_out,
+                                    int64_t ld_q_out, int64_t hs_q_out, int32_t *status,
+                                    void *stream);
+
+/* Workspace of dspark_latent_attention, for any number of requests, rows and
+ * positions; need not be cleared. */
+DSPARK_API size_t dspark_latent_attention_workspace_bytes(int32_t n_q_heads, int32_t latent_dim);
+
+/* dspark_tree_attention in the absorbed form: for a query q of latent_dim + rope_dim
+ * elements over the visible positions p, with [c_p | r_p] their cache entries,
+ *   s_p = scale * q . [c_p | r_p]    m = max s_p    l = sum exp(s_p - m)
+ *   out = sum exp(s_p - m) c_p / l (latent_dim elements)     lse = m + ln l
+ * Windows, visibility, rows that see nothing, what is not seen, bad windows and bad
+ * positions as there.
+ *   q            [max_rows, n_q_heads * (latent_dim + rope_dim)] rows of `dtype` (BF16
+ *                or F32), ld_q elements apart
+ *   out          [max_rows, n_q_heads * latent_dim] rows, ld_out elements apart; must
+ *                not share an element with q
+ *   lse          [max_rows, n_q_heads] fp32, nullable
+ * BF16 rows over a BF16 cache with latent_dim 512, rope_dim 64, page_size a multiple
+ * of 16 and 16-byte aligned bases and strides run on the tensor cores, the weights
+ * exp(s - m) rounded to BF16; anything else in 32 bits throughout.  The order of all
+ * sums is fixed by the lengths: a call repeated gives the same bits.
+ * Errors: INVALID_ARG (null pointer, B outside 1..n_requests, n_q_heads < 1, dtype, a
+ * stride below a row, max_rows < 0, scale not finite, out over q, the cache's);
+ * UNSUPPORTED (latent_dim, rope_dim, more than 65535 heads); WORKSPACE; CUDA. */
+DSPARK_API int dspark_latent_attention(const void *q, int64_t ld_q, int32_t dtype,
+                                       int32_t n_q_heads, int32_t max_rows,
+                                       const int32_t *cu_seqlens, const int32_t *prefix_lens,
+                                       int32_t B, const uint32_t *ancestors, float scale,
+                                       const dspark_latent_cache *cache /* host */, void *out,
+                                       int64_t ld_out, float *lse, void *workspace,
+                                       size_t workspace_bytes, int32_t *status, void *stream);
+
+/* Causal attention of prompts, ragged: request r's queries are rows
+ * cu_seqlens[r]..cu_seqlens[r+1]-1 of q, its keys and values rows
+ * cu_keys[r]..cu_keys[r+1]-1 of k and v, and its last query stands at its last key:
+ * of n queries and m keys, query i sees keys 0..m - n + i (none if that is
+ * negative).  Of any length.  For query head h, with kv head g = h / (n_q_heads /
+ * n_kv_heads), and a query of key_dim + shared_dim elements:
+ *   s_j = scale * (q[0:key_dim] . k_jg + q[key_dim:] . k_shared_j)
+ *   out = softmax(s) . v_g (value_dim elements)     lse = ln sum exp(s_j)
+ * shared_dim = 0 (k_shared NULL) is attention over keys and values as they are; with
+ * it, the expanded form over a latent cache's rows, k_shared their rotated part.
+ *   q            [max_rows, n_q_heads * (key_dim + shared_dim)], ld_q elements apart
+ *   k, v         heads hs_k and hs_v elements apart (they may be the two parts of one
+ *                projection's heads), rows ld_k and ld_v; max_keys rows
+ *   k_shared     [max_keys, shared_dim] rows ld_shared elements apart
+ *   out          [max_rows, n_q_heads * value_dim], ld_out elements apart; must not
+ *                share an element with an input
+ *   lse          [max_rows, n_q_heads] fp32, nullable
+ * A row that sees nothing gets out = 0 and lse = -inf.  What a row does not see has
+ * no effect on it, NaN and infinities included.  BF16 with key_dim 128, shared_dim 64
+ * or 0, value_dim 128 and 16-byte aligned bases and strides runs on the tensor cores,
+ * the weights rounded to BF16; anything else in 32 bits throughout.
+ * A range outside the rows or the keys, or one that descends (BAD_LEN): that
+ * request's rows are unspecified, the others not affected.  Rows of no request are
+ * left alone.
+ * Errors: INVALID_ARG (null pointer, dtype, B < 1, n_q_heads not a positive multiple
+ * of n_kv_heads, a stride below what it spans, negative counts, scale not finite, out
+ * over q); UNSUPPORTED (key_dim, shared_dim or value_dim above
+ * DSPARK_MAX_HEAD_DIM, key_dim or value_dim < 1, more than 65535 heads); CUDA. */
+DSPARK_API int dspark_prompt_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                       int64_t hs_k, const void *k_shared, int64_t ld_shared,
+                                       const void *v, int64_t ld_v, int64_t hs_v, int32_t dtype,
+                                       int32_t n_q_heads, int32_t n_kv_heads, int32_t key_dim,
+                                       int32_t shared_dim, int32_t value_dim, int32_t max_rows,
+                                       int32_t max_keys, const int32_t *cu_seqlens,
+                                       const int32_t *cu_keys, int32_t B, float scale, void *out,
+                                       int64_t ld_out, float *lse, int32_t *status, void *stream);
+
+/* --------------------------------------------- a cache that is kept short
+ *
+ * Which positions of a cache a request attends to is gathered step by step, for each
+ * kv head; those that gathered least can then be evicted.  A head's entries need no
+ * order (keys carry their rotation), so an eviction moves entries from behind the new
+ * end into the places that became free before it and touches nothing else.  Later
+ * tokens are appended with cache_pos from the new length on and pos as before. */
+
+/* Adds the attention of a window's rows (dspark_tree_attention first, for lse) to what
+ * each position of the cache has gathered.  For request r with prefix P and the
+ * first n = counts[r] rows of its window, kv head h and position p:
+ *   weights_out[r][h][p] = (p < P ? decay * weights[r][h][p] : 0)
+ *       + sum over those rows and the head's query heads that see p of
+ *         exp(scale * q . k_p - lse)                     for p < P + n
+ *   weights_out[r][h][p] = 0                             from P + n on
+ *   positions[r][h][P + i] = pos[cu_seqlens[r] + i]      for i < n (with positions)
+ *   q, cu_seqlens, prefix_lens, ancestors, scale, cache   as in dspark_tree_attention
+ *   lse          [max_rows, n_q_heads] fp32, as it left them
+ *   counts       device [B] (nullable: whole windows): how many of a window's rows
+ *                count (the accepted ones: commit_lens)
+ *   decay        finite
+ *   weights, weights_out   [B, n_kv_heads, length] fp32, may be the same
+ *   pos, positions         device [max_rows] and [B, n_kv_heads, length] int32,
+ *                both or neither
+ * Sums are held in 32 bits and their order is fixed.  What a row does not see has no
+ * effect.  A window as dspark_tree_attention flags it, counts outside the window (BAD_LEN)
+ * and P + n > length (CAPACITY): that request's weights are left alone.  A page outside
+ * the pool flags BAD_INDEX; its positions gather nothing.
+ * Errors: those of dspark_tree_attention (there is no workspace and no out), and
+ * INVALID_ARG (length < 1, decay not finite, pos without positions). */
+DSPARK_API int dspark_attention_weights(const void *q, int64_t ld_q, int32_t dtype,
+                                        int32_t n_q_heads, int32_t max_rows,
+                                        const int32_t *cu_seqlens, const int32_t *prefix_lens,
+                                        int32_t B, const uint32_t *ancestors, float scale,
+                                        const dspark_kv_cache *cache /* host */, const float *lse,
+                                        const int32_t *counts, float decay, const float *weights,
+                                        float *weights_out, int32_t length, const int32_t *pos,
+                                        int32_t *positions, int32_t *status, void *stream);
+
+/* Workspace of dspark_kv_evict; need not be cleared. */
+DSPARK_API size_t dspark_kv_evict_workspace_bytes(int32_t B, int32_t n_kv_heads, int32_t length);
+
+/* Cuts each request's cache down to `keep` entries a kv head.  Of the n = lens[r]
+ * entries of a head, those stay that rank first by: position >= now[r] - recent; then
+ * the larger weight (a NaN below all others; BAD_INPUT); then the lower place.  With
+ * n' = min(n, keep), the i-th entry in order that stays from place n' on moves to the i-th
+ * free place below n'; the others lie as they did.
+ *   cache        keys, values and scales move; places from n' on keep what they held
+ *   lens, now    device [B]: entries in the cache, and tokens so far
+ *   weights, positions          [B, n_kv_heads, length], as dspark_attention_weights left
+ *                them (positions of a cache that has never been cut: 0, 1, 2, ...)
+ *   weights_out, positions_out  the same after the eviction, 0 from n' on; may be
+ *                weights and positions themselves
+ *   new_lens     device [B]: n'; may be lens
+ * lens below 0 or above length or the block table (BAD_LEN): that request, its
+ * entries, ledger and length are left as they are (new_lens = lens).  A page outside
+ * the pool flags BAD_INDEX, and the entry is not moved.
+ * Errors: INVALID_ARG (null pointer, B outside 1..n_requests, length < 1, keep < 1,
+ * recent outside 0..keep, the cache's); UNSUPPORTED (head_dim); WORKSPACE; CUDA. */
+DSPARK_API int dspark_kv_evict(const dspark_kv_cache *cache /* host */, const int32_t *lens,
+                               const int32_t *now, int32_t B, int32_t keep, int32_t recent,
+                               const float *weights, float *weights_out, const int32_t *positions,
+                               int32_t *positions_out, int32_t length, int32_t *new_lens,
+                               void *workspace, size_t workspace_bytes, int32_t *status,
+                               void *stream);
+
 #ifdef __cplusplus
 }
 #endif
