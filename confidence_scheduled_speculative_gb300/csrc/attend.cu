@@ -40,8 +40,8 @@
 #include "kvcache.cuh"
 #include "schedule.cuh"
 #include "tensor.cuh"
+#include "tensormap.cuh"
 
-#include <atomic>
 #include <type_traits>
 
 namespace dspark {
@@ -208,27 +208,6 @@ struct Ring {
             slot = 0;
             parity ^= 1;
         }
-    }
-};
-
-// Where a position lies, for a lane that steps through the tiles of a segment:
-// the table's entry is loaded ahead of its use.
-struct Place {
-    int col, token;
-    __device__ __forceinline__ void begin(const KvView &c, int pos) {
-        col = (unsigned)pos / (unsigned)c.page_size;
-        token = pos - col * c.page_size;
-    }
-    __device__ __forceinline__ void step(const KvView &c) {
-        token += kTile;
-        while (token >= c.page_size) {
-            token -= c.page_size;
-            ++col;
-        }
-    }
-    // the entry; the pool's size, a page it does not have, past the end
-    __device__ __forceinline__ int entry(const KvView &c, int r, bool in) const {
-        return in ? __ldg(c.table + (long long)r * c.table_width + col) : c.n_pages;
     }
 };
 
@@ -1207,50 +1186,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) attend_join_kernel(const T
 }
 
 namespace {
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                              CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder, looked up once.
-EncodeFn encoder() {
-    static std::atomic<EncodeFn> kept{nullptr};
-    EncodeFn f = kept.load(std::memory_order_acquire);
-    if (f) return f;
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-        return nullptr;
-    f = reinterpret_cast<EncodeFn>(p);
-    kept.store(f, std::memory_order_release);
-    return f;
-}
-
-int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
-
-// A 4-D tensor map of bfloat16 or bytes; boxes of `width` elements a row, with the
-// swizzle of that many bytes or none.  (L2 promotion: a head's codes are 128 bytes beside
-// the next head's, which 256 bytes fetch as well.  Two long contexts' trees then read 956
-// MB, with 128 bytes 618, in the same 264 us: HBM does not bound them.)
-bool encode(CUtensorMap *map, const void *p, int elem_bytes, int width, bool swizzle, const int64_t (&dims)[4],
-            const int64_t (&strides)[3], int box1, int box3) {
-    const EncodeFn f = encoder();
-    if (!f) return false;
-    cuuint64_t d[4], s[3];
-    for (int i = 0; i < 4; ++i) d[i] = (cuuint64_t)dims[i];
-    for (int i = 0; i < 3; ++i) s[i] = (cuuint64_t)(strides[i] * elem_bytes);
-    const cuuint32_t box[4] = {(cuuint32_t)width, (cuuint32_t)box1, 1, (cuuint32_t)box3};
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    const bool codes = elem_bytes == 1;
-    return f(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-             const_cast<void *>(p), d, s, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
-             : width * elem_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 

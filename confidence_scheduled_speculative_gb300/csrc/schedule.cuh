@@ -265,6 +265,27 @@ __device__ __forceinline__ bool share_of(const TensorArgs &t, Begin *begin, long
     return true;
 }
 
+// Where a position lies, for a lane that steps through the tiles of a segment:
+// the table's entry is loaded ahead of its use.
+struct Place {
+    int col, token;
+    __device__ __forceinline__ void begin(const KvView &c, int pos) {
+        col = (unsigned)pos / (unsigned)c.page_size;
+        token = pos - col * c.page_size;
+    }
+    __device__ __forceinline__ void step(const KvView &c) {
+        token += kTile;
+        while (token >= c.page_size) {
+            token -= c.page_size;
+            ++col;
+        }
+    }
+    // the entry; the pool's size, a page it does not have, past the end
+    __device__ __forceinline__ int entry(const KvView &c, int r, bool in) const {
+        return in ? __ldg(c.table + (long long)r * c.table_width + col) : c.n_pages;
+    }
+};
+
 // Tells the join, after a CTA's last segment s (its k-th) that is not a whole job, of
 // the job that begins here and ends in a later CTA, or of the one that the whole of
 // this CTA lies in.
