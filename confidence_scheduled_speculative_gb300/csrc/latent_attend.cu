@@ -12,28 +12,31 @@
 //   position, each with a running maximum and sum, joined at the end.
 //
 // latent_tensor_kernel   bfloat16 over a bfloat16 cache with 512 + 64 elements a token, on
-//   the tensor cores.  A job is a request and 64 of its (token, head) rows, taken as they
-//   come, so that a tile may end inside a token; a step is 64 positions, whose entries are
-//   fetched once for both products:  S = Q [C | R]^T into tensor memory, then
+//   the tensor cores of two CTAs at a time.  A job is a request and 128 of its (token,
+//   head) rows, taken as they come, so that a tile may end inside a token; a step is 64
+//   positions:  S = Q [C | R]^T into tensor memory, then
 //     y = S c   m' = max(m, max y)   w = 2^(y - m')   l = l 2^(m - m') + sum w
 //     O = O 2^(m - m') + W C
 //   m moves only when a row's maximum grows by 2^kLazy (until then w may pass 1, and O is
-//   not touched).  64 rows, not 128, since O alone is 512 columns of 32 bits a row and
-//   tensor memory has 512 columns for 128 lanes: with 64 rows O takes half of it, two
-//   score tiles an eighth, and two thirds of the queries the rest, which leaves shared
-//   memory for two and a half tiles of entries.
-//   One warp copies (TMA), one issues both products, four do the softmax, a thread half a
-//   row's positions, and four bring the next job's queries.  One CTA an SM.  CTAs work in
-//   teams of two where requests have more rows than a tile: the two take neighbouring row
-//   tiles over the same positions at the same time, so that the entries come from HBM once
-//   and from L2 the second time.  The tiles of all jobs are dealt evenly to the teams, so
-//   jobs are split along the positions where there are few, and latent_join_kernel adds
-//   the parts in a fixed order.
+//   not touched).
+//   A CTA has 64 of the rows: O alone is 512 columns of 32 bits a row, and for 128 rows
+//   that is all of an SM's tensor memory.  With products over a pair of CTAs 64 rows run at
+//   the full rate (alone they take half of it, or with .ws 0.6 to 0.8), and each CTA
+//   holds half of either product's right operand: the keys of 32 of the positions, and 256
+//   of the elements of all 64 as values.  An entry comes once for each product, but the
+//   keys' buffer is free again as soon as the scores are there.
+//   One warp copies (TMA), having asked L2 for the entries four tiles ahead, one of the
+//   first CTA issues both products, four do the softmax, a thread half a row's positions,
+//   and four bring the next job's queries.  The tiles of all jobs are dealt evenly to the
+//   pairs, so jobs are split along the positions where there are few, and
+//   latent_join_kernel adds the parts in a fixed order.
 
 #include "latentcache.cuh"
 #include "schedule.cuh"
 #include "tensor.cuh"
 #include "tensormap.cuh"
+
+#include <atomic>
 
 namespace dspark {
 
@@ -129,20 +132,21 @@ __global__ void __launch_bounds__(kAnyWarps * 32) latent_any_kernel(LatentArgs t
 
 // --------------------------------------------------- tensor-core kernel
 
-constexpr int kLatent = 512, kEntry = 576;  // of an entry, its latent part
-constexpr int kRows = 64;                   // (token, head) rows of a job
-constexpr int kLatentCtas = 160;            // at most
-constexpr int kChunkBytes = kTile * 128;    // 64 elements of 64 tokens, or of 64 rows
-constexpr int kUnitBytes = 4 * kChunkBytes; // half of a tile's latent parts
-constexpr int kUnits = 5, kKeyParts = 3;    // buffers: 2.5 tiles
-constexpr int kQChunks = 6;                 // 64-element parts of the queries in tensor memory
-constexpr int kQAt = 0;                     // the other three, in shared memory
-constexpr int kUnitAt = kQAt + 3 * kChunkBytes;
-constexpr int kKeyAt = kUnitAt + kUnits * kUnitBytes;
-constexpr int kWeightsAt = kKeyAt + kKeyParts * kChunkBytes;
-constexpr int kControlAt = kWeightsAt + 2 * kChunkBytes;
-constexpr int kLatentSmem = kControlAt + 2816;
-constexpr int kOutCol = 0, kScoreCol = 256, kQueryCol = 320;  // columns of tensor memory
+constexpr int kLatent = 512, kEntry = 576;   // of an entry, its latent part
+constexpr int kChunks = kEntry / 64;         // parts of 64 elements
+constexpr int kRows = 64;                    // (token, head) rows of a CTA
+constexpr int kPairRows = 2 * kRows;         // of a job
+constexpr int kLatentCtas = 160;             // at most
+constexpr int kChunkBytes = kRows * 128;     // 64 elements of 64 rows, or of 64 tokens
+constexpr int kKeyChunk = kTile / 2 * 128;   // of 32 tokens
+constexpr int kKeyBytes = kChunks * kKeyChunk, kValueBytes = 4 * kChunkBytes;
+constexpr int kStages = 2;                   // of keys, of values, of scores, of weights
+constexpr int kKeyAt = kChunks * kChunkBytes;  // behind the queries
+constexpr int kValueAt = kKeyAt + kStages * kKeyBytes;
+constexpr int kWeightsAt = kValueAt + kStages * kValueBytes;
+constexpr int kControlAt = kWeightsAt + kStages * kChunkBytes;
+constexpr int kLatentSmem = kControlAt + 3072;
+constexpr int kOutCol = 0, kScoreCol = 256;  // columns of tensor memory
 constexpr int kLatentThreads = 320, kCopyWarp = 8, kMatrixWarp = 9;
 constexpr int kLookAhead = 4;  // tiles whose pages are known, and asked for, ahead of their copy
 constexpr int kLatentJobCost = 2;  // of a job's begin and end, in tiles
@@ -167,41 +171,35 @@ __device__ __forceinline__ bool to_latent(const LatentTensorArgs &t, const Windo
     q->len = w.hi - w.lo;
     q->P = w.P;
     q->tiles = (q->P + q->len + kTile - 1) / kTile;
-    q->row_tiles = (q->len * t.a.n_q_heads + kRows - 1) / kRows;
+    q->row_tiles = (q->len * t.a.n_q_heads + kPairRows - 1) / kPairRows;
     return true;
 }
 
-// Consecutive tiles of one job that a CTA works through.
+// Consecutive tiles of one job that a pair works through.
 struct LatentSegment {
     LatentRequest q = {};
     int r, row_tile, first, count;
-    unsigned k;  // how many the team had before it
 };
 
-// Where a team's share begins: the request, which team's worth of its row tiles, and the
-// unit of that.
+// Where a pair's share begins, and how many units it has.
 struct LatentBegin {
-    int r, group, unit, left;
+    int r, row_tile, unit, left;
     LatentRequest q;
 };
 
-// Walks a team's units: requests in order, in each the row tiles, a team's worth at a
-// time, in each the positions.  Every warp role walks on its own and sees the same.
+// Walks a pair's units: requests in order, in each the row tiles, in each the positions.
+// Every warp role of both CTAs walks on its own and sees the same.
 struct LatentWalk {
-    int left, r, group, unit, team, member;
-    unsigned k;
+    int left, r, row_tile, unit;
     LatentRequest q = {};
     Window ahead;
 
-    __device__ __forceinline__ void begin(const LatentTensorArgs &t, const LatentBegin &b, int team_size, int of) {
+    __device__ __forceinline__ void begin(const LatentTensorArgs &t, const LatentBegin &b) {
         left = b.left;
         r = b.r;
-        group = b.group;
+        row_tile = b.row_tile;
         unit = b.unit;
         q = b.q;
-        team = team_size;
-        member = of;
-        k = 0;
         ahead = load_window(t.a, min(r + 1, t.a.B - 1));
     }
     __device__ __forceinline__ bool next(const LatentTensorArgs &t, LatentSegment *s) {
@@ -209,14 +207,13 @@ struct LatentWalk {
             const int take = t.whole ? 1 : min(q.tiles + kLatentJobCost - unit, left);
             s->q = q;
             s->r = r;
-            s->row_tile = group * team + member;
+            s->row_tile = row_tile;
             s->first = max(unit - kLatentJobCost, 0);
             s->count = t.whole ? q.tiles : max(unit + take - kLatentJobCost, 0) - s->first;
-            s->k = k;
             left -= take;
             unit = 0;
-            if (++group * team >= q.row_tiles) {
-                group = 0;
+            if (++row_tile == q.row_tiles) {
+                row_tile = 0;
                 while (left > 0) {
                     const bool has = to_latent(t, ahead, &q, false);
                     ++r;
@@ -224,64 +221,49 @@ struct LatentWalk {
                     if (has) break;
                 }
             }
-            if (s->count > 0) {
-                ++k;
-                if (s->row_tile < s->q.row_tiles) return true;  // (else the other member's alone)
-            }
+            if (s->count > 0) return true;
         }
         return false;
     }
 };
 
-// The size of teams, this CTA's team's share and where it begins (for all after the next
-// barrier); false where none are left for it.
-//   Teams of one do row_tiles x tiles steps on each CTA, each of whose entries may come from
-// HBM; teams of two do half as many, a step of which takes 0.92 of the time of two (an idle
-// member where the row tiles are odd; the entries come from HBM once).
+// This CTA's pair's share and where it begins (for all after the next barrier); false
+// where none are left for it.
 __device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBegin *begin, long long *scan,
-                                             Deal *deal, int *team_size) {
+                                             Deal *deal) {
     const AttendArgs &a = t.a;
-    const int tid = threadIdx.x, cta = blockIdx.x;
+    const int tid = threadIdx.x, cta = blockIdx.x, at = cta / 2;
     const int per = (a.B + kLatentThreads - 1) / kLatentThreads;
-    long long alone = 0, paired = 0;
+    long long mine = 0;
     LatentRequest q = {};
+    auto job = [&]() { return t.whole ? 1 : q.tiles + kLatentJobCost; };
     for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
-        if (to_latent(t, load_window(a, r), &q, cta == 0)) {
-            const int job = t.whole ? 1 : q.tiles + kLatentJobCost;
-            alone += (long long)job * q.row_tiles;
-            paired += (long long)job * ((q.row_tiles + 1) / 2);
-        }
-    const long long sum_alone = block_sum<long long>(alone, scan), sum_paired = block_sum<long long>(paired, scan);
-    const int team = t.whole || 12 * sum_alone <= 13 * sum_paired ? 1 : 2;
-    const long long mine = team == 1 ? alone : paired, T = team == 1 ? sum_alone : sum_paired;
-    long long total;
-    const long long before = block_exclusive_scan<long long>(mine, scan, &total);
-    const int n = (int)min((long long)((int)gridDim.x / team),
+        if (to_latent(t, load_window(a, r), &q, cta == 0)) mine += (long long)job() * q.row_tiles;
+    long long T;
+    const long long before = block_exclusive_scan<long long>(mine, scan, &T);
+    const int n = (int)min((long long)(gridDim.x / 2),
                            t.whole ? T : (T + kLatentJobCost + 1) / (kLatentJobCost + 2));
     if (tid == 0 && !t.whole) {
         t.desc[cta * kLatentDesc] = 0;
         t.desc[cta * kLatentDesc + 7] = -1;
     }
-    const int at = cta / team;
     if (at >= n) return false;
     deal->n = n;
     deal->each = div_nonneg(T, n);
     deal->rest = (int)(T - deal->each * n);
-    *team_size = team;
     const long long lo = deal->first(at), hi = deal->first(at + 1);
     if (lo >= before && lo < before + mine) {
         long long from = before;
         for (int r = tid * per;; ++r) {
             if (per > 1 && !to_latent(t, load_window(a, r), &q, false)) continue;
-            const int job = t.whole ? 1 : q.tiles + kLatentJobCost;
-            const long long units = (long long)job * ((q.row_tiles + team - 1) / team);
+            const long long units = (long long)job() * q.row_tiles;
             if (lo >= from + units) {
                 from += units;
                 continue;
             }
             begin->r = r;
-            begin->group = (int)div_nonneg(lo - from, job);
-            begin->unit = (int)(lo - from - (long long)begin->group * job);
+            begin->row_tile = (int)div_nonneg(lo - from, job());
+            begin->unit = (int)(lo - from - (long long)begin->row_tile * job());
             begin->left = (int)(hi - lo);
             begin->q = q;
             break;
@@ -290,91 +272,95 @@ __device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBe
     return true;
 }
 
+// Barriers that the issuing warp waits on are the first CTA's (the same place in the other
+// is not used); those that it commits to are each CTA's own.
 struct alignas(16) LatentControl {
-    unsigned long long unit_full[kUnits], unit_empty[kUnits], key_full[kKeyParts], key_empty[kKeyParts];
-    unsigned long long s_full[2], p_ready[2], o_done[2], q_full, q_empty, o_free, drain;
+    unsigned long long key_full[kStages], value_full[kStages], p_ready[2], q_full, o_free;  // the first's
+    unsigned long long key_empty[kStages], value_empty[kStages], s_full[2], o_done[2], value_seen[2], q_empty,
+        drain;
     unsigned tmem;
-    unsigned nonfinite[4];  // window tokens whose values were zeroed, by segment
+    unsigned nonfinite[4];  // window tokens whose values were zeroed in either CTA, by segment
     int abort;
     LatentBegin begin;
     long long scan[40];
     float top[2][2][kRows];  // [tile's parity][half of the positions]
     float sum[2][kRows];
 };
-static_assert(sizeof(LatentControl) <= 2816 && kLatentSmem <= 227 * 1024, "shared memory");
+static_assert(sizeof(LatentControl) <= 3072 && kLatentSmem <= 227 * 1024, "shared memory");
 
-// Where the entries of 64 rows x 64 elements lie: 16-byte piece c of row r.
+// Where the entries of rows of 64 elements lie: 16-byte piece c of row r.
 __device__ __forceinline__ int chunk_piece(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
-__global__ void __launch_bounds__(kLatentThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLatentThreads, 1)
 latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensorArgs t) {
     extern __shared__ __align__(1024) unsigned char smem[];
     LatentControl &ctl = *reinterpret_cast<LatentControl *>(smem + kControlAt);
     const AttendArgs &a = t.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const int rank = (int)cluster_rank();
     const uint32_t base = smem_addr(smem);
     if (tid == 0) {
-        for (int i = 0; i < kUnits; ++i) {
-            mbar_init(smem_addr(&ctl.unit_full[i]), 1);
-            mbar_init(smem_addr(&ctl.unit_empty[i]), 1);
-        }
-        for (int i = 0; i < kKeyParts; ++i) {
-            mbar_init(smem_addr(&ctl.key_full[i]), 1);
-            mbar_init(smem_addr(&ctl.key_empty[i]), 1);
-        }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&ctl.key_full[i]), 1);
+            mbar_init(smem_addr(&ctl.value_full[i]), 1);
+            mbar_init(smem_addr(&ctl.p_ready[i]), 8);
+            mbar_init(smem_addr(&ctl.key_empty[i]), 1);
+            mbar_init(smem_addr(&ctl.value_empty[i]), 1);
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
-            mbar_init(smem_addr(&ctl.p_ready[i]), 4);
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
+            mbar_init(smem_addr(&ctl.value_seen[i]), 1);
         }
-        mbar_init(smem_addr(&ctl.q_full), 4);
+        mbar_init(smem_addr(&ctl.q_full), 8);
+        mbar_init(smem_addr(&ctl.o_free), 8);
         mbar_init(smem_addr(&ctl.q_empty), 1);
-        mbar_init(smem_addr(&ctl.o_free), 4);
         mbar_init(smem_addr(&ctl.drain), 1);
         ctl.abort = 0;
         for (int i = 0; i < 4; ++i) ctl.nonfinite[i] = 0;
         fence_mbar_init();
         prefetch_map(&map);
     }
-    if (warp == kMatrixWarp) tmem_alloc(smem_addr(&ctl.tmem), 512);
+    if (warp == kMatrixWarp) tmem_alloc_pair(smem_addr(&ctl.tmem), 512);
     pdl_wait();
     pdl_trigger();
 
     Deal deal;
-    int team;
-    const int cta = blockIdx.x;
-    if (!latent_share(t, &ctl.begin, ctl.scan, &deal, &team)) {
+    if (!latent_share(t, &ctl.begin, ctl.scan, &deal)) {  // (neither CTA of the pair)
         if (warp == kMatrixWarp) {
             __syncwarp();
-            tmem_free(*(volatile unsigned *)&ctl.tmem, 512);
+            tmem_free_pair(*(volatile unsigned *)&ctl.tmem, 512);
         }
+        cluster_sync();
         return;
     }
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers are there
     tmem_fence_after();
     const uint32_t tmem = ctl.tmem;
     volatile int *abort = &ctl.abort;
     LatentWalk walk;
-    walk.begin(t, ctl.begin, team, cta % team);
+    walk.begin(t, ctl.begin);
     LatentSegment s = {};
     bool ok = true;
     auto wait = [&](unsigned long long *bar, unsigned parity) {
         return ok = warp_wait(ok, smem_addr(bar), parity, abort, a.status);
     };
+    auto first_cta = [&](unsigned long long *bar) { return cluster_addr(smem_addr(bar), 0); };
     const int hq = a.n_q_heads;
     unsigned done = 0, seg = 0;  // tiles and segments so far
 
     if (warp == kCopyWarp) {
         // ------------------------------------------------ copy warp
-        const int boxes = kTile / t.box;
-        const int box = lane >> 2, chunk = lane & 3;  // of a unit; lane b < boxes looks up box b
-        unsigned unit = 0, unit_parity = 0, part = 0, part_parity = 0;
+        // Boxes of a tile: lane b < boxes looks up box b.  Keys: nine parts of each of this
+        // CTA's half of the boxes.  Values: four of each box.
+        const int boxes = kTile / t.box, key_boxes = boxes / 2;
+        const int key_box = rank * key_boxes + lane / kChunks, key_chunk = lane % kChunks;
+        const bool key_lane = lane < kChunks * key_boxes;
+        const int value_box = lane >> 2, value_chunk = 4 * rank + (lane & 3);
+        const bool value_lane = value_box < boxes;
+        const uint32_t key_dst = base + kKeyAt + key_chunk * kKeyChunk + lane / kChunks * t.box * 128;
+        const uint32_t value_dst = base + kValueAt + (lane & 3) * kChunkBytes + value_box * t.box * 128;
         while (ok && walk.next(t, &s)) {
             const int n = s.q.P + s.q.len, from = s.first * kTile + lane * t.box;
-            // what each of the team's two asks L2 for, if both are there: the latent part's
-            // first half, with the key part, or its second half
-            const bool both = team == 2 && (s.row_tile ^ 1) < s.q.row_tiles;
-            const bool first_half = !both || cta % 2 == 0, second_half = !both || cta % 2 == 1;
             Place at;
             at.begin(a.cache, lane < boxes ? from : 0);
             // tile i's page and token of this lane's box, kLookAhead tiles ahead
@@ -388,195 +374,154 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
 #pragma unroll
                 for (int j = 0; j < kLookAhead; ++j) pages[j] = pages[j + 1], tokens[j] = tokens[j + 1];
             };
-            auto fetch = [&](int i) {  // to L2, the tile looked up before the last
-                const int page = pages[kLookAhead - 1], token = tokens[kLookAhead - 1];
-                if (i >= s.count) return;
-                const int my_page = __shfl_sync(kFullMask, page, box), my_token = __shfl_sync(kFullMask, token, box);
-                if (box >= boxes || (unsigned)my_page >= (unsigned)a.cache.n_pages) return;
-                if (first_half) {
-                    if (chunk == 0) tma_prefetch_4d(&map, kLatent, my_token, 0, my_page);
-                    tma_prefetch_4d(&map, chunk * 64, my_token, 0, my_page);
-                }
-                if (second_half) tma_prefetch_4d(&map, (4 + chunk) * 64, my_token, 0, my_page);
-            };
 #pragma unroll
             for (int j = 0; j < kLookAhead; ++j) {
                 look_up(j);
                 shift();
             }
             for (int i = 0; i < s.count; ++i) {
+                const unsigned stage = (done + i) & 1, parity = (done + i) >> 1;
                 look_up(i + kLookAhead);
+                {  // to L2, the tile that was looked up before
+                    const int page = __shfl_sync(kFullMask, pages[kLookAhead - 1], key_box % boxes);
+                    const int token = __shfl_sync(kFullMask, tokens[kLookAhead - 1], key_box % boxes);
+                    if (key_lane && (unsigned)page < (unsigned)a.cache.n_pages)
+                        tma_prefetch_4d(&map, key_chunk * 64, token, 0, page);
+                }
                 int page = pages[0];
                 const int token = tokens[0];
+                shift();
                 // a page outside the pool, as past the request's end, arrives as zeros
                 if (lane < boxes && from + i * kTile < n && (unsigned)page >= (unsigned)a.cache.n_pages) {
                     flag(a.status, DSPARK_STATUS_BAD_INDEX);
                     page = a.cache.n_pages;
                 }
-                const int my_page = __shfl_sync(kFullMask, page, box), my_token = __shfl_sync(kFullMask, token, box);
-                fetch(i + kLookAhead - 1);
-                shift();
-                if (!wait(&ctl.key_empty[part], part_parity ^ 1)) break;
-                const uint32_t key_bar = smem_addr(&ctl.key_full[part]);
-                if (lane == 0) mbar_expect(key_bar, kChunkBytes);
+                const int key_page = __shfl_sync(kFullMask, page, key_box % boxes);
+                const int key_token = __shfl_sync(kFullMask, token, key_box % boxes);
+                const int value_page = __shfl_sync(kFullMask, page, value_box % boxes);
+                const int value_token = __shfl_sync(kFullMask, token, value_box % boxes);
+                if (!wait(&ctl.key_empty[stage], parity ^ 1)) break;
+                if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.key_full[stage]), 2 * kKeyBytes);
                 __syncwarp();
-                if (lane < boxes)
-                    tma_load_4d(base + kKeyAt + part * kChunkBytes + lane * t.box * 128, &map, kLatent, token, 0, page,
-                                key_bar);
-                if (++part == kKeyParts) part = 0, part_parity ^= 1;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (!wait(&ctl.unit_empty[unit], unit_parity ^ 1)) break;
-                    const uint32_t bar = smem_addr(&ctl.unit_full[unit]);
-                    if (lane == 0) mbar_expect(bar, kUnitBytes);
-                    __syncwarp();
-                    if (box < boxes)
-                        tma_load_4d(base + kUnitAt + unit * kUnitBytes + chunk * kChunkBytes + box * t.box * 128, &map,
-                                    (4 * h + chunk) * 64, my_token, 0, my_page, bar);
-                    if (++unit == kUnits) unit = 0, unit_parity ^= 1;
-                }
-                if (!ok) break;
+                if (key_lane)
+                    tma_load_4d_pair(key_dst + stage * kKeyBytes, &map, key_chunk * 64, key_token, 0, key_page,
+                                     first_cta(&ctl.key_full[stage]));
+                if (!wait(&ctl.value_empty[stage], parity ^ 1)) break;
+                if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.value_full[stage]), 2 * kValueBytes);
+                __syncwarp();
+                if (value_lane)
+                    tma_load_4d_pair(value_dst + stage * kValueBytes, &map, value_chunk * 64, value_token, 0,
+                                     value_page, first_cta(&ctl.value_full[stage]));
             }
+            done += s.count;
         }
-        if (!ok && lane == 0) {
-            // copies still under way write this block's buffers: the last load of each
-            // slot, complete or never begun
-            for (int i = 0; i < kUnits; ++i)
-                mbar_wait(smem_addr(&ctl.unit_full[i]), i < (int)unit ? unit_parity : unit_parity ^ 1);
-            for (int i = 0; i < kKeyParts; ++i)
-                mbar_wait(smem_addr(&ctl.key_full[i]), i < (int)part ? part_parity : part_parity ^ 1);
+        if (!ok && rank == 0 && lane == 0) {
+            // copies still under way write the pair's buffers (each wait ends by itself; the
+            // CTAs leave together)
+            for (int i = 0; i < kStages; ++i)
+                for (int p = 0; p < 2; ++p) {
+                    mbar_wait(smem_addr(&ctl.key_full[i]), p, kWaitLimitNs / 4);
+                    mbar_wait(smem_addr(&ctl.value_full[i]), p, kWaitLimitNs / 4);
+                }
         }
     } else if (warp == kMatrixWarp) {
         // ---------------------------------------------- matrix warp
         // Keeps step as a whole, so that addresses stay in uniform registers; one lane
         // issues.  Scores of tile i, then the output of tile i - 1, whose weights are
         // computed meanwhile.
-        constexpr uint32_t score_word = mma_word(true, kTile, false) - kHalfRows;
-        constexpr uint32_t value_word = mma_word(true, 256, true) - kHalfRows;
-        const uint32_t ubase = __shfl_sync(kFullMask, base, 0), utmem = __shfl_sync(kFullMask, tmem, 0);
-        const bool leader = elect_one();
-        const uint64_t desc_q = smem_operand(ubase + kQAt, 16, 128);
-        const uint64_t desc_unit = smem_operand(ubase + kUnitAt, 16, 128);
-        const uint64_t desc_value = smem_operand(ubase + kUnitAt, kChunkBytes, 128);
-        const uint64_t desc_key = smem_operand(ubase + kKeyAt, 16, 128);
-        const uint64_t desc_w = smem_operand(ubase + kWeightsAt, 16, 128);
-        unsigned unit = 0, unit_parity = 0, value_unit = 0, part = 0, part_parity = 0;
-        // O += W C of the segment's tile i
-        auto values = [&](int i, unsigned tile) {
-            if (i == 0 && seg > 0 && !wait(&ctl.o_free, seg - 1)) return;
-            if (!wait(&ctl.p_ready[tile & 1], tile >> 1)) return;
-            tmem_fence_after();
-            const uint64_t w = desc_w + (tile & 1) * (kChunkBytes >> 4);
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const uint64_t v = desc_value + value_unit * (kUnitBytes >> 4);
-                if (leader) {
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_ws_ss(utmem + kOutCol + 128 * h, w + (k * 32 >> 4), v + (k * 16 * 128 >> 4), value_word,
-                                  i > 0 || k > 0);
-                    mma_commit(smem_addr(&ctl.unit_empty[value_unit]));
-                    if (h == 1) mma_commit(smem_addr(&ctl.o_done[tile & 1]));
-                }
-                __syncwarp();
-                if (++value_unit == kUnits) value_unit = 0;
-            }
-        };
-        while (ok && walk.next(t, &s)) {
-            if (!wait(&ctl.q_full, seg)) break;
-            const int count = __shfl_sync(kFullMask, s.count, 0);
-            for (int i = 0; i < count; ++i) {
-                // (the scores of tile - 2 have been read, and its weights multiplied)
-                const unsigned tile = done + i;
-                const uint32_t d = utmem + kScoreCol + (tile & 1) * 32;
-                if (!wait(&ctl.key_full[part], part_parity)) break;
+        if (rank == 0) {
+            constexpr uint32_t score_word = mma_word(true, kTile, false), value_word = mma_word(true, 256, true);
+            const uint32_t ubase = __shfl_sync(kFullMask, base, 0), utmem = __shfl_sync(kFullMask, tmem, 0);
+            const bool leader = elect_one();
+            const uint64_t desc_q = smem_operand(ubase, 16, 128);
+            const uint64_t desc_key = smem_operand(ubase + kKeyAt, 16, 128);
+            const uint64_t desc_value = smem_operand(ubase + kValueAt, kChunkBytes, 128);
+            const uint64_t desc_w = smem_operand(ubase + kWeightsAt, 16, 128);
+            // O += W C of the segment's tile i
+            auto values = [&](int i, unsigned tile) {
+                const unsigned b = tile & 1;
+                if (i == 0 && seg > 0 && !wait(&ctl.o_free, seg - 1)) return;
+                if (!wait(&ctl.value_full[b], tile >> 1)) return;
+                if (lane < 2) cluster_arrive(cluster_addr(smem_addr(&ctl.value_seen[b]), lane));
+                if (!wait(&ctl.p_ready[b], tile >> 1)) return;
                 tmem_fence_after();
+                const uint64_t w = desc_w + b * (kChunkBytes >> 4), v = desc_value + b * (kValueBytes >> 4);
                 if (leader) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ws_ss(d, desc_q + (2 * kChunkBytes + k * 32 >> 4),
-                                  desc_key + (part * kChunkBytes + k * 32 >> 4), score_word, k > 0);
-                    mma_commit(smem_addr(&ctl.key_empty[part]));
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_pair_ss(utmem + kOutCol + 128 * h, w + (k * 32 >> 4),
+                                        v + (2 * h * kChunkBytes + k * 16 * 128 >> 4), value_word, i > 0 || k > 0);
+                    mma_pair_commit(smem_addr(&ctl.value_empty[b]));
+                    mma_pair_commit(smem_addr(&ctl.o_done[b]));
                 }
                 __syncwarp();
-                if (++part == kKeyParts) part = 0, part_parity ^= 1;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!wait(&ctl.unit_full[unit], unit_parity)) break;
+            };
+            while (ok && walk.next(t, &s)) {
+                if (!wait(&ctl.q_full, seg)) break;
+                const int count = __shfl_sync(kFullMask, s.count, 0);
+                for (int i = 0; i < count; ++i) {
+                    // (the scores of tile - 2 have been read, and its weights multiplied)
+                    const unsigned tile = done + i, b = tile & 1;
+                    if (!wait(&ctl.key_full[b], tile >> 1)) break;
                     tmem_fence_after();
+                    const uint64_t k_at = desc_key + b * (kKeyBytes >> 4);
                     if (leader) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int c = 4 * h + k / 4;  // the 64-element part
-                            const uint64_t b = desc_unit + (unit * kUnitBytes + k / 4 * kChunkBytes + k % 4 * 32 >> 4);
-                            if (c < kQChunks)
-                                mma_ws_ts(d, utmem + kQueryCol + c * 32 + k % 4 * 8, b, score_word, true);
-                            else
-                                mma_ws_ss(d, desc_q + ((c - kQChunks) * kChunkBytes + k % 4 * 32 >> 4), b, score_word,
-                                          true);
-                        }
-                        if (h == 1) {
-                            mma_commit(smem_addr(&ctl.s_full[tile & 1]));
-                            if (i + 1 == count) mma_commit(smem_addr(&ctl.q_empty));
-                        }
+                        for (int k = 0; k < 4 * kChunks; ++k)
+                            mma_pair_ss(utmem + kScoreCol + b * 32, desc_q + (k / 4 * kChunkBytes + k % 4 * 32 >> 4),
+                                        k_at + (k / 4 * kKeyChunk + k % 4 * 32 >> 4), score_word, k > 0);
+                        mma_pair_commit(smem_addr(&ctl.s_full[b]));
+                        mma_pair_commit(smem_addr(&ctl.key_empty[b]));
+                        if (i + 1 == count) mma_pair_commit(smem_addr(&ctl.q_empty));
                     }
                     __syncwarp();
-                    if (++unit == kUnits) unit = 0, unit_parity ^= 1;
+                    if (i > 0) values(i - 1, tile - 1);
+                    if (!ok) break;
                 }
                 if (!ok) break;
-                if (i > 0) values(i - 1, tile - 1);
-                if (!ok) break;
+                values(count - 1, done + count - 1);
+                done += count;
+                ++seg;
             }
-            if (!ok) break;
-            values(count - 1, done + count - 1);
-            done += count;
-            ++seg;
+            // after a timeout: products still under way write tensor memory and barriers of
+            // the pair
+            if (!ok && leader) {
+                mma_pair_commit(smem_addr(&ctl.drain));
+                mbar_wait(smem_addr(&ctl.drain), 0);
+            }
+            __syncwarp();
         }
-        // after a timeout: products still under way write tensor memory and barriers of
-        // this block
-        if (!ok && leader) {
-            mma_commit(smem_addr(&ctl.drain));
-            mbar_wait(smem_addr(&ctl.drain), 0);
-        }
-        __syncwarp();
     } else if (warp >= 4) {
         // --------------------------------------------- query warps
-        // A lane of tensor memory a thread: row m's first six parts into lanes m and 64 + m;
-        // of the other three, which go to shared memory, each of the two takes half.
-        const int lane_at = tid - 128, m = lane_at & 63, half = lane_at >> 6;
-        const uint32_t lanes = tmem + ((uint32_t)(lane_at & ~31) << 16);
+        // Two threads a row, which bring every other of its parts.
+        const int m = (tid - 128) >> 1, half = tid & 1;
         while (ok && walk.next(t, &s)) {
-            const int row = s.row_tile * kRows + m;
+            const int row = s.row_tile * kPairRows + rank * kRows + m;
             const bool there = row < s.q.len * hq;
             const int token = there ? row / hq : 0, head = there ? row % hq : 0;
             const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
                                                              (s.q.row0 + token) * a.ld_q + (long long)head * kEntry);
-            auto piece = [&](int i) { return there ? __ldg(q + i) : make_uint4(0, 0, 0, 0); };
-            uint4 rest[12];
+            constexpr int kBatch = 12, kPieces = 8 * kChunks / 2;
+#pragma unroll 1
+            for (int p = 0; p < kPieces; p += kBatch) {
+                uint4 v[kBatch];
 #pragma unroll
-            for (int i = 0; i < 12; ++i) rest[i] = piece(8 * kQChunks + 12 * half + i);
-            if (seg > 0 && !wait(&ctl.q_empty, seg - 1)) break;
+                for (int i = 0; i < kBatch; ++i)
+                    v[i] = there ? __ldg(q + 2 * (p + i) + half) : make_uint4(0, 0, 0, 0);
+                if (p == 0 && seg > 0) wait(&ctl.q_empty, seg - 1);
+                if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < 12; ++i) {
-                const int p = 12 * half + i;
-                *reinterpret_cast<uint4 *>(smem + kQAt + p / 8 * kChunkBytes + chunk_piece(m, p % 8)) = rest[i];
-            }
-            tmem_fence_after();
-#pragma unroll 2
-            for (int c = 0; c < kQChunks; ++c) {
-                uint32_t x[32];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 v = piece(8 * c + i);
-                    x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+                for (int i = 0; i < kBatch; ++i) {
+                    const int at = 2 * (p + i) + half;
+                    *reinterpret_cast<uint4 *>(smem + at / 8 * kChunkBytes + chunk_piece(m, at % 8)) = v[i];
                 }
-                tmem_store32(lanes + kQueryCol + 32 * c, x);
             }
-            tmem_wait_store();
-            tmem_fence_before();
+            if (!ok) break;
             fence_async_proxy();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.q_full));
+            if (lane == 0) cluster_arrive(first_cta(&ctl.q_full));
             ++seg;
         }
     } else {
@@ -589,10 +534,10 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
         // to the next such barrier, and all leave there.
         bool met = true;
         while (walk.next(t, &s)) {
-            const int n = s.q.P + s.q.len, rows = min(s.q.len * hq - s.row_tile * kRows, kRows);
-            const bool valid = m < rows;
-            const int row = s.row_tile * kRows + min(m, rows - 1);
-            const int token = row / hq, head = row % hq, packed = s.q.row0 + token;
+            const int n = s.q.P + s.q.len, all = s.q.len * hq;
+            const int row = s.row_tile * kPairRows + rank * kRows + m, safe = min(row, all - 1);
+            const bool valid = row < all;
+            const int token = safe / hq, head = safe % hq, packed = s.q.row0 + token;
             const unsigned bits = ancestors_of(a, packed, token, s.q.len);
             if (tid == 0) ctl.nonfinite[(seg + 2) & 3] = 0;  // the one's before the last
             float mx = -INFINITY, l = 0.0f;  // running maximum (to base 2); this half's sum
@@ -675,14 +620,14 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                 if (p0 + kTile > s.q.P) {
                     // Latent vectors past the request's end become zeros, and so do NaN and
                     // infinities of the window (0 x NaN would reach rows that do not see
-                    // them); the rows that do get them at the end.  The scores have been
-                    // computed.
+                    // them); the rows that do get them at the end.  Each CTA does so for the
+                    // elements that it holds as values.
+                    if (!wait(&ctl.value_seen[b], tile >> 1)) continue;
                     const int from = max(s.q.P, p0);
-                    for (int j = tid; j < (p0 + kTile - from) * 64; j += 128) {
-                        const int pos = from + j / 64, piece = j % 64;  // of the latent part
-                        const unsigned u = (2 * tile + piece / 32) % kUnits;
-                        uint4 *at = reinterpret_cast<uint4 *>(smem + kUnitAt + u * kUnitBytes +
-                                                              piece / 8 % 4 * kChunkBytes +
+                    for (int j = tid; j < (p0 + kTile - from) * 32; j += 128) {
+                        const int pos = from + j / 32, piece = j % 32;
+                        uint4 *at = reinterpret_cast<uint4 *>(smem + kValueAt + b * kValueBytes +
+                                                              piece / 8 * kChunkBytes +
                                                               chunk_piece(pos - p0, piece % 8));
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (pos < n) {
@@ -698,36 +643,38 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                                 if (hi16) e[k] &= 0x0000FFFFu;
                             }
                             if (!bad) continue;
-                            atomicOr(&ctl.nonfinite[seg & 3], 1u << (pos - s.q.P));
+                            for (int k = 0; k < 2; ++k)
+                                cluster_or(cluster_addr(smem_addr(&ctl.nonfinite[seg & 3]), k),
+                                           1u << (pos - s.q.P));
                         }
                         *at = v;
                     }
+                    cluster_fence();  // (the noted tokens)
                 }
                 fence_async_proxy();
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&ctl.p_ready[b]));
+                if (lane == 0) cluster_arrive(first_cta(&ctl.p_ready[b]));
             }
             if (!met) break;
             const unsigned last = done + s.count - 1;
             wait(&ctl.o_done[last & 1], last >> 1);
             done += s.count;
             tmem_fence_after();
+            if ((s.first + s.count) * kTile > s.q.P) cluster_fence();
             // the row's sum: both halves'
             ctl.sum[half][m] = l;
             if (!named_all(1, 128, ok)) break;
             l = ctl.sum[0][m] + ctl.sum[1][m];
             const bool whole = s.count == s.q.tiles;
             const unsigned extra = *(volatile unsigned *)&ctl.nonfinite[seg & 3] & bits;
-            const int slot = 2 * cta + (s.k > 0);
+            const int slot = 2 * cta + (seg > 0);
             const float shift = mx == -INFINITY ? 0.0f : mx, inv = l == 0.0f ? 0.0f : 1.0f / l;
             __nv_bfloat16 *out =
                 static_cast<__nv_bfloat16 *>(a.out) + packed * a.ld_out + (long long)head * kLatent;
 #pragma unroll 1
             for (int d = 0; d < 256; d += 32) {
-                // columns 0..127 are elements 0..255, a lane half 128 of them; the others
-                // 256..511
-                const int e = (d & 128) * 2 + 128 * half + (d & 127);
+                const int e = 256 * half + d;  // the upper lanes hold the second CTA's elements
                 uint32_t o[32];
                 tmem_load32(lanes + kOutCol + d, o);
                 tmem_wait_load(o);
@@ -745,10 +692,11 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                 }
                 if (!whole) {
                     float4 *part = reinterpret_cast<float4 *>(t.part_o) + ((long long)slot * 128 + e / 4) * kRows + m;
+                    if (valid)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        part[j * kRows] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                                      __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                        for (int j = 0; j < 8; ++j)
+                            part[j * kRows] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                                          __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
                 } else if (valid) {
                     uint32_t w[16];
 #pragma unroll
@@ -766,39 +714,39 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             }
             tmem_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&ctl.o_free));
-            if (half == 0) {
+            if (lane == 0) cluster_arrive(first_cta(&ctl.o_free));
+            if (half == 0 && valid) {
                 if (!whole) {
                     t.part_ml[(long long)slot * 2 * kRows + m] = mx;
                     t.part_ml[((long long)slot * 2 + 1) * kRows + m] = l;
-                } else if (valid && a.lse) {
+                } else if (a.lse) {
                     a.lse[(long long)packed * hq + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
                 }
             }
-            ++seg;
             if (tid == 0 && !whole) {
-                // what the join is told: of a job that begins here and ends in a later CTA, or
-                // of the one that the whole of this CTA lies in
-                const int at = cta / team;
+                // what the join is told: of a job that begins here and ends in a later pair, or
+                // of the one that the whole of this pair's share lies in
+                const int at = cta / 2;
                 int *d = t.desc + cta * kLatentDesc;
                 if (s.first == 0) {
                     const long long hi = deal.first(at + 1);
-                    d[1] = deal.cta_of(hi - 1 + s.q.tiles - s.count, at) * team + cta % team;
+                    d[1] = deal.cta_of(hi - 1 + s.q.tiles - s.count, at) * 2 + rank;
                     d[2] = slot;
                     d[3] = s.q.row0;
-                    d[4] = s.row_tile;
-                    d[5] = rows;
-                    d[6] = team;
+                    d[4] = s.row_tile * kPairRows + rank * kRows;
+                    d[5] = min(all - d[4], kRows);
                     d[0] = 1;
-                } else if (s.k == 0 && s.first + s.count < s.q.tiles) {
+                } else if (seg == 0 && s.first + s.count < s.q.tiles) {
                     // (where its first tile is)
-                    d[7] = deal.cta_of(deal.first(at) - s.first, 0) * team + cta % team;
+                    d[7] = deal.cta_of(deal.first(at) - s.first, 0) * 2 + rank;
                 }
             }
+            ++seg;
         }
     }
     __syncthreads();
-    if (warp == kMatrixWarp) tmem_free(tmem, 512);
+    cluster_sync();  // the other CTA may arrive on, or multiply from, what is here
+    if (warp == kMatrixWarp) tmem_free_pair(tmem, 512);
 }
 
 // Joins the parts of the jobs that several CTAs share, in the CTAs' order: a block for
@@ -820,13 +768,14 @@ __global__ void __launch_bounds__(kLatentJoinThreads) latent_join_kernel(const L
         d0 = job(0);
         d1 = job(1);
     }
-    const int team = d1.z, rows = d1.y, n = (d0.y - c0) / team + 1;  // parts
-    const int share = (blockIdx.x - c0) / team, shares = max(n - 1, 1);
+    const int rows = d1.y, n = (d0.y - c0) / 2 + 1;  // parts, of every other CTA
+    if (rows <= 0) return;
+    const int share = (blockIdx.x - c0) / 2, shares = max(n - 1, 1);
     const long long fours = 128ll * rows, pieces = (long long)shares * gridDim.y;
     const long long piece = (long long)share * gridDim.y + blockIdx.y;
     const int begin = (int)(piece * fours / pieces), end = (int)((piece + 1) * fours / pieces);
     const int tid = threadIdx.x, hq = t.a.n_q_heads;
-    auto slot = [&](int i) { return (long long)(i == 0 ? d0.z : 2 * (c0 + i * team)); };
+    auto slot = [&](int i) { return (long long)(i == 0 ? d0.z : 2 * (c0 + 2 * i)); };
     for (int base = begin; base < end; base += kLatentJoinThreads) {
         const int items = min(end - base, kLatentJoinThreads), deals = kLatentJoinThreads / items;
         const int deal = tid / items, item = base + tid % items, four = item / rows, m = item % rows;
@@ -863,7 +812,7 @@ __global__ void __launch_bounds__(kLatentJoinThreads) latent_join_kernel(const L
             const float inv = 1.0f / l;
             if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-            const int row = d1.x * kRows + m, head = row % hq;
+            const int row = d1.x + m, head = row % hq;
             const long long packed = d0.w + row / hq;
             const __nv_bfloat162 u = __floats2bfloat162_rn(x.x, x.y), v = __floats2bfloat162_rn(x.z, x.w);
             *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
@@ -896,11 +845,33 @@ bool latent_tensor_fits(const AttendArgs &a, int dtype, const dspark_latent_cach
            a.n_q_heads <= (1 << 20);
 }
 
+// How many pairs of CTAs run at a time on the current device (they sit in one cluster of
+// SMs each, so an odd SM of those is left), looked up once.
+int pair_count() {
+    static std::atomic<int> kept[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    if ((n = kept[dev].load(std::memory_order_relaxed)) > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kLatentCtas);
+    cfg.blockDim = dim3(kLatentThreads);
+    cfg.dynamicSmemBytes = kLatentSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, latent_tensor_kernel, &cfg) != cudaSuccess || n < 1) return 1;
+    n = min(n, kLatentCtas / 2);
+    kept[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 cudaError_t launch_latent_tensor(const AttendArgs &a, const dspark_latent_cache &c, void *workspace,
                                  cudaStream_t stream) {
     LatentTensorArgs t;
     t.a = a;
-    t.box = gcd(c.page_size, kTile);
+    t.box = gcd(c.page_size, kTile / 2);
     // A split job's parts are joined by a second launch.  Where no request can have more
     // than kWholeTiles tiles, a job stays whole and that launch is not made.
     t.whole = (long long)c.table_width * c.page_size <= kWholeTiles * kTile;
@@ -914,7 +885,7 @@ cudaError_t launch_latent_tensor(const AttendArgs &a, const dspark_latent_cache 
     if (!encode(&map, c.data, 2, 64, true, dims, strides, t.box, 1)) return cudaErrorUnknown;
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(latent_tensor_kernel), kLatentSmem, 26);
     if (e != cudaSuccess) return e;
-    const int grid = min(sm_count(), kLatentCtas);
+    const int grid = 2 * pair_count();
     e = launch_pdl(latent_tensor_kernel, dim3(grid), dim3(kLatentThreads), kLatentSmem, stream, map, t);
     if (e != cudaSuccess || t.whole) return e;
     return launch_pdl(latent_join_kernel, dim3(grid, kLatentJoinPieces), dim3(kLatentJoinThreads), 0, stream, t);
