@@ -13,7 +13,7 @@
 //
 // latent_tensor_kernel   bfloat16 over a bfloat16 cache with 512 + 64 elements a token, on
 //   the tensor cores of two CTAs at a time.  A job is a request and 128 of its (token,
-//   head) rows, taken as they come, so that a tile may end inside a token; a step is 64
+//   head) rows, taken as they come, so that a tile may end inside a token; a step is 128
 //   positions:  S = Q [C | R]^T into tensor memory, then
 //     y = S c   m' = max(m, max y)   w = 2^(y - m')   l = l 2^(m - m') + sum w
 //     O = O 2^(m - m') + W C
@@ -22,10 +22,11 @@
 //   A CTA has 64 of the rows: O alone is 512 columns of 32 bits a row, and for 128 rows
 //   that is all of an SM's tensor memory.  With products over a pair of CTAs 64 rows run at
 //   the full rate (alone they take half of it, or with .ws 0.6 to 0.8), and each CTA
-//   holds half of either product's right operand: the keys of 32 of the positions, and 256
-//   of the elements of all 64 as values.  An entry comes once for each product, but the
-//   keys' buffer is free again as soon as the scores are there.
-//   One warp copies (TMA), having asked L2 for the entries four tiles ahead, one of the
+//   holds half of either product's right operand: the keys of 64 of the positions, and 256
+//   of the elements of all 128 as values.  (With 64 positions a step the scores take as long
+//   as with 128.)  An entry comes once for each product, a third of the keys, or half of the
+//   values, at a time, into buffers that the products of the tile before are just done with.
+//   One warp copies (TMA), having asked L2 for the entries two tiles ahead, one of the
 //   first CTA issues both products, four do the softmax, a thread half a row's positions,
 //   and four bring the next job's queries.  The tiles of all jobs are dealt evenly to the
 //   pairs, so jobs are split along the positions where there are few, and
@@ -137,18 +138,18 @@ constexpr int kChunks = kEntry / 64;         // parts of 64 elements
 constexpr int kRows = 64;                    // (token, head) rows of a CTA
 constexpr int kPairRows = 2 * kRows;         // of a job
 constexpr int kLatentCtas = 160;             // at most
+constexpr int kStep = 128;                   // positions a tile
 constexpr int kChunkBytes = kRows * 128;     // 64 elements of 64 rows, or of 64 tokens
-constexpr int kKeyChunk = kTile / 2 * 128;   // of 32 tokens
-constexpr int kKeyBytes = kChunks * kKeyChunk, kValueBytes = 4 * kChunkBytes;
-constexpr int kStages = 2;                   // of keys, of values, of scores, of weights
+constexpr int kKeyParts = 3, kKeyBytes = 3 * kChunkBytes;      // a third of a CTA's keys of a tile
+constexpr int kValueParts = 2, kValueBytes = 4 * kChunkBytes;  // half of its values: 128 elements
 constexpr int kKeyAt = kChunks * kChunkBytes;  // behind the queries
-constexpr int kValueAt = kKeyAt + kStages * kKeyBytes;
-constexpr int kWeightsAt = kValueAt + kStages * kValueBytes;
-constexpr int kControlAt = kWeightsAt + kStages * kChunkBytes;
+constexpr int kValueAt = kKeyAt + kKeyParts * kKeyBytes;
+constexpr int kWeightsAt = kValueAt + kValueParts * kValueBytes;
+constexpr int kControlAt = kWeightsAt + 2 * kChunkBytes;
 constexpr int kLatentSmem = kControlAt + 3072;
 constexpr int kOutCol = 0, kScoreCol = 256;  // columns of tensor memory
 constexpr int kLatentThreads = 320, kCopyWarp = 8, kMatrixWarp = 9;
-constexpr int kLookAhead = 4;  // tiles whose pages are known, and asked for, ahead of their copy
+constexpr int kFetchAhead = 2;  // tiles asked of L2 ahead of their copy
 constexpr int kLatentJobCost = 2;  // of a job's begin and end, in tiles
 constexpr int kLatentDesc = 8;     // words about a split job, for the join
 
@@ -170,7 +171,7 @@ __device__ __forceinline__ bool to_latent(const LatentTensorArgs &t, const Windo
     q->row0 = w.lo;
     q->len = w.hi - w.lo;
     q->P = w.P;
-    q->tiles = (q->P + q->len + kTile - 1) / kTile;
+    q->tiles = (q->P + q->len + kStep - 1) / kStep;
     q->row_tiles = (q->len * t.a.n_q_heads + kPairRows - 1) / kPairRows;
     return true;
 }
@@ -275,8 +276,8 @@ __device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBe
 // Barriers that the issuing warp waits on are the first CTA's (the same place in the other
 // is not used); those that it commits to are each CTA's own.
 struct alignas(16) LatentControl {
-    unsigned long long key_full[kStages], value_full[kStages], p_ready[2], q_full, o_free;  // the first's
-    unsigned long long key_empty[kStages], value_empty[kStages], s_full[2], o_done[2], value_seen[2], q_empty,
+    unsigned long long key_full[kKeyParts], value_full[kValueParts], p_ready[2], q_full, o_free;  // the first's
+    unsigned long long key_empty[kKeyParts], value_empty[kValueParts], s_full[2], o_done[2], value_seen[2], q_empty,
         drain;
     unsigned tmem;
     unsigned nonfinite[4];  // window tokens whose values were zeroed in either CTA, by segment
@@ -300,12 +301,14 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
     const int rank = (int)cluster_rank();
     const uint32_t base = smem_addr(smem);
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kKeyParts; ++i) {
             mbar_init(smem_addr(&ctl.key_full[i]), 1);
-            mbar_init(smem_addr(&ctl.value_full[i]), 1);
-            mbar_init(smem_addr(&ctl.p_ready[i]), 8);
             mbar_init(smem_addr(&ctl.key_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&ctl.value_full[i]), 1);
             mbar_init(smem_addr(&ctl.value_empty[i]), 1);
+            mbar_init(smem_addr(&ctl.p_ready[i]), 8);
             mbar_init(smem_addr(&ctl.s_full[i]), 1);
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
             mbar_init(smem_addr(&ctl.value_seen[i]), 1);
@@ -350,79 +353,94 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
 
     if (warp == kCopyWarp) {
         // ------------------------------------------------ copy warp
-        // Boxes of a tile: lane b < boxes looks up box b.  Keys: nine parts of each of this
-        // CTA's half of the boxes.  Values: four of each box.
-        const int boxes = kTile / t.box, key_boxes = boxes / 2;
-        const int key_box = rank * key_boxes + lane / kChunks, key_chunk = lane % kChunks;
-        const bool key_lane = lane < kChunks * key_boxes;
-        const int value_box = lane >> 2, value_chunk = 4 * rank + (lane & 3);
-        const bool value_lane = value_box < boxes;
-        const uint32_t key_dst = base + kKeyAt + key_chunk * kKeyChunk + lane / kChunks * t.box * 128;
-        const uint32_t value_dst = base + kValueAt + (lane & 3) * kChunkBytes + value_box * t.box * 128;
+        // Of a tile's boxes a CTA copies half as keys and all, of its elements, as values.  The
+        // table's entries of `per` tiles are looked up at a time, a box a lane, one such
+        // batch ahead.
+        const int boxes = kStep / t.box, key_boxes = boxes / 2, per = 32 / boxes;
+        const int key_box = rank * key_boxes + lane / 3, value_box = lane >> 1;
+        const bool key_lane = lane < 3 * key_boxes, value_lane = value_box < boxes;
+        const uint32_t key_dst = base + kKeyAt + lane % 3 * kChunkBytes + lane / 3 * t.box * 128;
+        const uint32_t value_dst = base + kValueAt + (lane & 1) * 2 * kChunkBytes + value_box * t.box * 128;
         while (ok && walk.next(t, &s)) {
-            const int n = s.q.P + s.q.len, from = s.first * kTile + lane * t.box;
-            Place at;
-            at.begin(a.cache, lane < boxes ? from : 0);
-            // tile i's page and token of this lane's box, kLookAhead tiles ahead
-            int pages[kLookAhead + 1], tokens[kLookAhead + 1];
-            auto look_up = [&](int i) {
-                tokens[kLookAhead] = at.token;
-                pages[kLookAhead] = at.entry(a.cache, s.r, lane < boxes && i < s.count && from + i * kTile < n);
-                at.step(a.cache);
+            const int n = s.q.P + s.q.len, from = s.first * kStep;
+            struct Batch {
+                int page, token;
+            } now, next;
+            auto look_up = [&](int tile) -> Batch {
+                const int pos = from + tile * kStep + lane * t.box;
+                const unsigned col = (unsigned)pos / (unsigned)a.cache.page_size;
+                return {tile + lane / boxes < s.count && pos < n
+                            ? __ldg(a.cache.table + (long long)s.r * a.cache.table_width + col)
+                            : a.cache.n_pages,
+                        (int)(pos - col * a.cache.page_size)};
             };
-            auto shift = [&]() {
+            now = look_up(0);
+            next = look_up(per);
+            Batch value = {};
+            // in the order of use: K0, K1, V0, K2, V1, ..., V(n-1)
+            for (int i = 0; i <= s.count; ++i) {
+                if (i < s.count) {
+                    const int j = i % per;
+                    if (j == 0 && i > 0) {
+                        now = next;
+                        next = look_up(i + per);
+                    }
+                    int page = __shfl_sync(kFullMask, now.page, (j * boxes + key_box) % 32);
+                    const int token = __shfl_sync(kFullMask, now.token, (j * boxes + key_box) % 32);
+                    // a page outside the pool, as past the request's end, arrives as zeros
+                    if ((unsigned)page >= (unsigned)a.cache.n_pages) {
+                        if (key_lane && from + i * kStep + key_box * t.box < n)
+                            flag(a.status, DSPARK_STATUS_BAD_INDEX);
+                        page = a.cache.n_pages;
+                    }
+#pragma unroll 1
+                    for (int part = 0; part < kKeyParts; ++part) {
+                        if (!wait(&ctl.key_empty[part], done + i + 1)) break;
+                        if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.key_full[part]), 2 * kKeyBytes);
+                        __syncwarp();
+                        if (key_lane)
+                            tma_load_4d_pair(key_dst + part * kKeyBytes, &map, (3 * part + lane % 3) * 64, token, 0,
+                                             page, first_cta(&ctl.key_full[part]));
+                    }
+                    if (!ok) break;
+                    // to L2, this CTA's half of a later tile
+                    const int f = j + kFetchAhead, at = (f % per * boxes + key_box) % 32;
+                    const int fetch_now = __shfl_sync(kFullMask, now.page, at);
+                    const int fetch_next = __shfl_sync(kFullMask, next.page, at);
+                    const int token_now = __shfl_sync(kFullMask, now.token, at);
+                    const int token_next = __shfl_sync(kFullMask, next.token, at);
+                    const int fetch = f < per ? fetch_now : fetch_next, token_at = f < per ? token_now : token_next;
+                    if (key_lane && (unsigned)fetch < (unsigned)a.cache.n_pages)
 #pragma unroll
-                for (int j = 0; j < kLookAhead; ++j) pages[j] = pages[j + 1], tokens[j] = tokens[j + 1];
-            };
-#pragma unroll
-            for (int j = 0; j < kLookAhead; ++j) {
-                look_up(j);
-                shift();
-            }
-            for (int i = 0; i < s.count; ++i) {
-                const unsigned stage = (done + i) & 1, parity = (done + i) >> 1;
-                look_up(i + kLookAhead);
-                {  // to L2, the tile that was looked up before
-                    const int page = __shfl_sync(kFullMask, pages[kLookAhead - 1], key_box % boxes);
-                    const int token = __shfl_sync(kFullMask, tokens[kLookAhead - 1], key_box % boxes);
-                    if (key_lane && (unsigned)page < (unsigned)a.cache.n_pages)
-                        tma_prefetch_4d(&map, key_chunk * 64, token, 0, page);
+                        for (int part = 0; part < kKeyParts; ++part)
+                            tma_prefetch_4d(&map, (3 * part + lane % 3) * 64, token_at, 0, fetch);
                 }
-                int page = pages[0];
-                const int token = tokens[0];
-                shift();
-                // a page outside the pool, as past the request's end, arrives as zeros
-                if (lane < boxes && from + i * kTile < n && (unsigned)page >= (unsigned)a.cache.n_pages) {
-                    flag(a.status, DSPARK_STATUS_BAD_INDEX);
-                    page = a.cache.n_pages;
+                if (i > 0) {
+#pragma unroll 1
+                    for (int part = 0; part < kValueParts; ++part) {
+                        if (!wait(&ctl.value_empty[part], done + i)) break;
+                        if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.value_full[part]), 2 * kValueBytes);
+                        __syncwarp();
+                        if (value_lane)
+                            tma_load_4d_pair(value_dst + part * kValueBytes, &map,
+                                             (4 * rank + 2 * part + (lane & 1)) * 64, value.token, 0, value.page,
+                                             first_cta(&ctl.value_full[part]));
+                    }
+                    if (!ok) break;
                 }
-                const int key_page = __shfl_sync(kFullMask, page, key_box % boxes);
-                const int key_token = __shfl_sync(kFullMask, token, key_box % boxes);
-                const int value_page = __shfl_sync(kFullMask, page, value_box % boxes);
-                const int value_token = __shfl_sync(kFullMask, token, value_box % boxes);
-                if (!wait(&ctl.key_empty[stage], parity ^ 1)) break;
-                if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.key_full[stage]), 2 * kKeyBytes);
-                __syncwarp();
-                if (key_lane)
-                    tma_load_4d_pair(key_dst + stage * kKeyBytes, &map, key_chunk * 64, key_token, 0, key_page,
-                                     first_cta(&ctl.key_full[stage]));
-                if (!wait(&ctl.value_empty[stage], parity ^ 1)) break;
-                if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.value_full[stage]), 2 * kValueBytes);
-                __syncwarp();
-                if (value_lane)
-                    tma_load_4d_pair(value_dst + stage * kValueBytes, &map, value_chunk * 64, value_token, 0,
-                                     value_page, first_cta(&ctl.value_full[stage]));
+                const int at = (i % per * boxes + value_box) % 32;
+                value = {__shfl_sync(kFullMask, now.page, at), __shfl_sync(kFullMask, now.token, at)};
+                if ((unsigned)value.page >= (unsigned)a.cache.n_pages) value.page = a.cache.n_pages;
             }
             done += s.count;
         }
         if (!ok && rank == 0 && lane == 0) {
             // copies still under way write the pair's buffers (each wait ends by itself; the
             // CTAs leave together)
-            for (int i = 0; i < kStages; ++i)
-                for (int p = 0; p < 2; ++p) {
-                    mbar_wait(smem_addr(&ctl.key_full[i]), p, kWaitLimitNs / 4);
-                    mbar_wait(smem_addr(&ctl.value_full[i]), p, kWaitLimitNs / 4);
-                }
+            for (int p = 0; p < 2; ++p) {
+                for (int i = 0; i < kKeyParts; ++i) mbar_wait(smem_addr(&ctl.key_full[i]), p, kWaitLimitNs / 4);
+                for (int i = 0; i < kValueParts; ++i) mbar_wait(smem_addr(&ctl.value_full[i]), p, kWaitLimitNs / 4);
+            }
         }
     } else if (warp == kMatrixWarp) {
         // ---------------------------------------------- matrix warp
@@ -430,30 +448,30 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
         // issues.  Scores of tile i, then the output of tile i - 1, whose weights are
         // computed meanwhile.
         if (rank == 0) {
-            constexpr uint32_t score_word = mma_word(true, kTile, false), value_word = mma_word(true, 256, true);
+            constexpr uint32_t score_word = mma_word(true, kStep, false), value_word = mma_word(true, 256, true);
             const uint32_t ubase = __shfl_sync(kFullMask, base, 0), utmem = __shfl_sync(kFullMask, tmem, 0);
             const bool leader = elect_one();
             const uint64_t desc_q = smem_operand(ubase, 16, 128);
             const uint64_t desc_key = smem_operand(ubase + kKeyAt, 16, 128);
-            const uint64_t desc_value = smem_operand(ubase + kValueAt, kChunkBytes, 128);
+            const uint64_t desc_value = smem_operand(ubase + kValueAt, 2 * kChunkBytes, 128);
             const uint64_t desc_w = smem_operand(ubase + kWeightsAt, 16, 128);
             // O += W C of the segment's tile i
             auto values = [&](int i, unsigned tile) {
                 const unsigned b = tile & 1;
                 if (i == 0 && seg > 0 && !wait(&ctl.o_free, seg - 1)) return;
-                if (!wait(&ctl.value_full[b], tile >> 1)) return;
+                if (!wait(&ctl.value_full[0], tile) || !wait(&ctl.value_full[1], tile)) return;
                 if (lane < 2) cluster_arrive(cluster_addr(smem_addr(&ctl.value_seen[b]), lane));
                 if (!wait(&ctl.p_ready[b], tile >> 1)) return;
                 tmem_fence_after();
-                const uint64_t w = desc_w + b * (kChunkBytes >> 4), v = desc_value + b * (kValueBytes >> 4);
                 if (leader) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < kValueParts; ++h) {
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_pair_ss(utmem + kOutCol + 128 * h, w + (k * 32 >> 4),
-                                        v + (2 * h * kChunkBytes + k * 16 * 128 >> 4), value_word, i > 0 || k > 0);
-                    mma_pair_commit(smem_addr(&ctl.value_empty[b]));
+                        for (int k = 0; k < kStep / 16; ++k)
+                            mma_pair_ss(utmem + kOutCol + 128 * h, desc_w + (k / 4 * kChunkBytes + k % 4 * 32 >> 4),
+                                        desc_value + (h * kValueBytes + k * 16 * 128 >> 4), value_word, i > 0 || k > 0);
+                        mma_pair_commit(smem_addr(&ctl.value_empty[h]));
+                    }
                     mma_pair_commit(smem_addr(&ctl.o_done[b]));
                 }
                 __syncwarp();
@@ -462,21 +480,28 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                 if (!wait(&ctl.q_full, seg)) break;
                 const int count = __shfl_sync(kFullMask, s.count, 0);
                 for (int i = 0; i < count; ++i) {
-                    // (the scores of tile - 2 have been read, and its weights multiplied)
+                    // (the scores of tile - 2 have been read)
                     const unsigned tile = done + i, b = tile & 1;
-                    if (!wait(&ctl.key_full[b], tile >> 1)) break;
-                    tmem_fence_after();
-                    const uint64_t k_at = desc_key + b * (kKeyBytes >> 4);
-                    if (leader) {
 #pragma unroll
-                        for (int k = 0; k < 4 * kChunks; ++k)
-                            mma_pair_ss(utmem + kScoreCol + b * 32, desc_q + (k / 4 * kChunkBytes + k % 4 * 32 >> 4),
-                                        k_at + (k / 4 * kKeyChunk + k % 4 * 32 >> 4), score_word, k > 0);
-                        mma_pair_commit(smem_addr(&ctl.s_full[b]));
-                        mma_pair_commit(smem_addr(&ctl.key_empty[b]));
-                        if (i + 1 == count) mma_pair_commit(smem_addr(&ctl.q_empty));
+                    for (int part = 0; part < kKeyParts; ++part) {
+                        if (!wait(&ctl.key_full[part], tile)) break;
+                        tmem_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < 12; ++k) {
+                                const int at = (3 * part + k / 4) * kChunkBytes + k % 4 * 32;
+                                mma_pair_ss(utmem + kScoreCol + b * 64, desc_q + (at >> 4), desc_key + (at >> 4),
+                                            score_word, part > 0 || k > 0);
+                            }
+                            mma_pair_commit(smem_addr(&ctl.key_empty[part]));
+                            if (part + 1 == kKeyParts) {
+                                mma_pair_commit(smem_addr(&ctl.s_full[b]));
+                                if (i + 1 == count) mma_pair_commit(smem_addr(&ctl.q_empty));
+                            }
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok) break;
                     if (i > 0) values(i - 1, tile - 1);
                     if (!ok) break;
                 }
@@ -529,7 +554,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
         const bool negative = a.scale < 0.0f;
-        const int m = tid & 63, half = tid >> 6;  // a row, and which 32 of a tile's positions
+        const int m = tid & 63, half = tid >> 6;  // a row, and which 64 of a tile's positions
         // The four warps meet once a tile and once behind the last: a warp that gave up comes
         // to the next such barrier, and all leave there.
         bool met = true;
@@ -543,23 +568,25 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             float mx = -INFINITY, l = 0.0f;  // running maximum (to base 2); this half's sum
             for (int i = 0; i < s.count; ++i) {
                 const unsigned tile = done + i, b = tile & 1;
-                const int p0 = (s.first + i) * kTile;
+                const int p0 = (s.first + i) * kStep;
                 wait(&ctl.s_full[b], tile >> 1);
                 tmem_fence_after();
-                uint32_t x[32];
-                tmem_load32(lanes + kScoreCol + 32 * b, x);
+                uint32_t x[64];
+                tmem_load32(lanes + kScoreCol + 64 * b, x);
+                tmem_load32(lanes + kScoreCol + 64 * b + 32, x + 32);
                 tmem_wait_load(x);
+                tmem_wait_load(x + 32);
                 if (negative) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] ^= 0x80000000u;
+                    for (int j = 0; j < 64; ++j) x[j] ^= 0x80000000u;
                 }
-                if (p0 + kTile > s.q.P) {
+                if (p0 + kStep > s.q.P) {
                     // prefix positions, then the row's ancestors in the window
-                    const int pre = max(s.q.P - p0, 0), skip = max(p0 - s.q.P, 0);
-                    const unsigned long long w = skip < 32 ? (unsigned long long)(bits >> skip) : 0;
-                    const unsigned sees = (unsigned)((w << pre | ((1ull << pre) - 1)) >> (32 * half));
+                    const int pre = s.q.P - (p0 + 64 * half);
+                    const unsigned long long w = pre >= 0 ? bits : pre > -32 ? bits >> -pre : 0;
+                    const unsigned long long sees = pre >= 64 ? ~0ull : pre > 0 ? w << pre | ((1ull << pre) - 1) : w;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 64; ++j)
                         if (!(sees >> j & 1)) x[j] = 0xFF800000u;
                 }
                 float part[4];
@@ -567,7 +594,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                 for (int j = 0; j < 4; ++j) {
                     part[j] = fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 4]));
 #pragma unroll
-                    for (int k = 8 + j; k < 32; k += 4) part[j] = fmaxf(part[j], __uint_as_float(x[k]));
+                    for (int k = 8 + j; k < 64; k += 4) part[j] = fmaxf(part[j], __uint_as_float(x[k]));
                 }
                 float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) * c;
                 ctl.top[b][half][m] = top;
@@ -597,37 +624,35 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                 }
                 const float shift = mx == -INFINITY ? 0.0f : mx;
                 float2 sum[2] = {};
-                unsigned char *weights = smem + kWeightsAt + b * kChunkBytes;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int e = 8 * j + 2 * k;
-                        const float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                                              make_float2(c, c), make_float2(-shift, -shift));
-                        const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                        sum[k & 1] = add2(sum[k & 1], u);
-                        // (bfloat16, 8 digits, as the latent vectors are: a product takes
-                        // operands of one type.  The sum keeps all digits, for lse)
-                        const __nv_bfloat162 two = __floats2bfloat162_rn(u.x, u.y);
-                        w[k] = *reinterpret_cast<const uint32_t *>(&two);
-                    }
-                    *reinterpret_cast<uint4 *>(weights + chunk_piece(m, 4 * half + j)) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
+                for (int j = 0; j < 32; ++j) {
+                    const float2 y = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])),
+                                          make_float2(c, c), make_float2(-shift, -shift));
+                    const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                    sum[j & 1] = add2(sum[j & 1], u);
+                    // (bfloat16, 8 digits, as the latent vectors are: a product takes operands
+                    // of one type.  The sum keeps all digits, for lse)
+                    const __nv_bfloat162 two = __floats2bfloat162_rn(u.x, u.y);
+                    x[j] = *reinterpret_cast<const uint32_t *>(&two);
                 }
+                // in the place of the last tile's, once they are multiplied
+                if (i > 0 && !wait(&ctl.o_done[(tile - 1) & 1], (tile - 1) >> 1)) continue;
+                unsigned char *weights = smem + kWeightsAt + half * kChunkBytes;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4 *>(weights + chunk_piece(m, j)) =
+                        make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                if (p0 + kTile > s.q.P) {
+                if (p0 + kStep > s.q.P) {
                     // Latent vectors past the request's end become zeros, and so do NaN and
                     // infinities of the window (0 x NaN would reach rows that do not see
                     // them); the rows that do get them at the end.  Each CTA does so for the
                     // elements that it holds as values.
                     if (!wait(&ctl.value_seen[b], tile >> 1)) continue;
                     const int from = max(s.q.P, p0);
-                    for (int j = tid; j < (p0 + kTile - from) * 32; j += 128) {
+                    for (int j = tid; j < (p0 + kStep - from) * 32; j += 128) {
                         const int pos = from + j / 32, piece = j % 32;
-                        uint4 *at = reinterpret_cast<uint4 *>(smem + kValueAt + b * kValueBytes +
-                                                              piece / 8 * kChunkBytes +
+                        uint4 *at = reinterpret_cast<uint4 *>(smem + kValueAt + piece / 8 * 2 * kChunkBytes +
                                                               chunk_piece(pos - p0, piece % 8));
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (pos < n) {
@@ -661,7 +686,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             wait(&ctl.o_done[last & 1], last >> 1);
             done += s.count;
             tmem_fence_after();
-            if ((s.first + s.count) * kTile > s.q.P) cluster_fence();
+            if ((s.first + s.count) * kStep > s.q.P) cluster_fence();
             // the row's sum: both halves'
             ctl.sum[half][m] = l;
             if (!named_all(1, 128, ok)) break;
@@ -871,7 +896,7 @@ cudaError_t launch_latent_tensor(const AttendArgs &a, const dspark_latent_cache 
                                  cudaStream_t stream) {
     LatentTensorArgs t;
     t.a = a;
-    t.box = gcd(c.page_size, kTile / 2);
+    t.box = gcd(c.page_size, kStep / 2);
     // A split job's parts are joined by a second launch.  Where no request can have more
     // than kWholeTiles tiles, a job stays whole and that launch is not made.
     t.whole = (long long)c.table_width * c.page_size <= kWholeTiles * kTile;
