@@ -26,7 +26,7 @@
 //   of the elements of all 128 as values.  (With 64 positions a step the scores take as long
 //   as with 128.)  An entry comes once for each product, a third of the keys, or half of the
 //   values, at a time, into buffers that the products of the tile before are just done with.
-//   One warp copies (TMA), having asked L2 for the entries two tiles ahead, one of the
+//   One warp copies (TMA; asking L2 for later tiles beside that takes longer), one of the
 //   first CTA issues both products, four do the softmax, a thread half a row's positions,
 //   and four bring the next job's queries.  The tiles of all jobs are dealt evenly to the
 //   pairs, so jobs are split along the positions where there are few, and
@@ -149,7 +149,6 @@ constexpr int kControlAt = kWeightsAt + 2 * kChunkBytes;
 constexpr int kLatentSmem = kControlAt + 3072;
 constexpr int kOutCol = 0, kScoreCol = 256;  // columns of tensor memory
 constexpr int kLatentThreads = 320, kCopyWarp = 8, kMatrixWarp = 9;
-constexpr int kFetchAhead = 2;  // tiles asked of L2 ahead of their copy
 constexpr int kLatentJobCost = 2;  // of a job's begin and end, in tiles
 constexpr int kLatentDesc = 8;     // words about a split job, for the join
 
@@ -180,27 +179,40 @@ __device__ __forceinline__ bool to_latent(const LatentTensorArgs &t, const Windo
 struct LatentSegment {
     LatentRequest q = {};
     int r, row_tile, first, count;
+    unsigned k;  // how many the team had before it
 };
 
-// Where a pair's share begins, and how many units it has.
+// Where a team's share begins, and how many units it has.
 struct LatentBegin {
-    int r, row_tile, unit, left;
+    int r, group, unit, left;
     LatentRequest q;
 };
 
-// Walks a pair's units: requests in order, in each the row tiles, in each the positions.
-// Every warp role of both CTAs walks on its own and sees the same.
+// Pairs of CTAs work in teams, whose members take neighbouring row tiles over the same
+// positions at the same time, so that the entries come from HBM once and from L2 to the
+// others.  `size` pairs a team; this pair is the `member`-th of team `at`.
+struct Team {
+    int size, member, at;
+};
+
+// Walks a team's units: requests in order, in each the row tiles, a team's worth at a
+// time, in each the positions.  Every warp role of both CTAs walks on its own and sees the
+// same.
 struct LatentWalk {
-    int left, r, row_tile, unit;
+    int left, r, group, unit;
+    Team team;
+    unsigned k;
     LatentRequest q = {};
     Window ahead;
 
-    __device__ __forceinline__ void begin(const LatentTensorArgs &t, const LatentBegin &b) {
+    __device__ __forceinline__ void begin(const LatentTensorArgs &t, const LatentBegin &b, const Team &of) {
         left = b.left;
         r = b.r;
-        row_tile = b.row_tile;
+        group = b.group;
         unit = b.unit;
         q = b.q;
+        team = of;
+        k = 0;
         ahead = load_window(t.a, min(r + 1, t.a.B - 1));
     }
     __device__ __forceinline__ bool next(const LatentTensorArgs &t, LatentSegment *s) {
@@ -208,13 +220,14 @@ struct LatentWalk {
             const int take = t.whole ? 1 : min(q.tiles + kLatentJobCost - unit, left);
             s->q = q;
             s->r = r;
-            s->row_tile = row_tile;
+            s->row_tile = group * team.size + team.member;
+            s->k = k;
             s->first = max(unit - kLatentJobCost, 0);
             s->count = t.whole ? q.tiles : max(unit + take - kLatentJobCost, 0) - s->first;
             left -= take;
             unit = 0;
-            if (++row_tile == q.row_tiles) {
-                row_tile = 0;
+            if (++group * team.size >= q.row_tiles) {
+                group = 0;
                 while (left > 0) {
                     const bool has = to_latent(t, ahead, &q, false);
                     ++r;
@@ -222,49 +235,66 @@ struct LatentWalk {
                     if (has) break;
                 }
             }
-            if (s->count > 0) return true;
+            if (s->count > 0) {
+                ++k;
+                if (s->row_tile < s->q.row_tiles) return true;  // (else other members' alone)
+            }
         }
         return false;
     }
 };
 
-// This CTA's pair's share and where it begins (for all after the next barrier); false
+// The size of teams, and this CTA's team's share and where it begins (for all after the next barrier); false
 // where none are left for it.
+//   Larger teams read less from HBM and leave members idle where the row tiles are no
+// multiple of them: the largest is taken whose members' steps are at most an eighth more
+// than those of pairs alone.
 __device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBegin *begin, long long *scan,
-                                             Deal *deal) {
+                                             Deal *deal, Team *team) {
     const AttendArgs &a = t.a;
-    const int tid = threadIdx.x, cta = blockIdx.x, at = cta / 2;
+    const int tid = threadIdx.x, cta = blockIdx.x, pairs = gridDim.x / 2;
     const int per = (a.B + kLatentThreads - 1) / kLatentThreads;
-    long long mine = 0;
+    long long mine[3] = {}, sum[3];  // teams of 1, 2 and 4
     LatentRequest q = {};
     auto job = [&]() { return t.whole ? 1 : q.tiles + kLatentJobCost; };
     for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
-        if (to_latent(t, load_window(a, r), &q, cta == 0)) mine += (long long)job() * q.row_tiles;
-    long long T;
-    const long long before = block_exclusive_scan<long long>(mine, scan, &T);
-    const int n = (int)min((long long)(gridDim.x / 2),
-                           t.whole ? T : (T + kLatentJobCost + 1) / (kLatentJobCost + 2));
+        if (to_latent(t, load_window(a, r), &q, cta == 0))
+#pragma unroll
+            for (int g = 0; g < 3; ++g) mine[g] += (long long)job() * ((q.row_tiles + (1 << g) - 1) >> g);
+    int best = 0;
+    long long before = block_exclusive_scan<long long>(mine[0], scan, &sum[0]);
+    if (!t.whole)
+#pragma unroll
+        for (int g = 1; g < 3; ++g) {
+            const long long at = block_exclusive_scan<long long>(mine[g], scan, &sum[g]);
+            if (sum[g] / (pairs >> g) * 8 <= sum[0] / pairs * 9) best = g, before = at;
+        }
+    const int size = 1 << best;
+    const long long own = best == 0 ? mine[0] : best == 1 ? mine[1] : mine[2];
+    const long long T = best == 0 ? sum[0] : best == 1 ? sum[1] : sum[2];
+    const int n = (int)min((long long)(pairs / size), t.whole ? T : (T + kLatentJobCost + 1) / (kLatentJobCost + 2));
     if (tid == 0 && !t.whole) {
         t.desc[cta * kLatentDesc] = 0;
         t.desc[cta * kLatentDesc + 7] = -1;
     }
-    if (at >= n) return false;
+    *team = {size, cta / 2 % size, cta / 2 / size};
+    if (team->at >= n) return false;
     deal->n = n;
     deal->each = div_nonneg(T, n);
     deal->rest = (int)(T - deal->each * n);
-    const long long lo = deal->first(at), hi = deal->first(at + 1);
-    if (lo >= before && lo < before + mine) {
+    const long long lo = deal->first(team->at), hi = deal->first(team->at + 1);
+    if (lo >= before && lo < before + own) {
         long long from = before;
         for (int r = tid * per;; ++r) {
             if (per > 1 && !to_latent(t, load_window(a, r), &q, false)) continue;
-            const long long units = (long long)job() * q.row_tiles;
+            const long long units = (long long)job() * ((q.row_tiles + size - 1) / size);
             if (lo >= from + units) {
                 from += units;
                 continue;
             }
             begin->r = r;
-            begin->row_tile = (int)div_nonneg(lo - from, job());
-            begin->unit = (int)(lo - from - (long long)begin->row_tile * job());
+            begin->group = (int)div_nonneg(lo - from, job());
+            begin->unit = (int)(lo - from - (long long)begin->group * job());
             begin->left = (int)(hi - lo);
             begin->q = q;
             break;
@@ -327,7 +357,8 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
     pdl_trigger();
 
     Deal deal;
-    if (!latent_share(t, &ctl.begin, ctl.scan, &deal)) {  // (neither CTA of the pair)
+    Team team;
+    if (!latent_share(t, &ctl.begin, ctl.scan, &deal, &team)) {  // (neither CTA of the pair)
         if (warp == kMatrixWarp) {
             __syncwarp();
             tmem_free_pair(*(volatile unsigned *)&ctl.tmem, 512);
@@ -341,7 +372,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
     const uint32_t tmem = ctl.tmem;
     volatile int *abort = &ctl.abort;
     LatentWalk walk;
-    walk.begin(t, ctl.begin);
+    walk.begin(t, ctl.begin, team);
     LatentSegment s = {};
     bool ok = true;
     auto wait = [&](unsigned long long *bar, unsigned parity) {
@@ -403,17 +434,6 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                                              page, first_cta(&ctl.key_full[part]));
                     }
                     if (!ok) break;
-                    // to L2, this CTA's half of a later tile
-                    const int f = j + kFetchAhead, at = (f % per * boxes + key_box) % 32;
-                    const int fetch_now = __shfl_sync(kFullMask, now.page, at);
-                    const int fetch_next = __shfl_sync(kFullMask, next.page, at);
-                    const int token_now = __shfl_sync(kFullMask, now.token, at);
-                    const int token_next = __shfl_sync(kFullMask, next.token, at);
-                    const int fetch = f < per ? fetch_now : fetch_next, token_at = f < per ? token_now : token_next;
-                    if (key_lane && (unsigned)fetch < (unsigned)a.cache.n_pages)
-#pragma unroll
-                        for (int part = 0; part < kKeyParts; ++part)
-                            tma_prefetch_4d(&map, (3 * part + lane % 3) * 64, token_at, 0, fetch);
                 }
                 if (i > 0) {
 #pragma unroll 1
@@ -528,22 +548,11 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             const int token = there ? row / hq : 0, head = there ? row % hq : 0;
             const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
                                                              (s.q.row0 + token) * a.ld_q + (long long)head * kEntry);
-            constexpr int kBatch = 12, kPieces = 8 * kChunks / 2;
-#pragma unroll 1
-            for (int p = 0; p < kPieces; p += kBatch) {
-                uint4 v[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    v[i] = there ? __ldg(q + 2 * (p + i) + half) : make_uint4(0, 0, 0, 0);
-                if (p == 0 && seg > 0) wait(&ctl.q_empty, seg - 1);
-                if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int at = 2 * (p + i) + half;
-                    *reinterpret_cast<uint4 *>(smem + at / 8 * kChunkBytes + chunk_piece(m, at % 8)) = v[i];
-                }
-            }
-            if (!ok) break;
+            if (seg > 0 && !wait(&ctl.q_empty, seg - 1)) break;
+#pragma unroll 4
+            for (int p = half; p < 8 * kChunks; p += 2)
+                copy16(base + p / 8 * kChunkBytes + chunk_piece(m, p % 8), q + p, there);
+            copy16_wait();
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) cluster_arrive(first_cta(&ctl.q_full));
@@ -693,7 +702,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             l = ctl.sum[0][m] + ctl.sum[1][m];
             const bool whole = s.count == s.q.tiles;
             const unsigned extra = *(volatile unsigned *)&ctl.nonfinite[seg & 3] & bits;
-            const int slot = 2 * cta + (seg > 0);
+            const int slot = 2 * cta + (s.k > 0);
             const float shift = mx == -INFINITY ? 0.0f : mx, inv = l == 0.0f ? 0.0f : 1.0f / l;
             __nv_bfloat16 *out =
                 static_cast<__nv_bfloat16 *>(a.out) + packed * a.ld_out + (long long)head * kLatent;
@@ -749,21 +758,22 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                 }
             }
             if (tid == 0 && !whole) {
-                // what the join is told: of a job that begins here and ends in a later pair, or
-                // of the one that the whole of this pair's share lies in
-                const int at = cta / 2;
+                // what the join is told: of a job that begins here and ends in a later team, or
+                // of the one that the whole of this team's share lies in
+                auto same = [&](int at) { return (at * team.size + team.member) * 2 + rank; };  // in a team
                 int *d = t.desc + cta * kLatentDesc;
                 if (s.first == 0) {
-                    const long long hi = deal.first(at + 1);
-                    d[1] = deal.cta_of(hi - 1 + s.q.tiles - s.count, at) * 2 + rank;
+                    const long long hi = deal.first(team.at + 1);
+                    d[1] = same(deal.cta_of(hi - 1 + s.q.tiles - s.count, team.at));
                     d[2] = slot;
                     d[3] = s.q.row0;
                     d[4] = s.row_tile * kPairRows + rank * kRows;
                     d[5] = min(all - d[4], kRows);
+                    d[6] = 2 * team.size;
                     d[0] = 1;
-                } else if (seg == 0 && s.first + s.count < s.q.tiles) {
+                } else if (s.k == 0 && s.first + s.count < s.q.tiles) {
                     // (where its first tile is)
-                    d[7] = deal.cta_of(deal.first(at) - s.first, 0) * 2 + rank;
+                    d[7] = same(deal.cta_of(deal.first(team.at) - s.first, 0));
                 }
             }
             ++seg;
@@ -793,22 +803,68 @@ __global__ void __launch_bounds__(kLatentJoinThreads) latent_join_kernel(const L
         d0 = job(0);
         d1 = job(1);
     }
-    const int rows = d1.y, n = (d0.y - c0) / 2 + 1;  // parts, of every other CTA
+    const int rows = d1.y, by = d1.z, n = (d0.y - c0) / by + 1;  // parts, of every by-th CTA
     if (rows <= 0) return;
-    const int share = (blockIdx.x - c0) / 2, shares = max(n - 1, 1);
+    const int share = (blockIdx.x - c0) / by, shares = max(n - 1, 1);
     const long long fours = 128ll * rows, pieces = (long long)shares * gridDim.y;
     const long long piece = (long long)share * gridDim.y + blockIdx.y;
     const int begin = (int)(piece * fours / pieces), end = (int)((piece + 1) * fours / pieces);
     const int tid = threadIdx.x, hq = t.a.n_q_heads;
-    auto slot = [&](int i) { return (long long)(i == 0 ? d0.z : 2 * (c0 + 2 * i)); };
+    auto slot = [&](int i) { return (long long)(i == 0 ? d0.z : 2 * (c0 + by * i)); };
+    auto ml = [&](int i, int which, int m) { return __ldcg(t.part_ml + (slot(i) * 2 + which) * kRows + m); };
+    auto from = [&](int i, int four, int m) {
+        return __ldcg(reinterpret_cast<const float4 *>(t.part_o) + (slot(i) * 128 + four) * kRows + m);
+    };
+    auto add = [](float4 &x, float f, float4 y) {
+        x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
+    };
+    auto put = [&](int four, int m, float4 x, float shift, float l) {
+        const float inv = 1.0f / l;
+        if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+        const int row = d1.x + m, head = row % hq;
+        const long long packed = d0.w + row / hq;
+        const __nv_bfloat162 u = __floats2bfloat162_rn(x.x, x.y), v = __floats2bfloat162_rn(x.z, x.w);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
+                                   (long long)head * kLatent + four * 4) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
+        if (t.a.lse && four == 0)
+            t.a.lse[packed * hq + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
+    };
+    constexpr int kFew = 4;
+    if (n <= kFew) {
+        // all loads of a piece of output before the first use
+        for (int item = begin + tid; item < end; item += kLatentJoinThreads) {
+            const int four = item / rows, m = item % rows;
+            float pm[kFew], pl[kFew], top = -INFINITY, l = 0.0f;
+            float4 po[kFew], x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                pm[i] = i < n ? ml(i, 0, m) : -INFINITY;
+                pl[i] = i < n ? ml(i, 1, m) : 0.0f;
+                if (i < n) po[i] = from(i, four, m);
+            }
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) top = fmaxf(top, pm[i]);
+            const float shift = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                if (i >= n) continue;
+                const float f = exp2_approx(pm[i] - shift);
+                l = fmaf(f, pl[i], l);
+                add(x, f, po[i]);
+            }
+            put(four, m, x, shift, l);
+        }
+        return;
+    }
     for (int base = begin; base < end; base += kLatentJoinThreads) {
         const int items = min(end - base, kLatentJoinThreads), deals = kLatentJoinThreads / items;
         const int deal = tid / items, item = base + tid % items, four = item / rows, m = item % rows;
-        auto ml = [&](int i, int which) { return __ldcg(t.part_ml + (slot(i) * 2 + which) * kRows + m); };
         float top = -INFINITY;
         if (deal < deals)
 #pragma unroll 4
-            for (int i = deal; i < n; i += deals) top = fmaxf(top, ml(i, 0));
+            for (int i = deal; i < n; i += deals) top = fmaxf(top, ml(i, 0, m));
         sum_l[tid] = top;
         __syncthreads();
         for (int i = 0; i < deals; ++i) top = fmaxf(top, sum_l[i * items + tid % items]);
@@ -818,11 +874,9 @@ __global__ void __launch_bounds__(kLatentJoinThreads) latent_join_kernel(const L
         if (deal < deals)
 #pragma unroll 4
             for (int i = deal; i < n; i += deals) {
-                const float f = exp2_approx(ml(i, 0) - shift);
-                const float4 y =
-                    __ldcg(reinterpret_cast<const float4 *>(t.part_o) + (slot(i) * 128 + four) * kRows + m);
-                l = fmaf(f, ml(i, 1), l);
-                x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
+                const float f = exp2_approx(ml(i, 0, m) - shift);
+                l = fmaf(f, ml(i, 1, m), l);
+                add(x, f, from(i, four, m));
             }
         __syncthreads();
         sum[tid] = x;
@@ -830,21 +884,10 @@ __global__ void __launch_bounds__(kLatentJoinThreads) latent_join_kernel(const L
         __syncthreads();
         if (deal == 0) {
             for (int i = 1; i < deals; ++i) {
-                const float4 y = sum[i * items + tid];
-                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                add(x, 1.0f, sum[i * items + tid]);
                 l += sum_l[i * items + tid];
             }
-            const float inv = 1.0f / l;
-            if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-            const int row = d1.x + m, head = row % hq;
-            const long long packed = d0.w + row / hq;
-            const __nv_bfloat162 u = __floats2bfloat162_rn(x.x, x.y), v = __floats2bfloat162_rn(x.z, x.w);
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
-                                       (long long)head * kLatent + four * 4) =
-                make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
-            if (t.a.lse && four == 0)
-                t.a.lse[packed * hq + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
+            put(four, m, x, shift, l);
         }
         __syncthreads();
     }

@@ -105,6 +105,14 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// 16 bytes into shared memory, asynchronously; zeros if !there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+// Ends this thread's copies so far.
+__device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---------------------------------------------------------- tensor memory
 
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, int cols) {
