@@ -8,8 +8,24 @@
 // prompt_any_kernel   any types, strides and dimensions, in 32 bits throughout: a CTA a
 //   (row, query head), its four warps take every fourth key, each with a running maximum
 //   and sum, joined at the end.
+//
+// prompt_tensor_kernel   bfloat16 with keys of 128 (and a shared part of 64 or none) and
+//   values of 128, on the tensor cores of two CTAs at a time.  A job is a (request, query
+//   head) and 512 of its queries, two tiles of 256, of which a CTA has 128 each; a step is
+//   128 keys:  S = Q K^T into tensor memory, then
+//     y = S c   m' = max(m, max y)   w = 2^(y - m')   l = l 2^(m - m') + sum w
+//     O = O 2^(m - m') + W V
+//   with W written over S in tensor memory and O kept there.  m moves only when a row's
+//   maximum grows by 2^kLazy (until then w may pass 1, and O is not touched).  One tile's
+//   softmax runs beside the other tile's products.  A CTA holds half of either product's
+//   right operand (64 keys; 64 of the values' elements), so that it is fetched once for 512
+//   queries and read from shared memory at three quarters of its bandwidth, not at all of it.
+//   One warp copies (TMA), one of the first CTA issues, four a tile do the softmax, a thread
+//   a row.  Jobs with the most keys come first.
 
 #include "kvcache.cuh"
+#include "tensor.cuh"
+#include "tensormap.cuh"
 
 namespace dspark {
 
@@ -126,6 +142,445 @@ __global__ void __launch_bounds__(kPromptWarps * 32) prompt_any_kernel(PromptArg
         a.lse[(long long)row * a.n_q_heads + h] = L == 0.0f ? -INFINITY : base + logf(L);
 }
 
+// --------------------------------------------------- tensor-core kernel
+
+constexpr int kPromptTile = 256, kPromptBlock = 2 * kPromptTile;  // queries a tile, a job
+constexpr int kPromptKeys = 128;                                  // a step
+constexpr int kPromptDim = 128, kPromptShared = 64;
+constexpr int kPromptStages = 3;
+constexpr int kRowsChunk = 128 * 128, kKeysChunk = 64 * 128;  // bytes of 64 elements of 128 rows, of 64 keys
+constexpr int kPromptThreads = 320, kPromptCopyWarp = 8, kPromptMatrixWarp = 9;
+constexpr int kPromptScoreCol = 0, kPromptOutCol = 256;  // columns of tensor memory, a tile's 128 on
+constexpr int kDiagonal = kPromptBlock / kPromptKeys + 1;  // steps of a job that some query sees a part of
+constexpr float kPromptLazy = 8.0f;  // log2 of how far weights may grow past 1
+constexpr float kPromptLog2e = 1.4426950408889634f, kPromptLn2 = 0.6931471805599453f;
+
+// Shared memory of a CTA: the queries of both tiles, rings of keys and values, control.
+template <bool kShared>
+struct PromptShape {
+    static constexpr int kParts = 2 + kShared;  // of 64 elements of a key
+    static constexpr int kQBytes = kParts * kRowsChunk;
+    static constexpr int kKeyBytes = kParts * kKeysChunk, kValueBytes = kPromptKeys * 128;
+    static constexpr int kKeyAt = 2 * kQBytes;
+    static constexpr int kValueAt = kKeyAt + kPromptStages * kKeyBytes;
+    static constexpr int kControl = kValueAt + kPromptStages * kValueBytes;
+    static constexpr int kTotal = kControl + 2048;
+    static_assert(kTotal <= 227 * 1024, "shared memory");
+};
+
+// Barriers that the issuing warp waits on are the first CTA's; those that it commits to
+// are each CTA's own.
+struct alignas(16) PromptControl {
+    unsigned long long q_full[2], key_full[kPromptStages], value_full[kPromptStages], p_ready[2];  // the first's
+    unsigned long long key_empty[kPromptStages], value_empty[kPromptStages], s_full[2], o_done[2], value_seen, drain;
+    unsigned tmem;
+    int abort;
+    int request, block;  // of the job
+    unsigned nonfinite[kDiagonal][kPromptKeys / 32];  // keys whose values were zeroed in either CTA
+    long long scan[40];
+};
+static_assert(sizeof(PromptControl) <= 2048, "control area");
+
+template <bool kShared>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
+prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_v,
+                     const PromptArgs a) {
+    using S = PromptShape<kShared>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    PromptControl &ctl = *reinterpret_cast<PromptControl *>(smem + S::kControl);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank(), head = blockIdx.x / 2 % a.n_q_heads;
+    const long long cluster = blockIdx.x / 2 / a.n_q_heads;  // the job's place among all blocks of 512 queries
+    const uint32_t base = smem_addr(smem);
+    if (tid == 0) {
+        for (int i = 0; i < kPromptStages; ++i) {
+            mbar_init(smem_addr(&ctl.key_full[i]), 1);
+            mbar_init(smem_addr(&ctl.value_full[i]), 1);
+            mbar_init(smem_addr(&ctl.key_empty[i]), 1);
+            mbar_init(smem_addr(&ctl.value_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&ctl.q_full[i]), 1);
+            mbar_init(smem_addr(&ctl.p_ready[i]), 8);
+            mbar_init(smem_addr(&ctl.s_full[i]), 1);
+            mbar_init(smem_addr(&ctl.o_done[i]), 1);
+        }
+        mbar_init(smem_addr(&ctl.value_seen), 1);
+        mbar_init(smem_addr(&ctl.drain), 1);
+        ctl.abort = 0;
+        ctl.request = -1;
+        fence_mbar_init();
+        prefetch_map(&map_q);
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+        if (kShared) prefetch_map(&map_s);
+    }
+    for (int i = tid; i < kDiagonal * kPromptKeys / 32; i += kPromptThreads) (&ctl.nonfinite[0][0])[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    {  // the request: each thread counts the blocks of a run of them
+        const int per = (a.B + kPromptThreads - 1) / kPromptThreads;
+        auto blocks = [&](int r, bool report) {
+            const PromptRange w = load_range(a, r);
+            return usable(a, w, report) ? (w.hi - w.lo + kPromptBlock - 1) / kPromptBlock : 0;
+        };
+        long long mine = 0, total;
+        for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r) mine += blocks(r, blockIdx.x == 0);
+        long long before = block_exclusive_scan<long long>(mine, ctl.scan, &total);
+        if (cluster >= before && cluster < before + mine)
+            for (int r = tid * per;; ++r) {
+                const int n = blocks(r, false);
+                if (cluster < before + n) {
+                    ctl.request = r;
+                    ctl.block = n - 1 - (int)(cluster - before);  // the last queries see most keys
+                    break;
+                }
+                before += n;
+            }
+    }
+    __syncthreads();
+    if (ctl.request < 0) return;  // (both CTAs)
+    if (warp == kPromptMatrixWarp) tmem_alloc_pair(smem_addr(&ctl.tmem), 512);
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers are there
+    tmem_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    volatile int *abort = &ctl.abort;
+    bool ok = true;
+    auto wait = [&](unsigned long long *bar, unsigned parity) {
+        return ok = warp_wait(ok, smem_addr(bar), parity, abort, a.status);
+    };
+    auto first_cta = [&](unsigned long long *bar) { return cluster_addr(smem_addr(bar), 0); };
+    const PromptRange w = load_range(a, ctl.request);
+    const int n = w.hi - w.lo, m = w.k1 - w.k0, row0 = ctl.block * kPromptBlock;
+    // query i sees keys 0..i + ahead
+    const int ahead = m - n;
+    // steps of tile t: up to the last key that its last query sees
+    auto steps_of = [&](int t) {
+        const int last = min(row0 + (t + 1) * kPromptTile, n) - 1;
+        return last < row0 + t * kPromptTile ? 0 : max(last + ahead + kPromptKeys, 0) / kPromptKeys;
+    };
+    const int steps[2] = {steps_of(0), steps_of(1)}, most = max(steps[0], steps[1]);
+    // from this step on some query does not see all keys
+    const int diagonal = max(row0 + ahead + 1, 0) / kPromptKeys;
+
+    if (warp == kPromptCopyWarp) {
+        // ------------------------------------------------ copy warp
+        const int group = head / a.group;
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+            if (!steps[t]) continue;
+            if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.q_full[t]), 2 * S::kQBytes);
+            __syncwarp();
+            if (lane < S::kParts)
+                tma_load_4d_pair(base + t * S::kQBytes + lane * kRowsChunk, &map_q, lane * 64,
+                                 w.lo + row0 + t * kPromptTile + rank * 128, head, 0, first_cta(&ctl.q_full[t]));
+        }
+        int stage = 0;
+        unsigned parity = 1;
+        for (int j = 0; j < most; ++j) {
+            if (!wait(&ctl.key_empty[stage], parity)) break;
+            if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.key_full[stage]), 2 * S::kKeyBytes);
+            __syncwarp();
+            const int key = w.k0 + j * kPromptKeys;
+            if (lane < S::kParts)
+                tma_load_4d_pair(base + S::kKeyAt + stage * S::kKeyBytes + lane * kKeysChunk,
+                                 lane < 2 ? &map_k : &map_s, lane < 2 ? lane * 64 : 0, key + rank * 64,
+                                 lane < 2 ? group : 0, 0, first_cta(&ctl.key_full[stage]));
+            if (!wait(&ctl.value_empty[stage], parity)) break;
+            if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.value_full[stage]), 2 * S::kValueBytes);
+            __syncwarp();
+            if (lane == 0)
+                tma_load_4d_pair(base + S::kValueAt + stage * S::kValueBytes, &map_v, rank * 64, key, group, 0,
+                                 first_cta(&ctl.value_full[stage]));
+            if (++stage == kPromptStages) stage = 0, parity ^= 1;
+        }
+        if (!ok && rank == 0 && lane == 0) {
+            // copies still under way write the pair's buffers (each wait ends by itself; the
+            // CTAs leave together)
+            for (int p = 0; p < 2; ++p)
+                for (int i = 0; i < kPromptStages; ++i) {
+                    mbar_wait(smem_addr(&ctl.key_full[i]), p, kWaitLimitNs / 4);
+                    mbar_wait(smem_addr(&ctl.value_full[i]), p, kWaitLimitNs / 4);
+                }
+        }
+    } else if (warp == kPromptMatrixWarp) {
+        // ---------------------------------------------- matrix warp
+        // Keeps step as a whole, so that addresses stay in uniform registers; one lane
+        // issues.  A tile's products of a step: its output with the last step's weights, then
+        // its scores, while the other tile's weights are computed.
+        if (rank == 0) {
+            constexpr uint32_t score_word = mma_word(true, kPromptKeys, false) + kPairOf128;
+            constexpr uint32_t value_word = mma_word(true, kPromptDim, true) + kPairOf128;
+            const uint32_t ubase = __shfl_sync(kFullMask, base, 0), utmem = __shfl_sync(kFullMask, tmem, 0);
+            const bool leader = elect_one();
+            const uint64_t desc_q = smem_operand(ubase, 16, 128);
+            const uint64_t desc_k = smem_operand(ubase + S::kKeyAt, 16, 128);
+            const uint64_t desc_v = smem_operand(ubase + S::kValueAt, 16, 128);
+            int key_stage = 0, value_stage = 0;
+            unsigned key_parity = 0, value_parity = 0;
+            for (int j = 0; j <= most && ok; ++j) {
+                // step j - 1's weights and values, step j's keys
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
+                    if (j > 0 && j <= steps[t]) {
+                        const bool first = t == 0 || steps[0] < j, last = t == 1 || steps[1] < j;
+                        if (first) {
+                            if (!wait(&ctl.value_full[value_stage], value_parity)) break;
+                            if (lane < 2) cluster_arrive(cluster_addr(smem_addr(&ctl.value_seen), lane));
+                        }
+                        if (!wait(&ctl.p_ready[t], j - 1)) break;
+                        tmem_fence_after();
+                        const uint64_t v = desc_v + value_stage * (S::kValueBytes >> 4);
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < kPromptKeys / 16; ++k)
+                                mma_pair_ts(utmem + kPromptOutCol + t * 128, utmem + kPromptScoreCol + t * 128 + k * 8,
+                                            v + (k * 16 * 128 >> 4), value_word, j > 1 || k > 0);
+                            if (last) mma_pair_commit(smem_addr(&ctl.value_empty[value_stage]));
+                            if (j == steps[t]) mma_pair_commit(smem_addr(&ctl.o_done[t]));
+                        }
+                        __syncwarp();
+                        if (last && ++value_stage == kPromptStages) value_stage = 0, value_parity ^= 1;
+                    }
+                    if (j < steps[t]) {
+                        const bool first = t == 0 || steps[0] <= j, last = t == 1 || steps[1] <= j;
+                        if (j == 0 && !wait(&ctl.q_full[t], 0)) break;
+                        if (first && !wait(&ctl.key_full[key_stage], key_parity)) break;
+                        tmem_fence_after();
+                        const uint64_t q = desc_q + t * (S::kQBytes >> 4);
+                        const uint64_t key = desc_k + key_stage * (S::kKeyBytes >> 4);
+                        if (leader) {
+#pragma unroll
+                            for (int k = 0; k < 4 * S::kParts; ++k)
+                                mma_pair_ss(utmem + kPromptScoreCol + t * 128,
+                                            q + (k / 4 * kRowsChunk + k % 4 * 32 >> 4),
+                                            key + (k / 4 * kKeysChunk + k % 4 * 32 >> 4), score_word, k > 0);
+                            mma_pair_commit(smem_addr(&ctl.s_full[t]));
+                            if (last) mma_pair_commit(smem_addr(&ctl.key_empty[key_stage]));
+                        }
+                        __syncwarp();
+                        if (last && ++key_stage == kPromptStages) key_stage = 0, key_parity ^= 1;
+                    }
+                }
+            }
+            // after a timeout: products still under way write tensor memory and barriers of
+            // the pair
+            if (!ok && leader) {
+                mma_pair_commit(smem_addr(&ctl.drain));
+                mbar_wait(smem_addr(&ctl.drain), 0);
+            }
+            __syncwarp();
+        }
+    } else {
+        // --------------------------------------------- softmax warps
+        const int t = warp >> 2, count = steps[t];
+        const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
+        const uint32_t scores = lanes + kPromptScoreCol + t * 128, outputs = lanes + kPromptOutCol + t * 128;
+        const float c = fmaxf(fabsf(a.scale) * kPromptLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
+        const bool negative = a.scale < 0.0f;
+        const int row = row0 + t * kPromptTile + rank * 128 + tid % 128;  // of the request's queries
+        const int sees = row + ahead + 1;                                 // keys
+        float mx = -INFINITY, l = 0.0f;  // running maximum (to base 2), sum
+        for (int j = 0; j < count; ++j) {
+            if (!wait(&ctl.s_full[t], j)) break;
+            tmem_fence_after();
+            uint32_t x[128];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_load32(scores + 32 * k, x + 32 * k);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_wait_load(x + 32 * k);
+            if (negative) {
+#pragma unroll
+                for (int k = 0; k < 128; ++k) x[k] ^= 0x80000000u;
+            }
+            const int there = sees - j * kPromptKeys;  // of the step's keys
+            if (j >= diagonal) {
+#pragma unroll
+                for (int k = 0; k < 128; ++k)
+                    if (k >= there) x[k] = 0xFF800000u;
+            }
+            float part[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                part[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 4]));
+#pragma unroll
+                for (int e = 8 + k; e < 128; e += 4) part[k] = fmaxf(part[k], __uint_as_float(x[e]));
+            }
+            const float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) * c;
+            // The maximum moves only when it grows by 2^kPromptLazy: until then the weights
+            // may pass 1, and sum and output stay as they are.  (The scores' barrier says that
+            // the last step's output is done too.)
+            const bool grow = top > mx + kPromptLazy || (mx == -INFINITY && top > mx);
+            if (__any_sync(kFullMask, grow)) {
+                const float f = grow ? exp2_approx(mx - top) : 1.0f;
+                if (grow) mx = top;
+                l *= f;
+                if (j > 0)
+#pragma unroll 1
+                    for (int d = 0; d < kPromptDim; d += 16) {
+                        uint32_t o[16];
+                        tmem_load16(outputs + d, o);
+                        tmem_wait_load16(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_store16(outputs + d, o);
+                    }
+            }
+            const float shift = mx == -INFINITY ? 0.0f : mx;
+            float2 sum[2] = {};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int at = 32 * k + 2 * e;
+                    const float2 y = fma2(make_float2(__uint_as_float(x[at]), __uint_as_float(x[at + 1])),
+                                          make_float2(c, c), make_float2(-shift, -shift));
+                    const float2 u = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                    sum[e & 1] = add2(sum[e & 1], u);
+                    // (bfloat16, 8 digits, as the values are: a product takes operands of one
+                    // type.  The sum keeps all digits, for lse)
+                    const __nv_bfloat162 two = __floats2bfloat162_rn(u.x, u.y);
+                    x[16 * k + e] = *reinterpret_cast<const uint32_t *>(&two);
+                }
+                tmem_store16(scores + 16 * k, x + 16 * k);  // over scores that have been read
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (j >= diagonal && (t == 0 || steps[0] <= j)) {
+                // NaN and infinities of values that some query does not see become zeros (0 x
+                // NaN would reach it); the rows that do see them get them at the end.  Each
+                // CTA does so for the elements that it holds.
+                wait(&ctl.value_seen, j);
+                unsigned char *values = smem + S::kValueAt + j % kPromptStages * S::kValueBytes;
+                if (ok)
+                    for (int i = tid % 128; i < kPromptKeys * 8; i += 128) {
+                        uint4 *at = reinterpret_cast<uint4 *>(values + i / 8 * 128 + ((i % 8 ^ (i / 8 & 7)) << 4));
+                        uint4 v = *at;
+                        unsigned *e = reinterpret_cast<unsigned *>(&v);
+                        bool bad = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const bool lo16 = (e[k] & 0x7F80u) == 0x7F80u;
+                            const bool hi16 = (e[k] & 0x7F800000u) == 0x7F800000u;
+                            bad = bad || lo16 || hi16;
+                            if (lo16) e[k] &= 0xFFFF0000u;
+                            if (hi16) e[k] &= 0x0000FFFFu;
+                        }
+                        if (!bad) continue;
+                        *at = v;
+                        const int key = i / 8;
+                        if (j * kPromptKeys + key < m)
+                            for (int k = 0; k < 2; ++k)
+                                cluster_or(cluster_addr(smem_addr(&ctl.nonfinite[j - diagonal][key / 32]), k),
+                                           1u << key % 32);
+                    }
+                cluster_fence();
+                fence_async_proxy();
+            }
+            tmem_wait_store();
+            tmem_fence_before();
+            __syncwarp();
+            if (!ok) break;
+            if (lane == 0) cluster_arrive(first_cta(&ctl.p_ready[t]));
+        }
+        if (count) wait(&ctl.o_done[t], 0);
+        tmem_fence_after();
+        const bool valid = row < n && ok;
+        if (__any_sync(kFullMask, valid)) {
+            const float shift = mx == -INFINITY ? 0.0f : mx, inv = l == 0.0f ? 0.0f : 1.0f / l;
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (long long)(w.lo + row) * a.ld_out +
+                                 (long long)head * kPromptDim;
+            if (count) cluster_fence();  // (the noted keys)
+#pragma unroll 1
+            for (int d = 0; d < kPromptDim; d += 32) {
+                uint32_t o[32] = {};
+                if (count) {
+                    tmem_load32(outputs + d, o);
+                    tmem_wait_load(o);
+                }
+                for (int j = diagonal; valid && j < most; ++j)
+                    for (int i = 0; i < kPromptKeys / 32; ++i) {
+                        const int left = sees - j * kPromptKeys - 32 * i;
+                        unsigned bits = *(volatile unsigned *)&ctl.nonfinite[j - diagonal][i];
+                        bits = left >= 32 ? bits : left > 0 ? bits & ((1u << left) - 1) : 0;
+                        for (; bits; bits &= bits - 1) {
+                            const long long key = w.k0 + j * kPromptKeys + 32 * i + __ffs(bits) - 1;
+                            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + key * a.ld_v +
+                                                     head / a.group * a.hs_v + d;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const float y = elem_value(v[k]);
+                                if (!(y - y == 0.0f)) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
+                            }
+                        }
+                    }
+                if (!valid) continue;
+                uint32_t p[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float u = __uint_as_float(o[2 * k]) * inv, v = __uint_as_float(o[2 * k + 1]) * inv;
+                    if (l == 0.0f) u = v = 0.0f;
+                    const __nv_bfloat162 two = __floats2bfloat162_rn(u, v);
+                    p[k] = *reinterpret_cast<const uint32_t *>(&two);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    reinterpret_cast<uint4 *>(out + d)[k] =
+                        make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+            }
+            if (valid && a.lse)
+                a.lse[(long long)(w.lo + row) * a.n_q_heads + head] =
+                    l == 0.0f ? -INFINITY : shift * kPromptLn2 + logf(l);
+        }
+        tmem_fence_before();
+    }
+    __syncthreads();
+    cluster_sync();  // the other CTA may arrive on, or multiply from, what is here
+    if (warp == kPromptMatrixWarp) tmem_free_pair(tmem, 512);
+}
+
+namespace {
+
+// Whether a call runs on the tensor cores: the dimensions that the kernel is laid out for,
+// and the strides and bases that TMA and the 16-byte accesses take.
+bool prompt_tensor_fits(const PromptArgs &a, int dtype) {
+    if (dtype != DSPARK_DTYPE_BF16 || a.key_dim != kPromptDim || a.value_dim != kPromptDim || a.max_keys < 1)
+        return false;
+    if (a.shared_dim != 0 && a.shared_dim != kPromptShared) return false;
+    for (long long s : {a.ld_q, a.ld_k, a.hs_k, a.ld_v, a.hs_v, a.ld_out, a.ld_shared})
+        if (s % 8 || s * 2 >= (1ll << 40)) return false;
+    return aligned(a.q, 16) && aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.out, 16) && aligned(a.shared, 16);
+}
+
+template <bool kShared>
+cudaError_t launch_prompt_tensor(const PromptArgs &a, cudaStream_t stream) {
+    using S = PromptShape<kShared>;
+    const int width = a.key_dim + a.shared_dim, n_kv_heads = a.n_q_heads / a.group;
+    // [head][row][element]
+    auto map = [&](CUtensorMap *to, const void *p, int dim, int rows, int heads, long long ld, long long hs, int box) {
+        const int64_t dims[4] = {dim, rows, heads, 1}, strides[3] = {ld, hs, ld};
+        return encode(to, p, 2, 64, true, dims, strides, box, 1);
+    };
+    CUtensorMap map_q, map_k, map_s = {}, map_v;
+    if (!map(&map_q, a.q, width, a.max_rows, a.n_q_heads, a.ld_q, width, 128) ||
+        !map(&map_k, a.k, a.key_dim, a.max_keys, n_kv_heads, a.ld_k, a.hs_k, 64) ||
+        !map(&map_v, a.v, a.value_dim, a.max_keys, n_kv_heads, a.ld_v, a.hs_v, kPromptKeys) ||
+        (kShared && !map(&map_s, a.shared, a.shared_dim, a.max_keys, 1, a.ld_shared, a.ld_shared, 64)))
+        return cudaErrorUnknown;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(prompt_tensor_kernel<kShared>), S::kTotal,
+                                27 + kShared);
+    if (e != cudaSuccess) return e;
+    // every request has one block that is not full at most
+    const long long grid = 2ll * a.n_q_heads * (a.max_rows / kPromptBlock + min(a.B, a.max_rows));
+    if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    return launch_pdl(prompt_tensor_kernel<kShared>, dim3((unsigned)grid), dim3(kPromptThreads), S::kTotal, stream,
+                      map_q, map_k, map_s, map_v, a);
+}
+
+}  // namespace
+
 }  // namespace dspark
 
 using namespace dspark;
@@ -182,9 +637,13 @@ extern "C" int dspark_prompt_attention(const void *q, int64_t ld_q, const void *
     a.scale = scale;
     a.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const dim3 grid(max_rows, n_q_heads), block(kPromptWarps * 32);
-    const cudaError_t e = dtype == DSPARK_DTYPE_BF16
-                              ? launch_pdl(prompt_any_kernel<__nv_bfloat16>, grid, block, 0, st, a)
-                              : launch_pdl(prompt_any_kernel<float>, grid, block, 0, st, a);
+    cudaError_t e;
+    if (prompt_tensor_fits(a, dtype)) {
+        e = shared_dim ? launch_prompt_tensor<true>(a, st) : launch_prompt_tensor<false>(a, st);
+    } else {
+        const dim3 grid(max_rows, n_q_heads), block(kPromptWarps * 32);
+        e = dtype == DSPARK_DTYPE_BF16 ? launch_pdl(prompt_any_kernel<__nv_bfloat16>, grid, block, 0, st, a)
+                                       : launch_pdl(prompt_any_kernel<float>, grid, block, 0, st, a);
+    }
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
