@@ -6,6 +6,17 @@
 //   weights_out_p = decay weights_p + sum exp(scale q . k_p - lse)
 // with lse the rows' log sums that the attention left, so the terms are its softmax.
 //
+// weights_kernel   bfloat16 rows over bfloat16 or E4M3 keys of 64 or 128 elements, on the
+//   matrix instruction of one warp, with positions as its rows and the window's (token,
+//   head) rows as its columns: keys are register operands that each thread loads for
+//   itself, once for all rows of the window (128 at a time), and a thread has the scores
+//   of few positions, so that the sum over rows is a sum in registers.  The elements of a
+//   contraction may come in any order that both operands share; here a thread's are
+//   contiguous, 16 bytes a load.  Products are exact in 32 bits: codes are halves as they
+//   are, and beside them queries are halves brought to 2^14 by a power of two a row, so
+//   that what they lose is below 2^-39 of a row's largest element.  A few rows leave most
+//   of the matrix instruction's rate unused, and HBM bounds the rest: tcgen05 would add
+//   the way of keys through shared memory.
 // weights_any_kernel   any types, strides, head and page sizes, in 32 bits throughout: a
 //   warp a position, its key held in registers, one row and query head after another.
 //
@@ -25,6 +36,7 @@
 
 #include "kvcache.cuh"
 #include "schedule.cuh"
+#include "tensor.cuh"
 
 namespace dspark {
 
@@ -105,6 +117,190 @@ __global__ void __launch_bounds__(kWeightsWarps * 32) weights_any_kernel(Weights
             t.weights_out[line + p] = p < w.P ? fmaf(t.decay, t.weights[line + p], sum) : sum;
             if (t.positions && p >= w.P && p < w.P + n) t.positions[line + p] = __ldg(t.pos + w.lo + (p - w.P));
         }
+    }
+}
+
+constexpr int kGatherWarps = 8, kGatherPositions = 512;  // of a CTA
+constexpr int kGatherRows = 128;                         // at a time
+constexpr float kGatherLog2e = 1.4426950408889634f;
+
+// x = a b + x: 16 x 16 times 16 x 8, halves or bfloat16.
+template <bool kHalf>
+__device__ __forceinline__ void mma_rows16(float (&x)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                           uint32_t b0, uint32_t b1) {
+    if constexpr (kHalf)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int D, bool kQuant>
+__global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsArgs t) {
+    constexpr int kPieces = D / 32;                 // of eight query elements a lane
+    constexpr int kLoads = kQuant ? D / 64 : D / 32;  // of 16 bytes a lane and key
+    __shared__ uint4 queries[kGatherRows / 8][kPieces][32];  // as the lanes take them
+    __shared__ float lse[kGatherRows], factor[kGatherRows];
+    __shared__ unsigned seen[kGatherRows];  // the window's tokens that a row sees
+    __shared__ float gathered[kGatherPositions];
+    pdl_trigger();
+    pdl_wait();
+    const AttendArgs &a = t.a;
+    const int r = blockIdx.z, kh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Window w = load_window(a, r);
+    const int n = counted(t, w, r, blockIdx.x == 0 && kh == 0 && tid == 0);
+    if (n < 0) return;
+    const int G = a.n_q_heads / a.cache.n_kv_heads, rows = n * G, len = w.hi - w.lo;
+    const int first = blockIdx.x * kGatherPositions, last = min(first + kGatherPositions, t.length);
+    const int end = n > 0 ? min(w.P + n, last) : first;  // from here on nothing is gathered
+    const long long line = ((long long)r * a.cache.n_kv_heads + kh) * t.length;
+    const int g = lane >> 2, q4 = lane & 3;  // a key's row of the matrix, its quarter of the elements
+
+    for (int row0 = 0; row0 < rows && first < end; row0 += kGatherRows) {
+        const int count = min(rows - row0, kGatherRows), tiles = (count + 7) / 8;
+        __syncthreads();
+        for (int i = warp; i < tiles * 8; i += kGatherWarps) {
+            const bool there = i < count;
+            const int token = there ? (row0 + i) / G : 0, row = w.lo + token;
+            const int head = kh * G + (there ? (row0 + i) % G : 0);
+            const __nv_bfloat16 *q =
+                static_cast<const __nv_bfloat16 *>(a.q) + (long long)row * a.ld_q + (long long)head * D;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (there && lane < D / 8) v = __ldg(reinterpret_cast<const uint4 *>(q) + lane);
+            float by = 1.0f;
+            if constexpr (kQuant) {
+                const unsigned e[4] = {v.x, v.y, v.z, v.w};
+                unsigned most = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) most = max(most, max(e[k] & 0x7FFFu, e[k] >> 16 & 0x7FFFu));
+                most = __reduce_max_sync(kFullMask, most);
+                // 2^(14 - its exponent); NaN and infinities stay what they are
+                const int exponent = min(max((int)(most >> 7), 20), 254) - 127;
+                const float up = __int_as_float((14 - exponent + 127) << 23);
+                by = __int_as_float((exponent - 14 + 127) << 23);
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __half2 two = __floats2half2_rn(__uint_as_float(e[k] << 16) * up,
+                                                          __uint_as_float(e[k] & 0xFFFF0000u) * up);
+                    h[k] = *reinterpret_cast<const uint32_t *>(&two);
+                }
+                v = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            // elements 8 lane.. are of the quarter (lane / 2) % 4 or lane % 4
+            if (lane < D / 8) {
+                const int quarter = kQuant ? lane / 2 % 4 : lane % 4;
+                const int piece = kQuant ? lane / 8 * 2 + lane % 2 : lane / 4;
+                queries[i / 8][piece][i % 8 * 4 + quarter] = v;
+            }
+            if (lane == 0) {
+                lse[i] = there ? t.lse[(long long)row * a.n_q_heads + head] : INFINITY;
+                factor[i] = by;
+                seen[i] = there ? ancestors_of(a, row, token, len) : 0;
+            }
+        }
+        __syncthreads();
+        for (int p0 = first + warp * 32; p0 < end; p0 += kGatherWarps * 32) {
+            // a position a lane: where its key lies
+            const int p = p0 + lane;
+            long long at = -1;
+            float own_scale = 1.0f;
+            if (p < end) {
+                int token;
+                const int page = kv_page(a.cache, r, p, &token);
+                if (page < 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+                else {
+                    at = kv_offset(a.cache, page, token, kh);
+                    if constexpr (kQuant)
+                        own_scale = __ldg(a.cache.k_scale + kv_scale_offset(a.cache, page, token, kh));
+                }
+            }
+            // keys g, g + 8, g + 16 and g + 24
+            uint4 key[4][kLoads];
+            float scale[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long long from = __shfl_sync(kFullMask, at, g + 8 * i);
+                scale[i] = __shfl_sync(kFullMask, own_scale, g + 8 * i);
+                const unsigned char *k = a.cache.k + from * (kQuant ? 1 : 2) + q4 * 16;
+#pragma unroll
+                for (int c = 0; c < kLoads; ++c)
+                    key[i][c] = from < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(k + c * 64));
+            }
+            const bool in_window = p0 + 32 > w.P;
+            float sum[4] = {};
+            for (int tile = 0; tile < tiles; ++tile) {
+                float x[2][4] = {};
+#pragma unroll
+                for (int c = 0; c < kLoads; ++c) {
+                    if constexpr (kQuant) {
+                        const uint4 b0 = queries[tile][2 * c][lane], b1 = queries[tile][2 * c + 1][lane];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 u0 = eight_halves(make_uint2(key[2 * i][c].x, key[2 * i][c].y));
+                            const uint4 v0 = eight_halves(make_uint2(key[2 * i + 1][c].x, key[2 * i + 1][c].y));
+                            mma_rows16<true>(x[i], u0.x, v0.x, u0.y, v0.y, b0.x, b0.y);
+                            mma_rows16<true>(x[i], u0.z, v0.z, u0.w, v0.w, b0.z, b0.w);
+                            const uint4 u1 = eight_halves(make_uint2(key[2 * i][c].z, key[2 * i][c].w));
+                            const uint4 v1 = eight_halves(make_uint2(key[2 * i + 1][c].z, key[2 * i + 1][c].w));
+                            mma_rows16<true>(x[i], u1.x, v1.x, u1.y, v1.y, b1.x, b1.y);
+                            mma_rows16<true>(x[i], u1.z, v1.z, u1.w, v1.w, b1.z, b1.w);
+                        }
+                    } else {
+                        const uint4 b = queries[tile][c][lane];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint4 u = key[2 * i][c], v = key[2 * i + 1][c];
+                            mma_rows16<false>(x[i], u.x, v.x, u.y, v.y, b.x, b.y);
+                            mma_rows16<false>(x[i], u.z, v.z, u.w, v.w, b.z, b.w);
+                        }
+                    }
+                }
+                // scores of keys g + 8 i with rows 2 q4 and 2 q4 + 1 of the tile
+                const int at_row = tile * 8 + 2 * q4;
+                const float2 base = *reinterpret_cast<const float2 *>(&lse[at_row]);
+                const float2 by = *reinterpret_cast<const float2 *>(&factor[at_row]);
+                const uint2 sees = *reinterpret_cast<const uint2 *>(&seen[at_row]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float y0 = x[i / 2][i % 2 * 2], y1 = x[i / 2][i % 2 * 2 + 1];
+                    if constexpr (kQuant) y0 *= by.x * scale[i], y1 *= by.y * scale[i];
+                    // (the difference from lse before the change of base: where a term
+                    // counts, it is small)
+                    float e0 = exp2_approx(fmaf(y0, a.scale, -base.x) * kGatherLog2e);
+                    float e1 = exp2_approx(fmaf(y1, a.scale, -base.y) * kGatherLog2e);
+                    if (in_window) {
+                        const int token = p0 + g + 8 * i - w.P;
+                        if (token >= 0 && !(sees.x >> min(token, 31) & 1)) e0 = 0.0f;
+                        if (token >= 0 && !(sees.y >> min(token, 31) & 1)) e1 = 0.0f;
+                    }
+                    sum[i] += e0 + e1;
+                }
+            }
+            float mine = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum[i] += __shfl_xor_sync(kFullMask, sum[i], 1);
+                sum[i] += __shfl_xor_sync(kFullMask, sum[i], 2);
+                const float of = __shfl_sync(kFullMask, sum[i], lane % 8 * 4);
+                if (lane / 8 == i) mine = of;
+            }
+            if (at < 0) mine = 0.0f;
+            gathered[p - first] = row0 == 0 ? mine : gathered[p - first] + mine;
+        }
+    }
+    __syncthreads();
+    for (int p = first + tid; p < last; p += kGatherWarps * 32) {
+        const float sum = p < end ? gathered[p - first] : 0.0f;
+        t.weights_out[line + p] = p < w.P ? fmaf(t.decay, t.weights[line + p], sum) : sum;
+        if (t.positions && p >= w.P && p < w.P + n) t.positions[line + p] = __ldg(t.pos + w.lo + (p - w.P));
     }
 }
 
@@ -321,6 +517,22 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // Entries that can move: as many as are kept, or as lie behind them.
 int most_moves(int keep, int length) { return length > keep ? min(keep, length - keep) : 0; }
 
+// Whether weights_kernel takes a call's types, heads and layouts.
+bool gather_fits(const AttendArgs &a, int dtype, const dspark_kv_cache &c) {
+    if (dtype != DSPARK_DTYPE_BF16 || c.dtype == DSPARK_DTYPE_F32 || (c.head_dim != 64 && c.head_dim != 128))
+        return false;
+    const int e = kv_elem_bytes(c.dtype);
+    for (int64_t s : {c.page_stride, c.token_stride, c.head_stride})
+        if (s * e % 16) return false;
+    return aligned(c.k, 16) && aligned(a.q, 16) && a.ld_q % 8 == 0;
+}
+
+template <int D, bool kQuant>
+cudaError_t launch_gather(const WeightsArgs &t, cudaStream_t stream) {
+    const dim3 grid((t.length + kGatherPositions - 1) / kGatherPositions, t.a.cache.n_kv_heads, t.a.B);
+    return launch_pdl(weights_kernel<D, kQuant>, grid, dim3(kGatherWarps * 32), 0, stream, t);
+}
+
 template <typename T>
 cudaError_t launch_weights(const WeightsArgs &t, int cache_dtype, cudaStream_t stream) {
     const dim3 grid((t.length + kWeightsPositions - 1) / kWeightsPositions, t.a.cache.n_kv_heads, t.a.B);
@@ -384,8 +596,15 @@ extern "C" int dspark_attention_weights(const void *q, int64_t ld_q, int32_t dty
     t.pos = pos;
     t.positions = positions;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == DSPARK_DTYPE_BF16 ? launch_weights<__nv_bfloat16>(t, cache->dtype, st)
-                                                     : launch_weights<float>(t, cache->dtype, st);
+    const bool quant = cache->dtype == DSPARK_DTYPE_E4M3, small = cache->head_dim == 64;
+    cudaError_t e;
+    if (gather_fits(a, dtype, *cache))
+        e = quant ? small ? launch_gather<64, true>(t, st) : launch_gather<128, true>(t, st)
+            : small ? launch_gather<64, false>(t, st)
+                    : launch_gather<128, false>(t, st);
+    else
+        e = dtype == DSPARK_DTYPE_BF16 ? launch_weights<__nv_bfloat16>(t, cache->dtype, st)
+                                       : launch_weights<float>(t, cache->dtype, st);
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
