@@ -52,6 +52,7 @@ struct WeightsArgs {
     int length;
     const int32_t *pos;
     int32_t *positions;
+    int span;  // positions of a CTA of weights_kernel
 };
 
 // How many rows of a window count, -1 if the request is left alone; with `report`,
@@ -120,7 +121,8 @@ __global__ void __launch_bounds__(kWeightsWarps * 32) weights_any_kernel(Weights
     }
 }
 
-constexpr int kGatherWarps = 8, kGatherPositions = 512;  // of a CTA
+constexpr int kGatherWarps = 8, kGatherStep = 32 * kGatherWarps;  // a CTA's positions at a time
+constexpr int kGatherMost = 2048;                                 // positions of a CTA
 constexpr int kGatherRows = 128;                         // at a time
 constexpr float kGatherLog2e = 1.4426950408889634f;
 
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsAr
     __shared__ uint4 queries[kGatherRows / 8][kPieces][32];  // as the lanes take them
     __shared__ float lse[kGatherRows], factor[kGatherRows];
     __shared__ unsigned seen[kGatherRows];  // the window's tokens that a row sees
-    __shared__ float gathered[kGatherPositions];
+    __shared__ float gathered[kGatherMost];  // by the rows before, where they are more than fit
     pdl_trigger();
     pdl_wait();
     const AttendArgs &a = t.a;
@@ -158,10 +160,49 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsAr
     const int n = counted(t, w, r, blockIdx.x == 0 && kh == 0 && tid == 0);
     if (n < 0) return;
     const int G = a.n_q_heads / a.cache.n_kv_heads, rows = n * G, len = w.hi - w.lo;
-    const int first = blockIdx.x * kGatherPositions, last = min(first + kGatherPositions, t.length);
+    const int first = blockIdx.x * t.span, last = min(first + t.span, t.length);
     const int end = n > 0 ? min(w.P + n, last) : first;  // from here on nothing is gathered
     const long long line = ((long long)r * a.cache.n_kv_heads + kh) * t.length;
     const int g = lane >> 2, q4 = lane & 3;  // a key's row of the matrix, its quarter of the elements
+
+    // A position a lane: where its key lies, looked up one step ahead of its loads, and
+    // then keys g, g + 8, g + 16 and g + 24 of the warp's 32.
+    struct Place {
+        long long at;
+        float scale;
+    };
+    auto look_up = [&](int p) -> Place {
+        Place x = {-1, 1.0f};
+        if (p < end) {
+            int token;
+            const int page = kv_page(a.cache, r, p, &token);
+            if (page < 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+            else {
+                x.at = kv_offset(a.cache, page, token, kh);
+                if constexpr (kQuant) x.scale = __ldg(a.cache.k_scale + kv_scale_offset(a.cache, page, token, kh));
+            }
+        }
+        return x;
+    };
+    uint4 key[4][kLoads];
+    auto fetch = [&](const Place &x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long from = __shfl_sync(kFullMask, x.at, g + 8 * i);
+            const unsigned char *k = a.cache.k + from * (kQuant ? 1 : 2) + q4 * 16;
+#pragma unroll
+            for (int c = 0; c < kLoads; ++c)
+                key[i][c] = from < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(k + c * 64));
+        }
+    };
+    const int own = first + warp * 32 + lane;  // the lane's first position
+    Place now = look_up(own), next = look_up(own + kGatherStep);
+    fetch(now);
+    auto put = [&](int p, float sum) {
+        if (p >= last) return;
+        t.weights_out[line + p] = p < w.P ? fmaf(t.decay, t.weights[line + p], sum) : sum;
+        if (t.positions && p >= w.P && p < w.P + n) t.positions[line + p] = __ldg(t.pos + w.lo + (p - w.P));
+    };
 
     for (int row0 = 0; row0 < rows && first < end; row0 += kGatherRows) {
         const int count = min(rows - row0, kGatherRows), tiles = (count + 7) / 8;
@@ -208,32 +249,10 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsAr
         }
         __syncthreads();
         for (int p0 = first + warp * 32; p0 < end; p0 += kGatherWarps * 32) {
-            // a position a lane: where its key lies
             const int p = p0 + lane;
-            long long at = -1;
-            float own_scale = 1.0f;
-            if (p < end) {
-                int token;
-                const int page = kv_page(a.cache, r, p, &token);
-                if (page < 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
-                else {
-                    at = kv_offset(a.cache, page, token, kh);
-                    if constexpr (kQuant)
-                        own_scale = __ldg(a.cache.k_scale + kv_scale_offset(a.cache, page, token, kh));
-                }
-            }
-            // keys g, g + 8, g + 16 and g + 24
-            uint4 key[4][kLoads];
             float scale[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const long long from = __shfl_sync(kFullMask, at, g + 8 * i);
-                scale[i] = __shfl_sync(kFullMask, own_scale, g + 8 * i);
-                const unsigned char *k = a.cache.k + from * (kQuant ? 1 : 2) + q4 * 16;
-#pragma unroll
-                for (int c = 0; c < kLoads; ++c)
-                    key[i][c] = from < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(k + c * 64));
-            }
+            for (int i = 0; i < 4; ++i) scale[i] = __shfl_sync(kFullMask, now.scale, g + 8 * i);
             const bool in_window = p0 + 32 > w.P;
             float sum[4] = {};
             for (int tile = 0; tile < tiles; ++tile) {
@@ -292,16 +311,20 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsAr
                 const float of = __shfl_sync(kFullMask, sum[i], lane % 8 * 4);
                 if (lane / 8 == i) mine = of;
             }
-            if (at < 0) mine = 0.0f;
-            gathered[p - first] = row0 == 0 ? mine : gathered[p - first] + mine;
+            if (now.at < 0) mine = 0.0f;
+            if (row0 > 0) mine += gathered[p - first];
+            if (row0 + kGatherRows < rows) gathered[p - first] = mine;
+            else put(p, mine);
+            // (the rows after these begin with the first positions again)
+            const bool more = p0 + kGatherStep < end;
+            now = more ? next : look_up(own);
+            next = look_up(more ? p + 2 * kGatherStep : own + kGatherStep);
+            if (more || row0 + kGatherRows < rows) fetch(now);
         }
     }
-    __syncthreads();
-    for (int p = first + tid; p < last; p += kGatherWarps * 32) {
-        const float sum = p < end ? gathered[p - first] : 0.0f;
-        t.weights_out[line + p] = p < w.P ? fmaf(t.decay, t.weights[line + p], sum) : sum;
-        if (t.positions && p >= w.P && p < w.P + n) t.positions[line + p] = __ldg(t.pos + w.lo + (p - w.P));
-    }
+    // positions of which no warp had one: all of them without rows
+    for (int p = first + tid; p < last; p += kGatherStep)
+        if (rows == 0 || p - lane >= end) put(p, 0.0f);
 }
 
 // -------------------------------------------------------------- eviction
@@ -529,8 +552,12 @@ bool gather_fits(const AttendArgs &a, int dtype, const dspark_kv_cache &c) {
 
 template <int D, bool kQuant>
 cudaError_t launch_gather(const WeightsArgs &t, cudaStream_t stream) {
-    const dim3 grid((t.length + kGatherPositions - 1) / kGatherPositions, t.a.cache.n_kv_heads, t.a.B);
-    return launch_pdl(weights_kernel<D, kQuant>, grid, dim3(kGatherWarps * 32), 0, stream, t);
+    // some four times as many CTAs as run at a time, of 256 to 2048 positions
+    const long long all = (long long)t.length * t.a.cache.n_kv_heads * t.a.B / (8 * sm_count());
+    WeightsArgs u = t;
+    u.span = (int)min(max((all + kGatherStep - 1) / kGatherStep, 1ll), (long long)(kGatherMost / kGatherStep)) * kGatherStep;
+    const dim3 grid((t.length + u.span - 1) / u.span, t.a.cache.n_kv_heads, t.a.B);
+    return launch_pdl(weights_kernel<D, kQuant>, grid, dim3(kGatherWarps * 32), 0, stream, u);
 }
 
 template <typename T>
