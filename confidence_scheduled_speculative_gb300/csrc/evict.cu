@@ -8,15 +8,15 @@
 //
 // weights_kernel   bfloat16 rows over bfloat16 or E4M3 keys of 64 or 128 elements, on the
 //   matrix instruction of one warp, with positions as its rows and the window's (token,
-//   head) rows as its columns: keys are register operands that each thread loads for
-//   itself, once for all rows of the window (128 at a time), and a thread has the scores
-//   of few positions, so that the sum over rows is a sum in registers.  The elements of a
-//   contraction may come in any order that both operands share; here a thread's are
-//   contiguous, 16 bytes a load.  Products are exact in 32 bits: codes are halves as they
-//   are, and beside them queries are halves brought to 2^14 by a power of two a row, so
-//   that what they lose is below 2^-39 of a row's largest element.  A few rows leave most
-//   of the matrix instruction's rate unused, and HBM bounds the rest: tcgen05 would add
-//   the way of keys through shared memory.
+//   head) rows as its columns, 64 at a time: a key is read once for all of them, and a
+//   thread has the scores of few positions, so that the sum over rows is a sum in
+//   registers.  The elements of a contraction may come in any order that both operands
+//   share; here a thread's are contiguous, so that it copies what it multiplies itself, 16
+//   bytes at a time and two steps ahead, and waits for no other thread.  Products are
+//   exact in 32 bits: codes are halves as they are, and beside them queries are halves
+//   brought to 2^14 by a power of two a row, so that what they lose is below 2^-39 of a
+//   row's largest element.  A few rows leave most of the matrix instruction's rate unused,
+//   and HBM bounds the rest: tcgen05 would add barriers between warps.
 // weights_any_kernel   any types, strides, head and page sizes, in 32 bits throughout: a
 //   warp a position, its key held in registers, one row and query head after another.
 //
@@ -121,9 +121,9 @@ __global__ void __launch_bounds__(kWeightsWarps * 32) weights_any_kernel(Weights
     }
 }
 
-constexpr int kGatherWarps = 8, kGatherStep = 32 * kGatherWarps;  // a CTA's positions at a time
-constexpr int kGatherMost = 2048;                                 // positions of a CTA
-constexpr int kGatherRows = 128;                         // at a time
+constexpr int kGatherWarps = 8, kGatherRows = 64;  // of a CTA; rows at a time
+constexpr int kGatherStages = 2;                   // steps of a warp under way
+constexpr int kGatherMost = 2048;                  // positions of a CTA
 constexpr float kGatherLog2e = 1.4426950408889634f;
 
 // x = a b + x: 16 x 16 times 16 x 8, halves or bfloat16.
@@ -144,14 +144,26 @@ __device__ __forceinline__ void mma_rows16(float (&x)[4], uint32_t a0, uint32_t 
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Shared memory of a CTA.  A step of a warp is kTiles times 16 positions, 4 KB at most.
+template <int D, bool kQuant>
+struct GatherShape {
+    static constexpr int kTiles = kQuant ? 2 : 1, kStep = 16 * kTiles;
+    static constexpr int kPieces = D / 32;                  // of eight query elements a lane
+    static constexpr int kLoads = kQuant ? D / 64 : D / 32;  // of 16 bytes a lane and key
+    uint4 keys[kGatherWarps][kGatherStages][2 * kTiles * kLoads][32];
+    uint4 queries[kGatherRows / 8][kPieces][32];
+    float lse[kGatherRows], factor[kGatherRows];
+    unsigned seen[kGatherRows];  // the window's tokens that a row sees
+    float scale[kGatherWarps][kGatherStages][32];
+    float gathered[kGatherMost];  // by the rows before, where they are more than fit
+};
+
 template <int D, bool kQuant>
 __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsArgs t) {
-    constexpr int kPieces = D / 32;                 // of eight query elements a lane
-    constexpr int kLoads = kQuant ? D / 64 : D / 32;  // of 16 bytes a lane and key
-    __shared__ uint4 queries[kGatherRows / 8][kPieces][32];  // as the lanes take them
-    __shared__ float lse[kGatherRows], factor[kGatherRows];
-    __shared__ unsigned seen[kGatherRows];  // the window's tokens that a row sees
-    __shared__ float gathered[kGatherMost];  // by the rows before, where they are more than fit
+    using S = GatherShape<D, kQuant>;
+    constexpr int kStep = S::kStep, kAll = kStep * kGatherWarps, kKeys = 2 * S::kTiles;
+    extern __shared__ __align__(16) unsigned char smem[];
+    S &sh = *reinterpret_cast<S *>(smem);
     pdl_trigger();
     pdl_wait();
     const AttendArgs &a = t.a;
@@ -165,56 +177,59 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsAr
     const long long line = ((long long)r * a.cache.n_kv_heads + kh) * t.length;
     const int g = lane >> 2, q4 = lane & 3;  // a key's row of the matrix, its quarter of the elements
 
-    // A position a lane: where its key lies, looked up one step ahead of its loads, and
-    // then keys g, g + 8, g + 16 and g + 24 of the warp's 32.
-    struct Place {
-        long long at;
-        float scale;
+    // A position a lane.  The table's entry is loaded a step ahead of the key's copies.
+    auto look_up = [&](int p) {
+        return lane < kStep && p < end
+                   ? __ldg(a.cache.table + (long long)r * a.cache.table_width + (unsigned)p / (unsigned)a.cache.page_size)
+                   : -1;
     };
-    auto look_up = [&](int p) -> Place {
-        Place x = {-1, 1.0f};
-        if (p < end) {
-            int token;
-            const int page = kv_page(a.cache, r, p, &token);
-            if (page < 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
-            else {
-                x.at = kv_offset(a.cache, page, token, kh);
-                if constexpr (kQuant) x.scale = __ldg(a.cache.k_scale + kv_scale_offset(a.cache, page, token, kh));
-            }
-        }
-        return x;
-    };
-    uint4 key[4][kLoads];
-    auto fetch = [&](const Place &x) {
+    // Starts the copies of keys g, g + 8, ... of the step, this lane's quarters; says which
+    // positions have one.
+    auto fetch = [&](int p, int page, int stage) {
+        const bool in = lane < kStep && p < end, good = (unsigned)page < (unsigned)a.cache.n_pages;
+        if (in && !good) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+        const int token = in ? (unsigned)p % (unsigned)a.cache.page_size : 0;
+        const long long at = in && good ? kv_offset(a.cache, page, token, kh) : -1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const long long from = __shfl_sync(kFullMask, x.at, g + 8 * i);
-            const unsigned char *k = a.cache.k + from * (kQuant ? 1 : 2) + q4 * 16;
+        for (int i = 0; i < kKeys; ++i) {
+            const long long from = __shfl_sync(kFullMask, at, g + 8 * i);
+            const unsigned char *k = a.cache.k + (from < 0 ? 0 : from) * (kQuant ? 1 : 2) + q4 * 16;
 #pragma unroll
-            for (int c = 0; c < kLoads; ++c)
-                key[i][c] = from < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(k + c * 64));
+            for (int c = 0; c < S::kLoads; ++c)
+                copy16(smem_addr(&sh.keys[warp][stage][i * S::kLoads + c][lane]), k + c * 64, from >= 0);
         }
+        if constexpr (kQuant)
+            copy4(smem_addr(&sh.scale[warp][stage][lane]),
+                  a.cache.k_scale + (at < 0 ? 0 : kv_scale_offset(a.cache, page, token, kh)), at >= 0);
+        copy16_commit();
+        return __ballot_sync(kFullMask, at >= 0);
     };
-    const int own = first + warp * 32 + lane;  // the lane's first position
-    Place now = look_up(own), next = look_up(own + kGatherStep);
-    fetch(now);
-    auto put = [&](int p, float sum) {
+    auto before = [&](int p) { return p < min(w.P, last) ? t.weights[line + p] : 0.0f; };
+    auto put = [&](int p, float old, float sum) {
         if (p >= last) return;
-        t.weights_out[line + p] = p < w.P ? fmaf(t.decay, t.weights[line + p], sum) : sum;
+        t.weights_out[line + p] = p < w.P ? fmaf(t.decay, old, sum) : sum;
         if (t.positions && p >= w.P && p < w.P + n) t.positions[line + p] = __ldg(t.pos + w.lo + (p - w.P));
     };
 
+    const int own = first + warp * kStep;  // the warp's first position
     for (int row0 = 0; row0 < rows && first < end; row0 += kGatherRows) {
         const int count = min(rows - row0, kGatherRows), tiles = (count + 7) / 8;
+        unsigned there[kGatherStages];  // of the stages' positions, those that have a key
+        int page[kGatherStages + 1];
+#pragma unroll
+        for (int i = 0; i <= kGatherStages; ++i) page[i] = look_up(own + i * kAll + lane);
+#pragma unroll
+        for (int i = 0; i < kGatherStages; ++i) there[i] = fetch(own + i * kAll + lane, page[i], i);
+        int next = page[kGatherStages];
         __syncthreads();
         for (int i = warp; i < tiles * 8; i += kGatherWarps) {
-            const bool there = i < count;
-            const int token = there ? (row0 + i) / G : 0, row = w.lo + token;
-            const int head = kh * G + (there ? (row0 + i) % G : 0);
+            const bool in = i < count;
+            const int token = in ? (row0 + i) / G : 0, row = w.lo + token;
+            const int head = kh * G + (in ? (row0 + i) % G : 0);
             const __nv_bfloat16 *q =
                 static_cast<const __nv_bfloat16 *>(a.q) + (long long)row * a.ld_q + (long long)head * D;
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (there && lane < D / 8) v = __ldg(reinterpret_cast<const uint4 *>(q) + lane);
+            if (in && lane < D / 8) v = __ldg(reinterpret_cast<const uint4 *>(q) + lane);
             float by = 1.0f;
             if constexpr (kQuant) {
                 const unsigned e[4] = {v.x, v.y, v.z, v.w};
@@ -239,57 +254,72 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsAr
             if (lane < D / 8) {
                 const int quarter = kQuant ? lane / 2 % 4 : lane % 4;
                 const int piece = kQuant ? lane / 8 * 2 + lane % 2 : lane / 4;
-                queries[i / 8][piece][i % 8 * 4 + quarter] = v;
+                sh.queries[i / 8][piece][i % 8 * 4 + quarter] = v;
             }
             if (lane == 0) {
-                lse[i] = there ? t.lse[(long long)row * a.n_q_heads + head] : INFINITY;
-                factor[i] = by;
-                seen[i] = there ? ancestors_of(a, row, token, len) : 0;
+                sh.lse[i] = in ? t.lse[(long long)row * a.n_q_heads + head] : INFINITY;
+                sh.factor[i] = by;
+                sh.seen[i] = in ? ancestors_of(a, row, token, len) : 0;
             }
         }
         __syncthreads();
-        for (int p0 = first + warp * 32; p0 < end; p0 += kGatherWarps * 32) {
-            const int p = p0 + lane;
-            float scale[4];
+        int stage = 0;
+        for (int p0 = own; p0 < end; p0 += kAll) {
+            const float old = before(p0 + lane);
+            copy16_wait_but<kGatherStages - 1>();
+            __syncwarp();  // (the scales are other lanes' copies)
+            uint4 key[kKeys][S::kLoads];
+            float scale[kKeys];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) scale[i] = __shfl_sync(kFullMask, now.scale, g + 8 * i);
-            const bool in_window = p0 + 32 > w.P;
-            float sum[4] = {};
+            for (int i = 0; i < kKeys; ++i) {
+#pragma unroll
+                for (int c = 0; c < S::kLoads; ++c) key[i][c] = sh.keys[warp][stage][i * S::kLoads + c][lane];
+                scale[i] = kQuant ? sh.scale[warp][stage][g + 8 * i] : 1.0f;
+            }
+            __syncwarp();
+            const unsigned now = there[0];
+#pragma unroll
+            for (int i = 0; i + 1 < kGatherStages; ++i) there[i] = there[i + 1];
+            there[kGatherStages - 1] = fetch(p0 + kGatherStages * kAll + lane, next, stage);
+            next = look_up(p0 + (kGatherStages + 1) * kAll + lane);
+            if (++stage == kGatherStages) stage = 0;
+            const bool in_window = p0 + kStep > w.P;
+            float sum[kKeys] = {};
             for (int tile = 0; tile < tiles; ++tile) {
-                float x[2][4] = {};
+                float y[S::kTiles][4] = {};
 #pragma unroll
-                for (int c = 0; c < kLoads; ++c) {
+                for (int c = 0; c < S::kLoads; ++c) {
                     if constexpr (kQuant) {
-                        const uint4 b0 = queries[tile][2 * c][lane], b1 = queries[tile][2 * c + 1][lane];
+                        const uint4 b0 = sh.queries[tile][2 * c][lane], b1 = sh.queries[tile][2 * c + 1][lane];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < S::kTiles; ++i) {
                             const uint4 u0 = eight_halves(make_uint2(key[2 * i][c].x, key[2 * i][c].y));
                             const uint4 v0 = eight_halves(make_uint2(key[2 * i + 1][c].x, key[2 * i + 1][c].y));
-                            mma_rows16<true>(x[i], u0.x, v0.x, u0.y, v0.y, b0.x, b0.y);
-                            mma_rows16<true>(x[i], u0.z, v0.z, u0.w, v0.w, b0.z, b0.w);
+                            mma_rows16<true>(y[i], u0.x, v0.x, u0.y, v0.y, b0.x, b0.y);
+                            mma_rows16<true>(y[i], u0.z, v0.z, u0.w, v0.w, b0.z, b0.w);
                             const uint4 u1 = eight_halves(make_uint2(key[2 * i][c].z, key[2 * i][c].w));
                             const uint4 v1 = eight_halves(make_uint2(key[2 * i + 1][c].z, key[2 * i + 1][c].w));
-                            mma_rows16<true>(x[i], u1.x, v1.x, u1.y, v1.y, b1.x, b1.y);
-                            mma_rows16<true>(x[i], u1.z, v1.z, u1.w, v1.w, b1.z, b1.w);
+                            mma_rows16<true>(y[i], u1.x, v1.x, u1.y, v1.y, b1.x, b1.y);
+                            mma_rows16<true>(y[i], u1.z, v1.z, u1.w, v1.w, b1.z, b1.w);
                         }
                     } else {
-                        const uint4 b = queries[tile][c][lane];
+                        const uint4 b = sh.queries[tile][c][lane];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int i = 0; i < S::kTiles; ++i) {
                             const uint4 u = key[2 * i][c], v = key[2 * i + 1][c];
-                            mma_rows16<false>(x[i], u.x, v.x, u.y, v.y, b.x, b.y);
-                            mma_rows16<false>(x[i], u.z, v.z, u.w, v.w, b.z, b.w);
+                            mma_rows16<false>(y[i], u.x, v.x, u.y, v.y, b.x, b.y);
+                            mma_rows16<false>(y[i], u.z, v.z, u.w, v.w, b.z, b.w);
                         }
                     }
                 }
                 // scores of keys g + 8 i with rows 2 q4 and 2 q4 + 1 of the tile
                 const int at_row = tile * 8 + 2 * q4;
-                const float2 base = *reinterpret_cast<const float2 *>(&lse[at_row]);
-                const float2 by = *reinterpret_cast<const float2 *>(&factor[at_row]);
-                const uint2 sees = *reinterpret_cast<const uint2 *>(&seen[at_row]);
+                const float2 base = *reinterpret_cast<const float2 *>(&sh.lse[at_row]);
+                const float2 by = *reinterpret_cast<const float2 *>(&sh.factor[at_row]);
+                const uint2 sees = *reinterpret_cast<const uint2 *>(&sh.seen[at_row]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float y0 = x[i / 2][i % 2 * 2], y1 = x[i / 2][i % 2 * 2 + 1];
+                for (int i = 0; i < kKeys; ++i) {
+                    float y0 = y[i / 2][i % 2 * 2], y1 = y[i / 2][i % 2 * 2 + 1];
                     if constexpr (kQuant) y0 *= by.x * scale[i], y1 *= by.y * scale[i];
                     // (the difference from lse before the change of base: where a term
                     // counts, it is small)
@@ -305,26 +335,25 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsAr
             }
             float mine = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kKeys; ++i) {
                 sum[i] += __shfl_xor_sync(kFullMask, sum[i], 1);
                 sum[i] += __shfl_xor_sync(kFullMask, sum[i], 2);
                 const float of = __shfl_sync(kFullMask, sum[i], lane % 8 * 4);
                 if (lane / 8 == i) mine = of;
             }
-            if (now.at < 0) mine = 0.0f;
-            if (row0 > 0) mine += gathered[p - first];
-            if (row0 + kGatherRows < rows) gathered[p - first] = mine;
-            else put(p, mine);
-            // (the rows after these begin with the first positions again)
-            const bool more = p0 + kGatherStep < end;
-            now = more ? next : look_up(own);
-            next = look_up(more ? p + 2 * kGatherStep : own + kGatherStep);
-            if (more || row0 + kGatherRows < rows) fetch(now);
+            if (!(now >> lane & 1)) mine = 0.0f;
+            const int p = p0 + lane;
+            if (lane < kStep) {
+                if (row0 > 0) mine += sh.gathered[p - first];
+                if (row0 + kGatherRows < rows) sh.gathered[p - first] = mine;
+                else put(p, old, mine);
+            }
         }
+        copy16_wait();
     }
     // positions of which no warp had one: all of them without rows
-    for (int p = first + tid; p < last; p += kGatherStep)
-        if (rows == 0 || p - lane >= end) put(p, 0.0f);
+    for (int p = first + tid; p < last; p += kGatherWarps * 32)
+        if (first + (p - first) / kStep * kStep >= end) put(p, before(p), 0.0f);
 }
 
 // -------------------------------------------------------------- eviction
@@ -552,12 +581,16 @@ bool gather_fits(const AttendArgs &a, int dtype, const dspark_kv_cache &c) {
 
 template <int D, bool kQuant>
 cudaError_t launch_gather(const WeightsArgs &t, cudaStream_t stream) {
+    using S = GatherShape<D, kQuant>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(weights_kernel<D, kQuant>), sizeof(S),
+                                29 + (D == 128) + 2 * kQuant);
+    if (e != cudaSuccess) return e;
     // some four times as many CTAs as run at a time, of 256 to 2048 positions
     const long long all = (long long)t.length * t.a.cache.n_kv_heads * t.a.B / (8 * sm_count());
     WeightsArgs u = t;
-    u.span = (int)min(max((all + kGatherStep - 1) / kGatherStep, 1ll), (long long)(kGatherMost / kGatherStep)) * kGatherStep;
+    u.span = (int)min(max((all + 255) / 256, 1ll), (long long)(kGatherMost / 256)) * 256;
     const dim3 grid((t.length + u.span - 1) / u.span, t.a.cache.n_kv_heads, t.a.B);
-    return launch_pdl(weights_kernel<D, kQuant>, grid, dim3(kGatherWarps * 32), 0, stream, u);
+    return launch_pdl(weights_kernel<D, kQuant>, grid, dim3(kGatherWarps * 32), sizeof(S), stream, u);
 }
 
 template <typename T>

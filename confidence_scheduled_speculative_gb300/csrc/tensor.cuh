@@ -110,6 +110,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
                  : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0)
+                 : "memory");
+}
+// A group of this thread's copies so far; and the end of all groups but the last kBut.
+__device__ __forceinline__ void copy16_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kBut>
+__device__ __forceinline__ void copy16_wait_but() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kBut) : "memory");
+}
 // Ends this thread's copies so far.
 __device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
