@@ -221,6 +221,11 @@ EVICT = [
     dict(lens=[300, 20, 299], keep=20, recent=0, kind="e4m3", D=128, page=64),
     dict(lens=[1023, 1024, 1025, 2500], keep=1000, recent=100, hkv=1, page=128),
     dict(lens=[5000, 33000], keep=4096, recent=1024, hkv=1, page=64, kind="e4m3"),
+    # two and eight CTAs a line, and longer than they hold
+    dict(lens=[20000, 17, 16385], keep=9000, recent=50, D=64, page=64),
+    dict(lens=[100000, 131040], keep=50000, recent=4096, hkv=1, page=128, kind="e4m3"),
+    dict(lens=[70001], keep=69990, recent=5, hkv=1, page=64, ties=True),
+    dict(lens=[140000, 500], keep=64000, recent=64000, hkv=1, page=64, kind="e4m3"),
     dict(lens=[700, 90], keep=80, recent=8, ties=True),
     dict(lens=[3000], keep=1500, recent=10, ties=True, spread=0.5),
     dict(lens=[300, 120], keep=64, recent=16, layout="heads", hkv=3),
