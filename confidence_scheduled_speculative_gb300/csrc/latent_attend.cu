@@ -26,9 +26,9 @@
 //   of the elements of all 128 as values.  (With 64 positions a step the scores take as long
 //   as with 128.)  An entry comes once for each product, a third of the keys, or half of the
 //   values, at a time, into buffers that the products of the tile before are just done with.
-//   One warp copies (TMA; asking L2 for later tiles beside that takes longer), one of the
-//   first CTA issues both products, four do the softmax, a thread half a row's positions,
-//   and four bring the next job's queries.  The tiles of all jobs are dealt evenly to the
+//   Four warps copy (TMA: a box is 64 elements of up to 64 tokens of a page, and issuing
+//   one takes a warp a hundred cycles), one of the first CTA issues both products, four do
+//   the softmax, a thread half a row's positions, and two bring the next job's queries.  The tiles of all jobs are dealt evenly to the
 //   pairs, so jobs are split along the positions where there are few, and
 //   latent_join_kernel adds the parts in a fixed order.
 
@@ -148,7 +148,8 @@ constexpr int kWeightsAt = kValueAt + kValueParts * kValueBytes;
 constexpr int kControlAt = kWeightsAt + 2 * kChunkBytes;
 constexpr int kLatentSmem = kControlAt + 3072;
 constexpr int kOutCol = 0, kScoreCol = 256;  // columns of tensor memory
-constexpr int kLatentThreads = 320, kCopyWarp = 8, kMatrixWarp = 9;
+constexpr int kLatentThreads = 352, kQueryWarp = 4, kMatrixWarp = 6, kCopyWarp = 7;
+constexpr int kCopyWarps = 4;  // two for keys, two for values
 constexpr int kLatentJobCost = 2;  // of a job's begin and end, in tiles
 constexpr int kLatentDesc = 8;     // words about a split job, for the join
 
@@ -254,24 +255,25 @@ __device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBe
     const AttendArgs &a = t.a;
     const int tid = threadIdx.x, cta = blockIdx.x, pairs = gridDim.x / 2;
     const int per = (a.B + kLatentThreads - 1) / kLatentThreads;
-    long long mine[3] = {}, sum[3];  // teams of 1, 2 and 4
     LatentRequest q = {};
     auto job = [&]() { return t.whole ? 1 : q.tiles + kLatentJobCost; };
-    for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
-        if (to_latent(t, load_window(a, r), &q, cta == 0))
-#pragma unroll
-            for (int g = 0; g < 3; ++g) mine[g] += (long long)job() * ((q.row_tiles + (1 << g) - 1) >> g);
-    int best = 0;
-    long long before = block_exclusive_scan<long long>(mine[0], scan, &sum[0]);
-    if (!t.whole)
-#pragma unroll
-        for (int g = 1; g < 3; ++g) {
-            const long long at = block_exclusive_scan<long long>(mine[g], scan, &sum[g]);
-            if (sum[g] / (pairs >> g) * 8 <= sum[0] / pairs * 9) best = g, before = at;
+    // (rolled up: code that runs once is fetched as slowly as it is long)
+    int size = 1;
+    long long own = 0, before = 0, T = 0, alone = 0;
+#pragma unroll 1
+    for (int g = 1; g <= (t.whole ? 1 : min(4, pairs)); g *= 2) {
+        long long mine = 0, sum;
+#pragma unroll 1
+        for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
+            if ((per == 1 && g > 1) ? q.tiles > 0 : to_latent(t, load_window(a, r), &q, cta == 0 && g == 1))
+                mine += (long long)job() * ((q.row_tiles + g - 1) / g);
+        const long long at = block_exclusive_scan<long long>(mine, scan, &sum);
+        if (g == 1) alone = sum;
+        if (g == 1 || div_nonneg(sum, pairs / g) * 8 <= div_nonneg(alone, pairs) * 9) {
+            size = g;
+            own = mine, before = at, T = sum;
         }
-    const int size = 1 << best;
-    const long long own = best == 0 ? mine[0] : best == 1 ? mine[1] : mine[2];
-    const long long T = best == 0 ? sum[0] : best == 1 ? sum[1] : sum[2];
+    }
     const int n = (int)min((long long)(pairs / size), t.whole ? T : (T + kLatentJobCost + 1) / (kLatentJobCost + 2));
     if (tid == 0 && !t.whole) {
         t.desc[cta * kLatentDesc] = 0;
@@ -343,7 +345,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
             mbar_init(smem_addr(&ctl.value_seen[i]), 1);
         }
-        mbar_init(smem_addr(&ctl.q_full), 8);
+        mbar_init(smem_addr(&ctl.q_full), 4);
         mbar_init(smem_addr(&ctl.o_free), 8);
         mbar_init(smem_addr(&ctl.q_empty), 1);
         mbar_init(smem_addr(&ctl.drain), 1);
@@ -352,6 +354,8 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
         fence_mbar_init();
         prefetch_map(&map);
     }
+    __syncwarp();
+    cluster_arrive_all();  // the barriers are there
     if (warp == kMatrixWarp) tmem_alloc_pair(smem_addr(&ctl.tmem), 512);
     pdl_wait();
     pdl_trigger();
@@ -363,11 +367,12 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             __syncwarp();
             tmem_free_pair(*(volatile unsigned *)&ctl.tmem, 512);
         }
+        cluster_wait_all();
         cluster_sync();
         return;
     }
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers are there
+    cluster_wait_all();
     tmem_fence_after();
     const uint32_t tmem = ctl.tmem;
     volatile int *abort = &ctl.abort;
@@ -382,16 +387,24 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
     const int hq = a.n_q_heads;
     unsigned done = 0, seg = 0;  // tiles and segments so far
 
-    if (warp == kCopyWarp) {
-        // ------------------------------------------------ copy warp
-        // Of a tile's boxes a CTA copies half as keys and all, of its elements, as values.  The
-        // table's entries of `per` tiles are looked up at a time, a box a lane, one such
-        // batch ahead.
+    if (warp >= kCopyWarp) {
+        // ----------------------------------------------- copy warps
+        // Of a tile's boxes a CTA copies half as keys and all, of its elements, as values:
+        // two warps every other box of nine parts each of the keys', two one half each of
+        // the values'.  The table's entries of `per` tiles are looked up at a time, a box a
+        // lane, one such batch ahead.
+        const int which = warp - kCopyWarp, half = which & 1;
+        const bool keys = which < 2;
         const int boxes = kStep / t.box, key_boxes = boxes / 2, per = 32 / boxes;
-        const int key_box = rank * key_boxes + lane / 3, value_box = lane >> 1;
-        const bool key_lane = lane < 3 * key_boxes, value_lane = value_box < boxes;
-        const uint32_t key_dst = base + kKeyAt + lane % 3 * kChunkBytes + lane / 3 * t.box * 128;
-        const uint32_t value_dst = base + kValueAt + (lane & 1) * 2 * kChunkBytes + value_box * t.box * 128;
+        // boxes that this lane copies from: of keys every other one, in parts of three (one
+        // box: the first warp two of the three, the second the other)
+        const int split = key_boxes > 1 ? 3 : 2 - half, chunk = key_boxes > 1 ? lane % 3 : 2 * half + lane;
+        const int place = key_boxes > 1 ? 2 * (lane / 3) + half : 0;
+        const int box = keys ? rank * key_boxes + place : lane >> 1;
+        const bool mine = keys ? key_boxes > 1 ? place < key_boxes : lane < split : box < boxes;
+        const uint32_t dst = keys ? base + kKeyAt + chunk * kChunkBytes + place * t.box * 128
+                                  : base + kValueAt + half * kValueBytes + (lane & 1) * 2 * kChunkBytes +
+                                        box * t.box * 128;
         while (ok && walk.next(t, &s)) {
             const int n = s.q.P + s.q.len, from = s.first * kStep;
             struct Batch {
@@ -407,54 +420,43 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             };
             now = look_up(0);
             next = look_up(per);
-            Batch value = {};
-            // in the order of use: K0, K1, V0, K2, V1, ..., V(n-1)
-            for (int i = 0; i <= s.count; ++i) {
-                if (i < s.count) {
-                    const int j = i % per;
-                    if (j == 0 && i > 0) {
-                        now = next;
-                        next = look_up(i + per);
-                    }
-                    int page = __shfl_sync(kFullMask, now.page, (j * boxes + key_box) % 32);
-                    const int token = __shfl_sync(kFullMask, now.token, (j * boxes + key_box) % 32);
-                    // a page outside the pool, as past the request's end, arrives as zeros
-                    if ((unsigned)page >= (unsigned)a.cache.n_pages) {
-                        if (key_lane && from + i * kStep + key_box * t.box < n)
-                            flag(a.status, DSPARK_STATUS_BAD_INDEX);
-                        page = a.cache.n_pages;
-                    }
+            for (int i = 0; i < s.count; ++i) {
+                const int j = i % per;
+                if (j == 0 && i > 0) {
+                    now = next;
+                    next = look_up(i + per);
+                }
+                int page = __shfl_sync(kFullMask, now.page, (j * boxes + box) % 32);
+                const int token = __shfl_sync(kFullMask, now.token, (j * boxes + box) % 32);
+                // a page outside the pool, as past the request's end, arrives as zeros
+                if ((unsigned)page >= (unsigned)a.cache.n_pages) {
+                    if (mine && from + i * kStep + box * t.box < n) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+                    page = a.cache.n_pages;
+                }
+                if (keys) {
 #pragma unroll 1
                     for (int part = 0; part < kKeyParts; ++part) {
                         if (!wait(&ctl.key_empty[part], done + i + 1)) break;
-                        if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.key_full[part]), 2 * kKeyBytes);
+                        if (rank == 0 && half == 0 && lane == 0)
+                            mbar_expect(smem_addr(&ctl.key_full[part]), 2 * kKeyBytes);
                         __syncwarp();
-                        if (key_lane)
-                            tma_load_4d_pair(key_dst + part * kKeyBytes, &map, (3 * part + lane % 3) * 64, token, 0,
-                                             page, first_cta(&ctl.key_full[part]));
+                        if (mine)
+                            tma_load_4d_pair(dst + part * kKeyBytes, &map, (3 * part + chunk) * 64, token, 0, page,
+                                             first_cta(&ctl.key_full[part]));
                     }
-                    if (!ok) break;
+                } else {
+                    if (!wait(&ctl.value_empty[half], done + i + 1)) break;
+                    if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.value_full[half]), 2 * kValueBytes);
+                    __syncwarp();
+                    if (mine)
+                        tma_load_4d_pair(dst, &map, (4 * rank + 2 * half + (lane & 1)) * 64, token, 0, page,
+                                         first_cta(&ctl.value_full[half]));
                 }
-                if (i > 0) {
-#pragma unroll 1
-                    for (int part = 0; part < kValueParts; ++part) {
-                        if (!wait(&ctl.value_empty[part], done + i)) break;
-                        if (rank == 0 && lane == 0) mbar_expect(smem_addr(&ctl.value_full[part]), 2 * kValueBytes);
-                        __syncwarp();
-                        if (value_lane)
-                            tma_load_4d_pair(value_dst + part * kValueBytes, &map,
-                                             (4 * rank + 2 * part + (lane & 1)) * 64, value.token, 0, value.page,
-                                             first_cta(&ctl.value_full[part]));
-                    }
-                    if (!ok) break;
-                }
-                const int at = (i % per * boxes + value_box) % 32;
-                value = {__shfl_sync(kFullMask, now.page, at), __shfl_sync(kFullMask, now.token, at)};
-                if ((unsigned)value.page >= (unsigned)a.cache.n_pages) value.page = a.cache.n_pages;
+                if (!ok) break;
             }
             done += s.count;
         }
-        if (!ok && rank == 0 && lane == 0) {
+        if (!ok && rank == 0 && which == 0 && lane == 0) {
             // copies still under way write the pair's buffers (each wait ends by itself; the
             // CTAs leave together)
             for (int p = 0; p < 2; ++p) {
@@ -484,7 +486,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                 if (!wait(&ctl.p_ready[b], tile >> 1)) return;
                 tmem_fence_after();
                 if (leader) {
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < kValueParts; ++h) {
 #pragma unroll
                         for (int k = 0; k < kStep / 16; ++k)
@@ -502,14 +504,14 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                 for (int i = 0; i < count; ++i) {
                     // (the scores of tile - 2 have been read)
                     const unsigned tile = done + i, b = tile & 1;
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < kKeyParts; ++part) {
                         if (!wait(&ctl.key_full[part], tile)) break;
                         tmem_fence_after();
                         if (leader) {
 #pragma unroll
                             for (int k = 0; k < 12; ++k) {
-                                const int at = (3 * part + k / 4) * kChunkBytes + k % 4 * 32;
+                                const int at = 3 * part * kChunkBytes + (k / 4 * kChunkBytes + k % 4 * 32);
                                 mma_pair_ss(utmem + kScoreCol + b * 64, desc_q + (at >> 4), desc_key + (at >> 4),
                                             score_word, part > 0 || k > 0);
                             }
@@ -538,10 +540,10 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             }
             __syncwarp();
         }
-    } else if (warp >= 4) {
+    } else if (warp >= kQueryWarp) {
         // --------------------------------------------- query warps
-        // Two threads a row, which bring every other of its parts.
-        const int m = (tid - 128) >> 1, half = tid & 1;
+        // A thread a row.
+        const int m = tid - kQueryWarp * 32;
         while (ok && walk.next(t, &s)) {
             const int row = s.row_tile * kPairRows + rank * kRows + m;
             const bool there = row < s.q.len * hq;
@@ -550,7 +552,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                                                              (s.q.row0 + token) * a.ld_q + (long long)head * kEntry);
             if (seg > 0 && !wait(&ctl.q_empty, seg - 1)) break;
 #pragma unroll 4
-            for (int p = half; p < 8 * kChunks; p += 2)
+            for (int p = 0; p < 8 * kChunks; ++p)
                 copy16(base + p / 8 * kChunkBytes + chunk_piece(m, p % 8), q + p, there);
             copy16_wait();
             fence_async_proxy();
