@@ -28,7 +28,7 @@
 //   values, at a time, into buffers that the products of the tile before are just done with.
 //   Four warps copy (TMA: a box is 64 elements of up to 64 tokens of a page, and issuing
 //   one takes a warp a hundred cycles), one of the first CTA issues both products, four do
-//   the softmax, a thread half a row's positions, and two bring the next job's queries.  The tiles of all jobs are dealt evenly to the
+//   the softmax, a thread half a row's positions, and three bring the next job's queries.  The tiles of all jobs are dealt evenly to the
 //   pairs, so jobs are split along the positions where there are few, and
 //   latent_join_kernel adds the parts in a fixed order.
 
@@ -148,8 +148,9 @@ constexpr int kWeightsAt = kValueAt + kValueParts * kValueBytes;
 constexpr int kControlAt = kWeightsAt + 2 * kChunkBytes;
 constexpr int kLatentSmem = kControlAt + 3072;
 constexpr int kOutCol = 0, kScoreCol = 256;  // columns of tensor memory
-constexpr int kLatentThreads = 352, kQueryWarp = 4, kMatrixWarp = 6, kCopyWarp = 7;
-constexpr int kCopyWarps = 4;  // two for keys, two for values
+constexpr int kLatentThreads = 384, kQueryWarp = 4, kMatrixWarp = 7, kCopyWarp = 8;
+constexpr int kQueryWarps = kMatrixWarp - kQueryWarp, kCopyWarps = 4;  // of these two for keys, two for values
+static_assert(kLatentThreads == 32 * (kCopyWarp + kCopyWarps), "roles");
 constexpr int kLatentJobCost = 2;  // of a job's begin and end, in tiles
 constexpr int kLatentDesc = 8;     // words about a split job, for the join
 
@@ -250,7 +251,7 @@ struct LatentWalk {
 //   Larger teams read less from HBM and leave members idle where the row tiles are no
 // multiple of them: the largest is taken whose members' steps are at most an eighth more
 // than those of pairs alone.
-__device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBegin *begin, long long *scan,
+__device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBegin *begin, int *scan,
                                              Deal *deal, Team *team) {
     const AttendArgs &a = t.a;
     const int tid = threadIdx.x, cta = blockIdx.x, pairs = gridDim.x / 2;
@@ -259,22 +260,22 @@ __device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBe
     auto job = [&]() { return t.whole ? 1 : q.tiles + kLatentJobCost; };
     // (rolled up: code that runs once is fetched as slowly as it is long)
     int size = 1;
-    long long own = 0, before = 0, T = 0, alone = 0;
+    int own = 0, before = 0, T = 0, alone = 0;  // units: a call has fewer than 2^31
 #pragma unroll 1
     for (int g = 1; g <= (t.whole ? 1 : min(4, pairs)); g *= 2) {
-        long long mine = 0, sum;
+        int mine = 0, sum;
 #pragma unroll 1
         for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
             if ((per == 1 && g > 1) ? q.tiles > 0 : to_latent(t, load_window(a, r), &q, cta == 0 && g == 1))
-                mine += (long long)job() * ((q.row_tiles + g - 1) / g);
-        const long long at = block_exclusive_scan<long long>(mine, scan, &sum);
+                mine += job() * ((q.row_tiles + g - 1) / g);
+        const int at = block_exclusive_scan<int>(mine, scan, &sum);
         if (g == 1) alone = sum;
-        if (g == 1 || div_nonneg(sum, pairs / g) * 8 <= div_nonneg(alone, pairs) * 9) {
+        if (g == 1 || sum / (pairs / g) * 8ll <= alone / pairs * 9ll) {
             size = g;
             own = mine, before = at, T = sum;
         }
     }
-    const int n = (int)min((long long)(pairs / size), t.whole ? T : (T + kLatentJobCost + 1) / (kLatentJobCost + 2));
+    const int n = min(pairs / size, t.whole ? T : (T + kLatentJobCost + 1) / (kLatentJobCost + 2));
     if (tid == 0 && !t.whole) {
         t.desc[cta * kLatentDesc] = 0;
         t.desc[cta * kLatentDesc + 7] = -1;
@@ -282,22 +283,22 @@ __device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBe
     *team = {size, cta / 2 % size, cta / 2 / size};
     if (team->at >= n) return false;
     deal->n = n;
-    deal->each = div_nonneg(T, n);
-    deal->rest = (int)(T - deal->each * n);
-    const long long lo = deal->first(team->at), hi = deal->first(team->at + 1);
-    if (lo >= before && lo < before + own) {
-        long long from = before;
+    deal->each = T / n;
+    deal->rest = T % n;
+    const int lo = (int)deal->first(team->at), hi = (int)deal->first(team->at + 1);
+    if (lo >= before && lo - before < own) {
+        int from = before;
         for (int r = tid * per;; ++r) {
             if (per > 1 && !to_latent(t, load_window(a, r), &q, false)) continue;
-            const long long units = (long long)job() * ((q.row_tiles + size - 1) / size);
-            if (lo >= from + units) {
+            const int units = job() * ((q.row_tiles + size - 1) / size);
+            if (lo - from >= units) {
                 from += units;
                 continue;
             }
             begin->r = r;
-            begin->group = (int)div_nonneg(lo - from, job());
-            begin->unit = (int)(lo - from - (long long)begin->group * job());
-            begin->left = (int)(hi - lo);
+            begin->group = (lo - from) / job();
+            begin->unit = (lo - from) % job();
+            begin->left = hi - lo;
             begin->q = q;
             break;
         }
@@ -315,7 +316,7 @@ struct alignas(16) LatentControl {
     unsigned nonfinite[4];  // window tokens whose values were zeroed in either CTA, by segment
     int abort;
     LatentBegin begin;
-    long long scan[40];
+    int scan[40];
     float top[2][2][kRows];  // [tile's parity][half of the positions]
     float sum[2][kRows];
 };
@@ -345,7 +346,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
             mbar_init(smem_addr(&ctl.o_done[i]), 1);
             mbar_init(smem_addr(&ctl.value_seen[i]), 1);
         }
-        mbar_init(smem_addr(&ctl.q_full), 4);
+        mbar_init(smem_addr(&ctl.q_full), 2 * kQueryWarps);
         mbar_init(smem_addr(&ctl.o_free), 8);
         mbar_init(smem_addr(&ctl.q_empty), 1);
         mbar_init(smem_addr(&ctl.drain), 1);
@@ -542,18 +543,25 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
         }
     } else if (warp >= kQueryWarp) {
         // --------------------------------------------- query warps
-        // A thread a row.
-        const int m = tid - kQueryWarp * 32;
+        // A warp a row at a time, 16 bytes a lane.
         while (ok && walk.next(t, &s)) {
-            const int row = s.row_tile * kPairRows + rank * kRows + m;
-            const bool there = row < s.q.len * hq;
-            const int token = there ? row / hq : 0, head = there ? row % hq : 0;
-            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                             (s.q.row0 + token) * a.ld_q + (long long)head * kEntry);
             if (seg > 0 && !wait(&ctl.q_empty, seg - 1)) break;
+            const int rows = s.q.len * hq, first = s.row_tile * kPairRows + rank * kRows;
+            int row = first + warp - kQueryWarp, token = row / hq, head = row - token * hq;
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + s.q.row0 * a.ld_q + 8 * lane;
+            uint32_t dst = base + lane / 8 * kChunkBytes + (warp - kQueryWarp) * 128;
 #pragma unroll 4
-            for (int p = 0; p < 8 * kChunks; ++p)
-                copy16(base + p / 8 * kChunkBytes + chunk_piece(m, p % 8), q + p, there);
+            for (int m = warp - kQueryWarp; m < kRows; m += kQueryWarps) {
+                const bool there = row < rows;
+                const __nv_bfloat16 *from = q + (there ? token * a.ld_q + (long long)head * kEntry : 0);
+                const uint32_t at = dst + ((lane % 8 ^ (m & 7)) << 4);
+                copy16(at, from, there);
+                copy16(at + 4 * kChunkBytes, from + 256, there);
+                if (lane < 8) copy16(at + 8 * kChunkBytes, from + 512, there);
+                dst += kQueryWarps * 128;
+                row += kQueryWarps;
+                for (head += kQueryWarps; head >= hq; head -= hq) ++token;
+            }
             copy16_wait();
             fence_async_proxy();
             __syncwarp();
@@ -912,7 +920,9 @@ bool latent_tensor_fits(const AttendArgs &a, int dtype, const dspark_latent_cach
     for (int64_t s : {c.token_stride, c.page_stride})
         if (s % 8 || s < 1 || s * 2 >= (1ll << 40)) return false;
     return aligned(c.data, 16) && aligned(a.q, 16) && aligned(a.out, 16) && a.ld_q % 8 == 0 && a.ld_out % 8 == 0 &&
-           a.n_q_heads <= (1 << 20);
+           // (the dealing counts tiles of 128 positions and 128 rows in 31 bits)
+           ((long long)c.table_width * c.page_size / kStep + kLatentJobCost + 1) *
+                   ((long long)DSPARK_MAX_WINDOW * a.n_q_heads / kPairRows + 1) * a.B < (1ll << 31);
 }
 
 // How many pairs of CTAs run at a time on the current device (they sit in one cluster of
