@@ -758,6 +758,12 @@ namespace {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Whether `out` is `in` itself, or shares none of its n words.
+bool same_or_apart(const void *in, const void *out, int64_t n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(in), y = reinterpret_cast<uintptr_t>(out), bytes = 4 * n;
+    return x == y || x >= y + bytes || y >= x + bytes;
+}
+
 // Entries that can move: as many as are kept, or as lie behind them.
 int most_moves(int keep, int length) { return length > keep ? min(keep, length - keep) : 0; }
 
@@ -842,6 +848,7 @@ extern "C" int dspark_attention_weights(const void *q, int64_t ld_q, int32_t dty
     if (ld_q < (int64_t)n_q_heads * cache->head_dim || (pos != nullptr) != (positions != nullptr))
         return DSPARK_ERR_INVALID_ARG;
     if (!(scale - scale == 0.0f) || !(decay - decay == 0.0f)) return DSPARK_ERR_INVALID_ARG;
+    if (!same_or_apart(weights, weights_out, (int64_t)B * cache->n_kv_heads * length)) return DSPARK_ERR_INVALID_ARG;
     if (n_q_heads > 65535 || B > 65535) return DSPARK_ERR_UNSUPPORTED;
     WeightsArgs t;
     AttendArgs &a = t.a;
@@ -895,6 +902,9 @@ extern "C" int dspark_kv_evict(const dspark_kv_cache *cache, const int32_t *lens
     if (rc != DSPARK_OK) return rc;
     if (!lens || !now || !weights || !weights_out || !positions || !positions_out || !new_lens || !status ||
         B < 1 || B > cache->n_requests || length < 1 || keep < 1 || recent < 0 || recent > keep)
+        return DSPARK_ERR_INVALID_ARG;
+    const int64_t words = (int64_t)B * cache->n_kv_heads * length;
+    if (!same_or_apart(weights, weights_out, words) || !same_or_apart(positions, positions_out, words))
         return DSPARK_ERR_INVALID_ARG;
     if (cache->n_kv_heads > 65535 || B > 65535 || length > (1 << 30)) return DSPARK_ERR_UNSUPPORTED;
     if (!workspace || !aligned(workspace, 256) ||

@@ -135,16 +135,15 @@ inline bool rows_overlap(const void *a, int64_t ld_a, int64_t bytes_a, const voi
                          int64_t bytes_b, int64_t rows) {
     const int64_t x = (int64_t)reinterpret_cast<uintptr_t>(a), y = (int64_t)reinterpret_cast<uintptr_t>(b);
     if (y >= x + (rows - 1) * ld_a + bytes_a || x >= y + (rows - 1) * ld_b + bytes_b) return false;
-    // the rows of b that begin last before, and first after, the begin of a row of a
-    // (with equal strides one row of a stands for all)
+    // the row of b that begins last before the begin of a row of a, and those that begin in
+    // it (with equal strides one row of a stands for all)
     for (int64_t i = 0; i < (ld_a == ld_b ? 1 : rows); ++i) {
         const int64_t from = x + i * ld_a - y;
-        const int64_t first = from / ld_b - (from % ld_b < 0);
-        for (int64_t j = first; j <= first + 1; ++j) {
-            const bool there = ld_a == ld_b ? j > -rows && j < rows : j >= 0 && j < rows;
-            const int64_t off = j * ld_b - from;  // from the begin of a's row to that of b's
-            if (there && off < bytes_a && off > -bytes_b) return true;
-        }
+        const int64_t least = ld_a == ld_b ? 1 - rows : 0;
+        int64_t j = from / ld_b - (from % ld_b < 0);
+        if (j < least) j = least;
+        for (; j < rows && j * ld_b - from < bytes_a; ++j)
+            if (j * ld_b - from > -bytes_b) return true;
     }
     return false;
 }

@@ -927,7 +927,7 @@ DSPARK_API int dspark_prompt_attention(const void *q, int64_t ld_q, const void *
  *   counts       device [B] (nullable: whole windows): how many of a window's rows
  *                count (the accepted ones: commit_lens)
  *   decay        finite
- *   weights, weights_out   [B, n_kv_heads, length] fp32, may be the same
+ *   weights, weights_out   [B, n_kv_heads, length] fp32, the same or apart
  *   pos, positions         device [max_rows] and [B, n_kv_heads, length] int32,
  *                both or neither
  * Sums are held in 32 bits and their order is fixed.  What a row does not see has no
@@ -935,7 +935,8 @@ DSPARK_API int dspark_prompt_attention(const void *q, int64_t ld_q, const void *
  * and P + n > length (CAPACITY): that request's weights are left alone.  A page outside
  * the pool flags BAD_INDEX; its positions gather nothing.
  * Errors: those of dspark_tree_attention (there is no workspace and no out), and
- * INVALID_ARG (length < 1, decay not finite, pos without positions). */
+ * INVALID_ARG (length < 1, decay not finite, pos without positions, weights_out over a
+ * part of weights); UNSUPPORTED (more than 65535 requests). */
 DSPARK_API int dspark_attention_weights(const void *q, int64_t ld_q, int32_t dtype,
                                         int32_t n_q_heads, int32_t max_rows,
                                         const int32_t *cu_seqlens, const int32_t *prefix_lens,
@@ -957,14 +958,15 @@ DSPARK_API size_t dspark_kv_evict_workspace_bytes(int32_t B, int32_t n_kv_heads,
  *   lens, now    device [B]: entries in the cache, and tokens so far
  *   weights, positions          [B, n_kv_heads, length], as dspark_attention_weights left
  *                them (positions of a cache that has never been cut: 0, 1, 2, ...)
- *   weights_out, positions_out  the same after the eviction, 0 from n' on; may be
- *                weights and positions themselves
+ *   weights_out, positions_out  the same after the eviction, 0 from n' on; weights and
+ *                positions themselves, or apart
  *   new_lens     device [B]: n'; may be lens
  * lens below 0 or above length or the block table (BAD_LEN): that request, its
  * entries, ledger and length are left as they are (new_lens = lens).  A page outside
  * the pool flags BAD_INDEX, and the entry is not moved.
  * Errors: INVALID_ARG (null pointer, B outside 1..n_requests, length < 1, keep < 1,
- * recent outside 0..keep, the cache's); UNSUPPORTED (head_dim); WORKSPACE; CUDA. */
+ * recent outside 0..keep, an output over a part of its input, the cache's);
+ * UNSUPPORTED (head_dim, length above 2^30, more than 65535 requests); WORKSPACE; CUDA. */
 DSPARK_API int dspark_kv_evict(const dspark_kv_cache *cache /* host */, const int32_t *lens,
                                const int32_t *now, int32_t B, int32_t keep, int32_t recent,
                                const float *weights, float *weights_out, const int32_t *positions,
