@@ -1,0 +1,120 @@
+"""Caches that are kept short, as the decode loop uses the calls: append, attend, gather,
+evict and go on."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import latent_oracle as lo
+import window_oracle as wo
+from gpu_helpers import require_gpu
+
+pytestmark = pytest.mark.gpu
+I32 = dict(dtype=torch.int32, device="cuda")
+
+
+@pytest.fixture(scope="module")
+def decode():
+    require_gpu()
+    from confidence_scheduled_speculative_gb300 import decode
+    return decode
+
+
+def entries(cache, r, n):
+    """Keys and values of request r's first n places in 64 bits: [n, heads, D]."""
+    p = torch.arange(n, device="cuda")
+    page, tok = cache.block_table[r][p // cache.k.size(1)].long(), p % cache.k.size(1)
+    out = []
+    for t, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        if s is None:
+            out.append(t[page, tok].double())
+        else:
+            out.append(wo.e4m3_values(t.view(torch.uint8)[page, tok]) * s[page, :, tok].double()[..., None])
+    return out
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+def test_rounds_of_eviction(decode, kind):
+    """Three windows with an eviction behind each: every place holds the entry of the token
+    that the ledger says, those kept are the fresh and the heaviest, and the next window's
+    attention is the formula over exactly these entries."""
+    B, hq, hkv, D, keep, recent = 3, 8, 2, 64, 24, 8
+    dt = torch.float32 if kind == "f32" else torch.bfloat16
+    cache = decode.PagedCache(B, 96, hq, hkv, D, page_size=16, dtype=wo.DTYPES[kind], seed=2, ledger=True)
+    g = torch.Generator("cuda").manual_seed(5)
+    status, lens, now = torch.zeros(1, **I32), torch.zeros(B, **I32), torch.zeros(B, **I32)
+    held = {}  # (request, position): the entry as it was stored
+    for step, (win, take) in enumerate([([32, 20, 5], [32, 20, 5]), ([9, 17, 6], [4, 17, 1]), ([7, 1, 8], [7, 1, 8]),
+                                        ([3, 3, 3], [3, 3, 3])]):
+        rows, counts = sum(win), torch.tensor(take, **I32)
+        cu = torch.tensor([0] + win, device="cuda").cumsum(0).int()
+        req = torch.repeat_interleave(torch.arange(B, device="cuda"), torch.tensor(win, device="cuda")).int()
+        offset = torch.arange(rows, **I32) - cu[req.long()]
+        pos, place = now[req.long()] + offset, lens[req.long()] + offset
+        x = torch.randn((rows, hq + 2 * hkv, D), generator=g, device="cuda").to(dt)
+        q, k, v = x[:, :hq] * 2, x[:, hq:hq + hkv], x[:, hq + hkv:]
+        cache.append(q, k, v, req=req, pos=pos, cache_pos=place, status=status)
+        out, lse = torch.zeros((rows, hq, D), device="cuda", dtype=dt), torch.zeros((rows, hq), device="cuda")
+        kw = dict(cu_seqlens=cu, prefix_lens=lens.clone(), scale=D ** -0.5, status=status)
+        cache.attend(q, out, lse=lse, **kw)
+        n = lens.tolist()
+
+        class Held:  # window_oracle's view of the cache
+            heads = hkv
+
+            def values(self, which, r, a, b):
+                return entries(cache, r, b)[0 if which == "k" else 1][a:b]
+
+        at = 0
+        unit = {"bf16": wo.BF16, "e4m3": wo.F16, "f32": 0.0}[kind]
+        for r, L in enumerate(win):
+            want = wo.attention(q[at:at + L], Held(), r, n[r], L, wo.chain_bits(L), D ** -0.5)
+            lo.compare(out[at:at + L], lse[at:at + L], want, unit, dt, (step, r))
+            ks, vs = entries(cache, r, n[r] + take[r])
+            for i in range(take[r]):
+                held[r, int(now[r]) + i] = ks[n[r] + i], vs[n[r] + i]
+            at += L
+        weights = cache.weights.clone()
+        cache.gather(q, lse, pos=pos, counts=counts, decay=0.5, **kw)
+        at = 0
+        for r, L in enumerate(win):
+            e, tol = lo.gathered(q[at:at + L], lse[at:at + L], Held(), r, n[r], L, take[r], wo.chain_bits(L), D ** -0.5)
+            e[:, :n[r]] += 0.5 * weights[r, :, :n[r]].double()
+            got = cache.weights[r, :, :n[r] + take[r]].double()
+            assert bool(((got - e).abs() <= tol + 3 * wo.U32 * e.abs()).all()), (step, r)
+            at += L
+        lens += counts
+        now += counts
+        weights, positions, before = cache.weights.clone(), cache.positions.clone(), lens.clone()
+        cache.evict(lens=before, now=now, keep=keep, recent=recent, new_lens=lens, status=status)
+        assert lens.tolist() == before.clamp(max=keep).tolist()
+        for r in range(B):
+            m = int(lens[r])
+            ks, vs = entries(cache, r, m)
+            for h in range(hkv):
+                of = lo.evicted(weights[r, h].tolist(), positions[r, h].tolist(), int(before[r]), int(now[r]), keep,
+                                recent)
+                assert cache.positions[r, h, :m].tolist() == [int(positions[r, h, p]) for p in of]
+                assert torch.equal(cache.weights[r, h, :m], weights[r, h][torch.tensor(of, device="cuda")])
+                assert set(range(max(int(now[r]) - recent, 0), int(now[r]))) <= set(cache.positions[r, h, :m].tolist())
+                for s, p in enumerate(cache.positions[r, h, :m].tolist()):
+                    assert torch.equal(ks[s, h], held[r, p][0][h]) and torch.equal(vs[s, h], held[r, p][1][h])
+    assert int(status) == 0 and lens.tolist() == [keep, keep, min(17, keep)] and not math.isnan(float(out.sum()))
+
+
+def test_a_cache_that_keeps_everything(decode):
+    """With room for all tokens nothing is evicted, and the loop commits what it does
+    without a ledger; cut short, it still runs."""
+    def run(keep, recent=16):
+        cfg = decode.ToyConfig(keep=keep, recent=recent, max_len=256)
+        target = decode.ToyTarget(cfg, B=3, seed=11)
+        gen = np.random.default_rng(3)
+        prompts = [gen.integers(0, cfg.vocab, n).tolist() for n in (2, 40, 100)]
+        return decode.generate(target, prompts, steps=6, gamma=5)
+
+    whole, _ = run(None)
+    assert run(256)[0] == whole
+    short, rows = run(32)
+    assert all(6 <= len(t) <= 36 for t in short) and max(rows) > 3
