@@ -852,17 +852,35 @@ def _heads(t: torch.Tensor, name: str, dtype, heads: int, dim: int, rows: int) -
     if t.dim() != 3 or not t.is_cuda:
         raise ValueError(f"{name}: expected a 3-D CUDA tensor [rows, heads, elements]")
     n, h, d = t.shape
+    ld, hs, sd = t.stride()
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.stride(2) != 1 and d > 1:
+    if sd != 1 and d > 1:
         raise ValueError(f"{name}: expected unit inner stride")
     if h != heads or d != dim:
         raise ValueError(f"{name}: expected {heads} heads of {dim} elements, got {h} of {d}")
     if n < rows:
         raise ValueError(f"{name}: expected at least {rows} rows, got {n}")
-    hs = t.stride(1) if h > 1 else max(t.stride(1), d)
-    ld = t.stride(0) if n > 1 else max(t.stride(0), (h - 1) * hs + d)
+    if h < 2:
+        hs = max(hs, d)
+    if n < 2:
+        ld = max(ld, (h - 1) * hs + d)
     return t.data_ptr() if n else _NO_ROWS, ld, hs
+
+
+def _matrix(t: torch.Tensor, name: str, dtype, dim: int, rows: int) -> tuple[int, int]:
+    """Pointer and row stride of [rows, dim], any row stride."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a 2-D CUDA tensor [rows, {dim}]")
+    n, d = t.shape
+    ld, sd = t.stride()
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: expected unit inner stride")
+    if d != dim or n < rows:
+        raise ValueError(f"{name}: expected at least {rows} rows of {dim} elements, got {n} of {d}")
+    return t.data_ptr() if n else _NO_ROWS, ld if n > 1 else max(ld, d)
 
 
 def dspark_latent_append(x, cache: LatentCache, *, req, pos, cos_sin, status, cache_pos=None,
@@ -877,9 +895,7 @@ def dspark_latent_append(x, cache: LatentCache, *, req, pos, cos_sin, status, ca
     code = _dtype_code(x)
     dim = cache.latent_dim + cache.rope_dim
     max_rows = x.size(0) if max_rows is None else max_rows
-    if x.dim() != 2:
-        raise ValueError("x: expected a 2-D tensor [rows, latent_dim + rope_dim]")
-    xp, ld_x, _ = _heads(x[:, None, :], "x", dtype, 1, dim, max_rows)
+    xp, ld_x = _matrix(x, "x", dtype, dim, max_rows)
     if weight is not None and weight.numel() != cache.latent_dim:
         raise ValueError(f"weight: expected {cache.latent_dim} elements")
     if cos_sin.dim() != 2 or cos_sin.size(1) != cache.rope_dim:
@@ -946,10 +962,8 @@ def dspark_prompt_attention(q, k, v, *, cu_seqlens, cu_keys, scale, out, status,
     B = cu_seqlens.numel() - 1
     S, sp, ls = 0, None, 0
     if k_shared is not None:
-        if k_shared.dim() != 2:
-            raise ValueError("k_shared: expected a 2-D tensor [keys, shared_dim]")
-        S = k_shared.size(1)
-        sp, ls, _ = _heads(k_shared[:, None, :], "k_shared", q.dtype, 1, S, max_keys)
+        S = k_shared.size(-1)
+        sp, ls = _matrix(k_shared, "k_shared", q.dtype, S, max_keys)
     qp, lq = _rows(q, "q", q.dtype, hq, K + S, max_rows)
     kp, lk, hk = _heads(k, "k", q.dtype, hkv, K, max_keys)
     vp, lv, hv = _heads(v, "v", q.dtype, hkv, V, max_keys)

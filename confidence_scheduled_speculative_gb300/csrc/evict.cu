@@ -27,12 +27,13 @@
 // it, the i-th the i-th: so all reads lie at or behind place `keep` and all writes before
 // it, entries move in any order and in parallel, and no more than have to.
 //
-// evict_select_kernel  a cluster of one to eight CTAs a (request, kv head), sixteen entries
-//   a thread, whose keys stay in registers: three passes for the digits (a histogram of
-//   each in shared memory, integer counts, summed over the cluster), then entries equal to
-//   the border, entries moved and the list of moves, each in the order of places by ballots
-//   and prefix sums, and the ledger.  Latency bounds it: 32 heads of 60000 to 131040 places
-//   took 323 us with a CTA each that read them again in every pass.
+// evict_select_kernel  a cluster of one to eight CTAs a (request, kv head), which hold the
+//   ranks of its entries in shared memory: three passes for the digits (a histogram of each
+//   beside them, integer counts, summed over the cluster), then entries equal to the border,
+//   entries moved and the list of moves, each in the order of places by ballots and prefix
+//   sums, and the ledger.  Latency bounds it: 32 heads of 60000 to 131040 places took 323 us
+//   with a CTA each that read them again in every pass, 120 with ranks in the registers of
+//   eight, of which two in three clusters run at a time.
 // evict_select_any_kernel  a CTA a (request, kv head) of any length, which does that.
 // evict_move_kernel    a CTA 128 moves of a (request, kv head): both slots looked up by a
 //   thread, then the entries' pieces streamed by all.
@@ -522,9 +523,9 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_any_kernel(EvictA
     }
 }
 
-constexpr int kSelectKeys = 16;  // of a thread
-// Threads of a CTA: where 512 hold a line, two CTAs fit an SM.
-constexpr int kFewThreads = 512;
+// Places that a CTA holds, and the threads of one whose line is short, so that several
+// fit an SM.
+constexpr int kSelectPlaces = 48 * 1024, kShortPlaces = 8192, kShortThreads = 512;
 constexpr int kSelectCtas = 8;  // of a cluster, at most
 
 // The sum over a cluster's CTAs of their words at `addr` (each CTA's own shared memory).
@@ -537,7 +538,8 @@ __device__ __forceinline__ int cluster_sum(uint32_t addr) {
 }
 
 template <int kCtas, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
+    extern __shared__ unsigned keys[];
     __shared__ int hist[2][kDigits];
     __shared__ int scan[40], found[2], counts[3];  // of this CTA: equal to the border, places left, moves
     pdl_trigger();
@@ -565,27 +567,38 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
     const bool apart = a.weights_out != a.weights, apart_p = a.positions_out != a.positions;
     const int whole = rank * kThreads + tid, threads = kCtas * kThreads;
     if (n > a.keep) {
-        // this thread's places: from + 32 i, of the warp's run of consecutive ones
+        // this thread's places: from + 32 i, of the warp's run of consecutive ones, and
+        // where their ranks lie
         const int per = (n + threads - 1) / threads, from = (whole - lane) * per + lane;
+        unsigned *key = keys + warp * 32 * per + lane;
         const long long fresh_from = (long long)__ldg(a.now + r) - a.recent;
-        unsigned key[kSelectKeys];
         bool nan = false;
+        constexpr int kAhead = 8;
+#pragma unroll 1
+        for (int i = 0; i < per; i += kAhead) {
+            float w[kAhead];
+            int position[kAhead];
+            auto in = [&](int k) { return i + k < per && from + 32 * (i + k) < n; };
 #pragma unroll
-        for (int i = 0; i < kSelectKeys; ++i) {
-            const int p = from + 32 * i;
-            key[i] = 0;
-            if (i < per && p < n) {
-                const float w = w_in[p];
-                const int position = p_in[p];
-                key[i] = rank_key(w, position, fresh_from);
-                nan = nan || key[i] == 0;
+            for (int k = 0; k < kAhead; ++k) {
+                const int p = in(k) ? from + 32 * (i + k) : 0;
+                w[k] = w_in[p];
+                position[k] = p_in[p];
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (!in(k)) continue;
+                const int p = from + 32 * (i + k);
+                const unsigned rank = rank_key(w[k], position[k], fresh_from);
+                key[32 * (i + k)] = rank;
+                nan = nan || rank == 0;
                 // (the ledger of entries that stay where they are)
-                if (apart && p < end) w_out[p] = w;
-                if (apart_p && p < end) p_out[p] = position;
+                if (apart && p < end) w_out[p] = w[k];
+                if (apart_p && p < end) p_out[p] = position[k];
             }
         }
         if (nan) flag(a.status, DSPARK_STATUS_BAD_INPUT);
-        auto there = [&](int i) { return i < per && from + 32 * i < n; };
+        auto there = [&](int i) { return from + 32 * i < n; };
         // the keep-th largest key, eleven, eleven and ten bits at a time
         unsigned border = 0;
         int need = a.keep;  // of the entries that agree with the border's digits so far
@@ -596,13 +609,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
             for (int i = tid; i < kDigits; i += kThreads) own[i] = 0;
             __syncthreads();
             int most = 0;  // (the fresh have one key: counted by ballots)
-#pragma unroll
-            for (int i = 0; i < kSelectKeys; ++i) {
-                if (i >= per) continue;
-                const bool in = there(i) && (pass == 0 || key[i] >> (shift + bits) == border);
-                const bool top = in && key[i] == 0xFFFFFFFFu;
+#pragma unroll 4
+            for (int i = 0; i < per; ++i) {
+                const unsigned k = there(i) ? key[32 * i] : 0;
+                const bool in = there(i) && (pass == 0 || k >> (shift + bits) == border);
+                const bool top = in && k == 0xFFFFFFFFu;
                 most += __popc(__ballot_sync(kFullMask, top));
-                if (in && !top) atomicAdd(&own[key[i] >> shift & ((1 << bits) - 1)], 1);
+                if (in && !top) atomicAdd(&own[k >> shift & ((1 << bits) - 1)], 1);
             }
             if (lane == 0 && most) atomicAdd(&own[(1 << bits) - 1], most);
             sync();
@@ -645,23 +658,21 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
             return sum;
         };
         int mine = 0, all;
-#pragma unroll
-        for (int i = 0; i < kSelectKeys; ++i)
-            if (i < per) mine += __popc(__ballot_sync(kFullMask, there(i) && key[i] == border));
+#pragma unroll 4
+        for (int i = 0; i < per; ++i) mine += __popc(__ballot_sync(kFullMask, there(i) && key[32 * i] == border));
         int equal = before_warp(mine, 0, &all);
-        // which of the places stay
+        // which of the places stay: in the ranks' place
         const unsigned before = lanemask_lt();
-        unsigned stays = 0;
         int left = 0, moved = 0;
-#pragma unroll
-        for (int i = 0; i < kSelectKeys; ++i) {
-            if (i >= per) continue;
+#pragma unroll 4
+        for (int i = 0; i < per; ++i) {
             const int p = from + 32 * i;
-            const bool eq = there(i) && key[i] == border;
+            const unsigned k = there(i) ? key[32 * i] : 0;
+            const bool eq = there(i) && k == border;
             const unsigned eqs = __ballot_sync(kFullMask, eq);
-            const bool yes = there(i) && (key[i] > border || (eq && equal + __popc(eqs & before) < need));
+            const bool yes = there(i) && (k > border || (eq && equal + __popc(eqs & before) < need));
             equal += __popc(eqs);
-            stays |= (unsigned)yes << i;
+            if (there(i)) key[32 * i] = yes;
             left += __popc(__ballot_sync(kFullMask, there(i) && p < a.keep && !yes));
             moved += __popc(__ballot_sync(kFullMask, p >= a.keep && yes));
         }
@@ -669,11 +680,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
         left = before_warp(left, 1, &all);
         moved = before_warp(moved, 2, &total);
         int32_t *to_list = a.moves + (long long)line * 2 * a.most, *from_list = to_list + a.most;
-#pragma unroll
-        for (int i = 0; i < kSelectKeys; ++i) {
-            if (i >= per) continue;
+#pragma unroll 4
+        for (int i = 0; i < per; ++i) {
             const int p = from + 32 * i;
-            const bool yes = stays >> i & 1, is_left = there(i) && p < a.keep && !yes, is_moved = p >= a.keep && yes;
+            const bool yes = there(i) && key[32 * i];
+            const bool is_left = there(i) && p < a.keep && !yes, is_moved = p >= a.keep && yes;
             const unsigned lefts = __ballot_sync(kFullMask, is_left), moves = __ballot_sync(kFullMask, is_moved);
             const int j = left + __popc(lefts & before), k = moved + __popc(moves & before);
             if (is_left && in_bounds(j, a.most, a.status)) to_list[j] = p;
@@ -803,9 +814,17 @@ cudaError_t launch_weights(const WeightsArgs &t, int cache_dtype, cudaStream_t s
 
 template <int kCtas, int kThreads>
 cudaError_t launch_select(const EvictArgs &a, cudaStream_t stream) {
+    constexpr int kMost = kThreads == kShortThreads ? kShortPlaces : kSelectPlaces;
+    constexpr int kSlot = 33 + (kThreads == kShortThreads ? 0 : kCtas == 1 ? 1 : kCtas == 2 ? 2 : kCtas == 4 ? 3 : 4);
+    // (a warp's run is whole, and as long as any other's)
+    const int run = (a.length + kCtas * kThreads - 1) / (kCtas * kThreads);
+    const size_t smem = (size_t)run * kThreads * 4;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(evict_select_kernel<kCtas, kThreads>), 4 * kMost, kSlot);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.cache.n_kv_heads * kCtas, a.B);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -932,14 +951,18 @@ extern "C" int dspark_kv_evict(const dspark_kv_cache *cache, const int32_t *lens
     a.moves = reinterpret_cast<int32_t *>(w + round256(B * 4) + round256(lines * 4));
     a.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // as many CTAs as hold a line of this length in their registers
-    constexpr int kFew = kFewThreads * kSelectKeys, kMany = kSelectThreads * kSelectKeys;
-    cudaError_t e = length <= kFew                  ? launch_select<1, kFewThreads>(a, st)
-                    : length <= kMany               ? launch_select<1, kSelectThreads>(a, st)
-                    : length <= 2 * kMany           ? launch_select<2, kSelectThreads>(a, st)
-                    : length <= 4 * kMany           ? launch_select<4, kSelectThreads>(a, st)
-                    : length <= kSelectCtas * kMany ? launch_select<kSelectCtas, kSelectThreads>(a, st)
-                                                    : launch_select_any(a, st);
+    // as few CTAs a line as hold it, or more while there are SMs for them and each has
+    // kShortPlaces or more
+    int ctas = 1;
+    while (ctas < kSelectCtas && ((long long)ctas * kSelectPlaces < length ||
+                                  ((long long)2 * ctas * lines <= sm_count() && length >= 2 * ctas * kShortPlaces)))
+        ctas *= 2;
+    cudaError_t e = length <= kShortPlaces                          ? launch_select<1, kShortThreads>(a, st)
+                    : (long long)ctas * kSelectPlaces < length ? launch_select_any(a, st)
+                    : ctas == 1                                     ? launch_select<1, kSelectThreads>(a, st)
+                    : ctas == 2                                     ? launch_select<2, kSelectThreads>(a, st)
+                    : ctas == 4                                     ? launch_select<4, kSelectThreads>(a, st)
+                                                                    : launch_select<8, kSelectThreads>(a, st);
     if (e == cudaSuccess) {
         const int elem = kv_elem_bytes(cache->dtype);
         const bool wide = cache->head_dim * elem % 16 == 0 && aligned(cache->k, 16) && aligned(cache->v, 16) &&

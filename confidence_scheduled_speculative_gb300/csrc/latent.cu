@@ -19,7 +19,8 @@
 namespace dspark {
 
 constexpr int kLatentThreads = 128;
-constexpr int kSteps = 4;
+template <typename T>
+constexpr int kSteps = 8 / sizeof(T);  // 32-byte or 64-byte units of a lane under way
 
 struct LatentAppendArgs {
     const void *x;
@@ -38,20 +39,23 @@ struct LatentAppendArgs {
     int32_t *status;
 };
 
-// Row w / parts and part w % parts of this warp's task, and the row's request and
-// position; false if there is nothing to write (a pad row, a position that cannot be
-// rotated).
+// Row w / parts and part w % parts of this warp's task; false behind the last row.
 __device__ __forceinline__ bool latent_task(const LatentAppendArgs &a, long long warp, int parts, int *row,
-                                            int *part, int *r, int *p) {
+                                            int *part) {
     const long long at = div_nonneg(warp, parts);
-    *part = (int)(warp - at * parts);
-    if (at >= (a.totals ? min(__ldg(a.totals), a.max_rows) : a.max_rows)) return false;
     *row = (int)at;
-    *r = __ldg(a.req + at);
-    *p = __ldg(a.pos + at);
+    *part = (int)(warp - at * parts);
+    return at < (a.totals ? min(__ldg(a.totals), a.max_rows) : a.max_rows);
+}
+
+// The row's request and position; false if there is nothing to write (a pad row, a position
+// that cannot be rotated, which the row's first part flags).
+__device__ __forceinline__ bool latent_row(const LatentAppendArgs &a, int row, int part, int *r, int *p) {
+    *r = __ldg(a.req + row);
+    *p = __ldg(a.pos + row);
     if (*r < 0) return false;
     if (*p >= 0 && *p < a.n_pos) return true;
-    if (*part == 0 && (threadIdx.x & 31) == 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
+    if (part == 0 && (threadIdx.x & 31) == 0) flag(a.status, DSPARK_STATUS_BAD_INDEX);
     return false;
 }
 
@@ -64,22 +68,36 @@ __device__ __forceinline__ long long latent_place(const LatentAppendArgs &a, int
     return -1;
 }
 
-// Eight elements a lane, in pieces of 16 bytes.
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
-    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+// Eight elements a lane, in pieces of 16 bytes, as they lie in memory and in 32 bits.
+template <typename T>
+struct Eight {
+    uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Eight<T> raw8(const T *p) {
+    Eight<T> x;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) x.v[i] = reinterpret_cast<const uint4 *>(p)[i];
+    return x;
+}
+__device__ __forceinline__ void wide8(const Eight<__nv_bfloat16> &e, float (&x)[8]) {
+    const unsigned w[4] = {e.v[0].x, e.v[0].y, e.v[0].z, e.v[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+__device__ __forceinline__ void wide8(const Eight<float> &e, float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float4 v = reinterpret_cast<const float4 *>(p)[i];
-        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+        x[4 * i] = __uint_as_float(e.v[i].x), x[4 * i + 1] = __uint_as_float(e.v[i].y);
+        x[4 * i + 2] = __uint_as_float(e.v[i].z), x[4 * i + 3] = __uint_as_float(e.v[i].w);
     }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
+    wide8(raw8(p), x);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
     unsigned w[4];
@@ -121,11 +139,25 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_kernel(LatentApp
     pdl_wait();
     const int lane = threadIdx.x & 31;
     int row, part, r, p;
-    if (!latent_task(a, ((long long)blockIdx.x * kLatentThreads + threadIdx.x) >> 5, parts, &row, &part, &r, &p))
-        return;
+    if (!latent_task(a, ((long long)blockIdx.x * kLatentThreads + threadIdx.x) >> 5, parts, &row, &part)) return;
     // this lane's pairs, and where its unit's two pieces lie in a rotated part
     const int R = a.rope_dim, units = R / 16, unit = lane % units;
     const int first = a.interleaved ? 16 * unit : 8 * unit, second = a.interleaved ? first + 8 : first + R / 2;
+    const int heads = 32 / units;  // a step
+    const int h0 = (part - 1) * kSteps<T> * heads + lane / units;
+    // the queries first: they do not wait for the row's position
+    Eight<T> u[kSteps<T>], v[kSteps<T>];
+    if (part > 0) {
+        const T *q = static_cast<const T *>(a.q) + row * a.ld_q;
+#pragma unroll
+        for (int i = 0; i < kSteps<T>; ++i) {
+            const int h = h0 + i * heads;
+            if (h >= a.n_q_heads) continue;
+            u[i] = raw8(q + h * a.hs_q + first);
+            v[i] = raw8(q + h * a.hs_q + second);
+        }
+    }
+    if (!latent_row(a, row, part, &r, &p)) return;
     float c[8], s[8];
     const float *angles = a.cos_sin + (long long)p * R + 8 * unit;
     load8(angles, c);
@@ -136,11 +168,11 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_kernel(LatentApp
         const T *x = static_cast<const T *>(a.x) + row * a.ld_x;
         C *out = reinterpret_cast<C *>(a.cache.k) + at;
         constexpr int kPieces = DSPARK_MAX_LATENT_DIM / 256;
-        float v[kPieces][8], key[2][8], sum = 0.0f;
+        float e[kPieces][8], key[2][8], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int d = (lane + 32 * i) * 8;
-            if (d < a.latent_dim) load8(x + d, v[i]);
+            if (d < a.latent_dim) load8(x + d, e[i]);
         }
         if (lane < units) {
             load8(x + a.latent_dim + first, key[0]);
@@ -151,7 +183,7 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_kernel(LatentApp
             for (int i = 0; i < kPieces; ++i)
                 if ((lane + 32 * i) * 8 < a.latent_dim)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+                    for (int j = 0; j < 8; ++j) sum = fmaf(e[i][j], e[i][j], sum);
             for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(kFullMask, sum, m);
             const float inv = 1.0f / sqrtf(sum / a.latent_dim + a.eps);
 #pragma unroll
@@ -161,13 +193,13 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_kernel(LatentApp
                 float w[8];
                 load8(static_cast<const T *>(a.weight) + d, w);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * w[j];
+                for (int j = 0; j < 8; ++j) e[i][j] = e[i][j] * inv * w[j];
             }
         }
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
             const int d = (lane + 32 * i) * 8;
-            if (d < a.latent_dim) store8(out + d, v[i]);
+            if (d < a.latent_dim) store8(out + d, e[i]);
         }
         if (lane < units) {
             rotate8(key[0], key[1], c, s, a.interleaved);
@@ -176,25 +208,17 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_kernel(LatentApp
         }
         return;
     }
-    const int heads = 32 / units;  // a step
-    const T *q = static_cast<const T *>(a.q) + row * a.ld_q;
     T *out = static_cast<T *>(a.q_out) + row * a.ld_q_out;
-    const int h0 = (part - 1) * kSteps * heads + lane / units;
-    float u[kSteps][8], v[kSteps][8];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < kSteps<T>; ++i) {
         const int h = h0 + i * heads;
         if (h >= a.n_q_heads) continue;
-        load8(q + h * a.hs_q + first, u[i]);
-        load8(q + h * a.hs_q + second, v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int h = h0 + i * heads;
-        if (h >= a.n_q_heads) continue;
-        rotate8(u[i], v[i], c, s, a.interleaved);
-        store8(out + h * a.hs_q_out + first, u[i]);
-        store8(out + h * a.hs_q_out + second, v[i]);
+        float x[8], y[8];
+        wide8(u[i], x);
+        wide8(v[i], y);
+        rotate8(x, y, c, s, a.interleaved);
+        store8(out + h * a.hs_q_out + first, x);
+        store8(out + h * a.hs_q_out + second, y);
     }
 }
 
@@ -214,8 +238,8 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_any_kernel(Laten
     pdl_wait();
     const int lane = threadIdx.x & 31, R = a.rope_dim;
     int row, part, r, p;
-    if (!latent_task(a, ((long long)blockIdx.x * kLatentThreads + threadIdx.x) >> 5, 1 + a.n_q_heads, &row, &part,
-                     &r, &p))
+    if (!latent_task(a, ((long long)blockIdx.x * kLatentThreads + threadIdx.x) >> 5, 1 + a.n_q_heads, &row, &part) ||
+        !latent_row(a, row, part, &r, &p))
         return;
     const float *angles = a.cos_sin + (long long)p * R;
     if (part > 0) {
@@ -255,7 +279,7 @@ bool append_pieces(const LatentAppendArgs &a, int dtype, const dspark_latent_cac
 
 template <typename T, typename C>
 cudaError_t launch_latent_append(const LatentAppendArgs &a, bool pieces, cudaStream_t stream) {
-    const int step = pieces ? 32 / (a.rope_dim / 16) * kSteps : 1;
+    const int step = pieces ? 32 / (a.rope_dim / 16) * kSteps<T> : 1;
     const int parts = 1 + (a.n_q_heads + step - 1) / step;
     constexpr int kWarps = kLatentThreads / 32;
     const long long grid = ((long long)a.max_rows * parts + kWarps - 1) / kWarps;

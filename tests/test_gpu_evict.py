@@ -226,6 +226,7 @@ EVICT = [
     dict(lens=[100000, 131040], keep=50000, recent=4096, hkv=1, page=128, kind="e4m3"),
     dict(lens=[70001], keep=69990, recent=5, hkv=1, page=64, ties=True),
     dict(lens=[140000, 500], keep=64000, recent=64000, hkv=1, page=64, kind="e4m3"),
+    dict(lens=[400000, 393217], keep=200000, recent=100, hkv=1, D=16, page=256, spread=0.1),
     dict(lens=[700, 90], keep=80, recent=8, ties=True),
     dict(lens=[3000], keep=1500, recent=10, ties=True, spread=0.5),
     dict(lens=[300, 120], keep=64, recent=16, layout="heads", hkv=3),
