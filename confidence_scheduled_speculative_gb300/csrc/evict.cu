@@ -227,13 +227,13 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsAr
         int next = page[kGatherStages];
         __syncthreads();
         for (int i = warp; i < tiles * 8; i += kGatherWarps) {
+            // (places past the last row hold it again: against zeros, infinite keys would give NaN)
             const bool in = i < count;
-            const int token = in ? (row0 + i) / G : 0, row = w.lo + token;
-            const int head = kh * G + (in ? (row0 + i) % G : 0);
+            const int of = row0 + min(i, count - 1), token = of / G, row = w.lo + token, head = kh * G + of % G;
             const __nv_bfloat16 *q =
                 static_cast<const __nv_bfloat16 *>(a.q) + (long long)row * a.ld_q + (long long)head * D;
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (in && lane < D / 8) v = __ldg(reinterpret_cast<const uint4 *>(q) + lane);
+            if (lane < D / 8) v = __ldg(reinterpret_cast<const uint4 *>(q) + lane);
             float by = 1.0f;
             if constexpr (kQuant) {
                 const unsigned e[4] = {v.x, v.y, v.z, v.w};
@@ -528,20 +528,18 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_any_kernel(EvictA
 constexpr int kSelectPlaces = 48 * 1024, kShortPlaces = 8192, kShortThreads = 512;
 constexpr int kSelectCtas = 8;  // of a cluster, at most
 
-// The sum over a cluster's CTAs of their words at `addr` (each CTA's own shared memory).
+// The word of CTA `rank` of the cluster where this one has *own.
 template <int kCtas>
-__device__ __forceinline__ int cluster_sum(uint32_t addr) {
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < kCtas; ++i) sum += (int)cluster_load(cluster_addr(addr, i));
-    return sum;
+__device__ __forceinline__ int word_of(const int *own, int rank) {
+    return kCtas == 1 ? *own : (int)cluster_load(cluster_addr(smem_addr(own), rank));
 }
 
 template <int kCtas, int kThreads>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
     extern __shared__ unsigned keys[];
     __shared__ int hist[2][kDigits];
-    __shared__ int scan[40], found[2], counts[3];  // of this CTA: equal to the border, places left, moves
+    __shared__ long long wide[40];
+    __shared__ int scan[40], found[2], counts[4];  // of this CTA: equal to the border; places left, moves
     pdl_trigger();
     pdl_wait();
     const int rank = blockIdx.x % kCtas, h = blockIdx.x / kCtas, r = blockIdx.y;
@@ -573,7 +571,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         unsigned *key = keys + warp * 32 * per + lane;
         const long long fresh_from = (long long)__ldg(a.now + r) - a.recent;
         bool nan = false;
-        constexpr int kAhead = 8;
+        // (a short line's all at once: 256 lines of 4113 places 25 us at eight, 20.6 at sixteen)
+        constexpr int kAhead = 16;
 #pragma unroll 1
         for (int i = 0; i < per; i += kAhead) {
             float w[kAhead];
@@ -625,7 +624,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
             int c[kOwn] = {}, sum = 0;
             if (top >= 0)
 #pragma unroll
-                for (int k = 0; k < kOwn; ++k) sum += c[k] = cluster_sum<kCtas>(smem_addr(&own[top - k]));
+                for (int k = 0; k < kOwn; ++k) {
+#pragma unroll
+                    for (int x = 0; x < kCtas; ++x) c[k] += word_of<kCtas>(&own[top - k], x);
+                    sum += c[k];
+                }
             int total, above = block_exclusive_scan<int>(sum, scan, &total);
 #pragma unroll
             for (int k = 0; k < kOwn; ++k) {
@@ -640,27 +643,30 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
             need = found[1];
             __syncthreads();
         }
-        // This thread's share of a sum in the order of places: what comes before the warp's
-        // run in the cluster, by a count of the warp's (`which` of counts, a word each).
-        auto before_warp = [&](int mine, int which, int *all) {
-            int total;
-            int sum = block_exclusive_scan<int>(lane == 0 ? mine : 0, scan, &total);
+        // What comes before the warp's run in the cluster, in the order of places, by two
+        // counts of each warp's (31 bits each: one scan), and the cluster's second count.
+        auto before_warp = [&](long long mine, int which, int *all) {
+            long long total;
+            long long sum = block_exclusive_scan<long long>(lane == 0 ? mine : 0, wide, &total);
             sum = __shfl_sync(kFullMask, sum, 0);
-            if (tid == 0) counts[which] = total;
+            if (tid == 0) {
+                counts[which] = (int)(total >> 32);
+                counts[which + 1] = (int)total;
+            }
             sync();
             *all = 0;
 #pragma unroll
             for (int i = 0; i < kCtas; ++i) {
-                const int c = (int)cluster_load(cluster_addr(smem_addr(&counts[which]), i));
-                if (i < rank) sum += c;
-                *all += c;
+                const int a0 = word_of<kCtas>(&counts[which], i), a1 = word_of<kCtas>(&counts[which + 1], i);
+                if (i < rank) sum += ((long long)a0 << 32) + a1;
+                *all += a1;
             }
             return sum;
         };
         int mine = 0, all;
 #pragma unroll 4
         for (int i = 0; i < per; ++i) mine += __popc(__ballot_sync(kFullMask, there(i) && key[32 * i] == border));
-        int equal = before_warp(mine, 0, &all);
+        int equal = (int)before_warp(mine, 0, &all);
         // which of the places stay: in the ranks' place
         const unsigned before = lanemask_lt();
         int left = 0, moved = 0;
@@ -677,8 +683,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
             moved += __popc(__ballot_sync(kFullMask, p >= a.keep && yes));
         }
         int total;
-        left = before_warp(left, 1, &all);
-        moved = before_warp(moved, 2, &total);
+        const long long both = before_warp(((long long)left << 32) + moved, 2, &total);
+        left = (int)(both >> 32);
+        moved = (int)both;
         int32_t *to_list = a.moves + (long long)line * 2 * a.most, *from_list = to_list + a.most;
 #pragma unroll 4
         for (int i = 0; i < per; ++i) {
@@ -868,7 +875,7 @@ extern "C" int dspark_attention_weights(const void *q, int64_t ld_q, int32_t dty
         return DSPARK_ERR_INVALID_ARG;
     if (!(scale - scale == 0.0f) || !(decay - decay == 0.0f)) return DSPARK_ERR_INVALID_ARG;
     if (!same_or_apart(weights, weights_out, (int64_t)B * cache->n_kv_heads * length)) return DSPARK_ERR_INVALID_ARG;
-    if (n_q_heads > 65535 || B > 65535) return DSPARK_ERR_UNSUPPORTED;
+    if (n_q_heads > 65535 || B > 65535 || length > (1 << 30)) return DSPARK_ERR_UNSUPPORTED;
     WeightsArgs t;
     AttendArgs &a = t.a;
     a.q = q;

@@ -855,7 +855,8 @@ DSPARK_API size_t dspark_latent_attention_workspace_bytes(int32_t n_q_heads, int
  *                not share an element with q
  *   lse          [max_rows, n_q_heads] fp32, nullable
  * BF16 rows over a BF16 cache with latent_dim 512, rope_dim 64, page_size a multiple
- * of 16 and 16-byte aligned bases and strides run on the tensor cores, the weights
+ * of 16, 16-byte aligned bases and strides and fewer than 2^31 tiles of 128 positions
+ * and 128 (row, head) pairs in full block tables run on the tensor cores, the weights
  * exp(s - m) rounded to BF16; anything else in 32 bits throughout.  The order of all
  * sums is fixed by the lengths: a call repeated gives the same bits.
  * Errors: INVALID_ARG (null pointer, B outside 1..n_requests, n_q_heads < 1, dtype, a
@@ -890,9 +891,9 @@ DSPARK_API int dspark_latent_attention(const void *q, int64_t ld_q, int32_t dtyp
  * no effect on it, NaN and infinities included.  BF16 with key_dim 128, shared_dim 64
  * or 0, value_dim 128 and 16-byte aligned bases and strides runs on the tensor cores,
  * the weights rounded to BF16; anything else in 32 bits throughout.
- * A range outside the rows or the keys, or one that descends (BAD_LEN): that
- * request's rows are unspecified, the others not affected.  Rows of no request are
- * left alone.
+ * A range outside the rows or the keys (BAD_LEN): that request's rows are unspecified,
+ * the others not affected.  Ranges of queries that descend (BAD_LEN) or overlap: all
+ * rows are unspecified.  Rows of no request are left alone.
  * Errors: INVALID_ARG (null pointer, dtype, B < 1, n_q_heads not a positive multiple
  * of n_kv_heads, a stride below what it spans, negative counts, scale not finite, out
  * over q); UNSUPPORTED (key_dim, shared_dim or value_dim above
@@ -930,13 +931,16 @@ DSPARK_API int dspark_prompt_attention(const void *q, int64_t ld_q, const void *
  *   weights, weights_out   [B, n_kv_heads, length] fp32, the same or apart
  *   pos, positions         device [max_rows] and [B, n_kv_heads, length] int32,
  *                both or neither
- * Sums are held in 32 bits and their order is fixed.  What a row does not see has no
+ * Sums are held in 32 bits and their order is fixed.  BF16 rows over BF16 or E4M3 keys of
+ * 64 or 128 elements with 16-byte aligned bases and strides run on the tensor cores, their
+ * products exact; beside E4M3 keys an element of a query may lose what is below 2^-39 of its
+ * row's largest.  Anything else runs in 32 bits throughout.  What a row does not see has no
  * effect.  A window as dspark_tree_attention flags it, counts outside the window (BAD_LEN)
- * and P + n > length (CAPACITY): that request's weights are left alone.  A page outside
- * the pool flags BAD_INDEX; its positions gather nothing.
+ * and P + n > length (CAPACITY): that request's weights and positions are left alone.
+ * A page outside the pool flags BAD_INDEX; its positions gather nothing.
  * Errors: those of dspark_tree_attention (there is no workspace and no out), and
  * INVALID_ARG (length < 1, decay not finite, pos without positions, weights_out over a
- * part of weights); UNSUPPORTED (more than 65535 requests). */
+ * part of weights); UNSUPPORTED (more than 65535 requests, length above 2^30). */
 DSPARK_API int dspark_attention_weights(const void *q, int64_t ld_q, int32_t dtype,
                                         int32_t n_q_heads, int32_t max_rows,
                                         const int32_t *cu_seqlens, const int32_t *prefix_lens,
@@ -954,7 +958,8 @@ DSPARK_API size_t dspark_kv_evict_workspace_bytes(int32_t B, int32_t n_kv_heads,
  * the larger weight (a NaN below all others; BAD_INPUT); then the lower place.  With
  * n' = min(n, keep), the i-th entry in order that stays from place n' on moves to the i-th
  * free place below n'; the others lie as they did.
- *   cache        keys, values and scales move; places from n' on keep what they held
+ *   cache        keys, values and scales move; places from n' on keep what they held.  Two
+ *                requests must not share a page
  *   lens, now    device [B]: entries in the cache, and tokens so far
  *   weights, positions          [B, n_kv_heads, length], as dspark_attention_weights left
  *                them (positions of a cache that has never been cut: 0, 1, 2, ...)

@@ -120,6 +120,18 @@ def test_gathered_over_what_is_unseen(api):
         p.check()
 
 
+def test_gathered_over_an_infinite_key(api):
+    """A key of -inf under queries above zero: s = -inf, which adds nothing."""
+    for D, hq in ((128, 5), (64, 8), (80, 3)):
+        p = Gathering(api, 470, prefix=[40], win=[1], hq=hq, hkv=1, D=D, page=16, kind="bf16")
+        p.q.copy_(p.q.abs() + 0.01)
+        p.cache.put("k", 0, 7, -math.inf)
+        p.run(api)
+        p.gather(api)
+        assert float(p.weights[0, 0, 7]) == float(p.before[0, 0, 7] * p.decay)  # (rounded once, both)
+        assert bool(p.weights.isfinite().all()) and int(p.status) == 0
+
+
 def test_gathering_bad_requests(api):
     kw = dict(hq=8, hkv=2, D=128, page=64, kind="bf16")
     p = Gathering(api, 460, prefix=[40, 100, 70], win=[4, 3, 2], counts=[4, 3, 2], **kw)

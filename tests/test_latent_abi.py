@@ -138,6 +138,7 @@ def test_weights_checks(lib):  # noqa: F811
                 dict(positions=FAKE), dict(wo=ctypes.c_void_p(FAKE.value + 4))):
         assert _weights(lib, _cache(), **bad) == -1, bad
     assert _weights(lib, _cache(head_dim=258)) == -4
+    assert _weights(lib, _cache(), length=(1 << 30) + 1) == -4
 
 
 def _evict(lib, cache, lens=FAKE, now=FAKE, B=3, keep=4, recent=1, w=FAKE, wo=FAKE, p=FAKE, po=FAKE, length=8,
