@@ -219,7 +219,6 @@ prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     for (int i = tid; i < kDiagonal * kPromptKeys / 32; i += kPromptThreads) (&ctl.nonfinite[0][0])[i] = 0;
     __syncthreads();
     pdl_wait();
-    pdl_trigger();
     {  // the request: each thread counts the blocks of a run of them
         const int per = (a.B + kPromptThreads - 1) / kPromptThreads;
         auto blocks = [&](int r, bool report) {
@@ -243,6 +242,7 @@ prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     __syncthreads();
     if (ctl.request < 0) return;  // (both CTAs)
     if (warp == kPromptMatrixWarp) tmem_alloc_pair(smem_addr(&ctl.tmem), 512);
+    pdl_trigger();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are there
     tmem_fence_after();
