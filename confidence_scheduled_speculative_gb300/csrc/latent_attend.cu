@@ -779,7 +779,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                     d[3] = s.q.row0;
                     d[4] = s.row_tile * kPairRows + rank * kRows;
                     d[5] = min(all - d[4], kRows);
-                    d[6] = 2 * team.size;
+                    d[6] = 31 - __clz(2 * team.size);
                     d[0] = 1;
                 } else if (s.k == 0 && s.first + s.count < s.q.tiles) {
                     // (where its first tile is)
@@ -795,13 +795,16 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
 }
 
 // Joins the parts of the jobs that several CTAs share, in the CTAs' order: a block for
-// each of these CTAs but the last takes its share of the rows' fours of elements; threads to
-// spare deal the parts among them.
-constexpr int kLatentJoinThreads = 256, kLatentJoinPieces = 16;
+// each of these CTAs but the last takes its share of the rows' fours of elements.  A thread
+// keeps to a row, and a block's groups of kRows threads take fours in turn, or where there
+// are many parts one four and the parts in turn.  L2's latency bounds it.
+constexpr int kJoinThreads = 256, kJoinGroups = kJoinThreads / kRows, kJoinPieces = 8;
+constexpr int kJoinFew = 8;  // parts that a thread adds alone
 
-__global__ void __launch_bounds__(kLatentJoinThreads) latent_join_kernel(const LatentTensorArgs t) {
-    __shared__ float4 sum[kLatentJoinThreads];
-    __shared__ float sum_l[kLatentJoinThreads];
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const LatentTensorArgs t) {
+    __shared__ float factor[kLatentCtas / 2][kRows];  // of a part (a pair has one of a job)
+    __shared__ float2 of_group[kJoinGroups][kRows];
+    __shared__ float4 sum[kJoinThreads];
     pdl_wait();
     pdl_trigger();
     int c0 = blockIdx.x;
@@ -813,93 +816,68 @@ __global__ void __launch_bounds__(kLatentJoinThreads) latent_join_kernel(const L
         d0 = job(0);
         d1 = job(1);
     }
-    const int rows = d1.y, by = d1.z, n = (d0.y - c0) / by + 1;  // parts, of every by-th CTA
+    const int rows = d1.y, by = d1.z, n = (d0.y - c0 >> by) + 1;  // parts, of every 2^by-th CTA
     if (rows <= 0) return;
-    const int share = (blockIdx.x - c0) / by, shares = max(n - 1, 1);
-    const long long fours = 128ll * rows, pieces = (long long)shares * gridDim.y;
-    const long long piece = (long long)share * gridDim.y + blockIdx.y;
-    const int begin = (int)(piece * fours / pieces), end = (int)((piece + 1) * fours / pieces);
-    const int tid = threadIdx.x, hq = t.a.n_q_heads;
-    auto slot = [&](int i) { return (long long)(i == 0 ? d0.z : 2 * (c0 + by * i)); };
-    auto ml = [&](int i, int which, int m) { return __ldcg(t.part_ml + (slot(i) * 2 + which) * kRows + m); };
-    auto from = [&](int i, int four, int m) {
-        return __ldcg(reinterpret_cast<const float4 *>(t.part_o) + (slot(i) * 128 + four) * kRows + m);
+    constexpr int kFours = kLatent / 4;
+    const int pieces = max(n - 1, 1) * kJoinPieces, piece = ((int)blockIdx.x - c0 >> by) * kJoinPieces + blockIdx.y;
+    const int each = (kFours + pieces - 1) / pieces, begin = piece * each, end = min(begin + each, kFours);
+    if (begin >= end) return;
+    const int tid = threadIdx.x, m = tid % kRows, group = tid / kRows;
+    const int deals = n > kJoinFew ? kJoinGroups : 1, deal = group % deals, step = kJoinGroups / deals;
+    auto slot = [&](int i) { return (long long)(i == 0 ? d0.z : 2 * (c0 + (i << by))); };
+    auto part = [&](int i, int four) {
+        return __ldcg(reinterpret_cast<const float4 *>(t.part_o) + (slot(i) * kFours + four) * kRows + m);
     };
     auto add = [](float4 &x, float f, float4 y) {
         x.x = fmaf(f, y.x, x.x), x.y = fmaf(f, y.y, x.y), x.z = fmaf(f, y.z, x.z), x.w = fmaf(f, y.w, x.w);
     };
-    auto put = [&](int four, int m, float4 x, float shift, float l) {
-        const float inv = 1.0f / l;
+    auto in = [&](int four) { return four < end && m < rows; };
+    // the row's maximum and sum, and each part's factor
+    float top = -INFINITY, l = 0.0f;
+    if (m < rows)
+        for (int i = group; i < n; i += kJoinGroups) {
+            const float *ml = t.part_ml + slot(i) * 2 * kRows + m;
+            const float pm = __ldcg(ml), pl = __ldcg(ml + kRows), higher = fmaxf(top, pm);
+            const float base = higher == -INFINITY ? 0.0f : higher;
+            l = l * exp2_approx(top - base) + pl * exp2_approx(pm - base);
+            top = higher;
+            factor[i][m] = pm;
+        }
+    of_group[group][m] = make_float2(top, l);
+    __syncthreads();
+    top = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kJoinGroups; ++i) top = fmaxf(top, of_group[i][m].x);
+    const float shift = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int i = 0; i < kJoinGroups; ++i) l = fmaf(exp2_approx(of_group[i][m].x - shift), of_group[i][m].y, l);
+    if (m < rows)
+        for (int i = group; i < n; i += kJoinGroups) factor[i][m] = exp2_approx(factor[i][m] - shift);
+    __syncthreads();
+    const int hq = t.a.n_q_heads, row = d1.x + m, head = row % hq;
+    const long long packed = d0.w + row / hq;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out + (long long)head * kLatent;
+    const float inv = 1.0f / l;
+    for (int four = begin + group / deals, at = begin; at < end; at += step, four += step) {
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (in(four))
+#pragma unroll 4
+            for (int i = deal; i < n; i += deals) add(x, factor[i][m], part(i, four));
+        if (deals > 1) {
+            sum[tid] = x;
+            __syncthreads();
+            if (deal == 0)
+#pragma unroll
+                for (int i = 1; i < kJoinGroups; ++i) add(x, 1.0f, sum[tid + i * kRows]);
+            __syncthreads();
+        }
+        if (deal > 0 || !in(four)) continue;
         if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         else x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
-        const int row = d1.x + m, head = row % hq;
-        const long long packed = d0.w + row / hq;
         const __nv_bfloat162 u = __floats2bfloat162_rn(x.x, x.y), v = __floats2bfloat162_rn(x.z, x.w);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(t.a.out) + packed * t.a.ld_out +
-                                   (long long)head * kLatent + four * 4) =
+        *reinterpret_cast<uint2 *>(out + four * 4) =
             make_uint2(*reinterpret_cast<const uint32_t *>(&u), *reinterpret_cast<const uint32_t *>(&v));
-        if (t.a.lse && four == 0)
-            t.a.lse[packed * hq + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
-    };
-    constexpr int kFew = 4;
-    if (n <= kFew) {
-        // all loads of a piece of output before the first use
-        for (int item = begin + tid; item < end; item += kLatentJoinThreads) {
-            const int four = item / rows, m = item % rows;
-            float pm[kFew], pl[kFew], top = -INFINITY, l = 0.0f;
-            float4 po[kFew], x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < kFew; ++i) {
-                pm[i] = i < n ? ml(i, 0, m) : -INFINITY;
-                pl[i] = i < n ? ml(i, 1, m) : 0.0f;
-                if (i < n) po[i] = from(i, four, m);
-            }
-#pragma unroll
-            for (int i = 0; i < kFew; ++i) top = fmaxf(top, pm[i]);
-            const float shift = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-            for (int i = 0; i < kFew; ++i) {
-                if (i >= n) continue;
-                const float f = exp2_approx(pm[i] - shift);
-                l = fmaf(f, pl[i], l);
-                add(x, f, po[i]);
-            }
-            put(four, m, x, shift, l);
-        }
-        return;
-    }
-    for (int base = begin; base < end; base += kLatentJoinThreads) {
-        const int items = min(end - base, kLatentJoinThreads), deals = kLatentJoinThreads / items;
-        const int deal = tid / items, item = base + tid % items, four = item / rows, m = item % rows;
-        float top = -INFINITY;
-        if (deal < deals)
-#pragma unroll 4
-            for (int i = deal; i < n; i += deals) top = fmaxf(top, ml(i, 0, m));
-        sum_l[tid] = top;
-        __syncthreads();
-        for (int i = 0; i < deals; ++i) top = fmaxf(top, sum_l[i * items + tid % items]);
-        const float shift = top == -INFINITY ? 0.0f : top;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float l = 0.0f;
-        if (deal < deals)
-#pragma unroll 4
-            for (int i = deal; i < n; i += deals) {
-                const float f = exp2_approx(ml(i, 0, m) - shift);
-                l = fmaf(f, ml(i, 1, m), l);
-                add(x, f, from(i, four, m));
-            }
-        __syncthreads();
-        sum[tid] = x;
-        sum_l[tid] = l;
-        __syncthreads();
-        if (deal == 0) {
-            for (int i = 1; i < deals; ++i) {
-                add(x, 1.0f, sum[i * items + tid]);
-                l += sum_l[i * items + tid];
-            }
-            put(four, m, x, shift, l);
-        }
-        __syncthreads();
+        if (t.a.lse && four == 0) t.a.lse[packed * hq + head] = l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
     }
 }
 
@@ -968,7 +946,7 @@ cudaError_t launch_latent_tensor(const AttendArgs &a, const dspark_latent_cache 
     const int grid = 2 * pair_count();
     e = launch_pdl(latent_tensor_kernel, dim3(grid), dim3(kLatentThreads), kLatentSmem, stream, map, t);
     if (e != cudaSuccess || t.whole) return e;
-    return launch_pdl(latent_join_kernel, dim3(grid, kLatentJoinPieces), dim3(kLatentJoinThreads), 0, stream, t);
+    return launch_pdl(latent_join_kernel, dim3(grid, kJoinPieces), dim3(kJoinThreads), 0, stream, t);
 }
 
 template <typename T>
