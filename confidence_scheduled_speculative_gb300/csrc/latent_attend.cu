@@ -199,11 +199,13 @@ struct Team {
 
 // Walks a team's units: requests in order, in each the row tiles, a team's worth at a
 // time, in each the positions.  Every warp role of both CTAs walks on its own and sees the
-// same.
+// same.  (What comes behind a segment is found when it is asked for, so that the first does
+// not wait for the second's window.)
 struct LatentWalk {
     int left, r, group, unit;
     Team team;
     unsigned k;
+    bool behind;
     LatentRequest q = {};
     Window ahead;
 
@@ -215,10 +217,20 @@ struct LatentWalk {
         q = b.q;
         team = of;
         k = 0;
+        behind = false;
         ahead = load_window(t.a, min(r + 1, t.a.B - 1));
     }
     __device__ __forceinline__ bool next(const LatentTensorArgs &t, LatentSegment *s) {
         while (left > 0) {
+            if (behind && ++group * team.size >= q.row_tiles) {
+                group = 0;
+                for (bool has = false; !has;) {  // (there are units left, so a request)
+                    if (++r >= t.a.B) return false;
+                    has = to_latent(t, ahead, &q, false);
+                    ahead = load_window(t.a, min(r + 1, t.a.B - 1));
+                }
+            }
+            behind = true;
             const int take = t.whole ? 1 : min(q.tiles + kLatentJobCost - unit, left);
             s->q = q;
             s->r = r;
@@ -228,15 +240,6 @@ struct LatentWalk {
             s->count = t.whole ? q.tiles : max(unit + take - kLatentJobCost, 0) - s->first;
             left -= take;
             unit = 0;
-            if (++group * team.size >= q.row_tiles) {
-                group = 0;
-                while (left > 0) {
-                    const bool has = to_latent(t, ahead, &q, false);
-                    ++r;
-                    ahead = load_window(t.a, min(r + 1, t.a.B - 1));
-                    if (has) break;
-                }
-            }
             if (s->count > 0) {
                 ++k;
                 if (s->row_tile < s->q.row_tiles) return true;  // (else other members' alone)
@@ -246,58 +249,79 @@ struct LatentWalk {
     }
 };
 
-// The size of teams, and this CTA's team's share and where it begins (for all after the next barrier); false
-// where none are left for it.
+// The size of teams, and this CTA's team's share and where it begins (for all after the
+// next barrier); false where none are left for it.
 //   Larger teams read less from HBM and leave members idle where the row tiles are no
 // multiple of them: the largest is taken whose members' steps are at most an eighth more
 // than those of pairs alone.
-__device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBegin *begin, int *scan,
+//   (Loops are rolled up: code that runs once is fetched as slowly as it is long.)
+__device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBegin *begin, int4 *of_warp,
                                              Deal *deal, Team *team) {
     const AttendArgs &a = t.a;
-    const int tid = threadIdx.x, cta = blockIdx.x, pairs = gridDim.x / 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x, pairs = gridDim.x / 2;
     const int per = (a.B + kLatentThreads - 1) / kLatentThreads;
     LatentRequest q = {};
     auto job = [&]() { return t.whole ? 1 : q.tiles + kLatentJobCost; };
-    // (rolled up: code that runs once is fetched as slowly as it is long)
-    int size = 1;
-    int own = 0, before = 0, T = 0, alone = 0;  // units: a call has fewer than 2^31
+    // units (a call has fewer than 2^31) for teams of 1, 2 and 4: a thread's, with those before
+    // it in its warp, and the warps'
+    int mine[3] = {}, before[3], all[3] = {};
 #pragma unroll 1
-    for (int g = 1; g <= (t.whole ? 1 : min(4, pairs)); g *= 2) {
-        int mine = 0, sum;
+    for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
+        if (to_latent(t, load_window(a, r), &q, cta == 0))
+#pragma unroll
+            for (int g = 0; g < 3; ++g) mine[g] += job() * (q.row_tiles + (1 << g) - 1 >> g);
+#pragma unroll
+    for (int g = 0; g < 3; ++g) before[g] = mine[g];
 #pragma unroll 1
-        for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r)
-            if ((per == 1 && g > 1) ? q.tiles > 0 : to_latent(t, load_window(a, r), &q, cta == 0 && g == 1))
-                mine += job() * ((q.row_tiles + g - 1) / g);
-        const int at = block_exclusive_scan<int>(mine, scan, &sum);
-        if (g == 1) alone = sum;
-        if (g == 1 || sum / (pairs / g) * 8ll <= alone / pairs * 9ll) {
-            size = g;
-            own = mine, before = at, T = sum;
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+        for (int g = 0; g < 3; ++g) {
+            const int x = __shfl_up_sync(kFullMask, before[g], d);
+            if (lane >= d) before[g] += x;
+        }
+    if (lane == 31) of_warp[warp] = make_int4(before[0], before[1], before[2], 0);
+    __syncthreads();
+#pragma unroll 1
+    for (int w = 0; w < kLatentThreads / 32; ++w) {
+        const int4 v = of_warp[w];
+        const int x[3] = {v.x, v.y, v.z};
+#pragma unroll
+        for (int g = 0; g < 3; ++g) {
+            all[g] += x[g];
+            if (w < warp) before[g] += x[g];
         }
     }
-    const int n = min(pairs / size, t.whole ? T : (T + kLatentJobCost + 1) / (kLatentJobCost + 2));
+    int shift = 0, own = mine[0], to = before[0], T = all[0];
+#pragma unroll
+    for (int g = 1; g < 3; ++g)
+        if (!t.whole && pairs >> g > 0 && all[g] * (8ll * pairs) <= all[0] * (9ll * (pairs >> g)))
+            shift = g, own = mine[g], to = before[g], T = all[g];
+    const int size = 1 << shift, from = to - own;
+    const int n = min(pairs >> shift, t.whole ? T : (T + kLatentJobCost + 1) / (kLatentJobCost + 2));
     if (tid == 0 && !t.whole) {
         t.desc[cta * kLatentDesc] = 0;
         t.desc[cta * kLatentDesc + 7] = -1;
     }
-    *team = {size, cta / 2 % size, cta / 2 / size};
+    *team = {size, cta / 2 & size - 1, cta / 2 >> shift};
     if (team->at >= n) return false;
+    const unsigned each = (unsigned)T / (unsigned)n;
     deal->n = n;
-    deal->each = T / n;
-    deal->rest = T % n;
+    deal->each = each;
+    deal->rest = T - (int)each * n;
     const int lo = (int)deal->first(team->at), hi = (int)deal->first(team->at + 1);
-    if (lo >= before && lo - before < own) {
-        int from = before;
-        for (int r = tid * per;; ++r) {
+    if (lo >= from && lo < to) {
+        int left = lo - from;
+#pragma unroll 1
+        for (int r = tid * per; r < a.B; ++r) {
             if (per > 1 && !to_latent(t, load_window(a, r), &q, false)) continue;
-            const int units = job() * ((q.row_tiles + size - 1) / size);
-            if (lo - from >= units) {
-                from += units;
+            const int units = job() * (q.row_tiles + size - 1 >> shift);
+            if (left >= units) {
+                left -= units;
                 continue;
             }
             begin->r = r;
-            begin->group = (lo - from) / job();
-            begin->unit = (lo - from) % job();
+            begin->group = left / job();
+            begin->unit = left - begin->group * job();
             begin->left = hi - lo;
             begin->q = q;
             break;
@@ -316,7 +340,7 @@ struct alignas(16) LatentControl {
     unsigned nonfinite[4];  // window tokens whose values were zeroed in either CTA, by segment
     int abort;
     LatentBegin begin;
-    int scan[40];
+    int4 of_warp[kLatentThreads / 32];
     float top[2][2][kRows];  // [tile's parity][half of the positions]
     float sum[2][kRows];
 };
@@ -363,7 +387,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
 
     Deal deal;
     Team team;
-    if (!latent_share(t, &ctl.begin, ctl.scan, &deal, &team)) {  // (neither CTA of the pair)
+    if (!latent_share(t, &ctl.begin, ctl.of_warp, &deal, &team)) {  // (neither CTA of the pair)
         if (warp == kMatrixWarp) {
             __syncwarp();
             tmem_free_pair(*(volatile unsigned *)&ctl.tmem, 512);
