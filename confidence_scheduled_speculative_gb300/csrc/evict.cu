@@ -568,54 +568,65 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a) {
         // this thread's places: from + 32 i, of the warp's run of consecutive ones, and
         // where their ranks lie
         const int per = (n + threads - 1) / threads, from = (whole - lane) * per + lane;
+        const int have = min(max((n - from + 31) / 32, 0), per);
         unsigned *key = keys + warp * 32 * per + lane;
         const long long fresh_from = (long long)__ldg(a.now + r) - a.recent;
+        // the keep-th largest key, eleven, eleven and ten bits at a time
+        constexpr int kBits = 11, kLastBits = 10;
+        static_assert(1 << kBits == kDigits && 2 * kBits + kLastBits == 32, "digits");
+        for (int i = tid; i < kDigits; i += kThreads) hist[0][i] = 0;
+        __syncthreads();
+        int most = 0;  // (the fresh have one key, which is counted apart)
         bool nan = false;
         // (a short line's all at once: 256 lines of 4113 places 25 us at eight, 20.6 at sixteen)
         constexpr int kAhead = 16;
 #pragma unroll 1
-        for (int i = 0; i < per; i += kAhead) {
+        for (int i = 0; i < have; i += kAhead) {
             float w[kAhead];
             int position[kAhead];
-            auto in = [&](int k) { return i + k < per && from + 32 * (i + k) < n; };
+            const float *w_at = w_in + from + 32 * i;
+            const int32_t *p_at = p_in + from + 32 * i;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i + k < have) {
+                    w[k] = w_at[32 * k];
+                    position[k] = p_at[32 * k];
+                }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const int p = in(k) ? from + 32 * (i + k) : 0;
-                w[k] = w_in[p];
-                position[k] = p_in[p];
-            }
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                if (!in(k)) continue;
+                if (i + k >= have) continue;
                 const int p = from + 32 * (i + k);
                 const unsigned rank = rank_key(w[k], position[k], fresh_from);
                 key[32 * (i + k)] = rank;
                 nan = nan || rank == 0;
+                if (rank == 0xFFFFFFFFu) ++most;
+                else atomicAdd(&hist[0][rank >> 32 - kBits], 1);
                 // (the ledger of entries that stay where they are)
                 if (apart && p < end) w_out[p] = w[k];
                 if (apart_p && p < end) p_out[p] = position[k];
             }
         }
         if (nan) flag(a.status, DSPARK_STATUS_BAD_INPUT);
-        auto there = [&](int i) { return from + 32 * i < n; };
-        // the keep-th largest key, eleven, eleven and ten bits at a time
+        auto there = [&](int i) { return i < have; };
         unsigned border = 0;
         int need = a.keep;  // of the entries that agree with the border's digits so far
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass == 2 ? 10 : 11;
+            const int bits = pass == 2 ? kLastBits : kBits, shift = 32 - kBits * pass - bits;
             int *own = hist[pass & 1];
-            for (int i = tid; i < kDigits; i += kThreads) own[i] = 0;
-            __syncthreads();
-            int most = 0;  // (the fresh have one key: counted by ballots)
+            if (pass > 0) {
+                for (int i = tid; i < kDigits; i += kThreads) own[i] = 0;
+                __syncthreads();
+                most = 0;
 #pragma unroll 4
-            for (int i = 0; i < per; ++i) {
-                const unsigned k = there(i) ? key[32 * i] : 0;
-                const bool in = there(i) && (pass == 0 || k >> (shift + bits) == border);
-                const bool top = in && k == 0xFFFFFFFFu;
-                most += __popc(__ballot_sync(kFullMask, top));
-                if (in && !top) atomicAdd(&own[k >> shift & ((1 << bits) - 1)], 1);
+                for (int i = 0; i < have; ++i) {
+                    const unsigned k = key[32 * i];
+                    if (k >> (shift + bits) != border) continue;
+                    if (k == 0xFFFFFFFFu) ++most;
+                    else atomicAdd(&own[k >> shift & ((1 << bits) - 1)], 1);
+                }
             }
+            most = __reduce_add_sync(kFullMask, most);
             if (lane == 0 && most) atomicAdd(&own[(1 << bits) - 1], most);
             sync();
             // thread t holds some digits in turn from above
