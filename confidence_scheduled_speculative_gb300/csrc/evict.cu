@@ -16,9 +16,14 @@
 //   exact in 32 bits: codes are halves as they are, and beside them queries are halves
 //   brought to 2^14 by a power of two a row, so that what they lose is below 2^-39 of a
 //   row's largest element.  A few rows leave most of the matrix instruction's rate unused,
-//   and HBM bounds the rest: tcgen05 would add barriers between warps.
+//   and HBM bounds the rest: tcgen05 would add barriers between warps.  Single tokens of 32
+//   requests of up to 8192 over E4M3 keys, 8 kv heads (152 MB) take 45.5 us, 3.3 TB/s: a
+//   step's conversions and waits; windows of up to 9 over bfloat16 keys (287 MB) 63.5 us, 4.5
+//   TB/s.  (Loads into registers a step ahead instead of copies 66 and 81 us; three steps
+//   under way, whose shared memory leaves one CTA an SM, 64 and 90.)
 // weights_any_kernel   any types, strides, head and page sizes, in 32 bits throughout: a
-//   warp a position, its key held in registers, one row and query head after another.
+//   warp a position, its key held in registers, one row and query head after another:
+//   684 and 1097 us in those two cases.
 //
 // Eviction, for each (request, kv head): of n entries those `keep` stay that rank first by
 // (fresh, weight, lower place).  An entry's rank is a 32-bit key (rank_key); the keep-th
@@ -31,12 +36,15 @@
 //   ranks of its entries in shared memory: three passes for the digits (a histogram of each
 //   beside them, integer counts, summed over the cluster), then entries equal to the border,
 //   entries moved and the list of moves, each in the order of places by ballots and prefix
-//   sums, and the ledger.  Latency bounds it: 32 heads of 60000 to 131040 places took 323 us
-//   with a CTA each that read them again in every pass, 120 with ranks in the registers of
-//   eight, of which two in three clusters run at a time.
-// evict_select_any_kernel  a CTA a (request, kv head) of any length, which does that.
+//   sums, and the ledger.  Latency and conflicts of the histogram's atomics bound it: 32
+//   heads of 60000 to 131040 places take some 50 us of an eviction's 99 (with the move).  That
+//   took 323 us with a CTA each that read them again in every pass, and 120 with ranks in the
+//   registers of eight CTAs, of which two in three clusters run at a time.
+// evict_select_any_kernel  a CTA a (request, kv head) of any length, which reads them again.
 // evict_move_kernel    a CTA 128 moves of a (request, kv head): both slots looked up by a
-//   thread, then the entries' pieces streamed by all.
+//   thread, then the entries' pieces streamed by all.  HBM bounds it, 4.6 TB/s of reads and
+//   writes of 128 bytes each here and there.  (64 moves a CTA 105 us for both, 256 98; eight
+//   pieces of a thread under way 103.)
 
 #include "kvcache.cuh"
 #include "schedule.cuh"
@@ -524,7 +532,8 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_any_kernel(EvictA
 }
 
 // Places that a CTA holds, and the threads of one whose line is short, so that several
-// fit an SM.
+// fit an SM: 256 lines of 4113 places by 512 and by 1024 threads 19.4 and 29.3 us, 32 of them
+// 15.5 and 16.8.
 constexpr int kSelectPlaces = 48 * 1024, kShortPlaces = 8192, kShortThreads = 512;
 constexpr int kSelectCtas = 8;  // of a cluster, at most
 
@@ -812,7 +821,8 @@ cudaError_t launch_gather(const WeightsArgs &t, cudaStream_t stream) {
     cudaError_t e = ensure_smem(reinterpret_cast<const void *>(weights_kernel<D, kQuant>), sizeof(S),
                                 29 + (D == 128) + 2 * kQuant);
     if (e != cudaSuccess) return e;
-    // some four times as many CTAs as run at a time, of 256 to 2048 positions
+    // some four times as many CTAs as run at a time, of 256 to 2048 positions (32 requests,
+    // twice, four and eight times as many: 53, 46 and 48 us; 8 windows 26, 26 and 30)
     const long long all = (long long)t.length * t.a.cache.n_kv_heads * t.a.B / (8 * sm_count());
     WeightsArgs u = t;
     u.span = (int)min(max((all + 255) / 256, 1ll), (long long)(kGatherMost / 256)) * 256;
@@ -970,7 +980,8 @@ extern "C" int dspark_kv_evict(const dspark_kv_cache *cache, const int32_t *lens
     a.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     // as few CTAs a line as hold it, or more while there are SMs for them and each has
-    // kShortPlaces or more
+    // kShortPlaces or more.  Eight lines of up to 131040 places by 4 and 8 CTAs 57 and 52 us,
+    // 32 of them 99 and 156; 128 of up to 40000 by 1, 2, 4: 161, 176 and 210.
     int ctas = 1;
     while (ctas < kSelectCtas && ((long long)ctas * kSelectPlaces < length ||
                                   ((long long)2 * ctas * lines <= sm_count() && length >= 2 * ctas * kShortPlaces)))

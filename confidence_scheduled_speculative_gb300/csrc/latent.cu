@@ -8,7 +8,10 @@
 // latent_append_kernel   a warp takes a row's cache entry, or a few steps of its query
 //   heads (kSteps, all their loads in flight before the first use).  A unit of rotation is
 //   eight pairs, sixteen elements in two 16-byte pieces, so that it stays in a lane; a lane
-//   has the same pairs in every step and fetches its cosines and sines once.
+//   has the same pairs in every step and fetches its cosines and sines once.  Queries are
+//   asked for before the row's position is known.  Windows of up to 17 tokens of 256
+//   requests with 128 heads take 21 us, 3.9 TB/s: the chain row, position, angles is what
+//   is left.  (With the queries asked for behind it 28 us; by the next kernel 81.)
 // latent_append_any_kernel   any dimensions, strides and alignment: a warp a row's entry
 //   or one head's part, one pair or element a lane and step.
 

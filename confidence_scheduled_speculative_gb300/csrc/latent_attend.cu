@@ -9,7 +9,9 @@
 //
 // latent_any_kernel   any types, strides, dimensions and page sizes, in 32 bits
 //   throughout: a CTA a (row, query head), its four warps take every fourth
-//   position, each with a running maximum and sum, joined at the end.
+//   position, each with a running maximum and sum, joined at the end.  It reads the cache
+//   for each of them again: single tokens of 4 short chats 64 us (the next 17), of 32
+//   requests of up to 8192 with 128 heads 9924 us (58.6).
 //
 // latent_tensor_kernel   bfloat16 over a bfloat16 cache with 512 + 64 elements a token, on
 //   the tensor cores of two CTAs at a time.  A job is a request and 128 of its (token,
@@ -28,9 +30,16 @@
 //   values, at a time, into buffers that the products of the tile before are just done with.
 //   Four warps copy (TMA: a box is 64 elements of up to 64 tokens of a page, and issuing
 //   one takes a warp a hundred cycles), one of the first CTA issues both products, four do
-//   the softmax, a thread half a row's positions, and three bring the next job's queries.  The tiles of all jobs are dealt evenly to the
-//   pairs, so jobs are split along the positions where there are few, and
-//   latent_join_kernel adds the parts in a fixed order.
+//   the softmax, a thread half a row's positions, and three bring the next job's queries.
+//   The tiles of all jobs are dealt evenly to the pairs, so jobs are split along the
+//   positions where there are few, and latent_join_kernel adds the parts in a fixed order.
+//   What bounds it: with many rows the products (trees of 32 tokens of 64 heads over two
+//   contexts of up to 131040, 841 GFLOP: 510 to 580 us, 1.45 to 1.65 PFLOP/s).  With few, HBM
+//   and what comes before and after (single tokens of 128 heads, 32 requests of up to 8192,
+//   165 MB: 58.6 us, of which 11 pass until the first scores, 32 for the tiles at 5.7 TB/s,
+//   4 for the last output and 11 for the join).  On the way the trees took 938 us with one CTA
+//   a job of 64 rows, 860 with pairs and 64 positions a step, 713 with 128, 654 without
+//   prefetches into L2.
 
 #include "latentcache.cuh"
 #include "schedule.cuh"
@@ -151,7 +160,9 @@ constexpr int kOutCol = 0, kScoreCol = 256;  // columns of tensor memory
 constexpr int kLatentThreads = 384, kQueryWarp = 4, kMatrixWarp = 7, kCopyWarp = 8;
 constexpr int kQueryWarps = kMatrixWarp - kQueryWarp, kCopyWarps = 4;  // of these two for keys, two for values
 static_assert(kLatentThreads == 32 * (kCopyWarp + kCopyWarps), "roles");
-constexpr int kLatentJobCost = 2;  // of a job's begin and end, in tiles
+// Of a job's begin and end, in tiles.  Single tokens of 32 requests with 0, 1, 2, 4: 63.5,
+// 62.0, 58.6, 57.7 us; windows with 16 heads 63.4, 59.0, 56.6, 57.1.
+constexpr int kLatentJobCost = 2;
 constexpr int kLatentDesc = 8;     // words about a split job, for the join
 
 struct LatentTensorArgs {
@@ -253,7 +264,8 @@ struct LatentWalk {
 // next barrier); false where none are left for it.
 //   Larger teams read less from HBM and leave members idle where the row tiles are no
 // multiple of them: the largest is taken whose members' steps are at most an eighth more
-// than those of pairs alone.
+// than those of pairs alone.  Trees of 16 row tiles over two long contexts, pairs alone and
+// in teams of four: 600 and 514 us; single tokens of one row tile stay alone (59 us).
 //   (Loops are rolled up: code that runs once is fetched as slowly as it is long.)
 __device__ __forceinline__ bool latent_share(const LatentTensorArgs &t, LatentBegin *begin, int4 *of_warp,
                                              Deal *deal, Team *team) {
@@ -821,7 +833,9 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
 // Joins the parts of the jobs that several CTAs share, in the CTAs' order: a block for
 // each of these CTAs but the last takes its share of the rows' fours of elements.  A thread
 // keeps to a row, and a block's groups of kRows threads take fours in turn, or where there
-// are many parts one four and the parts in turn.  L2's latency bounds it.
+// are many parts one four and the parts in turn.  Instructions that run once and L2 bound
+// it: of the 11 us that it adds to single tokens of 32 requests (107 parts of 256 KB) 4 are
+// the launch's, 3.5 the code's without parts.  Blocks a CTA, 4, 8 and 16: 65, 61 and 64 us.
 constexpr int kJoinThreads = 256, kJoinGroups = kJoinThreads / kRows, kJoinPieces = 8;
 constexpr int kJoinFew = 8;  // parts that a thread adds alone
 
@@ -955,7 +969,9 @@ cudaError_t launch_latent_tensor(const AttendArgs &a, const dspark_latent_cache 
     t.a = a;
     t.box = gcd(c.page_size, kStep / 2);
     // A split job's parts are joined by a second launch.  Where no request can have more
-    // than kWholeTiles tiles, a job stays whole and that launch is not made.
+    // than kWholeTiles tiles, a job stays whole and that launch is not made.  Whole and split,
+    // us: 4 requests of up to 256 tokens 17.3 and 23.8, of 500 17.3 and 22.8, of 1000 23.9 and
+    // 22.8; 64 of 256 18.1 and 26.2.
     t.whole = (long long)c.table_width * c.page_size <= kWholeTiles * kTile;
     unsigned char *w = static_cast<unsigned char *>(workspace);
     t.part_o = reinterpret_cast<float *>(w);
