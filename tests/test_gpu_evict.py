@@ -256,6 +256,73 @@ def test_evict(api, i, inplace):
     assert int(e.status) == 0
 
 
+def test_gather_and_evict_captured(api):
+    """One graph of a gathering and an eviction in place, replayed over lengths that change
+    between: the same bits as the calls themselves, with a workspace that two graphs share."""
+    def state():
+        p = Gathering(api, 470, prefix=[200, 90], win=[5, 3], hq=8, hkv=2, D=128, page=16, kind="e4m3", more=40)
+        p.positions = torch.arange(p.length, **I32).repeat(2, 2, 1)
+        p.lens = torch.zeros(2, **I32)
+        return p
+
+    def calls(p, ws):
+        api.dspark_attention_weights(p.q, p.kv, lse=p.lse, cu_seqlens=p.cu, prefix_lens=p.prefix_lens,
+                                     scale=p.scale, weights=p.before, pos=p.pos, positions=p.positions,
+                                     status=p.status)
+        api.dspark_kv_evict(p.kv, lens=p.lens, now=p.now, keep=64, recent=8, weights=p.before,
+                            positions=p.positions, workspace=ws, status=p.status)
+
+    def rounds(p, go):
+        for n in ([200, 90], [64, 64], [64, 50]):
+            p.prefix_lens.copy_(torch.tensor(n, **I32))
+            p.lens.copy_(p.prefix_lens + torch.tensor([5, 3], **I32))
+            p.now.copy_(p.lens)
+            go()
+        torch.cuda.synchronize()
+        assert int(p.status) == 0
+        return [t.clone() for t in (p.before, p.positions, p.lens, p.cache.k.view(torch.uint8),
+                                    p.cache.v.view(torch.uint8), p.cache.k_scale, p.cache.v_scale)]
+
+    ws = api.workspace(api.dspark_kv_evict_workspace_bytes(2, 2, state().length))
+    results = []
+    for captured in (False, True, True):
+        p = state()
+        p.kv, p.now = p.cache.kv(), torch.zeros(2, **I32)
+        if captured:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                calls(p, ws)
+            results.append(rounds(p, g.replay))
+        else:
+            results.append(rounds(p, lambda: calls(p, ws)))
+    for got in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got, results[0]))
+
+
+def test_evict_two_at_once(api):
+    """Evictions on two streams, of several CTAs a line and of one, each with its workspace."""
+    two = [Evicting(525, [100000, 60000], keep=30000, recent=4096, hkv=2, page=128, kind="e4m3"),
+           Evicting(526, [3000, 8000, 100], keep=700, recent=64, hkv=4)]
+    streams = [torch.cuda.Stream() for _ in two]
+    torch.cuda.synchronize()
+    kept = []
+    for e, s in zip(two, streams):
+        e.was = [t.clone() for t in (e.cache.k.view(torch.uint8), e.cache.v.view(torch.uint8))]
+        e.was_scale = [None if t is None else t.clone() for t in (e.cache.k_scale, e.cache.v_scale)]
+        e.w, e.p, e.new = e.weights.clone(), e.positions.clone(), e.n.clone()
+        kept.append((e, s, e.cache.kv(), api.workspace(
+            api.dspark_kv_evict_workspace_bytes(len(e.lens), e.hkv, e.length))))
+    torch.cuda.synchronize()
+    for e, s, kv, ws in kept:
+        with torch.cuda.stream(s):
+            api.dspark_kv_evict(kv, lens=e.new, now=e.now, keep=e.keep, recent=e.recent, weights=e.w, positions=e.p,
+                                workspace=ws, status=e.status)
+    torch.cuda.synchronize()
+    for e in two:
+        e.check()
+        assert int(e.status) == 0
+
+
 def test_evict_odd_weights(api):
     """NaN, infinities, negative and equal weights, -0 beside 0; every entry fresh, and
     positions at the ends of their range."""

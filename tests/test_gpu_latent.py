@@ -283,6 +283,38 @@ def test_bad_requests_do_not_disturb_others(api, shape):
     assert int(p.status) == api.STATUS_BAD_LEN
 
 
+@pytest.mark.parametrize("longest", [60, 3000])
+def test_more_requests_than_threads(api, longest):
+    """Whole jobs and split ones, empty and unusable windows among them."""
+    n = 900
+    win = [(5 * i) % 4 for i in range(n)]
+    p = Problem(220, [(53 * i) % 60 for i in range(n - 1)] + [longest], win[:-1] + [2], hq=16, page=64)
+    skip = (3, 500)
+    for r in skip:
+        p.prefix_lens[r] = 1 << 20
+    p.run(api).check(skip=skip)
+    assert int(p.status) == api.STATUS_BAD_INDEX
+
+
+def test_two_at_once(api):
+    """Calls on two streams, each with its workspace."""
+    two = [Problem(222 + i, *shape, hq=64, page=64).run(api).check()
+           for i, shape in enumerate([([7000, 300, 12], [1, 9, 4]), ([90, 5000], [17, 2])])]
+    first = [(p.out.clone(), p.lse.clone()) for p in two]
+    streams = [torch.cuda.Stream() for _ in two]
+    spaces = [api.workspace(api.dspark_latent_attention_workspace_bytes(64, 512)) for _ in two]
+    for p in two:
+        p.out.fill_(7), p.lse.fill_(7)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for p, s, ws in zip(two, streams, spaces):
+            with torch.cuda.stream(s):
+                p.call(api, ws)
+    torch.cuda.synchronize()
+    for p, (out, lse) in zip(two, first):
+        assert torch.equal(p.out, out) and torch.equal(p.lse, lse) and int(p.status) == 0
+
+
 def test_repeated_captured_and_shared_workspace(api):
     """The same bits again, on another stream, in a graph beside a second captured call
     with the same workspace, and without lse."""

@@ -144,6 +144,29 @@ def test_bad_ranges_do_not_disturb_others(api, shape):
     assert int(p.status) == api.STATUS_BAD_LEN
 
 
+def test_more_requests_than_threads(api):
+    p = Problem(345, [((7 * i) % 5, (7 * i) % 5 + (3 * i) % 20) for i in range(700)] + [(600, 700)], hq=2)
+    p.run(api).check()
+    assert int(p.status) == 0
+
+
+def test_two_at_once(api):
+    """Calls on two streams."""
+    two = [Problem(346, [(300, 900), (5, 5)], hq=6).run(api).check(), Problem(347, [(513, 513)], hq=8, S=0).run(api).check()]
+    first = [(p.out.clone(), p.lse.clone()) for p in two]
+    streams = [torch.cuda.Stream() for _ in two]
+    for p in two:
+        p.out.fill_(7), p.lse.fill_(7)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for p, s in zip(two, streams):
+            with torch.cuda.stream(s):
+                p.call(api)
+    torch.cuda.synchronize()
+    for p, (out, lse) in zip(two, first):
+        assert torch.equal(p.out, out) and torch.equal(p.lse, lse) and int(p.status) == 0
+
+
 def test_repeated_and_captured(api):
     p = Problem(350, [(300, 700), (129, 129)], hq=4).run(api).check()
     first = p.out.clone()
