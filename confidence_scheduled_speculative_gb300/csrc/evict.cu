@@ -36,10 +36,11 @@
 //   ranks of its entries in shared memory: three passes for the digits (a histogram of each
 //   beside them, integer counts, summed over the cluster), then entries equal to the border,
 //   entries moved and the list of moves, each in the order of places by ballots and prefix
-//   sums, and the ledger.  Latency and conflicts of the histogram's atomics bound it: 32
-//   heads of 60000 to 131040 places take some 50 us of an eviction's 99 (with the move).  That
-//   took 323 us with a CTA each that read them again in every pass, and 120 with ranks in the
-//   registers of eight CTAs, of which two in three clusters run at a time.
+//   sums, and the ledger.  Latency bounds it (barriers and sums over the cluster, and an
+//   SM's one CTA): 32 heads of 60000 to 131040 places take some 50 us of an eviction's 99 (with
+//   the move).  That took 323 us with a CTA each that read them again in every pass, and 120
+//   with ranks in the registers of eight CTAs, of which two in three clusters run at a time.
+//   (Two histograms that lanes take in turns for the first digit: 102 us.)
 // evict_select_any_kernel  a CTA a (request, kv head) of any length, which reads them again.
 // evict_move_kernel    a CTA 128 moves of a (request, kv head): both slots looked up by a
 //   thread, then the entries' pieces streamed by all.  HBM bounds it, 4.6 TB/s of reads and
