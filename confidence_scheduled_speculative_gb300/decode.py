@@ -207,10 +207,7 @@ class ToyTarget:
         """With ``keep``, after the first ``counts`` rows of each window were accepted (None:
         all): what they attended to is gathered, and the caches, of ``lens`` entries now and
         ``now`` tokens, are cut; ``lens`` is updated."""
-        c = self.cfg
-        if c.keep is None:
-            return
-        w, before = self.window, lens.clone()
+        c, w, before = self.cfg, self.window, lens.clone()
         for cache, (q, lse) in zip(self.caches, w["layers"]):
             cache.gather(q, lse, cu_seqlens=w["cu_seqlens"], prefix_lens=w["prefix_lens"],
                          scale=c.head_dim ** -0.5, pos=w["pos"], counts=counts, status=status)
@@ -288,10 +285,10 @@ class LatentToyTarget(ToyTarget):
         return x @ self.head
 
 
-def prefill(target: ToyTarget, prompts, status) -> tuple[torch.Tensor, torch.Tensor]:
+def prefill(target: ToyTarget, prompts, status) -> torch.Tensor:
     """Every prompt but its last token into the caches, in windows of up to 32 tokens (of a
-    latent target whole, expanded); returns the tokens and the caches' entries of each
-    request."""
+    latent target whole, expanded); returns the caches' entries of each request: its tokens,
+    or with ``keep`` those that are left."""
     device, i32 = target.embed.device, torch.int32
     lens = [len(p) - 1 for p in prompts]
     put = lambda x: torch.tensor(x, dtype=i32, device=device)
@@ -310,11 +307,14 @@ def prefill(target: ToyTarget, prompts, status) -> tuple[torch.Tensor, torch.Ten
             cached += put(sizes)
             continue
         seen = put([min(at, n) for n in lens])
-        target.forward(ids, req=req, pos=pos, cache_pos=pos - (seen - cached)[req.long()], cu_seqlens=cu,
-                       prefix_lens=cached.clone(), totals=cu[-1:], status=status)
+        short = target.cfg.keep is not None
+        where = dict(cache_pos=pos - (seen - cached)[req.long()]) if short else {}
+        target.forward(ids, req=req, pos=pos, cu_seqlens=cu, prefix_lens=cached.clone(), totals=cu[-1:],
+                       status=status, **where)
         cached += put(sizes)
-        target.accepted(None, lens=cached, now=seen + put(sizes), status=status)
-    return put(lens), cached
+        if short:
+            target.accepted(None, lens=cached, now=seen + put(sizes), status=status)
+    return cached
 
 
 def generate(target: ToyTarget, prompts, steps: int, gamma: int = 7):
@@ -327,8 +327,9 @@ def generate(target: ToyTarget, prompts, steps: int, gamma: int = 7):
         min_verify_len=1, max_verify_len=gamma + 1, forced_budget=-1, cost_kind=0,
         cost_M=budget, cost_val=1000.0 / (1.0 + 0.02 * budget), bias_ms=0.0, alpha_ms=0.0, tiers=(),
         capacity=B * (gamma + 1)), device)
-    tokens, cached = prefill(target, prompts, vs.status)
-    vs.prefix_lens.copy_(tokens)
+    cached = prefill(target, prompts, vs.status)
+    vs.prefix_lens.copy_(torch.tensor([len(p) - 1 for p in prompts], dtype=torch.int32))
+    short = target.cfg.keep is not None
     vs.anchor.copy_(torch.tensor([int(p[-1]) for p in prompts], dtype=torch.int32))
     # the drafter's confidence: falls with the depth, differs between requests
     depth = torch.arange(gamma, device=device)
@@ -337,18 +338,20 @@ def generate(target: ToyTarget, prompts, steps: int, gamma: int = 7):
     for _ in range(steps):
         vs.draft.copy_(target.draft(vs.anchor, gamma))
         vs.plan_pack()
-        # the window is stored from the caches' ends on (pads have no request)
-        evicted = torch.cat([vs.prefix_lens - cached, torch.zeros(1, dtype=torch.int32, device=device)])
+        where = {}
+        if short:  # the window is stored from the caches' ends on (pads have no request)
+            evicted = torch.cat([vs.prefix_lens - cached, torch.zeros(1, dtype=torch.int32, device=device)])
+            where = dict(cache_pos=vs.packed_pos - evicted[vs.packed_req.long()])
         logits = target.forward(vs.packed_ids, req=vs.packed_req, pos=vs.packed_pos,
-                                cache_pos=vs.packed_pos - evicted[vs.packed_req.long()],
                                 cu_seqlens=vs.cu_seqlens, prefix_lens=cached.clone(),
-                                totals=vs.totals, status=vs.status)
+                                totals=vs.totals, status=vs.status, **where)
         vs.greedy_accept(logits)
         committed.append((vs.out_tokens.clone(), vs.commit_lens.clone()))
         rows.append(vs.totals.clone())
         # rejected rows' keys and values are overwritten by the next window
         cached += vs.commit_lens
-        target.accepted(vs.commit_lens, lens=cached, now=vs.new_seq_lens, status=vs.status)
+        if short:
+            target.accepted(vs.commit_lens, lens=cached, now=vs.new_seq_lens, status=vs.status)
         vs.prefix_lens.copy_(vs.new_seq_lens)
         vs.anchor.copy_(vs.bonus)
     if int(vs.status) != 0:
