@@ -5,10 +5,11 @@
 //   s_j = scale (q_k . k_jg + q_s . k_shared_j),  mx = max s_j,  l = sum exp(s_j - mx)
 //   out = sum exp(s_j - mx) v_jg / l,             lse = mx + ln l
 //
-// prompt_any_kernel   any types, strides and dimensions, in 32 bits throughout: a CTA a
-//   (row, query head), its four warps take every fourth key, each with a running maximum
-//   and sum, joined at the end.  Each reads its keys itself: 4 prompts of up to 128 tokens 67
-//   us (the next 14), two of 8192 with 32 heads 459 ms (1.33).
+// prompt_any_kernel   any types, strides and dimensions, and requests of few scores where most
+//   are short; in 32 bits throughout: a CTA a (row, query head), its four warps take every
+//   fourth key, each with a running maximum and sum, joined at the end.  Each reads its keys
+//   itself: 4 prompts of up to 128 tokens 67 us (the next 14), two of 8192 with 32 heads 459
+//   ms (1.33).
 //
 // prompt_tensor_kernel   bfloat16 with keys of 128 (and a shared part of 64 or none) and
 //   values of 128, on the tensor cores of two CTAs at a time.  A job is a (request, query
@@ -46,6 +47,7 @@ struct PromptArgs {
     int B, n_q_heads, group, key_dim, shared_dim, value_dim, max_rows, max_keys;
     float scale;
     int32_t *status;
+    int split;  // both kernels are launched: requests of few scores are the first's
 };
 
 // A request's queries [lo, hi) and keys [k0, k1).
@@ -64,6 +66,16 @@ __device__ __forceinline__ bool usable(const PromptArgs &a, const PromptRange &w
     if (bad && report) flag(a.status, DSPARK_STATUS_BAD_LEN);
     return !bad;
 }
+
+// Where both kernels are launched, which one a request is for: by its scores, which cost
+// the kernel without tensor cores 0.37 ns each (with all SMs, a head) and the other next to
+// nothing beside its 147 ns a job.
+constexpr int kFewScores = 512;
+__device__ __forceinline__ bool few_scores(const PromptRange &w) {
+    return (long long)(w.hi - w.lo) * (w.k1 - w.k0) <= kFewScores;
+}
+// Other requests have at least so many queries and keys together (twice the root).
+constexpr int kManyTokens = 46;
 
 constexpr int kPromptWarps = 4;
 constexpr int kPromptSteps = DSPARK_MAX_HEAD_DIM / 32;
@@ -85,7 +97,7 @@ __global__ void __launch_bounds__(kPromptWarps * 32) prompt_any_kernel(PromptArg
         else last = mid - 1;
     }
     const PromptRange w = load_range(a, first);
-    if (!usable(a, w, false) || row < w.lo) return;
+    if (!usable(a, w, false) || row < w.lo || (a.split && !few_scores(w))) return;
     const long long sees = (long long)(w.k1 - w.k0) - (w.hi - w.lo) + (row - w.lo) + 1;  // keys
 
     const int K = a.key_dim, S = a.shared_dim, V = a.value_dim, g = h / a.group;
@@ -230,7 +242,8 @@ prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const int per = (a.B + kPromptThreads - 1) / kPromptThreads;
         auto blocks = [&](int r, bool report) {
             const PromptRange w = load_range(a, r);
-            return usable(a, w, report) ? (w.hi - w.lo + kPromptBlock - 1) / kPromptBlock : 0;
+            if (!usable(a, w, report) || (a.split && few_scores(w))) return 0;
+            return (w.hi - w.lo + kPromptBlock - 1) / kPromptBlock;
         };
         long long mine = 0, total;
         for (int i = 0, r = tid * per; i < per && r < a.B; ++i, ++r) mine += blocks(r, blockIdx.x == 0);
@@ -561,6 +574,15 @@ bool prompt_tensor_fits(const PromptArgs &a, int dtype) {
     return aligned(a.q, 16) && aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.out, 16) && aligned(a.shared, 16);
 }
 
+// How many requests can have more than few_scores.
+long long many_requests(const PromptArgs &a) { return ((long long)a.max_rows + a.max_keys) / kManyTokens; }
+
+template <typename T>
+cudaError_t launch_prompt_any(const PromptArgs &a, cudaStream_t stream) {
+    const dim3 grid(a.max_rows, a.n_q_heads), block(kPromptWarps * 32);
+    return launch_pdl(prompt_any_kernel<T>, grid, block, 0, stream, a);
+}
+
 template <bool kShared>
 cudaError_t launch_prompt_tensor(const PromptArgs &a, cudaStream_t stream) {
     using S = PromptShape<kShared>;
@@ -580,7 +602,9 @@ cudaError_t launch_prompt_tensor(const PromptArgs &a, cudaStream_t stream) {
                                 27 + kShared);
     if (e != cudaSuccess) return e;
     // every request has one block that is not full at most
-    const long long grid = 2ll * a.n_q_heads * (a.max_rows / kPromptBlock + min(a.B, a.max_rows));
+    const long long jobs = min(a.split ? many_requests(a) : (long long)a.B, (long long)a.max_rows);
+    const long long grid = 2ll * a.n_q_heads * (a.max_rows / kPromptBlock + jobs);
+    if (grid == 0) return cudaSuccess;
     if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     return launch_pdl(prompt_tensor_kernel<kShared>, dim3((unsigned)grid), dim3(kPromptThreads), S::kTotal, stream,
                       map_q, map_k, map_s, map_v, a);
@@ -645,12 +669,18 @@ extern "C" int dspark_prompt_attention(const void *q, int64_t ld_q, const void *
     a.status = status;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
+    a.split = 0;
     if (prompt_tensor_fits(a, dtype)) {
+        // A job takes a pair of CTAs some 11 us, however few its queries.  Where requests are
+        // short on average, those of few scores go to the other kernel, which needs a second
+        // launch and a CTA a row and head.  Jobs alone and split, us, 16 heads: 256 prompts of 1
+        // token 601 and 20, of up to 8 603 and 74, of up to 32 630 and 402; 32 of up to 32 81 and
+        // 57.  Of up to 64 (643, or 1216 without tensor cores) they stay.
+        a.split = many_requests(a) < B;
         e = shared_dim ? launch_prompt_tensor<true>(a, st) : launch_prompt_tensor<false>(a, st);
+        if (e == cudaSuccess && a.split) e = launch_prompt_any<__nv_bfloat16>(a, st);
     } else {
-        const dim3 grid(max_rows, n_q_heads), block(kPromptWarps * 32);
-        e = dtype == DSPARK_DTYPE_BF16 ? launch_pdl(prompt_any_kernel<__nv_bfloat16>, grid, block, 0, st, a)
-                                       : launch_pdl(prompt_any_kernel<float>, grid, block, 0, st, a);
+        e = dtype == DSPARK_DTYPE_BF16 ? launch_prompt_any<__nv_bfloat16>(a, st) : launch_prompt_any<float>(a, st);
     }
     return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }

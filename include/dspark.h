@@ -890,10 +890,11 @@ DSPARK_API int dspark_latent_attention(const void *q, int64_t ld_q, int32_t dtyp
  * A row that sees nothing gets out = 0 and lse = -inf.  What a row does not see has
  * no effect on it, NaN and infinities included.  BF16 with key_dim 128, shared_dim 64
  * or 0, value_dim 128 and 16-byte aligned bases and strides runs on the tensor cores,
- * the weights rounded to BF16; anything else in 32 bits throughout.
+ * the weights rounded to BF16; anything else in 32 bits throughout, and so, where
+ * max_rows + max_keys is below 46 B, requests of up to 512 (query, key) pairs.
  * A range outside the rows or the keys (BAD_LEN): that request's rows are unspecified,
- * the others not affected.  Ranges of queries that descend (BAD_LEN) or overlap: all
- * rows are unspecified.  Rows of no request are left alone.
+ * the others not affected.  Ranges that descend (BAD_LEN) or overlap: all rows are
+ * unspecified.  Rows of no request are left alone.
  * Errors: INVALID_ARG (null pointer, dtype, B < 1, n_q_heads not a positive multiple
  * of n_kv_heads, a stride below what it spans, negative counts, scale not finite, out
  * over q); UNSUPPORTED (key_dim, shared_dim or value_dim above

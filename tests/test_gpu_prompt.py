@@ -150,6 +150,18 @@ def test_more_requests_than_threads(api):
     assert int(p.status) == 0
 
 
+@pytest.mark.parametrize("shape", [dict(hq=3), dict(hq=4, hkv=2, S=0)])
+def test_short_requests_beside_long_ones(api, shape):
+    """Mostly single tokens, and requests on both sides of what counts as short."""
+    lens = [(1, 1)] * 150 + [(22, 23), (23, 23), (16, 32), (1, 512), (1, 513), (0, 3), (600, 700), (40, 10), (2, 257)]
+    p = Problem(348, lens + [(1, 2)] * 150, **shape).run(api).check()
+    assert int(p.status) == 0
+    p.cu[5], p.cu_k[8] = p.n + 100, 1 << 30  # two ranges that end outside, two that begin there
+    p.out.fill_(7), p.lse.fill_(7)
+    p.run(api)
+    assert int(p.status) == api.STATUS_BAD_LEN
+
+
 def test_two_at_once(api):
     """Calls on two streams."""
     two = [Problem(346, [(300, 900), (5, 5)], hq=6).run(api).check(), Problem(347, [(513, 513)], hq=8, S=0).run(api).check()]
