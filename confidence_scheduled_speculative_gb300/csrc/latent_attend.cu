@@ -155,7 +155,8 @@ constexpr int kKeyAt = kChunks * kChunkBytes;  // behind the queries
 constexpr int kValueAt = kKeyAt + kKeyParts * kKeyBytes;
 constexpr int kWeightsAt = kValueAt + kValueParts * kValueBytes;
 constexpr int kControlAt = kWeightsAt + 2 * kChunkBytes;
-constexpr int kLatentSmem = kControlAt + 3072;
+constexpr int kControlBytes = 3 * 1024;
+constexpr int kLatentSmem = kControlAt + kControlBytes;
 constexpr int kOutCol = 0, kScoreCol = 256;  // columns of tensor memory
 constexpr int kLatentThreads = 384, kQueryWarp = 4, kMatrixWarp = 7, kCopyWarp = 8;
 constexpr int kQueryWarps = kMatrixWarp - kQueryWarp, kCopyWarps = 4;  // of these two for keys, two for values
@@ -356,7 +357,7 @@ struct alignas(16) LatentControl {
     float top[2][2][kRows];  // [tile's parity][half of the positions]
     float sum[2][kRows];
 };
-static_assert(sizeof(LatentControl) <= 3072 && kLatentSmem <= 227 * 1024, "shared memory");
+static_assert(sizeof(LatentControl) <= kControlBytes && kLatentSmem <= 227 * 1024, "shared memory");
 
 // Where the entries of rows of 64 elements lie: 16-byte piece c of row r.
 __device__ __forceinline__ int chunk_piece(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
