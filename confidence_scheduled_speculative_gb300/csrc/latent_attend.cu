@@ -702,7 +702,7 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                 if (p0 + kStep > s.q.P) {
                     // Latent vectors past the request's end become zeros, and so do NaN and
                     // infinities of the window (0 x NaN would reach rows that do not see
-                    // them); the rows that do get them at the end.  Each CTA does so for the
+                    // them); the rows that do get NaN at the end.  Each CTA does so for the
                     // elements that it holds as values.
                     if (!wait(&ctl.value_seen[b], tile >> 1)) continue;
                     const int from = max(s.q.P, p0);
@@ -767,8 +767,10 @@ latent_tensor_kernel(const __grid_constant__ CUtensorMap map, const LatentTensor
                         reinterpret_cast<const __nv_bfloat16 *>(a.cache.k) + kv_offset(a.cache, page, tok, 0) + e;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
+                        // (an infinite element is a part of the key too, so that the score is
+                        // infinite or NaN and the weight 0 or NaN: either makes the product NaN)
                         const float y = elem_value(v[j]);
-                        if (!(y - y == 0.0f)) o[j] = __float_as_uint(__uint_as_float(o[j]) + y);
+                        if (!(y - y == 0.0f)) o[j] = __float_as_uint(NAN);
                     }
                 }
                 if (!whole) {

@@ -383,3 +383,18 @@ def test_no_rows(api):
                              q_rope=p.q[..., 512:], status=p.status)
     torch.cuda.synchronize()
     assert int(p.status) == 0 and torch.equal(before, p.cache.pool)
+
+
+@pytest.mark.parametrize("shape", [FAST, SLOW, dict(hq=128, page=64)])
+@pytest.mark.parametrize("prefix", [[70, 33], [2500, 1200]])
+def test_seen_infinite_elements(api, shape, prefix):
+    """One infinite element of an entry makes a score of infinity, of either sign as the query's
+    is: 0 times infinity, or NaN throughout, in the prefix as in the window, whole and split."""
+    tokens = dict(prefix=prefix, win=[5, 9])
+    for value in (math.inf, -math.inf):
+        for at in ((prefix[0] - 9, prefix[1] - 1), (prefix[0] + 2, prefix[1] + 4)):
+            p = Problem(205, **tokens, **shape)
+            for r, (pos, element) in enumerate(zip(at, (3, p.cache.latent - 1))):
+                p.cache.put(r, pos, value, element)
+            p.run(api).check()
+            assert bool(p.out.isnan().any()) and int(p.status) == 0
