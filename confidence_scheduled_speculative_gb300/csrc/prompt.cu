@@ -200,6 +200,18 @@ struct alignas(16) PromptControl {
 };
 static_assert(sizeof(PromptControl) <= 2048, "control area");
 
+// Whether a row's score of a key is -inf.
+__device__ __noinline__ bool weightless(const PromptArgs &a, int row, int head, long long key) {
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + row * a.ld_q +
+                             (long long)head * (a.key_dim + a.shared_dim);
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + key * a.ld_k + head / a.group * a.hs_k;
+    const __nv_bfloat16 *c = static_cast<const __nv_bfloat16 *>(a.shared) + key * a.ld_shared;
+    float s = 0.0f;
+    for (int i = 0; i < a.key_dim; ++i) s = fmaf(elem_value(q[i]), elem_value(k[i]), s);
+    for (int i = 0; i < a.shared_dim; ++i) s = fmaf(elem_value(q[a.key_dim + i]), elem_value(c[i]), s);
+    return s * a.scale == -INFINITY;
+}
+
 template <bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPromptThreads, 1)
 prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -529,10 +541,12 @@ prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                             const long long key = w.k0 + j * kPromptKeys + 32 * i + __ffs(bits) - 1;
                             const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + key * a.ld_v +
                                                      head / a.group * a.hs_v + d;
+                            const bool gone = weightless(a, w.lo + row, head, key);  // (0 times infinity is NaN)
 #pragma unroll
                             for (int k = 0; k < 32; ++k) {
                                 const float y = elem_value(v[k]);
-                                if (!(y - y == 0.0f)) o[k] = __float_as_uint(__uint_as_float(o[k]) + y);
+                                if (y - y == 0.0f) continue;
+                                o[k] = __float_as_uint(gone ? NAN : __uint_as_float(o[k]) + y);
                             }
                         }
                     }

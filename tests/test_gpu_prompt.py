@@ -216,3 +216,17 @@ def test_refusals(api):
     over = both.view(8, -1)[:, :256].unflatten(1, (2, 128))
     with pytest.raises(api.DsparkError):
         api.dspark_prompt_attention(both, p.k, p.v, k_shared=p.k_shared, out=over, **kw)
+
+
+@pytest.mark.parametrize("shape", [dict(hq=2), dict(hq=4, hkv=2, S=0), dict(hq=2, K=24, S=8, V=40)])
+def test_seen_infinite_elements(api, shape):
+    """Infinite values under a weight (infinite too), and under the weight 0 of a score of
+    -inf (NaN), among keys that all rows see and among those that some do."""
+    for value in (math.inf, -math.inf):
+        for at in (4, 300):
+            p = Problem(322, [(300, 510), (40, 40)], **shape)
+            p.v[at, :, 5] = value
+            p.v[at + 64, :, p.v.size(2) - 1] = value
+            p.k[at, :, 7] = value
+            p.run(api).check()
+            assert bool(p.out.isnan().any()) and bool(p.out.isinf().any()) and int(p.status) == 0
