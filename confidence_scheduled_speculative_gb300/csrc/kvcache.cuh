@@ -128,21 +128,22 @@ inline KvView kv_view(const dspark_kv_cache &c) {
     return w;
 }
 
-// Whether any of `rows` rows of `bytes_a` at a, ld_a bytes apart, shares a byte with one
-// of `bytes_b` at b, ld_b apart (no stride is below its rows' bytes).  Slices of one
-// buffer, side by side or one after the other, do not.
-inline bool rows_overlap(const void *a, int64_t ld_a, int64_t bytes_a, const void *b, int64_t ld_b,
-                         int64_t bytes_b, int64_t rows) {
+// Whether any of `rows_a` rows of `bytes_a` at a, ld_a bytes apart, shares a byte with one
+// of `rows_b` of `bytes_b` at b, ld_b apart (no stride is below its rows' bytes).  Slices of
+// one buffer, side by side or one after the other, do not.
+inline bool rows_overlap(const void *a, int64_t ld_a, int64_t bytes_a, int64_t rows_a, const void *b, int64_t ld_b,
+                         int64_t bytes_b, int64_t rows_b) {
+    if (rows_a < 1 || rows_b < 1) return false;
     const int64_t x = (int64_t)reinterpret_cast<uintptr_t>(a), y = (int64_t)reinterpret_cast<uintptr_t>(b);
-    if (y >= x + (rows - 1) * ld_a + bytes_a || x >= y + (rows - 1) * ld_b + bytes_b) return false;
+    if (y >= x + (rows_a - 1) * ld_a + bytes_a || x >= y + (rows_b - 1) * ld_b + bytes_b) return false;
     // the row of b that begins last before the begin of a row of a, and those that begin in
     // it (with equal strides one row of a stands for all)
-    for (int64_t i = 0; i < (ld_a == ld_b ? 1 : rows); ++i) {
+    for (int64_t i = 0; i < (ld_a == ld_b ? 1 : rows_a); ++i) {
         const int64_t from = x + i * ld_a - y;
-        const int64_t least = ld_a == ld_b ? 1 - rows : 0;
+        const int64_t least = ld_a == ld_b ? 1 - rows_a : 0;
         int64_t j = from / ld_b - (from % ld_b < 0);
         if (j < least) j = least;
-        for (; j < rows && j * ld_b - from < bytes_a; ++j)
+        for (; j < rows_b && j * ld_b - from < bytes_a; ++j)
             if (j * ld_b - from > -bytes_b) return true;
     }
     return false;

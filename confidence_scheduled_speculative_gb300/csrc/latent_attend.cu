@@ -1034,7 +1034,8 @@ extern "C" int dspark_latent_attention(const void *q, int64_t ld_q, int32_t dtyp
     if (max_rows == 0) return DSPARK_OK;
     // (a split job reads its queries again after another CTA has written its outputs)
     const int64_t e_bytes = kv_elem_bytes(dtype);
-    if (rows_overlap(q, ld_q * e_bytes, width * e_bytes, out, ld_out * e_bytes, width_out * e_bytes, max_rows))
+    if (rows_overlap(q, ld_q * e_bytes, width * e_bytes, max_rows, out, ld_out * e_bytes, width_out * e_bytes,
+                     max_rows))
         return DSPARK_ERR_INVALID_ARG;
     LatentArgs t;
     AttendArgs &a = t.a;

@@ -653,8 +653,14 @@ extern "C" int dspark_prompt_attention(const void *q, int64_t ld_q, const void *
     if (!(scale - scale == 0.0f)) return DSPARK_ERR_INVALID_ARG;
     if (max_rows == 0) return DSPARK_OK;
     const int64_t e_bytes = kv_elem_bytes(dtype);
-    if (rows_overlap(q, ld_q * e_bytes, width * e_bytes, out, ld_out * e_bytes, width_out * e_bytes, max_rows))
-        return DSPARK_ERR_INVALID_ARG;
+    auto under_out = [&](const void *p, int64_t ld, int64_t n, int64_t rows) {
+        return rows_overlap(p, ld * e_bytes, n * e_bytes, rows, out, ld_out * e_bytes, width_out * e_bytes, max_rows);
+    };
+    bool over = under_out(q, ld_q, width, max_rows) || (k_shared && under_out(k_shared, ld_shared, shared_dim, max_keys));
+    for (int g = 0; g < n_kv_heads; ++g)
+        over = over || under_out(static_cast<const char *>(k) + g * hs_k * e_bytes, ld_k, key_dim, max_keys) ||
+               under_out(static_cast<const char *>(v) + g * hs_v * e_bytes, ld_v, value_dim, max_keys);
+    if (over) return DSPARK_ERR_INVALID_ARG;
     PromptArgs a;
     a.q = q;
     a.ld_q = ld_q;

@@ -898,7 +898,7 @@ DSPARK_API int dspark_latent_attention(const void *q, int64_t ld_q, int32_t dtyp
  * unspecified.  Rows of no request are left alone.
  * Errors: INVALID_ARG (null pointer, dtype, B < 1, n_q_heads not a positive multiple
  * of n_kv_heads, a stride below what it spans, negative counts, scale not finite, out
- * over q); UNSUPPORTED (key_dim, shared_dim or value_dim above
+ * over an input); UNSUPPORTED (key_dim, shared_dim or value_dim above
  * DSPARK_MAX_HEAD_DIM, key_dim or value_dim < 1, more than 65535 heads); CUDA. */
 DSPARK_API int dspark_prompt_attention(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
                                        int64_t hs_k, const void *k_shared, int64_t ld_shared,

@@ -230,3 +230,22 @@ def test_seen_infinite_elements(api, shape):
             p.k[at, :, 7] = value
             p.run(api).check()
             assert bool(p.out.isnan().any()) and bool(p.out.isinf().any()) and int(p.status) == 0
+
+
+def test_output_beside_keys_and_values(api):
+    """In the same rows of one buffer, sharing no element; over a part of them it is refused."""
+    p = Problem(361, [(40, 40), (7, 7)], hq=2, pad=0).run(api)
+    first, n = p.out.clone(), p.k.size(0)
+    rows = torch.zeros((n, 2 * 256 + 64 + 256), device="cuda", dtype=torch.bfloat16)
+    heads = rows[:, :512].unflatten(1, (2, 256))
+    heads[..., :128], heads[..., 128:], rows[:, 512:576] = p.k, p.v, p.k_shared
+    kept = rows[:, :576].clone()
+    p.k, p.v, p.k_shared = heads[..., :128], heads[..., 128:], rows[:, 512:576]
+    p.out = rows[:, 576:].unflatten(1, (2, 128))
+    p.run(api)
+    assert torch.equal(p.out, first) and torch.equal(rows[:, :576], kept) and int(p.status) == 0
+    for at in (0, 128, 400, 575):  # over keys, values, both, the shared part
+        p.out = rows[:, at:at + 256].unflatten(1, (2, 128))
+        with pytest.raises(api.DsparkError):
+            p.run(api)
+    assert torch.equal(rows[:, :576], kept)

@@ -173,3 +173,18 @@ def test_evict_workspace(lib, B, H, n, ok):  # noqa: F811
     f = lib.dspark_kv_evict_workspace_bytes
     f.restype = ctypes.c_size_t
     assert (f(B, H, n) > 0) == ok and f(B, H, n) % 256 == 0
+
+
+def _at(elements):
+    return ctypes.c_void_p(0x100000 + 2 * elements)
+
+
+@pytest.mark.parametrize("name,ld", [("q", 768), ("k", 1024), ("v", 1024), ("s", 64)])
+def test_prompt_output_over_an_input(lib, name, ld):  # noqa: F811
+    """7 rows of queries, 9 of keys and values: the output shares its last element with the
+    first of an input, or its first with the last."""
+    rows, span = (7, 768) if name == "q" else (9, 64 if name == "s" else 3 * 256 + 128)
+    far = {x: ctypes.c_void_p(1 << 40 | i << 30) for i, x in enumerate(("q", "k", "v", "s"), 1)}
+    # (and in the middle: of keys and values between two heads, over the second)
+    for at in (-(7 * 512 - 1), (rows - 1) * ld + span - 1, 130 if name in "kv" else 3):
+        assert _prompt(lib, rows=7, **{**far, name: _at(0)}, out=_at(at)) == -1, at
