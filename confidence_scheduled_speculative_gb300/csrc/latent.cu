@@ -280,6 +280,23 @@ bool append_pieces(const LatentAppendArgs &a, int dtype, const dspark_latent_cac
     return ok && c.page_stride * ce % 16 == 0 && c.token_stride * ce % 16 == 0;
 }
 
+// Whether the queries' outputs are the queries themselves, or share no element with them:
+// rows side by side or apart in any strides, or, with the strides of the queries, parts of
+// the same rows' heads.
+bool same_or_apart(const LatentAppendArgs &a, int dtype) {
+    const int64_t e = kv_elem_bytes(dtype), part = a.rope_dim * e, H = a.n_q_heads;
+    const char *q = static_cast<const char *>(a.q), *out = static_cast<const char *>(a.q_out);
+    const bool rows_alike = a.ld_q == a.ld_q_out || a.max_rows == 1, heads_alike = a.hs_q == a.hs_q_out || H == 1;
+    if (q == out && rows_alike && heads_alike) return true;
+    const int64_t span = (H - 1) * a.hs_q * e + part, span_out = (H - 1) * a.hs_q_out * e + part;
+    if (!rows_overlap(q, a.ld_q * e, span, a.max_rows, out, a.ld_q_out * e, span_out, a.max_rows)) return true;
+    if (!rows_alike || !heads_alike) return false;
+    for (int64_t h = 1 - H; h < H; ++h)
+        if (rows_overlap(q, a.ld_q * e, part, a.max_rows, out + h * a.hs_q * e, a.ld_q * e, part, a.max_rows))
+            return false;
+    return true;
+}
+
 template <typename T, typename C>
 cudaError_t launch_latent_append(const LatentAppendArgs &a, bool pieces, cudaStream_t stream) {
     const int step = pieces ? 32 / (a.rope_dim / 16) * kSteps<T> : 1;
@@ -348,6 +365,7 @@ extern "C" int dspark_latent_append(const void *x, int64_t ld_x, const void *q, 
     a.max_rows = max_rows;
     a.cache = latent_view(*cache);
     a.status = status;
+    if (q && !same_or_apart(a, dtype)) return DSPARK_ERR_INVALID_ARG;
     const bool pieces = append_pieces(a, dtype, *cache);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == DSPARK_DTYPE_BF16

@@ -817,7 +817,8 @@ typedef struct {
  *   q, q_out     the rope_dim elements of n_q_heads heads a row, rows ld_* and
  *                heads hs_* elements apart, so that q may be a slice of the
  *                queries' projection and q_out of the absorbed queries.  They may
- *                be the same (in place) and must not overlap in any other way.
+ *                be the same (in place) and must not overlap in any other way; within
+ *                the spans of each other's rows they have the same strides.
  *                Both NULL with n_q_heads = 0 when only the cache is written
  *   nr           host: k_weight is [latent_dim] or NULL, q_weight NULL; cos_sin and
  *                its rope_dim, which is the cache's, are required
@@ -827,9 +828,9 @@ typedef struct {
  * query part is written); a position outside [0, n_pos) flags the same, and
  * nothing of that row is written.  Two rows of a call must not share a slot.
  * Errors: INVALID_ARG (null pointer, dtype, a stride below what it spans, negative
- * counts, rope_dim not the cache's, eps negative or NaN, a query weight, and for
- * the cache null pointers, dtype, counts < 1, negative strides); UNSUPPORTED
- * (latent_dim, rope_dim); CUDA. */
+ * counts, rope_dim not the cache's, eps negative or NaN, a query weight, q_out over a
+ * part of q, and for the cache null pointers, dtype, counts < 1, negative strides);
+ * UNSUPPORTED (latent_dim, rope_dim); CUDA. */
 DSPARK_API int dspark_latent_append(const void *x, int64_t ld_x, const void *q, int64_t ld_q,
                                     int64_t hs_q, int32_t dtype, int32_t n_q_heads,
                                     const dspark_latent_cache *cache /* host */,

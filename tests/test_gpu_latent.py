@@ -398,3 +398,26 @@ def test_seen_infinite_elements(api, shape, prefix):
                 p.cache.put(r, pos, value, element)
             p.run(api).check()
             assert bool(p.out.isnan().any()) and int(p.status) == 0
+
+
+def test_append_query_outputs_beside_the_queries(api):
+    """Parts of the same heads, or of the same rows, that share no element with the queries."""
+    gen = torch.Generator().manual_seed(3)
+    c = lo.Latent(gen, "bf16", [64], 16, filled=False)
+    x = torch.randn((6, 576), device="cuda").bfloat16()
+    wide = torch.randn((6, 4, 192), device="cuda").bfloat16()
+    status, pos = torch.zeros(1, **I32), torch.arange(6, **I32)
+    kw = dict(req=torch.zeros(6, **I32), pos=pos, cos_sin=torch.rand((64, 64), device="cuda"), status=status)
+    want = torch.zeros((6, 4, 64), device="cuda", dtype=torch.bfloat16)
+    api.dspark_latent_append(x, c.lc(), q_rope=wide[..., 128:], q_rope_out=want, **kw)
+    before = wide.clone()
+    api.dspark_latent_append(x, c.lc(), q_rope=wide[..., 128:], q_rope_out=wide[..., 64:128], **kw)
+    assert torch.equal(wide[..., 64:128], want) and torch.equal(wide[..., 128:], before[..., 128:])
+    assert torch.equal(wide[..., :64], before[..., :64])
+    rows = torch.cat([before.flatten(1), torch.zeros((6, 256), device="cuda", dtype=torch.bfloat16)], 1)
+    out = rows[:, 768:].unflatten(1, (4, 64))
+    api.dspark_latent_append(x, c.lc(), q_rope=rows[:, :768].unflatten(1, (4, 192))[..., 128:], q_rope_out=out, **kw)
+    assert torch.equal(out, want) and torch.equal(rows[:, :768], before.flatten(1)) and int(status) == 0
+    with pytest.raises(api.DsparkError):
+        api.dspark_latent_append(x, c.lc(), q_rope=wide[..., 128:], q_rope_out=wide[..., 120:184], **kw)
+    assert torch.equal(wide[..., 128:], before[..., 128:])

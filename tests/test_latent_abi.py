@@ -179,6 +179,25 @@ def _at(elements):
     return ctypes.c_void_p(0x100000 + 2 * elements)
 
 
+@pytest.mark.parametrize("out", [
+    dict(qo=_at(1), lqo=768, hso=192),  # the parts themselves, an element on
+    dict(qo=_at(192), lqo=768, hso=192),  # the next head's
+    dict(qo=_at(-192 + 63), lqo=768, hso=192),
+    dict(qo=_at(4 * 768 + 63), lqo=768, hso=192),  # the last row's
+    dict(qo=_at(0), lqo=2304, hso=576),  # the same begin, other strides
+    dict(qo=_at(0), lqo=768, hso=64),
+    dict(qo=_at(64), lqo=1536, hso=192),  # between the parts, in rows of another stride
+])
+def test_append_query_outputs_over_a_part_of_the_queries(lib, out):  # noqa: F811
+    assert _append(lib, _latent(), q=_at(0), rows=5, **out) == -1
+
+
+def test_append_query_outputs_of_one_row(lib):  # noqa: F811
+    """(the row stride says nothing then)"""
+    assert _append(lib, _latent(), q=_at(0), rows=1, qo=_at(3 * 192 + 63), lqo=2304, hso=192) == -1
+    assert _append(lib, _latent(), q=_at(0), rows=1, hq=1, qo=_at(1), lqo=2304, hso=576) == -1
+
+
 @pytest.mark.parametrize("name,ld", [("q", 768), ("k", 1024), ("v", 1024), ("s", 64)])
 def test_prompt_output_over_an_input(lib, name, ld):  # noqa: F811
     """7 rows of queries, 9 of keys and values: the output shares its last element with the
