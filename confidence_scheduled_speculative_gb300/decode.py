@@ -292,8 +292,9 @@ def prefill(target: ToyTarget, prompts, status) -> torch.Tensor:
     device, i32 = target.embed.device, torch.int32
     lens = [len(p) - 1 for p in prompts]
     put = lambda x: torch.tensor(x, dtype=i32, device=device)
-    cached = torch.zeros(len(lens), dtype=i32, device=device)
-    latent = isinstance(target, LatentToyTarget)
+    latent, short = isinstance(target, LatentToyTarget), target.cfg.keep is not None
+    # what is left of each request so far, if its caches are kept short
+    cached = put([0] * len(lens) if short else lens)
     most = max(max(lens), 1) if latent else api.MAX_WINDOW
     for at in range(0, max(lens), most):
         part = [p[at:min(at + most, n)] for p, n in zip(prompts, lens)]
@@ -304,15 +305,14 @@ def prefill(target: ToyTarget, prompts, status) -> torch.Tensor:
         ids = put(np.concatenate(part))
         if latent:
             target.prompt(ids, req=req, pos=pos, cu_seqlens=cu, status=status)
-            cached += put(sizes)
             continue
         seen = put([min(at, n) for n in lens])
-        short = target.cfg.keep is not None
-        where = dict(cache_pos=pos - (seen - cached)[req.long()]) if short else {}
-        target.forward(ids, req=req, pos=pos, cu_seqlens=cu, prefix_lens=cached.clone(), totals=cu[-1:],
-                       status=status, **where)
-        cached += put(sizes)
+        where = dict(prefix_lens=seen)
         if short:
+            where = dict(prefix_lens=cached.clone(), cache_pos=pos - (seen - cached)[req.long()])
+        target.forward(ids, req=req, pos=pos, cu_seqlens=cu, totals=cu[-1:], status=status, **where)
+        if short:
+            cached += put(sizes)
             target.accepted(None, lens=cached, now=seen + put(sizes), status=status)
     return cached
 
@@ -338,19 +338,18 @@ def generate(target: ToyTarget, prompts, steps: int, gamma: int = 7):
     for _ in range(steps):
         vs.draft.copy_(target.draft(vs.anchor, gamma))
         vs.plan_pack()
-        where = {}
+        where = dict(prefix_lens=vs.prefix_lens)
         if short:  # the window is stored from the caches' ends on (pads have no request)
             evicted = torch.cat([vs.prefix_lens - cached, torch.zeros(1, dtype=torch.int32, device=device)])
-            where = dict(cache_pos=vs.packed_pos - evicted[vs.packed_req.long()])
-        logits = target.forward(vs.packed_ids, req=vs.packed_req, pos=vs.packed_pos,
-                                cu_seqlens=vs.cu_seqlens, prefix_lens=cached.clone(),
+            where = dict(prefix_lens=cached.clone(), cache_pos=vs.packed_pos - evicted[vs.packed_req.long()])
+        logits = target.forward(vs.packed_ids, req=vs.packed_req, pos=vs.packed_pos, cu_seqlens=vs.cu_seqlens,
                                 totals=vs.totals, status=vs.status, **where)
         vs.greedy_accept(logits)
         committed.append((vs.out_tokens.clone(), vs.commit_lens.clone()))
         rows.append(vs.totals.clone())
         # rejected rows' keys and values are overwritten by the next window
-        cached += vs.commit_lens
         if short:
+            cached += vs.commit_lens
             target.accepted(vs.commit_lens, lens=cached, now=vs.new_seq_lens, status=vs.status)
         vs.prefix_lens.copy_(vs.new_seq_lens)
         vs.anchor.copy_(vs.bonus)

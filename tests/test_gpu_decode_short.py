@@ -118,3 +118,17 @@ def test_a_cache_that_keeps_everything(decode):
     assert run(256)[0] == whole
     short, rows = run(32)
     assert all(6 <= len(t) <= 36 for t in short) and max(rows) > 3
+
+
+def test_a_cache_that_keeps_everything_costs_nothing(decode):
+    """Without ``keep`` a step hands the lengths it has to the target, and makes no others."""
+    target = decode.ToyTarget(decode.ToyConfig(max_len=256), B=2, seed=12)
+    forward, seen = target.forward, []
+
+    def noted(ids, **kw):
+        seen.append(kw["prefix_lens"])
+        return forward(ids, **kw)
+
+    target.forward = noted
+    decode.generate(target, [[1, 2, 3], [4, 5]], steps=3, gamma=4)
+    assert len(seen) == 4 and seen[1] is seen[2] is seen[3]
