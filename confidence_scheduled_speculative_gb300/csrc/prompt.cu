@@ -332,6 +332,8 @@ prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (!ok && rank == 0 && lane == 0) {
             // copies still under way write the pair's buffers (each wait ends by itself; the
             // CTAs leave together)
+            for (int t = 0; t < 2; ++t)
+                if (steps[t]) mbar_wait(smem_addr(&ctl.q_full[t]), 0, kWaitLimitNs / 4);
             for (int p = 0; p < 2; ++p)
                 for (int i = 0; i < kPromptStages; ++i) {
                     mbar_wait(smem_addr(&ctl.key_full[i]), p, kWaitLimitNs / 4);
@@ -652,6 +654,7 @@ extern "C" int dspark_prompt_attention(const void *q, int64_t ld_q, const void *
         return DSPARK_ERR_INVALID_ARG;
     if (!(scale - scale == 0.0f)) return DSPARK_ERR_INVALID_ARG;
     if (max_rows == 0) return DSPARK_OK;
+    // (other CTAs read the inputs after one has written its outputs)
     const int64_t e_bytes = kv_elem_bytes(dtype);
     auto under_out = [&](const void *p, int64_t ld, int64_t n, int64_t rows) {
         return rows_overlap(p, ld * e_bytes, n * e_bytes, rows, out, ld_out * e_bytes, width_out * e_bytes, max_rows);
