@@ -164,6 +164,11 @@ static_assert(kLatentThreads == 32 * (kCopyWarp + kCopyWarps), "roles");
 // Of a job's begin and end, in tiles.  Single tokens of 32 requests with 0, 1, 2, 4: 63.5,
 // 62.0, 58.6, 57.7 us; windows with 16 heads 63.4, 59.0, 56.6, 57.1.
 constexpr int kLatentJobCost = 2;
+// A split job's parts are joined by a second launch.  Where no request can have more than
+// so many tiles, a job stays whole and that launch is not made.  Whole and split, us: 4
+// requests of up to 256 tokens 17.3 and 23.8, of 500 17.3 and 22.8, of 1000 23.9 and 22.8;
+// 64 of 256 18.1 and 26.2.
+constexpr int kLatentWholeTiles = 4;
 constexpr int kLatentDesc = 8;     // words about a split job, for the join
 
 struct LatentTensorArgs {
@@ -971,11 +976,7 @@ cudaError_t launch_latent_tensor(const AttendArgs &a, const dspark_latent_cache 
     LatentTensorArgs t;
     t.a = a;
     t.box = gcd(c.page_size, kStep / 2);
-    // A split job's parts are joined by a second launch.  Where no request can have more
-    // than kWholeTiles tiles, a job stays whole and that launch is not made.  Whole and split,
-    // us: 4 requests of up to 256 tokens 17.3 and 23.8, of 500 17.3 and 22.8, of 1000 23.9 and
-    // 22.8; 64 of 256 18.1 and 26.2.
-    t.whole = (long long)c.table_width * c.page_size <= kWholeTiles * kTile;
+    t.whole = (long long)c.table_width * c.page_size <= kLatentWholeTiles * kStep;
     unsigned char *w = static_cast<unsigned char *>(workspace);
     t.part_o = reinterpret_cast<float *>(w);
     t.part_ml = reinterpret_cast<float *>(w + latent_part_o_bytes());
