@@ -132,3 +132,108 @@ def test_a_cache_that_keeps_everything_costs_nothing(decode):
     target.forward = noted
     decode.generate(target, [[1, 2, 3], [4, 5]], steps=3, gamma=4)
     assert len(seen) == 4 and seen[1] is seen[2] is seen[3]
+
+
+# As in test_gpu_decode: some 8 roundings a layer and 4 outside, of at most half a unit
+# relative to the row's largest values, grown by at most 4.
+UNIT = {torch.bfloat16: wo.BF16, torch.float32: 2.0 ** -11}  # (fp32 products may run as TF32)
+
+
+def watched(decode, cfg, B, seed):
+    """The model of the decode loop, that compares what the loop hands it with counts of its
+    own, its logits with 64 bits over the entries that the caches hold, and the ledger with
+    the entries that went in."""
+    class Watched(decode.ToyTarget):
+        def __init__(self):
+            super().__init__(cfg, B, seed=seed)
+            self.held, self.now, self.cuts, self.entry = [0] * B, [0] * B, [0] * B, {}
+
+        def forward(self, ids, *, req, pos, cu_seqlens, prefix_lens, totals, status, cache_pos=None):
+            cu = cu_seqlens.tolist()
+            before = [[entries(c, r, self.held[r]) for r in range(B)] for c in self.caches]
+            logits = super().forward(ids, req=req, pos=pos, cu_seqlens=cu_seqlens, prefix_lens=prefix_lens,
+                                     totals=totals, status=status, cache_pos=cache_pos)
+            assert prefix_lens.tolist() == self.held and int(totals[0]) == cu[-1]
+            for r in range(B):
+                a, b = cu[r], cu[r + 1]
+                n = b - a
+                assert req[a:b].tolist() == [r] * n
+                assert pos[a:b].tolist() == list(range(self.now[r], self.now[r] + n))
+                assert cache_pos[a:b].tolist() == list(range(self.held[r], self.held[r] + n))
+                if not n:
+                    continue
+                want = self.logits64(ids[a:b], self.now[r], [layer[r] for layer in before])
+                error = 4 * (8 * cfg.layers + 4) * UNIT[cfg.dtype] / 2 * want.abs().amax(-1, keepdim=True)
+                assert bool(((logits[a:b].double() - want).abs() <= error).all()), r
+                for i, c in enumerate(self.caches):
+                    ks, vs = entries(c, r, self.held[r] + n)
+                    for j in range(n):
+                        self.entry[i, r, self.now[r] + j] = ks[self.held[r] + j], vs[self.held[r] + j]
+            self.rows = [b - a for a, b in zip(cu, cu[1:])]
+            return logits
+
+        def logits64(self, ids, now, before):
+            c, n, f = self.cfg, ids.numel(), lambda t: t.double()
+            x, half = f(self.embed)[ids.long()], c.head_dim // 2
+            cos, sin = (t[:, None] for t in f(self.cos_sin[now:now + n]).split(half, 1))
+            chain = torch.ones(n, n, device="cuda", dtype=torch.bool).tril()
+
+            def turned(h, w):
+                h = h / (h.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * f(w)
+                a, b = h[..., :half], h[..., half:]
+                return torch.cat([a * cos - b * sin, b * cos + a * sin], -1)
+
+            for (old_k, old_v), w_qkv, w_out, (wq, wk) in zip(before, self.w_qkv, self.w_out, self.norms):
+                q, k, v = (x @ f(w_qkv)).view(n, -1, c.head_dim).split([c.n_q_heads, c.n_kv_heads, c.n_kv_heads], 1)
+                group = c.n_q_heads // c.n_kv_heads
+                k, v = (torch.cat(t).repeat_interleave(group, 1) for t in ((old_k, turned(k, wk)), (old_v, v)))
+                s = torch.einsum("ihd,jhd->hij", turned(q, wq), k) * c.head_dim ** -0.5
+                sees = torch.cat([torch.ones(n, old_k.size(0), device="cuda", dtype=torch.bool), chain], 1)
+                o = torch.einsum("hij,jhd->ihd", s.masked_fill(~sees, -math.inf).softmax(-1), v)
+                x = x + o.reshape(n, -1) @ f(w_out)
+            return x @ f(self.head)
+
+        def accepted(self, counts, *, lens, now, status):
+            counts_of = self.rows if counts is None else counts.tolist()
+            super().accepted(counts, lens=lens, now=now, status=status)
+            for r, n in enumerate(counts_of):
+                self.now[r] += n
+                self.cuts[r] += self.held[r] + n > cfg.keep
+                self.held[r] = min(self.held[r] + n, cfg.keep)
+            assert lens.tolist() == self.held and now.tolist() == self.now
+            for i, c in enumerate(self.caches):
+                for r, (m, t) in enumerate(zip(self.held, self.now)):
+                    ks, vs = entries(c, r, m)
+                    for h in range(cfg.n_kv_heads):
+                        at = c.positions[r, h, :m].tolist()
+                        assert len(set(at)) == m and set(range(max(t - cfg.recent, 0), t)) <= set(at)
+                        assert all(0 <= p < t for p in at)
+                        assert bool((c.weights[r, h, :m] >= 0).all()) and bool((c.weights[r, h, m:] == 0).all())
+                        kept = [self.entry[i, r, p] for p in at]
+                        if kept:
+                            assert torch.equal(ks[:, h], torch.stack([k[h] for k, _ in kept]))
+                            assert torch.equal(vs[:, h], torch.stack([v[h] for _, v in kept]))
+
+    return Watched()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_loop_over_caches_that_are_cut(decode, dtype, monkeypatch):
+    """Prompts and steps that evict: places, lengths and ledger are those of the tokens so far,
+    and every window's logits are the model's over the entries that are left."""
+    cfg = decode.ToyConfig(dtype=decode.CACHE_DTYPES[dtype], cache=decode.CACHE_DTYPES[dtype], keep=32, recent=16,
+                           max_len=256)
+    target = watched(decode, cfg, B=3, seed=11)
+    gen = np.random.default_rng(3)
+    prompts = [gen.integers(0, cfg.vocab, n).tolist() for n in (2, 40, 100)]
+    prompt_cuts, prefill = [], decode.prefill
+
+    def counted(*args):
+        cached = prefill(*args)
+        prompt_cuts.extend(target.cuts)
+        return cached
+
+    monkeypatch.setattr(decode, "prefill", counted)
+    tokens, _ = decode.generate(target, prompts, steps=8, gamma=5)
+    assert target.now == [len(p) - 1 + len(t) for p, t in zip(prompts, tokens)]
+    assert prompt_cuts[2] >= 2 and min(c - p for c, p in zip(target.cuts[1:], prompt_cuts[1:])) >= 2
