@@ -364,3 +364,32 @@ def test_evict_refusals(api):
         api.dspark_kv_evict(e.cache.kv(), keep=4, recent=1, **{**kw, "positions": e.positions[:, :, 1:]})
     with pytest.raises(ValueError, match="weights"):
         api.dspark_kv_evict(e.cache.kv(), keep=4, recent=1, **{**kw, "weights": e.weights[0]})
+
+
+@pytest.mark.parametrize("case", [
+    # one CTA a line of more than 8192 places: a short ledger, and many lines
+    dict(lens=[10000, 8200, 9999], keep=4096, recent=64, hkv=1, page=64),
+    dict(lens=[9500, 3], keep=9000, recent=9000, hkv=2, page=64, ties=True),
+    dict(lens=[500 * i + 700 for i in range(19)] + [40000], keep=3000, recent=100, hkv=4, D=16, page=64, kind="e4m3"),
+])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_evict_one_cta_a_line(api, case, inplace):
+    e = Evicting(550, **case).run(api, inplace)
+    e.check()
+    assert int(e.status) == 0
+
+
+@pytest.mark.parametrize("case", [
+    # spans of 512 and of 2048 positions, and more rows than are multiplied at a time
+    dict(prefix=[8990, 700, 33] + [(91 * i) % 400 for i in range(17)], win=[9, 5, 32] + [i % 3 for i in range(17)],
+         hq=32, hkv=2, D=128, page=64),
+    dict(prefix=[8200, 4095] + [(37 * i) % 300 for i in range(38)], win=[9, 7] + [i % 6 for i in range(38)],
+         hq=128, hkv=8, D=64, page=64),
+])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_gathered_over_long_spans(api, case, kind):
+    p = Gathering(api, 490, tree="tree", kind=kind, **case)
+    blocks = -(-(p.length * case["hkv"] * len(p.win) // (8 * 152)) // 256)
+    assert blocks >= (8 if case["hkv"] == 8 else 2)
+    p.gather(api).check()
+    assert int(p.status) == 0

@@ -421,3 +421,55 @@ def test_append_query_outputs_beside_the_queries(api):
     with pytest.raises(api.DsparkError):
         api.dspark_latent_append(x, c.lc(), q_rope=wide[..., 128:], q_rope_out=wide[..., 120:184], **kw)
     assert torch.equal(wide[..., 128:], before[..., 128:])
+
+
+@pytest.mark.parametrize("shape", [FAST, dict(hq=128, page=64)])
+def test_unseen_entries_have_no_effect_on_split_jobs(api, shape):
+    """As test_unseen_entries_have_no_effect, where a job's parts are joined: NaN and infinities
+    of the window reach the rows that see them, through the join, and no others."""
+    for value in (math.nan, math.inf, -math.inf):
+        p = Problem(206, [2500, 1200, 0], [5, 9, 4], tree="orphans", **shape)
+        used = torch.zeros(p.cache.pages.shape[:2], dtype=torch.bool, device="cuda")
+        for r, n in enumerate((2505, 1209, 4)):
+            at = torch.arange(n, device="cuda")
+            used[p.cache.table[r][at // p.cache.page].long(), at % p.cache.page] = True
+        p.cache.pages[~used] = value
+        p.run(api).check()
+        p.cache.put(0, 2502, value, 5)
+        p.cache.put(1, 1202, value, 300)
+        p.run(api).check()
+        assert bool(p.out.isnan().any()) and bool(p.out.isfinite().any()) and int(p.status) == 0
+
+
+def team(p, pairs):
+    """How many pairs of CTAs go through the positions together: the largest of 1, 2 and 4 whose
+    members' steps are an eighth more at most than those of pairs alone."""
+    def steps(size):
+        return sum((-(-(P + L) // 128) + 2) * -(-(-(-L * p.hq // 128)) // size)
+                   for P, L in zip(p.prefix, p.win) if L)
+    return max(s for s in (1, 2, 4) if s == 1 or steps(s) * 8 * pairs <= steps(1) * 9 * (pairs // s))
+
+
+@pytest.mark.parametrize("size,prefix,win,hq", [
+    (4, [2500], [32], 64),
+    # 15, 16 and 1 row tiles: groups that leave one member idle, or three
+    (4, [2500, 700], [30, 32], 64),
+    (4, [6000, 90, 3000], [32, 1, 31], 64),
+    (2, [2500], [2], 128),
+    # 9, 2 and 9 row tiles, and 13
+    (2, [3000, 40, 900], [9, 2, 9], 128),
+    (2, [7000, 600], [13, 3], 128),
+])
+@pytest.mark.parametrize("tree", [None, "orphans"])
+def test_teams(api, size, prefix, win, hq, tree):
+    """Pairs of CTAs that go through the same positions in teams, members without a row tile,
+    and the join of their parts."""
+    p = Problem(260 + size, prefix, win, hq=hq, page=64, tree=tree)
+    assert {team(p, pairs) for pairs in range(72, 77)} == {size}
+    ws = api.workspace(api.dspark_latent_attention_workspace_bytes(hq, 512))
+    ws.fill_(255)
+    p.run(api, ws=ws).check()
+    first, first_lse = p.out.clone(), p.lse.clone()
+    p.out.fill_(7), p.lse.fill_(7)
+    p.run(api, ws=ws)
+    assert torch.equal(p.out, first) and torch.equal(p.lse, first_lse) and int(p.status) == 0

@@ -249,3 +249,21 @@ def test_output_beside_keys_and_values(api):
         with pytest.raises(api.DsparkError):
             p.run(api)
     assert torch.equal(rows[:, :576], kept)
+
+
+@pytest.mark.parametrize("shape", [dict(hq=3), dict(hq=4, hkv=2, S=0)])
+@pytest.mark.parametrize("last", [(3, 3), (600, 700)])
+@pytest.mark.parametrize("which", ["rows", "keys"])
+def test_bad_ranges_beside_short_requests(api, shape, last, which):
+    """Where both kernels run: a last range, short or long, that ends outside the rows or the
+    keys leaves the other requests of either kernel as they are."""
+    lens = [(1, 1)] * 150 + [(22, 23), (300, 400), (16, 33), (1, 513), (0, 3)] + [(1, 2)] * 150 + [last]
+    p = Problem(349, lens, **shape)
+    assert (p.q.size(0) + p.k.size(0)) // 46 < len(lens)
+    if which == "rows":
+        p.cu[-1] = p.q.size(0) + 9
+        p.n = p.q.size(0)
+    else:
+        p.cu_k[-1] = p.k.size(0) + 9
+    p.run(api).check(skip=(len(lens) - 1,))
+    assert int(p.status) == api.STATUS_BAD_LEN
