@@ -211,6 +211,27 @@ struct Ring {
     }
 };
 
+// Where a position lies, for a lane that steps through the tiles of a segment:
+// the table's entry is loaded ahead of its use.
+struct Place {
+    int col, token;
+    __device__ __forceinline__ void begin(const KvView &c, int pos) {
+        col = (unsigned)pos / (unsigned)c.page_size;
+        token = pos - col * c.page_size;
+    }
+    __device__ __forceinline__ void step(const KvView &c) {
+        token += kTile;
+        while (token >= c.page_size) {
+            token -= c.page_size;
+            ++col;
+        }
+    }
+    // the entry; the pool's size, a page it does not have, past the end
+    __device__ __forceinline__ int entry(const KvView &c, int r, bool in) const {
+        return in ? __ldg(c.table + (long long)r * c.table_width + col) : c.n_pages;
+    }
+};
+
 // Two E4M3 values' worth of a query: x = hi + lo.  A bfloat16 has 8 significant
 // digits; hi takes the upper four, and what remains of x has at most four more, so
 // that hi + lo = x exactly while lo's last digit is at least E4M3's smallest step, 2^-9:

@@ -137,7 +137,6 @@ __global__ void __launch_bounds__(kWeightsWarps * 32) weights_any_kernel(Weights
 constexpr int kGatherWarps = 8, kGatherRows = 64;  // of a CTA; rows at a time
 constexpr int kGatherStages = 2;                   // steps of a warp under way
 constexpr int kGatherMost = 2048;                  // positions of a CTA
-constexpr float kGatherLog2e = 1.4426950408889634f;
 
 // x = a b + x: 16 x 16 times 16 x 8, halves or bfloat16.
 template <bool kHalf>
@@ -336,8 +335,8 @@ __global__ void __launch_bounds__(kGatherWarps * 32, 2) weights_kernel(WeightsAr
                     if constexpr (kQuant) y0 *= by.x * scale[i], y1 *= by.y * scale[i];
                     // (the difference from lse before the change of base: where a term
                     // counts, it is small)
-                    float e0 = exp2_approx(fmaf(y0, a.scale, -base.x) * kGatherLog2e);
-                    float e1 = exp2_approx(fmaf(y1, a.scale, -base.y) * kGatherLog2e);
+                    float e0 = exp2_approx(fmaf(y0, a.scale, -base.x) * kLog2e);
+                    float e1 = exp2_approx(fmaf(y1, a.scale, -base.y) * kLog2e);
                     if (in_window) {
                         const int token = p0 + g + 8 * i - w.P;
                         if (token >= 0 && !(sees.x >> min(token, 31) & 1)) e0 = 0.0f;

@@ -1,5 +1,6 @@
 // kvcache.cuh -- the paged key/value cache as the kernels see it: slots,
-// element types and the E4M3 quantiser, shared by cache.cu and attend.cu.
+// element types and the E4M3 quantiser, shared by cache.cu, the attention kernels and
+// evict.cu; and what host-side checks of calls share.
 #pragma once
 
 #include <cuda_bf16.h>

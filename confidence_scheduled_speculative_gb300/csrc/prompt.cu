@@ -171,8 +171,6 @@ constexpr int kRowsChunk = 128 * 128, kKeysChunk = 64 * 128;  // bytes of 64 ele
 constexpr int kPromptThreads = 320, kPromptCopyWarp = 8, kPromptMatrixWarp = 9;
 constexpr int kPromptScoreCol = 0, kPromptOutCol = 256;  // columns of tensor memory, a tile's 128 on
 constexpr int kDiagonal = kPromptBlock / kPromptKeys + 1;  // steps of a job that some query sees a part of
-constexpr float kPromptLazy = 8.0f;  // log2 of how far weights may grow past 1
-constexpr float kPromptLog2e = 1.4426950408889634f, kPromptLn2 = 0.6931471805599453f;
 
 // Shared memory of a CTA: the queries of both tiles, rings of keys and values, control.
 template <bool kShared>
@@ -413,7 +411,7 @@ prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const int t = warp >> 2, count = steps[t];
         const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
         const uint32_t scores = lanes + kPromptScoreCol + t * 128, outputs = lanes + kPromptOutCol + t * 128;
-        const float c = fmaxf(fabsf(a.scale) * kPromptLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
+        const float c = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-100f);  // 0 would turn -inf into NaN
         const bool negative = a.scale < 0.0f;
         const int row = row0 + t * kPromptTile + rank * 128 + tid % 128;  // of the request's queries
         const int sees = row + ahead + 1;                                 // keys
@@ -444,10 +442,10 @@ prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 for (int e = 8 + k; e < 128; e += 4) part[k] = fmaxf(part[k], __uint_as_float(x[e]));
             }
             const float top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])) * c;
-            // The maximum moves only when it grows by 2^kPromptLazy: until then the weights
+            // The maximum moves only when it grows by 2^kLazy: until then the weights
             // may pass 1, and sum and output stay as they are.  (The scores' barrier says that
             // the last step's output is done too.)
-            const bool grow = top > mx + kPromptLazy || (mx == -INFINITY && top > mx);
+            const bool grow = top > mx + kLazy || (mx == -INFINITY && top > mx);
             if (__any_sync(kFullMask, grow)) {
                 const float f = grow ? exp2_approx(mx - top) : 1.0f;
                 if (grow) mx = top;
@@ -568,7 +566,7 @@ prompt_tensor_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
             if (valid && a.lse)
                 a.lse[(long long)(w.lo + row) * a.n_q_heads + head] =
-                    l == 0.0f ? -INFINITY : shift * kPromptLn2 + logf(l);
+                    l == 0.0f ? -INFINITY : shift * kLn2 + logf(l);
         }
         tmem_fence_before();
     }

@@ -1,5 +1,6 @@
-// schedule.cuh -- how attend.cu and fewrows.cuh share a call's work: the window as
-// the device finds it, and its jobs dealt to the CTAs in tiles of positions.
+// schedule.cuh -- a call's windows as the device finds them (attend.cu, latent_attend.cu,
+// evict.cu), units of work dealt to the CTAs (attend.cu, latent_attend.cu), and how attend.cu
+// and fewrows.cuh share a call's jobs in tiles of positions.
 #pragma once
 
 #include "kvcache.cuh"
@@ -69,12 +70,9 @@ constexpr int kTile = 64;           // positions a step
 constexpr int kRowsPerTile = 128;   // (token, query head) rows of one kv head
 constexpr int kMaxCtas = 320;       // two for each of up to 160 SMs
 constexpr int kTmemCols = 256;      // two score tiles of 64, the output's up to 128
-constexpr float kLazy = 8.0f;       // log2 of how far weights may grow past 1
 // Weights as halves (over E4M3) are taken 2^kHalfRoom times larger, so that those far
 // below the largest keep their digits: with 2^kLazy in front a half still holds them.
 constexpr float kHalfRoom = 6.0f;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kDescInts = 8;  // of a split job, for the join
 // The most tiles of a request for which jobs stay whole and the joining launch is not
 // made.  Whole and split: 8 requests of up to 300 tokens 13 and 21 us, of 440 15 and 21,
@@ -264,27 +262,6 @@ __device__ __forceinline__ bool share_of(const TensorArgs &t, Begin *begin, long
     }
     return true;
 }
-
-// Where a position lies, for a lane that steps through the tiles of a segment:
-// the table's entry is loaded ahead of its use.
-struct Place {
-    int col, token;
-    __device__ __forceinline__ void begin(const KvView &c, int pos) {
-        col = (unsigned)pos / (unsigned)c.page_size;
-        token = pos - col * c.page_size;
-    }
-    __device__ __forceinline__ void step(const KvView &c) {
-        token += kTile;
-        while (token >= c.page_size) {
-            token -= c.page_size;
-            ++col;
-        }
-    }
-    // the entry; the pool's size, a page it does not have, past the end
-    __device__ __forceinline__ int entry(const KvView &c, int r, bool in) const {
-        return in ? __ldg(c.table + (long long)r * c.table_width + col) : c.n_pages;
-    }
-};
 
 // Tells the join, after a CTA's last segment s (its k-th) that is not a whole job, of
 // the job that begins here and ends in a later CTA, or of the one that the whole of

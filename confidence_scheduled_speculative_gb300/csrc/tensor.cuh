@@ -1,6 +1,7 @@
-// tensor.cuh -- the sm_103a tensor-core and tensor-copy instructions that
-// attend.cu is built from: tensor memory, tcgen05.mma with its descriptors,
-// tiled TMA loads, and mbarrier waits that end.
+// tensor.cuh -- the sm_103a tensor-core and tensor-copy instructions that the
+// attention kernels (attend.cu, latent_attend.cu, prompt.cu) are built from: tensor
+// memory, tcgen05.mma with its descriptors, tiled TMA loads, mbarrier waits that end,
+// pairs of CTAs; evict.cu takes its copies and cluster accesses from here.
 #pragma once
 
 #include <cuda.h>
@@ -44,7 +45,7 @@ __device__ __forceinline__ bool role_wait(uint32_t bar, uint32_t parity, volatil
 // The same for a whole warp that has come this far (`ok`), with one answer for all its
 // lanes: what follows a wait are instructions that the warp executes as a whole
 // (tensor memory, shuffles, barriers), so no lane may go on where another gives up.
-// Every role of attend.cu waits through this.
+// Every role of the attention kernels waits through this.
 __device__ __forceinline__ bool warp_wait(bool ok, uint32_t bar, uint32_t parity, volatile int *abort,
                                           int32_t *status) {
     return __all_sync(0xFFFFFFFFu, ok && role_wait(bar, parity & 1, abort, status));
@@ -411,6 +412,11 @@ __device__ __forceinline__ bool elect_one() {
                  : "=r"(p));
     return p != 0;
 }
+
+// The softmax of the attention kernels, to base 2.
+constexpr float kLazy = 8.0f;  // log2 of how far weights may grow past 1
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
