@@ -15,11 +15,11 @@
 //   bytes at a time and two steps ahead, and waits for no other thread.  Products are
 //   exact in 32 bits: codes are halves as they are, and beside them queries are halves
 //   brought to 2^14 by a power of two a row, so that what they lose is below 2^-39 of a
-//   row's largest element.  A few rows leave most of the matrix instruction's rate unused,
-//   and HBM bounds the rest: tcgen05 would add barriers between warps.  Single tokens of 32
-//   requests of up to 8192 over E4M3 keys, 8 kv heads (152 MB) take 45.5 us, 3.3 TB/s: a
-//   step's conversions and waits; windows of up to 9 over bfloat16 keys (287 MB) 63.5 us, 4.5
-//   TB/s.  (Loads into registers a step ahead instead of copies 66 and 81 us; three steps
+//   row's largest element.  A few rows leave most of the matrix instruction's rate unused:
+//   tcgen05 would add barriers between warps.  Single tokens of 32 requests of up to 8192
+//   over E4M3 keys, 8 kv heads (152 MB) take 45 us, 3.4 TB/s: a step's conversions and waits.
+//   Windows of up to 9 over bfloat16 keys (287 MB) take 63 us, 4.5 TB/s, with HBM 57 % and
+//   issue slots 47 % busy: neither is full, a warp's step and the uneven ends bound it.  (Loads into registers a step ahead instead of copies 66 and 81 us; three steps
 //   under way, whose shared memory leaves one CTA an SM, 64 and 90.)
 // weights_any_kernel   any types, strides, head and page sizes, in 32 bits throughout: a
 //   warp a position, its key held in registers, one row and query head after another:

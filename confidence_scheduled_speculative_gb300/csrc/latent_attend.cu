@@ -34,10 +34,12 @@
 //   The tiles of all jobs are dealt evenly to the pairs, so jobs are split along the
 //   positions where there are few, and latent_join_kernel adds the parts in a fixed order.
 //   What bounds it: with many rows the products (trees of 32 tokens of 64 heads over two
-//   contexts of up to 131040, 841 GFLOP: 510 to 580 us, 1.45 to 1.65 PFLOP/s).  With few, HBM
-//   and what comes before and after (single tokens of 128 heads, 32 requests of up to 8192,
-//   165 MB: 58.6 us, of which 11 pass until the first scores, 32 for the tiles at 5.7 TB/s,
-//   4 for the last output and 11 for the join).  On the way the trees took 938 us with one CTA
+//   contexts of up to 131040, 841 GFLOP: 510 to 594 us by box, 1.42 to 1.65 PFLOP/s).  With
+//   few, HBM and what comes before and after (single tokens of 128 heads, 32 requests of up
+//   to 8192, 156 MB of entries: 59 us, of which 11 pass until the first scores, 4 with the
+//   last output and 11 in the join).  While steps follow one another entries come at 6.4
+//   TB/s, 0.95 of a copy (76 requests of 4096, 8192 and 16384, a job a pair: 76, 132 and 245
+//   us), which would be 24 of the 59; uneven lengths and jobs' ends are the other 9.  On the way the trees took 938 us with one CTA
 //   a job of 64 rows, 860 with pairs and 64 positions a step, 713 with 128, 654 without
 //   prefetches into L2.
 

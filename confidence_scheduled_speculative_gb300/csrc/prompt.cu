@@ -25,11 +25,16 @@
 //   One warp copies (TMA), one of the first CTA issues, four a tile do the softmax, a thread
 //   a row.  Jobs with the most keys come first.
 //   Two prompts of up to 8192 new tokens behind up to 4000 earlier ones, 32 heads (1782
-//   GFLOP) take 1315 to 1360 us, 1.33 PFLOP/s, 0.66 to 0.69 of the measured rate.  What
-//   bounds it is the chain of a tile's step: 1400 cycles from scores to weights, 1280 of
-//   products for both tiles, and the barriers between them, 3400 a step of two tiles, with
-//   the tensor cores busy for 61 %.  (Weights handed to the product in halves: 1510 us.
-//   Half of the exponentials left out, in an experiment: 1232, so it is not they.)
+//   GFLOP) take 1315 to 1377 us, 1.29 to 1.36 PFLOP/s, 0.68 to 0.72 of the measured rate.
+//   What bounds it: a step of two tiles takes 1.8 us, 3700 cycles, of which its products
+//   are 2560 (20 of 16 x 256 x 128 a tile, 64 cycles each).  The rest is a tile's chain, 1400
+//   cycles from scores to weights, its 1280 of products and the barriers between.  And some
+//   25 us of every job are outside of that (begin, what the diagonal's steps add, the last
+//   outputs): calls of one job a pair take 40, 85 and 256 us with 1024, 4096 and 16384 keys.
+//   Here a pair has ten jobs and 586 steps, 1050 us of steps and 250 of jobs, before the
+//   uneven end.  The tensor cores are busy for 61 % of the kernel.  (Weights handed to the
+//   product in halves: 1510 us.  Half of the exponentials left out, in an experiment: 1232,
+//   so it is not they.)
 
 #include "kvcache.cuh"
 #include "tensor.cuh"
@@ -68,8 +73,12 @@ __device__ __forceinline__ bool usable(const PromptArgs &a, const PromptRange &w
 }
 
 // Where both kernels are launched, which one a request is for: by its scores, which cost
-// the kernel without tensor cores 0.37 ns each (with all SMs, a head) and the other next to
-// nothing beside its 147 ns a job.
+// the kernel without tensor cores 0.25 to 0.37 ns each (with all SMs, a head) and the other
+// next to nothing beside its 150 ns a job.  256 requests of 16 heads, us, without and with:
+//   20 queries over 20 keys 470 and 639, 22 over 23 569 and 638, 26 over 26 700 and 643
+//   4 over 100 555 and 628, over 128 696 and 624;  one over 400 602 and 884, over 512 765 and
+//   698, over 640 953 and 781
+// so that about 512 the two differ by a tenth either way.
 constexpr int kFewScores = 512;
 __device__ __forceinline__ bool few_scores(const PromptRange &w) {
     return (long long)(w.hi - w.lo) * (w.k1 - w.k0) <= kFewScores;
