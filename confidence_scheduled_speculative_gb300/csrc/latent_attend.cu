@@ -34,7 +34,7 @@
 //   The tiles of all jobs are dealt evenly to the pairs, so jobs are split along the
 //   positions where there are few, and latent_join_kernel adds the parts in a fixed order.
 //   What bounds it: with many rows the products (trees of 32 tokens of 64 heads over two
-//   contexts of up to 131040, 841 GFLOP: 510 to 594 us by box, 1.42 to 1.65 PFLOP/s).  With
+//   contexts of up to 131040, 841 GFLOP: 510 to 594 us by GPU, 1.42 to 1.65 PFLOP/s).  With
 //   few, HBM and what comes before and after (single tokens of 128 heads, 32 requests of up
 //   to 8192, 156 MB of entries: 59 us, of which 11 pass until the first scores, 4 with the
 //   last output and 11 in the join).  While steps follow one another entries come at 6.4
